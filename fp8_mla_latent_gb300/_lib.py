@@ -8,6 +8,7 @@ device raises instead of computing anything.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -22,6 +23,7 @@ KV8_DECODE_TCGEN05_CTA, KV8_DECODE_TCGEN05_PAIR = 3, 4
 STATUS = {0: "KV8_OK", -1: "KV8_EINVAL", -2: "KV8_EALIGN", -3: "KV8_EUNSUPPORTED",
           -4: "KV8_ECUDA", -5: "KV8_EBOUNDS", -6: "KV8_EWORKSPACE", -7: "KV8_ETIMEOUT",
           -8: "KV8_ESCRATCH", -9: "KV8_EIO", -10: "KV8_EFORMAT"}
+KV8_PAGES_EINDEX, KV8_PAGES_ENOROOM, KV8_PAGES_ETIMEOUT = 1, 2, 4  # bits of the pages' err_word
 
 _lock = threading.Lock()
 _lib = None
@@ -63,6 +65,14 @@ def lib() -> ctypes.CDLL:
                                                               i32, P]),
                 "mla_absorb_decode_fp8_batch_noalloc": (i32, [P, P, P, P, P, P, i32, i32, i32, i32,
                                                               i64, f32, P, P, i32, P]),
+                "mla_absorb_chunk_fp8_batch_workspace_size": (i64, [i32, i32, i64, i32]),
+                "mla_absorb_chunk_fp8_batch": (i32, [P, i64, i64, P, i64, i64, P, P, P, P, P, i64, i32,
+                                                     i32, i32, i32, i64, i32, f32, P, P, P, i64, P]),
+                "kv8_pages_append": (i32, [P, P, P, i32, i32, i64, P, P, P, i64, P, P]),
+                "kv8_pages_fork": (i32, [P, P, P, i32, i32, i64, P, P, P, i32, P, P, P, P]),
+                "kv8_pages_free": (i32, [P, P, P, i32, i32, i64, P, i32, P, P]),
+                "kv8_pages_compact": (i32, [P, P, P, i32, i32, i64, P, P, P, P, P]),
+                "kv8_pages_copy": (i32, [P, P, i32, i64, P, P, i64, P, P]),
                 "kv8_noalloc_error": (i32, [P]),
                 "kv8_workspace_error": (i32, [P, P]),
                 "kv8_disk_open": (i32, [ctypes.c_char_p, i64, ctypes.POINTER(P)]),
@@ -408,6 +418,209 @@ def mla_absorb_decode_fp8_batch_noalloc(q_lat, q_rope, kv_codes, kv_scales, bloc
         _stream(stream))
     _check("mla_absorb_decode_fp8_batch_noalloc", st)
     return out
+
+
+def _strides(t):
+    """Element strides of the first two dimensions (0 for one of size 1, whose stride says nothing)."""
+    return tuple(t.stride(k) if t.shape[k] > 1 else 0 for k in (0, 1))
+
+
+def _on_device_of(first, *others):
+    """The device of a call's tensors, made current for it (its launch, its default stream)."""
+    if any(t is not None and t.device != first.device for t in others):
+        raise ValueError("all tensors must be on the same device")
+    return torch.cuda.device(first.device) if first.device.type == "cuda" else contextlib.nullcontext()
+
+
+# ----------------------------------------------------------------- chunks of new tokens
+def mla_absorb_chunk_fp8_batch_workspace_size(B: int, H: int, total_q: int, max_blocks: int) -> int:
+    n = lib().mla_absorb_chunk_fp8_batch_workspace_size(int(B), int(H), int(total_q), int(max_blocks))
+    if n < 0:
+        raise ValueError("invalid B, H, total_q or max_blocks")
+    return int(n)
+
+
+def mla_absorb_chunk_fp8_batch(q_lat, q_rope, kv_codes, kv_scales, block_table, seq_lens, q_start,
+                               sm_scale, causal=True, out=None, lse=None, workspace=None,
+                               block_size=KV8_BLOCK, stream=None):
+    """The new tokens of B sequences (bf16 q_lat [total_q,H,512], q_rope [total_q,H,64], sequence
+    b's rows q_start[b]..q_start[b+1]-1) over a paged cache that holds them -> bf16 out
+    [total_q,H,512].  The queries may be strided views whose last dimension is contiguous."""
+    for t, name, width in ((q_lat, "q_lat", KV8_DL), (q_rope, "q_rope", KV8_DR)):
+        if not (isinstance(t, torch.Tensor) and t.dtype == torch.bfloat16 and _is_device(t)
+                and t.dim() == 3 and t.shape[2] == width and t.stride(2) == 1):
+            raise ValueError(f"{name} must be a CUDA bfloat16 [total_q, H, {width}] tensor with unit "
+                             "stride in its last dimension")
+    _need_cache(kv_codes, kv_scales)
+    _need(block_table, "block_table", torch.int32, 2)
+    _need(seq_lens, "seq_lens", torch.int32, 1)
+    _need(q_start, "q_start", torch.int32, 1)
+    rows, H = q_lat.shape[:2]
+    B, max_blocks = block_table.shape
+    if tuple(q_rope.shape[:2]) != (rows, H):
+        raise ValueError("q_lat must be [total_q,H,512] and q_rope [total_q,H,64]")
+    if seq_lens.shape[0] != B or q_start.shape[0] != B + 1:
+        raise ValueError("seq_lens needs one entry per row of block_table, and q_start one more")
+    if out is None:
+        out = torch.empty((rows, H, KV8_DL), dtype=torch.bfloat16, device=q_lat.device)
+    _need(out, "out", torch.bfloat16, 3)
+    if tuple(out.shape) != (rows, H, KV8_DL):
+        raise ValueError("out must be [total_q,H,512]")
+    if lse is not None:
+        _need(lse, "lse", torch.float32, 2)
+        if tuple(lse.shape) != (rows, H):
+            raise ValueError("lse must be [total_q,H]")
+    need = mla_absorb_chunk_fp8_batch_workspace_size(B, H, rows, max_blocks)
+    if workspace is None:
+        workspace = alloc_workspace(need, q_lat.device)
+    _need_workspace(workspace)
+    with _on_device_of(q_lat, q_rope, kv_codes, kv_scales, block_table, seq_lens, q_start, out, lse,
+                       workspace):
+        st = lib().mla_absorb_chunk_fp8_batch(
+            _ptr(q_lat), *_strides(q_lat), _ptr(q_rope), *_strides(q_rope), _ptr(kv_codes),
+            _ptr(kv_scales), _ptr(block_table), _ptr(seq_lens), _ptr(q_start), rows, B, H, max_blocks,
+            int(block_size), int(kv_codes.shape[0] // block_size), int(bool(causal)),
+            float(sm_scale), _ptr(out), _ptr(lse), _ptr(workspace),
+            workspace.numel() * workspace.element_size(), _stream(stream))
+    _check("mla_absorb_chunk_fp8_batch", st)
+    return out
+
+
+# ----------------------------------------------------------------- pages
+def _page_table(block_table, seq_lens, page_refs, err_word):
+    """The checks of every call on a page table; its C arguments."""
+    _need(block_table, "block_table", torch.int32, 2)
+    _need(seq_lens, "seq_lens", torch.int32, 1)
+    _need(page_refs, "page_refs", torch.int32, 1)
+    if seq_lens.shape[0] != block_table.shape[0]:
+        raise ValueError("seq_lens must have one entry per row of block_table")
+    _need_err(err_word)
+    return (_ptr(block_table), _ptr(seq_lens), _ptr(page_refs), block_table.shape[0],
+            block_table.shape[1], page_refs.shape[0])
+
+
+def _need_err(err_word):
+    if err_word is not None and not (isinstance(err_word, torch.Tensor) and _is_device(err_word)
+                                     and err_word.dtype == torch.int32 and err_word.numel() >= 1):
+        raise ValueError("err_word must be a CUDA int32 tensor")
+
+
+def _moves_out(moves, n_moves, room, device):
+    """The list a call writes its page moves to, and their count; allocated if None."""
+    if moves is None:
+        moves = torch.empty((max(room, 1), 2), dtype=torch.int32, device=device)
+    if n_moves is None:
+        n_moves = torch.empty(1, dtype=torch.int32, device=device)
+    _need(moves, "moves", torch.int32, 2)
+    _need(n_moves, "n_moves", torch.int32, 1)
+    if moves.shape[1] != 2 or moves.shape[0] < room:
+        raise ValueError(f"moves must be [>= {room}, 2]")
+    if n_moves.numel() < 1:
+        raise ValueError("n_moves must have one entry")
+    return moves, n_moves
+
+
+def kv8_pages_append(block_table, seq_lens, page_refs, n_new, cap=None, q_start=None, dst_slot=None,
+                     err_word=None, stream=None):
+    """Room for n_new[b] more tokens of every sequence: pages taken, seq_lens raised.  Returns
+    (q_start int32 [B+1], dst_slot int64 [cap]): where each sequence's new rows start, and the
+    cache slots of the new tokens in that order (-1 behind the last).  Give dst_slot or cap."""
+    table = _page_table(block_table, seq_lens, page_refs, err_word)
+    B = table[3]
+    _need(n_new, "n_new", torch.int32, 1)
+    if n_new.shape[0] != B:
+        raise ValueError("n_new must have one entry per sequence")
+    if q_start is None:
+        q_start = torch.empty(B + 1, dtype=torch.int32, device=n_new.device)
+    _need(q_start, "q_start", torch.int32, 1)
+    if q_start.shape[0] != B + 1:
+        raise ValueError("q_start must have one entry more than there are sequences")
+    if dst_slot is None:
+        if cap is None:
+            raise ValueError("dst_slot or cap must be given")
+        dst_slot = torch.empty(int(cap), dtype=torch.int64, device=n_new.device)
+    _need(dst_slot, "dst_slot", torch.int64, 1)
+    with _on_device_of(block_table, seq_lens, page_refs, n_new, q_start, dst_slot, err_word):
+        st = lib().kv8_pages_append(*table, _ptr(n_new), _ptr(q_start), _ptr(dst_slot),
+                                    dst_slot.shape[0], _ptr(err_word), _stream(stream))
+    _check("kv8_pages_append", st)
+    return q_start, dst_slot
+
+
+def kv8_pages_fork(block_table, seq_lens, page_refs, src_seq, dst_seq, fork_len=None, moves=None,
+                   n_moves=None, err_word=None, stream=None):
+    """Sequences dst_seq become prefixes of src_seq (fork_len tokens, or all) that share their full
+    pages.  Returns (moves int32 [>= n, 2], n_moves int32 [1]) for kv8_pages_copy."""
+    table = _page_table(block_table, seq_lens, page_refs, err_word)
+    _need(src_seq, "src_seq", torch.int32, 1)
+    _need(dst_seq, "dst_seq", torch.int32, 1)
+    n = src_seq.shape[0]
+    if dst_seq.shape[0] != n:
+        raise ValueError("dst_seq must have one entry per entry of src_seq")
+    if fork_len is not None:
+        _need(fork_len, "fork_len", torch.int32, 1)
+        if fork_len.shape[0] != n:
+            raise ValueError("fork_len must have one entry per entry of src_seq")
+    moves, n_moves = _moves_out(moves, n_moves, n, block_table.device)
+    with _on_device_of(block_table, seq_lens, page_refs, src_seq, dst_seq, fork_len, moves, n_moves, err_word):
+        st = lib().kv8_pages_fork(*table, _ptr(src_seq), _ptr(dst_seq), _ptr(fork_len), n, _ptr(moves),
+                                  _ptr(n_moves), _ptr(err_word), _stream(stream))
+    _check("kv8_pages_fork", st)
+    return moves, n_moves
+
+
+def kv8_pages_free(block_table, seq_lens, page_refs, seq, err_word=None, stream=None):
+    """Empty the sequences seq: their pages lose a count, their entries become -1."""
+    table = _page_table(block_table, seq_lens, page_refs, err_word)
+    _need(seq, "seq", torch.int32, 1)
+    with _on_device_of(block_table, seq_lens, page_refs, seq, err_word):
+        st = lib().kv8_pages_free(*table, _ptr(seq), seq.shape[0], _ptr(err_word), _stream(stream))
+    _check("kv8_pages_free", st)
+
+
+def kv8_pages_compact(block_table, seq_lens, page_refs, moves=None, n_moves=None, n_live=None,
+                      err_word=None, stream=None):
+    """Pack the pages in use into the front of the pool.  Returns (moves int32 [>= n_blocks // 2, 2],
+    n_moves int32 [1]) for kv8_pages_copy; n_live (int32 [1], optional) takes the pages in use."""
+    table = _page_table(block_table, seq_lens, page_refs, err_word)
+    moves, n_moves = _moves_out(moves, n_moves, page_refs.shape[0] // 2, block_table.device)
+    if n_live is not None:
+        _need(n_live, "n_live", torch.int32, 1)
+        if n_live.numel() < 1:
+            raise ValueError("n_live must have one entry")
+    with _on_device_of(block_table, seq_lens, page_refs, moves, n_moves, n_live, err_word):
+        st = lib().kv8_pages_compact(*table, _ptr(moves), _ptr(n_moves), _ptr(n_live), _ptr(err_word),
+                                     _stream(stream))
+    _check("kv8_pages_compact", st)
+    return moves, n_moves
+
+
+def kv8_pages_copy(kv_codes, kv_scales, moves, n_moves=None, err_word=None, stream=None):
+    """Copy page moves[i, 0] over page moves[i, 1] in a cache (kv_codes uint8 [slots, 576],
+    kv_scales f32 [slots, 2]) or in every layer of a stack of them ([layers, slots, ...])."""
+    if isinstance(kv_codes, torch.Tensor) and kv_codes.dim() == 3:
+        _need(kv_codes, "kv_codes", torch.uint8, 3)
+        _need(kv_scales, "kv_scales", torch.float32, 3)
+        if kv_codes.shape[2] != KV8_D or tuple(kv_scales.shape) != (*kv_codes.shape[:2], 2):
+            raise ValueError("kv_codes must be [layers,slots,576] and kv_scales [layers,slots,2]")
+        if kv_codes.shape[0] == 0:
+            raise ValueError("kv_codes must have at least one layer")
+        layers, slots = kv_codes.shape[:2]
+    else:
+        _need_cache(kv_codes, kv_scales)
+        layers, slots = 1, kv_codes.shape[0]
+    _need(moves, "moves", torch.int32, 2)
+    if moves.shape[1] != 2:
+        raise ValueError("moves must be [n, 2]")
+    if n_moves is not None:
+        _need(n_moves, "n_moves", torch.int32, 1)
+        if n_moves.numel() < 1:
+            raise ValueError("n_moves must have one entry")
+    _need_err(err_word)
+    with _on_device_of(kv_codes, kv_scales, moves, n_moves, err_word):
+        st = lib().kv8_pages_copy(_ptr(kv_codes), _ptr(kv_scales), layers, slots, _ptr(moves),
+                                  _ptr(n_moves), moves.shape[0], _ptr(err_word), _stream(stream))
+    _check("kv8_pages_copy", st)
 
 
 # ----------------------------------------------------------------- cache file

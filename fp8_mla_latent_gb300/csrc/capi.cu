@@ -119,7 +119,7 @@ bool valid_scale(float s) { return s > 0.0f && s <= 3.0e38f; }
 
 extern "C" {
 
-int kv8_abi_version(void) { return 101; }
+int kv8_abi_version(void) { return 102; }
 
 const char* kv8_last_cuda_error(void) { return cudaGetErrorName(g_last_cuda_error); }
 
@@ -426,6 +426,179 @@ int kv8_noalloc_error(void* stream) {
   const int st = noalloc_scratch(&scratch);
   if (st != KV8_OK) return st;
   return kv8_workspace_error(scratch, stream);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Attention of a chunk of new tokens, and the pages of the cache.
+
+extern "C" {
+
+int64_t mla_absorb_chunk_fp8_batch_workspace_size(int B, int H, int64_t total_q, int max_blocks) {
+  if (B < 0 || H < 1 || H > 1024 || max_blocks < 1 || max_blocks >= (1 << 25) || total_q < 0 ||
+      total_q * H > INT32_MAX)
+    return -1;
+  return chunk_workspace(B, H, total_q, max_blocks);
+}
+
+int mla_absorb_chunk_fp8_batch(const uint16_t* q_lat, int64_t q_lat_token_stride,
+                               int64_t q_lat_head_stride, const uint16_t* q_rope,
+                               int64_t q_rope_token_stride, int64_t q_rope_head_stride,
+                               const uint8_t* kv_codes, const float* kv_scales,
+                               const int32_t* block_table, const int32_t* seq_lens,
+                               const int32_t* q_start, int64_t total_q, int B, int H,
+                               int max_blocks, int block_size, int64_t n_blocks, int causal,
+                               float sm_scale, uint16_t* out, float* lse, void* workspace,
+                               int64_t workspace_bytes, void* stream) {
+  const int64_t need = mla_absorb_chunk_fp8_batch_workspace_size(B, H, total_q, max_blocks);
+  if (need < 0 || n_blocks < 1 || !valid_scale(sm_scale)) return KV8_EINVAL;
+  const int64_t strides[4] = {q_lat_token_stride, q_lat_head_stride, q_rope_token_stride,
+                              q_rope_head_stride};
+  for (int64_t v : strides)
+    if (v < 0) return KV8_EINVAL;
+  if (block_size != KV8_BLOCK) return KV8_EUNSUPPORTED;
+  if (B == 0 || total_q == 0) return KV8_OK;
+  if (q_lat == nullptr || q_rope == nullptr || kv_codes == nullptr || kv_scales == nullptr ||
+      block_table == nullptr || seq_lens == nullptr || q_start == nullptr || out == nullptr)
+    return KV8_EINVAL;
+  for (int64_t v : strides)
+    if (v % 8 != 0) return KV8_EALIGN;
+  if (!aligned(q_lat, 16) || !aligned(q_rope, 16) || !aligned(kv_codes, 16) ||
+      !aligned(kv_scales, 16) || !aligned(block_table, 4) || !aligned(seq_lens, 4) ||
+      !aligned(q_start, 4) || !aligned(out, 16) || !aligned(lse, 4))
+    return KV8_EALIGN;
+  if (workspace == nullptr || workspace_bytes < need) return KV8_EWORKSPACE;
+  if (!aligned(workspace, 256)) return KV8_EALIGN;
+  ChunkArgs a{};
+  a.q_lat = q_lat;
+  a.q_rope = q_rope;
+  a.ql_t = q_lat_token_stride;
+  a.ql_h = q_lat_head_stride;
+  a.qr_t = q_rope_token_stride;
+  a.qr_h = q_rope_head_stride;
+  a.codes = kv_codes;
+  a.scales = kv_scales;
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.q_start = q_start;
+  a.total_q = total_q;
+  a.n_blocks = n_blocks;
+  a.B = B;
+  a.H = H;
+  a.max_blocks = max_blocks;
+  a.causal = causal != 0;
+  a.sm_scale = sm_scale;
+  a.out = out;
+  a.lse = lse;
+  const cudaError_t e = launch_chunk(a, workspace, static_cast<cudaStream_t>(stream));
+  if (e == cudaSuccess) return KV8_OK;
+  g_last_cuda_error = e;
+  return e == cudaErrorNotSupported ? KV8_EUNSUPPORTED : KV8_ECUDA;
+}
+
+}  // extern "C"
+
+namespace {
+
+// The checks that every call on a page table makes.
+int page_table(PageTable& t, int32_t* block_table, int32_t* seq_lens, int32_t* page_refs, int B,
+               int max_blocks, int64_t n_blocks, const unsigned* err_word) {
+  if (B < 1 || max_blocks < 1 || max_blocks >= (1 << 25) || n_blocks < 1) return KV8_EINVAL;
+  if (block_table == nullptr || seq_lens == nullptr || page_refs == nullptr) return KV8_EINVAL;
+  if (B > KV8_PAGES_MAX_SEQS || n_blocks > KV8_PAGES_MAX_BLOCKS) return KV8_EUNSUPPORTED;
+  if (!aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(page_refs, 4) ||
+      !aligned(err_word, 4))
+    return KV8_EALIGN;
+  t.block_table = block_table;
+  t.seq_lens = seq_lens;
+  t.page_refs = page_refs;
+  t.B = B;
+  t.max_blocks = max_blocks;
+  t.n_blocks = n_blocks;
+  return KV8_OK;
+}
+
+int launched(cudaError_t e) {
+  if (e != cudaSuccess) g_last_cuda_error = e;
+  return e == cudaSuccess ? KV8_OK : KV8_ECUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+int kv8_pages_append(int32_t* block_table, int32_t* seq_lens, int32_t* page_refs, int B,
+                     int max_blocks, int64_t n_blocks, const int32_t* n_new, int32_t* q_start,
+                     int64_t* dst_slot, int64_t cap, unsigned* err_word, void* stream) {
+  PageTable t;
+  const int st = page_table(t, block_table, seq_lens, page_refs, B, max_blocks, n_blocks, err_word);
+  if (st != KV8_OK) return st;
+  if (cap < 0 || cap > INT32_MAX || n_new == nullptr || q_start == nullptr ||
+      (cap > 0 && dst_slot == nullptr))
+    return KV8_EINVAL;
+  if (!aligned(n_new, 4) || !aligned(q_start, 4) || !aligned(dst_slot, 8)) return KV8_EALIGN;
+  return launched(launch_pages_append(t, n_new, q_start, dst_slot, cap, err_word,
+                                      static_cast<cudaStream_t>(stream)));
+}
+
+int kv8_pages_fork(int32_t* block_table, int32_t* seq_lens, int32_t* page_refs, int B,
+                   int max_blocks, int64_t n_blocks, const int32_t* src_seq,
+                   const int32_t* dst_seq, const int32_t* fork_len, int n, int32_t* moves,
+                   int32_t* n_moves, unsigned* err_word, void* stream) {
+  PageTable t;
+  const int st = page_table(t, block_table, seq_lens, page_refs, B, max_blocks, n_blocks, err_word);
+  if (st != KV8_OK) return st;
+  if (n < 0 || n_moves == nullptr ||
+      (n > 0 && (src_seq == nullptr || dst_seq == nullptr || moves == nullptr)))
+    return KV8_EINVAL;
+  if (n > KV8_PAGES_MAX_SEQS) return KV8_EUNSUPPORTED;
+  if (!aligned(src_seq, 4) || !aligned(dst_seq, 4) || !aligned(fork_len, 4) || !aligned(moves, 4) ||
+      !aligned(n_moves, 4))
+    return KV8_EALIGN;
+  return launched(launch_pages_fork(t, src_seq, dst_seq, fork_len, n, moves, n_moves, err_word,
+                                    static_cast<cudaStream_t>(stream)));
+}
+
+int kv8_pages_free(int32_t* block_table, int32_t* seq_lens, int32_t* page_refs, int B,
+                   int max_blocks, int64_t n_blocks, const int32_t* seq, int n,
+                   unsigned* err_word, void* stream) {
+  PageTable t;
+  const int st = page_table(t, block_table, seq_lens, page_refs, B, max_blocks, n_blocks, err_word);
+  if (st != KV8_OK) return st;
+  if (n < 0 || (n > 0 && seq == nullptr)) return KV8_EINVAL;
+  if (n > KV8_PAGES_MAX_SEQS) return KV8_EUNSUPPORTED;
+  if (!aligned(seq, 4)) return KV8_EALIGN;
+  if (n == 0) return KV8_OK;
+  return launched(launch_pages_free(t, seq, n, err_word, static_cast<cudaStream_t>(stream)));
+}
+
+int kv8_pages_compact(int32_t* block_table, const int32_t* seq_lens, int32_t* page_refs, int B,
+                      int max_blocks, int64_t n_blocks, int32_t* moves, int32_t* n_moves,
+                      int32_t* n_live, unsigned* err_word, void* stream) {
+  PageTable t;
+  const int st = page_table(t, block_table, const_cast<int32_t*>(seq_lens), page_refs, B,
+                            max_blocks, n_blocks, err_word);
+  if (st != KV8_OK) return st;
+  if (n_moves == nullptr || (n_blocks > 1 && moves == nullptr)) return KV8_EINVAL;
+  if (!aligned(moves, 4) || !aligned(n_moves, 4) || !aligned(n_live, 4)) return KV8_EALIGN;
+  return launched(launch_pages_compact(t, moves, n_moves, n_live, err_word,
+                                       static_cast<cudaStream_t>(stream)));
+}
+
+int kv8_pages_copy(uint8_t* kv_codes, float* kv_scales, int n_layers, int64_t n_slots,
+                   const int32_t* moves, const int32_t* n_moves, int64_t max_moves,
+                   unsigned* err_word, void* stream) {
+  if (n_layers < 1 || n_slots < KV8_BLOCK || max_moves < 0 || max_moves > INT32_MAX) return KV8_EINVAL;
+  if (n_layers > 1 && n_slots % KV8_BLOCK != 0) return KV8_EINVAL;
+  if (n_slots / KV8_BLOCK > KV8_PAGES_MAX_BLOCKS) return KV8_EUNSUPPORTED;
+  if (max_moves == 0) return KV8_OK;
+  if (kv_codes == nullptr || kv_scales == nullptr || moves == nullptr) return KV8_EINVAL;
+  if (!aligned(kv_codes, 16) || !aligned(kv_scales, 16) || !aligned(moves, 4) ||
+      !aligned(n_moves, 4) || !aligned(err_word, 4))
+    return KV8_EALIGN;
+  return launched(launch_pages_copy(kv_codes, kv_scales, n_layers, n_slots, moves, n_moves,
+                                    max_moves, err_word, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

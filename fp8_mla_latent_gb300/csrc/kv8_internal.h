@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "fp8mla.h"
+
 #include <atomic>
 #include <utility>
 
@@ -143,6 +145,47 @@ cudaError_t launch_produce(const float* src, int64_t n_rows, int64_t stride, con
 cudaError_t launch_prefill(const uint8_t* codes, const float* scales, const int64_t* slots,
                            int64_t n_slots, int64_t T, const uint16_t* w, int N, uint16_t* y,
                            float* k_rope, unsigned* err, cudaStream_t s);
+
+// A page table and its reference counts (pages.cu).
+struct PageTable {
+  int32_t* block_table;  // [B][max_blocks]
+  int32_t* seq_lens;     // [B]
+  int32_t* page_refs;    // [n_blocks] held entries naming the page; 0 = free
+  int B, max_blocks;
+  int64_t n_blocks;
+};
+cudaError_t launch_pages_append(const PageTable& t, const int32_t* n_new, int32_t* q_start, int64_t* dst_slot,
+                                int64_t cap, unsigned* err, cudaStream_t s);
+cudaError_t launch_pages_fork(const PageTable& t, const int32_t* src, const int32_t* dst, const int32_t* fork_len,
+                              int n, int32_t* moves, int32_t* n_moves, unsigned* err, cudaStream_t s);
+cudaError_t launch_pages_free(const PageTable& t, const int32_t* seq, int n, unsigned* err, cudaStream_t s);
+cudaError_t launch_pages_compact(const PageTable& t, int32_t* moves, int32_t* n_moves, int32_t* n_live, unsigned* err,
+                                 cudaStream_t s);
+cudaError_t launch_pages_copy(uint8_t* codes, float* scales, int n_layers, int64_t n_slots, const int32_t* moves,
+                              const int32_t* n_moves, int64_t max_moves, unsigned* err, cudaStream_t s);
+
+// The attention of a chunk of new tokens (chunk.cu).  Rows of a sequence are its
+// (token, head) pairs, token after token.
+struct ChunkArgs {
+  const uint16_t* q_lat;       // bf16 [total_q][H][512], strides in elements
+  const uint16_t* q_rope;      // bf16 [total_q][H][64]
+  int64_t ql_t, ql_h, qr_t, qr_h;
+  const uint8_t* codes;        // [n_blocks * 64][576]
+  const float* scales;         // [n_blocks * 64][2]
+  const int32_t* block_table;  // [B][max_blocks]
+  const int32_t* seq_lens;     // [B]
+  const int32_t* q_start;      // [B + 1]
+  int64_t total_q, n_blocks;
+  int B, H, max_blocks, causal;
+  float sm_scale;
+  uint16_t* out;               // bf16 [total_q][H][512]
+  float* lse;                  // [total_q][H] or nullptr
+  unsigned* err;               // workspace header word
+};
+// Bytes of workspace (deterministic in its arguments), and the call on them.
+int64_t chunk_workspace(int B, int H, int64_t total_q, int max_blocks);
+cudaError_t launch_chunk(ChunkArgs a, void* workspace, cudaStream_t s);
+
 cudaError_t launch_wait_timeout(unsigned* err, uint64_t limit_ns, cudaStream_t s);
 cudaError_t launch_wuv(const float* o, const uint16_t* w, int B, int H, int V, float* y,
                        cudaStream_t s);

@@ -1,0 +1,668 @@
+// pages.cu -- the pages of a paged fp8 latent cache: sequences that grow
+// (append), share a prefix (fork), leave (free), a pool that is packed (compact),
+// and the page data those steps ask to be moved (copy).  The page tables and the
+// reference counts live in device memory and every step runs on the device, so a
+// serving loop needs no host round trip between a step and the attention after it.
+//
+// State (caller's): block_table int32 [B][max_blocks], seq_lens int32 [B] and
+// page_refs int32 [n_blocks], the number of held table entries that name a page
+// (0 = free).  A sequence holds its first ceil(seq_len / 64) entries.  Free pages
+// are taken lowest index first, in the order of the sequences, so every result is
+// the same on every run.
+//
+// The table steps are one launch each of one thread-block cluster, at most
+// PG_CTAS CTAs of 1024 threads: a step is a validation that must be complete
+// before anything is written (all or nothing), a ranking of the free pages, and a
+// walk over table entries; the cluster barrier separates them without a second
+// launch, and what they read (a few hundred KB at most) bounds nothing: they are
+// launch latency and dependent L2 round trips (about 1 us each).  A CTA count of
+// one is kept while the entries to walk fit one pass of one CTA.
+//
+// The copy is the only step that moves real data: 2 x 37376 bytes per page and
+// layer, an HBM stream.  Bulk copies through a shared-memory ring, issued by one
+// thread per CTA, keep about 15 MB in flight over 152 SMs.
+#include "kv8_common.cuh"
+#include "tc_ptx.cuh"
+
+namespace kv8 {
+namespace {
+
+using namespace ptx;
+
+constexpr int PG_THREADS = 1024;
+constexpr int PG_WARPS = PG_THREADS / 32;
+constexpr int PG_CTAS = 8;        // largest portable cluster
+constexpr int PG_ROUNDS = 16;     // pages per lane and pass: 16384 of one CTA
+constexpr int ONE_PASS = 8 * PG_THREADS;  // entries one CTA walks before a cluster pays
+
+__device__ __forceinline__ uint32_t cluster_ctas() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+
+// The cluster barrier, from warps made to converge first; it also orders the
+// CTAs' global and shared memory accesses.
+__device__ __forceinline__ void all_ctas_sync() {
+  __syncthreads();
+  cluster_sync();
+}
+
+__device__ __forceinline__ void flag(unsigned* err, unsigned bit) {
+  if (err != nullptr) atomicOr(err, bit);
+}
+
+__device__ __forceinline__ int pages_of(int64_t tokens) { return (int)((tokens + PAGE - 1) / PAGE); }
+
+// Inclusive sum over the CTA (every thread); *total gets the CTA's sum.  `tmp`
+// holds PG_WARPS + 1 values and may be used again right after.
+__device__ __forceinline__ int64_t cta_scan(int64_t v, int64_t* tmp, int64_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  if (lane == 31) tmp[warp] = v;
+  __syncthreads();
+  if (warp == 0) {
+    int64_t w = tmp[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t u = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += u;
+    }
+    tmp[lane] = w;
+  }
+  __syncthreads();
+  if (warp > 0) v += tmp[warp - 1];
+  *total = tmp[PG_WARPS - 1];
+  __syncthreads();
+  return v;
+}
+
+// One pass over pages [lo, lo + PG_THREADS * PG_ROUNDS) cut at `hi`: lane masks of
+// the pages for which `is(refs[p], p)` holds, in index order.  Warp w takes 32 *
+// PG_ROUNDS consecutive pages, 32 at a time; every load of the pass is in flight
+// at once.  Returns the rank of the warp's first match (over the CTA), the CTA's
+// matches in *total and the warp's masks in m.
+template <typename F>
+__device__ __forceinline__ int64_t rank_pages(const int32_t* refs, int64_t lo, int64_t hi, F is,
+                                              uint32_t (&m)[PG_ROUNDS], int64_t* tmp, int64_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t p0 = lo + (int64_t)warp * 32 * PG_ROUNDS + lane;
+  int32_t r[PG_ROUNDS];
+#pragma unroll
+  for (int j = 0; j < PG_ROUNDS; ++j) r[j] = p0 + 32 * j < hi ? refs[p0 + 32 * j] : 0;
+  int n = 0;
+#pragma unroll
+  for (int j = 0; j < PG_ROUNDS; ++j) {
+    const int64_t p = p0 + 32 * j;
+    m[j] = __ballot_sync(0xffffffffu, p < hi && is(r[j], p));
+    n += __popc(m[j]);
+  }
+  const int64_t inc = cta_scan(lane == 0 ? n : 0, tmp, total);
+  return __shfl_sync(0xffffffffu, inc, 0) - n;
+}
+
+// The pages of a pass in rank order: f(rank, page), on the lane that holds it.
+template <typename F>
+__device__ __forceinline__ void each_ranked(int64_t rank, int64_t lo, const uint32_t (&m)[PG_ROUNDS], F f) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t below = (1u << lane) - 1u;
+#pragma unroll
+  for (int j = 0; j < PG_ROUNDS; ++j) {
+    if ((m[j] >> lane) & 1u)
+      f(rank + __popc(m[j] & below), lo + (int64_t)warp * 32 * PG_ROUNDS + 32 * j + lane);
+    rank += __popc(m[j]);
+  }
+}
+
+constexpr int64_t PASS_PAGES = (int64_t)PG_THREADS * PG_ROUNDS;
+
+// Whether the pool has `need` free pages (CTA-wide; reads no further than it must).
+__device__ __forceinline__ bool enough_free(const int32_t* refs, int64_t n_blocks, int64_t need, int64_t* tmp) {
+  int64_t got = 0;
+  for (int64_t lo = 0; lo < n_blocks && got < need; lo += PASS_PAGES) {
+    uint32_t m[PG_ROUNDS];
+    int64_t total;
+    (void)rank_pages(refs, lo, n_blocks, [](int32_t r, int64_t) { return r == 0; }, m, tmp, &total);
+    got += total;
+  }
+  return got >= need;
+}
+// The first `need` free pages: f(rank, page).
+template <typename F>
+__device__ __forceinline__ void take_free(const int32_t* refs, int64_t n_blocks, int64_t need, int64_t* tmp, F f) {
+  int64_t got = 0;
+  for (int64_t lo = 0; lo < n_blocks && got < need; lo += PASS_PAGES) {
+    uint32_t m[PG_ROUNDS];
+    int64_t total;
+    const int64_t rank =
+        rank_pages(refs, lo, n_blocks, [](int32_t r, int64_t) { return r == 0; }, m, tmp, &total);
+    each_ranked(got + rank, lo, m, [&](int64_t k, int64_t p) {
+      if (k < need) f(k, p);
+    });
+    got += total;
+  }
+}
+
+// The last index i of the ascending a[0..n] with a[i] <= x (a[0] <= x < a[n]).
+template <typename T>
+__device__ __forceinline__ int last_le(const T* a, int n, int64_t x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if ((int64_t)a[mid] <= x) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// ------------------------------------------------------------------ append
+// need_b = ceil((len + new) / 64) - ceil(len / 64) pages for sequence b.  CTA 0
+// validates, ranks and writes table, counts, lengths and q_start; then every CTA
+// writes a share of dst_slot (token i of sequence b at position len + i).
+__global__ void __launch_bounds__(PG_THREADS)
+append_kernel(PageTable t, const int32_t* __restrict__ n_new, int32_t* q_start, int64_t* dst_slot,
+              int64_t cap, unsigned* err) {
+  extern __shared__ int32_t first[];  // CTA 0: [B + 1] pages taken before sequence b
+  __shared__ int64_t tmp[PG_WARPS + 1];
+  __shared__ unsigned bad;
+  const int B = t.B;
+  if (cluster_rank() == 0) {
+    if (threadIdx.x == 0) bad = 0;
+    __syncthreads();
+    int64_t tokens = 0, pages = 0;
+    for (int b0 = 0; b0 < B; b0 += PG_THREADS) {
+      const int b = b0 + threadIdx.x;
+      int64_t fresh = 0, need = 0;
+      if (b < B) {
+        const int64_t len = t.seq_lens[b], nn = n_new[b];
+        if (len < 0 || nn < 0 || len > (int64_t)t.max_blocks * PAGE) {
+          atomicOr(&bad, KV8_PAGES_EINDEX);
+        } else if (nn > 0) {
+          fresh = nn;
+          if (len + nn > (int64_t)t.max_blocks * PAGE) {
+            atomicOr(&bad, KV8_PAGES_ENOROOM);
+          } else {
+            need = pages_of(len + nn) - pages_of(len);
+            if (len % PAGE != 0) {  // the tokens begin in a page that is this sequence's alone
+              const int32_t p = t.block_table[(int64_t)b * t.max_blocks + pages_of(len) - 1];
+              if (p < 0 || p >= t.n_blocks || t.page_refs[p] != 1) atomicOr(&bad, KV8_PAGES_EINDEX);
+            }
+          }
+        }
+      }
+      int64_t sum_t, sum_p;
+      const int64_t inc_t = cta_scan(fresh, tmp, &sum_t), inc_p = cta_scan(need, tmp, &sum_p);
+      if (b < B) {
+        const int64_t at = tokens + inc_t - fresh, pg = pages + inc_p - need;
+        q_start[b] = (int32_t)(at < INT32_MAX ? at : INT32_MAX);
+        first[b] = (int32_t)(pg < INT32_MAX ? pg : INT32_MAX);
+      }
+      tokens += sum_t;
+      pages += sum_p;
+    }
+    if (threadIdx.x == 0) {
+      if (tokens > cap || pages > t.n_blocks) bad |= KV8_PAGES_ENOROOM;
+      q_start[B] = (int32_t)(tokens < INT32_MAX ? tokens : INT32_MAX);
+      first[B] = (int32_t)(pages < INT32_MAX ? pages : INT32_MAX);
+    }
+    __syncthreads();
+    if (bad == 0 && !enough_free(t.page_refs, t.n_blocks, pages, tmp)) {
+      if (threadIdx.x == 0) bad = KV8_PAGES_ENOROOM;
+      __syncthreads();
+    }
+    if (bad != 0) {
+      // nothing is taken, and the call hands out no token
+      if (threadIdx.x == 0) flag(err, bad);
+      for (int b = threadIdx.x; b <= B; b += PG_THREADS) q_start[b] = 0;
+    } else {
+      take_free(t.page_refs, t.n_blocks, pages, tmp, [&](int64_t k, int64_t p) {
+        const int b = last_le(first, B, k);
+        const int col = pages_of(t.seq_lens[b]) + (int)(k - first[b]);
+        t.block_table[(int64_t)b * t.max_blocks + col] = (int32_t)p;
+        t.page_refs[p] = 1;
+      });
+      __syncthreads();  // every owner was found by the old lengths
+      for (int b = threadIdx.x; b < B; b += PG_THREADS) t.seq_lens[b] += n_new[b];
+    }
+  }
+  all_ctas_sync();
+  const int64_t total = q_start[B];
+  const int64_t stride = (int64_t)cluster_ctas() * PG_THREADS;
+  for (int64_t i = (int64_t)cluster_rank() * PG_THREADS + threadIdx.x; i < cap; i += stride) {
+    int64_t slot = -1;
+    if (i < total) {
+      const int b = last_le(q_start, B, i);
+      const int64_t pos = (int64_t)t.seq_lens[b] - n_new[b] + (i - q_start[b]);
+      slot = (int64_t)t.block_table[(int64_t)b * t.max_blocks + pos / PAGE] * PAGE + pos % PAGE;
+    }
+    dst_slot[i] = slot;
+  }
+}
+
+// ------------------------------------------------------------------ fork
+// dst row := the first entries of src row; whole pages are shared, a last page
+// that is only part full is copied to a fresh page (one move), so that a page in
+// which tokens are still written belongs to one sequence.  CTA 0 validates and
+// takes the fresh pages; then a warp per fork walks its entries, over all CTAs.
+__global__ void __launch_bounds__(PG_THREADS)
+fork_kernel(PageTable t, const int32_t* __restrict__ src, const int32_t* __restrict__ dst,
+            const int32_t* __restrict__ fork_len, int n, int32_t* moves, int32_t* n_moves, unsigned* err) {
+  extern __shared__ unsigned role[];  // CTA 0: [B] 1 = a destination, 2 = a source; then [n + 1] fresh pages before fork i
+  __shared__ int64_t tmp[PG_WARPS + 1];
+  __shared__ unsigned bad;
+  __shared__ unsigned go;
+  const int B = t.B;
+  const int lane = threadIdx.x & 31;
+  int32_t* first = reinterpret_cast<int32_t*>(role + B);
+  if (cluster_rank() == 0) {
+    if (threadIdx.x == 0) bad = 0;
+    for (int b = threadIdx.x; b < B; b += PG_THREADS) role[b] = 0;
+    __syncthreads();
+    int64_t pages = 0;
+    for (int i0 = 0; i0 < n; i0 += PG_THREADS) {
+      const int i = i0 + threadIdx.x;
+      int64_t need = 0;
+      if (i < n) {
+        const int32_t a = src[i], d = dst[i];
+        if (a < 0 || a >= B || d < 0 || d >= B || a == d) {
+          atomicOr(&bad, KV8_PAGES_EINDEX);
+        } else {
+          const int64_t len = t.seq_lens[a], take = fork_len != nullptr ? fork_len[i] : len;
+          if (len < 0 || len > (int64_t)t.max_blocks * PAGE || take < 0 || take > len || t.seq_lens[d] != 0 ||
+              (atomicOr(&role[d], 1u) & 1u) != 0u)
+            atomicOr(&bad, KV8_PAGES_EINDEX);
+          atomicOr(&role[a], 2u);
+          need = take % PAGE != 0;
+        }
+      }
+      int64_t sum;
+      const int64_t inc = cta_scan(need, tmp, &sum);
+      if (i < n) first[i] = (int32_t)(pages + inc - need);
+      pages += sum;
+    }
+    if (threadIdx.x == 0) first[n] = (int32_t)pages;
+    __syncthreads();
+    for (int b = threadIdx.x; b < B; b += PG_THREADS)
+      if (role[b] == 3u) atomicOr(&bad, KV8_PAGES_EINDEX);
+    __syncthreads();
+    if (bad == 0 && !enough_free(t.page_refs, t.n_blocks, pages, tmp)) {
+      if (threadIdx.x == 0) bad = KV8_PAGES_ENOROOM;
+      __syncthreads();
+    }
+    if (threadIdx.x == 0) {
+      n_moves[0] = bad != 0 ? 0 : (int32_t)pages;
+      if (bad != 0) flag(err, bad);
+      go = bad == 0;
+    }
+    if (bad == 0) {
+      take_free(t.page_refs, t.n_blocks, pages, tmp, [&](int64_t k, int64_t p) {
+        // forks without a fresh page repeat their successor's count: the last of equal counts owns it
+        const int i = last_le(first, n, k);
+        const int64_t take = fork_len != nullptr ? fork_len[i] : t.seq_lens[src[i]];
+        const int col = pages_of(take) - 1;
+        moves[2 * k] = t.block_table[(int64_t)src[i] * t.max_blocks + col];
+        moves[2 * k + 1] = (int32_t)p;
+        t.block_table[(int64_t)dst[i] * t.max_blocks + col] = (int32_t)p;
+        t.page_refs[p] = 1;
+      });
+    }
+  }
+  all_ctas_sync();  // CTA 0's writes, and `go` there
+  uint32_t ok;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(ok) : "r"(map_to(smem_u32(&go), 0)) : "memory");
+  if (ok != 0u) {
+    const int warps = (int)cluster_ctas() * PG_WARPS;
+    for (int i = (int)cluster_rank() * PG_WARPS + (threadIdx.x >> 5); i < n; i += warps) {
+      const int64_t take = fork_len != nullptr ? fork_len[i] : t.seq_lens[src[i]];
+      const int32_t* from = t.block_table + (int64_t)src[i] * t.max_blocks;
+      int32_t* to = t.block_table + (int64_t)dst[i] * t.max_blocks;
+      for (int64_t c = lane; c < take / PAGE; c += 32) {
+        const int32_t p = from[c];
+        to[c] = p;
+        if (p >= 0 && p < t.n_blocks) atomicAdd(&t.page_refs[p], 1); else flag(err, KV8_PAGES_EINDEX);
+      }
+      if (lane == 0) {
+        t.seq_lens[dst[i]] = (int32_t)take;
+        if (take % PAGE != 0) {
+          const int32_t p = from[take / PAGE];
+          if (p < 0 || p >= t.n_blocks) flag(err, KV8_PAGES_EINDEX);
+        }
+      }
+    }
+  }
+  all_ctas_sync();  // CTA 0's shared memory is read above
+}
+
+// ------------------------------------------------------------------ free
+// Every CTA validates the list by itself (it reads nothing that the call writes);
+// then a warp per sequence gives its pages back, over all CTAs.
+__global__ void __launch_bounds__(PG_THREADS)
+free_kernel(PageTable t, const int32_t* __restrict__ seq, int n, unsigned* err) {
+  extern __shared__ unsigned role[];  // [B]
+  __shared__ unsigned bad;
+  const int B = t.B, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) bad = 0;
+  for (int b = threadIdx.x; b < B; b += PG_THREADS) role[b] = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += PG_THREADS) {
+    const int32_t b = seq[i];
+    if (b < 0 || b >= B || atomicOr(&role[b], 1u) != 0u) atomicOr(&bad, KV8_PAGES_EINDEX);
+  }
+  __syncthreads();
+  if (bad != 0) {
+    if (cluster_rank() == 0 && threadIdx.x == 0) flag(err, bad);
+    return;
+  }
+  const int warps = (int)cluster_ctas() * PG_WARPS;
+  for (int i = (int)cluster_rank() * PG_WARPS + (threadIdx.x >> 5); i < n; i += warps) {
+    const int b = seq[i];
+    int64_t len = t.seq_lens[b];
+    if (len < 0 || len > (int64_t)t.max_blocks * PAGE) {
+      if (lane == 0) flag(err, KV8_PAGES_EINDEX);
+      len = len < 0 ? 0 : (int64_t)t.max_blocks * PAGE;
+    }
+    int32_t* row = t.block_table + (int64_t)b * t.max_blocks;
+    for (int c = lane; c < pages_of(len); c += 32) {
+      const int32_t p = row[c];
+      row[c] = -1;
+      if (p < 0 || p >= t.n_blocks) {
+        flag(err, KV8_PAGES_EINDEX);
+      } else if (atomicSub(&t.page_refs[p], 1) <= 0) {
+        atomicAdd(&t.page_refs[p], 1);  // held by no count: left at what it was
+        flag(err, KV8_PAGES_EINDEX);
+      }
+    }
+    __syncwarp();
+    if (lane == 0) t.seq_lens[b] = 0;
+  }
+}
+
+// ------------------------------------------------------------------ compact
+// With L live pages, the k-th live page at or above L moves to the k-th free page
+// below L: as few moves as can be, no page both source and destination.  Each CTA
+// ranks its share of the pool; moves ascend by source, so a table entry finds its
+// new page by bisection.
+__global__ void __launch_bounds__(PG_THREADS)
+compact_kernel(PageTable t, int32_t* moves, int32_t* n_moves, int32_t* n_live, unsigned* err) {
+  __shared__ int64_t tmp[PG_WARPS + 1];
+  __shared__ int64_t count[3];  // this CTA's live pages, holes below L, movers from L on
+  const int nc = (int)cluster_ctas(), rank = (int)cluster_rank();
+  const int64_t share = ((t.n_blocks + nc - 1) / nc + 31) / 32 * 32;
+  const int64_t lo = rank * share < t.n_blocks ? rank * share : t.n_blocks;
+  const int64_t hi = lo + share < t.n_blocks ? lo + share : t.n_blocks;
+  auto shared_of = [&](int k, int r) -> int64_t {
+    uint64_t v;
+    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(map_to(smem_u32(&count[k]), r)) : "memory");
+    return (int64_t)v;
+  };
+  auto tally = [&](auto is) -> int64_t {
+    int64_t n = 0;
+    for (int64_t p = lo; p < hi; p += PASS_PAGES) {
+      uint32_t m[PG_ROUNDS];
+      int64_t total;
+      (void)rank_pages(t.page_refs, p, hi, is, m, tmp, &total);
+      n += total;
+    }
+    return n;
+  };
+  int64_t n = tally([](int32_t r, int64_t) { return r > 0; });
+  if (threadIdx.x == 0) count[0] = n;
+  all_ctas_sync();
+  int64_t L = 0;
+  for (int r = 0; r < nc; ++r) L += shared_of(0, r);
+  auto hole = [L](int32_t r, int64_t p) { return r <= 0 && p < L; };
+  auto mover = [L](int32_t r, int64_t p) { return r > 0 && p >= L; };
+  const int64_t nh = tally(hole), nm = tally(mover);
+  if (threadIdx.x == 0) {
+    count[1] = nh;
+    count[2] = nm;
+  }
+  all_ctas_sync();
+  int64_t h0 = 0, m0 = 0, N = 0;
+  for (int r = 0; r < nc; ++r) {
+    if (r < rank) {
+      h0 += shared_of(1, r);
+      m0 += shared_of(2, r);
+    }
+    N += shared_of(2, r);
+  }
+  for (int64_t p = lo; p < hi; p += PASS_PAGES) {
+    uint32_t m[PG_ROUNDS];
+    int64_t total;
+    int64_t k = rank_pages(t.page_refs, p, hi, hole, m, tmp, &total);
+    each_ranked(h0 + k, p, m, [&](int64_t i, int64_t page) { moves[2 * i + 1] = (int32_t)page; });
+    h0 += total;
+    k = rank_pages(t.page_refs, p, hi, mover, m, tmp, &total);
+    each_ranked(m0 + k, p, m, [&](int64_t i, int64_t page) { moves[2 * i] = (int32_t)page; });
+    m0 += total;
+  }
+  if (rank == 0 && threadIdx.x == 0) {
+    n_moves[0] = (int32_t)N;
+    if (n_live != nullptr) n_live[0] = (int32_t)L;
+  }
+  all_ctas_sync();  // the moves are written, and every count read
+  const int64_t me = (int64_t)rank * PG_THREADS + threadIdx.x, all = (int64_t)nc * PG_THREADS;
+  // held entries first: they are told live from free by the old counts
+  const int64_t entries = (int64_t)t.B * t.max_blocks;
+  for (int64_t e = me; e < entries; e += all) {
+    const int b = (int)(e / t.max_blocks);
+    int64_t len = t.seq_lens[b];
+    const bool off = len < 0 || len > (int64_t)t.max_blocks * PAGE;
+    if (off) len = len < 0 ? 0 : (int64_t)t.max_blocks * PAGE;
+    if (e - (int64_t)b * t.max_blocks >= pages_of(len)) {
+      if (off) flag(err, KV8_PAGES_EINDEX);
+      continue;
+    }
+    const int32_t p = t.block_table[e];
+    if (off || p < 0 || p >= t.n_blocks || t.page_refs[p] <= 0) {
+      flag(err, KV8_PAGES_EINDEX);
+    } else if (p >= L) {
+      int64_t a = 0, z = N;  // the move whose source is p
+      while (z - a > 1) {
+        const int64_t mid = (a + z) >> 1;
+        if (moves[2 * mid] <= p) a = mid; else z = mid;
+      }
+      t.block_table[e] = moves[2 * a + 1];
+    }
+  }
+  all_ctas_sync();
+  for (int64_t k = me; k < N; k += all) {
+    const int32_t s = moves[2 * k], d = moves[2 * k + 1];
+    t.page_refs[d] = t.page_refs[s];
+    t.page_refs[s] = 0;
+  }
+}
+
+// ------------------------------------------------------------------ copy
+// Tasks of one third of a page's codes (12288 bytes; the first third also takes
+// the page's 512 bytes of scales), pair after pair, layer after layer; each CTA
+// takes a contiguous range of them.  One thread runs the ring: loads COPY_AHEAD
+// tasks ahead, a store as soon as its load has landed.  The other warps meanwhile
+// mark every destination in a bitmap in shared memory, so that a pair whose source
+// another pair overwrites, or whose destination is named twice, is left out
+// whatever the order in which CTAs run (the loads are harmless; stores wait for it).
+constexpr int COPY_THREADS = 256;
+constexpr int PARTS = 3;
+constexpr int PART_CODES = PAGE * D / PARTS;   // 12288
+constexpr int PAGE_SCALES = PAGE * 8;          // 512
+constexpr int SLOT = PART_CODES + PAGE_SCALES;
+constexpr int COPY_SLOTS = 7, COPY_AHEAD = 4;
+static_assert(PART_CODES % 16 == 0 && PAGE * D % PARTS == 0, "bulk copies move 16-byte units");
+constexpr int COPY_RING = COPY_SLOTS * SLOT;
+constexpr uint64_t COPY_WAIT_NS = 2000000000ull;
+
+__global__ void __launch_bounds__(COPY_THREADS)
+copy_kernel(uint8_t* codes, float* scales, int n_layers, int64_t n_slots, const int32_t* __restrict__ moves,
+            const int32_t* __restrict__ n_moves, int64_t max_moves, unsigned* err) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ uint64_t full[COPY_SLOTS];
+  __shared__ int never;
+  const int64_t n_blocks = n_slots / PAGE;
+  const int words = (int)((n_blocks + 31) / 32);
+  unsigned* named = reinterpret_cast<unsigned*>(ring + COPY_RING);
+  unsigned* twice = named + words;
+  int64_t n = max_moves;
+  if (n_moves != nullptr) {
+    n = *n_moves;
+    n = n < 0 ? 0 : (n < max_moves ? n : max_moves);
+  }
+  const int64_t tasks = n * n_layers * PARTS;
+  const int64_t f0 = tasks * blockIdx.x / gridDim.x, f1 = tasks * (blockIdx.x + 1) / gridDim.x;
+  if (f0 >= f1) return;
+  for (int w = threadIdx.x; w < 2 * words; w += COPY_THREADS) named[w] = 0;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < COPY_SLOTS; ++s) mbar_init(&full[s], 1);
+    never = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+
+  auto inside = [&](int32_t p) { return p >= 0 && p < n_blocks; };
+  struct Task { uint8_t *cs, *cd; float *ss, *sd; int32_t a, d; bool first; };
+  auto task = [&](int64_t f) {
+    Task k;
+    const int part = (int)(f % PARTS);
+    const int64_t layer = f / PARTS % n_layers, pair = f / PARTS / n_layers;
+    k.a = __ldg(&moves[2 * pair]);
+    k.d = __ldg(&moves[2 * pair + 1]);
+    const int64_t a = layer * n_slots + (int64_t)k.a * PAGE, d = layer * n_slots + (int64_t)k.d * PAGE;
+    k.cs = codes + a * D + part * PART_CODES;
+    k.cd = codes + d * D + part * PART_CODES;
+    k.ss = scales + a * 2;
+    k.sd = scales + d * 2;
+    k.first = part == 0;
+    return k;
+  };
+  auto load = [&](int64_t f) {
+    const Task k = task(f);
+    const int s = (int)((f - f0) % COPY_SLOTS);
+    const uint32_t at = smem_u32(ring + s * SLOT);
+    const bool ok = inside(k.a) && inside(k.d) && k.a != k.d;
+    mbar_arrive_expect_tx(&full[s], ok ? (uint32_t)(PART_CODES + (k.first ? PAGE_SCALES : 0)) : 0u);
+    if (ok) {
+      bulk_load_g2s(at, k.cs, PART_CODES, &full[s]);
+      if (k.first) bulk_load_g2s(at + PART_CODES, k.ss, PAGE_SCALES, &full[s]);
+    }
+  };
+  if (threadIdx.x == 0) {
+    for (int64_t f = f0; f < f1 && f < f0 + COPY_AHEAD; ++f) load(f);
+  } else {
+    for (int64_t i = threadIdx.x - 1; i < n; i += COPY_THREADS - 1) {
+      const int32_t a = __ldg(&moves[2 * i]), d = __ldg(&moves[2 * i + 1]);
+      if (inside(a) && inside(d) && a != d) {
+        const unsigned bit = 1u << (d & 31);
+        if (atomicOr(&named[d >> 5], bit) & bit) atomicOr(&twice[d >> 5], bit);
+      }
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  for (int64_t f = f0; f < f1; ++f) {
+    if (f + COPY_AHEAD < f1) {
+      // the slot of task f + COPY_AHEAD was stored from COPY_SLOTS - COPY_AHEAD tasks ago
+      asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(COPY_SLOTS - COPY_AHEAD - 1) : "memory");
+      load(f + COPY_AHEAD);
+    }
+    const int s = (int)((f - f0) % COPY_SLOTS);
+    if (!mbar_wait(&full[s], (uint32_t)((f - f0) / COPY_SLOTS & 1), &never, COPY_WAIT_NS)) {
+      flag(err, KV8_PAGES_ETIMEOUT);
+      for (int64_t g = f + 1; g < f1 && g <= f + COPY_AHEAD; ++g)  // the loads in flight land first
+        (void)mbar_wait(&full[(int)((g - f0) % COPY_SLOTS)], (uint32_t)((g - f0) / COPY_SLOTS & 1), &never,
+                        COPY_WAIT_NS);
+      break;
+    }
+    const Task k = task(f);
+    bool ok = inside(k.a) && inside(k.d) && k.a != k.d;
+    if (!inside(k.a) || !inside(k.d)) flag(err, KV8_PAGES_EINDEX);
+    if (ok && (((twice[k.d >> 5] >> (k.d & 31)) & 1u) != 0u || ((named[k.a >> 5] >> (k.a & 31)) & 1u) != 0u)) {
+      ok = false;
+      flag(err, KV8_PAGES_EINDEX);
+    }
+    if (ok) {
+      const uint32_t at = smem_u32(ring + s * SLOT);
+      bulk_store_s2g(k.cd, at, PART_CODES);
+      if (k.first) bulk_store_s2g(k.sd, at + PART_CODES, PAGE_SCALES);
+    }
+    bulk_commit();  // one group per task, empty ones too: the count above is in tasks
+  }
+  bulk_wait_all();
+}
+
+// One cluster of `ctas` CTAs.
+template <typename... P, typename... A>
+cudaError_t launch_cluster(void (*kernel)(P...), int ctas, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas, 1, 1);
+  cfg.blockDim = dim3(PG_THREADS, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// A kernel's opt-in to `bytes` of dynamic shared memory on the current device.
+template <typename K>
+cudaError_t allow_smem(std::atomic<int> (&memo)[MAX_DEVICES], K kernel, int bytes) {
+  int done = 0;
+  return per_device(memo, [&](int* v) {
+    *v = 1;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  }, &done);
+}
+
+int ctas_for(int64_t entries) { return entries <= ONE_PASS ? 1 : PG_CTAS; }
+
+}  // namespace
+
+cudaError_t launch_pages_append(const PageTable& t, const int32_t* n_new, int32_t* q_start, int64_t* dst_slot,
+                                int64_t cap, unsigned* err, cudaStream_t s) {
+  static std::atomic<int> memo[MAX_DEVICES];
+  const cudaError_t e = allow_smem(memo, append_kernel, (KV8_PAGES_MAX_SEQS + 1) * 4);
+  if (e != cudaSuccess) return e;
+  return launch_cluster(append_kernel, ctas_for(cap), (size_t)(t.B + 1) * 4, s, t, n_new, q_start, dst_slot, cap, err);
+}
+
+cudaError_t launch_pages_fork(const PageTable& t, const int32_t* src, const int32_t* dst, const int32_t* fork_len,
+                              int n, int32_t* moves, int32_t* n_moves, unsigned* err, cudaStream_t s) {
+  static std::atomic<int> memo[MAX_DEVICES];
+  const cudaError_t e = allow_smem(memo, fork_kernel, (2 * KV8_PAGES_MAX_SEQS + 1) * 4);
+  if (e != cudaSuccess) return e;
+  return launch_cluster(fork_kernel, ctas_for((int64_t)n * t.max_blocks), (size_t)(t.B + n + 1) * 4, s, t, src, dst,
+                        fork_len, n, moves, n_moves, err);
+}
+
+cudaError_t launch_pages_free(const PageTable& t, const int32_t* seq, int n, unsigned* err, cudaStream_t s) {
+  static std::atomic<int> memo[MAX_DEVICES];
+  const cudaError_t e = allow_smem(memo, free_kernel, KV8_PAGES_MAX_SEQS * 4);
+  if (e != cudaSuccess) return e;
+  return launch_cluster(free_kernel, ctas_for((int64_t)n * t.max_blocks), (size_t)t.B * 4, s, t, seq, n, err);
+}
+
+cudaError_t launch_pages_compact(const PageTable& t, int32_t* moves, int32_t* n_moves, int32_t* n_live, unsigned* err,
+                                 cudaStream_t s) {
+  const int64_t work = t.n_blocks + (int64_t)t.B * t.max_blocks;
+  return launch_cluster(compact_kernel, ctas_for(work), 0, s, t, moves, n_moves, n_live, err);
+}
+
+cudaError_t launch_pages_copy(uint8_t* codes, float* scales, int n_layers, int64_t n_slots, const int32_t* moves,
+                              const int32_t* n_moves, int64_t max_moves, unsigned* err, cudaStream_t s) {
+  static std::atomic<int> memo[MAX_DEVICES];
+  const int maps = (int)((n_slots / PAGE + 31) / 32) * 8;
+  const cudaError_t e = allow_smem(memo, copy_kernel, COPY_RING + KV8_PAGES_MAX_BLOCKS / 4);
+  if (e != cudaSuccess) return e;
+  const int64_t tasks = max_moves * n_layers * PARTS;
+  copy_kernel<<<(unsigned)(tasks < NUM_SMS ? tasks : NUM_SMS), COPY_THREADS, COPY_RING + maps, s>>>(
+      codes, scales, n_layers, n_slots, moves, n_moves, max_moves, err);
+  return cudaGetLastError();
+}
+
+}  // namespace kv8

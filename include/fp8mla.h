@@ -332,6 +332,150 @@ int mla_absorb_decode_fp8_batch_noalloc(const float* q_lat, const float* q_rope,
  * the current device, like kv8_workspace_error(). */
 int kv8_noalloc_error(void* stream);
 
+/* ---------------------------------------------------------------------------
+ * mla_absorb_chunk_fp8_batch -- absorbed attention of a chunk of new tokens per
+ * sequence over the paged cache (a prompt's next chunk, drafted tokens to check,
+ * single tokens, mixed in one batch).  The KV8 page has no counterpart; the
+ * arithmetic per (token, head) is that of mla_absorb_decode_fp8.
+ *
+ * Sequence b's new tokens are rows q_start[b] .. q_start[b + 1] - 1 of the
+ * queries, and its cache already holds them: they are the last n_b = q_start[b +
+ * 1] - q_start[b] of its seq_lens[b] tokens.  Token i of them sees keys
+ *   t < seq_lens[b] - n_b + i + 1   (causal != 0),   t < seq_lens[b]   (causal == 0);
+ * a row that sees nothing gives out = 0 and lse = -inf.  Sequences may have no
+ * query (n_b = 0).  Rows of the arrays outside [q_start[0], q_start[B]) are
+ * neither read nor written.
+ *
+ *   q_lat       device bf16 [total_q][H][512], q_rope device bf16 [total_q][H][64]:
+ *               16-byte aligned, the strides of a token and of a head given in
+ *               elements, non-negative multiples of 8.
+ *   kv_codes, kv_scales, block_table, seq_lens, block_size, n_blocks, sm_scale: as
+ *               for mla_absorb_decode_fp8_batch (the workspace reports a bad table
+ *               entry or length the same way).  Keys that a row does not see never
+ *               reach its result, whatever their bytes.
+ *   q_start     device int32 [B + 1], non-decreasing within [0, total_q].  A
+ *               sequence whose range breaks that has no query and sets the error
+ *               word (KV8_EBOUNDS).
+ *   total_q     rows of the query arrays, 0 <= total_q, total_q * H <= 2^31 - 1.
+ *   out         device bf16 [total_q][H][512], 16-byte aligned.
+ *   lse         device f32 [total_q][H] or NULL.
+ *   workspace   >= mla_absorb_chunk_fp8_batch_workspace_size(B, H, total_q,
+ *               max_blocks) bytes, 256-byte aligned; not shared by calls that
+ *               overlap in time (two replayed graphs among them).  Its error word is
+ *               read with kv8_workspace_error().
+ * Precision: a bf16 query value is held as two e4m3 terms, exactly where it is at
+ * least 2^-9 of its row's largest; each softmax weight as two e4m3 terms (relative
+ * error <= 2^-9); sums, maxima and denominators in f32; out rounded to bf16 once.
+ * lse within 2e-5 of its size or of 1.  A query row with a NaN or an infinity gives
+ * NaN.
+ * Errors: KV8_EINVAL, KV8_EALIGN, KV8_EUNSUPPORTED, KV8_EWORKSPACE, KV8_ECUDA.
+ * ------------------------------------------------------------------------- */
+int64_t mla_absorb_chunk_fp8_batch_workspace_size(int B, int H, int64_t total_q, int max_blocks);
+int mla_absorb_chunk_fp8_batch(const uint16_t* q_lat, int64_t q_lat_token_stride,
+                               int64_t q_lat_head_stride, const uint16_t* q_rope,
+                               int64_t q_rope_token_stride, int64_t q_rope_head_stride,
+                               const uint8_t* kv_codes, const float* kv_scales,
+                               const int32_t* block_table, const int32_t* seq_lens,
+                               const int32_t* q_start, int64_t total_q, int B, int H,
+                               int max_blocks, int block_size, int64_t n_blocks, int causal,
+                               float sm_scale, uint16_t* out, float* lse, void* workspace,
+                               int64_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Pages.  The calls below keep the page table of a paged cache on the device:
+ *   block_table  device int32 [B][max_blocks]; sequence b holds its first
+ *                ceil(seq_lens[b] / 64) entries, the rest is free for it to take.
+ *   seq_lens     device int32 [B].
+ *   page_refs    device int32 [n_blocks]: the number of held entries that name the
+ *                page.  0 = free.  Zeroed by the caller before the first use.
+ * Free pages are taken lowest index first, in the order of the sequences (or of the
+ * forks), so a call's result does not depend on timing.  A page that is only part
+ * full belongs to one sequence; full pages may be shared.
+ *
+ * err_word: device uint32 or NULL; a call that meets bad data sets bits in it
+ * (atomic OR; the caller clears it): KV8_PAGES_EINDEX, KV8_PAGES_ENOROOM or, from
+ * kv8_pages_copy, KV8_PAGES_ETIMEOUT (a bounded device-side wait gave up).
+ * Limits: 1 <= B <= KV8_PAGES_MAX_SEQS, 1 <= n_blocks <= KV8_PAGES_MAX_BLOCKS, 1 <=
+ * max_blocks < 2^25 (KV8_EUNSUPPORTED above the first two).  Pointers 4-byte
+ * aligned (8 for int64, 16 for the cache).  The arrays of a call must not overlap.
+ * ------------------------------------------------------------------------- */
+#define KV8_PAGES_MAX_SEQS 16384
+#define KV8_PAGES_MAX_BLOCKS 524288
+#define KV8_PAGES_EINDEX 1u   /* a sequence, page, length or pair that cannot be */
+#define KV8_PAGES_ENOROOM 2u  /* no free page, table row or slot array large enough */
+#define KV8_PAGES_ETIMEOUT 4u
+
+/* kv8_pages_append -- makes room for n_new[b] >= 0 more tokens of every sequence:
+ * takes the pages they need, raises seq_lens, and writes
+ *   q_start   device int32 [B + 1]: the exclusive sums of n_new, and their total
+ *             (the q_start of mla_absorb_chunk_fp8_batch);
+ *   dst_slot  device int64 [cap]: the cache slots of the new tokens in that order
+ *             (the dst_slot of kv8_quantize_rows and kv8_produce_rows); -1 behind
+ *             the last one.
+ * All or nothing: if a length is bad, a sequence's part-full last page is not its
+ * own, the tokens exceed cap, a table row or the free pages, then nothing is taken,
+ * q_start is 0 throughout, dst_slot is -1 throughout and the error word is set.
+ * 0 <= cap < 2^31.  Errors: KV8_EINVAL, KV8_EALIGN, KV8_EUNSUPPORTED, KV8_ECUDA. */
+int kv8_pages_append(int32_t* block_table, int32_t* seq_lens, int32_t* page_refs, int B,
+                     int max_blocks, int64_t n_blocks, const int32_t* n_new, int32_t* q_start,
+                     int64_t* dst_slot, int64_t cap, unsigned* err_word, void* stream);
+
+/* kv8_pages_fork -- sequence dst_seq[i] becomes the first fork_len[i] tokens of
+ * src_seq[i] (all of them where fork_len is NULL), i = 0 .. n - 1.  Full pages are
+ * shared; a part-full last page is given a fresh page and listed in
+ *   moves    device int32 [>= n][2]: pairs (page, fresh page), in the order of i, for
+ *            kv8_pages_copy; *n_moves (device int32) is their number.  Pairs behind
+ *            it are left as they were.
+ * A destination is an empty sequence (seq_len 0), named once and no source; a
+ * source may be named often.  All or nothing otherwise (*n_moves = 0), and if the
+ * free pages run out.  A held entry of a source that names no page is copied as it
+ * is and sets the error word.  0 <= n <= KV8_PAGES_MAX_SEQS.  Errors: KV8_EINVAL,
+ * KV8_EALIGN, KV8_EUNSUPPORTED, KV8_ECUDA. */
+int kv8_pages_fork(int32_t* block_table, int32_t* seq_lens, int32_t* page_refs, int B,
+                   int max_blocks, int64_t n_blocks, const int32_t* src_seq,
+                   const int32_t* dst_seq, const int32_t* fork_len, int n, int32_t* moves,
+                   int32_t* n_moves, unsigned* err_word, void* stream);
+
+/* kv8_pages_free -- empties the sequences seq[0 .. n - 1]: gives their pages back
+ * (one count each), sets their entries to -1 and their seq_lens to 0.  A sequence
+ * that is out of range or named twice makes the call do nothing but set the error
+ * word.  A held entry that names no page, or a page whose count is 0 already, sets
+ * the error word and changes no count.  0 <= n <= KV8_PAGES_MAX_SEQS.  Errors:
+ * KV8_EINVAL, KV8_EALIGN, KV8_EUNSUPPORTED, KV8_ECUDA. */
+int kv8_pages_free(int32_t* block_table, int32_t* seq_lens, int32_t* page_refs, int B,
+                   int max_blocks, int64_t n_blocks, const int32_t* seq, int n,
+                   unsigned* err_word, void* stream);
+
+/* kv8_pages_compact -- packs the pool: with L pages in use, the k-th used page at or
+ * above L takes the place of the k-th free page below L.  Held table entries and
+ * page_refs follow;
+ *   moves    device int32 [>= n_blocks / 2][2]: the pairs (old page, new page) in
+ *            ascending order, for kv8_pages_copy; *n_moves their number, *n_live
+ *            (or NULL) L.  Pairs behind *n_moves are left as they were.
+ * Afterwards pages [0, L) are in use and the rest is free.  A held entry that names
+ * no page in use stays as it is and sets the error word.  Errors: KV8_EINVAL,
+ * KV8_EALIGN, KV8_EUNSUPPORTED, KV8_ECUDA. */
+int kv8_pages_compact(int32_t* block_table, const int32_t* seq_lens, int32_t* page_refs, int B,
+                      int max_blocks, int64_t n_blocks, int32_t* moves, int32_t* n_moves,
+                      int32_t* n_live, unsigned* err_word, void* stream);
+
+/* kv8_pages_copy -- copies the codes and scales of page moves[i][0] over page
+ * moves[i][1], in every one of n_layers pools that lie behind one another and share
+ * the table:
+ *   kv_codes   device uint8 [n_layers][n_slots][576], kv_scales f32
+ *              [n_layers][n_slots][2], both 16-byte aligned; n_slots a multiple of 64
+ *              (of one layer: at least 64, a part-page at the end is not used).
+ *   moves      device int32 [max_moves][2], max_moves >= 0.  n_moves: device int32,
+ *              the number of pairs that count (clamped to [0, max_moves]), or NULL for
+ *              all of them.
+ * A pair of a page and itself is nothing to do.  A pair is left out, and sets the
+ * error word, if it names a page outside the pool, if its destination is named by
+ * another pair too (then none of them is copied), or if its source is another
+ * pair's destination.  Errors: KV8_EINVAL, KV8_EALIGN, KV8_EUNSUPPORTED, KV8_ECUDA. */
+int kv8_pages_copy(uint8_t* kv_codes, float* kv_scales, int n_layers, int64_t n_slots,
+                   const int32_t* moves, const int32_t* n_moves, int64_t max_moves,
+                   unsigned* err_word, void* stream);
+
 /* kv8_workspace_error -- synchronises `stream`, then reports the device-side
  * error word of the last decode call that used `workspace`: KV8_OK,
  * KV8_EBOUNDS (a bad block-table entry or seq_len) or KV8_ETIMEOUT (a kernel
