@@ -542,6 +542,30 @@ __device__ __forceinline__ void mma_f16_pair_warp(uint32_t d_tmem, uint64_t ades
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// pair MMA, kind::f8f6f4 (A and B e4m3), both operands in shared memory or A in TMEM
+// (each CTA's own 128 rows, at the same address), issued by the pair's even CTA through
+// one elected lane of a converged warp
+__device__ __forceinline__ void mma_f8_pair_warp(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                                 uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_f8_ts_pair_warp(uint32_t d_tmem, uint32_t a_tmem,
+                                                    uint64_t bdesc, uint32_t idesc,
+                                                    uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
 // arrive on the barrier at this offset in every CTA of `cta_mask` once the pair
 // MMAs issued so far are done
 __device__ __forceinline__ void mma_commit_pair_warp(uint64_t* bar, uint16_t cta_mask) {
@@ -552,6 +576,23 @@ __device__ __forceinline__ void mma_commit_pair_warp(uint64_t* bar, uint16_t cta
       "[%0], %1;\n\t}" ::"r"(smem_u32(bar)),
       "h"(cta_mask)
       : "memory");
+}
+// tma_load_2d_pair (below), issued by a whole converged warp (one elected lane)
+__device__ __forceinline__ void tma_load_2d_pair_warp(uint32_t dst, const void* tmap, int x, int y,
+                                                      uint32_t bar_cluster) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar_cluster)
+      : "memory");
+}
+// mbar_wait_cluster by every lane of a converged warp (as mbar_wait_warp)
+__device__ __forceinline__ bool mbar_wait_cluster_warp(uint64_t* bar, uint32_t parity,
+                                                       const volatile int* abort,
+                                                       uint64_t limit_ns) {
+  const bool ok = mbar_wait_cluster(bar, parity, abort, limit_ns);
+  return __all_sync(0xffffffffu, ok);
 }
 // TMA load into this CTA's shared memory that completes its bytes on a barrier
 // of either CTA of the pair (given by its shared::cluster address)

@@ -164,11 +164,12 @@ def test_bad_table_entries_and_lengths_are_reported_and_read_as_empty():
 
 def test_bad_query_ranges_are_reported_and_leave_their_rows():
     c = Case(16, [3, 4, 2], [300, 200, 90], seed=17)
-    want, _, _ = run(c)
     c.start.copy_(torch.tensor([0, 3, 100, 9], dtype=torch.int32))
-    out, _, err = run(c)
-    assert err == -5 and torch.equal(out[:3], want[:3])
-    assert (out[3:] == 7).all()
+    out, l, err = run(c)
+    assert err == -5
+    ref, _, tol, _ = c.reference(0)  # the batch's other sequences decide where a row's keys are cut
+    assert ((out[:3].double() - ref).abs() <= tol).all()
+    assert (out[3:] == 7).all() and (l[3:] == 7).all()
 
 
 def test_no_query_at_all():
