@@ -25,23 +25,21 @@
 //         them unless it lies 2^-9 below its row's largest): hi of Lc in TMEM, the rest
 //         in shared memory.  S_L is double-buffered in TMEM; S_R is not: its MMAs come last
 //         in a tile, when the previous one has long been read.
-//   sixteen softmax warps in two groups that take alternate tiles.  A thread owns a row
-//         (its TMEM lane) and 64 tokens: u = sLc S_L + sRc S_R, its own running maximum
-//         m and denominator l of p = 2^(c u - m), and the weights
-//         g'_t = 2^(c u_t + log2 sLc_t - M_g) P_TOP as f16.  The reference M_g follows the
-//         largest weight p_t sLc_t of the row, not the largest score, so that the top weights
-//         fill the e4m3 range however the row scales differ; it is lazy (moves up by more
-//         than 2^TAU, down by more than 2^DOWN) and is handed from tile to tile, and with it
-//         from group to group, through shared memory.  g' goes to the row's context CTA by
+//   eight softmax warps, each 32 rows x 64 tokens of a tile: u = sLc S_L + sRc S_R, per
+//         thread p = 2^(c u - M_g) P_TOP, its sum l, and the weights g' = p sLc as f16.  The
+//         reference M_g follows the largest weight 2^(c u) sLc of the row, not the largest
+//         score, so that the top weights fill the e4m3 range however the row scales differ
+//         (a scale under 2^-96 counts as that, so that p stays in range); it is lazy (moves up
+//         by more than 2^TAU, down by more than 2^DOWN).  g' goes to the row's context CTA by
 //         asynchronous remote stores.
 // Context pair (ranks 2, 3), per key tile:
-//   sixteen warps split g' into two e4m3 terms (hi + residual) in place, as the A operand,
+//   eight warps split g' into two e4m3 terms (hi + residual) in place, as the A operand,
 //         and rescale the rows of O whose M_g moved;
 //   O += g'_hi V + g'_lo V    M = 256, N = 256 channels (each CTA holds half of them as
 //         B, the cache tile read MN-major), 16 MMAs into all 512 TMEM columns.
-//   At the end of a row tile the rows are scaled by 2^(M_g - m) / (P_TOP l), rounded to
-//   bf16 and written; where the range holds only part of a row tile's keys, the partial
-//   (f32 o, m, l) goes to the workspace and a second launch joins the parts.
+//   At the end of a row tile the rows are divided by l, rounded to bf16 and written; where
+//   the range holds only part of a row tile's keys, the partial (f32 o, l and M_g) goes to the
+//   workspace and a second launch joins the parts.
 //
 // Keys that a row does not see have weight 0; since 0 x NaN is NaN, the context warps also
 // clear NaN codes from V tiles that some row of the tile sees only in part (where every row
@@ -54,6 +52,8 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "kv8_common.cuh"
 #include "tc_ptx.cuh"
 
@@ -65,7 +65,8 @@ using namespace ptx;
 constexpr int ROWS = 256;                    // rows of a row tile: 128 per CTA of a pair
 constexpr int CROWS = 128;
 constexpr int W_TMA = 0, W_MMA = 1, W_LANE = 2;
-constexpr int N_LANE_WARPS = 16;             // four per TMEM lane quarter
+constexpr int N_LANE_WARPS = 8;              // two per TMEM lane quarter: more would leave a thread
+                                             // under 100 registers, and a spill here misses L1
 constexpr int NTHREADS = (W_LANE + N_LANE_WARPS) * 32;
 constexpr int MAX_CLUSTERS = NUM_SMS / 4;
 constexpr int MIN_TILES = 2;                 // key tiles that are worth a cluster of their own
@@ -73,21 +74,20 @@ constexpr int BLK = PAGE * 128;              // 8 KB: [64 tokens x 128 bytes]
 constexpr int RBLK = PAGE * DR;              // 4 KB: [64 tokens x 64 bytes]
 constexpr int KTILE = 4 * BLK + RBLK;        // a score CTA's page of a tile: 36 KB
 constexpr int NK = 3;                        // K ring, in tiles; loaded and freed in two halves
-constexpr int NSC = 4;                       // row-scale ring, in tiles (even: a slot is always the same group's)
+constexpr int NSC = 5;                       // row-scale ring, in tiles (see the load warp)
 constexpr int VBLK = TILE * 128;             // 16 KB: [128 tokens x 128 channels]
 constexpr int VTILE = 2 * VBLK;              // a context CTA's half of the channels
-constexpr int NVT = 4;                       // V ring, in tiles
-constexpr int SUB = 64;                      // tokens of a softmax thread's share of a tile
+constexpr int NVT = 3;                       // V ring, in tiles
+constexpr int PART = 64;                     // tokens of a softmax warp's share of a tile (a page)
 constexpr int OP_ATOM = CROWS * 128;         // 16 KB: [128 rows x 128 tokens], e4m3
-constexpr int P_F = CROWS * TILE * 2;        // payload: g' f16 (eight 4 KB chunks), then rescale factors
+constexpr int P_F = CROWS * TILE * 2;        // payload: g' f16 (256 bytes a row), then rescale factors
 constexpr int P_BYTES = P_F + CROWS * 4;
 constexpr int P_STRIDE = 33 * 1024;
-constexpr int CHUNK = 32 * SUB * 2;          // 4 KB: 32 rows x 64 tokens
 constexpr float TAU = 1.0f;
-constexpr float P_TOP = 128.0f;              // g' <= 2^TAU * P_TOP = 256 <= 448
+constexpr float P_TOP = 128.0f, P_LOG = 7.0f;  // g' <= 2^TAU * P_TOP = 256 <= 448
 constexpr float DOWN = 10.0f;
 constexpr float DOWN_CAP = 60.0f;
-constexpr float K_CAP = 114.0f;              // log2 of the factor that takes p to p / 2^(M_g - m)
+constexpr float LG_MIN = -96.0f;             // log2 of the smallest row scale that sets a reference
 constexpr uint64_t WAIT_NS = 2000000000ull;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
@@ -98,16 +98,14 @@ constexpr int B_KEMPTY = B_KFULL + 2 * NK;   // [2 NK] ranks 0, 1: consumed
 constexpr int B_SCFULL = B_KEMPTY + 2 * NK;  // [NSC] score: row scales of a tile loaded
 constexpr int B_SFULL = B_SCFULL + NSC;      // [2] ranks 0, 1: S of a tile in TMEM
 constexpr int B_SEMPTY = B_SFULL + 2;        // [2] rank 0: S read (8 warps x 2 CTAs)
-constexpr int B_QREADY = B_SEMPTY + 2;       // rank 0: the row tile's query in place (16 warps x 2)
-constexpr int B_PX = B_QREADY + 1;           // [4] score: the four warps of a lane quarter meet
-constexpr int B_EX = B_PX + 4;               // [2 groups][4] score: a group's two warps of a quarter
-constexpr int B_CH = B_EX + 8;               // [2 groups][4] score: a tile's M_g published
-constexpr int B_PFREE = B_CH + 8;            // [2] ranks 0, 1: payload buffer free
+constexpr int B_QREADY = B_SEMPTY + 2;       // rank 0: the row tile's query in place (8 warps x 2)
+constexpr int B_PX = B_QREADY + 1;           // [4] score: the two warps of a lane quarter meet
+constexpr int B_PFREE = B_PX + 4;            // [2] ranks 0, 1: payload buffer free
 constexpr int B_PFULL = B_PFREE + 2;         // [2] context: payload arrived
 constexpr int B_VT = B_PFULL + 2;            // [NVT] context: V tile loaded
 constexpr int B_VEMPTY = B_VT + NVT;         // [NVT] ranks 2, 3: consumed
 constexpr int B_CVT = B_VEMPTY + NVT;        // context: every warp has read the payload
-constexpr int B_RS = B_CVT + 1;              // [2] rank 2: operand, V and O half ready (16 warps x 2)
+constexpr int B_RS = B_CVT + 1;              // [2] rank 2: operand, V and O half ready (8 warps x 2)
 constexpr int B_ODONE = B_RS + 2;            // [2] ranks 2, 3: MMAs of an O half done
 constexpr int NRF = 4;
 constexpr int B_RF = B_ODONE + 2;            // [NRF] context: row factors of a finished row tile arrived
@@ -116,24 +114,25 @@ constexpr int NBAR = B_DRAIN + 1;
 
 // shared memory (dynamic, 1024-byte aligned)
 constexpr int OFF_FLAGS = 512;               // tmem base, abort flag
-constexpr int OFF_FACTS = OFF_FLAGS + 16;    // [4] pages present in the tiles of the ring
-constexpr int OFF_XMAX = 1024;               // score: [2 phases][2 groups][2 halves][128] tile maxima
-constexpr int OFF_MG = OFF_XMAX + 4096;      // score: [2][128] M_g after a tile
-constexpr int OFF_XL = OFF_MG + 1024;        // score: [4 parts][128] (m, l)
-constexpr int OFF_XQ = OFF_XL + 4096;        // score: [4 parts][128] query maxima
-constexpr int OFF_SC = OFF_XQ + 2048;        // score: [NSC][128][2] row scales
-constexpr int OFF_PL = OFF_SC + NSC * 1024;  // score: [16 warps][3][64] sLc, sRc, log2 sLc
-constexpr int OFF_QL = (OFF_PL + 16 * 768 + 1023) / 1024 * 1024;  // score: lo of Lc, four atoms
+constexpr int OFF_FACTS = OFF_FLAGS + 16;    // [8] pages present in the tiles of a ring
+constexpr int OFF_XMAX = 1024;               // score: [2][128 rows][2 parts] a tile's largest weights
+constexpr int OFF_XL = OFF_XMAX + 2048;      // score: [128 rows][2 parts] l
+constexpr int OFF_XQ = OFF_XL + 1024;        // score: [128 rows][2 parts] query maxima
+constexpr int OFF_MG = OFF_XQ + 1024;        // score: [128] M_g at a row tile's end
+constexpr int OFF_SC = OFF_MG + 512;         // score: [NSC][128][2] row scales
+constexpr int OFF_QL = (OFF_SC + NSC * 1024 + 1023) / 1024 * 1024;  // score: lo of Lc, four atoms
 constexpr int OFF_QR = OFF_QL + 4 * OP_ATOM;                      // score: Rc, hi | lo
 constexpr int OFF_K = OFF_QR + OP_ATOM;
 constexpr int TOTAL_S = OFF_K + NK * KTILE;
 constexpr int OFF_RF = 1024;                 // context: [NRF][128] row factors
 constexpr int OFF_P = 4096;                  // context: two payloads / operands
 constexpr int OFF_V = OFF_P + 2 * P_STRIDE;
-constexpr int TOTAL_C = OFF_V + NVT * VTILE;
+constexpr int OFF_ST = OFF_V + NVT * VTILE;  // context: [8 warps][2 KB] results on their way out
+constexpr int TOTAL_C = OFF_ST + N_LANE_WARPS * 2048;
 constexpr int SMEM = TOTAL_S > TOTAL_C ? TOTAL_S : TOTAL_C;
 // TMEM columns of a score CTA
 constexpr int T_SL = 0, T_SR = 256, T_QH = 384;
+static_assert(NSC >= NK + 2 && NSC <= 8 && NVT <= 8 && OFF_FACTS + 32 <= OFF_XMAX, "rings");
 static_assert(NBAR * 8 <= OFF_FLAGS && OFF_RF + NRF * 512 <= OFF_P, "shared memory layout");
 static_assert(OFF_K % 1024 == 0 && KTILE % 1024 == 0 && OFF_V % 1024 == 0 && P_STRIDE % 1024 == 0, "swizzle atoms");
 static_assert(P_BYTES <= P_STRIDE && 2 * OP_ATOM <= P_STRIDE, "payload and operand share a buffer");
@@ -390,9 +389,14 @@ __device__ __forceinline__ uint32_t no_nan(uint32_t v) {
   return v & ~__vcmpeq4(v & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
 }
 
-// byte offset of 16-byte unit u (0..7) of row r (0..31) in a payload chunk
+__device__ __forceinline__ void sts64(uint32_t addr, uint2 v) {
+  asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(addr), "r"(v.x), "r"(v.y) : "memory");
+}
+
+// byte offset of 16-byte unit u (0..15) of row r in a payload: unit 4 s + i holds tokens
+// 32 s + 8 j + 2 i, + 1 for j = 0 .. 3
 __device__ __forceinline__ uint32_t prow(int r, int u) {
-  return (uint32_t)(r * 128 + ((u ^ (r & 7)) << 4));
+  return (uint32_t)(r * 256 + ((u ^ (r & 7)) << 4));
 }
 
 struct Workspace {
@@ -426,10 +430,9 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < NBAR; ++i) mbar_init(&bars[i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&bars[B_SEMPTY + i], 16);
+    for (int i = 0; i < 2; ++i) mbar_init(&bars[B_SEMPTY + i], 2 * N_LANE_WARPS);
     mbar_init(&bars[B_QREADY], 2 * N_LANE_WARPS);
-    for (int i = 0; i < 4; ++i) mbar_init(&bars[B_PX + i], 4);
-    for (int i = 0; i < 8; ++i) mbar_init(&bars[B_EX + i], 2);
+    for (int i = 0; i < 4; ++i) mbar_init(&bars[B_PX + i], N_LANE_WARPS / 4);
     mbar_init(&bars[B_CVT], N_LANE_WARPS);
     for (int i = 0; i < 2; ++i) mbar_init(&bars[B_RS + i], 2 * N_LANE_WARPS);
     *abort_flag = 0;
@@ -493,8 +496,9 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
             }
           }
           if (!ok) break;
-          // the row scales' slot held tile g - 4: the MMAs of tile g - 3, done by now, began
-          // their last ones when the softmax warps had read S, and the scales, of tile g - 4
+          // the row scales' slot held tile g - 5: the MMAs of tile g - 3, done by now, began
+          // their last ones when the softmax warps had read S of tile g - 4, and so were
+          // through with tile g - 5
           facts[sc] = (s0 >= 0 ? 1u : 0u) | (s1 >= 0 ? 2u : 0u);
           mbar_arrive_expect_tx_warp(&bars[B_SCFULL + sc], 512u * pages);
           if (s0 >= 0) tma_load_1d_warp(scr + sc * 1024, &smap, (int)(2 * s0), &bars[B_SCFULL + sc]);
@@ -576,20 +580,23 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
       __syncwarp();
     } else {
       // ---------------------------------------------------------- query and softmax
+      // A warp owns 32 rows (its TMEM lane quarter) and one part of the channels (of the
+      // query) or of the tokens (of a tile).  A thread holds four rows, 8 p + lane / 4, and
+      // of 64 columns the pairs 8 j + 2 (lane % 4), so that a token's scales, read from shared
+      // memory, serve four rows.
       const int q = warp & 3;                 // TMEM lane quarter
-      const int part = (warp - W_LANE) >> 2;  // quarter of the query's channels
-      const int grp = part >> 1, sub = part & 1;  // tiles of this parity; half of the tile's tokens
-      const int hh = q * 32 + lane;           // row of this CTA = TMEM lane
+      const int part = (warp - W_LANE) >> 2;  // 256 channels of Lc and 32 of Rc; a page of a tile
+      const int i4 = lane & 3, r8 = lane >> 2;
+      const int mine = q * 32 + 8 * i4 + r8;  // the row this lane speaks for in exchanges
       const uint32_t lane_addr = (uint32_t)(q * 32) << 16;
       float* xmax = reinterpret_cast<float*>(sm + OFF_XMAX);
+      float* xl = reinterpret_cast<float*>(sm + OFF_XL);
+      uint32_t* xq = reinterpret_cast<uint32_t*>(sm + OFF_XQ);
       float* mgs = reinterpret_cast<float*>(sm + OFF_MG);
-      float2* xl = reinterpret_cast<float2*>(sm + OFF_XL);
-      float* xq = reinterpret_cast<float*>(sm + OFF_XQ);
-      float* pl = reinterpret_cast<float*>(sm + OFF_PL) + (warp - W_LANE) * 192;
       const uint32_t qready = map_to(smem_u32(&bars[B_QREADY]), 0);
-      const uint32_t sempty = map_to(smem_u32(&bars[B_SEMPTY + grp]), 0);
-      const uint32_t ctx_p = map_to(smem_u32(sm + OFF_P), rank + 2) + grp * P_STRIDE;
-      const uint32_t ctx_pfull = map_to(smem_u32(&bars[B_PFULL + grp]), rank + 2);
+      const uint32_t sempty = map_to(smem_u32(&bars[B_SEMPTY]), 0);
+      const uint32_t ctx_p = map_to(smem_u32(sm + OFF_P), rank + 2);
+      const uint32_t ctx_pfull = map_to(smem_u32(&bars[B_PFULL]), rank + 2);
       const uint32_t ctx_rf = map_to(smem_u32(sm + OFF_RF), rank + 2);
       const uint32_t ctx_rfbar = map_to(smem_u32(&bars[B_RF]), rank + 2);
       uint32_t px = 0;
@@ -598,255 +605,265 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
         if (lane == 0) mbar_arrive(&bars[B_PX + q]);
         return wait(B_PX + q, px++);
       };
-      bool ok = true;
-      for (; ok && w.more(); w.next(a)) {
-        // ---- the query of this row: 128 channels of Lc and 16 of Rc per thread, as two
-        // e4m3 terms on the scale that puts the row's largest value in [128, 256)
-        const int64_t r = (int64_t)w.rt * ROWS + rank * CROWS + hh;
-        const bool real = r < (int64_t)w.s.nq * a.H;
-        const int tok = real ? (int)((uint32_t)r / (uint32_t)a.H) : w.s.nq - 1;
-        const int head = real ? (int)((uint32_t)r % (uint32_t)a.H) : 0;
-        const int lim = limit_of(a, w.s, tok);
-        float c;
-        {
-          const uint4* pq = reinterpret_cast<const uint4*>(a.q_lat + (w.s.q0 + tok) * a.ql_t + head * a.ql_h + part * 128);
-          const uint4* pr = reinterpret_cast<const uint4*>(a.q_rope + (w.s.q0 + tok) * a.qr_t + head * a.qr_h + part * 16);
-          // the largest magnitude, as bf16 bits (an ordered integer; 0x7F80 and up is inf or NaN)
-          uint32_t top = 0;
-          const uint4 zero4 = make_uint4(0u, 0u, 0u, 0u);
-          auto most = [&](const uint4& v) {
-            top = __vmaxu2(__vmaxu2(top, v.x & 0x7FFF7FFFu), __vmaxu2(v.y & 0x7FFF7FFFu, v.z & 0x7FFF7FFFu));
-            top = __vmaxu2(top, v.w & 0x7FFF7FFFu);
-          };
+      // the value of the four that belongs to row `mine`
+      auto own = [&](float v0, float v1, float v2, float v3) -> float {
+        const float a01 = (i4 & 1) ? v1 : v0, a23 = (i4 & 1) ? v3 : v2;
+        return (i4 & 2) ? a23 : a01;
+      };
+      // The queries of a row tile: two e4m3 terms on the scale that puts a row's largest value
+      // in [128, 256); c folds the scale back in, with sm_scale log2 e.
+      auto load_query = [&](const Walk& x, float (&c)[4]) -> bool {
+        const uint4 *pq[4], *pr[4];  // (null past the sequence's last row)
+        float top[4];                // a row's largest magnitude, as bf16 bits (ordered; 0x7F80 and up is inf or NaN)
+        auto get = [](const uint4* p, int j) { return p != nullptr ? __ldg(p + j) : make_uint4(0u, 0u, 0u, 0u); };
 #pragma unroll
-          for (int j = 0; j < 16; ++j) most(real ? __ldg(pq + j) : zero4);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) most(real ? __ldg(pr + j) : zero4);
-          top = (top & 0xFFFFu) > (top >> 16) ? (top & 0xFFFFu) : (top >> 16);
-          xq[part * CROWS + hh] = __uint_as_float(top);
-          if (!quarter_sync()) {
-            ok = false;
-            break;
-          }
-#pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            const uint32_t v = __float_as_uint(xq[p * CROWS + hh]);
-            top = v > top ? v : top;
-          }
-          const bool nan = top >= 0x7F80u;
-          // exponent e: max in [2^e, 2^(e+1)); the scale 2^(7 - e), at most 2^87
-          int e = (int)(top >> 7) - 127;
-          e = e < -80 ? -80 : e;
-          if (top == 0 || nan) e = 7;
-          const float sc = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
-          c = fmaxf(a.sm_scale * LOG2E * __uint_as_float((uint32_t)(127 - 7 + e) << 23), 1e-37f);
-          // (a row with a NaN or an infinity is all NaN codes, and c = sm log2 e)
-          auto terms = [&](uint32_t w0, uint32_t w1, uint32_t& hi, uint32_t& lo) {
-            const float v[4] = {bf16_lo(w0) * sc, bf16_hi(w0) * sc, bf16_lo(w1) * sc, bf16_hi(w1) * sc};
-            split4(v, hi, lo);
-            if (nan) hi = 0x7F7F7F7Fu;
-          };
-          const uint32_t qlo = smem_u32(sm + OFF_QL) + part * OP_ATOM, qrp = smem_u32(sm + OFF_QR);
-#pragma unroll 1
-          for (int hl = 0; hl < 4; ++hl) {  // 32 channels, from cache now
-            uint4 x[4];
-            uint32_t hw[8];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) x[j] = real ? __ldg(pq + 4 * hl + j) : zero4;
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              uint32_t lw[4];
-              terms(x[2 * u].x, x[2 * u].y, hw[4 * u], lw[0]);
-              terms(x[2 * u].z, x[2 * u].w, hw[4 * u + 1], lw[1]);
-              terms(x[2 * u + 1].x, x[2 * u + 1].y, hw[4 * u + 2], lw[2]);
-              terms(x[2 * u + 1].z, x[2 * u + 1].w, hw[4 * u + 3], lw[3]);
-              sts128(qlo + sw128(hh, 2 * hl + u), make_uint4(lw[0], lw[1], lw[2], lw[3]));
-            }
-            __syncwarp();
-            tmem_st8(tmem + lane_addr + T_QH + part * 32 + 8 * hl, hw);
-          }
-          const uint4 y0 = real ? __ldg(pr) : zero4, y1 = real ? __ldg(pr + 1) : zero4;
-          uint32_t hr[4], lr[4];
-          terms(y0.x, y0.y, hr[0], lr[0]);
-          terms(y0.z, y0.w, hr[1], lr[1]);
-          terms(y1.x, y1.y, hr[2], lr[2]);
-          terms(y1.z, y1.w, hr[3], lr[3]);
-          sts128(qrp + sw128(hh, part), make_uint4(hr[0], hr[1], hr[2], hr[3]));
-          sts128(qrp + sw128(hh, 4 + part), make_uint4(lr[0], lr[1], lr[2], lr[3]));
-          __syncwarp();
-          tmem_wait_st();
-          fence_proxy_async_smem();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) arrive_cluster(qready);
+        for (int p = 0; p < 4; ++p) {
+          const int64_t r = (int64_t)x.rt * ROWS + rank * CROWS + q * 32 + 8 * p + r8;
+          const int64_t tok = x.s.q0 + (int64_t)((uint32_t)r / (uint32_t)a.H), head = (uint32_t)r % (uint32_t)a.H;
+          const bool real = r < (int64_t)x.s.nq * a.H;
+          pq[p] = real ? reinterpret_cast<const uint4*>(a.q_lat + tok * a.ql_t + head * a.ql_h + part * 256) + i4 : nullptr;
+          pr[p] = real ? reinterpret_cast<const uint4*>(a.q_rope + tok * a.qr_t + head * a.qr_h + part * 32) + i4 : nullptr;
         }
-        const uint64_t c2 = pk2(c, c);
-        float m = -INFINITY, l = 0.f;   // this thread's tokens
-        float mghi = -INFINITY;
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          uint32_t t2 = 0;
+#pragma unroll
+          for (int j = 0; j < 9; ++j) {
+            const uint4 v = j < 8 ? get(pq[p], 4 * j) : get(pr[p], 0);
+            t2 = __vmaxu2(t2, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                                       __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+          }
+          t2 = __vmaxu2(t2, __shfl_xor_sync(0xffffffffu, t2, 1));
+          t2 = __vmaxu2(t2, __shfl_xor_sync(0xffffffffu, t2, 2));
+          top[p] = __uint_as_float((t2 & 0xFFFFu) > (t2 >> 16) ? (t2 & 0xFFFFu) : (t2 >> 16));
+        }
+        xq[mine * 2 + part] = __float_as_uint(own(top[0], top[1], top[2], top[3]));
+        if (!quarter_sync()) return false;
+        const uint32_t qlo = smem_u32(sm + OFF_QL) + 2 * part * OP_ATOM, qrp = smem_u32(sm + OFF_QR);
+#pragma unroll
+        for (int hl = 0; hl < 2; ++hl) {  // (read again: all four rows' values at once would spill)
+          uint32_t hw[32];
+#pragma unroll
+          for (int p2 = 0; p2 < 2; ++p2) {
+            const int p = 2 * hl + p2, row = q * 32 + 8 * p + r8;
+            const uint2 m2 = reinterpret_cast<const uint2*>(xq)[row];
+            const uint32_t mx = m2.x > m2.y ? m2.x : m2.y;
+            const bool nan = mx >= 0x7F80u;
+            // largest value in [2^e, 2^(e+1)): the scale 2^(7 - e), at most 2^87
+            int e = (int)(mx >> 7) - 127;
+            e = e < -80 ? -80 : e;
+            if (mx == 0 || nan) e = 7;
+            const float sc = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
+            c[p] = fmaxf(a.sm_scale * LOG2E * __uint_as_float((uint32_t)(127 - 7 + e) << 23), 1e-37f);
+            // (a row with a NaN or an infinity is all NaN codes)
+            auto terms = [&](uint32_t w0, uint32_t w1, uint32_t& hi, uint32_t& lo) {
+              const float f4[4] = {bf16_lo(w0) * sc, bf16_hi(w0) * sc, bf16_lo(w1) * sc, bf16_hi(w1) * sc};
+              split4(f4, hi, lo);
+              if (nan) hi = 0x7F7F7F7Fu;
+            };
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {  // channels 32 j + 8 i4 .. + 7 of the part
+              const uint4 v = get(pq[p], 4 * j);
+              uint2 lo;
+              terms(v.x, v.y, hw[4 * j + 2 * p2], lo.x);
+              terms(v.z, v.w, hw[4 * j + 2 * p2 + 1], lo.y);
+              sts64(qlo + (j >> 2) * OP_ATOM + sw128(row, 2 * (j & 3) + (i4 >> 1)) + (i4 & 1) * 8, lo);
+            }
+            const uint4 v = get(pr[p], 0);
+            uint2 hi, lo;
+            terms(v.x, v.y, hi.x, lo.x);
+            terms(v.z, v.w, hi.y, lo.y);
+            sts64(qrp + sw128(row, 2 * part + (i4 >> 1)) + (i4 & 1) * 8, hi);
+            sts64(qrp + sw128(row, 4 + 2 * part + (i4 >> 1)) + (i4 & 1) * 8, lo);
+          }
+          __syncwarp();
+          tmem_st_16x64(tmem + lane_addr + ((uint32_t)(16 * hl) << 16) + T_QH + part * 64, hw);
+        }
+        __syncwarp();
+        tmem_wait_st();
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster_local(qready);
+        return true;
+      };
+
+      bool ok = true;
+      float c[4] = {1.f, 1.f, 1.f, 1.f};
+      if (w.more()) ok = load_query(w, c);
+      while (ok && w.more()) {
+        Walk wn = w;  // the next segment, whose query is loaded as soon as this one's MMAs are done
+        wn.next(a);
+        float cn[4];
+        int lim[4];   // keys that the rows see
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          const int64_t r = (int64_t)w.rt * ROWS + rank * CROWS + q * 32 + 8 * p + r8;
+          const int tok = (int)((uint32_t)r / (uint32_t)a.H);
+          lim[p] = limit_of(a, w.s, tok < w.s.nq ? tok : w.s.nq - 1) - part * PART;
+        }
+        float l[4], mg[4], mghi[4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          mg[p] = mghi[p] = -INFINITY;
+          l[p] = 0.f;  // this thread's tokens
+        }
         for (int i = 0; i < w.n; ++i) {
-          const int g = gt + i;
-          if ((g & 1) != grp) continue;
-          const int sc = g % NSC;
+          const int g = gt + i, buf = g & 1, sc = g % NSC;
           if (!wait(B_SCFULL + sc, (uint32_t)(g / NSC))) {
             ok = false;
             break;
           }
-          // this half's row scales in planar order, and log2 sLc (this warp's copy)
-          const bool here = (facts[sc] >> sub) & 1u;
-          {
-            const float4 s4 = reinterpret_cast<const float4*>(sm + OFF_SC + sc * 1024)[sub * 32 + lane];
-            __syncwarp();
-            reinterpret_cast<float2*>(pl)[lane] = make_float2(s4.x, s4.z);
-            reinterpret_cast<float2*>(pl + 64)[lane] = make_float2(s4.y, s4.w);
-            reinterpret_cast<float2*>(pl + 128)[lane] = make_float2(lg2_approx(s4.x), lg2_approx(s4.z));
-            __syncwarp();
+          const float2* s2 = reinterpret_cast<const float2*>(sm + OFF_SC + sc * 1024) + part * PART;
+          const bool here = (facts[sc] >> part) & 1u;
+          // tokens of this part that the rows see
+          int n[4];
+          bool less = false;
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            n[p] = here ? lim[p] - (w.t + i) * TILE : 0;
+            less = less || n[p] < PART;
           }
-          // tokens of this half that the row sees
-          const int n = here ? min(max(lim - ((w.t + i) * TILE + sub * SUB), 0), SUB) : 0;
-          const bool cut = __any_sync(0xffffffffu, n < SUB);
-          if (!wait(B_SFULL + grp, (uint32_t)(g >> 1))) {
+          const bool cut = __any_sync(0xffffffffu, less);
+          if (!wait(B_SFULL + buf, (uint32_t)(g >> 1))) {
             ok = false;
             break;
           }
           tc_fence_after();
-          uint64_t u2[SUB / 2];
-          float umax = -INFINITY, ymax = -INFINITY;
-          const float4* sl4 = reinterpret_cast<const float4*>(pl);
-          const float4* sr4 = reinterpret_cast<const float4*>(pl + 64);
-          const float4* lg4 = reinterpret_cast<const float4*>(pl + 128);
-          const uint32_t tl = tmem + lane_addr + T_SL + grp * TILE + sub * SUB;
-          const uint32_t tr = tmem + lane_addr + T_SR + sub * SUB;
+          if (i == w.n - 1 && wn.more() && !load_query(wn, cn)) {
+            ok = false;
+            break;
+          }
+          uint32_t u[2][32];   // S_L, then u = sLc S_L + sRc S_R, as pairs of tokens
+          uint64_t sl[8];      // sLc of the thread's tokens
+          float ymax[4];
 #pragma unroll
-          for (int j = 0; j < SUB / 8; ++j) {
-            uint32_t rl[8], rr[8];
-            tmem_ld8(tl + 8 * j, rl);
-            tmem_ld8(tr + 8 * j, rr);
-            tmem_wait_ld();
-            if (j == SUB / 8 - 1) {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) arrive_cluster(sempty);
-            }
+          for (int p = 0; p < 4; ++p) ymax[p] = -INFINITY;
+          auto scores = [&](auto some_out_of_sight) {
 #pragma unroll
-            for (int v = 0; v < 2; ++v) {  // tokens 8 j + 4 v ..
-              const float4 s4 = sl4[2 * j + v], r4 = sr4[2 * j + v], g4 = lg4[2 * j + v];
-              uint64_t ua = fma2(pk2(r4.x, r4.y), pk2(__uint_as_float(rr[4 * v]), __uint_as_float(rr[4 * v + 1])),
-                                 mul2(pk2(s4.x, s4.y), pk2(__uint_as_float(rl[4 * v]), __uint_as_float(rl[4 * v + 1]))));
-              uint64_t ub = fma2(pk2(r4.z, r4.w), pk2(__uint_as_float(rr[4 * v + 2]), __uint_as_float(rr[4 * v + 3])),
-                                 mul2(pk2(s4.z, s4.w), pk2(__uint_as_float(rl[4 * v + 2]), __uint_as_float(rl[4 * v + 3]))));
-              if (cut) {
-                const int t = 8 * j + 4 * v;
-                const float2 fa = up2(ua), fb = up2(ub);
-                ua = pk2(t < n ? fa.x : -INFINITY, t + 1 < n ? fa.y : -INFINITY);
-                ub = pk2(t + 2 < n ? fb.x : -INFINITY, t + 3 < n ? fb.y : -INFINITY);
+            for (int h = 0; h < 2; ++h) {  // 32 tokens
+              uint32_t rr[2][16];
+              const uint32_t tl = tmem + lane_addr + T_SL + buf * TILE + part * PART + 32 * h;
+              const uint32_t tr = tmem + lane_addr + T_SR + part * PART + 32 * h;
+              tmem_ld_16x32(tl, &u[0][16 * h]);
+              tmem_ld_16x32(tr, rr[0]);
+              tmem_ld_16x32(tl + (16u << 16), &u[1][16 * h]);
+              tmem_ld_16x32(tr + (16u << 16), rr[1]);
+              tmem_wait_ld();
+              if (h == 1) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_cluster_local(sempty + buf * 8);
               }
-              u2[4 * j + 2 * v] = ua;
-              u2[4 * j + 2 * v + 1] = ub;
-              const float2 fa = up2(ua), fb = up2(ub);
-              umax = max3(umax, fa.x, fa.y);
-              umax = max3(umax, fb.x, fb.y);
-              // (where a token is out of sight u is -inf and y is -inf or NaN, which max drops)
-              const float2 ya = up2(fma2(c2, ua, pk2(g4.x, g4.y))), yb = up2(fma2(c2, ub, pk2(g4.z, g4.w)));
-              ymax = max3(ymax, ya.x, ya.y);
-              ymax = max3(ymax, yb.x, yb.y);
+#pragma unroll
+              for (int j4 = 0; j4 < 4; ++j4) {
+                const int j = 4 * h + j4;
+                const float4 s4 = *reinterpret_cast<const float4*>(s2 + 8 * j + 2 * i4);
+                const uint64_t s = pk2(s4.x, s4.z), sr = pk2(s4.y, s4.w);
+                const uint64_t lg = pk2(fmaxf(lg2_approx(s4.x), LG_MIN), fmaxf(lg2_approx(s4.z), LG_MIN));
+                // (a scale out of sight may be anything: made finite, its weight is 0)
+                sl[j] = pk2(fminf(fmaxf(s4.x, 0.f), 3.0e38f), fminf(fmaxf(s4.z, 0.f), 3.0e38f));
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                  uint32_t* x = &u[p >> 1][4 * j + 2 * (p & 1)];
+                  const uint32_t* y = &rr[p >> 1][4 * j4 + 2 * (p & 1)];
+                  float2 f = up2(fma2(sr, pk2(__uint_as_float(y[0]), __uint_as_float(y[1])),
+                                      mul2(s, pk2(__uint_as_float(x[0]), __uint_as_float(x[1])))));
+                  if (some_out_of_sight) {
+                    f.x = 8 * j + 2 * i4 < n[p] ? f.x : -INFINITY;
+                    f.y = 8 * j + 2 * i4 + 1 < n[p] ? f.y : -INFINITY;
+                  }
+                  x[0] = __float_as_uint(f.x);
+                  x[1] = __float_as_uint(f.y);
+                  // (where a token is out of sight u is -inf and v is -inf or NaN, which max drops)
+                  const float2 v = up2(fma2(pk2(c[p], c[p]), pk2(f.x, f.y), lg));
+                  ymax[p] = max3(ymax[p], v.x, v.y);
+                }
+              }
             }
+          };
+          if (cut) scores(std::true_type());
+          else scores(std::false_type());
+          auto pair = [&](int p, int j) -> uint64_t {
+            return pk2(__uint_as_float(u[p >> 1][4 * j + 2 * (p & 1)]),
+                       __uint_as_float(u[p >> 1][4 * j + 2 * (p & 1) + 1]));
+          };
+          // the rows' largest weights over the tile
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            ymax[p] = fmaxf(ymax[p], __shfl_xor_sync(0xffffffffu, ymax[p], 1));
+            ymax[p] = fmaxf(ymax[p], __shfl_xor_sync(0xffffffffu, ymax[p], 2));
           }
-          // M_g after the previous tile (waited for on every tile, also where a row tile
-          // begins: the waits then see every phase)
-          if (g > 0 && !wait(B_CH + ((g - 1) & 1) * 4 + q, (uint32_t)((g - 1) >> 1))) {
+          float* xm = xmax + buf * 2 * CROWS;
+          xm[mine * 2 + part] = own(ymax[0], ymax[1], ymax[2], ymax[3]);
+          if (!quarter_sync()) {
             ok = false;
             break;
           }
-          const float mg = i > 0 ? mgs[((g - 1) & 1) * CROWS + hh] : -INFINITY;
-          // the tile's largest weight over both halves
-          float* xm = xmax + (((g >> 1) & 1) * 2 + grp) * 2 * CROWS + hh;
-          xm[sub * CROWS] = ymax;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars[B_EX + grp * 4 + q]);
-          if (!wait(B_EX + grp * 4 + q, (uint32_t)(g >> 1))) {
+          if (g >= 2 && !wait(B_PFREE + buf, (uint32_t)((g >> 1) - 1))) {
             ok = false;
             break;
           }
-          ymax = fmaxf(ymax, xm[(sub ^ 1) * CROWS]);
-          mghi = fmaxf(mghi, mg);
-          float mgn = mg;
-          if (ymax > mg + TAU || (ymax < mg - DOWN && ymax >= mghi - DOWN_CAP && ymax > -INFINITY)) mgn = ymax;
-          mghi = fmaxf(mghi, mgn);
-          if (sub == 0) {
-            mgs[(g & 1) * CROWS + hh] = mgn;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[B_CH + grp * 4 + q]);
-          }
-          // this thread's denominator, and the factor from p to g'
-          const float mn = fmaxf(m, c * umax);
-          l *= m == mn ? 1.f : ex2_approx(m - mn);
-          m = mn;
-          const float kf = (mn > -INFINITY && mgn > -INFINITY) ? P_TOP * ex2_approx(fminf(mn - mgn, K_CAP)) : 0.f;
-          const float mneg = -fmaxf(mn, -3.0e38f);
-          const uint64_t m2 = pk2(mneg, mneg), k2 = pk2(kf, kf);
-          if (g >= 2 && !wait(B_PFREE + grp, (uint32_t)((g >> 1) - 1))) {
-            ok = false;
-            break;
-          }
-          const uint32_t dst = ctx_p + (q * 2 + sub) * CHUNK;
-          uint64_t ls2 = pk2(0.f, 0.f);
+          const uint32_t dst = ctx_p + buf * P_STRIDE, bar = ctx_pfull + buf * 8;
+          float fm = 1.f;  // what O of row `mine` is multiplied by before this tile is added
 #pragma unroll
-          for (int j = 0; j < SUB / 8; ++j) {  // eight tokens, 16 bytes of g'
-            uint32_t h[4];
+          for (int p = 0; p < 4; ++p) {
+            const float2 v = reinterpret_cast<const float2*>(xm)[q * 32 + 8 * p + r8];
+            const float ym = fmaxf(v.x, v.y);
+            float mgn = mg[p];
+            if (ym > mgn + TAU || (ym < mgn - DOWN && ym >= mghi[p] - DOWN_CAP && ym > -INFINITY)) mgn = ym;
+            const float fp = mgn == mg[p] ? 1.f : (mg[p] > -INFINITY ? ex2_approx(mg[p] - mgn) : 0.f);
+            fm = i4 == p ? fp : fm;
+            mg[p] = mgn;
+            mghi[p] = fmaxf(mghi[p], mgn);
+            l[p] *= fp;
+            // p = 2^(c u - M_g) P_TOP (nothing in sight so far: u is -inf, and p 0)
+            const float mneg = P_LOG - fmaxf(mgn, -3.0e38f);
+            const uint64_t c2 = pk2(c[p], c[p]), m2 = pk2(mneg, mneg);
+            uint64_t ls2 = pk2(0.f, 0.f);
 #pragma unroll
-            for (int v = 0; v < 2; ++v) {
-              const float4 s4 = sl4[2 * j + v];
+            for (int jh = 0; jh < 2; ++jh) {
+              uint32_t h[4];
 #pragma unroll
-              for (int p = 0; p < 2; ++p) {
-                const float2 z = up2(fma2(c2, u2[4 * j + 2 * v + p], m2));
+              for (int j4 = 0; j4 < 4; ++j4) {
+                const int j = 4 * jh + j4;
+                const float2 z = up2(fma2(c2, pair(p, j), m2));
                 const uint64_t e = pk2(ex2_approx(z.x), ex2_approx(z.y));
                 ls2 = add2(ls2, e);
-                float2 x = up2(mul2(mul2(e, k2), p == 0 ? pk2(s4.x, s4.y) : pk2(s4.z, s4.w)));
-                if (cut) {
-                  const int t = 8 * j + 4 * v + 2 * p;
-                  x.x = t < n ? x.x : 0.f;
-                  x.y = t + 1 < n ? x.y : 0.f;
-                }
+                const float2 x = up2(mul2(e, sl[j]));
                 const __half2 h2 = __floats2half2_rn(x.x, x.y);
-                h[2 * v + p] = *reinterpret_cast<const uint32_t*>(&h2);
+                h[j4] = *reinterpret_cast<const uint32_t*>(&h2);
               }
+              st_async_v4(dst + prow(q * 32 + 8 * p + r8, part * 8 + jh * 4 + i4), make_uint4(h[0], h[1], h[2], h[3]), bar);
             }
-            st_async_v4(dst + prow(lane, j), make_uint4(h[0], h[1], h[2], h[3]), ctx_pfull);
+            const float2 ls = up2(ls2);
+            l[p] += ls.x + ls.y;
           }
-          if (sub == 0) {
-            // what the row's O is multiplied by before this tile is added
-            const float f = mgn == mg ? 1.f : (mg > -INFINITY ? ex2_approx(mg - mgn) : 0.f);
-            st_async_b32(ctx_p + P_F + hh * 4, __float_as_uint(f), ctx_pfull);
-          }
-          const float2 ls = up2(ls2);
-          l += ls.x + ls.y;
+          if (part == 0) st_async_b32(dst + P_F + mine * 4, __float_as_uint(fm), bar);
         }
         if (!ok) break;
-        // ---- the row tile's (or its part's) end: every MMA on this query is done; the
-        // four threads of a row join their (m, l)
-        const int last = gt + w.n - 1;
-        gt += w.n;
-        xl[part * CROWS + hh] = make_float2(m, l);
-        if (!wait(B_SFULL + (last & 1), (uint32_t)(last >> 1)) || !quarter_sync()) {
+        // ---- the row tile's (or its part's) end: the eight threads of a row add their l
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          l[p] += __shfl_xor_sync(0xffffffffu, l[p], 1);
+          l[p] += __shfl_xor_sync(0xffffffffu, l[p], 2);
+        }
+        xl[mine * 2 + part] = own(l[0], l[1], l[2], l[3]);
+        if (part == 0) mgs[mine] = own(mg[0], mg[1], mg[2], mg[3]);
+        if (!quarter_sync()) {
           ok = false;
           break;
         }
-        if (part == 0) {
-          float M = -INFINITY, L = 0.f;
-#pragma unroll
-          for (int p = 0; p < 4; ++p) M = fmaxf(M, xl[p * CROWS + hh].x);
-#pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            const float2 v = xl[p * CROWS + hh];
-            L += v.y * (v.x > -INFINITY ? ex2_approx(v.x - M) : 1.f);  // (a NaN l stays one)
-          }
-          const float mg = mgs[(last & 1) * CROWS + hh];
-          float f = mg > -INFINITY ? ex2_approx(mg - M) * (1.f / P_TOP) : 0.f;
-          if (L != L) f = L;
+        if (part == 0) {  // a row per lane
+          const int hh = q * 32 + lane;
+          const float L = xl[hh * 2] + xl[hh * 2 + 1];  // on the scale 2^-M_g P_TOP, as O
+          const float M = mgs[hh] - P_LOG;
+          float f = 1.f;
           if (w.whole()) {
-            f = L > 0.f ? f / L : f;
-            if (a.lse != nullptr && real)
-              a.lse[(w.s.q0 + tok) * a.H + head] = L == 0.f ? -INFINITY : (M + log2f(L)) * LN2;
+            f = L == 0.f ? 0.f : 1.f / L;  // (a NaN stays one)
+            const int64_t r = (int64_t)w.rt * ROWS + rank * CROWS + hh;
+            if (a.lse != nullptr && r < (int64_t)w.s.nq * a.H)
+              a.lse[w.s.q0 * a.H + r] = L == 0.f ? -INFINITY : (M + log2f(L)) * LN2;
           } else {
             const int64_t at = (int64_t)(2 * k + (w.seg == 0 ? 0 : 1)) * ROWS + rank * CROWS + hh;
             ws.m[at] = M;
@@ -854,13 +871,17 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
           }
           st_async_b32(ctx_rf + (w.seg % NRF) * 512 + hh * 4, __float_as_uint(f), ctx_rfbar + (w.seg % NRF) * 8);
         }
+        gt += w.n;
+        w = wn;
+#pragma unroll
+        for (int p = 0; p < 4; ++p) c[p] = cn[p];
       }
       if (!ok && lane == 0) fail();
       // the context CTAs' last commits to this CTA have landed
       if (ok && gt > 0) {
         const int zero = 0;
         for (int i = gt > 2 ? gt - 2 : 0; i < gt; ++i)
-          if ((i & 1) == grp) (void)mbar_wait(&bars[B_PFREE + grp], (i >> 1) & 1, &zero, WAIT_NS);
+          (void)mbar_wait(&bars[B_PFREE + (i & 1)], (i >> 1) & 1, &zero, WAIT_NS);
       }
       __syncwarp();
     }
@@ -944,7 +965,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
     } else {
       // ---------------------------------------------------------- operand, O rescale, results
       const int q = warp & 3;
-      const int part = (warp - W_LANE) >> 2;  // 32 tokens of the tile; 64 columns of an O half
+      const int part = (warp - W_LANE) >> 2;  // 64 tokens of the tile; 128 columns of an O half
       const int hh = q * 32 + lane;
       const uint32_t lane_addr = (uint32_t)(q * 32) << 16;
       const uint32_t rs = map_to(smem_u32(&bars[B_RS]), 2);
@@ -957,10 +978,16 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
             ok = false;
             break;
           }
-          const uint32_t src = pbuf + pb * P_STRIDE + (q * 2 + (part >> 1)) * CHUNK;
-          uint4 pv[4];
+          const uint32_t src = pbuf + pb * P_STRIDE;
+          uint32_t pv[2][4][4];  // [s][i][j]: tokens 32 s + 8 j + 2 i, + 1 of the part
 #pragma unroll
-          for (int u = 0; u < 4; ++u) pv[u] = lds128(src + prow(lane, 4 * (part & 1) + u));
+          for (int u = 0; u < 8; ++u) {
+            const uint4 v = lds128(src + prow(hh, part * 8 + u));
+            pv[u >> 2][u & 3][0] = v.x;
+            pv[u >> 2][u & 3][1] = v.y;
+            pv[u >> 2][u & 3][2] = v.z;
+            pv[u >> 2][u & 3][3] = v.w;
+          }
           const float f = reinterpret_cast<const float*>(sm + OFF_P + pb * P_STRIDE + P_F)[hh];
           const bool any = __any_sync(0xffffffffu, f != 1.f) && i > 0;
           // every warp has read this payload: its buffer may now take the operand, and the
@@ -974,19 +1001,17 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
           if (warp == W_LANE && lane == 0) mbar_arrive_expect_tx(&bars[B_PFULL + pb], P_BYTES);
           const uint32_t opnd = pbuf + pb * P_STRIDE;
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {  // 16 tokens per 16-byte unit
-            const uint32_t x[8] = {pv[2 * j].x, pv[2 * j].y, pv[2 * j].z, pv[2 * j].w,
-                                   pv[2 * j + 1].x, pv[2 * j + 1].y, pv[2 * j + 1].z, pv[2 * j + 1].w};
+          for (int j = 0; j < 4; ++j) {  // 16 tokens per 16-byte unit
             uint32_t hw[4], lw[4];
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
+            for (int v = 0; v < 4; ++v) {  // tokens 16 j + 4 v .. + 3
               uint16_t h0, l0, h1, l1;
-              split_h2(x[2 * v], h0, l0);
-              split_h2(x[2 * v + 1], h1, l1);
+              split_h2(pv[j >> 1][2 * (v & 1)][2 * (j & 1) + (v >> 1)], h0, l0);
+              split_h2(pv[j >> 1][2 * (v & 1) + 1][2 * (j & 1) + (v >> 1)], h1, l1);
               hw[v] = (uint32_t)h0 | ((uint32_t)h1 << 16);
               lw[v] = (uint32_t)l0 | ((uint32_t)l1 << 16);
             }
-            const uint32_t off = sw128(hh, part * 2 + j);
+            const uint32_t off = sw128(hh, part * 4 + j);
             sts128(opnd + off, make_uint4(hw[0], hw[1], hw[2], hw[3]));
             sts128(opnd + OP_ATOM + off, make_uint4(lw[0], lw[1], lw[2], lw[3]));
           }
@@ -996,9 +1021,9 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
           }
           if ((w.t + i + 1) * TILE > lim0 || facts[vs] != 3u) {
             // some row does not see all of this tile: no NaN code may stay in it
-            const uint32_t vb = vring + vs * VTILE + (warp - W_LANE) * 2048 + lane * 16;
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            const uint32_t vb = vring + vs * VTILE + (warp - W_LANE) * 4096 + lane * 16;
+#pragma unroll 2
+            for (int u = 0; u < 8; ++u) {
               const uint4 v = lds128(vb + u * 512);
               sts128(vb + u * 512, make_uint4(no_nan(v.x), no_nan(v.y), no_nan(v.z), no_nan(v.w)));
             }
@@ -1015,22 +1040,23 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
             if (any) {
               tc_fence_after();
               __syncwarp();
-              const uint32_t col = tmem + lane_addr + h * 256 + part * 64;
-#pragma unroll 1
-              for (int c0 = 0; c0 < 64; c0 += 16) {
-                uint32_t r[16];
-                tmem_ld16(col + c0, r);
-                tmem_wait_ld();
+              const uint32_t col = tmem + lane_addr + h * 256 + part * 128;
+              uint32_t o[4][32];
 #pragma unroll
-                for (int v = 0; v < 16; ++v) r[v] = __float_as_uint(__uint_as_float(r[v]) * f);
-                tmem_st16(col + c0, r);
+              for (int s = 0; s < 4; ++s) tmem_ld32(col + 32 * s, o[s]);
+              tmem_wait_ld();
+#pragma unroll
+              for (int s = 0; s < 4; ++s) {
+#pragma unroll
+                for (int v = 0; v < 32; ++v) o[s][v] = __float_as_uint(__uint_as_float(o[s][v]) * f);
+                tmem_st32(col + 32 * s, o[s]);
               }
               __syncwarp();
               tmem_wait_st();
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) arrive_cluster(rs + h * 8);
+            if (lane == 0) arrive_cluster_local(rs + h * 8);
           }
           if (!ok) break;
         }
@@ -1046,39 +1072,55 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
         tc_fence_after();
         __syncwarp();
         const float f = reinterpret_cast<const float*>(sm + OFF_RF + rf * 512)[hh];
-        const int64_t r = (int64_t)w.rt * ROWS + half_of * CROWS + hh;
-        const bool real = r < (int64_t)w.s.nq * a.H;
+        // 64 bytes of every row at a time (32 columns of bf16, or 16 of a partial's f32) through
+        // shared memory, so that a warp's stores write whole sectors: eight rows each
         const bool whole = w.whole();
-        uint16_t* out = a.out + (w.s.q0 * a.H + r) * DL;
-        float* po = ws.o + ((int64_t)(2 * k + (w.seg == 0 ? 0 : 1)) * ROWS + half_of * CROWS + hh) * DL;
+        const int64_t r0 = (int64_t)w.rt * ROWS + half_of * CROWS + q * 32;  // the warp's first row
+        const int64_t left = (int64_t)w.s.nq * a.H - r0;
+        const uint32_t stage = smem_u32(sm + OFF_ST) + (warp - W_LANE) * 2048;
+        auto unit = [](int r, int u) -> uint32_t { return (uint32_t)(r * 64 + ((u ^ ((r >> 1) & 3)) << 4)); };
+        uint8_t* dst = whole ? reinterpret_cast<uint8_t*>(a.out + (w.s.q0 * a.H + r0) * DL)
+                             : reinterpret_cast<uint8_t*>(
+                                   ws.o + ((int64_t)(2 * k + (w.seg == 0 ? 0 : 1)) * ROWS + half_of * CROWS + q * 32) * DL);
+        const int row_bytes = whole ? DL * 2 : DL * 4;
+        auto flush = [&](int byte) {
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = 8 * i + (lane >> 2);
+            const uint4 v = lds128(stage + unit(r, lane & 3));
+            if (r < left) *reinterpret_cast<uint4*>(dst + (int64_t)r * row_bytes + byte + (lane & 3) * 16) = v;
+          }
+          __syncwarp();
+        };
 #pragma unroll 1
-        for (int s = 0; s < 4; ++s) {  // 32 columns at a time
-          const int col = (s >> 1) * 256 + part * 64 + (s & 1) * 32;
+        for (int s = 0; s < 8; ++s) {  // 32 columns at a time
+          const int col = (s >> 2) * 256 + part * 128 + (s & 3) * 32;
           uint32_t v[32];
           tmem_ld32(tmem + lane_addr + col, v);
           tmem_wait_ld();
-          if (f == 0.f) {  // nothing seen, or nothing that counts
+          // (a factor of 0: nothing seen, or nothing that counts)
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = 0u;
-          }
+          for (int j = 0; j < 32; ++j) v[j] = f == 0.f ? 0u : __float_as_uint(__uint_as_float(v[j]) * f);
           if (whole) {
 #pragma unroll
-            for (int j = 0; j < 32; j += 8) {
-              uint32_t o[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(v[j + 2 * e]) * f,
-                                                                __uint_as_float(v[j + 2 * e + 1]) * f);
-                o[e] = *reinterpret_cast<const uint32_t*>(&b2);
-              }
-              if (real) *reinterpret_cast<uint4*>(out + col + j) = make_uint4(o[0], o[1], o[2], o[3]);
+            for (int j = 0; j < 16; ++j) {
+              const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+              v[j] = *reinterpret_cast<const uint32_t*>(&b2);
             }
-          } else if (real) {
 #pragma unroll
-            for (int j = 0; j < 32; j += 4)
-              *reinterpret_cast<float4*>(po + col + j) =
-                  make_float4(__uint_as_float(v[j]) * f, __uint_as_float(v[j + 1]) * f,
-                              __uint_as_float(v[j + 2]) * f, __uint_as_float(v[j + 3]) * f);
+            for (int u = 0; u < 4; ++u)
+              sts128(stage + unit(lane, u), make_uint4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]));
+            flush(col * 2);
+          } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                sts128(stage + unit(lane, u), make_uint4(v[16 * h + 4 * u], v[16 * h + 4 * u + 1],
+                                                         v[16 * h + 4 * u + 2], v[16 * h + 4 * u + 3]));
+              flush((col + 16 * h) * 4);
+            }
           }
         }
         // the factor buffer's next use, NRF segments on: its bytes come after this row
