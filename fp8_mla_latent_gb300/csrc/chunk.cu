@@ -25,15 +25,15 @@
 //         them unless it lies 2^-9 below its row's largest): hi of Lc in TMEM, the rest
 //         in shared memory.  S_L is double-buffered in TMEM; S_R is not: its MMAs come last
 //         in a tile, when the previous one has long been read.
-//   eight softmax warps, each 32 rows x 64 tokens of a tile: u = sLc S_L + sRc S_R, per
-//         thread p = 2^(c u - M_g) P_TOP, its sum l, and the weights g' = p sLc as f16.  The
+//   sixteen softmax warps, each 32 rows x 32 tokens of a tile: u = sLc S_L + sRc S_R, per
+//         thread p = 2^(c u - M_g + 7), its sum l, and the weights g' = p sLc as f16.  The
 //         reference M_g follows the largest weight 2^(c u) sLc of the row, not the largest
 //         score, so that the top weights fill the e4m3 range however the row scales differ
-//         (a scale under 2^-96 counts as that, so that p stays in range); it is lazy (moves up
+//         (a scale under 2^-40 counts as that, so that p stays in range); it is lazy (moves up
 //         by more than 2^TAU, down by more than 2^DOWN).  g' goes to the row's context CTA by
 //         asynchronous remote stores.
 // Context pair (ranks 2, 3), per key tile:
-//   eight warps split g' into two e4m3 terms (hi + residual) in place, as the A operand,
+//   sixteen warps split g' into two e4m3 terms (hi + residual) in place, as the A operand,
 //         and rescale the rows of O whose M_g moved;
 //   O += g'_hi V + g'_lo V    M = 256, N = 256 channels (each CTA holds half of them as
 //         B, the cache tile read MN-major), 16 MMAs into all 512 TMEM columns.
@@ -64,9 +64,8 @@ using namespace ptx;
 
 constexpr int ROWS = 256;                    // rows of a row tile: 128 per CTA of a pair
 constexpr int CROWS = 128;
-constexpr int W_TMA = 0, W_MMA = 1, W_LANE = 2;
-constexpr int N_LANE_WARPS = 8;              // two per TMEM lane quarter: more would leave a thread
-                                             // under 100 registers, and a spill here misses L1
+constexpr int W_TMA = 0, W_MMA = 1, W_SCALE = 2, W_LANE = 3;
+constexpr int N_LANE_WARPS = 16;             // four per TMEM lane quarter, and per scheduler
 constexpr int NTHREADS = (W_LANE + N_LANE_WARPS) * 32;
 constexpr int MAX_CLUSTERS = NUM_SMS / 4;
 constexpr int MIN_TILES = 2;                 // key tiles that are worth a cluster of their own
@@ -74,20 +73,21 @@ constexpr int BLK = PAGE * 128;              // 8 KB: [64 tokens x 128 bytes]
 constexpr int RBLK = PAGE * DR;              // 4 KB: [64 tokens x 64 bytes]
 constexpr int KTILE = 4 * BLK + RBLK;        // a score CTA's page of a tile: 36 KB
 constexpr int NK = 3;                        // K ring, in tiles; loaded and freed in two halves
-constexpr int NSC = 5;                       // row-scale ring, in tiles (see the load warp)
+constexpr int NSC = 5;                       // row-scale rings, in tiles (see the load warp)
 constexpr int VBLK = TILE * 128;             // 16 KB: [128 tokens x 128 channels]
 constexpr int VTILE = 2 * VBLK;              // a context CTA's half of the channels
 constexpr int NVT = 3;                       // V ring, in tiles
-constexpr int PART = 64;                     // tokens of a softmax warp's share of a tile (a page)
+constexpr int PART = 32;                     // tokens of a softmax warp's share of a tile
 constexpr int OP_ATOM = CROWS * 128;         // 16 KB: [128 rows x 128 tokens], e4m3
 constexpr int P_F = CROWS * TILE * 2;        // payload: g' f16 (256 bytes a row), then rescale factors
 constexpr int P_BYTES = P_F + CROWS * 4;
 constexpr int P_STRIDE = 33 * 1024;
 constexpr float TAU = 1.0f;
-constexpr float P_TOP = 128.0f, P_LOG = 7.0f;  // g' <= 2^TAU * P_TOP = 256 <= 448
+constexpr float P_LOG = 7.0f;                // g' <= 2^(TAU + P_LOG) = 256 <= 448
 constexpr float DOWN = 10.0f;
-constexpr float DOWN_CAP = 60.0f;
-constexpr float LG_MIN = -96.0f;             // log2 of the smallest row scale that sets a reference
+// bounds that keep p and l in range, 2^(P_LOG + TAU + 40 + 50) times a count of keys: the smallest
+// log2 of a row scale that sets a reference, and how far a row's reference may come down in all
+constexpr float LG_MIN = -40.0f, DOWN_CAP = 50.0f;
 constexpr uint64_t WAIT_NS = 2000000000ull;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
@@ -96,16 +96,17 @@ constexpr float LN2 = 0.6931471805599453f;
 constexpr int B_KFULL = 0;                   // [2 NK] rank 0: both CTAs' halves of a K half tile loaded
 constexpr int B_KEMPTY = B_KFULL + 2 * NK;   // [2 NK] ranks 0, 1: consumed
 constexpr int B_SCFULL = B_KEMPTY + 2 * NK;  // [NSC] score: row scales of a tile loaded
-constexpr int B_SFULL = B_SCFULL + NSC;      // [2] ranks 0, 1: S of a tile in TMEM
-constexpr int B_SEMPTY = B_SFULL + 2;        // [2] rank 0: S read (8 warps x 2 CTAs)
-constexpr int B_QREADY = B_SEMPTY + 2;       // rank 0: the row tile's query in place (8 warps x 2)
-constexpr int B_PX = B_QREADY + 1;           // [4] score: the two warps of a lane quarter meet
+constexpr int B_PL = B_SCFULL + NSC;         // [NSC] score: a tile's scales prepared
+constexpr int B_SFULL = B_PL + NSC;      // [2] ranks 0, 1: S of a tile in TMEM
+constexpr int B_SEMPTY = B_SFULL + 2;        // [2] rank 0: S read (16 warps x 2 CTAs)
+constexpr int B_QREADY = B_SEMPTY + 2;       // rank 0: the row tile's query in place (16 warps x 2)
+constexpr int B_PX = B_QREADY + 1;           // [4] score: the four warps of a lane quarter meet
 constexpr int B_PFREE = B_PX + 4;            // [2] ranks 0, 1: payload buffer free
 constexpr int B_PFULL = B_PFREE + 2;         // [2] context: payload arrived
 constexpr int B_VT = B_PFULL + 2;            // [NVT] context: V tile loaded
 constexpr int B_VEMPTY = B_VT + NVT;         // [NVT] ranks 2, 3: consumed
 constexpr int B_CVT = B_VEMPTY + NVT;        // context: every warp has read the payload
-constexpr int B_RS = B_CVT + 1;              // [2] rank 2: operand, V and O half ready (8 warps x 2)
+constexpr int B_RS = B_CVT + 1;              // [2] rank 2: operand, V and O half ready (16 warps x 2)
 constexpr int B_ODONE = B_RS + 2;            // [2] ranks 2, 3: MMAs of an O half done
 constexpr int NRF = 4;
 constexpr int B_RF = B_ODONE + 2;            // [NRF] context: row factors of a finished row tile arrived
@@ -115,19 +116,24 @@ constexpr int NBAR = B_DRAIN + 1;
 // shared memory (dynamic, 1024-byte aligned)
 constexpr int OFF_FLAGS = 512;               // tmem base, abort flag
 constexpr int OFF_FACTS = OFF_FLAGS + 16;    // [8] pages present in the tiles of a ring
-constexpr int OFF_XMAX = 1024;               // score: [2][128 rows][2 parts] a tile's largest weights
-constexpr int OFF_XL = OFF_XMAX + 2048;      // score: [128 rows][2 parts] l
-constexpr int OFF_XQ = OFF_XL + 1024;        // score: [128 rows][2 parts] query maxima
-constexpr int OFF_MG = OFF_XQ + 1024;        // score: [128] M_g at a row tile's end
-constexpr int OFF_SC = OFF_MG + 512;         // score: [NSC][128][2] row scales
-constexpr int OFF_QL = (OFF_SC + NSC * 1024 + 1023) / 1024 * 1024;  // score: lo of Lc, four atoms
+constexpr int OFF_XMAX = 1024;               // score: [2][128 rows][4 parts] a tile's largest weights
+constexpr int OFF_XL = OFF_XMAX + 4096;      // score: [128 rows][4 parts] l
+constexpr int OFF_XQ = OFF_XL + 2048;        // score: [128 rows][4 parts] query maxima
+constexpr int OFF_MG = OFF_XQ + 2048;        // score: [128] M_g at a row tile's end
+constexpr int OFF_LIM = OFF_MG + 512;        // score: [2][128] keys that the rows see
+constexpr int OFF_C = OFF_LIM + 1024;        // score: [2][128] the rows' c
+constexpr int OFF_WALK = OFF_C + 1024;       // score: [16 warps][2] segments
+constexpr int OFF_SC = OFF_WALK + 2048;      // score: [NSC][128][2] row scales
+constexpr int OFF_PL = OFF_SC + NSC * 1024;  // score: [NSC] of a tile's 64 token pairs: (sLc, sLc, sRc, sRc), then log2 sLc
+constexpr int PL_BYTES = 64 * 16 + 64 * 8;
+constexpr int OFF_QL = (OFF_PL + NSC * PL_BYTES + 1023) / 1024 * 1024;  // score: lo of Lc, four atoms
 constexpr int OFF_QR = OFF_QL + 4 * OP_ATOM;                      // score: Rc, hi | lo
 constexpr int OFF_K = OFF_QR + OP_ATOM;
 constexpr int TOTAL_S = OFF_K + NK * KTILE;
 constexpr int OFF_RF = 1024;                 // context: [NRF][128] row factors
 constexpr int OFF_P = 4096;                  // context: two payloads / operands
 constexpr int OFF_V = OFF_P + 2 * P_STRIDE;
-constexpr int OFF_ST = OFF_V + NVT * VTILE;  // context: [8 warps][2 KB] results on their way out
+constexpr int OFF_ST = OFF_V + NVT * VTILE;  // context: [16 warps][2 KB] results on their way out
 constexpr int TOTAL_C = OFF_ST + N_LANE_WARPS * 2048;
 constexpr int SMEM = TOTAL_S > TOTAL_C ? TOTAL_S : TOTAL_C;
 // TMEM columns of a score CTA
@@ -305,6 +311,8 @@ struct Walk {
   __device__ __forceinline__ bool whole() const { return t == 0 && n == nt; }
 };
 
+static_assert(sizeof(Walk) * 2 * N_LANE_WARPS <= OFF_SC - OFF_WALK, "segments");
+
 // The block-table entries of 32 pages, one per lane, from page `from` on.
 struct PageWindow {
   int64_t from;
@@ -360,7 +368,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 __device__ __forceinline__ float lg2_approx(float x) {
   float y;
-  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
@@ -518,6 +526,29 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
           (void)mbar_wait(&bars[B_SCFULL + i % NSC], (i / NSC) & 1, &zero, WAIT_NS);
       }
       __syncwarp();
+    } else if (warp == W_SCALE) {
+      // the row scales of every tile in the form that the softmax warps use: pairs of tokens,
+      // sLc made finite (a scale out of sight may be anything; its weight is 0 then, and in
+      // sight the NaN or infinity shows in sRc), and log2 sLc
+      bool ok = true;
+      for (int64_t i = 0; ok && i < w.left; ++i) {
+        const int g = (int)i, sc = g % NSC;
+        ok = wait(B_SCFULL + sc, (uint32_t)(g / NSC));
+        if (!ok) break;
+        float4* pl = reinterpret_cast<float4*>(sm + OFF_PL + sc * PL_BYTES);
+        float2* lg = reinterpret_cast<float2*>(pl + 64);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float4 s = reinterpret_cast<const float4*>(sm + OFF_SC + sc * 1024)[lane + 32 * h];
+          const float x = fminf(fmaxf(s.x, 0.f), 3.0e38f), y = fminf(fmaxf(s.z, 0.f), 3.0e38f);
+          pl[lane + 32 * h] = make_float4(x, y, fmaf(0.f, s.x, s.y), fmaf(0.f, s.z, s.w));
+          lg[lane + 32 * h] = make_float2(fmaxf(lg2_approx(x), LG_MIN), fmaxf(lg2_approx(y), LG_MIN));
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[B_PL + sc]);
+      }
+      if (!ok && lane == 0) fail();
+      __syncwarp();
     } else if (warp == W_MMA) {
       if (rank == 0) {
         const uint32_t id = idesc_f16(ROWS, TILE, false, false);  // e4m3 x e4m3 (format 0)
@@ -582,23 +613,21 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
       // ---------------------------------------------------------- query and softmax
       // A warp owns 32 rows (its TMEM lane quarter) and one part of the channels (of the
       // query) or of the tokens (of a tile).  A thread holds four rows, 8 p + lane / 4, and
-      // of 64 columns the pairs 8 j + 2 (lane % 4), so that a token's scales, read from shared
+      // of 32 columns the pairs 8 j + 2 (lane % 4), so that a token's scales, read from shared
       // memory, serve four rows.
       const int q = warp & 3;                 // TMEM lane quarter
-      const int part = (warp - W_LANE) >> 2;  // 256 channels of Lc and 32 of Rc; a page of a tile
+      const int part = (warp - W_LANE) >> 2;  // 128 channels of Lc and 16 of Rc; 32 tokens of a tile
       const int i4 = lane & 3, r8 = lane >> 2;
-      const int mine = q * 32 + 8 * i4 + r8;  // the row this lane speaks for in exchanges
+      const int row0 = q * 32 + r8;           // the thread's rows: row0 + 8 p
+      const int mine = row0 + 8 * i4;         // the row this lane speaks for in exchanges
       const uint32_t lane_addr = (uint32_t)(q * 32) << 16;
       float* xmax = reinterpret_cast<float*>(sm + OFF_XMAX);
       float* xl = reinterpret_cast<float*>(sm + OFF_XL);
       uint32_t* xq = reinterpret_cast<uint32_t*>(sm + OFF_XQ);
       float* mgs = reinterpret_cast<float*>(sm + OFF_MG);
-      const uint32_t qready = map_to(smem_u32(&bars[B_QREADY]), 0);
-      const uint32_t sempty = map_to(smem_u32(&bars[B_SEMPTY]), 0);
-      const uint32_t ctx_p = map_to(smem_u32(sm + OFF_P), rank + 2);
-      const uint32_t ctx_pfull = map_to(smem_u32(&bars[B_PFULL]), rank + 2);
-      const uint32_t ctx_rf = map_to(smem_u32(sm + OFF_RF), rank + 2);
-      const uint32_t ctx_rfbar = map_to(smem_u32(&bars[B_RF]), rank + 2);
+      int* lims = reinterpret_cast<int*>(sm + OFF_LIM);
+      float* cs = reinterpret_cast<float*>(sm + OFF_C);
+      Walk* walks = reinterpret_cast<Walk*>(sm + OFF_WALK) + (warp - W_LANE) * 2;
       uint32_t px = 0;
       auto quarter_sync = [&]() -> bool {
         __syncwarp();
@@ -612,24 +641,26 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
       };
       // The queries of a row tile: two e4m3 terms on the scale that puts a row's largest value
       // in [128, 256); c folds the scale back in, with sm_scale log2 e.
-      auto load_query = [&](const Walk& x, float (&c)[4]) -> bool {
+      auto load_query = [&](const Walk& x) -> bool {
         const uint4 *pq[4], *pr[4];  // (null past the sequence's last row)
         float top[4];                // a row's largest magnitude, as bf16 bits (ordered; 0x7F80 and up is inf or NaN)
         auto get = [](const uint4* p, int j) { return p != nullptr ? __ldg(p + j) : make_uint4(0u, 0u, 0u, 0u); };
+        const int64_t r0 = (int64_t)x.rt * ROWS + rank * CROWS, rows = (int64_t)x.s.nq * a.H;
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
-          const int64_t r = (int64_t)x.rt * ROWS + rank * CROWS + q * 32 + 8 * p + r8;
+          const int64_t r = r0 + row0 + 8 * p;
           const int64_t tok = x.s.q0 + (int64_t)((uint32_t)r / (uint32_t)a.H), head = (uint32_t)r % (uint32_t)a.H;
-          const bool real = r < (int64_t)x.s.nq * a.H;
-          pq[p] = real ? reinterpret_cast<const uint4*>(a.q_lat + tok * a.ql_t + head * a.ql_h + part * 256) + i4 : nullptr;
-          pr[p] = real ? reinterpret_cast<const uint4*>(a.q_rope + tok * a.qr_t + head * a.qr_h + part * 32) + i4 : nullptr;
+          pq[p] = r < rows ? reinterpret_cast<const uint4*>(a.q_lat + tok * a.ql_t + head * a.ql_h + part * 128) + i4 : nullptr;
+          pr[p] = r < rows && i4 < 2
+                      ? reinterpret_cast<const uint4*>(a.q_rope + tok * a.qr_t + head * a.qr_h + part * 16) + i4
+                      : nullptr;
         }
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
           uint32_t t2 = 0;
 #pragma unroll
-          for (int j = 0; j < 9; ++j) {
-            const uint4 v = j < 8 ? get(pq[p], 4 * j) : get(pr[p], 0);
+          for (int j = 0; j < 5; ++j) {
+            const uint4 v = j < 4 ? get(pq[p], 4 * j) : get(pr[p], 0);
             t2 = __vmaxu2(t2, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
                                        __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
           }
@@ -637,24 +668,31 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
           t2 = __vmaxu2(t2, __shfl_xor_sync(0xffffffffu, t2, 2));
           top[p] = __uint_as_float((t2 & 0xFFFFu) > (t2 >> 16) ? (t2 & 0xFFFFu) : (t2 >> 16));
         }
-        xq[mine * 2 + part] = __float_as_uint(own(top[0], top[1], top[2], top[3]));
+        xq[mine * 4 + part] = __float_as_uint(own(top[0], top[1], top[2], top[3]));
+        if (part == 0) {  // the keys that row q * 32 + lane sees (rows past the last one: as many as that)
+          const int tok = (int)((uint32_t)(r0 + q * 32 + lane) / (uint32_t)a.H);
+          lims[(x.seg & 1) * CROWS + q * 32 + lane] = limit_of(a, x.s, tok < x.s.nq ? tok : x.s.nq - 1);
+        }
         if (!quarter_sync()) return false;
-        const uint32_t qlo = smem_u32(sm + OFF_QL) + 2 * part * OP_ATOM, qrp = smem_u32(sm + OFF_QR);
+        const uint32_t qlo = smem_u32(sm + OFF_QL) + part * OP_ATOM, qrp = smem_u32(sm + OFF_QR);
 #pragma unroll
         for (int hl = 0; hl < 2; ++hl) {  // (read again: all four rows' values at once would spill)
-          uint32_t hw[32];
+          uint32_t hw[16];
 #pragma unroll
           for (int p2 = 0; p2 < 2; ++p2) {
-            const int p = 2 * hl + p2, row = q * 32 + 8 * p + r8;
-            const uint2 m2 = reinterpret_cast<const uint2*>(xq)[row];
-            const uint32_t mx = m2.x > m2.y ? m2.x : m2.y;
+            const int p = 2 * hl + p2, row = row0 + 8 * p;
+            const uint4 m4 = reinterpret_cast<const uint4*>(xq)[row];
+            uint32_t mx = m4.x > m4.y ? m4.x : m4.y;
+            mx = m4.z > mx ? m4.z : mx;
+            mx = m4.w > mx ? m4.w : mx;
             const bool nan = mx >= 0x7F80u;
             // largest value in [2^e, 2^(e+1)): the scale 2^(7 - e), at most 2^87
             int e = (int)(mx >> 7) - 127;
             e = e < -80 ? -80 : e;
             if (mx == 0 || nan) e = 7;
             const float sc = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
-            c[p] = fmaxf(a.sm_scale * LOG2E * __uint_as_float((uint32_t)(127 - 7 + e) << 23), 1e-37f);
+            if (part == 0 && i4 == 0)
+              cs[(x.seg & 1) * CROWS + row] = fmaxf(a.sm_scale * LOG2E * __uint_as_float((uint32_t)(127 - 7 + e) << 23), 1e-37f);
             // (a row with a NaN or an infinity is all NaN codes)
             auto terms = [&](uint32_t w0, uint32_t w1, uint32_t& hi, uint32_t& lo) {
               const float f4[4] = {bf16_lo(w0) * sc, bf16_hi(w0) * sc, bf16_lo(w1) * sc, bf16_hi(w1) * sc};
@@ -662,219 +700,232 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
               if (nan) hi = 0x7F7F7F7Fu;
             };
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {  // channels 32 j + 8 i4 .. + 7 of the part
+            for (int j = 0; j < 4; ++j) {  // channels 32 j + 8 i4 .. + 7 of the part
               const uint4 v = get(pq[p], 4 * j);
               uint2 lo;
               terms(v.x, v.y, hw[4 * j + 2 * p2], lo.x);
               terms(v.z, v.w, hw[4 * j + 2 * p2 + 1], lo.y);
-              sts64(qlo + (j >> 2) * OP_ATOM + sw128(row, 2 * (j & 3) + (i4 >> 1)) + (i4 & 1) * 8, lo);
+              sts64(qlo + sw128(row, 2 * j + (i4 >> 1)) + (i4 & 1) * 8, lo);
             }
-            const uint4 v = get(pr[p], 0);
-            uint2 hi, lo;
-            terms(v.x, v.y, hi.x, lo.x);
-            terms(v.z, v.w, hi.y, lo.y);
-            sts64(qrp + sw128(row, 2 * part + (i4 >> 1)) + (i4 & 1) * 8, hi);
-            sts64(qrp + sw128(row, 4 + 2 * part + (i4 >> 1)) + (i4 & 1) * 8, lo);
+            if (i4 < 2) {
+              const uint4 v = get(pr[p], 0);
+              uint2 hi, lo;
+              terms(v.x, v.y, hi.x, lo.x);
+              terms(v.z, v.w, hi.y, lo.y);
+              sts64(qrp + sw128(row, part) + i4 * 8, hi);
+              sts64(qrp + sw128(row, 4 + part) + i4 * 8, lo);
+            }
           }
           __syncwarp();
-          tmem_st_16x64(tmem + lane_addr + ((uint32_t)(16 * hl) << 16) + T_QH + part * 64, hw);
+          tmem_st_16x32(tmem + lane_addr + ((uint32_t)(16 * hl) << 16) + T_QH + part * 32, hw);
         }
         __syncwarp();
         tmem_wait_st();
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_cluster_local(qready);
+        if (lane == 0) arrive_cluster_local(map_to(smem_u32(&bars[B_QREADY]), 0));
         return true;
       };
 
-      bool ok = true;
-      float c[4] = {1.f, 1.f, 1.f, 1.f};
-      if (w.more()) ok = load_query(w, c);
-      while (ok && w.more()) {
-        Walk wn = w;  // the next segment, whose query is loaded as soon as this one's MMAs are done
-        wn.next(a);
-        float cn[4];
-        int lim[4];   // keys that the rows see
+      bool ok = true, more = w.more();
+      if (more) {
+        walks[0] = w;  // (every lane, the same)
+        __syncwarp();
+        ok = load_query(walks[0]) && quarter_sync();  // (the sync: cs and lims are read by every part)
+      }
+      for (int cur = 0; ok && more; cur ^= 1) {
+        // this segment, and the next, whose query is loaded as soon as this one's MMAs are done
+        const Walk& x = walks[cur];
+        {
+          Walk wn = x;
+          wn.next(a);
+          __syncwarp();
+          walks[cur ^ 1] = wn;
+          more = wn.more();
+        }
+        __syncwarp();
+        const int n_tiles = x.n;
+        const int* lim = lims + (x.seg & 1) * CROWS;
+        int first = lim[q * 32] - x.t * TILE - part * PART;  // tokens from this part on that the quarter's first row sees
+        uint64_t c2[4];                       // a row's c, twice
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
-          const int64_t r = (int64_t)w.rt * ROWS + rank * CROWS + q * 32 + 8 * p + r8;
-          const int tok = (int)((uint32_t)r / (uint32_t)a.H);
-          lim[p] = limit_of(a, w.s, tok < w.s.nq ? tok : w.s.nq - 1) - part * PART;
+          const float v = cs[(x.seg & 1) * CROWS + row0 + 8 * p];
+          c2[p] = pk2(v, v);
         }
-        float l[4], mg[4], mghi[4];
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          mg[p] = mghi[p] = -INFINITY;
-          l[p] = 0.f;  // this thread's tokens
-        }
-        for (int i = 0; i < w.n; ++i) {
+        float l[4] = {0.f, 0.f, 0.f, 0.f};    // this thread's tokens, of its four rows
+        float mg = -INFINITY, lift = 0.f;     // row `mine`: its reference, and how far that came down in all
+#pragma unroll 1
+        for (int i = 0; i < n_tiles; ++i, first -= TILE) {
           const int g = gt + i, buf = g & 1, sc = g % NSC;
-          if (!wait(B_SCFULL + sc, (uint32_t)(g / NSC))) {
-            ok = false;
-            break;
-          }
-          const float2* s2 = reinterpret_cast<const float2*>(sm + OFF_SC + sc * 1024) + part * PART;
-          const bool here = (facts[sc] >> part) & 1u;
-          // tokens of this part that the rows see
-          int n[4];
-          bool less = false;
-#pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            n[p] = here ? lim[p] - (w.t + i) * TILE : 0;
-            less = less || n[p] < PART;
-          }
-          const bool cut = __any_sync(0xffffffffu, less);
-          if (!wait(B_SFULL + buf, (uint32_t)(g >> 1))) {
+          if (!wait(B_PL + sc, (uint32_t)(g / NSC)) || !wait(B_SFULL + buf, (uint32_t)(g >> 1))) {
             ok = false;
             break;
           }
           tc_fence_after();
-          if (i == w.n - 1 && wn.more() && !load_query(wn, cn)) {
+          if (i == n_tiles - 1 && more && !load_query(walks[cur ^ 1])) {
             ok = false;
             break;
           }
-          uint32_t u[2][32];   // S_L, then u = sLc S_L + sRc S_R, as pairs of tokens
-          uint64_t sl[8];      // sLc of the thread's tokens
-          float ymax[4];
+          const float4* s4 = reinterpret_cast<const float4*>(sm + OFF_PL + sc * PL_BYTES) + part * 16 + i4;
+          const float2* g2 = reinterpret_cast<const float2*>(sm + OFF_PL + sc * PL_BYTES + 1024) + part * 16 + i4;
+          const bool here = (facts[sc] >> (part >> 1)) & 1u;
+          uint32_t u[2][16];   // S_L, then u = sLc S_L + sRc S_R, as pairs of tokens
+          uint64_t sl[4];      // sLc of the thread's tokens
+          {
+            uint32_t rr[2][16];
+            const uint32_t tl = tmem + lane_addr + T_SL + buf * TILE + part * PART;
+            const uint32_t tr = tmem + lane_addr + T_SR + part * PART;
+            tmem_ld_16x32(tl, u[0]);
+            tmem_ld_16x32(tr, rr[0]);
+            tmem_ld_16x32(tl + (16u << 16), u[1]);
+            tmem_ld_16x32(tr + (16u << 16), rr[1]);
+            tmem_wait_ld();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_cluster_local(map_to(smem_u32(&bars[B_SEMPTY + buf]), 0));
 #pragma unroll
-          for (int p = 0; p < 4; ++p) ymax[p] = -INFINITY;
-          auto scores = [&](auto some_out_of_sight) {
+            for (int j = 0; j < 4; ++j) {
+              const float4 s = s4[4 * j];
+              const uint64_t sr = pk2(s.z, s.w);
+              sl[j] = pk2(s.x, s.y);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {  // 32 tokens
-              uint32_t rr[2][16];
-              const uint32_t tl = tmem + lane_addr + T_SL + buf * TILE + part * PART + 32 * h;
-              const uint32_t tr = tmem + lane_addr + T_SR + part * PART + 32 * h;
-              tmem_ld_16x32(tl, &u[0][16 * h]);
-              tmem_ld_16x32(tr, rr[0]);
-              tmem_ld_16x32(tl + (16u << 16), &u[1][16 * h]);
-              tmem_ld_16x32(tr + (16u << 16), rr[1]);
-              tmem_wait_ld();
-              if (h == 1) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) arrive_cluster_local(sempty + buf * 8);
-              }
-#pragma unroll
-              for (int j4 = 0; j4 < 4; ++j4) {
-                const int j = 4 * h + j4;
-                const float4 s4 = *reinterpret_cast<const float4*>(s2 + 8 * j + 2 * i4);
-                const uint64_t s = pk2(s4.x, s4.z), sr = pk2(s4.y, s4.w);
-                const uint64_t lg = pk2(fmaxf(lg2_approx(s4.x), LG_MIN), fmaxf(lg2_approx(s4.z), LG_MIN));
-                // (a scale out of sight may be anything: made finite, its weight is 0)
-                sl[j] = pk2(fminf(fmaxf(s4.x, 0.f), 3.0e38f), fminf(fmaxf(s4.z, 0.f), 3.0e38f));
-#pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                  uint32_t* x = &u[p >> 1][4 * j + 2 * (p & 1)];
-                  const uint32_t* y = &rr[p >> 1][4 * j4 + 2 * (p & 1)];
-                  float2 f = up2(fma2(sr, pk2(__uint_as_float(y[0]), __uint_as_float(y[1])),
-                                      mul2(s, pk2(__uint_as_float(x[0]), __uint_as_float(x[1])))));
-                  if (some_out_of_sight) {
-                    f.x = 8 * j + 2 * i4 < n[p] ? f.x : -INFINITY;
-                    f.y = 8 * j + 2 * i4 + 1 < n[p] ? f.y : -INFINITY;
-                  }
-                  x[0] = __float_as_uint(f.x);
-                  x[1] = __float_as_uint(f.y);
-                  // (where a token is out of sight u is -inf and v is -inf or NaN, which max drops)
-                  const float2 v = up2(fma2(pk2(c[p], c[p]), pk2(f.x, f.y), lg));
-                  ymax[p] = max3(ymax[p], v.x, v.y);
-                }
+              for (int p = 0; p < 4; ++p) {
+                uint32_t* v = &u[p >> 1][4 * j + 2 * (p & 1)];
+                const uint32_t* y = &rr[p >> 1][4 * j + 2 * (p & 1)];
+                const float2 f = up2(fma2(sr, pk2(__uint_as_float(y[0]), __uint_as_float(y[1])),
+                                          mul2(sl[j], pk2(__uint_as_float(v[0]), __uint_as_float(v[1])))));
+                v[0] = __float_as_uint(f.x);
+                v[1] = __float_as_uint(f.y);
               }
             }
-          };
-          if (cut) scores(std::true_type());
-          else scores(std::false_type());
+          }
           auto pair = [&](int p, int j) -> uint64_t {
             return pk2(__uint_as_float(u[p >> 1][4 * j + 2 * (p & 1)]),
                        __uint_as_float(u[p >> 1][4 * j + 2 * (p & 1) + 1]));
           };
-          // the rows' largest weights over the tile
+          if (!here || first < PART) {  // some row does not see all of this part
 #pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            ymax[p] = fmaxf(ymax[p], __shfl_xor_sync(0xffffffffu, ymax[p], 1));
-            ymax[p] = fmaxf(ymax[p], __shfl_xor_sync(0xffffffffu, ymax[p], 2));
+            for (int p = 0; p < 4; ++p) {
+              const int n = here ? lim[row0 + 8 * p] - (lim[q * 32] - first) - 2 * i4 : 0;
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                  if (8 * j + h >= n) u[p >> 1][4 * j + 2 * (p & 1) + h] = 0xFF800000u;  // -inf
+            }
           }
-          float* xm = xmax + buf * 2 * CROWS;
-          xm[mine * 2 + part] = own(ymax[0], ymax[1], ymax[2], ymax[3]);
+          // the largest weight of row `mine` over the tile: the four rows' over this thread's
+          // tokens, then over the four lanes (each keeps the rows that are its), then the parts
+          float y[4];
+#pragma unroll
+          for (int p = 0; p < 4; ++p) y[p] = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 f = g2[4 * j];
+            const uint64_t lg = pk2(f.x, f.y);
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+              const float2 v = up2(fma2(c2[p], pair(p, j), lg));
+              y[p] = max3(y[p], v.x, v.y);
+            }
+          }
+          {
+            const bool b0 = i4 & 1, b1 = i4 & 2;
+            const float e0 = fmaxf(b0 ? y[1] : y[0], __shfl_xor_sync(0xffffffffu, b0 ? y[0] : y[1], 1));
+            const float e1 = fmaxf(b0 ? y[3] : y[2], __shfl_xor_sync(0xffffffffu, b0 ? y[2] : y[3], 1));
+            y[0] = fmaxf(b1 ? e1 : e0, __shfl_xor_sync(0xffffffffu, b1 ? e0 : e1, 2));
+          }
+          float* xm = xmax + buf * 4 * CROWS + mine * 4;
+          xm[part] = y[0];
           if (!quarter_sync()) {
             ok = false;
             break;
+          }
+          // its reference, and the factor of what was added up before (of l, and of O)
+          float f;
+          {
+            const float4 v = *reinterpret_cast<const float4*>(xm);
+            const float ym = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
+            float to = mg;
+            if (ym > mg + TAU) {
+              to = ym;
+            } else if (ym < mg - DOWN && mg - ym + lift <= DOWN_CAP) {
+              lift += mg - ym;
+              to = ym;
+            }
+            f = to == mg ? 1.f : (mg > -INFINITY ? ex2_approx(mg - to) : 0.f);
+            mg = to;
+          }
+          if (__any_sync(0xffffffffu, f != 1.f)) {
+#pragma unroll
+            for (int p = 0; p < 4; ++p) l[p] *= __shfl_sync(0xffffffffu, f, (lane & 28) + p);
           }
           if (g >= 2 && !wait(B_PFREE + buf, (uint32_t)((g >> 1) - 1))) {
             ok = false;
             break;
           }
-          const uint32_t dst = ctx_p + buf * P_STRIDE, bar = ctx_pfull + buf * 8;
-          float fm = 1.f;  // what O of row `mine` is multiplied by before this tile is added
+          // p = 2^(c u - M_g + 7) (nothing in sight so far: u is -inf, and p 0)
+          const float mneg = P_LOG - fmaxf(mg, -3.0e38f);
+          const uint32_t to = map_to(smem_u32(sm + OFF_P + buf * P_STRIDE), rank + 2);
+          const uint32_t bar = map_to(smem_u32(&bars[B_PFULL + buf]), rank + 2);
+          const uint32_t dst = to + prow(row0, part * 4 + i4);
+          if (part == 0) st_async_b32(to + P_F + mine * 4, __float_as_uint(f), bar);
 #pragma unroll
           for (int p = 0; p < 4; ++p) {
-            const float2 v = reinterpret_cast<const float2*>(xm)[q * 32 + 8 * p + r8];
-            const float ym = fmaxf(v.x, v.y);
-            float mgn = mg[p];
-            if (ym > mgn + TAU || (ym < mgn - DOWN && ym >= mghi[p] - DOWN_CAP && ym > -INFINITY)) mgn = ym;
-            const float fp = mgn == mg[p] ? 1.f : (mg[p] > -INFINITY ? ex2_approx(mg[p] - mgn) : 0.f);
-            fm = i4 == p ? fp : fm;
-            mg[p] = mgn;
-            mghi[p] = fmaxf(mghi[p], mgn);
-            l[p] *= fp;
-            // p = 2^(c u - M_g) P_TOP (nothing in sight so far: u is -inf, and p 0)
-            const float mneg = P_LOG - fmaxf(mgn, -3.0e38f);
-            const uint64_t c2 = pk2(c[p], c[p]), m2 = pk2(mneg, mneg);
-            uint64_t ls2 = pk2(0.f, 0.f);
+            const float mp = __shfl_sync(0xffffffffu, mneg, (lane & 28) + p);
+            const uint64_t m2 = pk2(mp, mp);
+            uint64_t ls2;
+            uint32_t h[4];
 #pragma unroll
-            for (int jh = 0; jh < 2; ++jh) {
-              uint32_t h[4];
-#pragma unroll
-              for (int j4 = 0; j4 < 4; ++j4) {
-                const int j = 4 * jh + j4;
-                const float2 z = up2(fma2(c2, pair(p, j), m2));
-                const uint64_t e = pk2(ex2_approx(z.x), ex2_approx(z.y));
-                ls2 = add2(ls2, e);
-                const float2 x = up2(mul2(e, sl[j]));
-                const __half2 h2 = __floats2half2_rn(x.x, x.y);
-                h[j4] = *reinterpret_cast<const uint32_t*>(&h2);
-              }
-              st_async_v4(dst + prow(q * 32 + 8 * p + r8, part * 8 + jh * 4 + i4), make_uint4(h[0], h[1], h[2], h[3]), bar);
+            for (int j = 0; j < 4; ++j) {
+              const float2 z = up2(fma2(c2[p], pair(p, j), m2));
+              const uint64_t e = pk2(ex2_approx(z.x), ex2_approx(z.y));
+              ls2 = j == 0 ? e : add2(ls2, e);
+              const float2 t2 = up2(mul2(e, sl[j]));
+              const __half2 h2 = __floats2half2_rn(t2.x, t2.y);
+              h[j] = *reinterpret_cast<const uint32_t*>(&h2);
             }
+            st_async_v4(dst + p * 2048, make_uint4(h[0], h[1], h[2], h[3]), bar);
             const float2 ls = up2(ls2);
             l[p] += ls.x + ls.y;
           }
-          if (part == 0) st_async_b32(dst + P_F + mine * 4, __float_as_uint(fm), bar);
         }
         if (!ok) break;
-        // ---- the row tile's (or its part's) end: the eight threads of a row add their l
+        // ---- the row tile's (or its part's) end: the sixteen threads of a row add their l
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
           l[p] += __shfl_xor_sync(0xffffffffu, l[p], 1);
           l[p] += __shfl_xor_sync(0xffffffffu, l[p], 2);
         }
-        xl[mine * 2 + part] = own(l[0], l[1], l[2], l[3]);
-        if (part == 0) mgs[mine] = own(mg[0], mg[1], mg[2], mg[3]);
+        xl[mine * 4 + part] = own(l[0], l[1], l[2], l[3]);
+        if (part == 0) mgs[mine] = mg;
         if (!quarter_sync()) {
           ok = false;
           break;
         }
         if (part == 0) {  // a row per lane
           const int hh = q * 32 + lane;
-          const float L = xl[hh * 2] + xl[hh * 2 + 1];  // on the scale 2^-M_g P_TOP, as O
+          const float4 l4 = reinterpret_cast<const float4*>(xl)[hh];
+          const float L = (l4.x + l4.y) + (l4.z + l4.w);  // on the scale 2^(7 - M_g), as O
           const float M = mgs[hh] - P_LOG;
           float f = 1.f;
-          if (w.whole()) {
+          if (x.whole()) {
             f = L == 0.f ? 0.f : 1.f / L;  // (a NaN stays one)
-            const int64_t r = (int64_t)w.rt * ROWS + rank * CROWS + hh;
-            if (a.lse != nullptr && r < (int64_t)w.s.nq * a.H)
-              a.lse[w.s.q0 * a.H + r] = L == 0.f ? -INFINITY : (M + log2f(L)) * LN2;
+            const int64_t r = (int64_t)x.rt * ROWS + rank * CROWS + hh;
+            if (a.lse != nullptr && r < (int64_t)x.s.nq * a.H)
+              a.lse[x.s.q0 * a.H + r] = L == 0.f ? -INFINITY : (M + log2f(L)) * LN2;
           } else {
-            const int64_t at = (int64_t)(2 * k + (w.seg == 0 ? 0 : 1)) * ROWS + rank * CROWS + hh;
+            const int64_t at = (int64_t)(2 * k + (x.seg == 0 ? 0 : 1)) * ROWS + rank * CROWS + hh;
             ws.m[at] = M;
             ws.l[at] = L;
           }
-          st_async_b32(ctx_rf + (w.seg % NRF) * 512 + hh * 4, __float_as_uint(f), ctx_rfbar + (w.seg % NRF) * 8);
+          const int rf = x.seg % NRF;
+          st_async_b32(map_to(smem_u32(sm + OFF_RF + rf * 512 + hh * 4), rank + 2), __float_as_uint(f),
+                       map_to(smem_u32(&bars[B_RF + rf]), rank + 2));
         }
-        gt += w.n;
-        w = wn;
-#pragma unroll
-        for (int p = 0; p < 4; ++p) c[p] = cn[p];
+        gt += n_tiles;
       }
       if (!ok && lane == 0) fail();
       // the context CTAs' last commits to this CTA have landed
@@ -924,6 +975,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
           (void)mbar_wait(&bars[B_VT + i % NVT], (i / NVT) & 1, &zero, WAIT_NS);
       }
       __syncwarp();
+    } else if (warp == W_SCALE) {
+      // (no scales here)
     } else if (warp == W_MMA) {
       if (rank == 2) {
         const uint32_t id = idesc_f16(ROWS, 256, false, true);  // A K-major, B = V MN-major
@@ -965,7 +1018,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
     } else {
       // ---------------------------------------------------------- operand, O rescale, results
       const int q = warp & 3;
-      const int part = (warp - W_LANE) >> 2;  // 64 tokens of the tile; 128 columns of an O half
+      const int part = (warp - W_LANE) >> 2;  // 32 tokens of the tile; 64 columns of an O half
       const int hh = q * 32 + lane;
       const uint32_t lane_addr = (uint32_t)(q * 32) << 16;
       const uint32_t rs = map_to(smem_u32(&bars[B_RS]), 2);
@@ -979,14 +1032,14 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
             break;
           }
           const uint32_t src = pbuf + pb * P_STRIDE;
-          uint32_t pv[2][4][4];  // [s][i][j]: tokens 32 s + 8 j + 2 i, + 1 of the part
+          uint32_t pv[4][4];  // [i][j]: tokens 8 j + 2 i, + 1 of the part
 #pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const uint4 v = lds128(src + prow(hh, part * 8 + u));
-            pv[u >> 2][u & 3][0] = v.x;
-            pv[u >> 2][u & 3][1] = v.y;
-            pv[u >> 2][u & 3][2] = v.z;
-            pv[u >> 2][u & 3][3] = v.w;
+          for (int u = 0; u < 4; ++u) {
+            const uint4 v = lds128(src + prow(hh, part * 4 + u));
+            pv[u][0] = v.x;
+            pv[u][1] = v.y;
+            pv[u][2] = v.z;
+            pv[u][3] = v.w;
           }
           const float f = reinterpret_cast<const float*>(sm + OFF_P + pb * P_STRIDE + P_F)[hh];
           const bool any = __any_sync(0xffffffffu, f != 1.f) && i > 0;
@@ -1001,17 +1054,17 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
           if (warp == W_LANE && lane == 0) mbar_arrive_expect_tx(&bars[B_PFULL + pb], P_BYTES);
           const uint32_t opnd = pbuf + pb * P_STRIDE;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {  // 16 tokens per 16-byte unit
+          for (int j = 0; j < 2; ++j) {  // 16 tokens per 16-byte unit
             uint32_t hw[4], lw[4];
 #pragma unroll
             for (int v = 0; v < 4; ++v) {  // tokens 16 j + 4 v .. + 3
               uint16_t h0, l0, h1, l1;
-              split_h2(pv[j >> 1][2 * (v & 1)][2 * (j & 1) + (v >> 1)], h0, l0);
-              split_h2(pv[j >> 1][2 * (v & 1) + 1][2 * (j & 1) + (v >> 1)], h1, l1);
+              split_h2(pv[2 * (v & 1)][2 * j + (v >> 1)], h0, l0);
+              split_h2(pv[2 * (v & 1) + 1][2 * j + (v >> 1)], h1, l1);
               hw[v] = (uint32_t)h0 | ((uint32_t)h1 << 16);
               lw[v] = (uint32_t)l0 | ((uint32_t)l1 << 16);
             }
-            const uint32_t off = sw128(hh, part * 4 + j);
+            const uint32_t off = sw128(hh, part * 2 + j);
             sts128(opnd + off, make_uint4(hw[0], hw[1], hw[2], hw[3]));
             sts128(opnd + OP_ATOM + off, make_uint4(lw[0], lw[1], lw[2], lw[3]));
           }
@@ -1021,9 +1074,9 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
           }
           if ((w.t + i + 1) * TILE > lim0 || facts[vs] != 3u) {
             // some row does not see all of this tile: no NaN code may stay in it
-            const uint32_t vb = vring + vs * VTILE + (warp - W_LANE) * 4096 + lane * 16;
-#pragma unroll 2
-            for (int u = 0; u < 8; ++u) {
+            const uint32_t vb = vring + vs * VTILE + (warp - W_LANE) * 2048 + lane * 16;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
               const uint4 v = lds128(vb + u * 512);
               sts128(vb + u * 512, make_uint4(no_nan(v.x), no_nan(v.y), no_nan(v.z), no_nan(v.w)));
             }
@@ -1040,13 +1093,13 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
             if (any) {
               tc_fence_after();
               __syncwarp();
-              const uint32_t col = tmem + lane_addr + h * 256 + part * 128;
-              uint32_t o[4][32];
+              const uint32_t col = tmem + lane_addr + h * 256 + part * 64;
+              uint32_t o[2][32];
 #pragma unroll
-              for (int s = 0; s < 4; ++s) tmem_ld32(col + 32 * s, o[s]);
+              for (int s = 0; s < 2; ++s) tmem_ld32(col + 32 * s, o[s]);
               tmem_wait_ld();
 #pragma unroll
-              for (int s = 0; s < 4; ++s) {
+              for (int s = 0; s < 2; ++s) {
 #pragma unroll
                 for (int v = 0; v < 32; ++v) o[s][v] = __float_as_uint(__uint_as_float(o[s][v]) * f);
                 tmem_st32(col + 32 * s, o[s]);
@@ -1094,8 +1147,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
           __syncwarp();
         };
 #pragma unroll 1
-        for (int s = 0; s < 8; ++s) {  // 32 columns at a time
-          const int col = (s >> 2) * 256 + part * 128 + (s & 3) * 32;
+        for (int s = 0; s < 4; ++s) {  // 32 columns at a time
+          const int col = (s >> 1) * 256 + part * 64 + (s & 1) * 32;
           uint32_t v[32];
           tmem_ld32(tmem + lane_addr + col, v);
           tmem_wait_ld();
