@@ -25,7 +25,7 @@
 //         them unless it lies 2^-9 below its row's largest): hi of Lc in TMEM, the rest
 //         in shared memory.  S_L is double-buffered in TMEM; S_R is not: its MMAs come last
 //         in a tile, when the previous one has long been read.
-//   sixteen softmax warps, each 32 rows x 32 tokens of a tile: u = sLc S_L + sRc S_R, per
+//   sixteen softmax warps, each 16 rows x 64 tokens of a tile: u = sLc S_L + sRc S_R, per
 //         thread p = 2^(c u - M_g + 7), its sum l, and the weights g' = p sLc as f16.  The
 //         reference M_g follows the largest weight 2^(c u) sLc of the row, not the largest
 //         score, so that the top weights fill the e4m3 range however the row scales differ
@@ -77,7 +77,7 @@ constexpr int NSC = 5;                       // row-scale rings, in tiles (see t
 constexpr int VBLK = TILE * 128;             // 16 KB: [128 tokens x 128 channels]
 constexpr int VTILE = 2 * VBLK;              // a context CTA's half of the channels
 constexpr int NVT = 3;                       // V ring, in tiles
-constexpr int PART = 32;                     // tokens of a softmax warp's share of a tile
+constexpr int SUB = 64;                      // tokens of a softmax warp's share of a tile (a page)
 constexpr int OP_ATOM = CROWS * 128;         // 16 KB: [128 rows x 128 tokens], e4m3
 constexpr int P_F = CROWS * TILE * 2;        // payload: g' f16 (256 bytes a row), then rescale factors
 constexpr int P_BYTES = P_F + CROWS * 4;
@@ -101,7 +101,8 @@ constexpr int B_SFULL = B_PL + NSC;      // [2] ranks 0, 1: S of a tile in TMEM
 constexpr int B_SEMPTY = B_SFULL + 2;        // [2] rank 0: S read (16 warps x 2 CTAs)
 constexpr int B_QREADY = B_SEMPTY + 2;       // rank 0: the row tile's query in place (16 warps x 2)
 constexpr int B_PX = B_QREADY + 1;           // [4] score: the four warps of a lane quarter meet
-constexpr int B_PFREE = B_PX + 4;            // [2] ranks 0, 1: payload buffer free
+constexpr int B_EX = B_PX + 4;               // [4][2] score: the two warps of sixteen rows meet
+constexpr int B_PFREE = B_EX + 8;            // [2] ranks 0, 1: payload buffer free
 constexpr int B_PFULL = B_PFREE + 2;         // [2] context: payload arrived
 constexpr int B_VT = B_PFULL + 2;            // [NVT] context: V tile loaded
 constexpr int B_VEMPTY = B_VT + NVT;         // [NVT] ranks 2, 3: consumed
@@ -116,9 +117,9 @@ constexpr int NBAR = B_DRAIN + 1;
 // shared memory (dynamic, 1024-byte aligned)
 constexpr int OFF_FLAGS = 512;               // tmem base, abort flag
 constexpr int OFF_FACTS = OFF_FLAGS + 16;    // [8] pages present in the tiles of a ring
-constexpr int OFF_XMAX = 1024;               // score: [2][128 rows][4 parts] a tile's largest weights
-constexpr int OFF_XL = OFF_XMAX + 4096;      // score: [128 rows][4 parts] l
-constexpr int OFF_XQ = OFF_XL + 2048;        // score: [128 rows][4 parts] query maxima
+constexpr int OFF_XMAX = 1024;               // score: [2][128 rows][2 pages] a tile's largest weights
+constexpr int OFF_XL = OFF_XMAX + 2048;      // score: [128 rows][2 pages] l
+constexpr int OFF_XQ = OFF_XL + 1024;        // score: [128 rows][4 parts] query maxima
 constexpr int OFF_MG = OFF_XQ + 2048;        // score: [128] M_g at a row tile's end
 constexpr int OFF_LIM = OFF_MG + 512;        // score: [2][128] keys that the rows see
 constexpr int OFF_C = OFF_LIM + 1024;        // score: [2][128] the rows' c
@@ -439,6 +440,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < NBAR; ++i) mbar_init(&bars[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&bars[B_SEMPTY + i], 2 * N_LANE_WARPS);
+    for (int i = 0; i < 8; ++i) mbar_init(&bars[B_EX + i], 2);
     mbar_init(&bars[B_QREADY], 2 * N_LANE_WARPS);
     for (int i = 0; i < 4; ++i) mbar_init(&bars[B_PX + i], N_LANE_WARPS / 4);
     mbar_init(&bars[B_CVT], N_LANE_WARPS);
@@ -504,7 +506,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
             }
           }
           if (!ok) break;
-          // the row scales' slot held tile g - 5: the MMAs of tile g - 3, done by now, began
+          // the row scales' slots held tile g - 5: the MMAs of tile g - 3, done by now, began
           // their last ones when the softmax warps had read S of tile g - 4, and so were
           // through with tile g - 5
           facts[sc] = (s0 >= 0 ? 1u : 0u) | (s1 >= 0 ? 2u : 0u);
@@ -611,12 +613,14 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
       __syncwarp();
     } else {
       // ---------------------------------------------------------- query and softmax
-      // A warp owns 32 rows (its TMEM lane quarter) and one part of the channels (of the
-      // query) or of the tokens (of a tile).  A thread holds four rows, 8 p + lane / 4, and
-      // of 32 columns the pairs 8 j + 2 (lane % 4), so that a token's scales, read from shared
-      // memory, serve four rows.
+      // The four warps of a TMEM lane quarter share its 32 rows: each takes a part of the
+      // query's channels for all of them, and one page of every tile for half of them (the two
+      // halves meet nowhere and fall out of step, so that one computes while the other waits).
+      // A thread holds the rows 8 p + lane / 4, and of the columns the pairs 8 j + 2 (lane %
+      // 4), so that a token's scales serve two rows.
       const int q = warp & 3;                 // TMEM lane quarter
-      const int part = (warp - W_LANE) >> 2;  // 128 channels of Lc and 16 of Rc; 32 tokens of a tile
+      const int part = (warp - W_LANE) >> 2;  // 128 channels of Lc and 16 of Rc
+      const int hl = part >> 1, sub = part & 1;  // rows 16 hl .. of the quarter; page of a tile
       const int i4 = lane & 3, r8 = lane >> 2;
       const int row0 = q * 32 + r8;           // the thread's rows: row0 + 8 p
       const int mine = row0 + 8 * i4;         // the row this lane speaks for in exchanges
@@ -628,6 +632,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
       int* lims = reinterpret_cast<int*>(sm + OFF_LIM);
       float* cs = reinterpret_cast<float*>(sm + OFF_C);
       Walk* walks = reinterpret_cast<Walk*>(sm + OFF_WALK) + (warp - W_LANE) * 2;
+      const int rh = row0 + 16 * hl;          // the thread's rows of a tile: rh, rh + 8
+      const int mh = rh + 8 * (i4 & 1);       // the row this lane speaks for there
       uint32_t px = 0;
       auto quarter_sync = [&]() -> bool {
         __syncwarp();
@@ -747,17 +753,18 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
         __syncwarp();
         const int n_tiles = x.n;
         const int* lim = lims + (x.seg & 1) * CROWS;
-        int first = lim[q * 32] - x.t * TILE - part * PART;  // tokens from this part on that the quarter's first row sees
-        uint64_t c2[4];                       // a row's c, twice
+        uint64_t c2[2];                       // the rows' c, twice
+        float l[2] = {0.f, 0.f};              // this thread's tokens, of its two rows
+        float mg = -INFINITY, lift = 0.f;     // row `mh`: its reference, and how far that came down in all
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          const float v = cs[(x.seg & 1) * CROWS + row0 + 8 * p];
+        for (int p = 0; p < 2; ++p) {
+          const float v = cs[(x.seg & 1) * CROWS + rh + 8 * p];
           c2[p] = pk2(v, v);
         }
-        float l[4] = {0.f, 0.f, 0.f, 0.f};    // this thread's tokens, of its four rows
-        float mg = -INFINITY, lift = 0.f;     // row `mine`: its reference, and how far that came down in all
+        int t0 = x.t * TILE + sub * SUB;
+        const int first = lim[q * 32 + 16 * hl];  // the keys that the first of the rows sees
 #pragma unroll 1
-        for (int i = 0; i < n_tiles; ++i, first -= TILE) {
+        for (int i = 0; i < n_tiles; ++i, t0 += TILE) {
           const int g = gt + i, buf = g & 1, sc = g % NSC;
           if (!wait(B_PL + sc, (uint32_t)(g / NSC)) || !wait(B_SFULL + buf, (uint32_t)(g >> 1))) {
             ok = false;
@@ -768,147 +775,154 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
             ok = false;
             break;
           }
-          const float4* s4 = reinterpret_cast<const float4*>(sm + OFF_PL + sc * PL_BYTES) + part * 16 + i4;
-          const float2* g2 = reinterpret_cast<const float2*>(sm + OFF_PL + sc * PL_BYTES + 1024) + part * 16 + i4;
-          const bool here = (facts[sc] >> (part >> 1)) & 1u;
-          uint32_t u[2][16];   // S_L, then u = sLc S_L + sRc S_R, as pairs of tokens
-          uint64_t sl[4];      // sLc of the thread's tokens
+          const float4* s4 = reinterpret_cast<const float4*>(sm + OFF_PL + sc * PL_BYTES) + sub * 32 + i4;
+          const float2* g2 = reinterpret_cast<const float2*>(sm + OFF_PL + sc * PL_BYTES + 1024) + sub * 32 + i4;
+          const bool here = (facts[sc] >> sub) & 1u;
+          uint32_t u[32];    // S_L, then u = sLc S_L + sRc S_R, as pairs of tokens
           {
-            uint32_t rr[2][16];
-            const uint32_t tl = tmem + lane_addr + T_SL + buf * TILE + part * PART;
-            const uint32_t tr = tmem + lane_addr + T_SR + part * PART;
-            tmem_ld_16x32(tl, u[0]);
-            tmem_ld_16x32(tr, rr[0]);
-            tmem_ld_16x32(tl + (16u << 16), u[1]);
-            tmem_ld_16x32(tr + (16u << 16), rr[1]);
+            const uint32_t tl = tmem + lane_addr + ((uint32_t)(16 * hl) << 16) + T_SL + buf * TILE + sub * SUB;
+            const uint32_t tr = tmem + lane_addr + ((uint32_t)(16 * hl) << 16) + T_SR + sub * SUB;
+            uint32_t rr[32];
+            tmem_ld_16x32(tl, u);
+            tmem_ld_16x32(tr, rr);
+            tmem_ld_16x32(tl + 32, u + 16);
+            tmem_ld_16x32(tr + 32, rr + 16);
             tmem_wait_ld();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive_cluster_local(map_to(smem_u32(&bars[B_SEMPTY + buf]), 0));
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 8; ++j) {
               const float4 s = s4[4 * j];
-              const uint64_t sr = pk2(s.z, s.w);
-              sl[j] = pk2(s.x, s.y);
+              const uint64_t sl = pk2(s.x, s.y), sr = pk2(s.z, s.w);
 #pragma unroll
-              for (int p = 0; p < 4; ++p) {
-                uint32_t* v = &u[p >> 1][4 * j + 2 * (p & 1)];
-                const uint32_t* y = &rr[p >> 1][4 * j + 2 * (p & 1)];
-                const float2 f = up2(fma2(sr, pk2(__uint_as_float(y[0]), __uint_as_float(y[1])),
-                                          mul2(sl[j], pk2(__uint_as_float(v[0]), __uint_as_float(v[1])))));
-                v[0] = __float_as_uint(f.x);
-                v[1] = __float_as_uint(f.y);
+              for (int e = 4 * j; e < 4 * j + 4; e += 2) {
+                const float2 f = up2(fma2(sr, pk2(__uint_as_float(rr[e]), __uint_as_float(rr[e + 1])),
+                                          mul2(sl, pk2(__uint_as_float(u[e]), __uint_as_float(u[e + 1])))));
+                u[e] = __float_as_uint(f.x);
+                u[e + 1] = __float_as_uint(f.y);
               }
             }
           }
           auto pair = [&](int p, int j) -> uint64_t {
-            return pk2(__uint_as_float(u[p >> 1][4 * j + 2 * (p & 1)]),
-                       __uint_as_float(u[p >> 1][4 * j + 2 * (p & 1) + 1]));
+            return pk2(__uint_as_float(u[4 * j + 2 * p]), __uint_as_float(u[4 * j + 2 * p + 1]));
           };
-          if (!here || first < PART) {  // some row does not see all of this part
+          if (!here || first - t0 < SUB) {  // some row does not see all of this page
 #pragma unroll
-            for (int p = 0; p < 4; ++p) {
-              const int n = here ? lim[row0 + 8 * p] - (lim[q * 32] - first) - 2 * i4 : 0;
+            for (int p = 0; p < 2; ++p) {
+              const int n = here ? lim[rh + 8 * p] - t0 - 2 * i4 : 0;
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
+              for (int j = 0; j < 8; ++j)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                  if (8 * j + h >= n) u[p >> 1][4 * j + 2 * (p & 1) + h] = 0xFF800000u;  // -inf
+                for (int e = 0; e < 2; ++e)
+                  if (8 * j + e >= n) u[4 * j + 2 * p + e] = 0xFF800000u;  // -inf
             }
           }
-          // the largest weight of row `mine` over the tile: the four rows' over this thread's
-          // tokens, then over the four lanes (each keeps the rows that are its), then the parts
-          float y[4];
+          // the largest weight of row `mh` over the tile: the two rows' over this thread's
+          // tokens, then over the four lanes, then over the two pages
+          float y[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-          for (int p = 0; p < 4; ++p) y[p] = -INFINITY;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
+          for (int j = 0; j < 8; ++j) {
             const float2 f = g2[4 * j];
             const uint64_t lg = pk2(f.x, f.y);
 #pragma unroll
-            for (int p = 0; p < 4; ++p) {
+            for (int p = 0; p < 2; ++p) {
               const float2 v = up2(fma2(c2[p], pair(p, j), lg));
               y[p] = max3(y[p], v.x, v.y);
             }
           }
-          {
-            const bool b0 = i4 & 1, b1 = i4 & 2;
-            const float e0 = fmaxf(b0 ? y[1] : y[0], __shfl_xor_sync(0xffffffffu, b0 ? y[0] : y[1], 1));
-            const float e1 = fmaxf(b0 ? y[3] : y[2], __shfl_xor_sync(0xffffffffu, b0 ? y[2] : y[3], 1));
-            y[0] = fmaxf(b1 ? e1 : e0, __shfl_xor_sync(0xffffffffu, b1 ? e0 : e1, 2));
-          }
-          float* xm = xmax + buf * 4 * CROWS + mine * 4;
-          xm[part] = y[0];
-          if (!quarter_sync()) {
+          const bool b0 = i4 & 1;
+          float ym = fmaxf(b0 ? y[1] : y[0], __shfl_xor_sync(0xffffffffu, b0 ? y[0] : y[1], 1));
+          ym = fmaxf(ym, __shfl_xor_sync(0xffffffffu, ym, 2));
+          float* xm = xmax + (buf * CROWS + mh) * 2;
+          xm[sub] = ym;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[B_EX + q * 2 + hl]);
+          if (!wait(B_EX + q * 2 + hl, (uint32_t)g)) {
             ok = false;
             break;
           }
           // its reference, and the factor of what was added up before (of l, and of O)
-          float f;
+          float mn = mg;
           {
-            const float4 v = *reinterpret_cast<const float4*>(xm);
-            const float ym = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
-            float to = mg;
+            const float2 v2 = *reinterpret_cast<const float2*>(xm);
+            ym = fmaxf(v2.x, v2.y);
             if (ym > mg + TAU) {
-              to = ym;
+              mn = ym;
             } else if (ym < mg - DOWN && mg - ym + lift <= DOWN_CAP) {
               lift += mg - ym;
-              to = ym;
+              mn = ym;
             }
-            f = to == mg ? 1.f : (mg > -INFINITY ? ex2_approx(mg - to) : 0.f);
-            mg = to;
           }
+          const float f = mn == mg ? 1.f : (mg > -INFINITY ? ex2_approx(mg - mn) : 0.f);
+          mg = mn;
           if (__any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll
-            for (int p = 0; p < 4; ++p) l[p] *= __shfl_sync(0xffffffffu, f, (lane & 28) + p);
+            for (int p = 0; p < 2; ++p) l[p] *= __shfl_sync(0xffffffffu, f, (lane & 28) + p);
           }
           if (g >= 2 && !wait(B_PFREE + buf, (uint32_t)((g >> 1) - 1))) {
             ok = false;
             break;
           }
-          // p = 2^(c u - M_g + 7) (nothing in sight so far: u is -inf, and p 0)
-          const float mneg = P_LOG - fmaxf(mg, -3.0e38f);
           const uint32_t to = map_to(smem_u32(sm + OFF_P + buf * P_STRIDE), rank + 2);
           const uint32_t bar = map_to(smem_u32(&bars[B_PFULL + buf]), rank + 2);
-          const uint32_t dst = to + prow(row0, part * 4 + i4);
-          if (part == 0) st_async_b32(to + P_F + mine * 4, __float_as_uint(f), bar);
+          if (sub == 0 && i4 < 2) st_async_b32(to + P_F + mh * 4, __float_as_uint(f), bar);
+          // p = 2^(c u - M_g + 7) (nothing in sight so far: u is -inf, and p 0)
+          const float mneg = P_LOG - fmaxf(mn, -3.0e38f);
+          uint64_t m2[2], ls2[2];
 #pragma unroll
-          for (int p = 0; p < 4; ++p) {
+          for (int p = 0; p < 2; ++p) {
             const float mp = __shfl_sync(0xffffffffu, mneg, (lane & 28) + p);
-            const uint64_t m2 = pk2(mp, mp);
-            uint64_t ls2;
-            uint32_t h[4];
+            m2[p] = pk2(mp, mp);
+            ls2[p] = pk2(0.f, 0.f);
+          }
+          const uint32_t dst = to + prow(rh, sub * 8 + i4);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float2 z = up2(fma2(c2[p], pair(p, j), m2));
-              const uint64_t e = pk2(ex2_approx(z.x), ex2_approx(z.y));
-              ls2 = j == 0 ? e : add2(ls2, e);
-              const float2 t2 = up2(mul2(e, sl[j]));
-              const __half2 h2 = __floats2half2_rn(t2.x, t2.y);
-              h[j] = *reinterpret_cast<const uint32_t*>(&h2);
+          for (int jh = 0; jh < 2; ++jh) {
+            uint32_t h[2][4];
+#pragma unroll
+            for (int j4 = 0; j4 < 4; ++j4) {
+              const int j = 4 * jh + j4;
+              const float2 s = *reinterpret_cast<const float2*>(s4 + 4 * j);
+#pragma unroll
+              for (int p = 0; p < 2; ++p) {
+                const float2 z = up2(fma2(c2[p], pair(p, j), m2[p]));
+                const uint64_t e = pk2(ex2_approx(z.x), ex2_approx(z.y));
+                ls2[p] = add2(ls2[p], e);
+                const float2 t2 = up2(mul2(e, pk2(s.x, s.y)));
+                const __half2 h2 = __floats2half2_rn(t2.x, t2.y);
+                h[p][j4] = *reinterpret_cast<const uint32_t*>(&h2);
+              }
             }
-            st_async_v4(dst + p * 2048, make_uint4(h[0], h[1], h[2], h[3]), bar);
-            const float2 ls = up2(ls2);
-            l[p] += ls.x + ls.y;
+            // (unit sub * 8 + 4 jh + i4 of row rh + 8 p: 4 jh turns bit 2 of the swizzled unit)
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+              st_async_v4((dst ^ (uint32_t)(jh * 64)) + p * 2048, make_uint4(h[p][0], h[p][1], h[p][2], h[p][3]), bar);
+          }
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            const float2 s = up2(ls2[p]);
+            l[p] += s.x + s.y;
           }
         }
         if (!ok) break;
-        // ---- the row tile's (or its part's) end: the sixteen threads of a row add their l
+        // ---- the row tile's (or its part's) end: the eight threads of a row add their l
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
+        for (int p = 0; p < 2; ++p) {
           l[p] += __shfl_xor_sync(0xffffffffu, l[p], 1);
           l[p] += __shfl_xor_sync(0xffffffffu, l[p], 2);
         }
-        xl[mine * 4 + part] = own(l[0], l[1], l[2], l[3]);
-        if (part == 0) mgs[mine] = mg;
+        if (i4 < 2) {
+          xl[mh * 2 + sub] = i4 ? l[1] : l[0];
+          if (sub == 0) mgs[mh] = mg;
+        }
         if (!quarter_sync()) {
           ok = false;
           break;
         }
         if (part == 0) {  // a row per lane
           const int hh = q * 32 + lane;
-          const float4 l4 = reinterpret_cast<const float4*>(xl)[hh];
-          const float L = (l4.x + l4.y) + (l4.z + l4.w);  // on the scale 2^(7 - M_g), as O
+          const float L = xl[hh * 2] + xl[hh * 2 + 1];  // on the scale 2^(7 - M_g), as O
           const float M = mgs[hh] - P_LOG;
           float f = 1.f;
           if (x.whole()) {
