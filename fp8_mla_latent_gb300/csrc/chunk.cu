@@ -33,7 +33,7 @@
 //         by more than 2^TAU, down by more than 2^DOWN).  g' goes to the row's context CTA by
 //         asynchronous remote stores.
 // Context pair (ranks 2, 3), per key tile:
-//   sixteen warps split g' into two e4m3 terms (hi + residual) in place, as the A operand,
+//   sixteen warps split g' into two e4m3 terms (hi + residual), the A operand,
 //         and rescale the rows of O whose M_g moved;
 //   O += g'_hi V + g'_lo V    M = 256, N = 256 channels (each CTA holds half of them as
 //         B, the cache tile read MN-major), 16 MMAs into all 512 TMEM columns.
@@ -76,7 +76,7 @@ constexpr int NK = 3;                        // K ring, in tiles; loaded and fre
 constexpr int NSC = 5;                       // row-scale rings, in tiles (see the load warp)
 constexpr int VBLK = TILE * 128;             // 16 KB: [128 tokens x 128 channels]
 constexpr int VTILE = 2 * VBLK;              // a context CTA's half of the channels
-constexpr int NVT = 3;                       // V ring, in tiles
+constexpr int NVT = 2;                       // V ring, in tiles
 constexpr int SUB = 64;                      // tokens of a softmax warp's share of a tile (a page)
 constexpr int OP_ATOM = CROWS * 128;         // 16 KB: [128 rows x 128 tokens], e4m3
 constexpr int P_F = CROWS * TILE * 2;        // payload: g' f16 (256 bytes a row), then rescale factors
@@ -102,12 +102,12 @@ constexpr int B_SEMPTY = B_SFULL + 2;        // [2] rank 0: S read (16 warps x 2
 constexpr int B_QREADY = B_SEMPTY + 2;       // rank 0: the row tile's query in place (16 warps x 2)
 constexpr int B_PX = B_QREADY + 1;           // [4] score: the four warps of a lane quarter meet
 constexpr int B_EX = B_PX + 4;               // [4][2] score: the two warps of sixteen rows meet
-constexpr int B_PFREE = B_EX + 8;            // [2] ranks 0, 1: payload buffer free
+constexpr int B_PFREE = B_EX + 8;              // [2] score: payload buffer read (the partner's 16 warps)
 constexpr int B_PFULL = B_PFREE + 2;         // [2] context: payload arrived
 constexpr int B_VT = B_PFULL + 2;            // [NVT] context: V tile loaded
 constexpr int B_VEMPTY = B_VT + NVT;         // [NVT] ranks 2, 3: consumed
-constexpr int B_CVT = B_VEMPTY + NVT;        // context: every warp has read the payload
-constexpr int B_RS = B_CVT + 1;              // [2] rank 2: operand, V and O half ready (16 warps x 2)
+constexpr int B_EP = B_VEMPTY + NVT;         // context: a row tile's results have left shared memory
+constexpr int B_RS = B_EP + 1;              // [2] rank 2: operand, V and O half ready (16 warps x 2)
 constexpr int B_ODONE = B_RS + 2;            // [2] ranks 2, 3: MMAs of an O half done
 constexpr int NRF = 4;
 constexpr int B_RF = B_ODONE + 2;            // [NRF] context: row factors of a finished row tile arrived
@@ -132,17 +132,17 @@ constexpr int OFF_QR = OFF_QL + 4 * OP_ATOM;                      // score: Rc, 
 constexpr int OFF_K = OFF_QR + OP_ATOM;
 constexpr int TOTAL_S = OFF_K + NK * KTILE;
 constexpr int OFF_RF = 1024;                 // context: [NRF][128] row factors
-constexpr int OFF_P = 4096;                  // context: two payloads / operands
-constexpr int OFF_V = OFF_P + 2 * P_STRIDE;
-constexpr int OFF_ST = OFF_V + NVT * VTILE;  // context: [16 warps][2 KB] results on their way out
-constexpr int TOTAL_C = OFF_ST + N_LANE_WARPS * 2048;
+constexpr int OFF_P = 4096;                  // context: two payloads
+constexpr int OFF_OP = OFF_P + 2 * P_STRIDE; // context: two operands (hi and lo atoms); results on their way out
+constexpr int OFF_V = OFF_OP + 4 * OP_ATOM;
+constexpr int TOTAL_C = OFF_V + NVT * VTILE;
 constexpr int SMEM = TOTAL_S > TOTAL_C ? TOTAL_S : TOTAL_C;
 // TMEM columns of a score CTA
 constexpr int T_SL = 0, T_SR = 256, T_QH = 384;
 static_assert(NSC >= NK + 2 && NSC <= 8 && NVT <= 8 && OFF_FACTS + 32 <= OFF_XMAX, "rings");
 static_assert(NBAR * 8 <= OFF_FLAGS && OFF_RF + NRF * 512 <= OFF_P, "shared memory layout");
 static_assert(OFF_K % 1024 == 0 && KTILE % 1024 == 0 && OFF_V % 1024 == 0 && P_STRIDE % 1024 == 0, "swizzle atoms");
-static_assert(P_BYTES <= P_STRIDE && 2 * OP_ATOM <= P_STRIDE, "payload and operand share a buffer");
+static_assert(P_BYTES <= P_STRIDE && N_LANE_WARPS * 2048 <= 4 * OP_ATOM, "payload and staging");
 static_assert(SMEM <= 232448, "shared memory above the per-CTA limit");
 
 // ------------------------------------------------------------------ work
@@ -443,7 +443,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
     for (int i = 0; i < 8; ++i) mbar_init(&bars[B_EX + i], 2);
     mbar_init(&bars[B_QREADY], 2 * N_LANE_WARPS);
     for (int i = 0; i < 4; ++i) mbar_init(&bars[B_PX + i], N_LANE_WARPS / 4);
-    mbar_init(&bars[B_CVT], N_LANE_WARPS);
+    mbar_init(&bars[B_EP], N_LANE_WARPS);
+    for (int i = 0; i < 2; ++i) mbar_init(&bars[B_PFREE + i], N_LANE_WARPS);
     for (int i = 0; i < 2; ++i) mbar_init(&bars[B_RS + i], 2 * N_LANE_WARPS);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -942,7 +943,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
         gt += n_tiles;
       }
       if (!ok && lane == 0) fail();
-      // the context CTAs' last commits to this CTA have landed
+      // the context CTAs' last arrivals at this CTA have landed
       if (ok && gt > 0) {
         const int zero = 0;
         for (int i = gt > 2 ? gt - 2 : 0; i < gt; ++i)
@@ -994,13 +995,13 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
     } else if (warp == W_MMA) {
       if (rank == 2) {
         const uint32_t id = idesc_f16(ROWS, 256, false, true);  // A K-major, B = V MN-major
-        const uint64_t pd = smem_desc(pbuf, 16, 1024, SW128);
+        const uint64_t pd = smem_desc(smem_u32(sm + OFF_OP), 16, 1024, SW128);
         const uint64_t vd = smem_desc(vring, 16, 1024, SW128);
         bool ok = true;
         for (; ok && w.more(); w.next(a)) {
           for (int i = 0; ok && i < w.n; ++i) {
             const int g = gt + i;
-            const uint64_t ad = pd + (uint64_t)((g & 1) * P_STRIDE >> 4);
+            const uint64_t ad = pd + (uint64_t)((g & 1) * 2 * OP_ATOM >> 4);
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
               if (!wait_cluster(B_RS + h, (uint32_t)g)) {
@@ -1019,7 +1020,6 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
             }
             if (!ok) break;
             mma_commit_pair_warp(&bars[B_VEMPTY + g % NVT], 0xC);
-            mma_commit_pair_warp(&bars[B_PFREE + (g & 1)], 0x3);
           }
           gt += w.n;
         }
@@ -1036,6 +1036,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
       const int hh = q * 32 + lane;
       const uint32_t lane_addr = (uint32_t)(q * 32) << 16;
       const uint32_t rs = map_to(smem_u32(&bars[B_RS]), 2);
+      const uint32_t pfree = map_to(smem_u32(&bars[B_PFREE]), rank - 2);
       bool ok = true;
       for (; ok && w.more(); w.next(a)) {
         const int lim0 = limit_of(a, w.s, (int)((uint32_t)(w.rt * ROWS) / (uint32_t)a.H));  // the tile's first row sees least
@@ -1057,16 +1058,14 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
           }
           const float f = reinterpret_cast<const float*>(sm + OFF_P + pb * P_STRIDE + P_F)[hh];
           const bool any = __any_sync(0xffffffffu, f != 1.f) && i > 0;
-          // every warp has read this payload: its buffer may now take the operand, and the
-          // next payload (whose bytes come after this tile's MMAs) may be expected
+          // the payload is read: the next one may be expected, and then come
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bars[B_CVT]);
-          if (!wait(B_CVT, (uint32_t)(g + w.seg))) {
-            ok = false;
-            break;
+          if (lane == 0) {
+            if (warp == W_LANE) mbar_arrive_expect_tx(&bars[B_PFULL + pb], P_BYTES);
+            arrive_cluster_local(pfree + pb * 8);
           }
-          if (warp == W_LANE && lane == 0) mbar_arrive_expect_tx(&bars[B_PFULL + pb], P_BYTES);
-          const uint32_t opnd = pbuf + pb * P_STRIDE;
+          // the operand buffer was read by the MMAs of tile g - 2, waited for with tile g - 1
+          const uint32_t opnd = smem_u32(sm + OFF_OP) + pb * 2 * OP_ATOM;
 #pragma unroll
           for (int j = 0; j < 2; ++j) {  // 16 tokens per 16-byte unit
             uint32_t hw[4], lw[4];
@@ -1144,7 +1143,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
         const bool whole = w.whole();
         const int64_t r0 = (int64_t)w.rt * ROWS + half_of * CROWS + q * 32;  // the warp's first row
         const int64_t left = (int64_t)w.s.nq * a.H - r0;
-        const uint32_t stage = smem_u32(sm + OFF_ST) + (warp - W_LANE) * 2048;
+        const uint32_t stage = smem_u32(sm + OFF_OP) + (warp - W_LANE) * 2048;
         auto unit = [](int r, int u) -> uint32_t { return (uint32_t)(r * 64 + ((u ^ ((r >> 1) & 3)) << 4)); };
         uint8_t* dst = whole ? reinterpret_cast<uint8_t*>(a.out + (w.s.q0 * a.H + r0) * DL)
                              : reinterpret_cast<uint8_t*>(
@@ -1190,15 +1189,18 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
             }
           }
         }
-        // the factor buffer's next use, NRF segments on: its bytes come after this row
-        // tile's successor has been accumulated
+        // the factor buffer's next phase, NRF segments on (its bytes come after the payloads of
+        // the tiles between, which every warp has to read); and the operand buffers may be
+        // written again when every warp's results have left them
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[B_CVT]);
-        if (!wait(B_CVT, (uint32_t)(gt + w.seg))) {
+        if (lane == 0) {
+          if (warp == W_LANE) mbar_arrive_expect_tx(&bars[B_RF + rf], CROWS * 4);
+          mbar_arrive(&bars[B_EP]);
+        }
+        if (!wait(B_EP, (uint32_t)w.seg)) {
           ok = false;
           break;
         }
-        if (warp == W_LANE && lane == 0) mbar_arrive_expect_tx(&bars[B_RF + rf], CROWS * 4);
       }
       if (!ok && lane == 0) fail();
       __syncwarp();
