@@ -69,6 +69,7 @@ constexpr int N_LANE_WARPS = 16;             // four per TMEM lane quarter, and 
 constexpr int NTHREADS = (W_LANE + N_LANE_WARPS) * 32;
 constexpr int MAX_CLUSTERS = NUM_SMS / 4;
 constexpr int MIN_TILES = 2;                 // key tiles that are worth a cluster of their own
+constexpr int SWITCH = 2;                    // what beginning a row tile costs, in key tiles
 constexpr int BLK = PAGE * 128;              // 8 KB: [64 tokens x 128 bytes]
 constexpr int RBLK = PAGE * DR;              // 4 KB: [64 tokens x 64 bytes]
 constexpr int KTILE = 4 * BLK + RBLK;        // a score CTA's page of a tile: 36 KB
@@ -147,14 +148,13 @@ static_assert(SMEM <= 232448, "shared memory above the per-CTA limit");
 
 // ------------------------------------------------------------------ work
 // Plan of cluster k: its first row tile (sequence b, row tile rt, nt key tiles of
-// which off come before the range), the unit where the range starts and its length.
+// which off come before the range), the unit where the range starts and its units.
 struct PlanEntry {
   int32_t b, rt, nt, off;
-  int64_t x, cnt;
+  int64_t x;
 };
 struct Plan {
-  int64_t n_clusters;
-  int64_t pad[3];
+  int64_t n_clusters, units;
   PlanEntry e[MAX_CLUSTERS];
 };
 
@@ -247,29 +247,35 @@ __global__ void __launch_bounds__(1024) plan_kernel(const ChunkArgs a, Plan* pla
     rt = (int)(p - base[lo]);
     return key_tiles(a, seq_info(a, b, false), rt);
   };
-  int64_t mine = 0, total;
+  // The ranges are equal on an axis where a row tile is SWITCH + nt long, and the border falls on a
+  // key tile of it; x counts units (key tiles).
+  int64_t mine = 0, units;
   for (int64_t p = threadIdx.x; p < pairs; p += 1024) mine += tiles(p);
-  (void)plan_sum(mine, tmp, &total);
-  int64_t nc = total / MIN_TILES;
-  nc = nc > clusters ? clusters : (nc < 1 ? (total > 0 ? 1 : 0) : nc);
-  if (threadIdx.x == 0) plan->n_clusters = nc;
+  (void)plan_sum(mine, tmp, &units);
+  const int64_t total = units + pairs * SWITCH;
+  int64_t nc = units / MIN_TILES;
+  nc = nc > clusters ? clusters : (nc < 1 ? (units > 0 ? 1 : 0) : nc);
+  if (threadIdx.x == 0) {
+    plan->n_clusters = nc;
+    plan->units = units;
+  }
   int64_t at = 0;
   for (int64_t p0 = 0; p0 < pairs; p0 += 1024) {
-    const int64_t n = tiles(p0 + threadIdx.x);
+    const int64_t p = p0 + threadIdx.x, n = tiles(p);
     int64_t sum;
-    const int64_t S = at + plan_sum(n, tmp, &sum) - n;
+    const int64_t before = at + plan_sum(n, tmp, &sum) - n;  // units before the row tile
+    const int64_t S = before + p * SWITCH, len = n + SWITCH;
     int64_t k = n > 0 ? S * nc / total : nc;
     while (k < nc && k * total / nc < S) ++k;
     for (; k < nc; ++k) {
       const int64_t x = k * total / nc;
-      if (x >= S + n) break;
+      if (x >= S + len) break;
       PlanEntry e;
       e.b = b;
       e.rt = rt;
       e.nt = (int32_t)n;
-      e.off = (int32_t)(x - S);
-      e.x = x;
-      e.cnt = (k + 1) * total / nc - x;
+      e.off = (int32_t)(x - S > SWITCH ? x - S - SWITCH : 0);
+      e.x = before + e.off;
       plan->e[k] = e;
     }
     at += sum;
@@ -284,12 +290,13 @@ struct Walk {
   int n;              // key tiles of the segment
   int seg;            // segments before this one
   int64_t left;       // units from this segment on
-  __device__ __forceinline__ void start(const ChunkArgs& a, const PlanEntry& e) {
+  __device__ __forceinline__ void start(const ChunkArgs& a, const Plan& plan, int k) {
+    const PlanEntry e = plan.e[k];
     b = e.b;
     rt = e.rt;
     nt = e.nt;
     t = e.off;
-    left = e.cnt;
+    left = (k + 1 < plan.n_clusters ? plan.e[k + 1].x : plan.units) - e.x;
     seg = 0;
     s = seq_info(a, b, false);
     n = (int)(left < nt - t ? left : nt - t);
@@ -465,7 +472,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
   grid_dependency_wait();  // the plan
   const bool work = k < ws.plan->n_clusters;
   Walk w;
-  if (work) w.start(a, ws.plan->e[k]);
+  if (work) w.start(a, *ws.plan, k);
   else w.left = 0;
   int gt = 0;  // key tiles of the range before this segment
 
@@ -783,25 +790,31 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
           {
             const uint32_t tl = tmem + lane_addr + ((uint32_t)(16 * hl) << 16) + T_SL + buf * TILE + sub * SUB;
             const uint32_t tr = tmem + lane_addr + ((uint32_t)(16 * hl) << 16) + T_SR + sub * SUB;
-            uint32_t rr[32];
             tmem_ld_16x32(tl, u);
-            tmem_ld_16x32(tr, rr);
             tmem_ld_16x32(tl + 32, u + 16);
-            tmem_ld_16x32(tr + 32, rr + 16);
-            tmem_wait_ld();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) arrive_cluster_local(map_to(smem_u32(&bars[B_SEMPTY + buf]), 0));
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float4 s = s4[4 * j];
-              const uint64_t sl = pk2(s.x, s.y), sr = pk2(s.z, s.w);
+            for (int jh = 0; jh < 2; ++jh) {
+              uint32_t rr[16];
+              tmem_ld_16x32(tr + 32 * jh, rr);
+              tmem_wait_ld();
+              if (jh == 1) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_cluster_local(map_to(smem_u32(&bars[B_SEMPTY + buf]), 0));
+              }
 #pragma unroll
-              for (int e = 4 * j; e < 4 * j + 4; e += 2) {
-                const float2 f = up2(fma2(sr, pk2(__uint_as_float(rr[e]), __uint_as_float(rr[e + 1])),
-                                          mul2(sl, pk2(__uint_as_float(u[e]), __uint_as_float(u[e + 1])))));
-                u[e] = __float_as_uint(f.x);
-                u[e + 1] = __float_as_uint(f.y);
+              for (int j4 = 0; j4 < 4; ++j4) {
+                const int j = 4 * jh + j4;
+                const float4 s = s4[4 * j];
+                const uint64_t sl = pk2(s.x, s.y), sr = pk2(s.z, s.w);
+#pragma unroll
+                for (int e = 0; e < 4; e += 2) {
+                  uint32_t* w2 = &u[4 * j + e];
+                  const float2 f = up2(fma2(sr, pk2(__uint_as_float(rr[4 * j4 + e]), __uint_as_float(rr[4 * j4 + e + 1])),
+                                            mul2(sl, pk2(__uint_as_float(w2[0]), __uint_as_float(w2[1])))));
+                  w2[0] = __float_as_uint(f.x);
+                  w2[1] = __float_as_uint(f.y);
+                }
               }
             }
           }
@@ -1107,15 +1120,14 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
               tc_fence_after();
               __syncwarp();
               const uint32_t col = tmem + lane_addr + h * 256 + part * 64;
-              uint32_t o[2][32];
+#pragma unroll 1
+              for (int s = 0; s < 64; s += 32) {
+                uint32_t o[32];
+                tmem_ld32(col + s, o);
+                tmem_wait_ld();
 #pragma unroll
-              for (int s = 0; s < 2; ++s) tmem_ld32(col + 32 * s, o[s]);
-              tmem_wait_ld();
-#pragma unroll
-              for (int s = 0; s < 2; ++s) {
-#pragma unroll
-                for (int v = 0; v < 32; ++v) o[s][v] = __float_as_uint(__uint_as_float(o[s][v]) * f);
-                tmem_st32(col + 32 * s, o[s]);
+                for (int v = 0; v < 32; ++v) o[v] = __float_as_uint(__uint_as_float(o[v]) * f);
+                tmem_st32(col + s, o);
               }
               __syncwarp();
               tmem_wait_st();
@@ -1142,51 +1154,49 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
         // shared memory, so that a warp's stores write whole sectors: eight rows each
         const bool whole = w.whole();
         const int64_t r0 = (int64_t)w.rt * ROWS + half_of * CROWS + q * 32;  // the warp's first row
-        const int64_t left = (int64_t)w.s.nq * a.H - r0;
+        const int64_t rows = (int64_t)w.s.nq * a.H - r0;
+        const int left = (int)(rows < 32 ? rows : 32) - (lane >> 2);         // rows from this lane's first on, by eights
         const uint32_t stage = smem_u32(sm + OFF_OP) + (warp - W_LANE) * 2048;
-        auto unit = [](int r, int u) -> uint32_t { return (uint32_t)(r * 64 + ((u ^ ((r >> 1) & 3)) << 4)); };
-        uint8_t* dst = whole ? reinterpret_cast<uint8_t*>(a.out + (w.s.q0 * a.H + r0) * DL)
-                             : reinterpret_cast<uint8_t*>(
-                                   ws.o + ((int64_t)(2 * k + (w.seg == 0 ? 0 : 1)) * ROWS + half_of * CROWS + q * 32) * DL);
+        const uint32_t put = stage + lane * 64, sw = (lane >> 1) & 3;        // this lane's row, its units turned by sw
+        const uint32_t take = stage + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
         const int row_bytes = whole ? DL * 2 : DL * 4;
+        uint8_t* dst = (whole ? reinterpret_cast<uint8_t*>(a.out + (w.s.q0 * a.H + r0) * DL)
+                              : reinterpret_cast<uint8_t*>(
+                                    ws.o + ((int64_t)(2 * k + (w.seg == 0 ? 0 : 1)) * ROWS + half_of * CROWS + q * 32) * DL)) +
+                       (lane >> 2) * row_bytes + (lane & 3) * 16;
         auto flush = [&](int byte) {
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int r = 8 * i + (lane >> 2);
-            const uint4 v = lds128(stage + unit(r, lane & 3));
-            if (r < left) *reinterpret_cast<uint4*>(dst + (int64_t)r * row_bytes + byte + (lane & 3) * 16) = v;
+            const uint4 v = lds128(take + i * 512);  // (eight rows on, the turn is the same)
+            if (8 * i < left) *reinterpret_cast<uint4*>(dst + 8 * i * row_bytes + byte) = v;
           }
           __syncwarp();
         };
 #pragma unroll 1
-        for (int s = 0; s < 4; ++s) {  // 32 columns at a time
-          const int col = (s >> 1) * 256 + part * 64 + (s & 1) * 32;
-          uint32_t v[32];
-          tmem_ld32(tmem + lane_addr + col, v);
+        for (int s = 0; s < 128; s += 16) {  // 16 columns at a time
+          const int col = (s >> 6) * 256 + part * 64 + (s & 63);
+          uint32_t v[16];
+          tmem_ld16(tmem + lane_addr + col, v);
           tmem_wait_ld();
           // (a factor of 0: nothing seen, or nothing that counts)
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = f == 0.f ? 0u : __float_as_uint(__uint_as_float(v[j]) * f);
+          for (int j = 0; j < 16; ++j) v[j] = f == 0.f ? 0u : __float_as_uint(__uint_as_float(v[j]) * f);
           if (whole) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
+            for (int j = 0; j < 8; ++j) {
               const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
               v[j] = *reinterpret_cast<const uint32_t*>(&b2);
             }
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-              sts128(stage + unit(lane, u), make_uint4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]));
-            flush(col * 2);
+            const uint32_t u0 = (s >> 3) & 2;  // the row's first or last two units
+            sts128(put + ((u0 ^ sw) << 4), make_uint4(v[0], v[1], v[2], v[3]));
+            sts128(put + (((u0 + 1) ^ sw) << 4), make_uint4(v[4], v[5], v[6], v[7]));
+            if (s & 16) flush((col - 16) * 2);
           } else {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-#pragma unroll
-              for (int u = 0; u < 4; ++u)
-                sts128(stage + unit(lane, u), make_uint4(v[16 * h + 4 * u], v[16 * h + 4 * u + 1],
-                                                         v[16 * h + 4 * u + 2], v[16 * h + 4 * u + 3]));
-              flush((col + 16 * h) * 4);
-            }
+            for (int u = 0; u < 4; ++u)
+              sts128(put + ((u ^ sw) << 4), make_uint4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]));
+            flush(col * 4);
           }
         }
         // the factor buffer's next phase, NRF segments on (its bytes come after the payloads of
@@ -1235,8 +1245,11 @@ __global__ void __launch_bounds__(256) join_kernel(const ChunkArgs a, const Work
   };
   int last = k;
   while (last + 1 < nc && ws.plan->e[last + 1].x < S + e.nt) ++last;
+  // (a cluster without units has no part)
+  auto none = [&](int j) { return ws.plan->e[j].x == (j + 1 < nc ? ws.plan->e[j + 1].x : ws.plan->units); };
   float M = -INFINITY;
-  for (int j = k - 1 + lane; j <= last; j += 32) M = fmaxf(M, ws.m[part(j)]);
+  for (int j = k - 1 + lane; j <= last; j += 32)
+    if (!none(j)) M = fmaxf(M, ws.m[part(j)]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   float L = 0.f;
@@ -1245,6 +1258,7 @@ __global__ void __launch_bounds__(256) join_kernel(const ChunkArgs a, const Work
   for (int c = 0; c < 4; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
   for (int j = k - 1; j <= last; ++j) {
+    if (none(j)) continue;
     const int64_t p = part(j);
     const float m = ws.m[p], l = ws.l[p];
     const float4* o = reinterpret_cast<const float4*>(ws.o + p * DL) + lane;
