@@ -541,21 +541,38 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
       // sLc made finite (a scale out of sight may be anything; its weight is 0 then, and in
       // sight the NaN or infinity shows in sRc), and log2 sLc
       bool ok = true;
-      for (int64_t i = 0; ok && i < w.left; ++i) {
-        const int g = (int)i, sc = g % NSC;
-        ok = wait(B_SCFULL + sc, (uint32_t)(g / NSC));
-        if (!ok) break;
-        float4* pl = reinterpret_cast<float4*>(sm + OFF_PL + sc * PL_BYTES);
-        float2* lg = reinterpret_cast<float2*>(pl + 64);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float4 s = reinterpret_cast<const float4*>(sm + OFF_SC + sc * 1024)[lane + 32 * h];
-          const float x = fminf(fmaxf(s.x, 0.f), 3.0e38f), y = fminf(fmaxf(s.z, 0.f), 3.0e38f);
-          pl[lane + 32 * h] = make_float4(x, y, fmaf(0.f, s.x, s.y), fmaf(0.f, s.z, s.w));
-          lg[lane + 32 * h] = make_float2(fmaxf(lg2_approx(x), LG_MIN), fmaxf(lg2_approx(y), LG_MIN));
+      for (; ok && w.more(); w.next(a)) {
+        // (and meanwhile the next row tile's queries come into L2)
+        Walk wn = w;
+        wn.next(a);
+        if (wn.more()) {
+          const int64_t r0 = (int64_t)wn.rt * ROWS + rank * CROWS, rows = (int64_t)wn.s.nq * a.H;
+          for (int r = lane; r < CROWS && r0 + r < rows; r += 32) {
+            const int64_t tok = wn.s.q0 + (uint32_t)(r0 + r) / (uint32_t)a.H, head = (uint32_t)(r0 + r) % (uint32_t)a.H;
+            prefetch_l2(a.q_lat + tok * a.ql_t + head * a.ql_h, DL * 2);
+            prefetch_l2(a.q_rope + tok * a.qr_t + head * a.qr_h, DR * 2);
+          }
+          __syncwarp();
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[B_PL + sc]);
+        for (int i = 0; i < w.n; ++i) {
+          const int g = gt + i, sc = g % NSC;
+          if (!wait(B_SCFULL + sc, (uint32_t)(g / NSC))) {
+            ok = false;
+            break;
+          }
+          float4* pl = reinterpret_cast<float4*>(sm + OFF_PL + sc * PL_BYTES);
+          float2* lg = reinterpret_cast<float2*>(pl + 64);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float4 s = reinterpret_cast<const float4*>(sm + OFF_SC + sc * 1024)[lane + 32 * h];
+            const float x = fminf(fmaxf(s.x, 0.f), 3.0e38f), y = fminf(fmaxf(s.z, 0.f), 3.0e38f);
+            pl[lane + 32 * h] = make_float4(x, y, fmaf(0.f, s.x, s.y), fmaf(0.f, s.z, s.w));
+            lg[lane + 32 * h] = make_float2(fmaxf(lg2_approx(x), LG_MIN), fmaxf(lg2_approx(y), LG_MIN));
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[B_PL + sc]);
+        }
+        gt += w.n;
       }
       if (!ok && lane == 0) fail();
       __syncwarp();
@@ -631,7 +648,6 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
       const int hl = part >> 1, sub = part & 1;  // rows 16 hl .. of the quarter; page of a tile
       const int i4 = lane & 3, r8 = lane >> 2;
       const int row0 = q * 32 + r8;           // the thread's rows: row0 + 8 p
-      const int mine = row0 + 8 * i4;         // the row this lane speaks for in exchanges
       const uint32_t lane_addr = (uint32_t)(q * 32) << 16;
       float* xmax = reinterpret_cast<float*>(sm + OFF_XMAX);
       float* xl = reinterpret_cast<float*>(sm + OFF_XL);
@@ -648,53 +664,51 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
         if (lane == 0) mbar_arrive(&bars[B_PX + q]);
         return wait(B_PX + q, px++);
       };
-      // the value of the four that belongs to row `mine`
-      auto own = [&](float v0, float v1, float v2, float v3) -> float {
-        const float a01 = (i4 & 1) ? v1 : v0, a23 = (i4 & 1) ? v3 : v2;
-        return (i4 & 2) ? a23 : a01;
-      };
       // The queries of a row tile: two e4m3 terms on the scale that puts a row's largest value
       // in [128, 256); c folds the scale back in, with sm_scale log2 e.
       auto load_query = [&](const Walk& x) -> bool {
-        const uint4 *pq[4], *pr[4];  // (null past the sequence's last row)
-        float top[4];                // a row's largest magnitude, as bf16 bits (ordered; 0x7F80 and up is inf or NaN)
-        auto get = [](const uint4* p, int j) { return p != nullptr ? __ldg(p + j) : make_uint4(0u, 0u, 0u, 0u); };
         const int64_t r0 = (int64_t)x.rt * ROWS + rank * CROWS, rows = (int64_t)x.s.nq * a.H;
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          const int64_t r = r0 + row0 + 8 * p;
-          const int64_t tok = x.s.q0 + (int64_t)((uint32_t)r / (uint32_t)a.H), head = (uint32_t)r % (uint32_t)a.H;
-          pq[p] = r < rows ? reinterpret_cast<const uint4*>(a.q_lat + tok * a.ql_t + head * a.ql_h + part * 128) + i4 : nullptr;
-          pr[p] = r < rows && i4 < 2
-                      ? reinterpret_cast<const uint4*>(a.q_rope + tok * a.qr_t + head * a.qr_h + part * 16) + i4
-                      : nullptr;
-        }
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          uint32_t t2 = 0;
-#pragma unroll
-          for (int j = 0; j < 5; ++j) {
-            const uint4 v = j < 4 ? get(pq[p], 4 * j) : get(pr[p], 0);
-            t2 = __vmaxu2(t2, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
-                                       __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
-          }
-          t2 = __vmaxu2(t2, __shfl_xor_sync(0xffffffffu, t2, 1));
-          t2 = __vmaxu2(t2, __shfl_xor_sync(0xffffffffu, t2, 2));
-          top[p] = __uint_as_float((t2 & 0xFFFFu) > (t2 >> 16) ? (t2 & 0xFFFFu) : (t2 >> 16));
-        }
-        xq[mine * 4 + part] = __float_as_uint(own(top[0], top[1], top[2], top[3]));
+        const uint32_t qlo = smem_u32(sm + OFF_QL) + part * OP_ATOM, qrp = smem_u32(sm + OFF_QR);
         if (part == 0) {  // the keys that row q * 32 + lane sees (rows past the last one: as many as that)
           const int tok = (int)((uint32_t)(r0 + q * 32 + lane) / (uint32_t)a.H);
           lims[(x.seg & 1) * CROWS + q * 32 + lane] = limit_of(a, x.s, tok < x.s.nq ? tok : x.s.nq - 1);
         }
-        if (!quarter_sync()) return false;
-        const uint32_t qlo = smem_u32(sm + OFF_QL) + part * OP_ATOM, qrp = smem_u32(sm + OFF_QR);
+#pragma unroll 1
+        for (int hl = 0; hl < 2; ++hl) {  // two of the thread's rows: their channels all in flight at once
+          uint4 v[2][5];
+          uint32_t top[2];                // a row's largest magnitude, as bf16 bits (ordered; 0x7F80 and up is inf or NaN)
 #pragma unroll
-        for (int hl = 0; hl < 2; ++hl) {  // (read again: all four rows' values at once would spill)
+          for (int p = 0; p < 2; ++p) {
+            const int64_t r = r0 + row0 + 16 * hl + 8 * p;
+            const uint32_t at = (uint32_t)(r < rows ? r : rows - 1);
+            const int64_t tok = x.s.q0 + at / (uint32_t)a.H, head = at % (uint32_t)a.H;
+            const uint4* pq = reinterpret_cast<const uint4*>(a.q_lat + tok * a.ql_t + head * a.ql_h + part * 128) + i4;
+            const uint4* pr = reinterpret_cast<const uint4*>(a.q_rope + tok * a.qr_t + head * a.qr_h + part * 16) + (i4 & 1);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[p][j] = __ldg(pq + 4 * j);
+            v[p][4] = __ldg(pr);
+            if (r >= rows) {  // past the last row: zeros
+#pragma unroll
+              for (int j = 0; j < 5; ++j) v[p][j] = make_uint4(0u, 0u, 0u, 0u);
+            }
+          }
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            uint32_t t2 = 0;
+#pragma unroll
+            for (int j = 0; j < 5; ++j)
+              t2 = __vmaxu2(t2, __vmaxu2(__vmaxu2(v[p][j].x & 0x7FFF7FFFu, v[p][j].y & 0x7FFF7FFFu),
+                                         __vmaxu2(v[p][j].z & 0x7FFF7FFFu, v[p][j].w & 0x7FFF7FFFu)));
+            t2 = __vmaxu2(t2, __shfl_xor_sync(0xffffffffu, t2, 1));
+            t2 = __vmaxu2(t2, __shfl_xor_sync(0xffffffffu, t2, 2));
+            top[p] = (t2 & 0xFFFFu) > (t2 >> 16) ? (t2 & 0xFFFFu) : (t2 >> 16);
+          }
+          if (i4 < 2) xq[(row0 + 16 * hl + 8 * i4) * 4 + part] = i4 ? top[1] : top[0];
+          if (!quarter_sync()) return false;
           uint32_t hw[16];
 #pragma unroll
-          for (int p2 = 0; p2 < 2; ++p2) {
-            const int p = 2 * hl + p2, row = row0 + 8 * p;
+          for (int p = 0; p < 2; ++p) {
+            const int row = row0 + 16 * hl + 8 * p;
             const uint4 m4 = reinterpret_cast<const uint4*>(xq)[row];
             uint32_t mx = m4.x > m4.y ? m4.x : m4.y;
             mx = m4.z > mx ? m4.z : mx;
@@ -713,19 +727,16 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
               split4(f4, hi, lo);
               if (nan) hi = 0x7F7F7F7Fu;
             };
+            uint2 hi, lo;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {  // channels 32 j + 8 i4 .. + 7 of the part
-              const uint4 v = get(pq[p], 4 * j);
-              uint2 lo;
-              terms(v.x, v.y, hw[4 * j + 2 * p2], lo.x);
-              terms(v.z, v.w, hw[4 * j + 2 * p2 + 1], lo.y);
+              terms(v[p][j].x, v[p][j].y, hw[4 * j + 2 * p], lo.x);
+              terms(v[p][j].z, v[p][j].w, hw[4 * j + 2 * p + 1], lo.y);
               sts64(qlo + sw128(row, 2 * j + (i4 >> 1)) + (i4 & 1) * 8, lo);
             }
+            terms(v[p][4].x, v[p][4].y, hi.x, lo.x);
+            terms(v[p][4].z, v[p][4].w, hi.y, lo.y);
             if (i4 < 2) {
-              const uint4 v = get(pr[p], 0);
-              uint2 hi, lo;
-              terms(v.x, v.y, hi.x, lo.x);
-              terms(v.z, v.w, hi.y, lo.y);
               sts64(qrp + sw128(row, part) + i4 * 8, hi);
               sts64(qrp + sw128(row, 4 + part) + i4 * 8, lo);
             }
