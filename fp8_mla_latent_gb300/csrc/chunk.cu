@@ -80,8 +80,9 @@ constexpr int VTILE = 2 * VBLK;              // a context CTA's half of the chan
 constexpr int NVT = 2;                       // V ring, in tiles
 constexpr int SUB = 64;                      // tokens of a softmax warp's share of a tile (a page)
 constexpr int OP_ATOM = CROWS * 128;         // 16 KB: [128 rows x 128 tokens], e4m3
-constexpr int P_F = CROWS * TILE * 2;        // payload: g' f16 (256 bytes a row), then rescale factors
-constexpr int P_BYTES = P_F + CROWS * 4;
+constexpr int P_F = CROWS * TILE * 2;        // payload: g' f16 (256 bytes a row), then rescale factors,
+constexpr int P_PAGES = P_F + CROWS * 4;     // then the pages present
+constexpr int P_BYTES = P_PAGES + 4;
 constexpr int P_STRIDE = 33 * 1024;
 constexpr float TAU = 1.0f;
 constexpr float P_LOG = 7.0f;                // g' <= 2^(TAU + P_LOG) = 256 <= 448
@@ -97,8 +98,8 @@ constexpr float LN2 = 0.6931471805599453f;
 constexpr int B_KFULL = 0;                   // [2 NK] rank 0: both CTAs' halves of a K half tile loaded
 constexpr int B_KEMPTY = B_KFULL + 2 * NK;   // [2 NK] ranks 0, 1: consumed
 constexpr int B_SCFULL = B_KEMPTY + 2 * NK;  // [NSC] score: row scales of a tile loaded
-constexpr int B_PL = B_SCFULL + NSC;         // [NSC] score: a tile's scales prepared
-constexpr int B_SFULL = B_PL + NSC;      // [2] ranks 0, 1: S of a tile in TMEM
+constexpr int B_SFULL = B_SCFULL + NSC;      // [2] score: S of a tile in TMEM (commit); its scales prepared, and
+                                             // its payload buffer free (the scale warp)
 constexpr int B_SEMPTY = B_SFULL + 2;        // [2] rank 0: S read (16 warps x 2 CTAs)
 constexpr int B_QREADY = B_SEMPTY + 2;       // rank 0: the row tile's query in place (16 warps x 2)
 constexpr int B_PX = B_QREADY + 1;           // [4] score: the four warps of a lane quarter meet
@@ -108,16 +109,17 @@ constexpr int B_PFULL = B_PFREE + 2;         // [2] context: payload arrived
 constexpr int B_VT = B_PFULL + 2;            // [NVT] context: V tile loaded
 constexpr int B_VEMPTY = B_VT + NVT;         // [NVT] ranks 2, 3: consumed
 constexpr int B_EP = B_VEMPTY + NVT;         // context: a row tile's results have left shared memory
-constexpr int B_RS = B_EP + 1;              // [2] rank 2: operand, V and O half ready (16 warps x 2)
-constexpr int B_ODONE = B_RS + 2;            // [2] ranks 2, 3: MMAs of an O half done
+constexpr int B_VR = B_EP + 1;               // [NVT] rank 2: rank 3's V tile loaded
+constexpr int B_RS = B_VR + NVT;             // [2 buffers][2] rank 2: operand, and O half ready (16 warps x 2)
+constexpr int B_ODONE = B_RS + 4;            // [2 buffers][2] ranks 2, 3: a tile's MMAs of an O half done
 constexpr int NRF = 4;
-constexpr int B_RF = B_ODONE + 2;            // [NRF] context: row factors of a finished row tile arrived
+constexpr int B_RF = B_ODONE + 4;            // [NRF] context: row factors of a finished row tile arrived
 constexpr int B_DRAIN = B_RF + NRF;          // every MMA done
 constexpr int NBAR = B_DRAIN + 1;
 
 // shared memory (dynamic, 1024-byte aligned)
 constexpr int OFF_FLAGS = 512;               // tmem base, abort flag
-constexpr int OFF_FACTS = OFF_FLAGS + 16;    // [8] pages present in the tiles of a ring
+constexpr int OFF_FACTS = OFF_FLAGS + 16;    // [8] score: pages present in the tiles of the ring
 constexpr int OFF_XMAX = 1024;               // score: [2][128 rows][2 pages] a tile's largest weights
 constexpr int OFF_XL = OFF_XMAX + 2048;      // score: [128 rows][2 pages] l
 constexpr int OFF_XQ = OFF_XL + 1024;        // score: [128 rows][4 parts] query maxima
@@ -452,7 +454,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
     for (int i = 0; i < 4; ++i) mbar_init(&bars[B_PX + i], N_LANE_WARPS / 4);
     mbar_init(&bars[B_EP], N_LANE_WARPS);
     for (int i = 0; i < 2; ++i) mbar_init(&bars[B_PFREE + i], N_LANE_WARPS);
-    for (int i = 0; i < 2; ++i) mbar_init(&bars[B_RS + i], 2 * N_LANE_WARPS);
+    for (int i = 0; i < 4; ++i) mbar_init(&bars[B_RS + i], 2 * N_LANE_WARPS);
+    for (int i = 0; i < 2; ++i) mbar_init(&bars[B_SFULL + i], 2);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     if (rank >= 2) {  // what the context CTAs expect first
@@ -569,8 +572,14 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
             pl[lane + 32 * h] = make_float4(x, y, fmaf(0.f, s.x, s.y), fmaf(0.f, s.z, s.w));
             lg[lane + 32 * h] = make_float2(fmaxf(lg2_approx(x), LG_MIN), fmaxf(lg2_approx(y), LG_MIN));
           }
+          // (the payload buffer of tile g: the context warps have read tile g - 2, and so the softmax
+          // warps were through with its S)
+          if (g >= 2 && !wait(B_PFREE + (g & 1), (uint32_t)((g >> 1) - 1))) {
+            ok = false;
+            break;
+          }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bars[B_PL + sc]);
+          if (lane == 0) mbar_arrive(&bars[B_SFULL + (g & 1)]);
         }
         gt += w.n;
       }
@@ -796,7 +805,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
 #pragma unroll 1
           for (; i < end; ++i, t0 += TILE) {
             const int g = gt + i, buf = g & 1, sc = g % NSC;
-            if (!wait(B_PL + sc, (uint32_t)(g / NSC)) || !wait(B_SFULL + buf, (uint32_t)(g >> 1))) {
+            if (!wait(B_SFULL + buf, (uint32_t)(g >> 1))) {
               ok = false;
               break;
             }
@@ -892,13 +901,10 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
 #pragma unroll
               for (int p = 0; p < 2; ++p) l[p] *= __shfl_sync(0xffffffffu, f, (lane & 28) + p);
             }
-            if (g >= 2 && !wait(B_PFREE + buf, (uint32_t)((g >> 1) - 1))) {
-              ok = false;
-              break;
-            }
             const uint32_t to = map_to(smem_u32(sm + OFF_P + buf * P_STRIDE), rank + 2);
             const uint32_t bar = map_to(smem_u32(&bars[B_PFULL + buf]), rank + 2);
             if (sub == 0 && i4 < 2) st_async_b32(to + P_F + mh * 4, __float_as_uint(f), bar);
+            if (warp == W_LANE && lane == 0) st_async_b32(to + P_PAGES, facts[sc], bar);
             // p = 2^(c u - M_g + 7) (nothing in sight so far: u is -inf, and p 0)
             const float mneg = P_LOG - fmaxf(mn, -3.0e38f);
             uint64_t m2[2], ls2[2];
@@ -1002,7 +1008,6 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
             ok = false;
             break;
           }
-          facts[vs] = (s0 >= 0 ? 1u : 0u) | (s1 >= 0 ? 2u : 0u);
           mbar_arrive_expect_tx_warp(&bars[B_VT + vs], 2u * BLK * ((s0 >= 0 ? 1u : 0u) + (s1 >= 0 ? 1u : 0u)));
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {
@@ -1034,9 +1039,13 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
           for (int i = 0; ok && i < w.n; ++i) {
             const int g = gt + i;
             const uint64_t ad = pd + (uint64_t)((g & 1) * 2 * OP_ATOM >> 4);
+            if (!wait(B_VT + g % NVT, (uint32_t)(g / NVT)) || !wait_cluster(B_VR + g % NVT, (uint32_t)(g / NVT))) {
+              ok = false;
+              break;
+            }
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
-              if (!wait_cluster(B_RS + h, (uint32_t)g)) {
+              if (!wait_cluster(B_RS + 2 * (g & 1) + h, (uint32_t)(g >> 1))) {
                 ok = false;
                 break;
               }
@@ -1048,7 +1057,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
                 mma_f8_pair_warp(tmem + h * 256, ad + 2 * kk, bd + 256 * kk, id, (i > 0 || kk > 0) ? 1u : 0u);
                 mma_f8_pair_warp(tmem + h * 256, ad + (OP_ATOM >> 4) + 2 * kk, bd + 256 * kk, id, 1u);
               }
-              mma_commit_pair_warp(&bars[B_ODONE + h], 0xC);
+              mma_commit_pair_warp(&bars[B_ODONE + 2 * (g & 1) + h], 0xC);
             }
             if (!ok) break;
             mma_commit_pair_warp(&bars[B_VEMPTY + g % NVT], 0xC);
@@ -1057,6 +1066,16 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
         }
         if (!ok && lane == 0) fail();
         mma_commit_pair_warp(&bars[B_DRAIN], 0xC);
+      } else {
+        // rank 3 tells the MMA's issuer of its V tiles
+        const uint32_t vr = map_to(smem_u32(&bars[B_VR]), 2);
+        bool ok = true;
+        for (int64_t g = 0; ok && g < w.left; ++g) {
+          ok = wait(B_VT + (int)(g % NVT), (uint32_t)(g / NVT));
+          if (ok && lane == 0) arrive_cluster_local(vr + (int)(g % NVT) * 8);
+          __syncwarp();
+        }
+        if (!ok && lane == 0) fail();
       }
       const int zero = 0;
       (void)mbar_wait(&bars[B_DRAIN], 0, &zero, 4 * WAIT_NS);
@@ -1089,6 +1108,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
             pv[u][3] = v.w;
           }
           const float f = reinterpret_cast<const float*>(sm + OFF_P + pb * P_STRIDE + P_F)[hh];
+          const uint32_t pages = *reinterpret_cast<const uint32_t*>(sm + OFF_P + pb * P_STRIDE + P_PAGES);
           const bool any = __any_sync(0xffffffffu, f != 1.f) && i > 0;
           // the payload is read: the next one may be expected, and then come
           __syncwarp();
@@ -1096,7 +1116,12 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
             if (warp == W_LANE) mbar_arrive_expect_tx(&bars[B_PFULL + pb], P_BYTES);
             arrive_cluster_local(pfree + pb * 8);
           }
-          // the operand buffer was read by the MMAs of tile g - 2, waited for with tile g - 1
+          // the operand buffer was read by the MMAs of tile g - 2 (at a row tile's start they were
+          // waited for with its predecessor's results)
+          if (i > 1 && !wait(B_ODONE + 2 * pb + 1, (uint32_t)((g >> 1) - 1))) {
+            ok = false;
+            break;
+          }
           const uint32_t opnd = smem_u32(sm + OFF_OP) + pb * 2 * OP_ATOM;
 #pragma unroll
           for (int j = 0; j < 2; ++j) {  // 16 tokens per 16-byte unit
@@ -1113,12 +1138,12 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
             sts128(opnd + off, make_uint4(hw[0], hw[1], hw[2], hw[3]));
             sts128(opnd + OP_ATOM + off, make_uint4(lw[0], lw[1], lw[2], lw[3]));
           }
-          if (!wait(B_VT + vs, (uint32_t)(g / NVT))) {
-            ok = false;
-            break;
-          }
-          if ((w.t + i + 1) * TILE > lim0 || facts[vs] != 3u) {
+          if ((w.t + i + 1) * TILE > lim0 || pages != 3u) {
             // some row does not see all of this tile: no NaN code may stay in it
+            if (!wait(B_VT + vs, (uint32_t)(g / NVT))) {
+              ok = false;
+              break;
+            }
             const uint32_t vb = vring + vs * VTILE + (warp - W_LANE) * 2048 + lane * 16;
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
@@ -1127,15 +1152,15 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
             }
           }
           fence_proxy_async_smem();
-          // each O half: the previous tile's MMAs on it are done (at a row tile's start the
-          // results were read after them), then the rows whose reference moved are rescaled
+          // rows whose reference moved are rescaled: one half of O after the other, each when the
+          // previous tile's MMAs on it are done (the first half while those on the second run)
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {
-            if (i > 0 && !wait(B_ODONE + h, (uint32_t)(g - 1))) {
-              ok = false;
-              break;
-            }
             if (any) {
+              if (!wait(B_ODONE + 2 * (pb ^ 1) + h, (uint32_t)((g - 1) >> 1))) {
+                ok = false;
+                break;
+              }
               tc_fence_after();
               __syncwarp();
               const uint32_t col = tmem + lane_addr + h * 256 + part * 64;
@@ -1150,10 +1175,10 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
               }
               __syncwarp();
               tmem_wait_st();
+              tc_fence_before();
+              __syncwarp();
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) arrive_cluster_local(rs + h * 8);
+            if (lane == 0) arrive_cluster_local(rs + (2 * pb + h) * 8);
           }
           if (!ok) break;
         }
@@ -1161,7 +1186,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
         const int last = gt + w.n - 1;
         gt += w.n;
         const int rf = w.seg % NRF;
-        if (!wait(B_ODONE, (uint32_t)last) || !wait(B_ODONE + 1, (uint32_t)last) ||
+        if (!wait(B_ODONE + 2 * (last & 1) + 1, (uint32_t)(last >> 1)) ||
             !wait_cluster(B_RF + rf, (uint32_t)(w.seg / NRF))) {
           ok = false;
           break;
