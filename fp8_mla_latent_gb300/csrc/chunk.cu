@@ -69,7 +69,7 @@ constexpr int N_LANE_WARPS = 16;             // four per TMEM lane quarter, and 
 constexpr int NTHREADS = (W_LANE + N_LANE_WARPS) * 32;
 constexpr int MAX_CLUSTERS = NUM_SMS / 4;
 constexpr int MIN_TILES = 2;                 // key tiles that are worth a cluster of their own
-constexpr int SWITCH = 2;                    // what beginning a row tile costs, in key tiles
+constexpr int SWITCH = 6;                    // what beginning a row tile costs, in key tiles
 constexpr int BLK = PAGE * 128;              // 8 KB: [64 tokens x 128 bytes]
 constexpr int RBLK = PAGE * DR;              // 4 KB: [64 tokens x 64 bytes]
 constexpr int KTILE = 4 * BLK + RBLK;        // a score CTA's page of a tile: 36 KB
@@ -791,157 +791,145 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
         }
         int t0 = x.t * TILE + sub * SUB;
         const int first = lim[q * 32 + 16 * hl];  // the keys that the first of the rows sees
-        // (all tiles but the last, then that one, once the next query is on its way: the tile loop
-        // has no registers to spare for the query's)
-        int i = 0;
 #pragma unroll 1
-        for (int end = n_tiles - 1; ok && end <= n_tiles; ++end) {
-          if (end == n_tiles && more) {
-            ok = wait(B_SFULL + ((gt + i) & 1), (uint32_t)((gt + i) >> 1));
-            tc_fence_after();
-            ok = ok && load_query(walks[cur ^ 1]);
-            if (!ok) break;
+        for (int i = 0; i < n_tiles; ++i, t0 += TILE) {
+          const int g = gt + i, buf = g & 1, sc = g % NSC;
+          if (!wait(B_SFULL + buf, (uint32_t)(g >> 1))) {
+            ok = false;
+            break;
           }
-#pragma unroll 1
-          for (; i < end; ++i, t0 += TILE) {
-            const int g = gt + i, buf = g & 1, sc = g % NSC;
-            if (!wait(B_SFULL + buf, (uint32_t)(g >> 1))) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const float4* s4 = reinterpret_cast<const float4*>(sm + OFF_PL + sc * PL_BYTES) + sub * 32 + i4;
-            const float2* g2 = reinterpret_cast<const float2*>(sm + OFF_PL + sc * PL_BYTES + 1024) + sub * 32 + i4;
-            const bool here = (facts[sc] >> sub) & 1u;
-            uint32_t u[32];    // S_L, then u = sLc S_L + sRc S_R, as pairs of tokens
-            {
-              const uint32_t tl = tmem + lane_addr + ((uint32_t)(16 * hl) << 16) + T_SL + buf * TILE + sub * SUB;
-              const uint32_t tr = tmem + lane_addr + ((uint32_t)(16 * hl) << 16) + T_SR + sub * SUB;
-              tmem_ld_16x32(tl, u);
-              tmem_ld_16x32(tl + 32, u + 16);
-#pragma unroll
-              for (int jh = 0; jh < 2; ++jh) {
-                uint32_t rr[16];
-                tmem_ld_16x32(tr + 32 * jh, rr);
-                tmem_wait_ld();
-                if (jh == 1) {
-                  tc_fence_before();
-                  __syncwarp();
-                  if (lane == 0) arrive_cluster_local(map_to(smem_u32(&bars[B_SEMPTY + buf]), 0));
-                }
-#pragma unroll
-                for (int j4 = 0; j4 < 4; ++j4) {
-                  const int j = 4 * jh + j4;
-                  const float4 s = s4[4 * j];
-                  const uint64_t sl = pk2(s.x, s.y), sr = pk2(s.z, s.w);
-#pragma unroll
-                  for (int e = 0; e < 4; e += 2) {
-                    uint32_t* w2 = &u[4 * j + e];
-                    const float2 f = up2(fma2(sr, pk2(__uint_as_float(rr[4 * j4 + e]), __uint_as_float(rr[4 * j4 + e + 1])),
-                                              mul2(sl, pk2(__uint_as_float(w2[0]), __uint_as_float(w2[1])))));
-                    w2[0] = __float_as_uint(f.x);
-                    w2[1] = __float_as_uint(f.y);
-                  }
-                }
-              }
-            }
-            auto pair = [&](int p, int j) -> uint64_t {
-              return pk2(__uint_as_float(u[4 * j + 2 * p]), __uint_as_float(u[4 * j + 2 * p + 1]));
-            };
-            if (!here || first - t0 < SUB) {  // some row does not see all of this page
-#pragma unroll
-              for (int p = 0; p < 2; ++p) {
-                const int n = here ? lim[rh + 8 * p] - t0 - 2 * i4 : 0;
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-#pragma unroll
-                  for (int e = 0; e < 2; ++e)
-                    if (8 * j + e >= n) u[4 * j + 2 * p + e] = 0xFF800000u;  // -inf
-              }
-            }
-            // the largest weight of row `mh` over the tile: the two rows' over this thread's
-            // tokens, then over the four lanes, then over the two pages
-            float y[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float2 f = g2[4 * j];
-              const uint64_t lg = pk2(f.x, f.y);
-#pragma unroll
-              for (int p = 0; p < 2; ++p) {
-                const float2 v = up2(fma2(c2[p], pair(p, j), lg));
-                y[p] = max3(y[p], v.x, v.y);
-              }
-            }
-            const bool b0 = i4 & 1;
-            float ym = fmaxf(b0 ? y[1] : y[0], __shfl_xor_sync(0xffffffffu, b0 ? y[0] : y[1], 1));
-            ym = fmaxf(ym, __shfl_xor_sync(0xffffffffu, ym, 2));
-            float* xm = xmax + (buf * CROWS + mh) * 2;
-            xm[sub] = ym;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[B_EX + q * 2 + hl]);
-            if (!wait(B_EX + q * 2 + hl, (uint32_t)g)) {
-              ok = false;
-              break;
-            }
-            // its reference, and the factor of what was added up before (of l, and of O)
-            float mn = mg;
-            {
-              const float2 v2 = *reinterpret_cast<const float2*>(xm);
-              ym = fmaxf(v2.x, v2.y);
-              if (ym > mg + TAU) {
-                mn = ym;
-              } else if (ym < mg - DOWN && mg - ym + lift <= DOWN_CAP) {
-                lift += mg - ym;
-                mn = ym;
-              }
-            }
-            const float f = mn == mg ? 1.f : (mg > -INFINITY ? ex2_approx(mg - mn) : 0.f);
-            mg = mn;
-            if (__any_sync(0xffffffffu, f != 1.f)) {
-#pragma unroll
-              for (int p = 0; p < 2; ++p) l[p] *= __shfl_sync(0xffffffffu, f, (lane & 28) + p);
-            }
-            const uint32_t to = map_to(smem_u32(sm + OFF_P + buf * P_STRIDE), rank + 2);
-            const uint32_t bar = map_to(smem_u32(&bars[B_PFULL + buf]), rank + 2);
-            if (sub == 0 && i4 < 2) st_async_b32(to + P_F + mh * 4, __float_as_uint(f), bar);
-            if (warp == W_LANE && lane == 0) st_async_b32(to + P_PAGES, facts[sc], bar);
-            // p = 2^(c u - M_g + 7) (nothing in sight so far: u is -inf, and p 0)
-            const float mneg = P_LOG - fmaxf(mn, -3.0e38f);
-            uint64_t m2[2], ls2[2];
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-              const float mp = __shfl_sync(0xffffffffu, mneg, (lane & 28) + p);
-              m2[p] = pk2(mp, mp);
-              ls2[p] = pk2(0.f, 0.f);
-            }
-            const uint32_t dst = to + prow(rh, sub * 8 + i4);
+          tc_fence_after();
+          const float4* s4 = reinterpret_cast<const float4*>(sm + OFF_PL + sc * PL_BYTES) + sub * 32 + i4;
+          const float2* g2 = reinterpret_cast<const float2*>(sm + OFF_PL + sc * PL_BYTES + 1024) + sub * 32 + i4;
+          const bool here = (facts[sc] >> sub) & 1u;
+          uint32_t u[32];    // S_L, then u = sLc S_L + sRc S_R, as pairs of tokens
+          {
+            const uint32_t tl = tmem + lane_addr + ((uint32_t)(16 * hl) << 16) + T_SL + buf * TILE + sub * SUB;
+            const uint32_t tr = tmem + lane_addr + ((uint32_t)(16 * hl) << 16) + T_SR + sub * SUB;
+            tmem_ld_16x32(tl, u);
+            tmem_ld_16x32(tl + 32, u + 16);
 #pragma unroll
             for (int jh = 0; jh < 2; ++jh) {
-              uint32_t h[2][4];
+              uint32_t rr[16];
+              tmem_ld_16x32(tr + 32 * jh, rr);
+              tmem_wait_ld();
+              if (jh == 1) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_cluster_local(map_to(smem_u32(&bars[B_SEMPTY + buf]), 0));
+              }
 #pragma unroll
               for (int j4 = 0; j4 < 4; ++j4) {
                 const int j = 4 * jh + j4;
-                const float2 s = *reinterpret_cast<const float2*>(s4 + 4 * j);
+                const float4 s = s4[4 * j];
+                const uint64_t sl = pk2(s.x, s.y), sr = pk2(s.z, s.w);
 #pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                  const float2 z = up2(fma2(c2[p], pair(p, j), m2[p]));
-                  const uint64_t e = pk2(ex2_approx(z.x), ex2_approx(z.y));
-                  ls2[p] = add2(ls2[p], e);
-                  const float2 t2 = up2(mul2(e, pk2(s.x, s.y)));
-                  const __half2 h2 = __floats2half2_rn(t2.x, t2.y);
-                  h[p][j4] = *reinterpret_cast<const uint32_t*>(&h2);
+                for (int e = 0; e < 4; e += 2) {
+                  uint32_t* w2 = &u[4 * j + e];
+                  const float2 f = up2(fma2(sr, pk2(__uint_as_float(rr[4 * j4 + e]), __uint_as_float(rr[4 * j4 + e + 1])),
+                                            mul2(sl, pk2(__uint_as_float(w2[0]), __uint_as_float(w2[1])))));
+                  w2[0] = __float_as_uint(f.x);
+                  w2[1] = __float_as_uint(f.y);
                 }
               }
-              // (unit sub * 8 + 4 jh + i4 of row rh + 8 p: 4 jh turns bit 2 of the swizzled unit)
-#pragma unroll
-              for (int p = 0; p < 2; ++p)
-                st_async_v4((dst ^ (uint32_t)(jh * 64)) + p * 2048, make_uint4(h[p][0], h[p][1], h[p][2], h[p][3]), bar);
             }
+          }
+          auto pair = [&](int p, int j) -> uint64_t {
+            return pk2(__uint_as_float(u[4 * j + 2 * p]), __uint_as_float(u[4 * j + 2 * p + 1]));
+          };
+          if (!here || first - t0 < SUB) {  // some row does not see all of this page
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-              const float2 s = up2(ls2[p]);
-              l[p] += s.x + s.y;
+              const int n = here ? lim[rh + 8 * p] - t0 - 2 * i4 : 0;
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  if (8 * j + e >= n) u[4 * j + 2 * p + e] = 0xFF800000u;  // -inf
             }
+          }
+          // the largest weight of row `mh` over the tile: the two rows' over this thread's
+          // tokens, then over the four lanes, then over the two pages
+          float y[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float2 f = g2[4 * j];
+            const uint64_t lg = pk2(f.x, f.y);
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+              const float2 v = up2(fma2(c2[p], pair(p, j), lg));
+              y[p] = max3(y[p], v.x, v.y);
+            }
+          }
+          const bool b0 = i4 & 1;
+          float ym = fmaxf(b0 ? y[1] : y[0], __shfl_xor_sync(0xffffffffu, b0 ? y[0] : y[1], 1));
+          ym = fmaxf(ym, __shfl_xor_sync(0xffffffffu, ym, 2));
+          float* xm = xmax + (buf * CROWS + mh) * 2;
+          xm[sub] = ym;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[B_EX + q * 2 + hl]);
+          if (!wait(B_EX + q * 2 + hl, (uint32_t)g)) {
+            ok = false;
+            break;
+          }
+          // its reference, and the factor of what was added up before (of l, and of O)
+          float mn = mg;
+          {
+            const float2 v2 = *reinterpret_cast<const float2*>(xm);
+            ym = fmaxf(v2.x, v2.y);
+            if (ym > mg + TAU) {
+              mn = ym;
+            } else if (ym < mg - DOWN && mg - ym + lift <= DOWN_CAP) {
+              lift += mg - ym;
+              mn = ym;
+            }
+          }
+          const float f = mn == mg ? 1.f : (mg > -INFINITY ? ex2_approx(mg - mn) : 0.f);
+          mg = mn;
+          if (__any_sync(0xffffffffu, f != 1.f)) {
+#pragma unroll
+            for (int p = 0; p < 2; ++p) l[p] *= __shfl_sync(0xffffffffu, f, (lane & 28) + p);
+          }
+          const uint32_t to = map_to(smem_u32(sm + OFF_P + buf * P_STRIDE), rank + 2);
+          const uint32_t bar = map_to(smem_u32(&bars[B_PFULL + buf]), rank + 2);
+          if (sub == 0 && i4 < 2) st_async_b32(to + P_F + mh * 4, __float_as_uint(f), bar);
+          if (warp == W_LANE && lane == 0) st_async_b32(to + P_PAGES, facts[sc], bar);
+          // p = 2^(c u - M_g + 7) (nothing in sight so far: u is -inf, and p 0)
+          const float mneg = P_LOG - fmaxf(mn, -3.0e38f);
+          uint64_t m2[2], ls2[2];
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            const float mp = __shfl_sync(0xffffffffu, mneg, (lane & 28) + p);
+            m2[p] = pk2(mp, mp);
+            ls2[p] = pk2(0.f, 0.f);
+          }
+          const uint32_t dst = to + prow(rh, sub * 8 + i4);
+#pragma unroll
+          for (int jh = 0; jh < 2; ++jh) {
+            uint32_t h[2][4];
+#pragma unroll
+            for (int j4 = 0; j4 < 4; ++j4) {
+              const int j = 4 * jh + j4;
+              const float2 s = *reinterpret_cast<const float2*>(s4 + 4 * j);
+#pragma unroll
+              for (int p = 0; p < 2; ++p) {
+                const float2 z = up2(fma2(c2[p], pair(p, j), m2[p]));
+                const uint64_t e = pk2(ex2_approx(z.x), ex2_approx(z.y));
+                ls2[p] = add2(ls2[p], e);
+                const float2 t2 = up2(mul2(e, pk2(s.x, s.y)));
+                const __half2 h2 = __floats2half2_rn(t2.x, t2.y);
+                h[p][j4] = *reinterpret_cast<const uint32_t*>(&h2);
+              }
+            }
+            // (unit sub * 8 + 4 jh + i4 of row rh + 8 p: 4 jh turns bit 2 of the swizzled unit)
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+              st_async_v4((dst ^ (uint32_t)(jh * 64)) + p * 2048, make_uint4(h[p][0], h[p][1], h[p][2], h[p][3]), bar);
+          }
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            const float2 s = up2(ls2[p]);
+            l[p] += s.x + s.y;
           }
         }
         if (!ok) break;
@@ -979,6 +967,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
                        map_to(smem_u32(&bars[B_RF + rf]), rank + 2));
         }
         gt += n_tiles;
+        if (more) ok = load_query(walks[cur ^ 1]) && quarter_sync();
       }
       if (!ok && lane == 0) fail();
       // the context CTAs' last arrivals at this CTA have landed
