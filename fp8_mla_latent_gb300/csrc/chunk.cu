@@ -219,11 +219,15 @@ __device__ __forceinline__ int64_t plan_sum(int64_t v, int64_t* tmp, int64_t* to
   return v;
 }
 
-// One CTA: row tiles before each sequence (base), the units of every row tile,
+constexpr int PLAN_NEAR = 4096;
+
+// One CTA: row tiles before each sequence (base, in shared memory if they fit), the units of every row tile,
 // their total, and the row tile that each cluster's range starts in.
 __global__ void __launch_bounds__(1024) plan_kernel(const ChunkArgs a, Plan* plan, int64_t* base, int clusters) {
   grid_dependents_launch();
   __shared__ int64_t tmp[32];
+  __shared__ int64_t near[PLAN_NEAR];
+  if (a.B < PLAN_NEAR) base = near;
   if (threadIdx.x == 0) *a.err = 0;
   __syncthreads();
   int64_t pairs = 0;
@@ -263,7 +267,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const ChunkArgs a, Plan* pla
   }
   int64_t at = 0;
   for (int64_t p0 = 0; p0 < pairs; p0 += 1024) {
-    const int64_t p = p0 + threadIdx.x, n = tiles(p);
+    const int64_t p = p0 + threadIdx.x, n = pairs <= 1024 ? mine : tiles(p);
     int64_t sum;
     const int64_t before = at + plan_sum(n, tmp, &sum) - n;  // units before the row tile
     const int64_t S = before + p * SWITCH, len = n + SWITCH;
@@ -473,6 +477,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   grid_dependency_wait();  // the plan
+  grid_dependents_launch();  // (the join kernel may come as soon as there is room)
   const bool work = k < ws.plan->n_clusters;
   Walk w;
   if (work) w.start(a, *ws.plan, k);
@@ -1258,17 +1263,21 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
   if (warp == W_MMA) tmem_dealloc_pair(tmem, 512);
 }
 
-// Joins the parts of the row tiles that range borders cut: block (x, k - 1) takes
-// eight rows, a warp each, of the row tile that cluster k starts in, if cluster k - 1
-// holds its beginning.
+// Joins the parts of the row tiles that range borders cut: 32 blocks for every
+// cluster k but the first take eight rows each, a warp a row, of the row tile that it
+// starts in, if cluster k - 1 holds its beginning.
 __global__ void __launch_bounds__(256) join_kernel(const ChunkArgs a, const Workspace ws) {
-  const int k = (int)blockIdx.y + 1, lane = threadIdx.x & 31;
-  const int row = (int)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int k = (int)blockIdx.x / (ROWS / 8) + 1, lane = threadIdx.x & 31;
+  const int row = (int)blockIdx.x % (ROWS / 8) * 8 + (threadIdx.x >> 5);
+  // (the plan was there before the first cluster began: it is read while the last ones work)
   const int64_t nc = ws.plan->n_clusters;
   if (k >= nc) return;
+  __shared__ int64_t xs[MAX_CLUSTERS + 1];    // the units where the ranges begin
+  if (threadIdx.x <= nc) xs[threadIdx.x] = threadIdx.x < nc ? ws.plan->e[threadIdx.x].x : ws.plan->units;
   const PlanEntry e = ws.plan->e[k];
+  __syncthreads();
   const int64_t S = e.x - e.off;              // the row tile's first unit
-  const int64_t xp = ws.plan->e[k - 1].x;
+  const int64_t xp = xs[k - 1];
   if (e.off == 0 || xp > S) return;           // whole, or begun before cluster k - 1
   const SeqInfo s = seq_info(a, e.b, false);
   const int64_t r = (int64_t)e.rt * ROWS + row;
@@ -1277,9 +1286,10 @@ __global__ void __launch_bounds__(256) join_kernel(const ChunkArgs a, const Work
     return (int64_t)(2 * j + (j == k - 1 && xp < S ? 1 : 0)) * ROWS + row;
   };
   int last = k;
-  while (last + 1 < nc && ws.plan->e[last + 1].x < S + e.nt) ++last;
+  while (last + 1 < nc && xs[last + 1] < S + e.nt) ++last;
   // (a cluster without units has no part)
-  auto none = [&](int j) { return ws.plan->e[j].x == (j + 1 < nc ? ws.plan->e[j + 1].x : ws.plan->units); };
+  auto none = [&](int j) { return xs[j] == xs[j + 1]; };
+  grid_dependency_wait();
   float M = -INFINITY;
   for (int j = k - 1 + lane; j <= last; j += 32)
     if (!none(j)) M = fmaxf(M, ws.m[part(j)]);
@@ -1378,8 +1388,7 @@ cudaError_t launch_chunk(ChunkArgs a, void* workspace, cudaStream_t s) {
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   e = launch_after_prep(chunk_kernel, 4 * clusters, NTHREADS, SMEM, s, a, ws, kmap, rmap, smap);
   if (e != cudaSuccess || clusters == 1) return e;
-  join_kernel<<<dim3(ROWS / 8, clusters - 1), 256, 0, s>>>(a, ws);
-  return cudaGetLastError();
+  return launch_after_prep(join_kernel, (unsigned)(ROWS / 8 * (clusters - 1)), 256, 0, s, a, ws);
 }
 
 }  // namespace kv8
