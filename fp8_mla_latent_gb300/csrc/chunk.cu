@@ -124,10 +124,10 @@ constexpr int OFF_XMAX = 1024;               // score: [2][128 rows][2 pages] a 
 constexpr int OFF_XL = OFF_XMAX + 2048;      // score: [128 rows][2 pages] l
 constexpr int OFF_XQ = OFF_XL + 1024;        // score: [128 rows][4 parts] query maxima
 constexpr int OFF_MG = OFF_XQ + 2048;        // score: [128] M_g at a row tile's end
-constexpr int OFF_LIM = OFF_MG + 512;        // score: [2][128] keys that the rows see
-constexpr int OFF_C = OFF_LIM + 1024;        // score: [2][128] the rows' c
-constexpr int OFF_WALK = OFF_C + 1024;       // score: [16 warps][2] segments
-constexpr int OFF_SC = OFF_WALK + 2048;      // score: [NSC][128][2] row scales
+constexpr int OFF_LIM = OFF_MG + 512;        // score: [128] keys that the rows see
+constexpr int OFF_C = OFF_LIM + 512;         // score: [128] the rows' c
+constexpr int OFF_WALK = OFF_C + 512;        // score: [16 warps] segments
+constexpr int OFF_SC = OFF_WALK + 1024;      // score: [NSC][128][2] row scales
 constexpr int OFF_PL = OFF_SC + NSC * 1024;  // score: [NSC] of a tile's 64 token pairs: (sLc, sLc, sRc, sRc), then log2 sLc
 constexpr int PL_BYTES = 64 * 16 + 64 * 8;
 constexpr int OFF_QL = (OFF_PL + NSC * PL_BYTES + 1023) / 1024 * 1024;  // score: lo of Lc, four atoms
@@ -325,7 +325,7 @@ struct Walk {
   __device__ __forceinline__ bool whole() const { return t == 0 && n == nt; }
 };
 
-static_assert(sizeof(Walk) * 2 * N_LANE_WARPS <= OFF_SC - OFF_WALK, "segments");
+static_assert(sizeof(Walk) * N_LANE_WARPS <= OFF_SC - OFF_WALK, "segments");
 
 // The block-table entries of 32 pages, one per lane, from page `from` on.
 struct PageWindow {
@@ -388,18 +388,7 @@ __device__ __forceinline__ float lg2_approx(float x) {
 __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
 
-// Two e4m3 terms of four f32 values on their scale: hi = e4m3(x), lo = e4m3(x - hi).
-__device__ __forceinline__ void split4(const float* x, uint32_t& hi, uint32_t& lo) {
-  const uint16_t h01 = f32x2_to_e4m3x2(x[0], x[1]), h23 = f32x2_to_e4m3x2(x[2], x[3]);
-  const uint32_t f01 = e4m3x2_to_f16x2(h01), f23 = e4m3x2_to_f16x2(h23);
-  const float2 d01 = __half22float2(*reinterpret_cast<const __half2*>(&f01));
-  const float2 d23 = __half22float2(*reinterpret_cast<const __half2*>(&f23));
-  const uint16_t l01 = f32x2_to_e4m3x2(x[0] - d01.x, x[1] - d01.y);
-  const uint16_t l23 = f32x2_to_e4m3x2(x[2] - d23.x, x[3] - d23.y);
-  hi = (uint32_t)h01 | ((uint32_t)h23 << 16);
-  lo = (uint32_t)l01 | ((uint32_t)l23 << 16);
-}
-// The same of an f16 pair (the residual of the hi term is exact in f16).
+// Two e4m3 terms of an f16 pair on its scale: hi = e4m3(x), lo = e4m3(x - hi) (the residual is exact in f16).
 __device__ __forceinline__ void split_h2(uint32_t x, uint16_t& hi, uint16_t& lo) {
   const __half2 v = *reinterpret_cast<const __half2*>(&x);
   hi = f16x2_to_e4m3x2(v);
@@ -667,9 +656,9 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
       float* xl = reinterpret_cast<float*>(sm + OFF_XL);
       uint32_t* xq = reinterpret_cast<uint32_t*>(sm + OFF_XQ);
       float* mgs = reinterpret_cast<float*>(sm + OFF_MG);
-      int* lims = reinterpret_cast<int*>(sm + OFF_LIM);
+      int* lim = reinterpret_cast<int*>(sm + OFF_LIM);
       float* cs = reinterpret_cast<float*>(sm + OFF_C);
-      Walk* walks = reinterpret_cast<Walk*>(sm + OFF_WALK) + (warp - W_LANE) * 2;
+      Walk* walk = reinterpret_cast<Walk*>(sm + OFF_WALK) + (warp - W_LANE);  // (it has no registers to spare)
       const int rh = row0 + 16 * hl;          // the thread's rows of a tile: rh, rh + 8
       const int mh = rh + 8 * (i4 & 1);       // the row this lane speaks for there
       uint32_t px = 0;
@@ -679,33 +668,30 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
         return wait(B_PX + q, px++);
       };
       // The queries of a row tile: two e4m3 terms on the scale that puts a row's largest value
-      // in [128, 256); c folds the scale back in, with sm_scale log2 e.
+      // in [128, 256); c folds the scale back in, with sm_scale log2 e. Two of the thread's rows
+      // at a time, their channels all in flight at once.
       auto load_query = [&](const Walk& x) -> bool {
         const int64_t r0 = (int64_t)x.rt * ROWS + rank * CROWS, rows = (int64_t)x.s.nq * a.H;
         const uint32_t qlo = smem_u32(sm + OFF_QL) + part * OP_ATOM, qrp = smem_u32(sm + OFF_QR);
-        if (part == 0) {  // the keys that row q * 32 + lane sees (rows past the last one: as many as that)
+        if (part == 0) {  // the keys that row q * 32 + lane sees (rows past the last one are copies of it)
           const int tok = (int)((uint32_t)(r0 + q * 32 + lane) / (uint32_t)a.H);
-          lims[(x.seg & 1) * CROWS + q * 32 + lane] = limit_of(a, x.s, tok < x.s.nq ? tok : x.s.nq - 1);
+          lim[q * 32 + lane] = limit_of(a, x.s, tok < x.s.nq ? tok : x.s.nq - 1);
         }
 #pragma unroll 1
-        for (int hl = 0; hl < 2; ++hl) {  // two of the thread's rows: their channels all in flight at once
+        for (int hl = 0; hl < 2; ++hl) {
           uint4 v[2][5];
-          uint32_t top[2];                // a row's largest magnitude, as bf16 bits (ordered; 0x7F80 and up is inf or NaN)
 #pragma unroll
           for (int p = 0; p < 2; ++p) {
             const int64_t r = r0 + row0 + 16 * hl + 8 * p;
             const uint32_t at = (uint32_t)(r < rows ? r : rows - 1);
             const int64_t tok = x.s.q0 + at / (uint32_t)a.H, head = at % (uint32_t)a.H;
             const uint4* pq = reinterpret_cast<const uint4*>(a.q_lat + tok * a.ql_t + head * a.ql_h + part * 128) + i4;
-            const uint4* pr = reinterpret_cast<const uint4*>(a.q_rope + tok * a.qr_t + head * a.qr_h + part * 16) + (i4 & 1);
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[p][j] = __ldg(pq + 4 * j);
-            v[p][4] = __ldg(pr);
-            if (r >= rows) {  // past the last row: zeros
-#pragma unroll
-              for (int j = 0; j < 5; ++j) v[p][j] = make_uint4(0u, 0u, 0u, 0u);
-            }
+            v[p][4] = __ldg(reinterpret_cast<const uint4*>(a.q_rope + tok * a.qr_t + head * a.qr_h + part * 16) + (i4 & 1));
           }
+          // a row's largest magnitude, as bf16 bits (ordered; 0x7F80 and up is inf or NaN)
+          uint32_t top[2];
 #pragma unroll
           for (int p = 0; p < 2; ++p) {
             uint32_t t2 = 0;
@@ -727,19 +713,25 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
             uint32_t mx = m4.x > m4.y ? m4.x : m4.y;
             mx = m4.z > mx ? m4.z : mx;
             mx = m4.w > mx ? m4.w : mx;
-            const bool nan = mx >= 0x7F80u;
+            // (a row with a NaN or an infinity is all NaN codes)
+            const uint32_t nan = mx >= 0x7F80u ? 0x7F7F7F7Fu : 0u;
             // largest value in [2^e, 2^(e+1)): the scale 2^(7 - e), at most 2^87
             int e = (int)(mx >> 7) - 127;
             e = e < -80 ? -80 : e;
-            if (mx == 0 || nan) e = 7;
+            if (mx == 0 || nan != 0u) e = 7;
             const float sc = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
             if (part == 0 && i4 == 0)
-              cs[(x.seg & 1) * CROWS + row] = fmaxf(a.sm_scale * LOG2E * __uint_as_float((uint32_t)(127 - 7 + e) << 23), 1e-37f);
-            // (a row with a NaN or an infinity is all NaN codes)
+              cs[row] = fmaxf(a.sm_scale * LOG2E * __uint_as_float((uint32_t)(127 - 7 + e) << 23), 1e-37f);
+            // (scaled by a power of two a bf16 is exact in f16 wherever it counts: the lo term ends
+            // at 2^-10)
             auto terms = [&](uint32_t w0, uint32_t w1, uint32_t& hi, uint32_t& lo) {
-              const float f4[4] = {bf16_lo(w0) * sc, bf16_hi(w0) * sc, bf16_lo(w1) * sc, bf16_hi(w1) * sc};
-              split4(f4, hi, lo);
-              if (nan) hi = 0x7F7F7F7Fu;
+              const __half2 a0 = __floats2half2_rn(bf16_lo(w0) * sc, bf16_hi(w0) * sc);
+              const __half2 a1 = __floats2half2_rn(bf16_lo(w1) * sc, bf16_hi(w1) * sc);
+              uint16_t h0, l0, h1, l1;
+              split_h2(*reinterpret_cast<const uint32_t*>(&a0), h0, l0);
+              split_h2(*reinterpret_cast<const uint32_t*>(&a1), h1, l1);
+              hi = ((uint32_t)h0 | ((uint32_t)h1 << 16)) | nan;
+              lo = (uint32_t)l0 | ((uint32_t)l1 << 16);
             };
             uint2 hi, lo;
 #pragma unroll
@@ -768,30 +760,19 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
       };
 
       bool ok = true, more = w.more();
-      if (more) {
-        walks[0] = w;  // (every lane, the same)
-        __syncwarp();
-        ok = load_query(walks[0]) && quarter_sync();  // (the sync: cs and lims are read by every part)
-      }
-      for (int cur = 0; ok && more; cur ^= 1) {
-        // this segment, and the next, whose query is loaded as soon as this one's MMAs are done
-        const Walk& x = walks[cur];
-        {
-          Walk wn = x;
-          wn.next(a);
-          __syncwarp();
-          walks[cur ^ 1] = wn;
-          more = wn.more();
-        }
-        __syncwarp();
+      if (more) *walk = w;  // (every lane, the same)
+      __syncwarp();
+      while (ok && more) {
+        const Walk& x = *walk;
+        ok = load_query(x) && quarter_sync();  // (the sync: cs and lim are read by every part)
+        if (!ok) break;
         const int n_tiles = x.n;
-        const int* lim = lims + (x.seg & 1) * CROWS;
         uint64_t c2[2];                       // the rows' c, twice
         float l[2] = {0.f, 0.f};              // this thread's tokens, of its two rows
         float mg = -INFINITY, lift = 0.f;     // row `mh`: its reference, and how far that came down in all
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-          const float v = cs[(x.seg & 1) * CROWS + rh + 8 * p];
+          const float v = cs[rh + 8 * p];
           c2[p] = pk2(v, v);
         }
         int t0 = x.t * TILE + sub * SUB;
@@ -972,7 +953,12 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
                        map_to(smem_u32(&bars[B_RF + rf]), rank + 2));
         }
         gt += n_tiles;
-        if (more) ok = load_query(walks[cur ^ 1]) && quarter_sync();
+        Walk wn = x;
+        wn.next(a);
+        more = wn.more();
+        __syncwarp();
+        *walk = wn;
+        __syncwarp();
       }
       if (!ok && lane == 0) fail();
       // the context CTAs' last arrivals at this CTA have landed
