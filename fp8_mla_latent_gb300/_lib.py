@@ -97,13 +97,13 @@ def library_path() -> str:
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    if stream is None:  # (the handle alone: a Stream object costs 3 us a call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _is_device(t) -> bool:
@@ -425,11 +425,16 @@ def _strides(t):
     return tuple(t.stride(k) if t.shape[k] > 1 else 0 for k in (0, 1))
 
 
+_AS_IS = contextlib.nullcontext()
+
+
 def _on_device_of(first, *others):
     """The device of a call's tensors, made current for it (its launch, its default stream)."""
-    if any(t is not None and t.device != first.device for t in others):
-        raise ValueError("all tensors must be on the same device")
-    return torch.cuda.device(first.device) if first.device.type == "cuda" else contextlib.nullcontext()
+    d = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != d:
+            raise ValueError("all tensors must be on the same device")
+    return torch.cuda.device(d) if d >= 0 and d != torch.cuda.current_device() else _AS_IS
 
 
 # ----------------------------------------------------------------- chunks of new tokens
