@@ -81,6 +81,39 @@ __device__ __forceinline__ int64_t cta_scan(int64_t v, int64_t* tmp, int64_t* to
   return v;
 }
 
+// The same of two values; `tmp` holds 2 PG_WARPS.
+__device__ __forceinline__ void cta_scan2(int64_t (&v)[2], int64_t* tmp, int64_t (&total)[2]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int64_t u = __shfl_up_sync(0xffffffffu, v[k], o);
+      if (lane >= o) v[k] += u;
+    }
+  if (lane == 31) {
+    tmp[warp] = v[0];
+    tmp[PG_WARPS + warp] = v[1];
+  }
+  __syncthreads();
+  if (warp < 2) {
+    int64_t w = tmp[warp * PG_WARPS + lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t u = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += u;
+    }
+    tmp[warp * PG_WARPS + lane] = w;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (warp > 0) v[k] += tmp[k * PG_WARPS + warp - 1];
+    total[k] = tmp[k * PG_WARPS + PG_WARPS - 1];
+  }
+  __syncthreads();
+}
+
 // One pass over pages [lo, lo + PG_THREADS * PG_ROUNDS) cut at `hi`: lane masks of
 // the pages for which `is(refs[p], p)` holds, in index order.  Warp w takes 32 *
 // PG_ROUNDS consecutive pages, 32 at a time; every load of the pass is in flight
@@ -120,31 +153,38 @@ __device__ __forceinline__ void each_ranked(int64_t rank, int64_t lo, const uint
 
 constexpr int64_t PASS_PAGES = (int64_t)PG_THREADS * PG_ROUNDS;
 
-// Whether the pool has `need` free pages (CTA-wide; reads no further than it must).
-__device__ __forceinline__ bool enough_free(const int32_t* refs, int64_t n_blocks, int64_t need, int64_t* tmp) {
-  int64_t got = 0;
-  for (int64_t lo = 0; lo < n_blocks && got < need; lo += PASS_PAGES) {
-    uint32_t m[PG_ROUNDS];
-    int64_t total;
-    (void)rank_pages(refs, lo, n_blocks, [](int32_t r, int64_t) { return r == 0; }, m, tmp, &total);
-    got += total;
-  }
-  return got >= need;
-}
-// The first `need` free pages: f(rank, page).
+// The first `need` free pages: f(rank, page); false, and f not called, if the pool has fewer
+// (CTA-wide).  The first pass, mostly the only one, is ranked once for both.
 template <typename F>
-__device__ __forceinline__ void take_free(const int32_t* refs, int64_t n_blocks, int64_t need, int64_t* tmp, F f) {
-  int64_t got = 0;
-  for (int64_t lo = 0; lo < n_blocks && got < need; lo += PASS_PAGES) {
-    uint32_t m[PG_ROUNDS];
+__device__ __forceinline__ bool take_free(const int32_t* refs, int64_t n_blocks, int64_t need, int64_t* tmp, F f) {
+  if (need == 0) return true;
+  auto is = [](int32_t r, int64_t) { return r == 0; };
+  auto give = [&](int64_t k, int64_t p) {
+    if (k < need) f(k, p);
+  };
+  uint32_t m[PG_ROUNDS];
+  int64_t got;
+  const int64_t rank = rank_pages(refs, 0, n_blocks, is, m, tmp, &got);
+  if (got >= need) {
+    each_ranked(rank, 0, m, give);
+    return true;
+  }
+#pragma unroll 1
+  for (int64_t lo = PASS_PAGES; lo < n_blocks && got < need; lo += PASS_PAGES) {
     int64_t total;
-    const int64_t rank =
-        rank_pages(refs, lo, n_blocks, [](int32_t r, int64_t) { return r == 0; }, m, tmp, &total);
-    each_ranked(got + rank, lo, m, [&](int64_t k, int64_t p) {
-      if (k < need) f(k, p);
-    });
+    (void)rank_pages(refs, lo, n_blocks, is, m, tmp, &total);
     got += total;
   }
+  if (got < need) return false;
+  got = 0;
+#pragma unroll 1
+  for (int64_t lo = 0; lo < n_blocks && got < need; lo += PASS_PAGES) {
+    int64_t total;
+    const int64_t r = rank_pages(refs, lo, n_blocks, is, m, tmp, &total);
+    each_ranked(got + r, lo, m, give);
+    got += total;
+  }
+  return true;
 }
 
 // The last index i of the ascending a[0..n] with a[i] <= x (a[0] <= x < a[n]).
@@ -165,10 +205,11 @@ __device__ __forceinline__ int last_le(const T* a, int n, int64_t x) {
 __global__ void __launch_bounds__(PG_THREADS)
 append_kernel(PageTable t, const int32_t* __restrict__ n_new, int32_t* q_start, int64_t* dst_slot,
               int64_t cap, unsigned* err) {
-  extern __shared__ int32_t first[];  // CTA 0: [B + 1] pages taken before sequence b
-  __shared__ int64_t tmp[PG_WARPS + 1];
+  extern __shared__ int32_t first[];  // CTA 0: [B + 1] pages taken before sequence b, [B] pages it had; then everywhere: q_start
+  __shared__ int64_t tmp[2 * PG_WARPS];
   __shared__ unsigned bad;
   const int B = t.B;
+  int32_t* had = first + B + 1;
   if (cluster_rank() == 0) {
     if (threadIdx.x == 0) bad = 0;
     __syncthreads();
@@ -186,6 +227,7 @@ append_kernel(PageTable t, const int32_t* __restrict__ n_new, int32_t* q_start, 
             atomicOr(&bad, KV8_PAGES_ENOROOM);
           } else {
             need = pages_of(len + nn) - pages_of(len);
+            had[b] = pages_of(len);
             if (len % PAGE != 0) {  // the tokens begin in a page that is this sequence's alone
               const int32_t p = t.block_table[(int64_t)b * t.max_blocks + pages_of(len) - 1];
               if (p < 0 || p >= t.n_blocks || t.page_refs[p] != 1) atomicOr(&bad, KV8_PAGES_EINDEX);
@@ -193,15 +235,15 @@ append_kernel(PageTable t, const int32_t* __restrict__ n_new, int32_t* q_start, 
           }
         }
       }
-      int64_t sum_t, sum_p;
-      const int64_t inc_t = cta_scan(fresh, tmp, &sum_t), inc_p = cta_scan(need, tmp, &sum_p);
+      int64_t inc[2] = {fresh, need}, sum[2];
+      cta_scan2(inc, tmp, sum);
       if (b < B) {
-        const int64_t at = tokens + inc_t - fresh, pg = pages + inc_p - need;
+        const int64_t at = tokens + inc[0] - fresh, pg = pages + inc[1] - need;
         q_start[b] = (int32_t)(at < INT32_MAX ? at : INT32_MAX);
         first[b] = (int32_t)(pg < INT32_MAX ? pg : INT32_MAX);
       }
-      tokens += sum_t;
-      pages += sum_p;
+      tokens += sum[0];
+      pages += sum[1];
     }
     if (threadIdx.x == 0) {
       if (tokens > cap || pages > t.n_blocks) bad |= KV8_PAGES_ENOROOM;
@@ -209,33 +251,31 @@ append_kernel(PageTable t, const int32_t* __restrict__ n_new, int32_t* q_start, 
       first[B] = (int32_t)(pages < INT32_MAX ? pages : INT32_MAX);
     }
     __syncthreads();
-    if (bad == 0 && !enough_free(t.page_refs, t.n_blocks, pages, tmp)) {
+    if (bad == 0 && !take_free(t.page_refs, t.n_blocks, pages, tmp, [&](int64_t k, int64_t p) {
+          const int b = last_le(first, B, k);
+          t.block_table[(int64_t)b * t.max_blocks + had[b] + (k - first[b])] = (int32_t)p;
+          t.page_refs[p] = 1;
+        }))
       if (threadIdx.x == 0) bad = KV8_PAGES_ENOROOM;
-      __syncthreads();
-    }
+    __syncthreads();
     if (bad != 0) {
       // nothing is taken, and the call hands out no token
       if (threadIdx.x == 0) flag(err, bad);
       for (int b = threadIdx.x; b <= B; b += PG_THREADS) q_start[b] = 0;
     } else {
-      take_free(t.page_refs, t.n_blocks, pages, tmp, [&](int64_t k, int64_t p) {
-        const int b = last_le(first, B, k);
-        const int col = pages_of(t.seq_lens[b]) + (int)(k - first[b]);
-        t.block_table[(int64_t)b * t.max_blocks + col] = (int32_t)p;
-        t.page_refs[p] = 1;
-      });
-      __syncthreads();  // every owner was found by the old lengths
       for (int b = threadIdx.x; b < B; b += PG_THREADS) t.seq_lens[b] += n_new[b];
     }
   }
   all_ctas_sync();
-  const int64_t total = q_start[B];
+  for (int b = threadIdx.x; b <= B; b += PG_THREADS) first[b] = q_start[b];
+  __syncthreads();
+  const int64_t total = first[B];
   const int64_t stride = (int64_t)cluster_ctas() * PG_THREADS;
   for (int64_t i = (int64_t)cluster_rank() * PG_THREADS + threadIdx.x; i < cap; i += stride) {
     int64_t slot = -1;
     if (i < total) {
-      const int b = last_le(q_start, B, i);
-      const int64_t pos = (int64_t)t.seq_lens[b] - n_new[b] + (i - q_start[b]);
+      const int b = last_le(first, B, i);
+      const int64_t pos = (int64_t)t.seq_lens[b] - n_new[b] + (i - first[b]);
       slot = (int64_t)t.block_table[(int64_t)b * t.max_blocks + pos / PAGE] * PAGE + pos % PAGE;
     }
     dst_slot[i] = slot;
@@ -250,7 +290,7 @@ append_kernel(PageTable t, const int32_t* __restrict__ n_new, int32_t* q_start, 
 __global__ void __launch_bounds__(PG_THREADS)
 fork_kernel(PageTable t, const int32_t* __restrict__ src, const int32_t* __restrict__ dst,
             const int32_t* __restrict__ fork_len, int n, int32_t* moves, int32_t* n_moves, unsigned* err) {
-  extern __shared__ unsigned role[];  // CTA 0: [B] 1 = a destination, 2 = a source; then [n + 1] fresh pages before fork i
+  extern __shared__ unsigned role[];  // CTA 0: [B] 1 = a destination, 2 = a source; then [n + 1] fresh pages before fork i, [n] those pages
   __shared__ int64_t tmp[PG_WARPS + 1];
   __shared__ unsigned bad;
   __shared__ unsigned go;
@@ -288,26 +328,28 @@ fork_kernel(PageTable t, const int32_t* __restrict__ src, const int32_t* __restr
     for (int b = threadIdx.x; b < B; b += PG_THREADS)
       if (role[b] == 3u) atomicOr(&bad, KV8_PAGES_EINDEX);
     __syncthreads();
-    if (bad == 0 && !enough_free(t.page_refs, t.n_blocks, pages, tmp)) {
+    int32_t* fresh = first + n + 1;
+    if (bad == 0 && !take_free(t.page_refs, t.n_blocks, pages, tmp, [&](int64_t k, int64_t p) { fresh[k] = (int32_t)p; }))
       if (threadIdx.x == 0) bad = KV8_PAGES_ENOROOM;
-      __syncthreads();
+    __syncthreads();
+    if (bad == 0) {
+      // (a thread per fork: the few lanes that hold the free pages would walk them one by one)
+      for (int i = threadIdx.x; i < n; i += PG_THREADS) {
+        const int k = first[i];
+        if (first[i + 1] == k) continue;
+        const int32_t a = src[i], p = fresh[k];
+        const int64_t take = fork_len != nullptr ? fork_len[i] : t.seq_lens[a];
+        const int64_t col = pages_of(take) - 1;
+        moves[2 * k] = t.block_table[(int64_t)a * t.max_blocks + col];
+        moves[2 * k + 1] = p;
+        t.block_table[(int64_t)dst[i] * t.max_blocks + col] = p;
+        t.page_refs[p] = 1;
+      }
     }
     if (threadIdx.x == 0) {
       n_moves[0] = bad != 0 ? 0 : (int32_t)pages;
       if (bad != 0) flag(err, bad);
       go = bad == 0;
-    }
-    if (bad == 0) {
-      take_free(t.page_refs, t.n_blocks, pages, tmp, [&](int64_t k, int64_t p) {
-        // forks without a fresh page repeat their successor's count: the last of equal counts owns it
-        const int i = last_le(first, n, k);
-        const int64_t take = fork_len != nullptr ? fork_len[i] : t.seq_lens[src[i]];
-        const int col = pages_of(take) - 1;
-        moves[2 * k] = t.block_table[(int64_t)src[i] * t.max_blocks + col];
-        moves[2 * k + 1] = (int32_t)p;
-        t.block_table[(int64_t)dst[i] * t.max_blocks + col] = (int32_t)p;
-        t.page_refs[p] = 1;
-      });
     }
   }
   all_ctas_sync();  // CTA 0's writes, and `go` there
@@ -383,72 +425,97 @@ free_kernel(PageTable t, const int32_t* __restrict__ seq, int n, unsigned* err) 
 // ------------------------------------------------------------------ compact
 // With L live pages, the k-th live page at or above L moves to the k-th free page
 // below L: as few moves as can be, no page both source and destination.  Each CTA
-// ranks its share of the pool; moves ascend by source, so a table entry finds its
-// new page by bisection.
+// holds its share of the pool as a bitmap of live pages in shared memory, and beside
+// it how many pages of the whole pool move before each word's: a table entry finds
+// its move by counting bits there (in another CTA's shared memory, mostly), in place
+// of a search with a round trip to L2 at each of its steps.
+constexpr int64_t MAX_SHARE = KV8_PAGES_MAX_BLOCKS / PG_CTAS;
+static_assert(MAX_SHARE >= ONE_PASS && MAX_SHARE % 32 == 0, "the bitmap holds any share");
+
 __global__ void __launch_bounds__(PG_THREADS)
 compact_kernel(PageTable t, int32_t* moves, int32_t* n_moves, int32_t* n_live, unsigned* err) {
-  __shared__ int64_t tmp[PG_WARPS + 1];
+  __shared__ uint32_t live[MAX_SHARE / 32];
+  __shared__ int32_t before[MAX_SHARE / 32];
+  __shared__ int64_t tmp[2 * PG_WARPS];
   __shared__ int64_t count[3];  // this CTA's live pages, holes below L, movers from L on
   const int nc = (int)cluster_ctas(), rank = (int)cluster_rank();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t share = ((t.n_blocks + nc - 1) / nc + 31) / 32 * 32;
   const int64_t lo = rank * share < t.n_blocks ? rank * share : t.n_blocks;
   const int64_t hi = lo + share < t.n_blocks ? lo + share : t.n_blocks;
-  auto shared_of = [&](int k, int r) -> int64_t {
+  const int words = (int)((hi - lo + 31) / 32);
+  auto count_of = [&](int k, int r) -> int64_t {
     uint64_t v;
     asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(map_to(smem_u32(&count[k]), r)) : "memory");
     return (int64_t)v;
   };
-  auto tally = [&](auto is) -> int64_t {
-    int64_t n = 0;
-    for (int64_t p = lo; p < hi; p += PASS_PAGES) {
-      uint32_t m[PG_ROUNDS];
-      int64_t total;
-      (void)rank_pages(t.page_refs, p, hi, is, m, tmp, &total);
-      n += total;
+  int64_t n = 0;
+#pragma unroll 4
+  for (int w = warp; w < words; w += PG_WARPS) {
+    const int64_t p = lo + 32 * w + lane;
+    const uint32_t m = __ballot_sync(0xffffffffu, p < hi && t.page_refs[p] > 0);
+    if (lane == 0) {
+      live[w] = m;
+      n += __popc(m);
     }
-    return n;
-  };
-  int64_t n = tally([](int32_t r, int64_t) { return r > 0; });
-  if (threadIdx.x == 0) count[0] = n;
+  }
+  int64_t sum;
+  (void)cta_scan(n, tmp, &sum);
+  if (threadIdx.x == 0) count[0] = sum;
   all_ctas_sync();
   int64_t L = 0;
-  for (int r = 0; r < nc; ++r) L += shared_of(0, r);
-  auto hole = [L](int32_t r, int64_t p) { return r <= 0 && p < L; };
-  auto mover = [L](int32_t r, int64_t p) { return r > 0 && p >= L; };
-  const int64_t nh = tally(hole), nm = tally(mover);
+  for (int r = 0; r < nc; ++r) L += count_of(0, r);
+  // of word w: the pages below L without an owner, and those from L on that have one
+  auto low = [&](int w) -> uint32_t {
+    const int64_t d = L - lo - 32 * (int64_t)w;
+    return d <= 0 ? 0u : d >= 32 ? 0xffffffffu : (1u << d) - 1u;
+  };
+  auto holes = [&](int w) -> uint32_t { return ~live[w] & low(w); };  // (L is no more than the pool's pages)
+  auto movers = [&](int w) -> uint32_t { return live[w] & ~low(w); };
+  const int each = (words + PG_THREADS - 1) / PG_THREADS;  // consecutive words of a thread
+  const int w0 = min((int)threadIdx.x * each, words), w1 = min(w0 + each, words);
+  int64_t at[2] = {0, 0}, all_of[2], own[2];
+  for (int w = w0; w < w1; ++w) {
+    at[0] += __popc(holes(w));
+    at[1] += __popc(movers(w));
+  }
+  own[0] = at[0];
+  own[1] = at[1];
+  cta_scan2(at, tmp, all_of);
   if (threadIdx.x == 0) {
-    count[1] = nh;
-    count[2] = nm;
+    count[1] = all_of[0];
+    count[2] = all_of[1];
   }
   all_ctas_sync();
-  int64_t h0 = 0, m0 = 0, N = 0;
+  int64_t h = at[0] - own[0], v = at[1] - own[1], N = 0;
   for (int r = 0; r < nc; ++r) {
+    const int64_t c1 = count_of(1, r), c2 = count_of(2, r);
     if (r < rank) {
-      h0 += shared_of(1, r);
-      m0 += shared_of(2, r);
+      h += c1;
+      v += c2;
     }
-    N += shared_of(2, r);
+    N += c2;
   }
-  for (int64_t p = lo; p < hi; p += PASS_PAGES) {
-    uint32_t m[PG_ROUNDS];
-    int64_t total;
-    int64_t k = rank_pages(t.page_refs, p, hi, hole, m, tmp, &total);
-    each_ranked(h0 + k, p, m, [&](int64_t i, int64_t page) { moves[2 * i + 1] = (int32_t)page; });
-    h0 += total;
-    k = rank_pages(t.page_refs, p, hi, mover, m, tmp, &total);
-    each_ranked(m0 + k, p, m, [&](int64_t i, int64_t page) { moves[2 * i] = (int32_t)page; });
-    m0 += total;
+  for (int w = w0; w < w1; ++w) {
+    before[w] = (int32_t)v;
+    for (uint32_t m = holes(w); m != 0; m &= m - 1) moves[2 * h++ + 1] = (int32_t)(lo + 32 * w + __ffs(m) - 1);
+    for (uint32_t m = movers(w); m != 0; m &= m - 1) moves[2 * v++] = (int32_t)(lo + 32 * w + __ffs(m) - 1);
   }
   if (rank == 0 && threadIdx.x == 0) {
     n_moves[0] = (int32_t)N;
     if (n_live != nullptr) n_live[0] = (int32_t)L;
   }
-  all_ctas_sync();  // the moves are written, and every count read
+  all_ctas_sync();  // the moves, and every word's count
   const int64_t me = (int64_t)rank * PG_THREADS + threadIdx.x, all = (int64_t)nc * PG_THREADS;
-  // held entries first: they are told live from free by the old counts
+  for (int64_t k = me; k < N; k += all) {
+    const int32_t s = moves[2 * k], d = moves[2 * k + 1];
+    t.page_refs[d] = t.page_refs[s];
+    t.page_refs[s] = 0;
+  }
   const int64_t entries = (int64_t)t.B * t.max_blocks;
   for (int64_t e = me; e < entries; e += all) {
     const int b = (int)(e / t.max_blocks);
+    const int32_t p = t.block_table[e];
     int64_t len = t.seq_lens[b];
     const bool off = len < 0 || len > (int64_t)t.max_blocks * PAGE;
     if (off) len = len < 0 ? 0 : (int64_t)t.max_blocks * PAGE;
@@ -456,24 +523,25 @@ compact_kernel(PageTable t, int32_t* moves, int32_t* n_moves, int32_t* n_live, u
       if (off) flag(err, KV8_PAGES_EINDEX);
       continue;
     }
-    const int32_t p = t.block_table[e];
-    if (off || p < 0 || p >= t.n_blocks || t.page_refs[p] <= 0) {
+    if (off || p < 0 || p >= t.n_blocks) {
+      flag(err, KV8_PAGES_EINDEX);
+      continue;
+    }
+    const int r = (int)(p / share), w = (int)(p - r * share) >> 5;
+    uint32_t m;
+    int32_t k;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(m) : "r"(map_to(smem_u32(&live[w]), r)) : "memory");
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(k) : "r"(map_to(smem_u32(&before[w]), r)) : "memory");
+    const uint32_t bit = 1u << (p & 31);
+    if ((m & bit) == 0u) {
       flag(err, KV8_PAGES_EINDEX);
     } else if (p >= L) {
-      int64_t a = 0, z = N;  // the move whose source is p
-      while (z - a > 1) {
-        const int64_t mid = (a + z) >> 1;
-        if (moves[2 * mid] <= p) a = mid; else z = mid;
-      }
-      t.block_table[e] = moves[2 * a + 1];
+      const int64_t d = L - (p & ~31);  // (below L in this word: they stay)
+      if (d > 0) m &= ~((1u << d) - 1u);
+      t.block_table[e] = moves[2 * (k + __popc(m & (bit - 1u))) + 1];
     }
   }
-  all_ctas_sync();
-  for (int64_t k = me; k < N; k += all) {
-    const int32_t s = moves[2 * k], d = moves[2 * k + 1];
-    t.page_refs[d] = t.page_refs[s];
-    t.page_refs[s] = 0;
-  }
+  all_ctas_sync();  // this CTA's shared memory is read no more
 }
 
 // ------------------------------------------------------------------ copy
@@ -653,17 +721,17 @@ int ctas_for(int64_t entries) { return entries <= ONE_PASS ? 1 : PG_CTAS; }
 cudaError_t launch_pages_append(const PageTable& t, const int32_t* n_new, int32_t* q_start, int64_t* dst_slot,
                                 int64_t cap, unsigned* err, cudaStream_t s) {
   static std::atomic<int> memo[MAX_DEVICES];
-  const cudaError_t e = allow_smem(memo, append_kernel, (KV8_PAGES_MAX_SEQS + 1) * 4);
+  const cudaError_t e = allow_smem(memo, append_kernel, (2 * KV8_PAGES_MAX_SEQS + 1) * 4);
   if (e != cudaSuccess) return e;
-  return launch_cluster(append_kernel, ctas_for(cap), (size_t)(t.B + 1) * 4, s, t, n_new, q_start, dst_slot, cap, err);
+  return launch_cluster(append_kernel, ctas_for(cap), (size_t)(2 * t.B + 1) * 4, s, t, n_new, q_start, dst_slot, cap, err);
 }
 
 cudaError_t launch_pages_fork(const PageTable& t, const int32_t* src, const int32_t* dst, const int32_t* fork_len,
                               int n, int32_t* moves, int32_t* n_moves, unsigned* err, cudaStream_t s) {
   static std::atomic<int> memo[MAX_DEVICES];
-  const cudaError_t e = allow_smem(memo, fork_kernel, (2 * KV8_PAGES_MAX_SEQS + 1) * 4);
+  const cudaError_t e = allow_smem(memo, fork_kernel, (3 * KV8_PAGES_MAX_SEQS + 1) * 4);
   if (e != cudaSuccess) return e;
-  return launch_cluster(fork_kernel, ctas_for((int64_t)n * t.max_blocks), (size_t)(t.B + n + 1) * 4, s, t, src, dst,
+  return launch_cluster(fork_kernel, ctas_for((int64_t)n * t.max_blocks), (size_t)(t.B + 2 * n + 1) * 4, s, t, src, dst,
                         fork_len, n, moves, n_moves, err);
 }
 
