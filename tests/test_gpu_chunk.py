@@ -239,3 +239,48 @@ def test_a_prompt_in_pieces_is_the_prompt_at_once(pieces):
         check(d)
         at += n
     check(c)
+
+
+@pytest.mark.parametrize("H,nq,lens,causal", [(128, [300, 170], [400, 1000], True), (128, [90, 200], [2000, 50], False),
+                                              (64, [41] * 12, [60 * i + 41 for i in range(12)], True),
+                                              (20, [700, 1, 300], [900, 5000, 333], True)])
+def test_many_row_tiles_a_cluster(H, nq, lens, causal):
+    """Every cluster goes through many row tiles, whole ones and parts that are joined."""
+    check(Case(H, nq, lens, seed=sum(nq), pad=5), causal)
+
+
+def test_a_workspace_of_any_content_shared_by_calls_in_a_row():
+    c, d = Case(128, [6, 3], [900, 333], seed=24), Case(16, [90, 1], [200, 1000], seed=25)
+    want = [run(k)[:2] for k in (c, d)]
+    size = max(pkg.mla_absorb_chunk_fp8_batch_workspace_size(2, k.H, k.q_lat.shape[0], k.max_blocks) for k in (c, d))
+    ws = pkg.alloc_workspace(size)
+    ws.view(torch.uint8).fill_(0xFF)
+    got = []
+    for _ in range(3):
+        for k in (c, d):
+            out = torch.empty((k.q_lat.shape[0], k.H, DL), dtype=torch.bfloat16, device="cuda")
+            lse = torch.empty(out.shape[:2], device="cuda")
+            pkg.mla_absorb_chunk_fp8_batch(*k.args(), SM_SCALE, out=out, lse=lse, workspace=ws)
+            got.append((out, lse))
+    for i, (out, lse) in enumerate(got):
+        n = sum((c, d)[i % 2].nq)
+        assert torch.equal(out[:n], want[i % 2][0][:n]) and torch.equal(lse[:n], want[i % 2][1][:n])
+
+
+def test_pages_far_up_a_large_pool():
+    """Rows past 2^31 bytes of codes, and past 2^31 / 8 of scales."""
+    c = Case(16, [30, 2], [500, 300], seed=26)
+    want = run(c)[:2]
+    far = 70000
+    codes = torch.full((far * 64, 576), 0x7F, dtype=torch.uint8, device="cuda")
+    scales = torch.full((far * 64, 2), float("nan"), device="cuda")
+    table = c.table.clone()
+    held = sorted(int(p) for p in c.table.flatten().tolist() if p >= 0)
+    for i, p in enumerate(held):
+        to = far - 1 - i * 37
+        codes[to * 64: to * 64 + 64] = c.codes[p * 64: p * 64 + 64]
+        scales[to * 64: to * 64 + 64] = c.scales[p * 64: p * 64 + 64]
+        table[c.table == p] = to
+    c.codes, c.scales, c.table = codes, scales, table
+    out, l, err = run(c)
+    assert err == 0 and torch.equal(out, want[0]) and torch.equal(l, want[1])

@@ -425,3 +425,56 @@ def test_a_captured_step_replayed():
         lat = codes[int(s[0])].view(torch.float8_e4m3fn).float() * scales[int(s[0]), 0]
         assert torch.equal(quantized(rows)[0][0], codes[int(s[0])]) or (lat[:DL] - rows[0, :DL]).abs().max() < 0.5
     assert torch.isfinite(out).all()
+
+
+def test_free_pages_far_up_a_large_pool():
+    """Pages are found a pass of the pool after the other; too few of them change nothing."""
+    rng = np.random.default_rng(77)
+    p = Pool(40, 30, 50000)
+    p.refs[:] = 1
+    spots = np.concatenate([rng.choice(16000, 5, replace=False), 16384 + rng.choice(16000, 90, replace=False),
+                            33000 + rng.choice(17000, 100, replace=False)])
+    p.refs[spots] = 0
+    d = Dev(p)
+    n_new = np.zeros(40, np.int32)
+    n_new[:20] = rng.integers(1, 500, 20)
+    q, s, err = p.append(n_new, int(n_new.sum()))
+    gq, gs = d.append(n_new, int(n_new.sum()))
+    assert err == 0 and np.array_equal(gq, q) and np.array_equal(gs, s)
+    d.same(p)
+    src, dst = [int(i) for i in rng.integers(0, 20, 15)], list(range(20, 35))
+    moves, err = p.fork(src, dst)
+    assert err == 0 and d.fork(src, dst) == moves
+    d.same(p)
+    before = p.copy()
+    n_new = np.full(40, 600, np.int32)
+    n_new[:35] = 0
+    while True:  # as many as are free, and then one page more
+        need = sum((int(n) + 63) // 64 for n in n_new)
+        if need > int((p.refs == 0).sum()):
+            break
+        n_new[35:] += 64
+    assert n_new.max() <= 30 * PAGE
+    q, s, err = p.append(n_new, int(n_new.sum()))
+    gq, gs = d.append(n_new, int(n_new.sum()))
+    assert err == 2 and (gq == 0).all() and (gs == -1).all()
+    d.same(before, 2)
+
+
+def test_copy_far_up_a_large_pool():
+    """Pages past 2^31 bytes of codes."""
+    n_blocks = 70000
+    codes = torch.zeros((n_blocks * PAGE, D), dtype=torch.uint8, device="cuda")
+    scales = torch.zeros((n_blocks * PAGE, 2), device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(5)
+    pairs = [(3, 69999), (69998, 4), (60001, 60003)]
+    for a, _ in pairs:
+        codes[a * PAGE: (a + 1) * PAGE].random_(0, 256, generator=g)
+        scales[a * PAGE: (a + 1) * PAGE].normal_(generator=g)
+    pkg.kv8_pages_copy(codes, scales, torch.tensor(pairs, dtype=torch.int32, device="cuda"))
+    for a, b in pairs:
+        for w in (codes, scales):
+            assert torch.equal(w[a * PAGE: (a + 1) * PAGE], w[b * PAGE: (b + 1) * PAGE])
+            w[a * PAGE: (a + 1) * PAGE] = 0
+            w[b * PAGE: (b + 1) * PAGE] = 0
+    assert not codes.any() and not scales.any()
