@@ -68,8 +68,15 @@ constexpr int W_TMA = 0, W_MMA = 1, W_SCALE = 2, W_LANE = 3;
 constexpr int N_LANE_WARPS = 16;             // four per TMEM lane quarter, and per scheduler
 constexpr int NTHREADS = (W_LANE + N_LANE_WARPS) * 32;
 constexpr int MAX_CLUSTERS = NUM_SMS / 4;
-constexpr int MIN_TILES = 2;                 // key tiles that are worth a cluster of their own
-constexpr int SWITCH = 6;                    // what beginning a row tile costs, in key tiles
+// A cluster per row tile, or more while each has MIN_TILES key tiles.  One token at 128 heads over
+// 2048 keys (16 tiles): 29.5 us a call in ranges of two, 32.9 of four; over 512 keys (4 tiles) 25.0
+// of two, 27.5 of one; four row tiles of one key tile each: 20.6 in four clusters, 32 in two.
+constexpr int MIN_TILES = 2;
+// What beginning a row tile costs, in key tiles: 19 thousand cycles (the query is loaded and split
+// while the context pair writes its results, and the pipeline fills) against 3.1 thousand a tile.  A
+// prompt of 4096 tokens at 128 heads: 2.97 ms when ranges count 2 for it, 2.31 for 4, 2.11 for 5,
+// 2.00 for 6, 2.02 for 7.
+constexpr int SWITCH = 6;
 constexpr int BLK = PAGE * 128;              // 8 KB: [64 tokens x 128 bytes]
 constexpr int RBLK = PAGE * DR;              // 4 KB: [64 tokens x 64 bytes]
 constexpr int KTILE = 4 * BLK + RBLK;        // a score CTA's page of a tile: 36 KB
@@ -259,7 +266,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const ChunkArgs a, Plan* pla
   for (int64_t p = threadIdx.x; p < pairs; p += 1024) mine += tiles(p);
   (void)plan_sum(mine, tmp, &units);
   const int64_t total = units + pairs * SWITCH;
-  int64_t nc = units / MIN_TILES;
+  int64_t nc = units / MIN_TILES > pairs ? units / MIN_TILES : pairs;
   nc = nc > clusters ? clusters : (nc < 1 ? (units > 0 ? 1 : 0) : nc);
   if (threadIdx.x == 0) {
     plan->n_clusters = nc;
@@ -1249,12 +1256,21 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
   if (warp == W_MMA) tmem_dealloc_pair(tmem, 512);
 }
 
-// Joins the parts of the row tiles that range borders cut: 32 blocks for every
-// cluster k but the first take eight rows each, a warp a row, of the row tile that it
-// starts in, if cluster k - 1 holds its beginning.
+// Joins the parts of the row tiles that range borders cut: for every cluster k but the
+// first, the row tile that it starts in, if cluster k - 1 holds its beginning; a warp per
+// row, or per row and SPLIT-th of its channels.  In four parts a single row tile in many
+// parts is read by 128 SMs in place of 32 (one token over 8192 keys at 128 heads: 38.8
+// against 45.6 us a call); where most clusters hold a border the blocks that gives cost
+// more than that (4 x 32 tokens over 16384 keys: 234.8 against 230.3 us).
+constexpr int JOIN_BLOCKS = ROWS / 8;
+constexpr int FEW_ROW_TILES = 8;
+
+template <int SPLIT>
 __global__ void __launch_bounds__(256) join_kernel(const ChunkArgs a, const Workspace ws) {
-  const int k = (int)blockIdx.x / (ROWS / 8) + 1, lane = threadIdx.x & 31;
-  const int row = (int)blockIdx.x % (ROWS / 8) * 8 + (threadIdx.x >> 5);
+  static_assert(MAX_CLUSTERS <= 64, "two parts a lane");
+  const int k = (int)blockIdx.x / (JOIN_BLOCKS * SPLIT) + 1, lane = threadIdx.x & 31;
+  const int row = (int)blockIdx.x % (JOIN_BLOCKS * SPLIT) / SPLIT * 8 + (threadIdx.x >> 5);
+  const int ch = (int)blockIdx.x % SPLIT * (DL / SPLIT);
   // (the plan was there before the first cluster began: it is read while the last ones work)
   const int64_t nc = ws.plan->n_clusters;
   if (k >= nc) return;
@@ -1273,54 +1289,74 @@ __global__ void __launch_bounds__(256) join_kernel(const ChunkArgs a, const Work
   };
   int last = k;
   while (last + 1 < nc && xs[last + 1] < S + e.nt) ++last;
-  // (a cluster without units has no part)
-  auto none = [&](int j) { return xs[j] == xs[j + 1]; };
   grid_dependency_wait();
-  float M = -INFINITY;
-  for (int j = k - 1 + lane; j <= last; j += 32)
-    if (!none(j)) M = fmaxf(M, ws.m[part(j)]);
+  // a lane per part: its reference, its sum (a cluster without units has no part); at most
+  // MAX_CLUSTERS of them, so two each
+  float m[2], wt[2], M = -INFINITY, L = 0.f;
+  bool there[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int j = k - 1 + lane + 32 * h;
+    there[h] = j <= last && xs[j] != xs[j + 1];
+    m[h] = there[h] ? ws.m[part(j)] : -INFINITY;
+    wt[h] = there[h] ? ws.l[part(j)] : 0.f;
+    M = fmaxf(M, m[h]);
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float L = 0.f;
-  float4 acc[4];
+  uint32_t has[2];
 #pragma unroll
-  for (int c = 0; c < 4; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-  for (int j = k - 1; j <= last; ++j) {
-    if (none(j)) continue;
-    const int64_t p = part(j);
-    const float m = ws.m[p], l = ws.l[p];
-    const float4* o = reinterpret_cast<const float4*>(ws.o + p * DL) + lane;
-    const float wt = m > -INFINITY ? ex2_approx(m - M) : 1.f;  // (a NaN l stays one)
-    L += wt * l;
+  for (int h = 0; h < 2; ++h) {
+    const float l = wt[h];
+    wt[h] = m[h] > -INFINITY ? ex2_approx(m[h] - M) : 1.f;  // (a NaN l stays one)
+    L += wt[h] * l;
+    has[h] = __ballot_sync(0xffffffffu, there[h]);
+  }
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const float4 v = o[32 * c];
-      acc[c].x += wt * v.x;
-      acc[c].y += wt * v.y;
-      acc[c].z += wt * v.z;
-      acc[c].w += wt * v.w;
+  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  constexpr int N = 4 / SPLIT;  // 16-byte units a lane
+  float4 acc[N];
+#pragma unroll
+  for (int c = 0; c < N; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int n = min(last - (k - 1) + 1 - 32 * h, 32);
+#pragma unroll(SPLIT == 1 ? 4 : 8)
+    for (int i = 0; i < n; ++i) {
+      const float w = __shfl_sync(0xffffffffu, wt[h], i);
+      const float4* o = reinterpret_cast<const float4*>(ws.o + part(k - 1 + 32 * h + i) * DL + ch) + lane;
+#pragma unroll
+      for (int c = 0; c < N; ++c) {
+        const float4 v = ((has[h] >> i) & 1u) ? o[32 * c] : make_float4(0.f, 0.f, 0.f, 0.f);
+        acc[c].x += w * v.x;
+        acc[c].y += w * v.y;
+        acc[c].z += w * v.z;
+        acc[c].w += w * v.w;
+      }
     }
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;
   const int64_t at = s.q0 * a.H + r;
-  uint2* out = reinterpret_cast<uint2*>(a.out + at * DL) + lane;
+  uint2* out = reinterpret_cast<uint2*>(a.out + at * DL + ch) + lane;
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
+  for (int c = 0; c < N; ++c) {
     const __nv_bfloat162 x = __floats2bfloat162_rn(acc[c].x * inv, acc[c].y * inv);
     const __nv_bfloat162 y = __floats2bfloat162_rn(acc[c].z * inv, acc[c].w * inv);
     out[32 * c] = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
   }
+  if (ch != 0) return;
   if (a.lse != nullptr && lane == 0) a.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * LN2;
 }
 
 constexpr int64_t OFF_PLAN = 256, OFF_BASE = 2048;
 static_assert(OFF_PLAN + sizeof(Plan) <= OFF_BASE, "plan area");
 
+int64_t most_row_tiles(int B, int H, int64_t total_q) { return total_q * H / ROWS + B; }
+
 // Clusters that a call of these sizes can use, whatever the lengths turn out to be.
 int most_clusters(int B, int H, int64_t total_q, int max_blocks) {
-  const int64_t row_tiles = total_q * H / ROWS + B, keys = ((int64_t)max_blocks * PAGE + TILE - 1) / TILE;
-  const int64_t units = row_tiles * keys / MIN_TILES;
+  const int64_t keys = ((int64_t)max_blocks * PAGE + TILE - 1) / TILE;
+  const int64_t tiles = most_row_tiles(B, H, total_q), units = tiles * (keys > MIN_TILES ? keys : MIN_TILES) / MIN_TILES;
   return (int)(units < 1 ? 1 : (units < MAX_CLUSTERS ? units : MAX_CLUSTERS));
 }
 
@@ -1374,7 +1410,10 @@ cudaError_t launch_chunk(ChunkArgs a, void* workspace, cudaStream_t s) {
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   e = launch_after_prep(chunk_kernel, 4 * clusters, NTHREADS, SMEM, s, a, ws, kmap, rmap, smap);
   if (e != cudaSuccess || clusters == 1) return e;
-  return launch_after_prep(join_kernel, (unsigned)(ROWS / 8 * (clusters - 1)), 256, 0, s, a, ws);
+  const unsigned blocks = JOIN_BLOCKS * (clusters - 1);
+  if (most_row_tiles(a.B, a.H, a.total_q) < FEW_ROW_TILES)
+    return launch_after_prep(join_kernel<4>, 4 * blocks, 256, 0, s, a, ws);
+  return launch_after_prep(join_kernel<1>, blocks, 256, 0, s, a, ws);
 }
 
 }  // namespace kv8
