@@ -197,7 +197,7 @@ __device__ __forceinline__ int limit_of(const ChunkArgs& a, const SeqInfo& s, in
 __device__ __forceinline__ int key_tiles(const ChunkArgs& a, const SeqInfo& s, int rt) {
   const int64_t last = ((int64_t)rt * ROWS + ROWS - 1) / a.H;
   const int lim = limit_of(a, s, last < s.nq ? (int)last : s.nq - 1);
-  return lim > 0 ? (lim + TILE - 1) / TILE : 1;
+  return lim > 0 ? (lim - 1) / TILE + 1 : 1;
 }
 
 __device__ __forceinline__ int64_t plan_sum(int64_t v, int64_t* tmp, int64_t* total) {
@@ -1125,7 +1125,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
             sts128(opnd + off, make_uint4(hw[0], hw[1], hw[2], hw[3]));
             sts128(opnd + OP_ATOM + off, make_uint4(lw[0], lw[1], lw[2], lw[3]));
           }
-          if ((w.t + i + 1) * TILE > lim0 || pages != 3u) {
+          if (w.t + i + 1 > lim0 / TILE || pages != 3u) {
             // some row does not see all of this tile: no NaN code may stay in it
             if (!wait(B_VT + vs, (uint32_t)(g / NVT))) {
               ok = false;

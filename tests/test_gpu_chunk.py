@@ -284,3 +284,16 @@ def test_pages_far_up_a_large_pool():
     c.codes, c.scales, c.table = codes, scales, table
     out, l, err = run(c)
     assert err == 0 and torch.equal(out, want[0]) and torch.equal(l, want[1])
+
+
+def test_thousands_of_sequences():
+    """More sequences and row tiles than the plan holds in shared memory or in one pass."""
+    lens = [1 + (29 * i) % 90 for i in range(4500)]
+    c = Case(2, [1 + (i % 7 == 0) for i in range(4500)], [max(2, t) for t in lens], seed=27)
+    out, l, err = run(c)
+    assert err == 0
+    few = list(range(0, 4500, 90)) + [4095, 4096, 4097, 4499]
+    nq = list(c.nq)
+    c.nq = [n if b in few else 0 for b, n in enumerate(nq)]
+    c.check(out, l)
+    assert torch.isfinite(out.float()).all() and torch.isfinite(l).all()
