@@ -45,8 +45,27 @@
 // clear NaN codes from V tiles that some row of the tile sees only in part (where every row
 // sees a NaN, its NaN denominator carries it).
 //
-// The units of all row tiles are cut into equal ranges, one per cluster, by a one-CTA plan
-// kernel from q_start and seq_lens on the device.  Every wait is bounded (2 s): on a timeout
+// The units of all row tiles are cut into ranges of equal cost, one per cluster, by a one-CTA
+// plan kernel from q_start and seq_lens on the device (36 clusters are resident at once: their
+// 144 SMs are what a call uses).
+//
+// What bounds it.  A tile's MMAs take 2304 cycles on a score pair (36 of 64 cycles: 576 channels,
+// twice for the query's two terms, at twice the rate of bf16) and 2048 on a context pair.  A tile
+// takes about 3050: the sixteen warps of either side are a chain of
+// waits and arithmetic that long (softmax: 200 the wait for S, 900 reading and scaling it, 350 the
+// largest weight, 600 the exchange and the reference, 900 the exponentials and stores; context:
+// 850 the split, 150 a wait, 2 x 800 the rescale where a reference moved), at 54 % of the issue
+// slots; the tensor pipe is active 78 % of a score SM's time.  Ways to overlap two tiles were
+// slower: softmax warps in two groups on alternate tiles wait for the one S_R buffer (TMEM is
+// full), and more registers a thread, for two tiles at once, do not fit 19 warps.
+//
+// Measured, one GB300 (fractions of the bf16 rate of a large matrix product, 1895 TFLOP/s): 2 x 256
+// tokens over 65536 keys at 128 heads 5.98 ms, 1560 TFLOP/s, 0.82; a prompt of 4096 tokens 1.98 ms,
+// 1180, 0.62 (row tiles begin every 16 key tiles on average); 32 x 4 drafted tokens over up to
+// 16384 keys 0.23 ms, 1080, 0.57; one token of 4 heads over 256 keys 22 us, of which 4 are the plan,
+// 5 the query, 5 the pipeline and 5 the results.
+//
+// Every wait is bounded (2 s): on a timeout
 // the CTA flags the workspace error word, drains its MMAs and copies and meets its cluster
 // at the closing barrier.
 #include <cuda.h>

@@ -15,12 +15,16 @@
 // before anything is written (all or nothing), a ranking of the free pages, and a
 // walk over table entries; the cluster barrier separates them without a second
 // launch, and what they read (a few hundred KB at most) bounds nothing: they are
-// launch latency and dependent L2 round trips (about 1 us each).  A CTA count of
-// one is kept while the entries to walk fit one pass of one CTA.
+// launch latency (3 us) and dependent L2 round trips (about 1 us each), so the work
+// on them is to have fewer in a row.  A CTA count of one is kept while the entries to
+// walk fit one pass of one CTA.  Measured (device time under a profiler): for 2 forks
+// of short sequences free 4, fork 8, append 6 us; for 192 forks of up to 4096 tokens
+// among 256 sequences free 7, fork 12, append 14 us; compact 9 us for 100 pages, 12 us
+// for 8000 in 256 sequences.
 //
 // The copy is the only step that moves real data: 2 x 37376 bytes per page and
 // layer, an HBM stream.  Bulk copies through a shared-memory ring, issued by one
-// thread per CTA, keep about 15 MB in flight over 152 SMs.
+// thread per CTA, keep about 11 MB of loads in flight over 152 SMs.
 #include "kv8_common.cuh"
 #include "tc_ptx.cuh"
 
