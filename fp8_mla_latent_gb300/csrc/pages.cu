@@ -20,7 +20,7 @@
 // walk fit one pass of one CTA.  Measured (device time under a profiler): for 2 forks
 // of short sequences free 4, fork 8, append 6 us; for 192 forks of up to 4096 tokens
 // among 256 sequences free 7, fork 12, append 14 us; compact 9 us for 100 pages, 12 us
-// for 8000 in 256 sequences.
+// for 6200 in 256 sequences.
 //
 // The copy is the only step that moves real data: 2 x 37376 bytes per page and
 // layer, an HBM stream.  Bulk copies through a shared-memory ring, issued by one
