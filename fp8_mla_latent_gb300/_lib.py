@@ -41,6 +41,8 @@ class Kv8Error(RuntimeError):
 def lib() -> ctypes.CDLL:
     """Load libfp8mla.so, building it in-tree first if it is missing or stale."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not _build.up_to_date():
@@ -422,7 +424,9 @@ def mla_absorb_decode_fp8_batch_noalloc(q_lat, q_rope, kv_codes, kv_scales, bloc
 
 def _strides(t):
     """Element strides of the first two dimensions (0 for one of size 1, whose stride says nothing)."""
-    return tuple(t.stride(k) if t.shape[k] > 1 else 0 for k in (0, 1))
+    a, b = t.stride()[:2]
+    rows, heads = t.shape[:2]
+    return a if rows > 1 else 0, b if heads > 1 else 0
 
 
 _AS_IS = contextlib.nullcontext()
@@ -460,20 +464,21 @@ def mla_absorb_chunk_fp8_batch(q_lat, q_rope, kv_codes, kv_scales, block_table, 
     _need(block_table, "block_table", torch.int32, 2)
     _need(seq_lens, "seq_lens", torch.int32, 1)
     _need(q_start, "q_start", torch.int32, 1)
-    rows, H = q_lat.shape[:2]
+    rows, H, _ = q_lat.shape
     B, max_blocks = block_table.shape
-    if tuple(q_rope.shape[:2]) != (rows, H):
+    if q_rope.shape[0] != rows or q_rope.shape[1] != H:
         raise ValueError("q_lat must be [total_q,H,512] and q_rope [total_q,H,64]")
     if seq_lens.shape[0] != B or q_start.shape[0] != B + 1:
         raise ValueError("seq_lens needs one entry per row of block_table, and q_start one more")
     if out is None:
         out = torch.empty((rows, H, KV8_DL), dtype=torch.bfloat16, device=q_lat.device)
-    _need(out, "out", torch.bfloat16, 3)
-    if tuple(out.shape) != (rows, H, KV8_DL):
-        raise ValueError("out must be [total_q,H,512]")
+    else:
+        _need(out, "out", torch.bfloat16, 3)
+        if out.shape != (rows, H, KV8_DL):
+            raise ValueError("out must be [total_q,H,512]")
     if lse is not None:
         _need(lse, "lse", torch.float32, 2)
-        if tuple(lse.shape) != (rows, H):
+        if lse.shape != (rows, H):
             raise ValueError("lse must be [total_q,H]")
     need = mla_absorb_chunk_fp8_batch_workspace_size(B, H, rows, max_blocks)
     if workspace is None:

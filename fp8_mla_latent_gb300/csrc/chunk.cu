@@ -1384,7 +1384,7 @@ int64_t base_bytes(int B) { return ((int64_t)(B + 1) * 8 + 255) / 256 * 256; }
 }  // namespace
 
 int64_t chunk_workspace(int B, int H, int64_t total_q, int max_blocks) {
-  const int64_t rows = 2ll * most_clusters(B, H, total_q, max_blocks) * ROWS;
+  const int64_t most = most_clusters(B, H, total_q, max_blocks), rows = most > 1 ? 2 * most * ROWS : 0;  // (one cuts no row tile)
   return OFF_BASE + base_bytes(B) + rows * (8 + DL * 4);
 }
 
