@@ -478,3 +478,26 @@ def test_copy_far_up_a_large_pool():
             w[a * PAGE: (a + 1) * PAGE] = 0
             w[b * PAGE: (b + 1) * PAGE] = 0
     assert not codes.any() and not scales.any()
+
+
+def test_calls_with_nothing_to_do():
+    p = Pool(3, 4, 9)
+    p.append([70, 0, 3], 73)
+    d = Dev(p)
+    q, s = d.append([0, 0, 0], 0)
+    assert (q == 0).all() and len(s) == 0
+    q, s = d.append([0, 0, 0], 4)
+    assert (q == 0).all() and (s == -1).all()
+    assert d.fork([], []) == []
+    d.free([])
+    d.same(p)
+    codes, scales = pool_bytes(np.random.default_rng(1), 1, 9)
+    want = codes.clone()
+    pkg.kv8_pages_copy(codes, scales, torch.zeros((0, 2), dtype=torch.int32, device="cuda"), err_word=d.err)
+    pkg.kv8_pages_copy(codes, scales, torch.tensor([[0, 1]], dtype=torch.int32, device="cuda"), n_moves=i32([0]),
+                       err_word=d.err)
+    assert torch.equal(codes, want)
+    d.same(p)
+    e = Dev(Pool(3, 4, 9))
+    assert e.compact() == ([], 0)
+    e.same(Pool(3, 4, 9))
