@@ -73,7 +73,8 @@ class Case:
         held to 2^-9 (two e4m3 terms) plus 2^-11 (the f16 value that is split), or to 2^-17 of the
         row's largest where the second term runs out of bits; p_t moves by the score's error, the
         query's (2^-17 of its row's largest value) and the f32 sums' (2^-19 of the sum of
-        magnitudes); out is rounded to bf16, 2^-9."""
+        magnitudes); out is rounded to bf16: half a step, torch.finfo(torch.bfloat16).eps / 2 = 2^-8 of
+        the value (a step is 2^-7 of the binade's first value)."""
         n, T, H = self.nq[b], self.lens_list[b], self.H
         dev = self.device
         first = int(self.start[b])
@@ -99,7 +100,7 @@ class Case:
         each = torch.maximum((2.0 ** -9 + 2.0 ** -11 + 2 * ez[..., None]) * p,
                              2.0 ** -17 * gmax[..., None] / s[:, 0].clamp(min=1e-300))
         each = torch.where(see, each, 0.0)
-        tol = torch.einsum("nht,td->nhd", each, key[:, :DL].abs()) + 2.0 ** -9 * 1.01 * out.abs() + 1e-30
+        tol = torch.einsum("nht,td->nhd", each, key[:, :DL].abs()) + 2.0 ** -8 * out.abs() + 1e-30
         return out, lse, tol, ez + 2e-5 * torch.where(some, lse, 0.0).abs().clamp(min=1.0)
 
     def args(self):
