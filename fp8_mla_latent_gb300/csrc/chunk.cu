@@ -1290,25 +1290,27 @@ __global__ void __launch_bounds__(256) join_kernel(const ChunkArgs a, const Work
   const int k = (int)blockIdx.x / (JOIN_BLOCKS * SPLIT) + 1, lane = threadIdx.x & 31;
   const int row = (int)blockIdx.x % (JOIN_BLOCKS * SPLIT) / SPLIT * 8 + (threadIdx.x >> 5);
   const int ch = (int)blockIdx.x % SPLIT * (DL / SPLIT);
-  // (the plan was there before the first cluster began: it is read while the last ones work)
+  // (the plan was there before the first cluster began: it is read while the last ones work; a block
+  // without a row waits as well, so that this launch is not over before the chunk kernel is)
   const int64_t nc = ws.plan->n_clusters;
-  if (k >= nc) return;
+  if (k >= nc) return grid_dependency_wait();
   __shared__ int64_t xs[MAX_CLUSTERS + 1];    // the units where the ranges begin
   if (threadIdx.x <= nc) xs[threadIdx.x] = threadIdx.x < nc ? ws.plan->e[threadIdx.x].x : ws.plan->units;
   const PlanEntry e = ws.plan->e[k];
   __syncthreads();
   const int64_t S = e.x - e.off;              // the row tile's first unit
   const int64_t xp = xs[k - 1];
-  if (e.off == 0 || xp > S) return;           // whole, or begun before cluster k - 1
   const SeqInfo s = seq_info(a, e.b, false);
   const int64_t r = (int64_t)e.rt * ROWS + row;
-  if (r >= (int64_t)s.nq * a.H) return;
+  // (not whole, nor begun before cluster k - 1)
+  const bool mine = e.off != 0 && xp <= S && r < (int64_t)s.nq * a.H;
   auto part = [&](int j) -> int64_t {         // slot of cluster j's part
     return (int64_t)(2 * j + (j == k - 1 && xp < S ? 1 : 0)) * ROWS + row;
   };
   int last = k;
   while (last + 1 < nc && xs[last + 1] < S + e.nt) ++last;
   grid_dependency_wait();
+  if (!mine) return;
   // a lane per part: its reference, its sum (a cluster without units has no part); at most
   // MAX_CLUSTERS of them, so two each
   float m[2], wt[2], M = -INFINITY, L = 0.f;
