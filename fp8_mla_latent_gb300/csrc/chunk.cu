@@ -106,10 +106,10 @@ constexpr int VTILE = 2 * VBLK;              // a context CTA's half of the chan
 constexpr int NVT = 2;                       // V ring, in tiles
 constexpr int SUB = 64;                      // tokens of a softmax warp's share of a tile (a page)
 constexpr int OP_ATOM = CROWS * 128;         // 16 KB: [128 rows x 128 tokens], e4m3
-constexpr int P_F = CROWS * TILE * 2;        // payload: g' f16 (256 bytes a row), then rescale factors,
-constexpr int P_PAGES = P_F + CROWS * 4;     // then the pages present
+constexpr int P_F = CROWS * TILE * 2;        // payload: g' f16 (256 bytes a row), then the two pages' references,
+constexpr int P_PAGES = P_F + CROWS * 8;     // then the pages present
 constexpr int P_BYTES = P_PAGES + 4;
-constexpr int P_STRIDE = 33 * 1024;
+constexpr int P_STRIDE = 34 * 1024;
 constexpr float TAU = 1.0f;
 constexpr float P_LOG = 7.0f;                // g' <= 2^(TAU + P_LOG) = 256 <= 448
 constexpr float DOWN = 10.0f;
@@ -129,8 +129,7 @@ constexpr int B_SFULL = B_SCFULL + NSC;      // [2] score: S of a tile in TMEM (
 constexpr int B_SEMPTY = B_SFULL + 2;        // [2] rank 0: S read (16 warps x 2 CTAs)
 constexpr int B_QREADY = B_SEMPTY + 2;       // rank 0: the row tile's query in place (16 warps x 2)
 constexpr int B_PX = B_QREADY + 1;           // [4] score: the four warps of a lane quarter meet
-constexpr int B_EX = B_PX + 4;               // [4][2] score: the two warps of sixteen rows meet
-constexpr int B_PFREE = B_EX + 8;              // [2] score: payload buffer read (the partner's 16 warps)
+constexpr int B_PFREE = B_PX + 4;            // [2] score: payload buffer read (the partner's 16 warps)
 constexpr int B_PFULL = B_PFREE + 2;         // [2] context: payload arrived
 constexpr int B_VT = B_PFULL + 2;            // [NVT] context: V tile loaded
 constexpr int B_VEMPTY = B_VT + NVT;         // [NVT] ranks 2, 3: consumed
@@ -146,11 +145,10 @@ constexpr int NBAR = B_DRAIN + 1;
 // shared memory (dynamic, 1024-byte aligned)
 constexpr int OFF_FLAGS = 512;               // tmem base, abort flag
 constexpr int OFF_FACTS = OFF_FLAGS + 16;    // [8] score: pages present in the tiles of the ring
-constexpr int OFF_XMAX = 1024;               // score: [2][128 rows][2 pages] a tile's largest weights
-constexpr int OFF_XL = OFF_XMAX + 2048;      // score: [128 rows][2 pages] l
+constexpr int OFF_XL = 1024;                 // score: [128 rows][2 pages] l
 constexpr int OFF_XQ = OFF_XL + 1024;        // score: [128 rows][4 parts] query maxima
-constexpr int OFF_MG = OFF_XQ + 2048;        // score: [128] M_g at a row tile's end
-constexpr int OFF_LIM = OFF_MG + 512;        // score: [128] keys that the rows see
+constexpr int OFF_MG = OFF_XQ + 2048;        // score: [128 rows][2 pages] M_g at a row tile's end
+constexpr int OFF_LIM = OFF_MG + 1024;       // score: [128] keys that the rows see
 constexpr int OFF_C = OFF_LIM + 512;         // score: [128] the rows' c
 constexpr int OFF_WALK = OFF_C + 512;        // score: [16 warps] segments
 constexpr int OFF_SC = OFF_WALK + 1024;      // score: [NSC][128][2] row scales
@@ -160,16 +158,16 @@ constexpr int OFF_QL = (OFF_PL + NSC * PL_BYTES + 1023) / 1024 * 1024;  // score
 constexpr int OFF_QR = OFF_QL + 4 * OP_ATOM;                      // score: Rc, hi | lo
 constexpr int OFF_K = OFF_QR + OP_ATOM;
 constexpr int TOTAL_S = OFF_K + NK * KTILE;
-constexpr int OFF_RF = 1024;                 // context: [NRF][128] row factors
-constexpr int OFF_P = 4096;                  // context: two payloads
+constexpr int OFF_RF = 1024;                 // context: [NRF][128] row factors, and the references they go with
+constexpr int OFF_P = 5120;                  // context: two payloads
 constexpr int OFF_OP = OFF_P + 2 * P_STRIDE; // context: two operands (hi and lo atoms); results on their way out
 constexpr int OFF_V = OFF_OP + 4 * OP_ATOM;
 constexpr int TOTAL_C = OFF_V + NVT * VTILE;
 constexpr int SMEM = TOTAL_S > TOTAL_C ? TOTAL_S : TOTAL_C;
 // TMEM columns of a score CTA
 constexpr int T_SL = 0, T_SR = 256, T_QH = 384;
-static_assert(NSC >= NK + 2 && NSC <= 8 && NVT <= 8 && OFF_FACTS + 32 <= OFF_XMAX, "rings");
-static_assert(NBAR * 8 <= OFF_FLAGS && OFF_RF + NRF * 512 <= OFF_P, "shared memory layout");
+static_assert(NSC >= NK + 2 && NSC <= 8 && NVT <= 8 && OFF_FACTS + 32 <= OFF_XL, "rings");
+static_assert(NBAR * 8 <= OFF_FLAGS && OFF_RF + NRF * CROWS * 8 <= OFF_P, "shared memory layout");
 static_assert(OFF_K % 1024 == 0 && KTILE % 1024 == 0 && OFF_V % 1024 == 0 && P_STRIDE % 1024 == 0, "swizzle atoms");
 static_assert(P_BYTES <= P_STRIDE && N_LANE_WARPS * 2048 <= 4 * OP_ATOM, "payload and staging");
 static_assert(SMEM <= 232448, "shared memory above the per-CTA limit");
@@ -421,6 +419,10 @@ __device__ __forceinline__ void split_h2(uint32_t x, uint16_t& hi, uint16_t& lo)
   const uint32_t d = e4m3x2_to_f16x2(hi);
   lo = f16x2_to_e4m3x2(__hsub2(v, *reinterpret_cast<const __half2*>(&d)));
 }
+__device__ __forceinline__ uint32_t scaled_h2(uint32_t x, __half2 s) {
+  const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&x), s);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
 // NaN codes (0x7F, 0xFF) of four bytes set to 0
 __device__ __forceinline__ uint32_t no_nan(uint32_t v) {
   return v & ~__vcmpeq4(v & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
@@ -468,7 +470,6 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < NBAR; ++i) mbar_init(&bars[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&bars[B_SEMPTY + i], 2 * N_LANE_WARPS);
-    for (int i = 0; i < 8; ++i) mbar_init(&bars[B_EX + i], 2);
     mbar_init(&bars[B_QREADY], 2 * N_LANE_WARPS);
     for (int i = 0; i < 4; ++i) mbar_init(&bars[B_PX + i], N_LANE_WARPS / 4);
     mbar_init(&bars[B_EP], N_LANE_WARPS);
@@ -479,7 +480,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     if (rank >= 2) {  // what the context CTAs expect first
       for (int i = 0; i < 2; ++i) mbar_arrive_expect_tx(&bars[B_PFULL + i], P_BYTES);
-      for (int i = 0; i < NRF; ++i) mbar_arrive_expect_tx(&bars[B_RF + i], CROWS * 4);
+      for (int i = 0; i < NRF; ++i) mbar_arrive_expect_tx(&bars[B_RF + i], CROWS * 8);
     }
   }
   if (warp == W_MMA) {
@@ -678,7 +679,6 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
       const int i4 = lane & 3, r8 = lane >> 2;
       const int row0 = q * 32 + r8;           // the thread's rows: row0 + 8 p
       const uint32_t lane_addr = (uint32_t)(q * 32) << 16;
-      float* xmax = reinterpret_cast<float*>(sm + OFF_XMAX);
       float* xl = reinterpret_cast<float*>(sm + OFF_XL);
       uint32_t* xq = reinterpret_cast<uint32_t*>(sm + OFF_XQ);
       float* mgs = reinterpret_cast<float*>(sm + OFF_MG);
@@ -876,25 +876,13 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
           const bool b0 = i4 & 1;
           float ym = fmaxf(b0 ? y[1] : y[0], __shfl_xor_sync(0xffffffffu, b0 ? y[0] : y[1], 1));
           ym = fmaxf(ym, __shfl_xor_sync(0xffffffffu, ym, 2));
-          float* xm = xmax + (buf * CROWS + mh) * 2;
-          xm[sub] = ym;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars[B_EX + q * 2 + hl]);
-          if (!wait(B_EX + q * 2 + hl, (uint32_t)g)) {
-            ok = false;
-            break;
-          }
-          // its reference, and the factor of what was added up before (of l, and of O)
+          // its reference there, a whole number, and the factor of the l added up before
           float mn = mg;
-          {
-            const float2 v2 = *reinterpret_cast<const float2*>(xm);
-            ym = fmaxf(v2.x, v2.y);
-            if (ym > mg + TAU) {
-              mn = ym;
-            } else if (ym < mg - DOWN && mg - ym + lift <= DOWN_CAP) {
-              lift += mg - ym;
-              mn = ym;
-            }
+          if (ym > mg + TAU) {
+            mn = floorf(ym);
+          } else if (ym < mg - DOWN && mg - floorf(ym) + lift <= DOWN_CAP) {
+            mn = floorf(ym);
+            lift += mg - mn;
           }
           const float f = mn == mg ? 1.f : (mg > -INFINITY ? ex2_approx(mg - mn) : 0.f);
           mg = mn;
@@ -904,7 +892,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
           }
           const uint32_t to = map_to(smem_u32(sm + OFF_P + buf * P_STRIDE), rank + 2);
           const uint32_t bar = map_to(smem_u32(&bars[B_PFULL + buf]), rank + 2);
-          if (sub == 0 && i4 < 2) st_async_b32(to + P_F + mh * 4, __float_as_uint(f), bar);
+          if (i4 < 2) st_async_b32(to + P_F + (sub * CROWS + mh) * 4, __float_as_uint(mn), bar);
           if (warp == W_LANE && lane == 0) st_async_b32(to + P_PAGES, facts[sc], bar);
           // p = 2^(c u - M_g + 7) (nothing in sight so far: u is -inf, and p 0)
           const float mneg = P_LOG - fmaxf(mn, -3.0e38f);
@@ -953,7 +941,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
         }
         if (i4 < 2) {
           xl[mh * 2 + sub] = i4 ? l[1] : l[0];
-          if (sub == 0) mgs[mh] = mg;
+          mgs[mh * 2 + sub] = mg;
         }
         if (!quarter_sync()) {
           ok = false;
@@ -961,8 +949,10 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
         }
         if (part == 0) {  // a row per lane
           const int hh = q * 32 + lane;
-          const float L = xl[hh * 2] + xl[hh * 2 + 1];  // on the scale 2^(7 - M_g), as O
-          const float M = mgs[hh] - P_LOG;
+          // on the scale 2^(7 - the larger reference)
+          const float m0 = mgs[hh * 2], m1 = mgs[hh * 2 + 1], mm = fmaxf(m0, m1), M = mm - P_LOG;
+          const float L = xl[hh * 2] * (m0 == mm ? 1.f : ex2_approx(m0 - mm)) +
+                          xl[hh * 2 + 1] * (m1 == mm ? 1.f : ex2_approx(m1 - mm));
           float f = 1.f;
           if (x.whole()) {
             f = L == 0.f ? 0.f : 1.f / L;  // (a NaN stays one)
@@ -975,8 +965,10 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
             ws.l[at] = L;
           }
           const int rf = x.seg % NRF;
-          st_async_b32(map_to(smem_u32(sm + OFF_RF + rf * 512 + hh * 4), rank + 2), __float_as_uint(f),
-                       map_to(smem_u32(&bars[B_RF + rf]), rank + 2));
+          const uint32_t to = map_to(smem_u32(sm + OFF_RF + (rf * CROWS + hh) * 8), rank + 2);
+          const uint32_t bar = map_to(smem_u32(&bars[B_RF + rf]), rank + 2);
+          st_async_b32(to, __float_as_uint(f), bar);
+          st_async_b32(to + 4, __float_as_uint(mm), bar);
         }
         gt += n_tiles;
         Walk wn = x;
@@ -1097,6 +1089,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
       bool ok = true;
       for (; ok && w.more(); w.next(a)) {
         const int lim0 = limit_of(a, w.s, (int)((uint32_t)(w.rt * ROWS) / (uint32_t)a.H));  // the tile's first row sees least
+        float ref = -INFINITY, down = 0.f;  // the row's reference in O, and how far it came down in all
         for (int i = 0; i < w.n; ++i) {
           const int g = gt + i, pb = g & 1, vs = g % NVT;
           if (!wait_cluster(B_PFULL + pb, (uint32_t)(g >> 1))) {
@@ -1113,15 +1106,27 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
             pv[u][2] = v.z;
             pv[u][3] = v.w;
           }
-          const float f = reinterpret_cast<const float*>(sm + OFF_P + pb * P_STRIDE + P_F)[hh];
+          const float m0 = reinterpret_cast<const float*>(sm + OFF_P + pb * P_STRIDE + P_F)[hh];
+          const float m1 = reinterpret_cast<const float*>(sm + OFF_P + pb * P_STRIDE + P_F)[CROWS + hh];
           const uint32_t pages = *reinterpret_cast<const uint32_t*>(sm + OFF_P + pb * P_STRIDE + P_PAGES);
-          const bool any = __any_sync(0xffffffffu, f != 1.f) && i > 0;
           // the payload is read: the next one may be expected, and then come
           __syncwarp();
           if (lane == 0) {
             if (warp == W_LANE) mbar_arrive_expect_tx(&bars[B_PFULL + pb], P_BYTES);
             arrive_cluster_local(pfree + pb * 8);
           }
+          // O's reference is the larger of the pages', or above both: the factor of what was added up
+          // before, and the one that brings this warp's page onto it (powers of two, both)
+          const float top = fmaxf(m0, m1), own = part < 2 ? m0 : m1, was = ref;
+          if (top > ref) {
+            ref = top;
+          } else if (top < ref - DOWN && ref - top + down <= DOWN_CAP) {
+            down += ref - top;
+            ref = top;
+          }
+          const float f = ref == was ? 1.f : (was > -INFINITY ? ex2_approx(was - ref) : 0.f);
+          const bool any = __any_sync(0xffffffffu, f != 1.f) && i > 0;
+          const __half2 onto = __float2half2_rn(own == ref ? 1.f : ex2_approx(own - ref));
           // the operand buffer was read by the MMAs of tile g - 2 (at a row tile's start they were
           // waited for with its predecessor's results)
           if (i > 1 && !wait(B_ODONE + 2 * pb + 1, (uint32_t)((g >> 1) - 1))) {
@@ -1135,8 +1140,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
 #pragma unroll
             for (int v = 0; v < 4; ++v) {  // tokens 16 j + 4 v .. + 3
               uint16_t h0, l0, h1, l1;
-              split_h2(pv[2 * (v & 1)][2 * j + (v >> 1)], h0, l0);
-              split_h2(pv[2 * (v & 1) + 1][2 * j + (v >> 1)], h1, l1);
+              split_h2(scaled_h2(pv[2 * (v & 1)][2 * j + (v >> 1)], onto), h0, l0);
+              split_h2(scaled_h2(pv[2 * (v & 1) + 1][2 * j + (v >> 1)], onto), h1, l1);
               hw[v] = (uint32_t)h0 | ((uint32_t)h1 << 16);
               lw[v] = (uint32_t)l0 | ((uint32_t)l1 << 16);
             }
@@ -1199,7 +1204,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
         }
         tc_fence_after();
         __syncwarp();
-        const float f = reinterpret_cast<const float*>(sm + OFF_RF + rf * 512)[hh];
+        const float2 f2 = reinterpret_cast<const float2*>(sm + OFF_RF + rf * CROWS * 8)[hh];
+        const float f = f2.x, up = ref == f2.y ? 1.f : ex2_approx(ref - f2.y);  // (O onto the reference of l)
         // 64 bytes of every row at a time (32 columns of bf16, or 16 of a partial's f32) through
         // shared memory, so that a warp's stores write whole sectors: eight rows each
         const bool whole = w.whole();
@@ -1231,7 +1237,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
           tmem_wait_ld();
           // (a factor of 0: nothing seen, or nothing that counts)
 #pragma unroll
-          for (int j = 0; j < 16; ++j) v[j] = f == 0.f ? 0u : __float_as_uint(__uint_as_float(v[j]) * f);
+          for (int j = 0; j < 16; ++j) v[j] = f == 0.f ? 0u : __float_as_uint(__uint_as_float(v[j]) * up * f);
           if (whole) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -1254,7 +1260,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
         // written again when every warp's results have left them
         __syncwarp();
         if (lane == 0) {
-          if (warp == W_LANE) mbar_arrive_expect_tx(&bars[B_RF + rf], CROWS * 4);
+          if (warp == W_LANE) mbar_arrive_expect_tx(&bars[B_RF + rf], CROWS * 8);
           mbar_arrive(&bars[B_EP]);
         }
         if (!wait(B_EP, (uint32_t)w.seg)) {
