@@ -29,12 +29,14 @@
 //         thread p = 2^(c u - M_g + 7), its sum l, and the weights g' = p sLc as f16.  The
 //         reference M_g follows the largest weight 2^(c u) sLc of the row, not the largest
 //         score, so that the top weights fill the e4m3 range however the row scales differ
-//         (a scale under 2^-40 counts as that, so that p stays in range); it is lazy (moves up
-//         by more than 2^TAU, down by more than 2^DOWN).  g' goes to the row's context CTA by
-//         asynchronous remote stores.
+//         (a scale under 2^-40 counts as that, so that p stays in range); it is a whole number,
+//         and lazy (moves up by more than 2^TAU, down by more than 2^DOWN).  Each page of a tile,
+//         so each warp, has its own, which saves the two warps of a row from meeting in every
+//         tile (2 %).  g' and M_g go to the row's context CTA by asynchronous remote stores.
 // Context pair (ranks 2, 3), per key tile:
-//   sixteen warps split g' into two e4m3 terms (hi + residual), the A operand,
-//         and rescale the rows of O whose M_g moved;
+//   sixteen warps bring the pages' g' onto one reference (a power of two apart), split it into
+//         two e4m3 terms (hi + residual), the A operand, and rescale the rows of O whose
+//         reference moved;
 //   O += g'_hi V + g'_lo V    M = 256, N = 256 channels (each CTA holds half of them as
 //         B, the cache tile read MN-major), 16 MMAs into all 512 TMEM columns.
 //   At the end of a row tile the rows are divided by l, rounded to bf16 and written; where
@@ -51,18 +53,18 @@
 //
 // What bounds it.  A tile's MMAs take 2304 cycles on a score pair (36 of 64 cycles: 576 channels,
 // twice for the query's two terms, at twice the rate of bf16) and 2048 on a context pair.  A tile
-// takes about 3050: the sixteen warps of either side are a chain of
-// waits and arithmetic that long (softmax: 200 the wait for S, 900 reading and scaling it, 350 the
-// largest weight, 600 the exchange and the reference, 900 the exponentials and stores; context:
+// takes about 2950: the sixteen warps of either side are a chain of
+// waits and arithmetic that long (softmax: 250 the wait for S, 830 reading and scaling it, 500 the
+// largest weight, 430 the reference, 950 the exponentials and stores; context:
 // 850 the split, 150 a wait, 2 x 800 the rescale where a reference moved), at 54 % of the issue
 // slots; the tensor pipe is active 78 % of a score SM's time.  Ways to overlap two tiles were
 // slower: softmax warps in two groups on alternate tiles wait for the one S_R buffer (TMEM is
 // full), and more registers a thread, for two tiles at once, do not fit 19 warps.
 //
 // Measured, one GB300 (fractions of the bf16 rate of a large matrix product, 1895 TFLOP/s): 2 x 256
-// tokens over 65536 keys at 128 heads 5.98 ms, 1560 TFLOP/s, 0.82; a prompt of 4096 tokens 1.98 ms,
-// 1180, 0.62 (row tiles begin every 16 key tiles on average); 32 x 4 drafted tokens over up to
-// 16384 keys 0.23 ms, 1080, 0.57; one token of 4 heads over 256 keys 22 us, of which 4 are the plan,
+// tokens over 65536 keys at 128 heads 5.86 ms, 1590 TFLOP/s, 0.84; a prompt of 4096 tokens 1.95 ms,
+// 1200, 0.63 (row tiles begin every 16 key tiles on average); 32 x 4 drafted tokens over up to
+// 16384 keys 0.225 ms, 1105, 0.58; one token of 4 heads over 256 keys 22 us, of which 4 are the plan,
 // 5 the query, 5 the pipeline and 5 the results.
 //
 // Every wait is bounded (2 s): on a timeout
@@ -860,8 +862,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
                   if (8 * j + e >= n) u[4 * j + 2 * p + e] = 0xFF800000u;  // -inf
             }
           }
-          // the largest weight of row `mh` over the tile: the two rows' over this thread's
-          // tokens, then over the four lanes, then over the two pages
+          // the largest weight of row `mh` over the page: the two rows' over this thread's
+          // tokens, then over the four lanes
           float y[2] = {-INFINITY, -INFINITY};
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
