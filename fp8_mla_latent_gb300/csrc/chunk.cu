@@ -29,13 +29,14 @@
 //         thread p = 2^(c u - M_g + 7), its sum l, and the weights g' = p sLc as f16.  The
 //         reference M_g follows the largest weight 2^(c u) sLc of the row, not the largest
 //         score, so that the top weights fill the e4m3 range however the row scales differ
-//         (a scale under 2^-40 counts as that, so that p stays in range); it is a whole number,
-//         and lazy (moves up by more than 2^TAU, down by more than 2^DOWN).  Each page of a tile,
-//         so each warp, has its own, which saves the two warps of a row from meeting in every
-//         tile (2 %).  g' and M_g go to the row's context CTA by asynchronous remote stores.
+//         (a scale under 2^-40 counts as that, so that p stays in range); it is lazy (moves up
+//         by more than 2^TAU, down by more than 2^DOWN).  Each page of a tile, so each warp, has
+//         its own, which saves the two warps of a row from meeting in every tile (2 %).  g' and
+//         M_g go to the row's context CTA by asynchronous remote stores.
 // Context pair (ranks 2, 3), per key tile:
-//   sixteen warps bring the pages' g' onto one reference (a power of two apart), split it into
-//         two e4m3 terms (hi + residual), the A operand, and rescale the rows of O whose
+//   sixteen warps bring the pages' g' onto one reference, the larger of the two (the other page's
+//         by a factor in f16: two roundings of 2^-11, where the terms' own is 2^-9), split it
+//         into two e4m3 terms (hi + residual), the A operand, and rescale the rows of O whose
 //         reference moved;
 //   O += g'_hi V + g'_lo V    M = 256, N = 256 channels (each CTA holds half of them as
 //         B, the cache tile read MN-major), 16 MMAs into all 512 TMEM columns.
@@ -878,13 +879,13 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
           const bool b0 = i4 & 1;
           float ym = fmaxf(b0 ? y[1] : y[0], __shfl_xor_sync(0xffffffffu, b0 ? y[0] : y[1], 1));
           ym = fmaxf(ym, __shfl_xor_sync(0xffffffffu, ym, 2));
-          // its reference there, a whole number, and the factor of the l added up before
+          // its reference there, and the factor of the l added up before
           float mn = mg;
           if (ym > mg + TAU) {
-            mn = floorf(ym);
-          } else if (ym < mg - DOWN && mg - floorf(ym) + lift <= DOWN_CAP) {
-            mn = floorf(ym);
-            lift += mg - mn;
+            mn = ym;
+          } else if (ym < mg - DOWN && mg - ym + lift <= DOWN_CAP) {
+            lift += mg - ym;
+            mn = ym;
           }
           const float f = mn == mg ? 1.f : (mg > -INFINITY ? ex2_approx(mg - mn) : 0.f);
           mg = mn;
@@ -1118,7 +1119,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
             arrive_cluster_local(pfree + pb * 8);
           }
           // O's reference is the larger of the pages', or above both: the factor of what was added up
-          // before, and the one that brings this warp's page onto it (powers of two, both)
+          // before, and the one that brings this warp's page onto it
           const float top = fmaxf(m0, m1), own = part < 2 ? m0 : m1, was = ref;
           if (top > ref) {
             ref = top;

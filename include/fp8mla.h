@@ -365,10 +365,11 @@ int kv8_noalloc_error(void* stream);
  *               read with kv8_workspace_error().
  * Precision: a bf16 query value is held as two e4m3 terms, exactly where it is at
  * least 2^-9 of its row's largest; each softmax weight, times its key's sLc, as two
- * e4m3 terms (relative error <= 2^-9, and at least 2^-17 of the row's largest such
- * product; an sLc under 2^-40 counts as 2^-40 in that comparison); sums, maxima and
- * denominators in f32; out rounded to bf16 once.  lse within 2e-5 of its size or of
- * 1.  A query row with a NaN or an infinity gives NaN, unless it sees nothing.
+ * e4m3 terms of an f16 value (relative error <= 2^-9 + 3 * 2^-11, or 2^-17 of the
+ * row's largest such product if that is more; an sLc under 2^-40 counts as 2^-40 in
+ * that comparison); sums, maxima and denominators in f32; out rounded to bf16 once.
+ * lse within 2e-5 of its size or of 1.  A query row with a NaN or an infinity gives
+ * NaN, unless it sees nothing.
  * Errors: KV8_EINVAL, KV8_EALIGN, KV8_EUNSUPPORTED, KV8_EWORKSPACE, KV8_ECUDA.
  * ------------------------------------------------------------------------- */
 int64_t mla_absorb_chunk_fp8_batch_workspace_size(int B, int H, int64_t total_q, int max_blocks);

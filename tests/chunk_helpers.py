@@ -70,7 +70,9 @@ class Case:
         """(out, lse, tol_out, tol_lse) of sequence b in float64 (keep: which keys have a page).
 
         The tolerances follow the arithmetic that the call states.  A weight g_t = p_t sLc_t is
-        held to 2^-9 (two e4m3 terms) plus 2^-11 (the f16 value that is split), or to 2^-17 of the
+        held to 2^-9 (two e4m3 terms) plus 3 2^-11 (half a step of f16 is eps / 2 = 2^-11: of the
+        value, of the factor between its page's reference and the row's, and of their product, which
+        is what is split; (1 + 2^-9)(1 + 2^-11)^3 - 1 < 2^-9 + 3 2^-11 + 2^-17), or to 2^-17 of the
         row's largest where the second term runs out of bits; p_t moves by the score's error, the
         query's (2^-17 of its row's largest value) and the f32 sums' (2^-19 of the sum of
         magnitudes); out is rounded to bf16: half a step, torch.finfo(torch.bfloat16).eps / 2 = 2^-8 of
@@ -97,7 +99,7 @@ class Case:
         ez = sm_scale * (2.0 ** -17 * q.abs().amax(-1)[..., None] * key.abs().sum(-1) + 2.0 ** -19 * mag)
         ez = torch.where(see, ez, 0.0).amax(-1) if T else torch.zeros((n, H), dtype=torch.float64, device=dev)
         gmax = (p * s[:, 0]).amax(-1) if T else torch.zeros((n, H), dtype=torch.float64, device=dev)
-        each = torch.maximum((2.0 ** -9 + 2.0 ** -11 + 2 * ez[..., None]) * p,
+        each = torch.maximum((2.0 ** -9 + 3 * 2.0 ** -11 + 2.0 ** -17 + 2 * ez[..., None]) * p,
                              2.0 ** -17 * gmax[..., None] / s[:, 0].clamp(min=1e-300))
         each = torch.where(see, each, 0.0)
         tol = torch.einsum("nht,td->nhd", each, key[:, :DL].abs()) + 2.0 ** -8 * out.abs() + 1e-30
