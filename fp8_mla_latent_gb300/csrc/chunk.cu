@@ -63,9 +63,9 @@
 // full), and more registers a thread, for two tiles at once, do not fit 19 warps.
 //
 // Measured, one GB300 (fractions of the bf16 rate of a large matrix product, 1895 TFLOP/s): 2 x 256
-// tokens over 65536 keys at 128 heads 5.86 ms, 1590 TFLOP/s, 0.84; a prompt of 4096 tokens 1.95 ms,
-// 1200, 0.63 (row tiles begin every 16 key tiles on average); 32 x 4 drafted tokens over up to
-// 16384 keys 0.225 ms, 1105, 0.58; one token of 4 heads over 256 keys 22 us, of which 4 are the plan,
+// tokens over 65536 keys at 128 heads 5.84 ms, 1600 TFLOP/s, 0.84; a prompt of 4096 tokens 1.96 ms,
+// 1190, 0.63 (row tiles begin every 16 key tiles on average); 32 x 4 drafted tokens over up to
+// 16384 keys 0.228 ms, 1090, 0.58; one token of 4 heads over 256 keys 22 us, of which 4 are the plan,
 // 5 the query, 5 the pipeline and 5 the results.
 //
 // Every wait is bounded (2 s): on a timeout
