@@ -432,6 +432,12 @@ def _strides(t):
 _AS_IS = contextlib.nullcontext()
 
 
+def _allocating(stream):
+    """What a call allocates for itself, while it is to run on `stream`, is that stream's memory: what
+    the current one frees may still be in use there."""
+    return torch.cuda.stream(stream) if isinstance(stream, torch.cuda.Stream) else _AS_IS
+
+
 def _on_device_of(first, *others):
     """The device of a call's tensors, made current for it (its launch, its default stream)."""
     d = first.get_device()
@@ -471,7 +477,8 @@ def mla_absorb_chunk_fp8_batch(q_lat, q_rope, kv_codes, kv_scales, block_table, 
     if seq_lens.shape[0] != B or q_start.shape[0] != B + 1:
         raise ValueError("seq_lens needs one entry per row of block_table, and q_start one more")
     if out is None:
-        out = torch.empty((rows, H, KV8_DL), dtype=torch.bfloat16, device=q_lat.device)
+        with _allocating(stream):
+            out = torch.empty((rows, H, KV8_DL), dtype=torch.bfloat16, device=q_lat.device)
     else:
         _need(out, "out", torch.bfloat16, 3)
         if out.shape != (rows, H, KV8_DL):
@@ -482,7 +489,8 @@ def mla_absorb_chunk_fp8_batch(q_lat, q_rope, kv_codes, kv_scales, block_table, 
             raise ValueError("lse must be [total_q,H]")
     need = mla_absorb_chunk_fp8_batch_workspace_size(B, H, rows, max_blocks)
     if workspace is None:
-        workspace = alloc_workspace(need, q_lat.device)
+        with _allocating(stream):
+            workspace = alloc_workspace(need, q_lat.device)
     _need_workspace(workspace)
     with _on_device_of(q_lat, q_rope, kv_codes, kv_scales, block_table, seq_lens, q_start, out, lse,
                        workspace):
@@ -515,12 +523,13 @@ def _need_err(err_word):
         raise ValueError("err_word must be a CUDA int32 tensor")
 
 
-def _moves_out(moves, n_moves, room, device):
+def _moves_out(moves, n_moves, room, device, stream):
     """The list a call writes its page moves to, and their count; allocated if None."""
-    if moves is None:
-        moves = torch.empty((max(room, 1), 2), dtype=torch.int32, device=device)
-    if n_moves is None:
-        n_moves = torch.empty(1, dtype=torch.int32, device=device)
+    with _allocating(stream):
+        if moves is None:
+            moves = torch.empty((max(room, 1), 2), dtype=torch.int32, device=device)
+        if n_moves is None:
+            n_moves = torch.empty(1, dtype=torch.int32, device=device)
     _need(moves, "moves", torch.int32, 2)
     _need(n_moves, "n_moves", torch.int32, 1)
     if moves.shape[1] != 2 or moves.shape[0] < room:
@@ -541,14 +550,16 @@ def kv8_pages_append(block_table, seq_lens, page_refs, n_new, cap=None, q_start=
     if n_new.shape[0] != B:
         raise ValueError("n_new must have one entry per sequence")
     if q_start is None:
-        q_start = torch.empty(B + 1, dtype=torch.int32, device=n_new.device)
+        with _allocating(stream):
+            q_start = torch.empty(B + 1, dtype=torch.int32, device=n_new.device)
     _need(q_start, "q_start", torch.int32, 1)
     if q_start.shape[0] != B + 1:
         raise ValueError("q_start must have one entry more than there are sequences")
     if dst_slot is None:
         if cap is None:
             raise ValueError("dst_slot or cap must be given")
-        dst_slot = torch.empty(int(cap), dtype=torch.int64, device=n_new.device)
+        with _allocating(stream):
+            dst_slot = torch.empty(int(cap), dtype=torch.int64, device=n_new.device)
     _need(dst_slot, "dst_slot", torch.int64, 1)
     with _on_device_of(block_table, seq_lens, page_refs, n_new, q_start, dst_slot, err_word):
         st = lib().kv8_pages_append(*table, _ptr(n_new), _ptr(q_start), _ptr(dst_slot),
@@ -571,7 +582,7 @@ def kv8_pages_fork(block_table, seq_lens, page_refs, src_seq, dst_seq, fork_len=
         _need(fork_len, "fork_len", torch.int32, 1)
         if fork_len.shape[0] != n:
             raise ValueError("fork_len must have one entry per entry of src_seq")
-    moves, n_moves = _moves_out(moves, n_moves, n, block_table.device)
+    moves, n_moves = _moves_out(moves, n_moves, n, block_table.device, stream)
     with _on_device_of(block_table, seq_lens, page_refs, src_seq, dst_seq, fork_len, moves, n_moves, err_word):
         st = lib().kv8_pages_fork(*table, _ptr(src_seq), _ptr(dst_seq), _ptr(fork_len), n, _ptr(moves),
                                   _ptr(n_moves), _ptr(err_word), _stream(stream))
@@ -593,7 +604,7 @@ def kv8_pages_compact(block_table, seq_lens, page_refs, moves=None, n_moves=None
     """Pack the pages in use into the front of the pool.  Returns (moves int32 [>= n_blocks // 2, 2],
     n_moves int32 [1]) for kv8_pages_copy; n_live (int32 [1], optional) takes the pages in use."""
     table = _page_table(block_table, seq_lens, page_refs, err_word)
-    moves, n_moves = _moves_out(moves, n_moves, page_refs.shape[0] // 2, block_table.device)
+    moves, n_moves = _moves_out(moves, n_moves, page_refs.shape[0] // 2, block_table.device, stream)
     if n_live is not None:
         _need(n_live, "n_live", torch.int32, 1)
         if n_live.numel() < 1:

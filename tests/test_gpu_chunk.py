@@ -297,3 +297,22 @@ def test_thousands_of_sequences():
     c.nq = [n if b in few else 0 for b, n in enumerate(nq)]
     c.check(out, l)
     assert torch.isfinite(out.float()).all() and torch.isfinite(l).all()
+
+
+def test_on_a_stream_of_its_own_while_the_current_one_is_busy():
+    """What the call allocates for itself is not memory that the current stream still reads."""
+    c = Case(64, [40], [500], seed=28)
+    want = run(c)[0]
+    s = torch.cuda.Stream()
+    for _ in range(3):
+        held = torch.full(want.shape, 3.0, dtype=torch.bfloat16, device="cuda")
+        kept = torch.empty_like(held)
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20000000)  # 10 ms or so
+        kept.copy_(held)
+        del held
+        out = pkg.mla_absorb_chunk_fp8_batch(*c.args(), SM_SCALE, stream=s)
+        s.synchronize()
+        assert torch.equal(out, want)
+        torch.cuda.synchronize()
+        assert (kept == 3.0).all()

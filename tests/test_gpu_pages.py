@@ -501,3 +501,30 @@ def test_calls_with_nothing_to_do():
     e = Dev(Pool(3, 4, 9))
     assert e.compact() == ([], 0)
     e.same(Pool(3, 4, 9))
+
+
+def test_on_a_stream_of_its_own_while_the_current_one_is_busy():
+    """What a call allocates for itself is not memory that the current stream still reads."""
+    p = Pool(3, 40, 100)
+    p.append([70, 0, 3], 73)
+    s = torch.cuda.Stream()
+    for cap in (5000, 70000):
+        want = p.copy()
+        moves, _ = want.fork([0], [1])
+        q_want, s_want, _ = want.append([0, 5, 0], cap)
+        d = Dev(p)
+        src, dst, n_new = i32([0]), i32([1]), i32([0, 5, 0])
+        held = [torch.full((n,), 3, dtype=t, device="cuda") for n, t in ((cap, torch.int64), (4, torch.int32),
+                                                                         (2, torch.int32), (1, torch.int32))]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20000000)  # 10 ms or so
+        kept = [h.clone() for h in held]
+        del held
+        m, n = pkg.kv8_pages_fork(*d.state(), src, dst, err_word=d.err, stream=s)
+        q, slots = pkg.kv8_pages_append(*d.state(), n_new, cap=cap, err_word=d.err, stream=s)
+        s.synchronize()
+        torch.cuda.synchronize()
+        assert [tuple(r) for r in m[: int(n[0])].tolist()] == moves
+        assert np.array_equal(q.cpu().numpy(), q_want) and np.array_equal(slots.cpu().numpy(), s_want)
+        assert all((k == 3).all() for k in kept)
+        d.same(want)
