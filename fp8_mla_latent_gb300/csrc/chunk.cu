@@ -117,7 +117,8 @@ constexpr float TAU = 1.0f;
 constexpr float P_LOG = 7.0f;                // g' <= 2^(TAU + P_LOG) = 256 <= 448
 constexpr float DOWN = 10.0f;
 // bounds that keep p and l in range, 2^(P_LOG + TAU + 40 + 50) times a count of keys: the smallest
-// log2 of a row scale that sets a reference, and how far a row's reference may come down in all
+// log2 of a row scale that sets a reference, and how far below its highest value so far a row's
+// reference may come (l and O hold no more than 2^(highest - reference) times what they did there)
 constexpr float LG_MIN = -40.0f, DOWN_CAP = 50.0f;
 constexpr uint64_t WAIT_NS = 2000000000ull;
 constexpr float LOG2E = 1.4426950408889634f;
@@ -798,7 +799,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
         const int n_tiles = x.n;
         uint64_t c2[2];                       // the rows' c, twice
         float l[2] = {0.f, 0.f};              // this thread's tokens, of its two rows
-        float mg = -INFINITY, lift = 0.f;     // row `mh`: its reference, and how far that came down in all
+        float mg = -INFINITY, mhi = -INFINITY;  // row `mh`: its reference, and the highest one so far
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
           const float v = cs[rh + 8 * p];
@@ -883,12 +884,12 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
           float mn = mg;
           if (ym > mg + TAU) {
             mn = ym;
-          } else if (ym < mg - DOWN && mg - ym + lift <= DOWN_CAP) {
-            lift += mg - ym;
+          } else if (ym < mg - DOWN && ym >= mhi - DOWN_CAP) {
             mn = ym;
           }
           const float f = mn == mg ? 1.f : (mg > -INFINITY ? ex2_approx(mg - mn) : 0.f);
           mg = mn;
+          mhi = fmaxf(mhi, mn);
           if (__any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll
             for (int p = 0; p < 2; ++p) l[p] *= __shfl_sync(0xffffffffu, f, (lane & 28) + p);
@@ -1092,7 +1093,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
       bool ok = true;
       for (; ok && w.more(); w.next(a)) {
         const int lim0 = limit_of(a, w.s, (int)((uint32_t)(w.rt * ROWS) / (uint32_t)a.H));  // the tile's first row sees least
-        float ref = -INFINITY, down = 0.f;  // the row's reference in O, and how far it came down in all
+        float ref = -INFINITY, hi = -INFINITY;  // the row's reference in O, and the highest one so far
         for (int i = 0; i < w.n; ++i) {
           const int g = gt + i, pb = g & 1, vs = g % NVT;
           if (!wait_cluster(B_PFULL + pb, (uint32_t)(g >> 1))) {
@@ -1123,10 +1124,10 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
           const float top = fmaxf(m0, m1), own = part < 2 ? m0 : m1, was = ref;
           if (top > ref) {
             ref = top;
-          } else if (top < ref - DOWN && ref - top + down <= DOWN_CAP) {
-            down += ref - top;
+          } else if (top < ref - DOWN && top >= hi - DOWN_CAP) {
             ref = top;
           }
+          hi = fmaxf(hi, ref);
           const float f = ref == was ? 1.f : (was > -INFINITY ? ex2_approx(was - ref) : 0.f);
           const bool any = __any_sync(0xffffffffu, f != 1.f) && i > 0;
           const __half2 onto = __float2half2_rn(own == ref ? 1.f : ex2_approx(own - ref));
