@@ -1300,10 +1300,11 @@ __global__ void __launch_bounds__(256) join_kernel(const ChunkArgs a, const Work
   const int k = (int)blockIdx.x / (JOIN_BLOCKS * SPLIT) + 1, lane = threadIdx.x & 31;
   const int row = (int)blockIdx.x % (JOIN_BLOCKS * SPLIT) / SPLIT * 8 + (threadIdx.x >> 5);
   const int ch = (int)blockIdx.x % SPLIT * (DL / SPLIT);
-  // (the plan was there before the first cluster began: it is read while the last ones work; a block
-  // without a row waits as well, so that this launch is not over before the chunk kernel is)
+  // (every block waits, with a row or without: the plan's and the parts' visibility, and that this
+  // launch is not over before the chunk kernel is, come with the wait)
+  grid_dependency_wait();
   const int64_t nc = ws.plan->n_clusters;
-  if (k >= nc) return grid_dependency_wait();
+  if (k >= nc) return;
   __shared__ int64_t xs[MAX_CLUSTERS + 1];    // the units where the ranges begin
   if (threadIdx.x <= nc) xs[threadIdx.x] = threadIdx.x < nc ? ws.plan->e[threadIdx.x].x : ws.plan->units;
   const PlanEntry e = ws.plan->e[k];
@@ -1319,7 +1320,6 @@ __global__ void __launch_bounds__(256) join_kernel(const ChunkArgs a, const Work
   };
   int last = k;
   while (last + 1 < nc && xs[last + 1] < S + e.nt) ++last;
-  grid_dependency_wait();
   if (!mine) return;
   // a lane per part: its reference, its sum (a cluster without units has no part); at most
   // MAX_CLUSTERS of them, so two each
