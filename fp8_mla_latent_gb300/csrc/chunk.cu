@@ -124,22 +124,29 @@ constexpr uint64_t WAIT_NS = 2000000000ull;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 
-// mbarriers (the same offsets in all four CTAs: commits are multicast)
+// mbarriers (the same offsets in all four CTAs: commits are multicast).  What passes between CTAs is
+// ordered at cluster scope.  Shared memory that one CTA's warps wrote or read, and that another CTA's
+// stores overwrite or whose MMAs read it: the warps arrive at their own CTA's barrier, and a warp
+// that has nothing else to do waits there and arrives at the other CTA's (the relays).  TMEM alone:
+// a relaxed arrival between the fences of tcgen05.  Releases at cluster scope by the sixteen warps
+// themselves make drafts 15 % slower where it is the payloads' buffers alone and 45 % with the operands,
+// relays of the S buffers and the O halves as well 19 %; this 2 %.
 constexpr int B_KFULL = 0;                   // [2 NK] rank 0: both CTAs' halves of a K half tile loaded
 constexpr int B_KEMPTY = B_KFULL + 2 * NK;   // [2 NK] ranks 0, 1: consumed
 constexpr int B_SCFULL = B_KEMPTY + 2 * NK;  // [NSC] score: row scales of a tile loaded
 constexpr int B_SFULL = B_SCFULL + NSC;      // [2] score: S of a tile in TMEM (commit); its scales prepared, and
                                              // its payload buffer free (the scale warp)
 constexpr int B_SEMPTY = B_SFULL + 2;        // [2] rank 0: S read (16 warps x 2 CTAs)
-constexpr int B_QREADY = B_SEMPTY + 2;       // rank 0: the row tile's query in place (16 warps x 2)
+constexpr int B_QREADY = B_SEMPTY + 2;       // score: the row tile's query in place (16 warps; in rank 0 also rank 1's relay)
 constexpr int B_PX = B_QREADY + 1;           // [4] score: the four warps of a lane quarter meet
-constexpr int B_PFREE = B_PX + 4;            // [2] score: payload buffer read (the partner's 16 warps)
+constexpr int B_PFREE = B_PX + 4;            // [2] context: payload buffer read (16 warps); score: the partner's relay of it
 constexpr int B_PFULL = B_PFREE + 2;         // [2] context: payload arrived
 constexpr int B_VT = B_PFULL + 2;            // [NVT] context: V tile loaded
 constexpr int B_VEMPTY = B_VT + NVT;         // [NVT] ranks 2, 3: consumed
 constexpr int B_EP = B_VEMPTY + NVT;         // context: a row tile's results have left shared memory
-constexpr int B_VR = B_EP + 1;               // [NVT] rank 2: rank 3's V tile loaded
-constexpr int B_RS = B_VR + NVT;             // [2 buffers][2] rank 2: operand, and O half ready (16 warps x 2)
+constexpr int B_OP = B_EP + 1;               // [2] context: operand of a tile written (16 warps; in rank 2 also rank 3's
+                                             // relay, when its V tile is loaded as well)
+constexpr int B_RS = B_OP + 2;               // [2 buffers][2] rank 2: O half ready (16 warps x 2 CTAs)
 constexpr int B_ODONE = B_RS + 4;            // [2 buffers][2] ranks 2, 3: a tile's MMAs of an O half done
 constexpr int NRF = 4;
 constexpr int B_RF = B_ODONE + 4;            // [NRF] context: row factors of a finished row tile arrived
@@ -471,14 +478,26 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
     return mbar_wait_cluster_warp(&bars[bar], parity & 1, abort_flag, WAIT_NS);
   };
 
+  // what this CTA's warps have done, told to another CTA (by a whole converged warp)
+  auto relay = [&](int bar, uint32_t parity, uint32_t to) -> bool {
+    if (!wait(bar, parity)) return false;
+    tc_fence_after();
+    tc_fence_before();
+    if (lane == 0) arrive_cluster(to);
+    __syncwarp();
+    return true;
+  };
+
   if (threadIdx.x == 0) {
     for (int i = 0; i < NBAR; ++i) mbar_init(&bars[i], 1);
+    const int here = N_LANE_WARPS + (rank == 0 || rank == 2);  // (and the relay of the pair's other CTA)
     for (int i = 0; i < 2; ++i) mbar_init(&bars[B_SEMPTY + i], 2 * N_LANE_WARPS);
-    mbar_init(&bars[B_QREADY], 2 * N_LANE_WARPS);
+    mbar_init(&bars[B_QREADY], here);
     for (int i = 0; i < 4; ++i) mbar_init(&bars[B_PX + i], N_LANE_WARPS / 4);
     mbar_init(&bars[B_EP], N_LANE_WARPS);
-    for (int i = 0; i < 2; ++i) mbar_init(&bars[B_PFREE + i], N_LANE_WARPS);
+    for (int i = 0; i < 2; ++i) mbar_init(&bars[B_PFREE + i], rank < 2 ? 1 : N_LANE_WARPS);
     for (int i = 0; i < 4; ++i) mbar_init(&bars[B_RS + i], 2 * N_LANE_WARPS);
+    for (int i = 0; i < 2; ++i) mbar_init(&bars[B_OP + i], here);
     for (int i = 0; i < 2; ++i) mbar_init(&bars[B_SFULL + i], 2);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -588,6 +607,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
             ok = false;
             break;
           }
+          // (what the softmax warps read there for tile g - 5 is in that tile's payload, and this warp
+          // has waited until payload g - 3 was received and read: B_PFREE below)
           float4* pl = reinterpret_cast<float4*>(sm + OFF_PL + sc * PL_BYTES);
           float2* lg = reinterpret_cast<float2*>(pl + 64);
 #pragma unroll
@@ -599,7 +620,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
           }
           // (the payload buffer of tile g: the context warps have read tile g - 2, and so the softmax
           // warps were through with its S)
-          if (g >= 2 && !wait(B_PFREE + (g & 1), (uint32_t)((g >> 1) - 1))) {
+          if (g >= 2 && !wait_cluster(B_PFREE + (g & 1), (uint32_t)((g >> 1) - 1))) {
             ok = false;
             break;
           }
@@ -665,6 +686,12 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
         }
         if (!ok && lane == 0) fail();
         mma_commit_pair_warp(&bars[B_DRAIN], 3);
+      } else {
+        // rank 1 tells the MMA's issuer of its query
+        const uint32_t qready = map_to(smem_u32(&bars[B_QREADY]), 0);
+        bool ok = true;
+        for (; ok && w.more(); w.next(a)) ok = relay(B_QREADY, (uint32_t)w.seg, qready);
+        if (!ok && lane == 0) fail();
       }
       // every MMA of the pair is done and its commits have landed here
       const int zero = 0;
@@ -785,7 +812,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_cluster_local(map_to(smem_u32(&bars[B_QREADY]), 0));
+        if (lane == 0) mbar_arrive(&bars[B_QREADY]);
         return true;
       };
 
@@ -832,7 +859,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
               if (jh == 1) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) arrive_cluster_local(map_to(smem_u32(&bars[B_SEMPTY + buf]), 0));
+                if (lane == 0) arrive_cluster_relaxed(map_to(smem_u32(&bars[B_SEMPTY + buf]), 0));
               }
 #pragma unroll
               for (int j4 = 0; j4 < 4; ++j4) {
@@ -1030,7 +1057,14 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
       }
       __syncwarp();
     } else if (warp == W_SCALE) {
-      // (no scales here)
+      // (no scales here: this warp tells the score CTA which payloads are read, so that its writes of
+      // the next ones come after those reads)
+      const uint32_t pfree = map_to(smem_u32(&bars[B_PFREE]), rank - 2);
+      bool ok = true;
+      for (int64_t g = 0; ok && g < w.left; ++g)
+        ok = relay(B_PFREE + (int)(g & 1), (uint32_t)(g >> 1), pfree + (int)(g & 1) * 8);
+      if (!ok && lane == 0) fail();
+      __syncwarp();
     } else if (warp == W_MMA) {
       if (rank == 2) {
         const uint32_t id = idesc_f16(ROWS, 256, false, true);  // A K-major, B = V MN-major
@@ -1041,7 +1075,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
           for (int i = 0; ok && i < w.n; ++i) {
             const int g = gt + i;
             const uint64_t ad = pd + (uint64_t)((g & 1) * 2 * OP_ATOM >> 4);
-            if (!wait(B_VT + g % NVT, (uint32_t)(g / NVT)) || !wait_cluster(B_VR + g % NVT, (uint32_t)(g / NVT))) {
+            if (!wait(B_VT + g % NVT, (uint32_t)(g / NVT)) || !wait_cluster(B_OP + (g & 1), (uint32_t)(g >> 1))) {
               ok = false;
               break;
             }
@@ -1069,13 +1103,12 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
         if (!ok && lane == 0) fail();
         mma_commit_pair_warp(&bars[B_DRAIN], 0xC);
       } else {
-        // rank 3 tells the MMA's issuer of its V tiles
-        const uint32_t vr = map_to(smem_u32(&bars[B_VR]), 2);
+        // rank 3 tells the MMA's issuer of its V tiles and operands
+        const uint32_t op = map_to(smem_u32(&bars[B_OP]), 2);
         bool ok = true;
         for (int64_t g = 0; ok && g < w.left; ++g) {
           ok = wait(B_VT + (int)(g % NVT), (uint32_t)(g / NVT));
-          if (ok && lane == 0) arrive_cluster_local(vr + (int)(g % NVT) * 8);
-          __syncwarp();
+          ok = ok && relay(B_OP + (int)(g & 1), (uint32_t)(g >> 1), op + (int)(g & 1) * 8);
         }
         if (!ok && lane == 0) fail();
       }
@@ -1089,7 +1122,6 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
       const int hh = q * 32 + lane;
       const uint32_t lane_addr = (uint32_t)(q * 32) << 16;
       const uint32_t rs = map_to(smem_u32(&bars[B_RS]), 2);
-      const uint32_t pfree = map_to(smem_u32(&bars[B_PFREE]), rank - 2);
       bool ok = true;
       for (; ok && w.more(); w.next(a)) {
         const int lim0 = limit_of(a, w.s, (int)((uint32_t)(w.rt * ROWS) / (uint32_t)a.H));  // the tile's first row sees least
@@ -1117,7 +1149,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
           __syncwarp();
           if (lane == 0) {
             if (warp == W_LANE) mbar_arrive_expect_tx(&bars[B_PFULL + pb], P_BYTES);
-            arrive_cluster_local(pfree + pb * 8);
+            mbar_arrive(&bars[B_PFREE + pb]);
           }
           // O's reference is the larger of the pages', or above both: the factor of what was added up
           // before, and the one that brings this warp's page onto it
@@ -1167,6 +1199,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
             }
           }
           fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[B_OP + pb]);
           // rows whose reference moved are rescaled: one half of O after the other, each when the
           // previous tile's MMAs on it are done (the first half while those on the second run)
 #pragma unroll 1
@@ -1193,7 +1227,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
               tc_fence_before();
               __syncwarp();
             }
-            if (lane == 0) arrive_cluster_local(rs + (2 * pb + h) * 8);
+            if (lane == 0) arrive_cluster_relaxed(rs + (2 * pb + h) * 8);
           }
           if (!ok) break;
         }
@@ -1259,6 +1293,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
             flush(col * 4);
           }
         }
+        tc_fence_before();  // (the loads from O, before the next row tile's MMAs)
         // the factor buffer's next phase, NRF segments on (its bytes come after the payloads of
         // the tiles between, which every warp has to read); and the operand buffers may be
         // written again when every warp's results have left them

@@ -513,11 +513,11 @@ __device__ __forceinline__ void arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
 }
-// the same, for writes that only this SM reads (its tensor core, when an MMA that the other CTA
-// issues gets to them): ordered at CTA scope.  At cluster scope the arrive waits about a
-// thousand cycles for every store of the thread, its asynchronous remote ones among them.
-__device__ __forceinline__ void arrive_cluster_local(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+// The same for tcgen05 accesses alone (waited for, and between tc_fence_before and the waiter's
+// tc_fence_after): nothing else is released.  A release at cluster scope waits for every
+// store of the thread, its asynchronous remote ones among them, about a thousand cycles.
+__device__ __forceinline__ void arrive_cluster_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
 }
 __device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {

@@ -29,3 +29,23 @@ def test_nothing_of_an_earlier_kernel_is_read_before_the_wait_for_it(kernel):
     before = b[b.index("{"): b.index("grid_dependency_wait()")]
     assert "ws." not in before and "a.out" not in before
     assert kernel != "join_kernel" or "return" not in before, "a block that leaves without the wait"
+
+
+def test_what_another_cta_has_to_see_is_released_and_acquired_at_cluster_scope():
+    """A CTA's payload, query, operand and accumulator buffers are read and written by its own warps
+    and, at the word of another CTA, by that CTA's stores or MMAs: a barrier of another CTA is arrived
+    at, and waited for, at cluster scope."""
+    assert "release.cta.shared::cluster" not in source("tc_ptx.cuh")
+    b = body(source("chunk.cu"), "chunk_kernel")
+    assert "arrive_cluster_local" not in b
+    # shared memory: a relay of the other CTA arrives, released at cluster scope
+    for bar in ("B_QREADY", "B_PFREE", "B_OP"):
+        waits = set(re.findall(r"\b(wait\w*|relay)\(%s" % bar, b))
+        assert waits == {"wait_cluster", "relay"}, (bar, waits)
+    relay = b[b.index("auto relay"):]
+    assert "arrive_cluster(to)" in relay[: relay.index("};")]
+    # TMEM alone: the warps arrive themselves, behind the wait for their accesses and the fence
+    for bar in ("B_SEMPTY", "B_RS"):
+        assert set(re.findall(r"\b(wait\w*)\(%s" % bar, b)) == {"wait_cluster"}, bar
+    for at in [m.start() for m in re.finditer(r"arrive_cluster_relaxed\(", b)]:
+        assert "tc_fence_before();" in b[at - 300: at]

@@ -89,3 +89,22 @@ def test_a_bulk_under_rows_of_far_larger_scale():
     c.q_lat *= 0.1
     c.q_lat[..., 0] = 0
     check_some(c, peaks, skip=1)
+
+
+@pytest.mark.parametrize("H,nq,T", [(128, 40, 3000), (16, 300, 9000), (128, 4, 30000)])
+def test_same_bits_in_many_runs_with_other_work_between(H, nq, T):
+    """Buffers that pass between the SMs of a cluster are overwritten only behind their reads: a
+    value that came too early would show as another result now and then."""
+    c = Case(H, [nq, 1], [T, 77], seed=33)
+    want, want_l = run(c)
+    ws = pkg.alloc_workspace(pkg.mla_absorb_chunk_fp8_batch_workspace_size(2, H, nq + 1, c.max_blocks))
+    out, lse = torch.empty_like(want), torch.empty_like(want_l)
+    noise, side = torch.randn((4096, 4096), device="cuda"), torch.cuda.Stream()
+    for i in range(40):
+        if i % 2:
+            with torch.cuda.stream(side):
+                noise.mul_(1.0001)
+        out.fill_(float("nan"))
+        pkg.mla_absorb_chunk_fp8_batch(*c.args(), SM_SCALE, out=out, lse=lse, workspace=ws)
+        assert torch.equal(out, want) and torch.equal(lse, want_l)
+    torch.cuda.synchronize()
