@@ -463,12 +463,28 @@ compact_kernel(PageTable t, int32_t* moves, int32_t* n_moves, int32_t* n_live, u
       n += __popc(m);
     }
   }
+  // a length that cannot be (which entries the sequence holds is not known then) makes the call do
+  // nothing: a CTA that meets one says so above its count of live pages
+  constexpr int64_t BAD = int64_t(1) << 40;
+  for (int b = rank * PG_THREADS + threadIdx.x; b < t.B; b += nc * PG_THREADS) {
+    const int64_t len = t.seq_lens[b];
+    if (len < 0 || len > (int64_t)t.max_blocks * PAGE) n += BAD;
+  }
   int64_t sum;
   (void)cta_scan(n, tmp, &sum);
   if (threadIdx.x == 0) count[0] = sum;
   all_ctas_sync();
   int64_t L = 0;
   for (int r = 0; r < nc; ++r) L += count_of(0, r);
+  if (L >= BAD) {
+    if (rank == 0 && threadIdx.x == 0) {
+      flag(err, KV8_PAGES_EINDEX);
+      n_moves[0] = 0;
+      if (n_live != nullptr) n_live[0] = (int32_t)t.n_blocks;
+    }
+    all_ctas_sync();  // this CTA's count is read no more
+    return;
+  }
   // of word w: the pages below L without an owner, and those from L on that have one
   auto low = [&](int w) -> uint32_t {
     const int64_t d = L - lo - 32 * (int64_t)w;
@@ -520,14 +536,8 @@ compact_kernel(PageTable t, int32_t* moves, int32_t* n_moves, int32_t* n_live, u
   for (int64_t e = me; e < entries; e += all) {
     const int b = (int)(e / t.max_blocks);
     const int32_t p = t.block_table[e];
-    int64_t len = t.seq_lens[b];
-    const bool off = len < 0 || len > (int64_t)t.max_blocks * PAGE;
-    if (off) len = len < 0 ? 0 : (int64_t)t.max_blocks * PAGE;
-    if (e - (int64_t)b * t.max_blocks >= pages_of(len)) {
-      if (off) flag(err, KV8_PAGES_EINDEX);
-      continue;
-    }
-    if (off || p < 0 || p >= t.n_blocks) {
+    if (e - (int64_t)b * t.max_blocks >= pages_of(t.seq_lens[b])) continue;
+    if (p < 0 || p >= t.n_blocks) {
       flag(err, KV8_PAGES_EINDEX);
       continue;
     }

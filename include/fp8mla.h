@@ -455,8 +455,9 @@ int kv8_pages_free(int32_t* block_table, int32_t* seq_lens, int32_t* page_refs, 
  *            ascending order, for kv8_pages_copy; *n_moves their number, *n_live
  *            (or NULL) L.  Pairs behind *n_moves are left as they were.
  * Afterwards pages [0, L) are in use and the rest is free.  A held entry that names
- * no page in use stays as it is and sets the error word.  Errors: KV8_EINVAL,
- * KV8_EALIGN, KV8_EUNSUPPORTED, KV8_ECUDA. */
+ * no page in use stays as it is and sets the error word.  A bad seq_len makes the call
+ * do nothing but set the error word: *n_moves = 0, and *n_live = n_blocks.  Errors:
+ * KV8_EINVAL, KV8_EALIGN, KV8_EUNSUPPORTED, KV8_ECUDA. */
 int kv8_pages_compact(int32_t* block_table, const int32_t* seq_lens, int32_t* page_refs, int B,
                       int max_blocks, int64_t n_blocks, int32_t* moves, int32_t* n_moves,
                       int32_t* n_live, unsigned* err_word, void* stream);
