@@ -12,8 +12,9 @@
 //
 // The table steps are one launch each of one thread-block cluster, at most
 // PG_CTAS CTAs of 1024 threads: a step is a validation that must be complete
-// before anything is written (all or nothing), a ranking of the free pages, and a
-// walk over table entries; the cluster barrier separates them without a second
+// before anything is written (lists, lengths and room: all or nothing; a held entry
+// that names no page is met in the walk, and reported), a ranking of the free pages,
+// and a walk over table entries; the cluster barrier separates them without a second
 // launch, and what they read (a few hundred KB at most) bounds nothing: they are
 // launch latency (3 us) and dependent L2 round trips (about 1 us each), so the work
 // on them is to have fewer in a row.  A CTA count of one is kept while the entries to
@@ -383,8 +384,9 @@ fork_kernel(PageTable t, const int32_t* __restrict__ src, const int32_t* __restr
 }
 
 // ------------------------------------------------------------------ free
-// Every CTA validates the list by itself (it reads nothing that the call writes);
-// then a warp per sequence gives its pages back, over all CTAs.
+// Every CTA validates the list and its sequences' lengths by itself; then a warp per
+// sequence gives its pages back, over all CTAs.  (A CTA that is behind may read the 0 that
+// another one has put in a length's place: that one has found every length good.)
 __global__ void __launch_bounds__(PG_THREADS)
 free_kernel(PageTable t, const int32_t* __restrict__ seq, int n, unsigned* err) {
   extern __shared__ unsigned role[];  // [B]
@@ -395,7 +397,12 @@ free_kernel(PageTable t, const int32_t* __restrict__ seq, int n, unsigned* err) 
   __syncthreads();
   for (int i = threadIdx.x; i < n; i += PG_THREADS) {
     const int32_t b = seq[i];
-    if (b < 0 || b >= B || atomicOr(&role[b], 1u) != 0u) atomicOr(&bad, KV8_PAGES_EINDEX);
+    if (b < 0 || b >= B || atomicOr(&role[b], 1u) != 0u) {
+      atomicOr(&bad, KV8_PAGES_EINDEX);
+    } else {
+      const int64_t len = t.seq_lens[b];
+      if (len < 0 || len > (int64_t)t.max_blocks * PAGE) atomicOr(&bad, KV8_PAGES_EINDEX);
+    }
   }
   __syncthreads();
   if (bad != 0) {
@@ -405,11 +412,7 @@ free_kernel(PageTable t, const int32_t* __restrict__ seq, int n, unsigned* err) 
   const int warps = (int)cluster_ctas() * PG_WARPS;
   for (int i = (int)cluster_rank() * PG_WARPS + (threadIdx.x >> 5); i < n; i += warps) {
     const int b = seq[i];
-    int64_t len = t.seq_lens[b];
-    if (len < 0 || len > (int64_t)t.max_blocks * PAGE) {
-      if (lane == 0) flag(err, KV8_PAGES_EINDEX);
-      len = len < 0 ? 0 : (int64_t)t.max_blocks * PAGE;
-    }
+    const int64_t len = t.seq_lens[b];
     int32_t* row = t.block_table + (int64_t)b * t.max_blocks;
     for (int c = lane; c < pages_of(len); c += 32) {
       const int32_t p = row[c];

@@ -440,8 +440,8 @@ int kv8_pages_fork(int32_t* block_table, int32_t* seq_lens, int32_t* page_refs, 
 
 /* kv8_pages_free -- empties the sequences seq[0 .. n - 1]: gives their pages back
  * (one count each), sets their entries to -1 and their seq_lens to 0.  A sequence
- * that is out of range or named twice makes the call do nothing but set the error
- * word.  A held entry that names no page, or a page whose count is 0 already, sets
+ * that is out of range, named twice or of a bad seq_len makes the call do nothing but
+ * set the error word.  A held entry that names no page, or a page whose count is 0 already, sets
  * the error word and changes no count.  0 <= n <= KV8_PAGES_MAX_SEQS.  Errors:
  * KV8_EINVAL, KV8_EALIGN, KV8_EUNSUPPORTED, KV8_ECUDA. */
 int kv8_pages_free(int32_t* block_table, int32_t* seq_lens, int32_t* page_refs, int B,

@@ -36,3 +36,22 @@ def test_compact_with_a_bad_length_changes_nothing(B, n_blocks, length):
         want = p.copy()
         assert d.compact() == want.compact()
         d.same(want)
+
+
+@pytest.mark.parametrize("length", [-1, 4 * 64 + 1, 2 ** 31 - 1, -2 ** 31])
+@pytest.mark.parametrize("B", [4, 3000])  # (one CTA, and a cluster)
+def test_free_with_a_bad_length_changes_nothing(B, length):
+    """A row's entries behind the held ones may say anything, another sequence's pages among them:
+    with a length that cannot be, none of them is given back, nor any other sequence of the list."""
+    p = pool(B, 4, B + 60)
+    p.table[2, 1:] = p.table[1, :3]  # (left from an earlier use of the row)
+    q = p.copy()
+    q.lens[2] = length
+    everyone = list(range(B))
+    for seq in ([2], [1, 2, 3], everyone):
+        d = Dev(q)
+        d.free(seq)
+        d.same(q, 1)
+    d = Dev(p)
+    d.free(everyone)
+    assert int(d.err[0]) == 0 and not d.refs.any() and not d.lens.any()
