@@ -364,12 +364,15 @@ int kv8_noalloc_error(void* stream);
  *               overlap in time (two replayed graphs among them).  Its error word is
  *               read with kv8_workspace_error().
  * Precision: a bf16 query value is held as two e4m3 terms, exactly where it is at
- * least 2^-9 of its row's largest; each softmax weight, times its key's sLc, as two
- * e4m3 terms of an f16 value (relative error <= 2^-9 + 3 * 2^-11, or 2^-17 of the
- * row's largest such product if that is more; an sLc under 2^-40 counts as 2^-40 in
- * that comparison); sums, maxima and denominators in f32; out rounded to bf16 once.
- * lse within 2e-5 of its size or of 1.  A query row with a NaN or an infinity gives
- * NaN, unless it sees nothing.
+ * least 2^-9 of its row's largest (of all 576), to 2^-17 of that elsewhere, and sums are
+ * f32, so that a row's score of key t is off by at most
+ *   E_t = sm_scale (2^-17 max_c |q_c| sum_c |key_tc| + 2^-19 sum_c |q_c key_tc|),
+ *   key_t = (sLc_t dec Lc_t, sRc_t dec Rc_t);
+ * lse by the largest E_t that the row sees and 2e-5 of lse's size or of 1.  A softmax
+ * weight moves by 2 E of itself; times its key's sLc it is held as two e4m3 terms of an
+ * f16 value (relative error <= 2^-9 + 3 * 2^-11, or 2^-17 of the row's largest such
+ * product if that is more; an sLc under 2^-40 counts as 2^-40 in that comparison);
+ * maxima and denominators are f32; out is rounded to bf16 once.  A query row with a NaN or an infinity gives NaN, unless it sees nothing.
  * Errors: KV8_EINVAL, KV8_EALIGN, KV8_EUNSUPPORTED, KV8_EWORKSPACE, KV8_ECUDA.
  * ------------------------------------------------------------------------- */
 int64_t mla_absorb_chunk_fp8_batch_workspace_size(int B, int H, int64_t total_q, int max_blocks);

@@ -108,3 +108,17 @@ def test_same_bits_in_many_runs_with_other_work_between(H, nq, T):
         pkg.mla_absorb_chunk_fp8_batch(*c.args(), SM_SCALE, out=out, lse=lse, workspace=ws)
         assert torch.equal(out, want) and torch.equal(lse, want_l)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("times", [64, 256, 512])
+@pytest.mark.parametrize("part", ["rope", "latent"])
+def test_queries_with_an_outlying_channel(part, times):
+    """One channel of the query far above the others, which the two terms of its row's scale then
+    hold to 2^-17 of it.  out and lse keep the call's stated bounds: a score is off by
+    sm_scale (2^-17 max |q| sum |key| + 2^-19 sum |q key|) at most, lse by the largest of these and
+    2e-5 of its size or of 1 (Case.reference has both, and what follows for out).  (2e-5 alone does
+    not hold: at 64, 256 and 512 times lse was off by 2.8e-5, 7.1e-5 and 1.2e-4.)"""
+    c = Case(16, [9, 40], [300, 1000], seed=34 + times)
+    (c.q_rope if part == "rope" else c.q_lat)[..., 17] *= times
+    out, lse = run(c)
+    c.check(out, lse)
