@@ -371,7 +371,9 @@ int kv8_noalloc_error(void* stream);
  * lse by the largest E_t that the row sees and 2e-5 of lse's size or of 1.  A softmax
  * weight moves by 2 E of itself; times its key's sLc it is held as two e4m3 terms of an
  * f16 value (relative error <= 2^-9 + 3 * 2^-11, or 2^-17 of the row's largest such
- * product if that is more; an sLc under 2^-40 counts as 2^-40 in that comparison);
+ * product if that is more, but no more than 2^-7 of the largest in its tile of 128
+ * keys, as long as that is over 2^-50 of the row's; an sLc under 2^-40 counts as 2^-40
+ * in these comparisons, and one under 0, which no call here writes, as 0 throughout);
  * maxima and denominators are f32; out is rounded to bf16 once.  A query row with a NaN or an infinity gives NaN, unless it sees nothing.
  * Errors: KV8_EINVAL, KV8_EALIGN, KV8_EUNSUPPORTED, KV8_EWORKSPACE, KV8_ECUDA.
  * ------------------------------------------------------------------------- */

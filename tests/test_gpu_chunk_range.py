@@ -122,3 +122,30 @@ def test_queries_with_an_outlying_channel(part, times):
     (c.q_rope if part == "rope" else c.q_lat)[..., 17] *= times
     out, lse = run(c)
     c.check(out, lse)
+
+
+def test_a_negative_latent_scale_counts_as_none():
+    """No call writes one: the row scale is a largest magnitude."""
+    c = Case(16, [9, 3], [300, 200], seed=35)
+    for b in (0, 1):
+        slot = c.slots[b][::7].cuda()
+        c.scales[slot, 0] = -c.scales[slot, 0]
+    out, lse = run(c)
+    c.scales[:, 0] = torch.where(c.scales[:, 0] < 0, 0.0, c.scales[:, 0])
+    want, want_l = run(c)
+    assert torch.equal(out, want) and torch.equal(lse, want_l)
+    c.check(want, want_l)
+
+
+@pytest.mark.parametrize("H,nq,lens", [(128, [4, 9, 1], [3000, 700, 5000]), (16, [1, 0, 3], [90, 5, 400])])
+def test_same_bits_with_a_wider_table(H, nq, lens):
+    """Columns that no sequence holds change the workspace and the launch, not the result."""
+    c = Case(H, nq, lens, seed=36)
+    want, want_l = run(c)
+    for wide in (c.max_blocks + 1, 300, 5000):
+        table = torch.full((len(nq), wide), -1, dtype=torch.int32, device="cuda")
+        table[:, : c.max_blocks] = c.table
+        d = Case(H, nq, lens, seed=36)
+        d.table, d.max_blocks = table, wide
+        out, lse = run(d)
+        assert torch.equal(out, want) and torch.equal(lse, want_l)
