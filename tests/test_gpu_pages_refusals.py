@@ -1,9 +1,11 @@
-"""Page calls on a table whose lengths cannot be: compact and free change nothing."""
+"""Page calls on a table whose lengths cannot be: compact and free change nothing.  And a captured
+serving step against an eager one."""
 import numpy as np
 import pytest
 import torch
 
 import fp8_mla_latent_gb300 as pkg
+from chunk_helpers import D, DL, DR, SM_SCALE
 from pages_ref import Pool
 from test_gpu_pages import Dev
 
@@ -55,3 +57,54 @@ def test_free_with_a_bad_length_changes_nothing(B, length):
     d = Dev(p)
     d.free(everyone)
     assert int(d.err[0]) == 0 and not d.refs.any() and not d.lens.any()
+
+
+def test_a_captured_step_gives_what_an_eager_one_gives():
+    """append, quantize, attention in one graph; after every replay the new rows of every sequence lie in
+    its slots, and the attention is that of an eager call on the same state, bit for bit."""
+    H, mb, nb, B = 16, 4, 12, 3
+    p = Pool(B, mb, nb)
+    p.append([63, 10, 64], 137)
+    d = Dev(p)
+    g = torch.Generator(device="cuda").manual_seed(6)
+    codes = torch.randint(0, 0x7F, (nb * 64, D), dtype=torch.uint8, device="cuda", generator=g)
+    scales = 0.002 + 0.003 * torch.rand((nb * 64, 2), device="cuda", generator=g)
+    rows = torch.randn((B, D), device="cuda", generator=g)
+    n_new = torch.ones(B, dtype=torch.int32, device="cuda")
+    q_start = torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+    slots = torch.zeros(B, dtype=torch.int64, device="cuda")
+    ql = torch.randn((B, H, DL), device="cuda", generator=g).bfloat16()
+    qr = torch.randn((B, H, DR), device="cuda", generator=g).bfloat16()
+    out = torch.empty((B, H, DL), dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty((B, H), device="cuda")
+    ws = pkg.alloc_workspace(pkg.mla_absorb_chunk_fp8_batch_workspace_size(B, H, B, mb))
+
+    def step():
+        pkg.kv8_pages_append(*d.state(), n_new, q_start=q_start, dst_slot=slots, err_word=d.err)
+        pkg.kv8_quantize_rows(rows, codes, scales, dst_slot=slots)
+        pkg.mla_absorb_chunk_fp8_batch(ql, qr, codes, scales, d.table, d.lens, q_start, SM_SCALE, out=out, lse=lse,
+                                       workspace=ws)
+
+    step()
+    p.append([1, 1, 1], 3)
+    d.same(p)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(5):
+        rows.copy_(torch.randn((B, D), device="cuda", generator=g) * (1 + i))
+        ql.copy_(torch.randn((B, H, DL), device="cuda", generator=g).bfloat16())
+        out.fill_(float("nan"))
+        lse.fill_(float("nan"))
+        graph.replay()
+        _, s, _ = p.append([1, 1, 1], 3)
+        d.same(p)
+        assert np.array_equal(slots.cpu().numpy(), s)
+        c2, s2 = torch.zeros_like(codes[:B]), torch.zeros_like(scales[:B])
+        pkg.kv8_quantize_rows(rows, c2, s2)
+        assert torch.equal(codes[slots], c2) and torch.equal(scales[slots], s2)
+        lse2 = torch.empty_like(lse)
+        want = pkg.mla_absorb_chunk_fp8_batch(ql, qr, codes, scales, d.table, d.lens,
+                                              torch.arange(B + 1, dtype=torch.int32, device="cuda"), SM_SCALE, lse=lse2)
+        assert torch.equal(out, want) and torch.equal(lse, lse2)
+        assert torch.isfinite(lse).all() and pkg.kv8_workspace_error(ws) == 0
