@@ -460,7 +460,9 @@ def mla_absorb_chunk_fp8_batch(q_lat, q_rope, kv_codes, kv_scales, block_table, 
                                block_size=KV8_BLOCK, stream=None):
     """The new tokens of B sequences (bf16 q_lat [total_q,H,512], q_rope [total_q,H,64], sequence
     b's rows q_start[b]..q_start[b+1]-1) over a paged cache that holds them -> bf16 out
-    [total_q,H,512].  The queries may be strided views whose last dimension is contiguous."""
+    [total_q,H,512].  The queries may be strided views whose last dimension is contiguous.  Bad
+    table entries, lengths and query ranges, and timeouts, are told by kv8_workspace_error(workspace)
+    alone: without a workspace of the caller's they are not heard of."""
     for t, name, width in ((q_lat, "q_lat", KV8_DL), (q_rope, "q_rope", KV8_DR)):
         if not (isinstance(t, torch.Tensor) and t.dtype == torch.bfloat16 and _is_device(t)
                 and t.dim() == 3 and t.shape[2] == width and t.stride(2) == 1):
@@ -543,7 +545,8 @@ def kv8_pages_append(block_table, seq_lens, page_refs, n_new, cap=None, q_start=
                      err_word=None, stream=None):
     """Room for n_new[b] more tokens of every sequence: pages taken, seq_lens raised.  Returns
     (q_start int32 [B+1], dst_slot int64 [cap]): where each sequence's new rows start, and the
-    cache slots of the new tokens in that order (-1 behind the last).  Give dst_slot or cap."""
+    cache slots of the new tokens in that order (-1 behind the last).  Give dst_slot or cap.  An
+    append that cannot be gives no token a slot (q_start all 0) and says so in err_word alone."""
     table = _page_table(block_table, seq_lens, page_refs, err_word)
     B = table[3]
     _need(n_new, "n_new", torch.int32, 1)

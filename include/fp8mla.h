@@ -355,7 +355,8 @@ int kv8_noalloc_error(void* stream);
  *               reach its result, whatever their bytes.
  *   q_start     device int32 [B + 1], non-decreasing within [0, total_q].  A
  *               sequence whose range breaks that has no query and sets the error
- *               word (KV8_EBOUNDS).
+ *               word (KV8_EBOUNDS); rows that the ranges around it then share are
+ *               undefined.
  *   total_q     rows of the query arrays, 0 <= total_q, total_q * H <= 2^31 - 1.
  *   out         device bf16 [total_q][H][512], 16-byte aligned.
  *   lse         device f32 [total_q][H] or NULL.
@@ -401,7 +402,9 @@ int mla_absorb_chunk_fp8_batch(const uint16_t* q_lat, int64_t q_lat_token_stride
  *
  * err_word: device uint32 or NULL; a call that meets bad data sets bits in it
  * (atomic OR; the caller clears it): KV8_PAGES_EINDEX, KV8_PAGES_ENOROOM or, from
- * kv8_pages_copy, KV8_PAGES_ETIMEOUT (a bounded device-side wait gave up).
+ * kv8_pages_copy, KV8_PAGES_ETIMEOUT (a bounded device-side wait gave up).  Without
+ * it a refused append looks like one without new tokens, a refused fork or compact
+ * like one without moves.
  * Limits: 1 <= B <= KV8_PAGES_MAX_SEQS, 1 <= n_blocks <= KV8_PAGES_MAX_BLOCKS, 1 <=
  * max_blocks < 2^25 (KV8_EUNSUPPORTED above the first two).  Pointers 4-byte
  * aligned (8 for int64, 16 for the cache).  The arrays of a call must not overlap.
@@ -485,10 +488,11 @@ int kv8_pages_copy(uint8_t* kv_codes, float* kv_scales, int n_layers, int64_t n_
                    unsigned* err_word, void* stream);
 
 /* kv8_workspace_error -- synchronises `stream`, then reports the device-side
- * error word of the last decode call that used `workspace`: KV8_OK,
- * KV8_EBOUNDS (a bad block-table entry or seq_len) or KV8_ETIMEOUT (a kernel
- * gave up a wait after its bound and returned without a result).  A debugging
- * aid; the decode calls themselves never sync. */
+ * error word of the last decode or chunk call that used `workspace` (a call with
+ * nothing to do, B = 0 or total_q = 0, does not): KV8_OK, KV8_EBOUNDS (a bad
+ * block-table entry, seq_len or query range) or KV8_ETIMEOUT (a kernel gave up a
+ * wait after its bound and returned without a result).  A debugging aid; the calls
+ * themselves never sync. */
 int kv8_workspace_error(const void* workspace, void* stream);
 
 /* Human-readable text for a kv8_status value (static storage). */
