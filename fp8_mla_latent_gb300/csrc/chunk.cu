@@ -54,18 +54,18 @@
 //
 // What bounds it.  A tile's MMAs take 2304 cycles on a score pair (36 of 64 cycles: 576 channels,
 // twice for the query's two terms, at twice the rate of bf16) and 2048 on a context pair.  A tile
-// takes about 2950: the sixteen warps of either side are a chain of
-// waits and arithmetic that long (softmax: 250 the wait for S, 830 reading and scaling it, 500 the
-// largest weight, 430 the reference, 950 the exponentials and stores; context:
-// 850 the split, 150 a wait, 2 x 800 the rescale where a reference moved), at 54 % of the issue
-// slots; the tensor pipe is active 78 % of a score SM's time.  Ways to overlap two tiles were
-// slower: softmax warps in two groups on alternate tiles wait for the one S_R buffer (TMEM is
-// full), and more registers a thread, for two tiles at once, do not fit 19 warps.
+// takes about 3100 on normal values with outlying rows: the sixteen warps of either side are a chain
+// of waits and arithmetic that long (as traced, which adds a tenth: softmax 380 the wait for S, 840
+// reading and scaling it, 470 the largest weight, 380 the reference, 1090 the exponentials and stores;
+// context 1000 the split, 2 x 800 the rescale where a reference moved, for a warp's 32 rows three
+// tiles of four), at 52 % of the issue slots; the tensor pipe is active 76 % of a score SM's time.
+// Ways to overlap two tiles were slower: softmax warps in two groups on alternate tiles wait for the
+// one S_R buffer (TMEM is full), and more registers a thread, for two tiles at once, do not fit 19 warps.
 //
 // Measured, one GB300 (fractions of the bf16 rate of a large matrix product, 1895 TFLOP/s): 2 x 256
-// tokens over 65536 keys at 128 heads 5.84 ms, 1600 TFLOP/s, 0.84; a prompt of 4096 tokens 1.96 ms,
-// 1190, 0.63 (row tiles begin every 16 key tiles on average); 32 x 4 drafted tokens over up to
-// 16384 keys 0.228 ms, 1090, 0.58; one token of 4 heads over 256 keys 22 us, of which 4 are the plan,
+// tokens over 65536 keys at 128 heads 6.2 ms, 1500 TFLOP/s, 0.79; a prompt of 4096 tokens 2.04 ms,
+// 1150, 0.61 (row tiles begin every 16 key tiles on average); 32 x 4 drafted tokens over up to
+// 16384 keys 0.235 ms, 1060, 0.56; one token of 4 heads over 256 keys 22.5 us, of which 4 are the plan,
 // 5 the query, 5 the pipeline and 5 the results.
 //
 // Every wait is bounded (2 s): on a timeout
@@ -90,14 +90,16 @@ constexpr int W_TMA = 0, W_MMA = 1, W_SCALE = 2, W_LANE = 3;
 constexpr int N_LANE_WARPS = 16;             // four per TMEM lane quarter, and per scheduler
 constexpr int NTHREADS = (W_LANE + N_LANE_WARPS) * 32;
 constexpr int MAX_CLUSTERS = NUM_SMS / 4;
-// A cluster per row tile, or more while each has MIN_TILES key tiles.  One token at 128 heads over
-// 2048 keys (16 tiles): 29.5 us a call in ranges of two, 32.9 of four; over 512 keys (4 tiles) 25.0
-// of two, 27.5 of one; four row tiles of one key tile each: 20.6 in four clusters, 32 in two.
+// A cluster per row tile, or more while that gives each MIN_TILES key tiles on average.  (The ranges
+// differ by up to SWITCH, below, which is counted in front of every row tile, the first of a range
+// among them: 4 tiles fall into ranges of 0 and 4, 16 into 0, 0, 2, 3, 2, 3, 3, 3.)  Device times for
+// 1, 2 and 4, us: one token of 128 heads over 512 keys 30.8, 28.7, 26.7, over 2048 35.4, 32.8, 36.8,
+// over 8192 47.2, 47.0, 41.0; two row tiles of 8 key tiles 32.8, 34.9, 38.7.
 constexpr int MIN_TILES = 2;
 // What beginning a row tile costs, in key tiles: 19 thousand cycles (the query is loaded and split
 // while the context pair writes its results, and the pipeline fills) against 3.1 thousand a tile.  A
-// prompt of 4096 tokens at 128 heads: 2.97 ms when ranges count 2 for it, 2.31 for 4, 2.11 for 5,
-// 2.00 for 6, 2.02 for 7.
+// prompt of 4096 tokens at 128 heads: 2.40 ms when ranges count 4 for it, 2.17 for 5, 2.04 for 6, 2.06
+// for 7, 2.09 for 8; five sequences without a mask 103, 102, 98, 99, 100 us.
 constexpr int SWITCH = 6;
 constexpr int BLK = PAGE * 128;              // 8 KB: [64 tokens x 128 bytes]
 constexpr int RBLK = PAGE * DR;              // 4 KB: [64 tokens x 64 bytes]
@@ -130,7 +132,7 @@ constexpr float LN2 = 0.6931471805599453f;
 // that has nothing else to do waits there and arrives at the other CTA's (the relays).  TMEM alone:
 // a relaxed arrival between the fences of tcgen05.  Releases at cluster scope by the sixteen warps
 // themselves make drafts 15 % slower where it is the payloads' buffers alone and 45 % with the operands,
-// relays of the S buffers and the O halves as well 19 %; this 2 %.
+// relays of the S buffers and the O halves as well 19 %; this 2 to 4 %.
 constexpr int B_KFULL = 0;                   // [2 NK] rank 0: both CTAs' halves of a K half tile loaded
 constexpr int B_KEMPTY = B_KFULL + 2 * NK;   // [2 NK] ranks 0, 1: consumed
 constexpr int B_SCFULL = B_KEMPTY + 2 * NK;  // [NSC] score: row scales of a tile loaded
@@ -1323,9 +1325,9 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
 // Joins the parts of the row tiles that range borders cut: for every cluster k but the
 // first, the row tile that it starts in, if cluster k - 1 holds its beginning; a warp per
 // row, or per row and SPLIT-th of its channels.  In four parts a single row tile in many
-// parts is read by 128 SMs in place of 32 (one token over 8192 keys at 128 heads: 38.8
-// against 45.6 us a call); where most clusters hold a border the blocks that gives cost
-// more than that (4 x 32 tokens over 16384 keys: 234.8 against 230.3 us).
+// parts is read by 128 SMs in place of 32 (one token over 8192 keys at 128 heads: 47.0
+// against 55.6 us); where most clusters hold a border the blocks that gives cost more
+// than that (32 x 4 tokens over up to 16384 keys: 241 against 236 us).
 constexpr int JOIN_BLOCKS = ROWS / 8;
 constexpr int FEW_ROW_TILES = 8;
 

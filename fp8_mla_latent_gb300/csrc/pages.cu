@@ -19,9 +19,9 @@
 // launch latency (3 us) and dependent L2 round trips (about 1 us each), so the work
 // on them is to have fewer in a row.  A CTA count of one is kept while the entries to
 // walk fit one pass of one CTA.  Measured (device time under a profiler): for 2 forks
-// of short sequences free 4, fork 8, append 6 us; for 192 forks of up to 4096 tokens
-// among 256 sequences free 7, fork 12, append 14 us; compact 9 us for 100 pages, 12 us
-// for 6200 in 256 sequences.
+// of short sequences free 4, fork 9, append 6 us; for 192 forks of up to 4096 tokens
+// among 256 sequences free 7, fork 11, append 14 us; compact 10 us for 100 pages, 13 us
+// for 6200 in 256 sequences.  (Sequences of thousands of pages were not measured.)
 //
 // The copy is the only step that moves real data: 2 x 37376 bytes per page and
 // layer, an HBM stream.  Bulk copies through a shared-memory ring, issued by one
