@@ -149,3 +149,34 @@ def test_same_bits_with_a_wider_table(H, nq, lens):
         d.table, d.max_blocks = table, wide
         out, lse = run(d)
         assert torch.equal(out, want) and torch.equal(lse, want_l)
+
+
+@pytest.mark.parametrize("binades", [6.0, 9.0, 9.9, 10.1, 13.0, 30.0, 47.0, 60.0])
+def test_a_weight_is_held_to_its_tiles_largest(binades):
+    """A bulk of weights that vary little, under a key `binades` above them in every other tile of the
+    first half: a weight is off by its own relative error, or by what the header allows beside it,
+    the smaller of 2^-17 of the row's largest and 2^-7 of its tile's largest (while that is over
+    2^-50 of the row's)."""
+    def rows(b, t, g):
+        x = torch.cat([0.5 + 0.3 * torch.randn((t, DL), generator=g), 0.02 * torch.randn((t, DR), generator=g)], 1)
+        x[: t // 2: 2 * TILE] = torch.cat([0.1 * torch.randn(DL, generator=g), torch.full((DR,), binades / 16.99 * 2.55)])
+        return x
+    c = Case(128, [72], [8192], seed=37, rows=rows)
+    c.q_lat *= 0.02
+    c.q_rope.fill_(1.0)
+    out, _ = run(c, causal=False)
+    tokens, heads = [0, 35, 71], [0, 1, 77, 127]
+    slot = c.slots[0].cuda()
+    row, s = e4m3_values("cuda")[c.codes[slot].long()], c.scales[slot].double()
+    key = torch.cat([row[:, :DL] * s[:, :1], row[:, DL:] * s[:, 1:]], 1)
+    q = torch.cat([c.q_lat, c.q_rope], -1)[tokens][:, heads].flatten(0, 1).double()
+    p = torch.softmax(q @ key.T * SM_SCALE, -1)
+    ez = SM_SCALE * (2.0 ** -17 * q.abs().amax(-1)[:, None] * key.abs().sum(-1) + 2.0 ** -19 * (q.abs() @ key.abs().T))
+    weight = p * s[:, 0]
+    top, tile = weight.amax(-1, keepdim=True), weight.unflatten(1, (-1, TILE)).amax(-1).repeat_interleave(TILE, 1)
+    other = torch.where(tile >= 2.0 ** -50 * top, torch.minimum(2.0 ** -17 * top, 2.0 ** -7 * tile), 2.0 ** -17 * top)
+    each = torch.maximum((2.0 ** -9 + 3 * 2.0 ** -11 + 2.0 ** -17 + 2 * ez.amax(-1, keepdim=True)) * p, other / s[:, 0])
+    ref = p @ key[:, :DL]
+    tol = each @ key[:, :DL].abs() + 2.0 ** -8 * ref.abs() + 1e-30
+    got = out[tokens][:, heads].flatten(0, 1).double()
+    assert float(((got - ref).abs() / tol).amax()) <= 1.0
