@@ -375,7 +375,8 @@ int kv8_noalloc_error(void* stream);
  * product if that is more, but no more than 2^-7 of the largest in its tile of 128
  * keys, as long as that is over 2^-50 of the row's; an sLc under 2^-40 counts as 2^-40
  * in these comparisons, and one under 0, which no call here writes, as 0 throughout);
- * maxima and denominators are f32; out is rounded to bf16 once.  A query row with a NaN or an infinity gives NaN, unless it sees nothing.
+ * maxima and denominators are f32; out is rounded to bf16 once.  A query row with a NaN
+ * or an infinity gives NaN, unless it sees nothing.
  * Errors: KV8_EINVAL, KV8_EALIGN, KV8_EUNSUPPORTED, KV8_EWORKSPACE, KV8_ECUDA.
  * ------------------------------------------------------------------------- */
 int64_t mla_absorb_chunk_fp8_batch_workspace_size(int B, int H, int64_t total_q, int max_blocks);
@@ -449,9 +450,9 @@ int kv8_pages_fork(int32_t* block_table, int32_t* seq_lens, int32_t* page_refs, 
 /* kv8_pages_free -- empties the sequences seq[0 .. n - 1]: gives their pages back
  * (one count each), sets their entries to -1 and their seq_lens to 0.  A sequence
  * that is out of range, named twice or of a bad seq_len makes the call do nothing but
- * set the error word.  A held entry that names no page, or a page whose count is 0 already, sets
- * the error word and changes no count.  0 <= n <= KV8_PAGES_MAX_SEQS.  Errors:
- * KV8_EINVAL, KV8_EALIGN, KV8_EUNSUPPORTED, KV8_ECUDA. */
+ * set the error word.  A held entry that names no page, or a page whose count is 0
+ * already, sets the error word and changes no count.  0 <= n <= KV8_PAGES_MAX_SEQS.
+ * Errors: KV8_EINVAL, KV8_EALIGN, KV8_EUNSUPPORTED, KV8_ECUDA. */
 int kv8_pages_free(int32_t* block_table, int32_t* seq_lens, int32_t* page_refs, int B,
                    int max_blocks, int64_t n_blocks, const int32_t* seq, int n,
                    unsigned* err_word, void* stream);
