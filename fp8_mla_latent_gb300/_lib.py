@@ -23,6 +23,7 @@ KV8_DECODE_TCGEN05_CTA, KV8_DECODE_TCGEN05_PAIR = 3, 4
 STATUS = {0: "KV8_OK", -1: "KV8_EINVAL", -2: "KV8_EALIGN", -3: "KV8_EUNSUPPORTED",
           -4: "KV8_ECUDA", -5: "KV8_EBOUNDS", -6: "KV8_EWORKSPACE", -7: "KV8_ETIMEOUT",
           -8: "KV8_ESCRATCH", -9: "KV8_EIO", -10: "KV8_EFORMAT"}
+KV8_BF16, KV8_F16, KV8_F32, KV8_NORM_MAX_WIDTH = 0, 1, 2, 32768
 KV8_PAGES_EINDEX, KV8_PAGES_ENOROOM, KV8_PAGES_ETIMEOUT = 1, 2, 4  # bits of the pages' err_word
 
 _lock = threading.Lock()
@@ -53,6 +54,8 @@ def lib() -> ctypes.CDLL:
                 "kv8_quantize_rows": (i32, [P, i64, i64, P, P, P, i64, P]),
                 "kv8_produce_rows": (i32, [P, i64, i64, P, ctypes.c_float, P, P, P, i64, P, P, P,
                                            i64, P, P]),
+                "kv8_norm_quantize_rows": (i32, [P, i64, P, i64, P, i64, P, f32, i64, i32, i32, i32, P, i64,
+                                                 P, i64, P, P]),
                 "mla_wuv_epilogue": (i32, [P, P, i32, i32, i32, P, P]),
                 "kv8_selftest_wait_timeout": (i32, [P, i64, i64, P]),
                 "kv8_prefill_project": (i32, [P, P, i64, P, i64, P, i32, P, P, P, P]),
@@ -70,6 +73,13 @@ def lib() -> ctypes.CDLL:
                 "mla_absorb_chunk_fp8_batch_workspace_size": (i64, [i32, i32, i64, i32]),
                 "mla_absorb_chunk_fp8_batch": (i32, [P, i64, i64, P, i64, i64, P, P, P, P, P, i64, i32,
                                                      i32, i32, i32, i64, i32, f32, P, P, P, i64, P]),
+                "mla_absorb_window_fp8_batch_workspace_size": (i64, [i32, i32, i64, i32, i32, i32]),
+                "mla_absorb_window_fp8_batch": (i32, [P, i64, i64, P, i64, i64, P, P, P, P, P, i64, i32,
+                                                      i32, i32, i32, i64, i32, i32, f32, P, P, P, i64, P]),
+                "mla_absorb_shared_fp8_batch_workspace_size": (i64, [i32, i32, i64, i32, i32]),
+                "mla_absorb_shared_fp8_batch": (i32, [P, i64, i64, P, i64, i64, P, P, P, P, P, i64, i32,
+                                                      i32, i32, i32, i64, P, P, i32, i32, f32, P, P, P,
+                                                      i64, P]),
                 "kv8_pages_append": (i32, [P, P, P, i32, i32, i64, P, P, P, i64, P, P]),
                 "kv8_pages_fork": (i32, [P, P, P, i32, i32, i64, P, P, P, i32, P, P, P, P]),
                 "kv8_pages_free": (i32, [P, P, P, i32, i32, i64, P, i32, P, P]),
@@ -199,6 +209,58 @@ def kv8_produce_rows(src, norm_weight, eps, positions, rope_cos, rope_sin, kv_co
                                 _ptr(kv_scales), kv_codes.shape[0], _ptr(err_word),
                                 _stream(stream))
     _check("kv8_produce_rows", st)
+
+
+_ROW_TYPES = {torch.bfloat16: KV8_BF16, torch.float16: KV8_F16, torch.float32: KV8_F32}
+
+
+def _row_stride(t):
+    """Elements between the rows of a 2-D tensor (its width for a single row, whose stride says nothing)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def kv8_norm_quantize_rows(x, norm_weight, eps, residual=None, residual_out=None, normed=None, codes=None,
+                           scales=None, group=0, stream=None):
+    """t = x + residual; y = RMS norm of t times norm_weight; codes (e4m3 as uint8 [n, width]) and scales
+    (f32 [n, 1], or [n, ceil(width / group)] with a scale for every `group` channels) of y.  x [n, width]
+    is bf16, f16 or f32; residual_out takes t and normed takes y in that type.  Rows may be strided.
+    Returns (codes, scales)."""
+    if not (isinstance(x, torch.Tensor) and x.dtype in _ROW_TYPES and _is_device(x) and x.dim() == 2
+            and x.shape[1] >= 1 and (x.stride(1) == 1 or x.shape[1] == 1)):
+        raise ValueError("x must be a CUDA bfloat16, float16 or float32 [n, width] tensor with unit column stride")
+    n, width = x.shape
+    for t, name, dtype in ((residual, "residual", x.dtype), (residual_out, "residual_out", x.dtype),
+                           (normed, "normed", x.dtype), (codes, "codes", torch.uint8)):
+        if t is None:
+            continue
+        if not (isinstance(t, torch.Tensor) and t.dtype == dtype and _is_device(t) and t.shape == (n, width)
+                and (t.stride(1) == 1 or width == 1)):
+            raise ValueError(f"{name} must be a CUDA {dtype} [{n}, {width}] tensor with unit column stride")
+    if residual_out is not None and residual is None:
+        raise ValueError("residual_out needs residual")
+    _need(norm_weight, "norm_weight", torch.float32, 1)
+    if norm_weight.shape[0] != width:
+        raise ValueError("norm_weight must have one entry per column of x")
+    group = int(group)
+    if group not in (0, 32, 64, 128, 256):
+        raise ValueError("group must be 0, 32, 64, 128 or 256")
+    groups = -(-width // group) if group else 1
+    if codes is None or scales is None:
+        with _allocating(stream):
+            codes = torch.empty((n, width), dtype=torch.uint8, device=x.device) if codes is None else codes
+            scales = torch.empty((n, groups), dtype=torch.float32, device=x.device) if scales is None else scales
+    _need(scales, "scales", torch.float32, 2)
+    if scales.shape != (n, groups):
+        raise ValueError(f"scales must be [{n}, {groups}]")
+    with _on_device_of(x, residual, residual_out, norm_weight, normed, codes, scales):
+        st = lib().kv8_norm_quantize_rows(
+            _ptr(x), _row_stride(x), _ptr(residual), 0 if residual is None else _row_stride(residual),
+            _ptr(residual_out), 0 if residual_out is None else _row_stride(residual_out), _ptr(norm_weight),
+            float(eps), n, width, _ROW_TYPES[x.dtype], group, _ptr(normed),
+            0 if normed is None else _row_stride(normed), _ptr(codes), _row_stride(codes), _ptr(scales),
+            _stream(stream))
+    _check("kv8_norm_quantize_rows", st)
+    return codes, scales
 
 
 def kv8_prefill_project(kv_codes, kv_scales, w_ukv, T=None, slots=None, y=None, k_rope=None,
@@ -455,14 +517,27 @@ def mla_absorb_chunk_fp8_batch_workspace_size(B: int, H: int, total_q: int, max_
     return int(n)
 
 
-def mla_absorb_chunk_fp8_batch(q_lat, q_rope, kv_codes, kv_scales, block_table, seq_lens, q_start,
-                               sm_scale, causal=True, out=None, lse=None, workspace=None,
-                               block_size=KV8_BLOCK, stream=None):
-    """The new tokens of B sequences (bf16 q_lat [total_q,H,512], q_rope [total_q,H,64], sequence
-    b's rows q_start[b]..q_start[b+1]-1) over a paged cache that holds them -> bf16 out
-    [total_q,H,512].  The queries may be strided views whose last dimension is contiguous.  Bad
-    table entries, lengths and query ranges, and timeouts, are told by kv8_workspace_error(workspace)
-    alone: without a workspace of the caller's they are not heard of."""
+def mla_absorb_window_fp8_batch_workspace_size(B: int, H: int, total_q: int, max_blocks: int, window: int,
+                                               n_sink: int) -> int:
+    n = lib().mla_absorb_window_fp8_batch_workspace_size(int(B), int(H), int(total_q), int(max_blocks),
+                                                         int(window), int(n_sink))
+    if n < 0:
+        raise ValueError("invalid B, H, total_q, max_blocks, window or n_sink")
+    return int(n)
+
+
+def mla_absorb_shared_fp8_batch_workspace_size(B: int, H: int, total_q: int, max_blocks: int, G: int) -> int:
+    n = lib().mla_absorb_shared_fp8_batch_workspace_size(int(B), int(H), int(total_q), int(max_blocks), int(G))
+    if n < 0:
+        raise ValueError("invalid B, H, total_q, max_blocks or G")
+    return int(n)
+
+
+def _chunk_call(fn, size, own, q_lat, q_rope, kv_codes, kv_scales, block_table, seq_lens, q_start, sm_scale,
+                out, lse, workspace, block_size, stream, also=()):
+    """The checks and the call of an attention of new tokens over the paged cache: `size` are the arguments
+    of its workspace size, and `own` those of its call, that it does not share with the others (`also`:
+    the tensors among them)."""
     for t, name, width in ((q_lat, "q_lat", KV8_DL), (q_rope, "q_rope", KV8_DR)):
         if not (isinstance(t, torch.Tensor) and t.dtype == torch.bfloat16 and _is_device(t)
                 and t.dim() == 3 and t.shape[2] == width and t.stride(2) == 1):
@@ -489,21 +564,64 @@ def mla_absorb_chunk_fp8_batch(q_lat, q_rope, kv_codes, kv_scales, block_table, 
         _need(lse, "lse", torch.float32, 2)
         if lse.shape != (rows, H):
             raise ValueError("lse must be [total_q,H]")
-    need = mla_absorb_chunk_fp8_batch_workspace_size(B, H, rows, max_blocks)
+    need = globals()[fn + "_workspace_size"](B, H, rows, max_blocks, *size)
     if workspace is None:
         with _allocating(stream):
             workspace = alloc_workspace(need, q_lat.device)
     _need_workspace(workspace)
     with _on_device_of(q_lat, q_rope, kv_codes, kv_scales, block_table, seq_lens, q_start, out, lse,
-                       workspace):
-        st = lib().mla_absorb_chunk_fp8_batch(
+                       workspace, *also):
+        st = getattr(lib(), fn)(
             _ptr(q_lat), *_strides(q_lat), _ptr(q_rope), *_strides(q_rope), _ptr(kv_codes),
             _ptr(kv_scales), _ptr(block_table), _ptr(seq_lens), _ptr(q_start), rows, B, H, max_blocks,
-            int(block_size), int(kv_codes.shape[0] // block_size), int(bool(causal)),
+            int(block_size), int(kv_codes.shape[0] // block_size), *own,
             float(sm_scale), _ptr(out), _ptr(lse), _ptr(workspace),
             workspace.numel() * workspace.element_size(), _stream(stream))
-    _check("mla_absorb_chunk_fp8_batch", st)
+    _check(fn, st)
     return out
+
+
+def mla_absorb_chunk_fp8_batch(q_lat, q_rope, kv_codes, kv_scales, block_table, seq_lens, q_start,
+                               sm_scale, causal=True, out=None, lse=None, workspace=None,
+                               block_size=KV8_BLOCK, stream=None):
+    """The new tokens of B sequences (bf16 q_lat [total_q,H,512], q_rope [total_q,H,64], sequence
+    b's rows q_start[b]..q_start[b+1]-1) over a paged cache that holds them -> bf16 out
+    [total_q,H,512].  The queries may be strided views whose last dimension is contiguous.  Bad
+    table entries, lengths and query ranges, and timeouts, are told by kv8_workspace_error(workspace)
+    alone: without a workspace of the caller's they are not heard of."""
+    return _chunk_call("mla_absorb_chunk_fp8_batch", (), (int(bool(causal)),), q_lat, q_rope, kv_codes,
+                       kv_scales, block_table, seq_lens, q_start, sm_scale, out, lse, workspace, block_size,
+                       stream)
+
+
+def mla_absorb_window_fp8_batch(q_lat, q_rope, kv_codes, kv_scales, block_table, seq_lens, q_start,
+                                sm_scale, window, n_sink=0, out=None, lse=None, workspace=None,
+                                block_size=KV8_BLOCK, stream=None):
+    """mla_absorb_chunk_fp8_batch with a sliding window: a new token sees the last `window` keys up to
+    itself and the first `n_sink` ones.  Pages that no new token sees need not be there."""
+    window, n_sink = int(window), int(n_sink)
+    if not 1 <= window < 2 ** 31 or not 0 <= n_sink < 2 ** 31:
+        raise ValueError("window must be at least 1, n_sink at least 0, and both below 2^31")
+    return _chunk_call("mla_absorb_window_fp8_batch", (window, n_sink), (window, n_sink), q_lat, q_rope,
+                       kv_codes, kv_scales, block_table, seq_lens, q_start, sm_scale, out, lse, workspace,
+                       block_size, stream)
+
+
+def mla_absorb_shared_fp8_batch(q_lat, q_rope, kv_codes, kv_scales, block_table, seq_lens, q_start,
+                                sm_scale, group_start, shared_len, causal=True, out=None, lse=None,
+                                workspace=None, block_size=KV8_BLOCK, stream=None):
+    """mla_absorb_chunk_fp8_batch where sequences group_start[g]..group_start[g+1]-1 share their first
+    shared_len[g] tokens, the whole pages of them by the same table entries: computed once for the
+    group.  group_start int32 [G+1], shared_len int32 [G]."""
+    _need(group_start, "group_start", torch.int32, 1)
+    _need(shared_len, "shared_len", torch.int32, 1)
+    G = shared_len.shape[0]
+    if group_start.shape[0] != G + 1:
+        raise ValueError("group_start must have one entry more than shared_len")
+    return _chunk_call("mla_absorb_shared_fp8_batch", (G,),
+                       (_ptr(group_start), _ptr(shared_len), G, int(bool(causal))), q_lat, q_rope, kv_codes,
+                       kv_scales, block_table, seq_lens, q_start, sm_scale, out, lse, workspace, block_size,
+                       stream, (group_start, shared_len))
 
 
 # ----------------------------------------------------------------- pages

@@ -179,6 +179,53 @@ int kv8_produce_rows(const float* src, int64_t n_rows, int64_t src_row_stride,
   return e == cudaSuccess ? KV8_OK : KV8_ECUDA;
 }
 
+int kv8_norm_quantize_rows(const void* x, int64_t x_row_stride, const void* residual,
+                           int64_t residual_row_stride, void* residual_out,
+                           int64_t residual_out_row_stride, const float* norm_weight, float eps,
+                           int64_t n_rows, int width, int dtype, int group, void* normed,
+                           int64_t normed_row_stride, uint8_t* codes, int64_t codes_row_stride,
+                           float* scales, void* stream) {
+  if (n_rows < 0 || width < 1 || dtype < KV8_BF16 || dtype > KV8_F32) return KV8_EINVAL;
+  if (!(eps >= 0.0f) || eps > 3.0e38f) return KV8_EINVAL;  // also rejects NaN
+  if (group != 0 && group != 32 && group != 64 && group != 128 && group != 256) return KV8_EUNSUPPORTED;
+  if (width > KV8_NORM_MAX_WIDTH || n_rows > INT32_MAX) return KV8_EUNSUPPORTED;
+  if (n_rows == 0) return KV8_OK;
+  if (x == nullptr || norm_weight == nullptr || codes == nullptr || scales == nullptr ||
+      (residual_out != nullptr && residual == nullptr))
+    return KV8_EINVAL;
+  // rows that are written lie apart; rows that are read may be one row
+  if (x_row_stride < 0 || (residual != nullptr && residual_row_stride < 0)) return KV8_EINVAL;
+  if (n_rows > 1 && (codes_row_stride < width || (residual_out != nullptr && residual_out_row_stride < width) ||
+                     (normed != nullptr && normed_row_stride < width)))
+    return KV8_EINVAL;
+  const int64_t size = dtype == KV8_F32 ? 4 : 2;
+  if (!aligned(x, size) || !aligned(residual, size) || !aligned(residual_out, size) ||
+      !aligned(normed, size) || !aligned(norm_weight, 4) || !aligned(scales, 4))
+    return KV8_EALIGN;
+  NormArgs a{};
+  a.x = x;
+  a.residual = residual;
+  a.residual_out = residual_out;
+  a.normed = normed;
+  a.weight = norm_weight;
+  a.codes = codes;
+  a.scales = scales;
+  a.x_stride = x_row_stride;
+  a.residual_stride = residual_row_stride;
+  a.residual_out_stride = residual_out_row_stride;
+  a.normed_stride = normed_row_stride;
+  a.codes_stride = codes_row_stride;
+  a.n_rows = n_rows;
+  a.width = width;
+  a.group = group;
+  a.n_groups = group == 0 ? 1 : (width + group - 1) / group;
+  a.eps = eps;
+  const cudaError_t e = launch_norm(a, dtype, static_cast<cudaStream_t>(stream));
+  if (e == cudaSuccess) return KV8_OK;
+  g_last_cuda_error = e;
+  return KV8_ECUDA;
+}
+
 int kv8_prefill_project(const uint8_t* kv_codes, const float* kv_scales, int64_t n_slots,
                         const int64_t* slots, int64_t T, const uint16_t* w_ukv, int N,
                         uint16_t* y, float* k_rope, unsigned* err_word, void* stream) {
@@ -433,25 +480,31 @@ int kv8_noalloc_error(void* stream) {
 // ---------------------------------------------------------------------------
 // Attention of a chunk of new tokens, and the pages of the cache.
 
-extern "C" {
+namespace {
 
-int64_t mla_absorb_chunk_fp8_batch_workspace_size(int B, int H, int64_t total_q, int max_blocks) {
-  if (B < 0 || H < 1 || H > 1024 || max_blocks < 1 || max_blocks >= (1 << 25) || total_q < 0 ||
-      total_q * H > INT32_MAX)
-    return -1;
-  return chunk_workspace(B, H, total_q, max_blocks);
+bool chunk_sizes(int B, int H, int64_t total_q, int max_blocks) {
+  return B >= 0 && H >= 1 && H <= 1024 && max_blocks >= 1 && max_blocks < (1 << 25) && total_q >= 0 &&
+         total_q <= INT32_MAX && total_q * H <= INT32_MAX;
 }
 
-int mla_absorb_chunk_fp8_batch(const uint16_t* q_lat, int64_t q_lat_token_stride,
-                               int64_t q_lat_head_stride, const uint16_t* q_rope,
-                               int64_t q_rope_token_stride, int64_t q_rope_head_stride,
-                               const uint8_t* kv_codes, const float* kv_scales,
-                               const int32_t* block_table, const int32_t* seq_lens,
-                               const int32_t* q_start, int64_t total_q, int B, int H,
-                               int max_blocks, int block_size, int64_t n_blocks, int causal,
-                               float sm_scale, uint16_t* out, float* lse, void* workspace,
-                               int64_t workspace_bytes, void* stream) {
-  const int64_t need = mla_absorb_chunk_fp8_batch_workspace_size(B, H, total_q, max_blocks);
+// A launch's status, as a call returns it.
+int told(cudaError_t e) {
+  if (e == cudaSuccess) return KV8_OK;
+  g_last_cuda_error = e;
+  return e == cudaErrorNotSupported ? KV8_EUNSUPPORTED : KV8_ECUDA;
+}
+
+constexpr int KV8_RUN = 1;  // the arguments are good, and there is something to do
+
+// The checks that the calls on chunks of new tokens share, and their arguments (`need`: the bytes of
+// workspace, negative for bad sizes).
+int chunk_args(ChunkArgs& a, int64_t need, const uint16_t* q_lat, int64_t q_lat_token_stride,
+               int64_t q_lat_head_stride, const uint16_t* q_rope, int64_t q_rope_token_stride,
+               int64_t q_rope_head_stride, const uint8_t* kv_codes, const float* kv_scales,
+               const int32_t* block_table, const int32_t* seq_lens, const int32_t* q_start,
+               int64_t total_q, int B, int H, int max_blocks, int block_size, int64_t n_blocks,
+               int causal, float sm_scale, uint16_t* out, float* lse, void* workspace,
+               int64_t workspace_bytes) {
   if (need < 0 || n_blocks < 1 || !valid_scale(sm_scale)) return KV8_EINVAL;
   const int64_t strides[4] = {q_lat_token_stride, q_lat_head_stride, q_rope_token_stride,
                               q_rope_head_stride};
@@ -470,7 +523,7 @@ int mla_absorb_chunk_fp8_batch(const uint16_t* q_lat, int64_t q_lat_token_stride
     return KV8_EALIGN;
   if (workspace == nullptr || workspace_bytes < need) return KV8_EWORKSPACE;
   if (!aligned(workspace, 256)) return KV8_EALIGN;
-  ChunkArgs a{};
+  a = ChunkArgs{};
   a.q_lat = q_lat;
   a.q_rope = q_rope;
   a.ql_t = q_lat_token_stride;
@@ -491,10 +544,92 @@ int mla_absorb_chunk_fp8_batch(const uint16_t* q_lat, int64_t q_lat_token_stride
   a.sm_scale = sm_scale;
   a.out = out;
   a.lse = lse;
-  const cudaError_t e = launch_chunk(a, workspace, static_cast<cudaStream_t>(stream));
-  if (e == cudaSuccess) return KV8_OK;
-  g_last_cuda_error = e;
-  return e == cudaErrorNotSupported ? KV8_EUNSUPPORTED : KV8_ECUDA;
+  return KV8_RUN;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t mla_absorb_chunk_fp8_batch_workspace_size(int B, int H, int64_t total_q, int max_blocks) {
+  return chunk_sizes(B, H, total_q, max_blocks) ? chunk_workspace(B, H, total_q, max_blocks) : -1;
+}
+
+int mla_absorb_chunk_fp8_batch(const uint16_t* q_lat, int64_t q_lat_token_stride,
+                               int64_t q_lat_head_stride, const uint16_t* q_rope,
+                               int64_t q_rope_token_stride, int64_t q_rope_head_stride,
+                               const uint8_t* kv_codes, const float* kv_scales,
+                               const int32_t* block_table, const int32_t* seq_lens,
+                               const int32_t* q_start, int64_t total_q, int B, int H,
+                               int max_blocks, int block_size, int64_t n_blocks, int causal,
+                               float sm_scale, uint16_t* out, float* lse, void* workspace,
+                               int64_t workspace_bytes, void* stream) {
+  ChunkArgs a;
+  const int64_t need = mla_absorb_chunk_fp8_batch_workspace_size(B, H, total_q, max_blocks);
+  const int st = chunk_args(a, need, q_lat, q_lat_token_stride, q_lat_head_stride, q_rope,
+                            q_rope_token_stride, q_rope_head_stride, kv_codes, kv_scales, block_table,
+                            seq_lens, q_start, total_q, B, H, max_blocks, block_size, n_blocks, causal,
+                            sm_scale, out, lse, workspace, workspace_bytes);
+  return st == KV8_RUN ? told(launch_chunk(a, workspace, static_cast<cudaStream_t>(stream))) : st;
+}
+
+int64_t mla_absorb_window_fp8_batch_workspace_size(int B, int H, int64_t total_q, int max_blocks,
+                                                   int window, int n_sink) {
+  if (!chunk_sizes(B, H, total_q, max_blocks) || window < 1 || n_sink < 0) return -1;
+  return window_workspace(B, H, total_q, max_blocks, window, n_sink);
+}
+
+int mla_absorb_window_fp8_batch(const uint16_t* q_lat, int64_t q_lat_token_stride,
+                                int64_t q_lat_head_stride, const uint16_t* q_rope,
+                                int64_t q_rope_token_stride, int64_t q_rope_head_stride,
+                                const uint8_t* kv_codes, const float* kv_scales,
+                                const int32_t* block_table, const int32_t* seq_lens,
+                                const int32_t* q_start, int64_t total_q, int B, int H,
+                                int max_blocks, int block_size, int64_t n_blocks, int window,
+                                int n_sink, float sm_scale, uint16_t* out, float* lse,
+                                void* workspace, int64_t workspace_bytes, void* stream) {
+  ChunkArgs a;
+  const int64_t need =
+      mla_absorb_window_fp8_batch_workspace_size(B, H, total_q, max_blocks, window, n_sink);
+  const int st = chunk_args(a, need, q_lat, q_lat_token_stride, q_lat_head_stride, q_rope,
+                            q_rope_token_stride, q_rope_head_stride, kv_codes, kv_scales, block_table,
+                            seq_lens, q_start, total_q, B, H, max_blocks, block_size, n_blocks, 1,
+                            sm_scale, out, lse, workspace, workspace_bytes);
+  if (st != KV8_RUN) return st;
+  a.window = window;
+  a.n_sink = n_sink;
+  return told(launch_window(a, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+int64_t mla_absorb_shared_fp8_batch_workspace_size(int B, int H, int64_t total_q, int max_blocks,
+                                                   int G) {
+  if (!chunk_sizes(B, H, total_q, max_blocks) || G < 0 || G > (1 << 28) || B > (1 << 28)) return -1;
+  return shared_workspace(B, H, total_q, max_blocks, G);
+}
+
+int mla_absorb_shared_fp8_batch(const uint16_t* q_lat, int64_t q_lat_token_stride,
+                                int64_t q_lat_head_stride, const uint16_t* q_rope,
+                                int64_t q_rope_token_stride, int64_t q_rope_head_stride,
+                                const uint8_t* kv_codes, const float* kv_scales,
+                                const int32_t* block_table, const int32_t* seq_lens,
+                                const int32_t* q_start, int64_t total_q, int B, int H,
+                                int max_blocks, int block_size, int64_t n_blocks,
+                                const int32_t* group_start, const int32_t* shared_len, int G,
+                                int causal, float sm_scale, uint16_t* out, float* lse,
+                                void* workspace, int64_t workspace_bytes, void* stream) {
+  ChunkArgs a;
+  const int64_t need = mla_absorb_shared_fp8_batch_workspace_size(B, H, total_q, max_blocks, G);
+  const int st = chunk_args(a, need, q_lat, q_lat_token_stride, q_lat_head_stride, q_rope,
+                            q_rope_token_stride, q_rope_head_stride, kv_codes, kv_scales, block_table,
+                            seq_lens, q_start, total_q, B, H, max_blocks, block_size, n_blocks, causal,
+                            sm_scale, out, lse, workspace, workspace_bytes);
+  if (st != KV8_RUN) return st;
+  if (G > 0 && (group_start == nullptr || shared_len == nullptr)) return KV8_EINVAL;
+  if (!aligned(group_start, 4) || !aligned(shared_len, 4)) return KV8_EALIGN;
+  a.group_start = group_start;
+  a.shared_len = shared_len;
+  a.G = G;
+  return told(launch_shared(a, workspace, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

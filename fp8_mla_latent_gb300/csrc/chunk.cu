@@ -84,6 +84,9 @@ namespace {
 
 using namespace ptx;
 
+// what a call's rows see: all keys before them; with a window; a prefix shared by several sequences apart
+constexpr int kPlain = 0, kWindow = 1, kShared = 2;
+
 constexpr int ROWS = 256;                    // rows of a row tile: 128 per CTA of a pair
 constexpr int CROWS = 128;
 constexpr int W_TMA = 0, W_MMA = 1, W_SCALE = 2, W_LANE = 3;
@@ -193,16 +196,29 @@ struct PlanEntry {
   int64_t x;
 };
 struct Plan {
-  int64_t n_clusters, units;
+  int64_t n_clusters, units, part_rows;
   PlanEntry e[MAX_CLUSTERS];
 };
 
+template <int MODE>
 struct SeqInfo {
   int64_t q0;  // first row of the query arrays
   int nq, T;
 };
-__device__ __forceinline__ SeqInfo seq_info(const ChunkArgs& a, int b, bool tell) {
-  SeqInfo s;
+template <>
+struct SeqInfo<kShared> {
+  int64_t q0;
+  int nq, T;               // (T counts from the first key, token 64 page0)
+  int row, page0, causal;  // row of the block table, first page there
+  int part;                // row of its first part (below), or -1
+};
+template <int MODE>
+__device__ __forceinline__ SeqInfo<MODE> seq_info(const ChunkArgs& a, int b, bool tell) {
+  if constexpr (MODE == kShared) {
+    const int4 u = a.entries[b].u, v = a.entries[b].v;
+    return {u.x, u.y, u.z, u.w, v.x, v.y, v.z};
+  } else {
+  SeqInfo<MODE> s;
   const int64_t q0 = __ldg(&a.q_start[b]), q1 = __ldg(&a.q_start[b + 1]);
   const int64_t T = __ldg(&a.seq_lens[b]), room = (int64_t)a.max_blocks * PAGE;
   const bool bad = q0 < 0 || q1 < q0 || q1 > a.total_q;
@@ -212,21 +228,59 @@ __device__ __forceinline__ SeqInfo seq_info(const ChunkArgs& a, int b, bool tell
   s.nq = bad ? 0 : (int)(q1 - q0);
   s.T = (int)(T < 0 ? 0 : (T > room ? room : T));
   return s;
+  }
 }
-__device__ __forceinline__ int row_tiles(const ChunkArgs& a, const SeqInfo& s) {
+template <int MODE>
+__device__ __forceinline__ int row_tiles(const ChunkArgs& a, const SeqInfo<MODE>& s) {
   return (int)(((int64_t)s.nq * a.H + ROWS - 1) / ROWS);
 }
-// keys that token i of the sequence sees
-__device__ __forceinline__ int limit_of(const ChunkArgs& a, const SeqInfo& s, int i) {
-  if (!a.causal) return s.T;
+// keys that token i of the sequence sees (with a window: before which its last one ends)
+template <int MODE>
+__device__ __forceinline__ int limit_of(const ChunkArgs& a, const SeqInfo<MODE>& s, int i) {
+  if constexpr (MODE == kPlain) {
+    if (!a.causal) return s.T;
+  }
+  if constexpr (MODE == kShared) {
+    if (!s.causal) return s.T;
+  }
   const int lim = s.T - s.nq + i + 1;
   return lim < 0 ? 0 : lim;
 }
-// key tiles of a row tile: those that its last row sees; one where it sees none, so
-// that its (empty) rows are written by the same path
-__device__ __forceinline__ int key_tiles(const ChunkArgs& a, const SeqInfo& s, int rt) {
+template <int MODE>
+__device__ __forceinline__ int first_token(const ChunkArgs& a, int rt) {
+  return (int)((uint32_t)(rt * ROWS) / (uint32_t)a.H);
+}
+template <int MODE>
+__device__ __forceinline__ int last_token(const ChunkArgs& a, const SeqInfo<MODE>& s, int rt) {
   const int64_t last = ((int64_t)rt * ROWS + ROWS - 1) / a.H;
-  const int lim = limit_of(a, s, last < s.nq ? (int)last : s.nq - 1);
+  return last < s.nq ? (int)last : s.nq - 1;
+}
+// A window's first key, of a row that sees keys up to lim.
+__device__ __forceinline__ int window_from(const ChunkArgs& a, int lim) { return lim > a.window ? lim - a.window : 0; }
+
+// The pages that a row tile reads, in order: all of them from the first; or with a window, the
+// first tokens' pages, then those from the first row's window on (its window begins first).
+template <int MODE>
+struct Pages {
+  __device__ __forceinline__ int at(int i) const { return i; }
+};
+template <>
+struct Pages<kWindow> {
+  int sinks, skip;  // pages of first tokens; pages between them and the window
+  __device__ __forceinline__ int at(int i) const { return i < sinks ? i : i + skip; }
+};
+// Key tiles of a row tile: those that its last row sees; one where it sees none, so
+// that its (empty) rows are written by the same path.
+template <int MODE>
+__device__ __forceinline__ int key_tiles(const ChunkArgs& a, const SeqInfo<MODE>& s, int rt, Pages<MODE>* pages) {
+  const int lim = limit_of(a, s, last_token(a, s, rt));
+  if constexpr (MODE == kWindow) {
+    const int from = window_from(a, limit_of(a, s, first_token<MODE>(a, rt))), wp = from / PAGE;
+    pages->sinks = ((a.n_sink < from ? a.n_sink : from) + PAGE - 1) / PAGE;
+    pages->skip = wp > pages->sinks ? wp - pages->sinks : 0;
+    const int n = (lim > 0 ? (lim - 1) / PAGE + 1 : 0) - pages->skip;
+    return n > 0 ? (n + 1) / 2 : 1;
+  }
   return lim > 0 ? (lim - 1) / TILE + 1 : 1;
 }
 
@@ -256,39 +310,158 @@ __device__ __forceinline__ int64_t plan_sum(int64_t v, int64_t* tmp, int64_t* to
   return v;
 }
 
+// Sequences that share a prefix.  The rows of a group's sequences lie behind one another, so that the
+// prefix is one more sequence, whose rows are the group's and which all of them see whole, and the
+// others keep the keys behind it; entry g is group g's prefix, entry G + b sequence b.  Either gives
+// parts (f32 o, l and M_g of every row), which the join adds up; a sequence that shares nothing
+// is as in a call without groups.
+//
+// The prefix is whole pages that every row of the group sees; a group takes part where its row tiles
+// are fewer together than apart by more than the parts cost: SHARE key tiles a row tile (its start, and
+// 256 rows of f32 written twice and read twice), and where its sequences have PART_ROWS rows on average
+// at most (above, they fill their row tiles, and little is saved).
+constexpr int PART_ROWS = 1024, SHARE = SWITCH + 10;
+
+__device__ __forceinline__ int64_t warp_sum(int64_t v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ int64_t warp_min(int64_t v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const int64_t u = __shfl_xor_sync(0xffffffffu, v, o);
+    v = u < v ? u : v;
+  }
+  return v;
+}
+
+__device__ void make_entries(const ChunkArgs& a, Plan* plan, int64_t* tmp) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int bad = 0;
+  for (int g = threadIdx.x; g < a.G; g += 1024) {
+    const int f = __ldg(&a.group_start[g]), l = __ldg(&a.group_start[g + 1]);
+    bad |= f < 0 || l < f || l > a.B;
+    a.entries[g].u = make_int4(0, 0, 0, 0);
+    a.entries[g].v = make_int4(0, 0, -1, 0);
+  }
+  for (int b = threadIdx.x; b < a.B; b += 1024) {
+    const SeqInfo<kPlain> s = seq_info<kPlain>(a, b, true);
+    a.entries[a.G + b].u = make_int4((int)s.q0, s.nq, s.T, b);
+    a.entries[a.G + b].v = make_int4(0, a.causal, -1, 0);
+  }
+  if (threadIdx.x == 0) plan->part_rows = 0;
+  bad = __syncthreads_or(bad);
+  if (bad && threadIdx.x == 0) atomicOr(a.err, ERR_BLOCK_TABLE);
+  if (bad || a.G == 0) return;  // (ranges that may overlap: nothing is shared)
+  // what each group would share, a warp per group
+  for (int g = warp; g < a.G; g += 32) {
+    const int f = __ldg(&a.group_start[g]), l = __ldg(&a.group_start[g + 1]);
+    int64_t P = __ldg(&a.shared_len[g]), apart = 0, tokens = 0, members = 0, q0 = INT32_MAX, row = INT32_MAX;
+    if (P < 0 && lane == 0) atomicOr(a.err, ERR_SEQ_LEN);
+    for (int b = f + lane; b < l; b += 32) {
+      const int4 u = a.entries[a.G + b].u;
+      // (a range that breaks the order has no query; nothing is shared then)
+      if (__ldg(&a.q_start[b + 1]) - __ldg(&a.q_start[b]) != u.y) P = 0;
+      if (u.y == 0) continue;
+      const int64_t see = a.causal ? (int64_t)u.z - u.y + 1 : u.z;
+      P = see < P ? see : P;
+      apart += ((int64_t)u.y * a.H + ROWS - 1) / ROWS;
+      tokens += u.y;
+      ++members;
+      if (row == INT32_MAX) row = b;  // (a sequence without queries need not hold the prefix)
+      q0 = u.x < q0 ? u.x : q0;
+    }
+    P = warp_min(P);
+    q0 = warp_min(q0);
+    row = warp_min(row);
+    apart = warp_sum(apart);
+    tokens = warp_sum(tokens);
+    members = warp_sum(members);
+    P = P > 0 ? P / PAGE : 0;
+    const int64_t rows = tokens * a.H, together = (rows + ROWS - 1) / ROWS, tiles = (P + 1) / 2;
+    const bool take = members > 1 && P > 0 && rows <= PART_ROWS * members && together * (tiles + SHARE) < apart * tiles;
+    if (take && lane == 0) {
+      a.entries[g].u = make_int4((int)q0, (int)tokens, (int)P * PAGE, (int)row);
+      a.entries[g].v = make_int4(0, 0, 0, 0);
+    }
+  }
+  __syncthreads();
+  // the rows of their parts, as far as there is room
+  int64_t at = 0;
+  for (int g0 = 0; g0 < a.G; g0 += 1024) {
+    const int g = g0 + threadIdx.x;
+    const int64_t rows = g < a.G ? (int64_t)a.entries[g].u.y * a.H : 0;
+    int64_t sum;
+    const int64_t from = at + plan_sum(rows, tmp, &sum) - rows;
+    if (rows > 0) {
+      // (the groups that have room are the first ones: those behind one without begin further on)
+      if (from + rows <= a.part_rows) {
+        a.entries[g].v.z = (int)from;
+        atomicMax(reinterpret_cast<unsigned long long*>(&plan->part_rows), (unsigned long long)(from + rows));
+      } else {
+        a.entries[g].u.y = 0;
+      }
+    }
+    at += sum;
+  }
+  __syncthreads();
+  for (int g = warp; g < a.G; g += 32) {
+    const int4 u = a.entries[g].u;
+    if (u.y == 0) continue;
+    const int f = __ldg(&a.group_start[g]), l = __ldg(&a.group_start[g + 1]), from = a.entries[g].v.z;
+    for (int b = f + lane; b < l; b += 32) {
+      int4 m = a.entries[a.G + b].u;
+      if (m.y == 0) continue;
+      const int token = m.x - u.x;
+      m.z -= u.z;
+      a.entries[a.G + b].u = m;
+      a.entries[a.G + b].v = make_int4(u.z / PAGE, a.causal, (int)a.part_rows + from + token * a.H, 0);
+      for (int i = 0; i < m.y; ++i) a.part_seq[from / a.H + token + i] = make_int2(g, b);
+    }
+  }
+  __syncthreads();
+}
+
 constexpr int PLAN_NEAR = 4096;
 
 // One CTA: row tiles before each sequence (base, in shared memory if they fit), the units of every row tile,
 // their total, and the row tile that each cluster's range starts in.
+template <int MODE>
 __global__ void __launch_bounds__(1024) plan_kernel(const ChunkArgs a, Plan* plan, int64_t* base, int clusters) {
   grid_dependents_launch();
   __shared__ int64_t tmp[32];
-  __shared__ int64_t near[PLAN_NEAR];
-  if (a.B < PLAN_NEAR) base = near;
+  __shared__ int64_t near[MODE == kShared ? 1 : PLAN_NEAR];  // (the join reads it of a shared call)
+  if constexpr (MODE != kShared) {
+    if (a.B < PLAN_NEAR) base = near;
+  }
   if (threadIdx.x == 0) *a.err = 0;
   __syncthreads();
+  const int n_seq = MODE == kShared ? a.G + a.B : a.B;
+  if constexpr (MODE == kShared) make_entries(a, plan, tmp);
   int64_t pairs = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 1024) {
+  for (int b0 = 0; b0 < n_seq; b0 += 1024) {
     const int b = b0 + threadIdx.x;
-    const int64_t n = b < a.B ? row_tiles(a, seq_info(a, b, true)) : 0;
+    const int64_t n = b < n_seq ? row_tiles(a, seq_info<MODE>(a, b, true)) : 0;
     int64_t sum;
     const int64_t inc = plan_sum(n, tmp, &sum);
-    if (b < a.B) base[b] = pairs + inc - n;
+    if (b < n_seq) base[b] = pairs + inc - n;
     pairs += sum;
   }
-  if (threadIdx.x == 0) base[a.B] = pairs;
+  if (threadIdx.x == 0) base[n_seq] = pairs;
   __syncthreads();
   int b = 0, rt = 0;
   auto tiles = [&](int64_t p) -> int64_t {
     if (p >= pairs) return 0;
-    int lo = 0, hi = a.B;
+    int lo = 0, hi = n_seq;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (base[mid] <= p) lo = mid; else hi = mid;
     }
     b = lo;
     rt = (int)(p - base[lo]);
-    return key_tiles(a, seq_info(a, b, false), rt);
+    Pages<MODE> pages;
+    return key_tiles(a, seq_info<MODE>(a, b, false), rt, &pages);
   };
   // The ranges are equal on an axis where a row tile is SWITCH + nt long, and the border falls on a
   // key tile of it; x counts units (key tiles).
@@ -301,6 +474,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const ChunkArgs a, Plan* pla
   if (threadIdx.x == 0) {
     plan->n_clusters = nc;
     plan->units = units;
+    if (MODE == kShared) a.unit[pairs] = units;
   }
   int64_t at = 0;
   for (int64_t p0 = 0; p0 < pairs; p0 += 1024) {
@@ -308,6 +482,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const ChunkArgs a, Plan* pla
     int64_t sum;
     const int64_t before = at + plan_sum(n, tmp, &sum) - n;  // units before the row tile
     const int64_t S = before + p * SWITCH, len = n + SWITCH;
+    if (MODE == kShared && p < pairs) a.unit[p] = before;
     int64_t k = n > 0 ? S * nc / total : nc;
     while (k < nc && k * total / nc < S) ++k;
     for (; k < nc; ++k) {
@@ -327,8 +502,9 @@ __global__ void __launch_bounds__(1024) plan_kernel(const ChunkArgs a, Plan* pla
 
 // A cluster's way through its range: one segment (a run of key tiles of one row tile)
 // after the other.
-struct Walk {
-  SeqInfo s;
+template <int MODE>
+struct Walk : Pages<MODE> {
+  SeqInfo<MODE> s;
   int b, rt, nt, t;   // row tile, its key tiles, first key tile of the segment
   int n;              // key tiles of the segment
   int seg;            // segments before this one
@@ -341,7 +517,8 @@ struct Walk {
     t = e.off;
     left = (k + 1 < plan.n_clusters ? plan.e[k + 1].x : plan.units) - e.x;
     seg = 0;
-    s = seq_info(a, b, false);
+    s = seq_info<MODE>(a, b, false);
+    if constexpr (MODE == kWindow) (void)key_tiles(a, s, rt, this);
     n = (int)(left < nt - t ? left : nt - t);
   }
   __device__ __forceinline__ bool more() const { return left > 0; }
@@ -353,28 +530,41 @@ struct Walk {
     if (++rt >= row_tiles(a, s)) {
       rt = 0;
       do {
-        s = seq_info(a, ++b, false);
+        s = seq_info<MODE>(a, ++b, false);
       } while (s.nq == 0);
     }
-    nt = key_tiles(a, s, rt);
+    nt = key_tiles(a, s, rt, this);
     n = (int)(left < nt ? left : nt);
   }
   __device__ __forceinline__ bool whole() const { return t == 0 && n == nt; }
+  // whether the row tile's results are final (and not parts that the join adds up)
+  __device__ __forceinline__ bool final() const {
+    if constexpr (MODE == kShared) {
+      if (s.part >= 0) return false;
+    }
+    return whole();
+  }
 };
 
-static_assert(sizeof(Walk) * N_LANE_WARPS <= OFF_SC - OFF_WALK, "segments");
+static_assert(sizeof(Walk<kShared>) * N_LANE_WARPS <= OFF_SC - OFF_WALK && sizeof(Walk<kWindow>) <= sizeof(Walk<kShared>),
+              "segments");
 
-// The block-table entries of 32 pages, one per lane, from page `from` on.
+// The block-table entries of 32 of a row tile's pages, one per lane, from page `from` on.
 struct PageWindow {
   int64_t from;
   int32_t e;
   // cache slot of the page's first row, or -1 (past the sequence, or an entry out of range)
-  __device__ __forceinline__ int64_t slot(const ChunkArgs& a, const Walk& w, int64_t page, int lane, bool tell) {
+  template <int MODE>
+  __device__ __forceinline__ int64_t slot(const ChunkArgs& a, const Walk<MODE>& w, int64_t page, int lane, bool tell) {
     if (page < from || page >= from + 32) {
       from = page;
       e = -1;
-      if ((page + lane) * PAGE < w.s.T) {
-        e = __ldg(&a.block_table[(int64_t)w.b * a.max_blocks + page + lane]);
+      const int64_t at = MODE == kWindow ? w.at((int)page + lane) : page + lane;
+      if (at * PAGE < w.s.T) {
+        if constexpr (MODE == kShared)
+          e = __ldg(&a.block_table[(int64_t)w.s.row * a.max_blocks + w.s.page0 + at]);
+        else
+          e = __ldg(&a.block_table[(int64_t)w.b * a.max_blocks + at]);
         if (e < 0 || (int64_t)e >= a.n_blocks) {
           if (tell) atomicOr(a.err, ERR_BLOCK_TABLE);
           e = -1;
@@ -456,8 +646,18 @@ struct Workspace {
   float* m;   // [2 MAX_CLUSTERS][256]: slot 2k the first segment of cluster k, 2k + 1 its last
   float* l;
   float* o;   // [..][256][512]
+  int64_t parts;  // (shared prefixes) behind the slots: the parts of row tiles that one cluster held whole
+  // where the parts of row `row` of a row tile go, as a row of these arrays
+  template <int MODE>
+  __device__ __forceinline__ int64_t part_row(const Walk<MODE>& w, int k, int row) const {
+    if constexpr (MODE == kShared) {
+      if (w.whole()) return parts + w.s.part + (int64_t)w.rt * ROWS + row;
+    }
+    return (int64_t)(2 * k + (w.seg == 0 ? 0 : 1)) * ROWS + row;
+  }
 };
 
+template <int MODE>
 __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
     chunk_kernel(const ChunkArgs a, const Workspace ws, const __grid_constant__ CUtensorMap kmap,
                  const __grid_constant__ CUtensorMap rmap, const __grid_constant__ CUtensorMap smap) {
@@ -520,7 +720,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
   grid_dependency_wait();  // the plan
   grid_dependents_launch();  // (the join kernel may come as soon as there is room)
   const bool work = k < ws.plan->n_clusters;
-  Walk w;
+  Walk<MODE> w;
   if (work) w.start(a, *ws.plan, k);
   else w.left = 0;
   int gt = 0;  // key tiles of the range before this segment
@@ -592,7 +792,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
       bool ok = true;
       for (; ok && w.more(); w.next(a)) {
         // (and meanwhile the next row tile's queries come into L2)
-        Walk wn = w;
+        Walk<MODE> wn = w;
         wn.next(a);
         if (wn.more()) {
           const int64_t r0 = (int64_t)wn.rt * ROWS + rank * CROWS, rows = (int64_t)wn.s.nq * a.H;
@@ -717,7 +917,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
       float* mgs = reinterpret_cast<float*>(sm + OFF_MG);
       int* lim = reinterpret_cast<int*>(sm + OFF_LIM);
       float* cs = reinterpret_cast<float*>(sm + OFF_C);
-      Walk* walk = reinterpret_cast<Walk*>(sm + OFF_WALK) + (warp - W_LANE);  // (it has no registers to spare)
+      Walk<MODE>* walk = reinterpret_cast<Walk<MODE>*>(sm + OFF_WALK) + (warp - W_LANE);  // (it has no registers to spare)
       const int rh = row0 + 16 * hl;          // the thread's rows of a tile: rh, rh + 8
       const int mh = rh + 8 * (i4 & 1);       // the row this lane speaks for there
       uint32_t px = 0;
@@ -729,7 +929,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
       // The queries of a row tile: two e4m3 terms on the scale that puts a row's largest value
       // in [128, 256); c folds the scale back in, with sm_scale log2 e. Two of the thread's rows
       // at a time, their channels all in flight at once.
-      auto load_query = [&](const Walk& x) -> bool {
+      auto load_query = [&](const Walk<MODE>& x) -> bool {
         const int64_t r0 = (int64_t)x.rt * ROWS + rank * CROWS, rows = (int64_t)x.s.nq * a.H;
         const uint32_t qlo = smem_u32(sm + OFF_QL) + part * OP_ATOM, qrp = smem_u32(sm + OFF_QR);
         if (part == 0) {  // the keys that row q * 32 + lane sees (rows past the last one are copies of it)
@@ -822,7 +1022,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
       if (more) *walk = w;  // (every lane, the same)
       __syncwarp();
       while (ok && more) {
-        const Walk& x = *walk;
+        const Walk<MODE>& x = *walk;
         ok = load_query(x) && quarter_sync();  // (the sync: cs and lim are read by every part)
         if (!ok) break;
         const int n_tiles = x.n;
@@ -836,9 +1036,12 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
         }
         int t0 = x.t * TILE + sub * SUB;
         const int first = lim[q * 32 + 16 * hl];  // the keys that the first of the rows sees
+        // (a window: where that of the last of the rows begins)
+        const int from = MODE == kWindow ? window_from(a, lim[q * 32 + 16 * hl + 15]) : 0;
 #pragma unroll 1
         for (int i = 0; i < n_tiles; ++i, t0 += TILE) {
           const int g = gt + i, buf = g & 1, sc = g % NSC;
+          if constexpr (MODE == kWindow) t0 = x.at(2 * (x.t + i) + sub) * PAGE;
           if (!wait(B_SFULL + buf, (uint32_t)(g >> 1))) {
             ok = false;
             break;
@@ -882,15 +1085,20 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
           auto pair = [&](int p, int j) -> uint64_t {
             return pk2(__uint_as_float(u[4 * j + 2 * p]), __uint_as_float(u[4 * j + 2 * p + 1]));
           };
-          if (!here || first - t0 < SUB) {  // some row does not see all of this page
+          // some row does not see all of this page
+          if (!here || first - t0 < SUB || (MODE == kWindow && t0 < from && a.n_sink - t0 < SUB)) {
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
               const int n = here ? lim[rh + 8 * p] - t0 - 2 * i4 : 0;
+              // (and of the keys before `after`, those from `sinks` on are behind the window)
+              const int after = MODE == kWindow ? window_from(a, lim[rh + 8 * p]) - t0 - 2 * i4 : 0;
+              const int sinks = MODE == kWindow ? a.n_sink - t0 - 2 * i4 : 0;
 #pragma unroll
               for (int j = 0; j < 8; ++j)
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
-                  if (8 * j + e >= n) u[4 * j + 2 * p + e] = 0xFF800000u;  // -inf
+                  if (8 * j + e >= n || (MODE == kWindow && 8 * j + e < after && 8 * j + e >= sinks))
+                    u[4 * j + 2 * p + e] = 0xFF800000u;  // -inf
             }
           }
           // the largest weight of row `mh` over the page: the two rows' over this thread's
@@ -987,15 +1195,18 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
           const float L = xl[hh * 2] * (m0 == mm ? 1.f : ex2_approx(m0 - mm)) +
                           xl[hh * 2 + 1] * (m1 == mm ? 1.f : ex2_approx(m1 - mm));
           float f = 1.f;
-          if (x.whole()) {
+          if (x.final()) {
             f = L == 0.f ? 0.f : 1.f / L;  // (a NaN stays one)
             const int64_t r = (int64_t)x.rt * ROWS + rank * CROWS + hh;
             if (a.lse != nullptr && r < (int64_t)x.s.nq * a.H)
               a.lse[x.s.q0 * a.H + r] = L == 0.f ? -INFINITY : (M + log2f(L)) * LN2;
           } else {
-            const int64_t at = (int64_t)(2 * k + (x.seg == 0 ? 0 : 1)) * ROWS + rank * CROWS + hh;
-            ws.m[at] = M;
-            ws.l[at] = L;
+            const int row = rank * CROWS + hh;
+            const int64_t at = ws.part_row(x, k, row);
+            if (MODE != kShared || (int64_t)x.rt * ROWS + row < (int64_t)x.s.nq * a.H) {
+              ws.m[at] = M;
+              ws.l[at] = L;
+            }
           }
           const int rf = x.seg % NRF;
           const uint32_t to = map_to(smem_u32(sm + OFF_RF + (rf * CROWS + hh) * 8), rank + 2);
@@ -1004,7 +1215,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
           st_async_b32(to + 4, __float_as_uint(mm), bar);
         }
         gt += n_tiles;
-        Walk wn = x;
+        Walk<MODE> wn = x;
         wn.next(a);
         more = wn.more();
         __syncwarp();
@@ -1126,7 +1337,9 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
       const uint32_t rs = map_to(smem_u32(&bars[B_RS]), 2);
       bool ok = true;
       for (; ok && w.more(); w.next(a)) {
-        const int lim0 = limit_of(a, w.s, (int)((uint32_t)(w.rt * ROWS) / (uint32_t)a.H));  // the tile's first row sees least
+        const int lim0 = limit_of(a, w.s, first_token<MODE>(a, w.rt));  // the tile's first row sees least
+        // (a window: that of the tile's last row begins last)
+        const int from = MODE == kWindow ? window_from(a, limit_of(a, w.s, last_token(a, w.s, w.rt))) : 0;
         float ref = -INFINITY, hi = -INFINITY;  // the row's reference in O, and the highest one so far
         for (int i = 0; i < w.n; ++i) {
           const int g = gt + i, pb = g & 1, vs = g % NVT;
@@ -1187,7 +1400,16 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
             sts128(opnd + off, make_uint4(hw[0], hw[1], hw[2], hw[3]));
             sts128(opnd + OP_ATOM + off, make_uint4(lw[0], lw[1], lw[2], lw[3]));
           }
-          if (w.t + i + 1 > lim0 / TILE || pages != 3u) {
+          bool part_seen = w.t + i + 1 > lim0 / TILE;
+          if constexpr (MODE == kWindow) {
+            part_seen = false;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int t0 = w.at(2 * (w.t + i) + h) * PAGE;
+              part_seen |= lim0 - t0 < PAGE || (t0 < from && a.n_sink - t0 < PAGE);
+            }
+          }
+          if (part_seen || pages != 3u) {
             // some row does not see all of this tile: no NaN code may stay in it
             if (!wait(B_VT + vs, (uint32_t)(g / NVT))) {
               ok = false;
@@ -1248,7 +1470,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
         const float f = f2.x, up = ref == f2.y ? 1.f : ex2_approx(ref - f2.y);  // (O onto the reference of l)
         // 64 bytes of every row at a time (32 columns of bf16, or 16 of a partial's f32) through
         // shared memory, so that a warp's stores write whole sectors: eight rows each
-        const bool whole = w.whole();
+        const bool whole = w.final();
         const int64_t r0 = (int64_t)w.rt * ROWS + half_of * CROWS + q * 32;  // the warp's first row
         const int64_t rows = (int64_t)w.s.nq * a.H - r0;
         const int left = (int)(rows < 32 ? rows : 32) - (lane >> 2);         // rows from this lane's first on, by eights
@@ -1257,8 +1479,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
         const uint32_t take = stage + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
         const int row_bytes = whole ? DL * 2 : DL * 4;
         uint8_t* dst = (whole ? reinterpret_cast<uint8_t*>(a.out + (w.s.q0 * a.H + r0) * DL)
-                              : reinterpret_cast<uint8_t*>(
-                                    ws.o + ((int64_t)(2 * k + (w.seg == 0 ? 0 : 1)) * ROWS + half_of * CROWS + q * 32) * DL)) +
+                              : reinterpret_cast<uint8_t*>(ws.o + ws.part_row(w, k, half_of * CROWS + q * 32) * DL)) +
                        (lane >> 2) * row_bytes + (lane & 3) * 16;
         auto flush = [&](int byte) {
           __syncwarp();
@@ -1331,8 +1552,101 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
 constexpr int JOIN_BLOCKS = ROWS / 8;
 constexpr int FEW_ROW_TILES = 8;
 
-template <int SPLIT>
-__global__ void __launch_bounds__(256) join_kernel(const ChunkArgs a, const Workspace ws) {
+// A row of a group with a shared prefix: the parts of the prefix and of the rest, each one whole row
+// tile's or those that range borders cut it into, by one warp.
+__device__ __forceinline__ void join_parts(const ChunkArgs& a, const Workspace& ws, const int64_t* base, int64_t row,
+                                           int lane) {
+  const int64_t nc = ws.plan->n_clusters;
+  const int2 of = a.part_seq[row / a.H];
+  // where the ranges begin, two a lane (behind the last: never)
+  int64_t xs[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) xs[h] = lane + 32 * h < nc ? ws.plan->e[lane + 32 * h].x : INT64_MAX;
+  int64_t from[2];   // the parts' row in the slots of cluster 0, or of the whole
+  int k0[2], n[2];   // their clusters (n = 0: the row tile is whole), and the first of them's slot
+  bool second[2];
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    const int v = which == 0 ? of.x : a.G + of.y;
+    const int part = a.entries[v].v.z;
+    const int64_t r = row + (which == 0 ? 0 : a.part_rows) - part;  // row of the entry
+    const int64_t p = base[v] + r / ROWS, S = a.unit[p], E = a.unit[p + 1];
+    int first = -1, last = -1;  // the last range that begins at S or before, and before E
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      first += __popc(__ballot_sync(0xffffffffu, xs[h] <= S));
+      last += __popc(__ballot_sync(0xffffffffu, xs[h] < E));
+    }
+    const int64_t x0 = __shfl_sync(0xffffffffu, first < 32 ? xs[0] : xs[1], first & 31);
+    k0[which] = first;
+    second[which] = x0 < S;
+    n[which] = last - first + 1;
+    from[which] = r % ROWS;
+    if (n[which] == 1) from[which] = ws.parts + part + r;
+  }
+  // a lane per part: its reference, its sum (a cluster without units has no part)
+  float m[2][2], wt[2][2], M = -INFINITY, L = 0.f;
+  uint32_t has[2][2];
+  auto slot = [&](int which, int j) -> int64_t {
+    return n[which] == 1 ? from[which] : (int64_t)(2 * (k0[which] + j) + (j == 0 && second[which] ? 1 : 0)) * ROWS + from[which];
+  };
+#pragma unroll
+  for (int which = 0; which < 2; ++which)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int j = lane + 32 * h, k = k0[which] + j;
+      const int64_t x0 = __shfl_sync(0xffffffffu, xs[0], k & 31), x1 = __shfl_sync(0xffffffffu, xs[1], k & 31);
+      const int64_t y0 = __shfl_sync(0xffffffffu, xs[0], (k + 1) & 31), y1 = __shfl_sync(0xffffffffu, xs[1], (k + 1) & 31);
+      const bool there = j < n[which] && (k < 32 ? x0 : x1) != (k + 1 < 32 ? y0 : (k + 1 < 64 ? y1 : INT64_MAX));
+      m[which][h] = there ? ws.m[slot(which, j)] : -INFINITY;
+      wt[which][h] = there ? ws.l[slot(which, j)] : 0.f;
+      has[which][h] = __ballot_sync(0xffffffffu, there);
+      M = fmaxf(M, m[which][h]);
+    }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float4 acc[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int which = 0; which < 2; ++which)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float l = wt[which][h], f = m[which][h] > -INFINITY ? ex2_approx(m[which][h] - M) : 1.f;  // (a NaN l stays one)
+      L += f * l;
+      const int parts = min(n[which] - 32 * h, 32);
+#pragma unroll 2
+      for (int i = 0; i < parts; ++i) {
+        const float w = __shfl_sync(0xffffffffu, f, i);
+        if (!((has[which][h] >> i) & 1u)) continue;
+        const float4* o = reinterpret_cast<const float4*>(ws.o + slot(which, 32 * h + i) * DL) + lane;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float4 v = o[32 * c];
+          acc[c].x += w * v.x;
+          acc[c].y += w * v.y;
+          acc[c].z += w * v.z;
+          acc[c].w += w * v.w;
+        }
+      }
+    }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  const int4 u = a.entries[of.x].u;
+  const int64_t at = (int64_t)u.x * a.H + row - a.entries[of.x].v.z;
+  uint2* out = reinterpret_cast<uint2*>(a.out + at * DL) + lane;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(acc[c].x * inv, acc[c].y * inv);
+    const __nv_bfloat162 y = __floats2bfloat162_rn(acc[c].z * inv, acc[c].w * inv);
+    out[32 * c] = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+  }
+  if (a.lse != nullptr && lane == 0) a.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * LN2;
+}
+
+template <int MODE, int SPLIT>
+__global__ void __launch_bounds__(256) join_kernel(const ChunkArgs a, const Workspace ws, const int64_t* base, int cut_blocks) {
   static_assert(MAX_CLUSTERS <= 64, "two parts a lane");
   const int k = (int)blockIdx.x / (JOIN_BLOCKS * SPLIT) + 1, lane = threadIdx.x & 31;
   const int row = (int)blockIdx.x % (JOIN_BLOCKS * SPLIT) / SPLIT * 8 + (threadIdx.x >> 5);
@@ -1340,6 +1654,13 @@ __global__ void __launch_bounds__(256) join_kernel(const ChunkArgs a, const Work
   // (every block waits, with a row or without: the plan's and the parts' visibility, and that this
   // launch is not over before the chunk kernel is, come with the wait)
   grid_dependency_wait();
+  if constexpr (MODE == kShared) {
+    if ((int)blockIdx.x >= cut_blocks) {  // (behind the blocks for the row tiles that were cut)
+      const int64_t r = (int64_t)((int)blockIdx.x - cut_blocks) * 8 + (threadIdx.x >> 5);
+      if (r < ws.plan->part_rows) join_parts(a, ws, base, r, lane);
+      return;
+    }
+  }
   const int64_t nc = ws.plan->n_clusters;
   if (k >= nc) return;
   __shared__ int64_t xs[MAX_CLUSTERS + 1];    // the units where the ranges begin
@@ -1348,7 +1669,10 @@ __global__ void __launch_bounds__(256) join_kernel(const ChunkArgs a, const Work
   __syncthreads();
   const int64_t S = e.x - e.off;              // the row tile's first unit
   const int64_t xp = xs[k - 1];
-  const SeqInfo s = seq_info(a, e.b, false);
+  const SeqInfo<MODE> s = seq_info<MODE>(a, e.b, false);
+  if constexpr (MODE == kShared) {
+    if (s.part >= 0) return;
+  }
   const int64_t r = (int64_t)e.rt * ROWS + row;
   // (not whole, nor begun before cluster k - 1)
   const bool mine = e.off != 0 && xp <= S && r < (int64_t)s.nq * a.H;
@@ -1419,52 +1743,80 @@ __global__ void __launch_bounds__(256) join_kernel(const ChunkArgs a, const Work
 constexpr int64_t OFF_PLAN = 256, OFF_BASE = 2048;
 static_assert(OFF_PLAN + sizeof(Plan) <= OFF_BASE, "plan area");
 
-int64_t most_row_tiles(int B, int H, int64_t total_q) { return total_q * H / ROWS + B; }
+// What the workspace of a call holds, behind the plan (from sizes alone).
+struct Layout {
+  int most;         // clusters that a call of these sizes can use, whatever the lengths turn out to be
+  int64_t tiles;    // row tiles at most
+  int64_t part_rows;
+  int64_t entries, unit, part_seq, m, rows, bytes;
+};
 
-// Clusters that a call of these sizes can use, whatever the lengths turn out to be.
-int most_clusters(int B, int H, int64_t total_q, int max_blocks) {
-  const int64_t keys = ((int64_t)max_blocks * PAGE + TILE - 1) / TILE;
-  const int64_t tiles = most_row_tiles(B, H, total_q), units = tiles * (keys > MIN_TILES ? keys : MIN_TILES) / MIN_TILES;
-  return (int)(units < 1 ? 1 : (units < MAX_CLUSTERS ? units : MAX_CLUSTERS));
+template <int MODE>
+Layout layout_of(int B, int H, int64_t total_q, int max_blocks, int G, int64_t window, int64_t n_sink) {
+  auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
+  Layout w;
+  int64_t keys = ((int64_t)max_blocks * PAGE + TILE - 1) / TILE;
+  w.tiles = total_q * H / ROWS + B;
+  if (MODE == kShared) w.tiles += total_q * H / ROWS + G;
+  if (MODE == kWindow) {  // (a row tile's tokens lie within ROWS of one another)
+    const int64_t seen = window + n_sink + ROWS + 4 * PAGE;
+    if (seen / TILE + 1 < keys) keys = seen / TILE + 1;
+  }
+  const int64_t units = w.tiles * (keys > MIN_TILES ? keys : MIN_TILES) / MIN_TILES;
+  w.most = (int)(units < 1 ? 1 : (units < MAX_CLUSTERS ? units : MAX_CLUSTERS));
+  w.part_rows = 0;
+  if (MODE == kShared && G > 0) {
+    const int64_t rows = total_q * H, few = (int64_t)PART_ROWS * B, cap = 1 << 20;
+    w.part_rows = rows < few ? rows : few;
+    if (w.part_rows > cap) w.part_rows = cap;
+  }
+  int64_t at = OFF_BASE + up((int64_t)(B + (MODE == kShared ? G : 0) + 1) * 8);
+  w.entries = at;
+  if (MODE == kShared) at += up((int64_t)(G + B) * (int64_t)sizeof(ChunkEntry));
+  w.unit = at;
+  if (MODE == kShared) at += up((w.tiles + 1) * 8);
+  w.part_seq = at;
+  if (MODE == kShared) at += up((w.part_rows / H + 1) * 8);
+  w.m = at;
+  w.rows = (w.most > 1 ? 2 * (int64_t)w.most * ROWS : 0) + 2 * w.part_rows;  // (one cluster cuts no row tile)
+  w.bytes = at + w.rows * (8 + DL * 4);
+  return w;
 }
 
-int64_t base_bytes(int B) { return ((int64_t)(B + 1) * 8 + 255) / 256 * 256; }
-
-}  // namespace
-
-int64_t chunk_workspace(int B, int H, int64_t total_q, int max_blocks) {
-  const int64_t most = most_clusters(B, H, total_q, max_blocks), rows = most > 1 ? 2 * most * ROWS : 0;  // (one cuts no row tile)
-  return OFF_BASE + base_bytes(B) + rows * (8 + DL * 4);
-}
-
-cudaError_t launch_chunk(ChunkArgs a, void* workspace, cudaStream_t s) {
+template <int MODE>
+cudaError_t launch(ChunkArgs a, void* workspace, cudaStream_t s) {
   static std::atomic<int> memo[MAX_DEVICES];
   int fit = 0;  // clusters that the device holds at once
   cudaError_t e = per_device(memo, [](int* v) {
-    cudaError_t r = cudaFuncSetAttribute(chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    cudaError_t r = cudaFuncSetAttribute(chunk_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (r != cudaSuccess) return r;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(NUM_SMS, 1, 1);
     cfg.blockDim = dim3(NTHREADS, 1, 1);
     cfg.dynamicSmemBytes = SMEM;
     int n = 0;
-    r = cudaOccupancyMaxActiveClusters(&n, chunk_kernel, &cfg);
+    r = cudaOccupancyMaxActiveClusters(&n, chunk_kernel<MODE>, &cfg);
     if (r != cudaSuccess) return r;
     if (n < 1) return cudaErrorLaunchOutOfResources;
     *v = n > MAX_CLUSTERS ? MAX_CLUSTERS : n;
     return cudaSuccess;
   }, &fit);
   if (e != cudaSuccess) return e;
-  const int most = most_clusters(a.B, a.H, a.total_q, a.max_blocks);
-  const int clusters = most < fit ? most : fit;
+  const Layout w = layout_of<MODE>(a.B, a.H, a.total_q, a.max_blocks, a.G, a.window, a.n_sink);
+  const int clusters = w.most < fit ? w.most : fit;
   char* p = static_cast<char*>(workspace);
   a.err = reinterpret_cast<unsigned*>(p);
+  a.entries = reinterpret_cast<ChunkEntry*>(p + w.entries);
+  a.unit = reinterpret_cast<int64_t*>(p + w.unit);
+  a.part_seq = reinterpret_cast<int2*>(p + w.part_seq);
+  a.part_rows = w.part_rows;
   Workspace ws;
   ws.plan = reinterpret_cast<Plan*>(p + OFF_PLAN);
   int64_t* base = reinterpret_cast<int64_t*>(p + OFF_BASE);
-  ws.m = reinterpret_cast<float*>(p + OFF_BASE + base_bytes(a.B));
-  ws.l = ws.m + 2 * most * ROWS;
-  ws.o = ws.l + 2 * most * ROWS;
+  ws.m = reinterpret_cast<float*>(p + w.m);
+  ws.l = ws.m + w.rows;
+  ws.o = ws.l + w.rows;
+  ws.parts = w.rows - 2 * w.part_rows;
   DecodeArgs d{};  // what the cache's tensor maps are made from
   d.codes = a.codes;
   d.scales = a.scales;
@@ -1474,14 +1826,31 @@ cudaError_t launch_chunk(ChunkArgs a, void* workspace, cudaStream_t s) {
   if ((e = make_cache_map(d, &kmap)) != cudaSuccess || (e = make_rc_map(d, &rmap)) != cudaSuccess ||
       (e = make_scale_map(d, &smap)) != cudaSuccess)
     return e;
-  plan_kernel<<<1, 1024, 0, s>>>(a, ws.plan, base, clusters);
+  plan_kernel<MODE><<<1, 1024, 0, s>>>(a, ws.plan, base, clusters);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  e = launch_after_prep(chunk_kernel, 4 * clusters, NTHREADS, SMEM, s, a, ws, kmap, rmap, smap);
-  if (e != cudaSuccess || clusters == 1) return e;
+  e = launch_after_prep(chunk_kernel<MODE>, 4 * clusters, NTHREADS, SMEM, s, a, ws, kmap, rmap, smap);
+  const unsigned part_blocks = (unsigned)((w.part_rows + 7) / 8);
+  if (e != cudaSuccess || (clusters == 1 && part_blocks == 0)) return e;
   const unsigned blocks = JOIN_BLOCKS * (clusters - 1);
-  if (most_row_tiles(a.B, a.H, a.total_q) < FEW_ROW_TILES)
-    return launch_after_prep(join_kernel<4>, 4 * blocks, 256, 0, s, a, ws);
-  return launch_after_prep(join_kernel<1>, blocks, 256, 0, s, a, ws);
+  if (w.tiles < FEW_ROW_TILES)
+    return launch_after_prep(join_kernel<MODE, 4>, 4 * blocks + part_blocks, 256, 0, s, a, ws, base, (int)(4 * blocks));
+  return launch_after_prep(join_kernel<MODE, 1>, blocks + part_blocks, 256, 0, s, a, ws, base, (int)blocks);
 }
+
+}  // namespace
+
+int64_t chunk_workspace(int B, int H, int64_t total_q, int max_blocks) {
+  return layout_of<kPlain>(B, H, total_q, max_blocks, 0, 0, 0).bytes;
+}
+int64_t window_workspace(int B, int H, int64_t total_q, int max_blocks, int window, int n_sink) {
+  return layout_of<kWindow>(B, H, total_q, max_blocks, 0, window, n_sink).bytes;
+}
+int64_t shared_workspace(int B, int H, int64_t total_q, int max_blocks, int G) {
+  return layout_of<kShared>(B, H, total_q, max_blocks, G, 0, 0).bytes;
+}
+
+cudaError_t launch_chunk(const ChunkArgs& a, void* workspace, cudaStream_t s) { return launch<kPlain>(a, workspace, s); }
+cudaError_t launch_window(const ChunkArgs& a, void* workspace, cudaStream_t s) { return launch<kWindow>(a, workspace, s); }
+cudaError_t launch_shared(const ChunkArgs& a, void* workspace, cudaStream_t s) { return launch<kShared>(a, workspace, s); }
 
 }  // namespace kv8

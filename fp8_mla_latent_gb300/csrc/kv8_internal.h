@@ -146,6 +146,22 @@ cudaError_t launch_prefill(const uint8_t* codes, const float* scales, const int6
                            int64_t n_slots, int64_t T, const uint16_t* w, int N, uint16_t* y,
                            float* k_rope, unsigned* err, cudaStream_t s);
 
+// The norm of rows with an output in 8 bits (norm.cu); rows are typed by a kv8_dtype, strides in elements.
+struct NormArgs {
+  const void* x;
+  const void* residual;      // or nullptr
+  void* residual_out;        // or nullptr
+  void* normed;              // or nullptr
+  const float* weight;
+  uint8_t* codes;
+  float* scales;             // [n_rows][n_groups]
+  int64_t x_stride, residual_stride, residual_out_stride, normed_stride, codes_stride;
+  int64_t n_rows;
+  int width, group, n_groups;  // group: channels of a scale, 0 for the whole row
+  float eps;
+};
+cudaError_t launch_norm(const NormArgs& a, int dtype, cudaStream_t s);
+
 // A page table and its reference counts (pages.cu).
 struct PageTable {
   int32_t* block_table;  // [B][max_blocks]
@@ -164,6 +180,11 @@ cudaError_t launch_pages_compact(const PageTable& t, int32_t* moves, int32_t* n_
 cudaError_t launch_pages_copy(uint8_t* codes, float* scales, int n_layers, int64_t n_slots, const int32_t* moves,
                               const int32_t* n_moves, int64_t max_moves, unsigned* err, cudaStream_t s);
 
+// A sequence of a call with shared prefixes (chunk.cu, SeqInfo): q0, nq, T, row; page0, causal, part, 0.
+struct ChunkEntry {
+  int4 u, v;
+};
+
 // The attention of a chunk of new tokens (chunk.cu).  Rows of a sequence are its
 // (token, head) pairs, token after token.
 struct ChunkArgs {
@@ -181,10 +202,23 @@ struct ChunkArgs {
   uint16_t* out;               // bf16 [total_q][H][512]
   float* lse;                  // [total_q][H] or nullptr
   unsigned* err;               // workspace header word
+  int window, n_sink;          // with a window
+  // sequences that share prefixes: G groups of consecutive ones; the rest lies in the workspace
+  const int32_t* group_start;  // [G + 1]
+  const int32_t* shared_len;   // [G]
+  int G;
+  ChunkEntry* entries;         // [G + B] the prefixes, the sequences
+  int64_t* unit;               // [row tiles + 1] units before each
+  int2* part_seq;              // group and sequence of the tokens that have parts
+  int64_t part_rows;           // room for their rows
 };
-// Bytes of workspace (deterministic in its arguments), and the call on them.
+// Bytes of workspace (deterministic in their arguments), and the calls on them.
 int64_t chunk_workspace(int B, int H, int64_t total_q, int max_blocks);
-cudaError_t launch_chunk(ChunkArgs a, void* workspace, cudaStream_t s);
+int64_t window_workspace(int B, int H, int64_t total_q, int max_blocks, int window, int n_sink);
+int64_t shared_workspace(int B, int H, int64_t total_q, int max_blocks, int G);
+cudaError_t launch_chunk(const ChunkArgs& a, void* workspace, cudaStream_t s);
+cudaError_t launch_window(const ChunkArgs& a, void* workspace, cudaStream_t s);
+cudaError_t launch_shared(const ChunkArgs& a, void* workspace, cudaStream_t s);
 
 cudaError_t launch_wait_timeout(unsigned* err, uint64_t limit_ns, cudaStream_t s);
 cudaError_t launch_wuv(const float* o, const uint16_t* w, int B, int H, int V, float* y,

@@ -145,6 +145,47 @@ int kv8_produce_rows(const float* src, int64_t n_rows, int64_t src_row_stride,
                      int64_t n_slots, unsigned* err_word, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * kv8_norm_quantize_rows -- the norm that opens a layer, with the residual's addition in front
+ * and the quantizer behind, in one pass over the rows.  The KV8 page has no counterpart; the
+ * 8-bit rows are those of kv8_quantize_rows.  For each row r, in f32:
+ *   t = x + residual                                  (rounded once)
+ *   y = (t * inv) * norm_weight,  inv = 1 / sqrt(sum_i t_i^2 / width + eps)
+ *   over the row (group == 0), or over every `group` channels of it, the last ones
+ *   perhaps fewer:  amax = max |y| over non-NaN entries;  scale = amax / 448;  code =
+ *   e4m3(y * (448 / amax)), with the rules of kv8_quantize_rows (448 / amax not finite:
+ *   signed zeros; NaN stored as 0x00).
+ * t and y are rounded to the rows' type where they are written, but not on their way to the
+ * codes.  A row whose sum of squares is NaN, or over the range of f32, has no finite y but
+ * zeros: codes and scales are 0 then.  The sum has a fixed order for given sizes, so the same
+ * call gives the same bits.
+ *
+ *   x             device [n_rows] rows of `width` values of dtype (a kv8_dtype), x_row_stride
+ *                 (elements, >= 0) apart.
+ *   residual      the same of residual_row_stride, or NULL (t = x).
+ *   residual_out  t in dtype, rows residual_out_row_stride apart, or NULL (and NULL where
+ *                 residual is).  It may be residual or x itself, with that one's stride.
+ *   norm_weight   device f32 [width], 4-byte aligned.
+ *   eps           finite, >= 0.
+ *   n_rows, width n_rows >= 0 (0 launches nothing), 1 <= width <= KV8_NORM_MAX_WIDTH.
+ *   group         0, 32, 64, 128 or 256.
+ *   normed        y in dtype, rows normed_row_stride apart, or NULL.  It may be x itself, with
+ *                 its stride, or residual where that is not residual_out.
+ *   codes         device uint8, rows codes_row_stride apart.
+ *   scales        device f32 [n_rows][1], or [n_rows][ceil(width / group)].
+ * Rows are aligned to their elements; strides of what is written are >= width.  Rows of whole
+ * eights of channels at 16-byte boundaries (codes: 8, norm_weight: 16) are the fast ones.
+ * Errors: KV8_EINVAL, KV8_EALIGN, KV8_EUNSUPPORTED (group, width), KV8_ECUDA.
+ * ------------------------------------------------------------------------- */
+typedef enum { KV8_BF16 = 0, KV8_F16 = 1, KV8_F32 = 2 } kv8_dtype;
+#define KV8_NORM_MAX_WIDTH 32768
+int kv8_norm_quantize_rows(const void* x, int64_t x_row_stride, const void* residual,
+                           int64_t residual_row_stride, void* residual_out,
+                           int64_t residual_out_row_stride, const float* norm_weight, float eps,
+                           int64_t n_rows, int width, int dtype, int group, void* normed,
+                           int64_t normed_row_stride, uint8_t* codes, int64_t codes_row_stride,
+                           float* scales, void* stream);
+
+/* ---------------------------------------------------------------------------
  * mla_wuv_epilogue -- the step after the absorbed attention (KV8 page, PR
  * description: in the absorbed attention the latent is key and value at once, so
  * the attention's output is a latent context per head): the per-head value
@@ -389,6 +430,65 @@ int mla_absorb_chunk_fp8_batch(const uint16_t* q_lat, int64_t q_lat_token_stride
                                int max_blocks, int block_size, int64_t n_blocks, int causal,
                                float sm_scale, uint16_t* out, float* lse, void* workspace,
                                int64_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * mla_absorb_window_fp8_batch -- the attention of mla_absorb_chunk_fp8_batch with a sliding
+ * window and first tokens that stay visible.  Token i of a sequence's n_b new ones, at position
+ * p = seq_lens[b] - n_b + i, sees keys
+ *   t <= p   with   t > p - window   or   t < n_sink.
+ * What no new token sees is neither read nor looked up: the table's entries of pages that hold
+ * only such keys may be anything, and the pages given to others.
+ *
+ *   window     >= 1 (itself among them).   n_sink  >= 0.
+ *   workspace  >= mla_absorb_window_fp8_batch_workspace_size(B, H, total_q, max_blocks, window,
+ *              n_sink) bytes.
+ * Everything else, the precision among it, is as for mla_absorb_chunk_fp8_batch with causal.
+ * Errors: KV8_EINVAL, KV8_EALIGN, KV8_EUNSUPPORTED, KV8_EWORKSPACE, KV8_ECUDA.
+ * ------------------------------------------------------------------------- */
+int64_t mla_absorb_window_fp8_batch_workspace_size(int B, int H, int64_t total_q, int max_blocks,
+                                                   int window, int n_sink);
+int mla_absorb_window_fp8_batch(const uint16_t* q_lat, int64_t q_lat_token_stride,
+                                int64_t q_lat_head_stride, const uint16_t* q_rope,
+                                int64_t q_rope_token_stride, int64_t q_rope_head_stride,
+                                const uint8_t* kv_codes, const float* kv_scales,
+                                const int32_t* block_table, const int32_t* seq_lens,
+                                const int32_t* q_start, int64_t total_q, int B, int H,
+                                int max_blocks, int block_size, int64_t n_blocks, int window,
+                                int n_sink, float sm_scale, uint16_t* out, float* lse,
+                                void* workspace, int64_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * mla_absorb_shared_fp8_batch -- the attention of mla_absorb_chunk_fp8_batch for sequences of
+ * which groups share a long prefix (as kv8_pages_fork makes them): the prefix is computed once
+ * for all rows of its group, the rest of each sequence by itself, and the two are joined.
+ *
+ *   group_start  device int32 [G + 1], non-decreasing within [0, B]: group g is sequences
+ *                group_start[g] .. group_start[g + 1] - 1.  Sequences outside every group share
+ *                nothing.  Ranges that break that set the error word (KV8_EBOUNDS), and nothing
+ *                is shared.
+ *   shared_len   device int32 [G]: the first shared_len[g] tokens of the group's sequences are
+ *                the same, and the table rows of those that have queries name the same pages for
+ *                the whole pages of them.  0 shares nothing; less than 0 sets the error word
+ *                (KV8_EBOUNDS) as well.
+ *   G            >= 0 (with 0, group_start and shared_len may be NULL).
+ *   workspace    >= mla_absorb_shared_fp8_batch_workspace_size(B, H, total_q, max_blocks, G) bytes.
+ * What is computed once is whole pages that every row of the group sees, and only where that is
+ * less work: the results are those of mla_absorb_chunk_fp8_batch within its precision in either
+ * case.  Everything else is as there.
+ * Errors: KV8_EINVAL, KV8_EALIGN, KV8_EUNSUPPORTED, KV8_EWORKSPACE, KV8_ECUDA.
+ * ------------------------------------------------------------------------- */
+int64_t mla_absorb_shared_fp8_batch_workspace_size(int B, int H, int64_t total_q, int max_blocks,
+                                                   int G);
+int mla_absorb_shared_fp8_batch(const uint16_t* q_lat, int64_t q_lat_token_stride,
+                                int64_t q_lat_head_stride, const uint16_t* q_rope,
+                                int64_t q_rope_token_stride, int64_t q_rope_head_stride,
+                                const uint8_t* kv_codes, const float* kv_scales,
+                                const int32_t* block_table, const int32_t* seq_lens,
+                                const int32_t* q_start, int64_t total_q, int B, int H,
+                                int max_blocks, int block_size, int64_t n_blocks,
+                                const int32_t* group_start, const int32_t* shared_len, int G,
+                                int causal, float sm_scale, uint16_t* out, float* lse,
+                                void* workspace, int64_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
  * Pages.  The calls below keep the page table of a paged cache on the device:

@@ -1,0 +1,175 @@
+"""The norm with the residual's addition and an output in 8 bits, against its definition in 64 bits."""
+import math
+
+import pytest
+import torch
+
+import fp8_mla_latent_gb300 as pkg
+from chunk_helpers import e4m3_values
+
+pytestmark = pytest.mark.gpu
+TYPES = [torch.bfloat16, torch.float16, torch.float32]
+EPS = 1e-6
+
+
+def inputs(n, w, dtype, seed=0, add=True):
+    g = torch.Generator().manual_seed(seed)
+    x = (torch.randn((n, w), generator=g) * 0.5).to(dtype).cuda()
+    r = (torch.randn((n, w), generator=g) * torch.exp(torch.randn(w, generator=g))).to(dtype).cuda() if add else None
+    return x, r, (1 + 0.2 * torch.randn(w, generator=g)).cuda()
+
+
+def check(x, r, weight, codes, scales, group, t_out=None, normed=None, eps=EPS):
+    """Every output within its roundings of the definition.  In f32 (u = 2^-24), t is off by u of itself.
+    The sum of w squares is off by (w / n + 12) u of itself at most, for n threads that add up w / n squares
+    each and ten steps between them, plus the squares' and t's 3 u; a thread holds at most 32 (and 64 in a
+    warp's row), so 80 u; 1 / sqrt halves that and adds 4 u; two products 2 u: y is off by e = 48 u.  A
+    scale adds u; what is rounded to a code is off by 2 e + 3 u <= 100 u.  A rounding is half a step of its type."""
+    u = 2.0 ** -24
+    n, w = x.shape
+    t = x.double() + (0 if r is None else r.double())
+    y = t / torch.sqrt((t * t).mean(1, keepdim=True) + eps) * weight.double()
+    if t_out is not None:
+        half = torch.finfo(x.dtype).eps / 2
+        assert ((t_out.double() - t).abs() <= (half + u) * t.abs() + 2.0 ** -25).all()
+    if normed is not None:
+        half = torch.finfo(x.dtype).eps / 2 if x.dtype != torch.float32 else 0
+        assert ((normed.double() - y).abs() <= (half + 48 * u) * y.abs() + 2.0 ** -25).all()
+    g = group or w
+    pad = -w % g
+    v = torch.nn.functional.pad(y, (0, pad)).unflatten(1, (-1, g))
+    s = v.abs().amax(-1) / 448
+    assert ((scales.double() - s).abs() <= 49 * u * s).all()
+    q = (v / s.clamp(min=1e-300)[..., None]).flatten(1)[:, :w]
+    got = e4m3_values("cuda")[codes.long()]
+    step = torch.exp2(torch.floor(torch.log2(q.abs().clamp(min=2.0 ** -6))) - 3)
+    assert ((got - q).abs() <= step / 2 + 100 * u * q.abs()).all()
+    assert (torch.signbit(got) == torch.signbit(q))[q != 0].all()
+
+
+def call(x, r, weight, group=0, **kw):
+    return pkg.kv8_norm_quantize_rows(x, weight, EPS, residual=r, group=group, **kw)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("w", [1, 2, 7, 8, 31, 33, 64, 127, 128, 255, 256, 257, 511, 512, 520, 576, 1000, 1024, 1501, 2048,
+                               4096, 7168, 8191, 8200, 16384, 16392, 32768])
+def test_widths(w, dtype):
+    for n, group, add in ((1, 0, True), (5, 128, True), (3, 32, False)):
+        x, r, weight = inputs(n, w, dtype, seed=w, add=add)
+        t, y = torch.empty_like(x), torch.empty_like(x)
+        codes, scales = call(x, r, weight, group, residual_out=t if add else None, normed=y)
+        check(x, r, weight, codes, scales, group, t if add else None, y)
+
+
+@pytest.mark.parametrize("group", [0, 32, 64, 128, 256])
+@pytest.mark.parametrize("n,w", [(1, 100), (3, 257), (40, 640), (333, 1501), (400, 2056), (200, 7168)])
+def test_groups_and_rows(n, w, group):
+    x, r, weight = inputs(n, w, torch.bfloat16, seed=n)
+    t = torch.empty_like(x)
+    codes, scales = call(x, r, weight, group, residual_out=t)
+    assert scales.shape == (n, -(-w // group) if group else 1)
+    check(x, r, weight, codes, scales, group, t)
+
+
+def test_many_rows():
+    x, r, weight = inputs(20000, 72, torch.bfloat16)
+    codes, scales = call(x, r, weight)
+    check(x, r, weight, codes, scales, 0)
+
+
+@pytest.mark.parametrize("w", [40, 512, 2000, 2001])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_strided_rows_and_what_lies_between_them(w, dtype):
+    """Rows of wider arrays, at 16-byte boundaries and at others; what lies between them stays as it is."""
+    for off, gap in ((0, 64), (8, 40), (3, 13)):
+        big = [torch.full((6, w + gap), 5.0, dtype=dtype, device="cuda") for _ in range(4)]
+        codes = torch.full((6, w + gap), 99, dtype=torch.uint8, device="cuda")
+        x, r, weight = inputs(6, w, dtype, seed=w + gap)
+        part = [b[:, off: off + w] for b in big]
+        part[0].copy_(x)
+        part[1].copy_(r)
+        want = call(x, r, weight, 64)
+        got = call(part[0], part[1], weight, 64, residual_out=part[2], normed=part[3], codes=codes[:, off: off + w])
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        check(x, r, weight, *got, 64, part[2], part[3])
+        for b, v in [(b, 5.0) for b in big] + [(codes, 99)]:
+            assert (b[:, :off] == v).all() and (b[:, off + w:] == v).all()
+
+
+def test_one_row_for_all():
+    """A residual (or input) that is one row, read again for every row."""
+    x, r, weight = inputs(9, 264, torch.bfloat16)
+    one = r[:1].expand(9, 264)
+    a, b = call(x, one, weight), call(x, one.contiguous(), weight)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("w", [64, 1000, 1001, 7168])
+def test_in_place(w):
+    x, r, weight = inputs(20, w, torch.bfloat16)
+    t, y = torch.empty_like(x), torch.empty_like(x)
+    want = call(x, r, weight, 128, residual_out=t, normed=y)
+    x2, r2 = x.clone(), r.clone()
+    got = call(x2, r2, weight, 128, residual_out=r2, normed=x2)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert torch.equal(r2, t) and torch.equal(x2, y)
+
+
+def test_the_same_bits_each_time_and_beside_other_rows():
+    """A row's outputs do not depend on its neighbours, at the same number of rows."""
+    x, r, weight = inputs(64, 1536, torch.bfloat16)
+    a = call(x, r, weight, 128)
+    b = call(x, r, weight, 128)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    x[1:], r[1:] = 3.0, -1.0
+    c = call(x, r, weight, 128)
+    assert torch.equal(a[0][0], c[0][0]) and torch.equal(a[1][0], c[1][0])
+
+
+@pytest.mark.parametrize("group", [0, 128])
+@pytest.mark.parametrize("w", [256, 261, 3000])
+def test_zeros_nan_and_infinities(w, group):
+    x, r, weight = inputs(6, w, torch.float32)
+    x[0], r[0] = 0.0, 0.0
+    x[1, 5] = math.nan
+    x[2, 7] = math.inf
+    x[3], r[3] = 1e30, 1e30           # the sum of squares is over the range
+    weight[3] = -0.0
+    weight[200] = math.nan
+    y = torch.empty_like(x)
+    codes, scales = call(x, r, weight, group, normed=y)
+    assert (codes[0, :3] == 0).all() and (scales[0] == 0).all()
+    for k in (1, 2, 3):
+        assert (codes[k] & 0x7F == 0).all() and (scales[k] == 0).all(), k
+    assert torch.isnan(y[1]).all() and torch.isnan(y[2, 7])
+    for k in (4, 5):                  # one column is NaN: code 0, not in the scale
+        assert codes[k, 200] == 0 and torch.isfinite(scales[k]).all() and (scales[k] > 0).all()
+        assert codes[k, 3] in (0, 0x80) and torch.isnan(y[k, 200])
+
+
+def test_subnormal_maximum():
+    """448 / amax is not finite: signed zeros, and the scale as computed."""
+    x = torch.tensor([[1.0, -1.0, 0.0, 2.0] * 16], device="cuda")
+    weight = torch.full((64,), 1e-39, device="cuda")
+    codes, scales = call(x, None, weight)
+    assert codes.flatten().tolist() == [0, 0x80, 0, 0] * 16
+    assert 0 < float(scales) < 1e-41
+
+
+def test_nothing_to_do():
+    x, r, weight = inputs(0, 64, torch.bfloat16)
+    codes, scales = call(x, r, weight)
+    assert codes.shape == (0, 64) and scales.shape == (0, 1)
+
+
+def test_captured():
+    x, r, weight = inputs(7, 2048, torch.bfloat16)
+    want = call(x, r, weight, 128)
+    codes, scales = torch.zeros_like(want[0]), torch.zeros_like(want[1])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(x, r, weight, 128, codes=codes, scales=scales)
+    codes.zero_()
+    g.replay()
+    assert torch.equal(codes, want[0]) and torch.equal(scales, want[1])

@@ -1,0 +1,207 @@
+"""Attention of sequences that share prefixes, against its definition in 64 bits."""
+import math
+
+import pytest
+import torch
+
+import fp8_mla_latent_gb300 as pkg
+from chunk_helpers import DL, PAGE, SM_SCALE
+from more_helpers import SharedCase
+
+pytestmark = pytest.mark.gpu
+
+
+def workspace(c):
+    return pkg.alloc_workspace(pkg.mla_absorb_shared_fp8_batch_workspace_size(
+        len(c.nq), c.H, c.q_lat.shape[0], c.max_blocks, c.shared_len.numel()))
+
+
+def run(c, causal=True, lse=True, ws=None):
+    rows = c.q_lat.shape[0]
+    ws = workspace(c) if ws is None else ws
+    out = torch.full((rows, c.H, DL), 7.0, dtype=torch.bfloat16, device="cuda")
+    l = torch.full((rows, c.H), 7.0, device="cuda") if lse else None
+    got = pkg.mla_absorb_shared_fp8_batch(*c.args(), SM_SCALE, c.group_start, c.shared_len, causal=causal, out=out,
+                                          lse=l, workspace=ws)
+    assert got is out
+    return out, l, pkg.kv8_workspace_error(ws)
+
+
+def check(c, causal=True, lse=True):
+    out, l, err = run(c, causal, lse)
+    assert err == 0
+    c.check(out, l, causal)
+    assert (out[sum(c.nq):] == 7).all() and (l is None or (l[sum(c.nq):] == 7).all()), "rows behind the last"
+    return out, l
+
+
+def chunk(c, causal=True):
+    l = torch.full(c.q_lat.shape[:2], 7.0, device="cuda")
+    out = torch.full((*c.q_lat.shape[:2], DL), 7.0, dtype=torch.bfloat16, device="cuda")
+    pkg.mla_absorb_chunk_fp8_batch(*c.args(), SM_SCALE, causal=causal, out=out, lse=l)
+    return out, l
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("H", [1, 3, 16, 64, 128, 130])
+def test_one_group(H, causal):
+    nq = [1, 1, 3, 1, 2, 1, 1, 5, 1, 1, 1, 1]
+    lens = [900 + (97 * i) % 300 for i in range(12)]
+    check(SharedCase(H, nq, lens, [12], [850], seed=H, pad=3), causal)
+
+
+@pytest.mark.parametrize("shared", [0, 1, 63, 64, 65, 127, 128, 640, 700, 704, 5000])
+def test_shared_lengths(shared):
+    """Around pages and tiles, and over the members' lengths; the shortest rows see no more than the prefix."""
+    lens = [704, 705, 768, 1000, 704, 720, 1500, 710]
+    check(SharedCase(16, [1] * 8, lens, [8], [shared], seed=shared))
+
+
+@pytest.mark.parametrize("H", [4, 20, 128])
+def test_several_groups_and_sequences_in_none(H):
+    sizes, shared = [3, 1, 0, 7, 9], [700, 900, 50, 1999, 1300]
+    lens = [750, 800, 702, 1000, *[2000 + 31 * i for i in range(7)], *[1301 + 64 * i for i in range(9)], 40, 300]
+    nq = [1 + (5 * i) % 4 for i in range(len(lens))]
+    check(SharedCase(H, nq, lens, sizes, shared, seed=H + 1, pad=5))
+
+
+def test_members_without_queries_or_tokens():
+    """The first member has neither: the prefix is read through the row of one that has queries."""
+    c = SharedCase(16, [0, 2, 0, 1, 1, 1, 2, 1], [0, 900, 70, 880, 900, 1000, 860, 990], [8], [850], seed=2)
+    check(c)
+
+
+def test_a_prefix_that_some_row_does_not_see():
+    """A chunk that begins inside the prefix: what every row of the group sees is computed once, no more."""
+    check(SharedCase(16, [1, 1, 300, 1, 1, 1], [900, 910, 1000, 920, 930, 940], [6], [850], seed=3))
+
+
+def test_prompts_that_fill_their_row_tiles():
+    check(SharedCase(128, [130, 70, 40], [700, 800, 900], [3], [600], seed=4))
+
+
+def test_long_prefix_over_all_clusters():
+    check(SharedCase(128, [1, 1, 2], [9000, 9100, 9050], [3], [8990], seed=5))
+
+
+def test_rows_that_see_nothing():
+    check(SharedCase(16, [5, 1, 1, 3], [2, 900, 900, 0], [4], [850], seed=6))
+
+
+def test_many_sequences_in_many_groups():
+    lens = [500 + (37 * i) % 300 for i in range(300)]
+    check(SharedCase(4, [1] * 300, lens, [5] * 60, [490] * 60, seed=7), lse=False)
+
+
+def test_a_prefix_is_computed_once():
+    """The other members' entries for it are not looked up where sharing pays."""
+    c = SharedCase(16, [1] * 16, [2000] * 16, [16], [1984], seed=8)
+    want, want_l = check(c)
+    c.table[1:, :31] = 2 ** 30
+    out, l, err = run(c)
+    assert err == 0 and torch.equal(out, want) and torch.equal(l, want_l)
+
+
+@pytest.mark.parametrize("groups", [[0, 3, 2, 8], [-1, 4, 8, 8], [0, 4, 8, 9], [5, 4, 3, 2]])
+def test_groups_that_cannot_be_are_told_and_share_nothing(groups):
+    c = SharedCase(16, [1] * 8, [900] * 8, [8], [850], seed=9)
+    want = chunk(c)
+    c.group_start = torch.tensor(groups, dtype=torch.int32, device="cuda")
+    c.shared_len = torch.tensor([850] * 3, dtype=torch.int32, device="cuda")
+    out, l, err = run(c)
+    assert err == -5 and torch.equal(out, want[0]) and torch.equal(l, want[1])
+
+
+def test_a_negative_length_is_told_and_shares_nothing():
+    c = SharedCase(16, [1] * 8, [900] * 8, [8], [850], seed=10)
+    want = chunk(c)
+    c.shared_len.fill_(-5)
+    out, l, err = run(c)
+    assert err == -5 and torch.equal(out, want[0]) and torch.equal(l, want[1])
+
+
+def test_without_groups_the_bits_of_chunk_attention():
+    c = SharedCase(16, [1, 40, 3], [900, 300, 70], [], [], seed=11, pad=4)
+    out, l, err = run(c)
+    want = chunk(c)
+    assert err == 0 and torch.equal(out, want[0]) and torch.equal(l, want[1])
+
+
+def test_a_bad_query_range_is_told():
+    """Its sequence has no query, the group shares nothing, and the others are right."""
+    c = SharedCase(16, [1] * 6, [900] * 6, [6], [850], seed=12)
+    want = chunk(c)
+    c.start[3] = 10 ** 6
+    out, l, err = run(c)
+    assert err == -5
+    assert torch.equal(out[:2], want[0][:2]) and torch.equal(out[4:], want[0][4:])
+
+
+def test_nan_in_the_prefix_and_in_one_sequence():
+    c = SharedCase(16, [1, 2, 1, 1, 1, 1, 1, 1], [1000] * 8, [8], [960], seed=13)
+    clean, clean_l = check(c)
+    slot = int(c.slots[2][990])
+    c.codes[slot] = 0x7F
+    c.scales[slot] = math.nan
+    out, l, _ = run(c)
+    hit = torch.zeros(9, dtype=torch.bool, device="cuda")
+    hit[3] = True
+    assert torch.isnan(out[hit]).all() and torch.isnan(l[hit]).all()
+    assert torch.equal(out[~hit], clean[~hit]) and torch.equal(l[~hit], clean_l[~hit])
+    c.codes[int(c.slots[0][100])] = 0x7F
+    out, l, _ = run(c)
+    assert torch.isnan(out).all() and torch.isnan(l).all()
+
+
+def test_a_dominant_token_in_the_prefix_or_behind_it():
+    """Parts of very different size are joined: 2^30 and more between their maxima."""
+    def rows(b, t, g):
+        x = 0.3 * torch.randn((t, 576), generator=g) + 0.5
+        x[5] *= 9 if b < 8 else 1
+        x[t - 3] *= 1 if b < 8 else 9
+        return x
+    c = SharedCase(32, [1] * 16, [1000 + i for i in range(16)], [8, 8], [970, 980], seed=14, rows=rows)
+    c.q_lat.copy_((c.q_lat.float() * 0.4 + 0.3).bfloat16())
+    check(c)
+
+
+def test_captured_and_replayed_with_lengths_that_change():
+    """One captured step over 5 more tokens of every sequence, the lengths read on the device."""
+    c = SharedCase(16, [1] * 10, [1100 + 7 * i for i in range(10)], [10], [1088], seed=15)
+    ws, full = workspace(c), c.lens.clone()
+    out, l = (torch.zeros_like(x) for x in check(c))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        pkg.mla_absorb_shared_fp8_batch(*c.args(), SM_SCALE, c.group_start, c.shared_len, out=out, lse=l, workspace=ws)
+    for back in (5, 3, 0):
+        c.lens.copy_(full - back)
+        g.replay()
+        want, want_l, err = run(c)
+        assert err == 0 and pkg.kv8_workspace_error(ws) == 0
+        assert torch.equal(out, want) and torch.equal(l, want_l)
+
+
+def test_fork_append_and_attend():
+    """Sequences made by the page calls: a prompt forked eight times, tokens appended, one step of attention."""
+    T, n, H = 1000, 8, 16
+    n_blocks, mb = 64, 24
+    g = torch.Generator().manual_seed(16)
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    table = torch.full((n + 1, mb), -1, dtype=torch.int32, device="cuda")
+    lens, refs = torch.zeros(n + 1, dtype=torch.int32, device="cuda"), torch.zeros(n_blocks, dtype=torch.int32, device="cuda")
+    codes = torch.full((n_blocks * PAGE, 576), 0x7F, dtype=torch.uint8, device="cuda")
+    scales = torch.full((n_blocks * PAGE, 2), math.nan, device="cuda")
+    _, slots = pkg.kv8_pages_append(table, lens, refs, i32(T, *[0] * n), cap=T)
+    pkg.kv8_quantize_rows(torch.randn((T, 576), generator=g).cuda(), codes, scales, slots)
+    moves, n_moves = pkg.kv8_pages_fork(table, lens, refs, i32(*[0] * n), i32(*range(1, n + 1)))
+    pkg.kv8_pages_copy(codes, scales, moves, n_moves)
+    start, slots = pkg.kv8_pages_append(table, lens, refs, i32(0, *[2] * n), cap=2 * n)
+    pkg.kv8_quantize_rows(torch.randn((2 * n, 576), generator=g).cuda(), codes, scales, slots)
+    q_lat = torch.randn((2 * n, H, 512), generator=g).bfloat16().cuda()
+    q_rope = torch.randn((2 * n, H, 64), generator=g).bfloat16().cuda()
+    args = (q_lat, q_rope, codes, scales, table, lens, start)
+    got = pkg.mla_absorb_shared_fp8_batch(*args, SM_SCALE, i32(1, n + 1), i32(T))
+    want = pkg.mla_absorb_chunk_fp8_batch(*args, SM_SCALE)
+    # both are within 2^-9 + 3 2^-11 + 2^-8 (the weights, the rounding to bf16) of the exact value, up to
+    # cancellation in the sum, which the largest magnitude stands for
+    assert float((got.double() - want.double()).abs().max()) <= 2 * (2 ** -9 + 3 * 2 ** -11 + 2 ** -8) * float(want.abs().max())

@@ -1,0 +1,193 @@
+"""Attention with a sliding window and first tokens that stay visible, against its definition in 64 bits."""
+import math
+
+import pytest
+import torch
+
+import fp8_mla_latent_gb300 as pkg
+from chunk_helpers import DL, PAGE, SM_SCALE
+from more_helpers import WindowCase
+
+pytestmark = pytest.mark.gpu
+
+
+def run(c, lse=True, ws=None, **kw):
+    rows = c.q_lat.shape[0]
+    if ws is None:
+        ws = pkg.alloc_workspace(pkg.mla_absorb_window_fp8_batch_workspace_size(len(c.nq), c.H, rows, c.max_blocks,
+                                                                                c.window, c.sinks))
+    out = torch.full((rows, c.H, DL), 7.0, dtype=torch.bfloat16, device="cuda")
+    l = torch.full((rows, c.H), 7.0, device="cuda") if lse else None
+    got = pkg.mla_absorb_window_fp8_batch(*c.args(), SM_SCALE, c.window, c.sinks, out=out, lse=l, workspace=ws, **kw)
+    assert got is out
+    return out, l, pkg.kv8_workspace_error(ws)
+
+
+def check(c, lse=True):
+    out, l, err = run(c, lse)
+    assert err == 0
+    c.check(out, l)
+    assert (out[sum(c.nq):] == 7).all() and (l is None or (l[sum(c.nq):] == 7).all()), "rows behind the last"
+    return out, l
+
+
+LENS = [1, 2, 63, 64, 65, 127, 128, 129, 192, 257, 300, 700]
+NQ = [1, 2, 5, 1, 65, 3, 4, 129, 2, 1, 7, 33]
+
+
+@pytest.mark.parametrize("sinks", [0, 1, 64, 70])
+@pytest.mark.parametrize("window", [1, 2, 63, 64, 65, 200])
+def test_windows_around_pages_and_tiles(window, sinks):
+    check(WindowCase(16, NQ, [max(t, n) for t, n in zip(LENS, NQ)], window, sinks, seed=window + sinks, pad=3))
+
+
+@pytest.mark.parametrize("H", [1, 3, 20, 128, 130])
+def test_head_counts(H):
+    check(WindowCase(H, NQ, [max(t, n) for t, n in zip(LENS, NQ)], 100, 4, seed=H))
+
+
+@pytest.mark.parametrize("H,nq,T,window,sinks", [
+    (128, 1, 4096, 1000, 64), (4, 1, 700, 128, 4), (16, 1, 9000, 4096, 4), (128, 130, 1500, 256, 128),
+    (1, 700, 900, 33, 5), (1024, 2, 400, 70, 0), (128, 4, 3000, 1, 0), (20, 333, 1999, 777, 300), (16, 40, 3000, 8, 2000)])
+def test_one_sequence(H, nq, T, window, sinks):
+    check(WindowCase(H, [nq], [T], window, sinks, seed=T))
+
+
+def test_many_single_tokens():
+    lens = [1 + (37 * i) % 900 for i in range(200)]
+    check(WindowCase(16, [1] * 200, lens, 150, 4, seed=5))
+
+
+def test_mixed_batch_with_sequences_that_have_no_query_or_no_token():
+    check(WindowCase(16, [0, 3, 0, 1, 40, 0], [70, 500, 0, 1, 290, 64], 50, 3, seed=6, pad=9))
+
+
+@pytest.mark.parametrize("H", [1, 16, 128])
+def test_rows_that_see_nothing(H):
+    """More queries than cached tokens: the first rows see no key; a sequence without a token."""
+    check(WindowCase(H, [5, 3, 2, 170], [2, 0, 1, 103], 40, 2, seed=7))
+
+
+def test_no_lse():
+    check(WindowCase(64, [3, 9], [400, 700], 100, 10, seed=8), lse=False)
+
+
+@pytest.mark.parametrize("window,sinks", [(5000, 0), (2 ** 31 - 1, 2 ** 31 - 1), (1, 2 ** 31 - 1)])
+def test_a_window_or_sinks_over_everything_give_the_bits_of_chunk_attention(window, sinks):
+    c = WindowCase(16, [3, 40, 1], [300, 700, 90], window, sinks, seed=9)
+    out, l, err = run(c)
+    assert err == 0
+    want_l = torch.empty_like(l)
+    want = pkg.mla_absorb_chunk_fp8_batch(*c.args(), SM_SCALE, lse=want_l)
+    assert torch.equal(out, want) and torch.equal(l, want_l)
+
+
+def unseen_pages(c):
+    for b in range(len(c.nq)):
+        see = c.sees(b).any(0)
+        for k in range((c.lens_list[b] + PAGE - 1) // PAGE):
+            if not see[k * PAGE: (k + 1) * PAGE].any():
+                yield b, k
+
+
+def test_pages_out_of_sight_need_not_be_there():
+    """Entries of pages that no row sees are free for anything, the pages hold NaN: no error, the same bits."""
+    c = WindowCase(16, [1, 30, 200, 2], [900, 1500, 1300, 70], 130, 70, seed=10)
+    want, want_l = check(c)
+    n = 0
+    for i, (b, k) in enumerate(unseen_pages(c)):
+        page = int(c.table[b, k])
+        c.codes[page * PAGE: (page + 1) * PAGE] = 0x7F
+        c.scales[page * PAGE: (page + 1) * PAGE] = math.nan
+        c.table[b, k] = (-1, 2 ** 31 - 1, -(2 ** 31), 10 ** 6)[i % 4]
+        n += 1
+    assert n > 20
+    out, l, err = run(c)
+    assert err == 0 and torch.equal(out, want) and torch.equal(l, want_l)
+
+
+def test_keys_out_of_sight_never_reach_a_row():
+    """NaN codes and scales behind a row's window and after it: rows that do not see them keep their
+    bits, those that see them are NaN."""
+    c = WindowCase(16, [60, 130], [400, 330], 90, 5, seed=11)
+    clean, clean_l, _ = run(c)
+    for b, at in ((0, 260), (0, 380), (1, 215), (1, 3)):
+        slot = int(c.slots[b][at])
+        c.codes[slot] = 0x7F
+        c.codes[slot, ::2] = 0xFF
+        c.scales[slot] = math.nan
+    out, l, err = run(c)
+    assert err == 0
+    for b, bad in ((0, (260, 380)), (1, (215, 3))):
+        first, n = int(c.start[b]), c.nq[b]
+        hit = c.sees(b)[:, list(bad)].any(1)
+        assert hit.any() and (b == 1 or not hit.all())
+        got, gl = out[first: first + n], l[first: first + n]
+        assert torch.equal(got[~hit], clean[first: first + n][~hit]) and torch.equal(gl[~hit], clean_l[first: first + n][~hit])
+        assert torch.isnan(got[hit]).all() and torch.isnan(gl[hit]).all()
+
+
+def test_a_bad_page_in_sight_is_told_and_left_out():
+    c = WindowCase(16, [4], [600], 200, 3, seed=12)
+    c.table[0, 8] = 10 ** 6  # tokens 512 .. 575
+    out, l, err = run(c)
+    assert err == -5
+    keep = torch.ones(600, dtype=torch.bool)
+    keep[512:576] = False
+    c.check(out, l, keep=[keep])
+
+
+def test_strided_queries():
+    c = WindowCase(20, [7, 3], [190, 401], 64, 4, seed=14)
+    want, want_l = check(c)
+    both = torch.cat([c.q_lat, c.q_rope], -1)
+    hm = both.transpose(0, 1).contiguous().transpose(0, 1)  # heads outermost in memory
+    c.q_lat, c.q_rope = hm[..., :DL], hm[..., DL:]
+    out, l, _ = run(c)
+    assert torch.equal(out, want) and torch.equal(l, want_l)
+
+
+def test_dominant_keys_behind_the_window_and_among_the_first_tokens():
+    """The rows' largest keys leave the window in the middle of the chunk; the first tokens' are larger still."""
+    def rows(b, t, g):
+        x = 0.3 * torch.randn((t, 576), generator=g) + 0.5
+        x[2] *= 8
+        x[500:520] *= 5
+        return x
+    c = WindowCase(32, [200], [700], 120, 4, seed=13, rows=rows)
+    c.q_lat.copy_((c.q_lat.float() * 0.4 + 0.3).bfloat16())
+    check(c)
+
+
+def test_captured_and_replayed_on_another_stream():
+    c = WindowCase(16, [3, 1, 70], [900, 65, 400], 100, 4, seed=15)
+    want, want_l = check(c)
+    ws = [pkg.alloc_workspace(pkg.mla_absorb_window_fp8_batch_workspace_size(3, 16, 74, c.max_blocks, 100, 4)) for _ in range(2)]
+    out, l = torch.zeros_like(want), torch.zeros_like(want_l)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        pkg.mla_absorb_window_fp8_batch(*c.args(), SM_SCALE, 100, 4, out=out, lse=l, workspace=ws[0])
+    s = torch.cuda.Stream()
+    for _ in range(3):
+        out.zero_()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            g.replay()
+        other = pkg.mla_absorb_window_fp8_batch(*c.args(), SM_SCALE, 100, 4, workspace=ws[1])
+        torch.cuda.current_stream().wait_stream(s)
+        assert torch.equal(out, want) and torch.equal(l, want_l) and torch.equal(other, want)
+
+
+def test_far_pages():
+    """Cache slots whose bytes lie behind 2^31 and 2^32."""
+    c = WindowCase(16, [2, 1], [400, 300], 150, 4, seed=16)
+    n_blocks = 2 ** 32 // (PAGE * 576) + 200
+    want, want_l = check(c)
+    codes = torch.full((n_blocks * PAGE, 576), 0x7F, dtype=torch.uint8, device="cuda")
+    scales = torch.full((n_blocks * PAGE, 2), math.nan, device="cuda")
+    k = c.codes.shape[0]
+    codes[-k:], scales[-k:] = c.codes, c.scales
+    c.table = torch.where(c.table >= 0, c.table + (n_blocks - k // PAGE), c.table)
+    c.codes, c.scales = codes, scales
+    out, l, err = run(c)
+    assert err == 0 and torch.equal(out, want) and torch.equal(l, want_l)
