@@ -31,6 +31,9 @@ __device__ __forceinline__ T from_f32(float v) {
   else return __float2bfloat16_rn(v);
 }
 
+// the code of a value whose row (or group) has no scale: a signed zero, 0x00 for NaN
+__device__ __forceinline__ uint32_t zero_byte(float v) { return v == v && signbit(v) ? 0x80u : 0u; }
+
 // A unit at p, of which `left` channels are the row's (VEC: all, at a 16-byte boundary).
 template <typename T, bool VEC>
 __device__ __forceinline__ void load_unit(const T* p, int left, float (&v)[UNIT]) {
@@ -178,8 +181,7 @@ __global__ void __launch_bounds__(WARP ? ROW_WARPS * 32 : MAX_THREADS) norm_kern
     for (int j = 0; j < UNIT; j += 2) {
       uint32_t two;
       if (guard) {
-        two = (t[i][j] == t[i][j] && signbit(t[i][j]) ? 0x80u : 0u) |
-              (t[i][j + 1] == t[i][j + 1] && signbit(t[i][j + 1]) ? 0x8000u : 0u);
+        two = zero_byte(t[i][j]) | (zero_byte(t[i][j + 1]) << 8);
       } else {
         float p0 = __fmul_rn(t[i][j], f), p1 = __fmul_rn(t[i][j + 1], f);
         p0 = isnan(p0) ? 0.f : p0;
@@ -198,11 +200,266 @@ __global__ void __launch_bounds__(WARP ? ROW_WARPS * 32 : MAX_THREADS) norm_kern
   }
 }
 
+// Many rows of whole units: a CTA goes over rows gridDim.x apart and keeps the weights in registers.  Each
+// thread brings its own channels of the next rows into shared memory by asynchronous copies and reads
+// them back itself, so that nothing is waited for together but the row's sums.
+constexpr int STREAM_UNITS = 4, STREAM_THREADS = 256;
+
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ uint64_t pair_of(float x, float y) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
+  return d;
+}
+__device__ __forceinline__ float2 of_pair(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+// two values of a 16-bit type
+template <typename T>
+__device__ __forceinline__ uint64_t unpack2(uint32_t v) {
+  if constexpr (std::is_same<T, __half>::value) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v));
+    return pair_of(f.x, f.y);
+  } else {
+    return pair_of(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(uint64_t v) {
+  const float2 f = of_pair(v);
+  if constexpr (std::is_same<T, __half>::value) {
+    const __half2 h = __floats2half2_rn(f.x, f.y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store_pairs(T* p, const uint64_t (&v)[4]) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float2 a = of_pair(v[2 * i]), b = of_pair(v[2 * i + 1]);
+      reinterpret_cast<float4*>(p)[i] = make_float4(a.x, a.y, b.x, b.y);
+    }
+  } else {
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack2<T>(v[0]), pack2<T>(v[1]), pack2<T>(v[2]), pack2<T>(v[3]));
+  }
+}
+
+template <typename T, bool ADD, int STAGES>
+__global__ void __launch_bounds__(STREAM_THREADS, 2) norm_stream_kernel(const NormArgs a) {
+  constexpr int E = STREAM_UNITS, Q = UNIT * (int)sizeof(T) / 16;  // 16-byte pieces of a unit
+  constexpr int ROWS_IN = ADD ? 2 : 1;
+  extern __shared__ __align__(16) uint8_t ring[];                  // [STAGES][ROWS_IN][E][Q][threads] pieces
+  __shared__ float tmp[4][STREAM_THREADS / 32];
+  const int n = blockDim.x, me = threadIdx.x, lane = me & 31, warps = n >> 5;
+  const uint32_t mine = (uint32_t)__cvta_generic_to_shared(ring) + me * 16;
+  const uint32_t stage_bytes = (uint32_t)(ROWS_IN * E * Q * n * 16);
+  auto ask = [&](int64_t row, int stage) {
+    if (row < a.n_rows) {
+#pragma unroll
+      for (int w = 0; w < ROWS_IN; ++w) {
+        const T* p = w == 0 ? static_cast<const T*>(a.x) + row * a.x_stride
+                            : static_cast<const T*>(a.residual) + row * a.residual_stride;
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          const int c = (i * n + me) * UNIT;
+          if (c >= a.width) continue;
+#pragma unroll
+          for (int q = 0; q < Q; ++q)
+            copy_async16(mine + stage * stage_bytes + (uint32_t)(((w * E + i) * Q + q) * n * 16), p + c + q * (16 / (int)sizeof(T)));
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  int64_t row = blockIdx.x;
+#pragma unroll
+  for (int k = 0; k < STAGES - 1; ++k) ask(row + (int64_t)k * gridDim.x, k);
+  uint64_t wt[E][4];
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    const int c = (i * n + me) * UNIT;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) wt[i][j] = 0;
+    if (c < a.width) {
+      const float4 u = __ldg(reinterpret_cast<const float4*>(a.weight + c));
+      const float4 v = __ldg(reinterpret_cast<const float4*>(a.weight + c) + 1);
+      wt[i][0] = pair_of(u.x, u.y);
+      wt[i][1] = pair_of(u.z, u.w);
+      wt[i][2] = pair_of(v.x, v.y);
+      wt[i][3] = pair_of(v.z, v.w);
+    }
+  }
+  int stage = 0, turn = 0;
+  for (; row < a.n_rows; row += gridDim.x) {
+    ask(row + (int64_t)(STAGES - 1) * gridDim.x, stage == 0 ? STAGES - 1 : stage - 1);
+    asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
+    uint64_t t[E][4];
+    uint64_t ss2 = 0;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const int c = (i * n + me) * UNIT;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) t[i][j] = 0;
+      if (c >= a.width) continue;
+#pragma unroll
+      for (int w = 0; w < ROWS_IN; ++w) {
+        uint64_t v[4];
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+          const uint4 u = lds128(mine + stage * stage_bytes + (uint32_t)(((w * E + i) * Q + q) * n * 16));
+          if constexpr (sizeof(T) == 4) {
+            v[2 * q] = pair_of(__uint_as_float(u.x), __uint_as_float(u.y));
+            v[2 * q + 1] = pair_of(__uint_as_float(u.z), __uint_as_float(u.w));
+          } else {
+            v[0] = unpack2<T>(u.x);
+            v[1] = unpack2<T>(u.y);
+            v[2] = unpack2<T>(u.z);
+            v[3] = unpack2<T>(u.w);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) t[i][j] = w == 0 ? v[j] : add_pair(t[i][j], v[j]);
+      }
+      if (ADD && a.residual_out != nullptr)
+        store_pairs<T>(static_cast<T*>(a.residual_out) + row * a.residual_out_stride + c, t[i]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) ss2 = fma_pair(t[i][j], t[i][j], ss2);
+    }
+    const float2 s2 = of_pair(ss2);
+    float ss = s2.x + s2.y;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    // (the row after next writes there again, behind the next one's barrier)
+    if (lane == 0) tmp[turn][me >> 5] = ss;
+    __syncthreads();
+    ss = 0.f;
+    for (int w = 0; w < warps; ++w) ss += tmp[turn][w];
+    const float inv = __fdiv_rn(1.f, __fsqrt_rn(__fadd_rn(__fdiv_rn(ss, (float)a.width), a.eps)));
+    const uint64_t inv2 = pair_of(inv, inv);
+    float top[E], all = 0.f;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const int c = (i * n + me) * UNIT;
+      float m = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        t[i][j] = mul_pair(mul_pair(t[i][j], inv2), wt[i][j]);
+        const float2 f = of_pair(t[i][j]);
+        m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
+      }
+      if (c >= a.width) m = 0.f;  // (nothing times an infinity)
+      if (a.normed != nullptr && c < a.width)
+        store_pairs<T>(static_cast<T*>(a.normed) + row * a.normed_stride + c, t[i]);
+      top[i] = m;
+      all = fmaxf(all, m);
+    }
+    float* scales = a.scales + row * a.n_groups;
+    if (a.group == 0) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, o));
+      if (lane == 0) tmp[2 + turn][me >> 5] = all;
+      __syncthreads();
+      for (int w = 0; w < warps; ++w) all = fmaxf(all, tmp[2 + turn][w]);
+      if (me == 0) scales[0] = __fdiv_rn(all, 448.f);
+    } else {
+      const int lanes = a.group / UNIT;  // at most 32
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          if (o >= lanes) break;
+          top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
+        }
+        const int u = i * n + me;
+        if ((u & (lanes - 1)) == 0 && u * UNIT < a.width) scales[u / lanes] = __fdiv_rn(top[i], 448.f);
+      }
+    }
+    const float fr = __fdiv_rn(448.f, all);
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const int c = (i * n + me) * UNIT;
+      if (c >= a.width) continue;
+      const float f = a.group == 0 ? fr : __fdiv_rn(448.f, top[i]);
+      uint32_t q[2];
+      if (isfinite(f)) {
+        const uint64_t f2 = pair_of(f, f);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float2 u = of_pair(mul_pair(t[i][2 * h], f2)), v = of_pair(mul_pair(t[i][2 * h + 1], f2));
+          const uint32_t w = (uint32_t)f32x2_to_e4m3x2(u.x, u.y) | ((uint32_t)f32x2_to_e4m3x2(v.x, v.y) << 16);
+          q[h] = w & ~__vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);  // (the NaN codes; what is finite saturates below)
+        }
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float2 u = of_pair(t[i][2 * h]), v = of_pair(t[i][2 * h + 1]);
+          q[h] = zero_byte(u.x) | (zero_byte(u.y) << 8) | (zero_byte(v.x) << 16) | (zero_byte(v.y) << 24);
+        }
+      }
+      *reinterpret_cast<uint2*>(a.codes + row * a.codes_stride + c) = make_uint2(q[0], q[1]);
+    }
+    turn ^= 1;
+    if (++stage == STAGES) stage = 0;
+  }
+}
+
+constexpr int STAGES_MOST = 2;
+
+// Whether rows of whole units go to the kernel above, and its launch.
+template <typename T, bool ADD>
+cudaError_t launch_stream(const NormArgs& a, cudaStream_t s) {
+  constexpr int STAGES = STAGES_MOST;
+  const int units = a.width / UNIT, threads = ((units + STREAM_UNITS - 1) / STREAM_UNITS + 31) / 32 * 32;
+  const size_t smem = (size_t)STAGES * (ADD ? 2 : 1) * STREAM_UNITS * UNIT * sizeof(T) * threads;
+  static std::atomic<int> memo[STREAM_THREADS / 32][MAX_DEVICES];
+  int per_sm = 0;
+  const cudaError_t e = per_device(memo[threads / 32 - 1], [&](int* v) {
+    auto kernel = norm_stream_kernel<T, ADD, STAGES>;
+    cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)(STAGES * (ADD ? 2 : 1) * STREAM_UNITS * UNIT * sizeof(T) * STREAM_THREADS));
+    if (r != cudaSuccess) return r;
+    int k = 0;
+    r = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&k, kernel, threads, smem);
+    *v = k < 1 ? 1 : k;
+    return r;
+  }, &per_sm);
+  if (e != cudaSuccess) return e;
+  const int64_t cap = (int64_t)NUM_SMS * per_sm;
+  norm_stream_kernel<T, ADD, STAGES><<<(unsigned)(a.n_rows < cap ? a.n_rows : cap), threads, smem, s>>>(a);
+  return cudaGetLastError();
+}
+
 template <typename T, bool VEC>
 cudaError_t launch_as(const NormArgs& a, cudaStream_t s) {
   const int units = (a.width + UNIT - 1) / UNIT;
   const unsigned warps = (unsigned)((a.n_rows + ROW_WARPS - 1) / ROW_WARPS), rows = (unsigned)a.n_rows;
   auto threads = [&](int e) { return ((units + e - 1) / e + 31) / 32 * 32; };
+  if (VEC && units > 64 && units <= STREAM_UNITS * STREAM_THREADS && a.n_rows > NUM_SMS)
+    return a.residual != nullptr ? launch_stream<T, true>(a, s) : launch_stream<T, false>(a, s);
   if (units <= 32) norm_kernel<T, 1, VEC, true><<<warps, ROW_WARPS * 32, 0, s>>>(a);
   else if (units <= 64) norm_kernel<T, 2, VEC, true><<<warps, ROW_WARPS * 32, 0, s>>>(a);
   else if (units <= 1024 && a.n_rows <= NUM_SMS) norm_kernel<T, 1, VEC, false><<<rows, threads(1), 0, s>>>(a);
