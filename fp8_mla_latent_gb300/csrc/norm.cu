@@ -34,7 +34,9 @@ __device__ __forceinline__ T from_f32(float v) {
 // the code of a value whose row (or group) has no scale: a signed zero, 0x00 for NaN
 __device__ __forceinline__ uint32_t zero_byte(float v) { return v == v && signbit(v) ? 0x80u : 0u; }
 
-// A unit at p, of which `left` channels are the row's (VEC: all, at a 16-byte boundary).
+// A thread's channels 0 .. 7 of its unit, in a row at p: eight in a row (VEC, at a 16-byte boundary), or
+// every 32nd of the 256 that its warp has, so that a warp's accesses lie together;
+// `left` channels from the first of them to the row's end.
 template <typename T, bool VEC>
 __device__ __forceinline__ void load_unit(const T* p, int left, float (&v)[UNIT]) {
   if constexpr (VEC) {
@@ -48,7 +50,7 @@ __device__ __forceinline__ void load_unit(const T* p, int left, float (&v)[UNIT]
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < UNIT; ++j) v[j] = j < left ? to_f32(p[j]) : 0.f;
+    for (int j = 0; j < UNIT; ++j) v[j] = 32 * j < left ? to_f32(p[32 * j]) : 0.f;
   }
 }
 template <typename T, bool VEC>
@@ -66,7 +68,7 @@ __device__ __forceinline__ void store_unit(T* p, int left, const float (&v)[UNIT
   } else {
 #pragma unroll
     for (int j = 0; j < UNIT; ++j)
-      if (j < left) p[j] = from_f32<T>(v[j]);
+      if (32 * j < left) p[32 * j] = from_f32<T>(v[j]);
   }
 }
 
@@ -92,17 +94,18 @@ __device__ __forceinline__ float row_reduce(float v, float* tmp) {
   return v;
 }
 
-template <typename T, int E, bool VEC, bool WARP>
+template <typename T, int UNITS, bool VEC, bool WARP>
 __global__ void __launch_bounds__(WARP ? ROW_WARPS * 32 : MAX_THREADS) norm_kernel(const NormArgs a) {
   __shared__ float tmp[2][32];
-  const int n = WARP ? 32 : blockDim.x, me = WARP ? threadIdx.x & 31 : threadIdx.x;
+  const int n = WARP ? 32 : blockDim.x, me = WARP ? threadIdx.x & 31 : threadIdx.x, lane = me & 31;
   const int64_t row = WARP ? (int64_t)blockIdx.x * ROW_WARPS + (threadIdx.x >> 5) : blockIdx.x;
   if (WARP && row >= a.n_rows) return;
+  auto at = [&](int i) { return VEC ? (i * n + me) * UNIT : (i * n + me - lane) * UNIT + lane; };
   const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
-  float t[E][UNIT];
+  float t[UNITS][UNIT];
 #pragma unroll
-  for (int i = 0; i < E; ++i) {
-    const int c = (i * n + me) * UNIT;
+  for (int i = 0; i < UNITS; ++i) {
+    const int c = at(i);
 #pragma unroll
     for (int j = 0; j < UNIT; ++j) t[i][j] = 0.f;
     if (c < a.width) load_unit<T, VEC>(x + c, a.width - c, t[i]);
@@ -111,8 +114,8 @@ __global__ void __launch_bounds__(WARP ? ROW_WARPS * 32 : MAX_THREADS) norm_kern
     const T* r = static_cast<const T*>(a.residual) + row * a.residual_stride;
     T* out = a.residual_out == nullptr ? nullptr : static_cast<T*>(a.residual_out) + row * a.residual_out_stride;
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const int c = (i * n + me) * UNIT;
+    for (int i = 0; i < UNITS; ++i) {
+      const int c = at(i);
       if (c >= a.width) continue;
       float v[UNIT];
       load_unit<T, VEC>(r + c, a.width - c, v);
@@ -123,79 +126,117 @@ __global__ void __launch_bounds__(WARP ? ROW_WARPS * 32 : MAX_THREADS) norm_kern
   }
   float ss = 0.f;
 #pragma unroll
-  for (int i = 0; i < E; ++i)
+  for (int i = 0; i < UNITS; ++i)
 #pragma unroll
     for (int j = 0; j < UNIT; ++j) ss = fmaf(t[i][j], t[i][j], ss);
   ss = row_reduce<WARP, false>(ss, tmp[0]);
   const float inv = __fdiv_rn(1.f, __fsqrt_rn(__fadd_rn(__fdiv_rn(ss, (float)a.width), a.eps)));
   T* normed = a.normed == nullptr ? nullptr : static_cast<T*>(a.normed) + row * a.normed_stride;
-  float top[E], all = 0.f;  // largest magnitudes, NaN left out
+  float all = 0.f;  // largest magnitude, NaN left out
 #pragma unroll
-  for (int i = 0; i < E; ++i) {
-    const int c = (i * n + me) * UNIT;
-    top[i] = 0.f;
-    if (c < a.width) {
-      float w[UNIT];
-      if constexpr (VEC) {
-        *reinterpret_cast<float4*>(w) = __ldg(reinterpret_cast<const float4*>(a.weight + c));
-        *reinterpret_cast<float4*>(w + 4) = __ldg(reinterpret_cast<const float4*>(a.weight + c) + 1);
-      } else {
+  for (int i = 0; i < UNITS; ++i) {
+    const int c = at(i);
+    if (c >= a.width) continue;
+    float w[UNIT];
+    if constexpr (VEC) {
+      *reinterpret_cast<float4*>(w) = __ldg(reinterpret_cast<const float4*>(a.weight + c));
+      *reinterpret_cast<float4*>(w + 4) = __ldg(reinterpret_cast<const float4*>(a.weight + c) + 1);
+    } else {
 #pragma unroll
-        for (int j = 0; j < UNIT; ++j) w[j] = j < a.width - c ? __ldg(a.weight + c + j) : 0.f;
-      }
-#pragma unroll
-      for (int j = 0; j < UNIT; ++j) {
-        t[i][j] = __fmul_rn(__fmul_rn(t[i][j], inv), w[j]);
-        if (VEC || j < a.width - c) top[i] = fmaxf(top[i], fabsf(t[i][j]));
-      }
-      if (normed != nullptr) store_unit<T, VEC>(normed + c, a.width - c, t[i]);
+      for (int j = 0; j < UNIT; ++j) w[j] = 32 * j < a.width - c ? __ldg(a.weight + c + 32 * j) : 0.f;
     }
-    all = fmaxf(all, top[i]);
+#pragma unroll
+    for (int j = 0; j < UNIT; ++j) {
+      t[i][j] = __fmul_rn(__fmul_rn(t[i][j], inv), w[j]);
+      if (!VEC && 32 * j >= a.width - c) t[i][j] = 0.f;  // (nothing times an infinity)
+      all = fmaxf(all, fabsf(t[i][j]));
+    }
+    if (normed != nullptr) store_unit<T, VEC>(normed + c, a.width - c, t[i]);
   }
   float* scales = a.scales + row * a.n_groups;
   if (a.group == 0) {
     all = row_reduce<WARP, true>(all, tmp[1]);
     if (me == 0) scales[0] = __fdiv_rn(all, 448.f);
-  } else {
-    const int lanes = a.group / UNIT;  // at most 32
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const float u = __shfl_xor_sync(0xffffffffu, top[i], o);
-        if (o < lanes) top[i] = fmaxf(top[i], u);
-      }
-      const int u = i * n + me;
-      if ((u & (lanes - 1)) == 0 && u * UNIT < a.width) scales[u / lanes] = __fdiv_rn(top[i], 448.f);
-    }
   }
   uint8_t* codes = a.codes + row * a.codes_stride;
 #pragma unroll
-  for (int i = 0; i < E; ++i) {
-    const int c = (i * n + me) * UNIT;
-    if (c >= a.width) continue;
-    const float f = __fdiv_rn(448.f, a.group == 0 ? all : top[i]);
-    const bool guard = !isfinite(f);
-    uint32_t q[2] = {0u, 0u};
+  for (int i = 0; i < UNITS; ++i) {
+    const int c = at(i);
+    if (!VEC) {
+      float top[UNIT];  // (of the groups that the channels lie in)
 #pragma unroll
-    for (int j = 0; j < UNIT; j += 2) {
-      uint32_t two;
-      if (guard) {
-        two = zero_byte(t[i][j]) | (zero_byte(t[i][j + 1]) << 8);
-      } else {
-        float p0 = __fmul_rn(t[i][j], f), p1 = __fmul_rn(t[i][j + 1], f);
-        p0 = isnan(p0) ? 0.f : p0;
-        p1 = isnan(p1) ? 0.f : p1;
-        two = f32x2_to_e4m3x2(p0, p1);
+      for (int j = 0; j < UNIT; ++j) top[j] = a.group == 0 ? all : fabsf(t[i][j]);
+      if (a.group != 0) {
+        const int span = a.group / 32;  // channels of a thread in a group: 1, 2, 4 or 8
+#pragma unroll
+        for (int o = 1; o < UNIT; o <<= 1) {
+          if (o >= span) break;
+#pragma unroll
+          for (int j = 0; j < UNIT; j += 2 * o) {
+            const float m = fmaxf(top[j], top[j + o]);  // (NaN loses)
+#pragma unroll
+            for (int k = 0; k < 2 * o; ++k) top[j + k] = m;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < UNIT; ++j) {
+          if (j & (span - 1)) {
+            top[j] = top[j - 1];
+            continue;
+          }
+          top[j] = fmaxf(top[j], 0.f);
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], o));
+          const int first = c - lane + 32 * j;
+          if (lane == 0 && first < a.width) scales[first / a.group] = __fdiv_rn(top[j], 448.f);
+        }
       }
-      q[j / 4] |= two << (8 * (j % 4));
-    }
-    if constexpr (VEC) {
-      *reinterpret_cast<uint2*>(codes + c) = make_uint2(q[0], q[1]);
-    } else {
+      float f = 0.f;
 #pragma unroll
-      for (int j = 0; j < UNIT; ++j)
-        if (j < a.width - c) codes[c + j] = (uint8_t)(q[j / 4] >> (8 * (j % 4)));
+      for (int j = 0; j < UNIT; ++j) {
+        if (j == 0 || (a.group != 0 && (j & (a.group / 32 - 1)) == 0)) f = __fdiv_rn(448.f, top[j]);
+        if (32 * j >= a.width - c) continue;
+        uint32_t q;
+        if (isfinite(f)) {
+          float p = __fmul_rn(t[i][j], f);
+          p = isnan(p) ? 0.f : p;
+          q = f32x2_to_e4m3x2(p, 0.f) & 0xFFu;
+        } else {
+          q = zero_byte(t[i][j]);
+        }
+        codes[c + 32 * j] = (uint8_t)q;
+      }
+    } else {
+      float top = all;
+      if (a.group != 0) {
+        top = 0.f;
+#pragma unroll
+        for (int j = 0; j < UNIT; ++j) top = fmaxf(top, fabsf(t[i][j]));
+        const int lanes = a.group / UNIT;  // at most 32
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const float u = __shfl_xor_sync(0xffffffffu, top, o);
+          if (o < lanes) top = fmaxf(top, u);
+        }
+        if ((lane & (lanes - 1)) == 0 && c < a.width) scales[c / a.group] = __fdiv_rn(top, 448.f);
+      }
+      if (c >= a.width) continue;
+      const float f = __fdiv_rn(448.f, top);
+      uint32_t q[2] = {0u, 0u};
+#pragma unroll
+      for (int j = 0; j < UNIT; j += 2) {
+        uint32_t two;
+        if (isfinite(f)) {
+          float p0 = __fmul_rn(t[i][j], f), p1 = __fmul_rn(t[i][j + 1], f);
+          p0 = isnan(p0) ? 0.f : p0;
+          p1 = isnan(p1) ? 0.f : p1;
+          two = f32x2_to_e4m3x2(p0, p1);
+        } else {
+          two = zero_byte(t[i][j]) | (zero_byte(t[i][j + 1]) << 8);
+        }
+        q[j / 4] |= two << (8 * (j % 4));
+      }
+      *reinterpret_cast<uint2*>(codes + c) = make_uint2(q[0], q[1]);
     }
   }
 }
@@ -203,7 +244,14 @@ __global__ void __launch_bounds__(WARP ? ROW_WARPS * 32 : MAX_THREADS) norm_kern
 // Many rows of whole units: a CTA goes over rows gridDim.x apart and keeps the weights in registers.  Each
 // thread brings its own channels of the next rows into shared memory by asynchronous copies and reads
 // them back itself, so that nothing is waited for together but the row's sums.
-constexpr int STREAM_UNITS = 4, STREAM_THREADS = 256;
+//
+// HBM bounds it: two CTAs of 16 warps hold one SM's share of the rows in flight (28 KB a CTA at 7168
+// channels of two 16-bit inputs; with four rows ahead instead of one it is slower, 131 us against 124).
+// With one input the instructions are next: 350 a warp and row of two units a thread, of which two
+// thirds do not depend on the units, so rows without a residual take four units a thread and three CTAs
+// (16384 x 7168 bf16 rows: 90 us with two, 74 with four; with a residual 124 and 127; f32 89 and 97).
+// Measured, one GB300, 16384 x 7168 bf16 with a residual: 124 us, 6.68 TB/s, 0.99 of the copy rate.
+constexpr int STAGES = 2;
 
 __device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -232,6 +280,12 @@ __device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
 __device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t d;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+// max(|a|, |b|, c), NaN left out
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
+  float d;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 // two values of a 16-bit type
@@ -268,13 +322,15 @@ __device__ __forceinline__ void store_pairs(T* p, const uint64_t (&v)[4]) {
   }
 }
 
-template <typename T, bool ADD, int STAGES>
-__global__ void __launch_bounds__(STREAM_THREADS, 2) norm_stream_kernel(const NormArgs a) {
-  constexpr int E = STREAM_UNITS, Q = UNIT * (int)sizeof(T) / 16;  // 16-byte pieces of a unit
+template <typename T, bool ADD, int E, int THREADS>
+__global__ void __launch_bounds__(THREADS, E == 2 ? 2 : (THREADS <= 256 ? 3 : 1)) norm_stream_kernel(const NormArgs a) {
+  constexpr int Q = UNIT * (int)sizeof(T) / 16;  // 16-byte pieces of a unit
   constexpr int ROWS_IN = ADD ? 2 : 1;
   extern __shared__ __align__(16) uint8_t ring[];                  // [STAGES][ROWS_IN][E][Q][threads] pieces
-  __shared__ float tmp[4][STREAM_THREADS / 32];
-  const int n = blockDim.x, me = threadIdx.x, lane = me & 31, warps = n >> 5;
+  __shared__ float4 tmp[4][THREADS / 128];  // (a warp's each; 0 behind the last)
+  const int n = blockDim.x, me = threadIdx.x, lane = me & 31;
+  for (int i = me; i < 4 * THREADS / 32; i += n) reinterpret_cast<float*>(tmp)[i] = 0.f;
+  __syncthreads();
   const uint32_t mine = (uint32_t)__cvta_generic_to_shared(ring) + me * 16;
   const uint32_t stage_bytes = (uint32_t)(ROWS_IN * E * Q * n * 16);
   auto ask = [&](int64_t row, int stage) {
@@ -298,6 +354,7 @@ __global__ void __launch_bounds__(STREAM_THREADS, 2) norm_stream_kernel(const No
   int64_t row = blockIdx.x;
 #pragma unroll
   for (int k = 0; k < STAGES - 1; ++k) ask(row + (int64_t)k * gridDim.x, k);
+  bool odd_weight = false;  // one of this thread's is not finite
   uint64_t wt[E][4];
 #pragma unroll
   for (int i = 0; i < E; ++i) {
@@ -311,8 +368,10 @@ __global__ void __launch_bounds__(STREAM_THREADS, 2) norm_stream_kernel(const No
       wt[i][1] = pair_of(u.z, u.w);
       wt[i][2] = pair_of(v.x, v.y);
       wt[i][3] = pair_of(v.z, v.w);
+      odd_weight |= !(u.x * 0.f + u.y * 0.f + u.z * 0.f + u.w * 0.f + v.x * 0.f + v.y * 0.f + v.z * 0.f + v.w * 0.f == 0.f);
     }
   }
+  const float per_width = __fdiv_rn(1.f, (float)a.width);
   int stage = 0, turn = 0;
   for (; row < a.n_rows; row += gridDim.x) {
     ask(row + (int64_t)(STAGES - 1) * gridDim.x, stage == 0 ? STAGES - 1 : stage - 1);
@@ -354,12 +413,17 @@ __global__ void __launch_bounds__(STREAM_THREADS, 2) norm_stream_kernel(const No
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     // (the row after next writes there again, behind the next one's barrier)
-    if (lane == 0) tmp[turn][me >> 5] = ss;
+    if (lane == 0) reinterpret_cast<float*>(tmp[turn])[me >> 5] = ss;
     __syncthreads();
     ss = 0.f;
-    for (int w = 0; w < warps; ++w) ss += tmp[turn][w];
-    const float inv = __fdiv_rn(1.f, __fsqrt_rn(__fadd_rn(__fdiv_rn(ss, (float)a.width), a.eps)));
+#pragma unroll
+    for (int w = 0; w < THREADS / 128; ++w) {
+      const float4 u = tmp[turn][w];
+      ss += (u.x + u.y) + (u.z + u.w);
+    }
+    const float inv = rsqrtf(__fadd_rn(__fmul_rn(ss, per_width), a.eps));
     const uint64_t inv2 = pair_of(inv, inv);
+    const bool odd = odd_weight || !(ss + inv < INFINITY);  // (otherwise no y is NaN)
     float top[E], all = 0.f;
 #pragma unroll
     for (int i = 0; i < E; ++i) {
@@ -369,7 +433,7 @@ __global__ void __launch_bounds__(STREAM_THREADS, 2) norm_stream_kernel(const No
       for (int j = 0; j < 4; ++j) {
         t[i][j] = mul_pair(mul_pair(t[i][j], inv2), wt[i][j]);
         const float2 f = of_pair(t[i][j]);
-        m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
+        m = max_abs(f.x, f.y, m);
       }
       if (c >= a.width) m = 0.f;  // (nothing times an infinity)
       if (a.normed != nullptr && c < a.width)
@@ -381,37 +445,45 @@ __global__ void __launch_bounds__(STREAM_THREADS, 2) norm_stream_kernel(const No
     if (a.group == 0) {
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, o));
-      if (lane == 0) tmp[2 + turn][me >> 5] = all;
+      if (lane == 0) reinterpret_cast<float*>(tmp[2 + turn])[me >> 5] = all;
       __syncthreads();
-      for (int w = 0; w < warps; ++w) all = fmaxf(all, tmp[2 + turn][w]);
+#pragma unroll
+      for (int w = 0; w < THREADS / 128; ++w) {
+        const float4 u = tmp[2 + turn][w];
+        all = fmaxf(all, fmaxf(fmaxf(u.x, u.y), fmaxf(u.z, u.w)));
+      }
       if (me == 0) scales[0] = __fdiv_rn(all, 448.f);
     } else {
-      const int lanes = a.group / UNIT;  // at most 32
+      const int lanes = a.group / UNIT;  // 4 .. 32
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
+      for (int o = 1; o < 32; o <<= 1) {
+        if (o >= lanes) break;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          if (o >= lanes) break;
-          top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
-        }
-        const int u = i * n + me;
-        if ((u & (lanes - 1)) == 0 && u * UNIT < a.width) scales[u / lanes] = __fdiv_rn(top[i], 448.f);
+        for (int i = 0; i < E; ++i) top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
       }
+      // (the divisions of a lane group's E groups of channels, one by each of its first lanes)
+      const int k = lane & (lanes - 1), u = k * n + me - k;
+#pragma unroll
+      for (int i = 0; i < E; ++i) all = k == i ? top[i] : all;
+      if (k < E && u * UNIT < a.width) scales[u / lanes] = __fdiv_rn(all, 448.f);
     }
     const float fr = __fdiv_rn(448.f, all);
 #pragma unroll
     for (int i = 0; i < E; ++i) {
       const int c = (i * n + me) * UNIT;
+      const float f = a.group == 0 ? fr : __shfl_sync(0xffffffffu, fr, (lane & ~(a.group / UNIT - 1)) + i);
       if (c >= a.width) continue;
-      const float f = a.group == 0 ? fr : __fdiv_rn(448.f, top[i]);
       uint32_t q[2];
-      if (isfinite(f)) {
+      if (f < INFINITY) {  // (f is not NaN: NaN is left out of the maximum)
         const uint64_t f2 = pair_of(f, f);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const float2 u = of_pair(mul_pair(t[i][2 * h], f2)), v = of_pair(mul_pair(t[i][2 * h + 1], f2));
-          const uint32_t w = (uint32_t)f32x2_to_e4m3x2(u.x, u.y) | ((uint32_t)f32x2_to_e4m3x2(v.x, v.y) << 16);
-          q[h] = w & ~__vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);  // (the NaN codes; what is finite saturates below)
+          q[h] = (uint32_t)f32x2_to_e4m3x2(u.x, u.y) | ((uint32_t)f32x2_to_e4m3x2(v.x, v.y) << 16);
+        }
+        if (odd || f == 0.f) {  // the NaN codes to 0 (what is finite saturates below them)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) q[h] &= ~__vcmpeq4(q[h] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
         }
       } else {
 #pragma unroll
@@ -427,20 +499,17 @@ __global__ void __launch_bounds__(STREAM_THREADS, 2) norm_stream_kernel(const No
   }
 }
 
-constexpr int STAGES_MOST = 2;
+constexpr size_t STREAM_SMEM = 220 * 1024;
 
-// Whether rows of whole units go to the kernel above, and its launch.
-template <typename T, bool ADD>
+template <typename T, bool ADD, int E, int THREADS>
 cudaError_t launch_stream(const NormArgs& a, cudaStream_t s) {
-  constexpr int STAGES = STAGES_MOST;
-  const int units = a.width / UNIT, threads = ((units + STREAM_UNITS - 1) / STREAM_UNITS + 31) / 32 * 32;
-  const size_t smem = (size_t)STAGES * (ADD ? 2 : 1) * STREAM_UNITS * UNIT * sizeof(T) * threads;
-  static std::atomic<int> memo[STREAM_THREADS / 32][MAX_DEVICES];
+  const int threads = ((a.width / UNIT + E - 1) / E + 31) / 32 * 32;
+  const size_t smem = (size_t)STAGES * (ADD ? 2 : 1) * E * UNIT * sizeof(T) * threads;
+  static std::atomic<int> memo[THREADS / 32][MAX_DEVICES];
   int per_sm = 0;
   const cudaError_t e = per_device(memo[threads / 32 - 1], [&](int* v) {
-    auto kernel = norm_stream_kernel<T, ADD, STAGES>;
-    cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)(STAGES * (ADD ? 2 : 1) * STREAM_UNITS * UNIT * sizeof(T) * STREAM_THREADS));
+    auto kernel = norm_stream_kernel<T, ADD, E, THREADS>;
+    cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)STREAM_SMEM);
     if (r != cudaSuccess) return r;
     int k = 0;
     r = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&k, kernel, threads, smem);
@@ -449,7 +518,7 @@ cudaError_t launch_stream(const NormArgs& a, cudaStream_t s) {
   }, &per_sm);
   if (e != cudaSuccess) return e;
   const int64_t cap = (int64_t)NUM_SMS * per_sm;
-  norm_stream_kernel<T, ADD, STAGES><<<(unsigned)(a.n_rows < cap ? a.n_rows : cap), threads, smem, s>>>(a);
+  norm_stream_kernel<T, ADD, E, THREADS><<<(unsigned)(a.n_rows < cap ? a.n_rows : cap), threads, smem, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -458,8 +527,20 @@ cudaError_t launch_as(const NormArgs& a, cudaStream_t s) {
   const int units = (a.width + UNIT - 1) / UNIT;
   const unsigned warps = (unsigned)((a.n_rows + ROW_WARPS - 1) / ROW_WARPS), rows = (unsigned)a.n_rows;
   auto threads = [&](int e) { return ((units + e - 1) / e + 31) / 32 * 32; };
-  if (VEC && units > 64 && units <= STREAM_UNITS * STREAM_THREADS && a.n_rows > NUM_SMS)
-    return a.residual != nullptr ? launch_stream<T, true>(a, s) : launch_stream<T, false>(a, s);
+  if constexpr (VEC) {
+    if (units > 64 && a.n_rows > NUM_SMS) {
+      const bool add = a.residual != nullptr;
+      if (units <= 1024) {
+        if (add) return launch_stream<T, true, 2, 512>(a, s);
+        if constexpr (sizeof(T) == 4) return launch_stream<T, false, 2, 512>(a, s);
+        else return launch_stream<T, false, 4, 256>(a, s);
+      }
+      // (two rows of twice 16384 values of 32 bits do not fit)
+      if constexpr (sizeof(T) == 2) {
+        if (units <= 2048) return add ? launch_stream<T, true, 4, 512>(a, s) : launch_stream<T, false, 4, 512>(a, s);
+      }
+    }
+  }
   if (units <= 32) norm_kernel<T, 1, VEC, true><<<warps, ROW_WARPS * 32, 0, s>>>(a);
   else if (units <= 64) norm_kernel<T, 2, VEC, true><<<warps, ROW_WARPS * 32, 0, s>>>(a);
   else if (units <= 1024 && a.n_rows <= NUM_SMS) norm_kernel<T, 1, VEC, false><<<rows, threads(1), 0, s>>>(a);
