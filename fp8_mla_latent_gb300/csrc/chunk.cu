@@ -72,20 +72,11 @@
 // the CTA flags the workspace error word, drains its MMAs and copies and meets its cluster
 // at the closing barrier.
 #include <cuda.h>
-#include <cuda_bf16.h>
 
-#include <type_traits>
-
-#include "kv8_common.cuh"
-#include "tc_ptx.cuh"
+#include "chunk_work.cuh"
 
 namespace kv8 {
 namespace {
-
-using namespace ptx;
-
-// what a call's rows see: all keys before them; with a window; a prefix shared by several sequences apart
-constexpr int kPlain = 0, kWindow = 1, kShared = 2;
 
 constexpr int ROWS = 256;                    // rows of a row tile: 128 per CTA of a pair
 constexpr int CROWS = 128;
@@ -126,8 +117,6 @@ constexpr float DOWN = 10.0f;
 // reference may come (l and O hold no more than 2^(highest - reference) times what they did there)
 constexpr float LG_MIN = -40.0f, DOWN_CAP = 50.0f;
 constexpr uint64_t WAIT_NS = 2000000000ull;
-constexpr float LOG2E = 1.4426950408889634f;
-constexpr float LN2 = 0.6931471805599453f;
 
 // mbarriers (the same offsets in all four CTAs: commits are multicast).  What passes between CTAs is
 // ordered at cluster scope.  Shared memory that one CTA's warps wrote or read, and that another CTA's
@@ -188,451 +177,31 @@ static_assert(OFF_K % 1024 == 0 && KTILE % 1024 == 0 && OFF_V % 1024 == 0 && P_S
 static_assert(P_BYTES <= P_STRIDE && N_LANE_WARPS * 2048 <= 4 * OP_ATOM, "payload and staging");
 static_assert(SMEM <= 232448, "shared memory above the per-CTA limit");
 
-// ------------------------------------------------------------------ work
-// Plan of cluster k: its first row tile (sequence b, row tile rt, nt key tiles of
-// which off come before the range), the unit where the range starts and its units.
-struct PlanEntry {
-  int32_t b, rt, nt, off;
-  int64_t x;
+struct Geo {
+  static constexpr int ROWS = kv8::ROWS, RANGES = MAX_CLUSTERS, SWITCH = kv8::SWITCH, MIN_TILES = kv8::MIN_TILES;
 };
-struct Plan {
-  int64_t n_clusters, units, part_rows;
-  PlanEntry e[MAX_CLUSTERS];
-};
-
+static_assert(ROWS == WIDE, "the row tiles that a shared prefix's cost is counted in");
 template <int MODE>
-struct SeqInfo {
-  int64_t q0;  // first row of the query arrays
-  int nq, T;
-};
-template <>
-struct SeqInfo<kShared> {
-  int64_t q0;
-  int nq, T;               // (T counts from the first key, token 64 page0)
-  int row, page0, causal;  // row of the block table, first page there
-  int part;                // row of its first part (below), or -1
-};
-template <int MODE>
-__device__ __forceinline__ SeqInfo<MODE> seq_info(const ChunkArgs& a, int b, bool tell) {
-  if constexpr (MODE == kShared) {
-    const int4 u = a.entries[b].u, v = a.entries[b].v;
-    return {u.x, u.y, u.z, u.w, v.x, v.y, v.z};
-  } else {
-  SeqInfo<MODE> s;
-  const int64_t q0 = __ldg(&a.q_start[b]), q1 = __ldg(&a.q_start[b + 1]);
-  const int64_t T = __ldg(&a.seq_lens[b]), room = (int64_t)a.max_blocks * PAGE;
-  const bool bad = q0 < 0 || q1 < q0 || q1 > a.total_q;
-  if (tell && bad) atomicOr(a.err, ERR_BLOCK_TABLE);
-  if (tell && (T < 0 || T > room)) atomicOr(a.err, ERR_SEQ_LEN);
-  s.q0 = q0;
-  s.nq = bad ? 0 : (int)(q1 - q0);
-  s.T = (int)(T < 0 ? 0 : (T > room ? room : T));
-  return s;
-  }
-}
-template <int MODE>
-__device__ __forceinline__ int row_tiles(const ChunkArgs& a, const SeqInfo<MODE>& s) {
-  return (int)(((int64_t)s.nq * a.H + ROWS - 1) / ROWS);
-}
-// keys that token i of the sequence sees (with a window: before which its last one ends)
-template <int MODE>
-__device__ __forceinline__ int limit_of(const ChunkArgs& a, const SeqInfo<MODE>& s, int i) {
-  if constexpr (MODE == kPlain) {
-    if (!a.causal) return s.T;
-  }
-  if constexpr (MODE == kShared) {
-    if (!s.causal) return s.T;
-  }
-  const int lim = s.T - s.nq + i + 1;
-  return lim < 0 ? 0 : lim;
-}
-template <int MODE>
-__device__ __forceinline__ int first_token(const ChunkArgs& a, int rt) {
-  return (int)((uint32_t)(rt * ROWS) / (uint32_t)a.H);
-}
-template <int MODE>
-__device__ __forceinline__ int last_token(const ChunkArgs& a, const SeqInfo<MODE>& s, int rt) {
-  const int64_t last = ((int64_t)rt * ROWS + ROWS - 1) / a.H;
-  return last < s.nq ? (int)last : s.nq - 1;
-}
-// A window's first key, of a row that sees keys up to lim.
-__device__ __forceinline__ int window_from(const ChunkArgs& a, int lim) { return lim > a.window ? lim - a.window : 0; }
-
-// The pages that a row tile reads, in order: all of them from the first; or with a window, the
-// first tokens' pages, then those from the first row's window on (its window begins first).
-template <int MODE>
-struct Pages {
-  __device__ __forceinline__ int at(int i) const { return i; }
-};
-template <>
-struct Pages<kWindow> {
-  int sinks, skip;  // pages of first tokens; pages between them and the window
-  __device__ __forceinline__ int at(int i) const { return i < sinks ? i : i + skip; }
-};
-// Key tiles of a row tile: those that its last row sees; one where it sees none, so
-// that its (empty) rows are written by the same path.
-template <int MODE>
-__device__ __forceinline__ int key_tiles(const ChunkArgs& a, const SeqInfo<MODE>& s, int rt, Pages<MODE>* pages) {
-  const int lim = limit_of(a, s, last_token(a, s, rt));
-  if constexpr (MODE == kWindow) {
-    const int from = window_from(a, limit_of(a, s, first_token<MODE>(a, rt))), wp = from / PAGE;
-    pages->sinks = ((a.n_sink < from ? a.n_sink : from) + PAGE - 1) / PAGE;
-    pages->skip = wp > pages->sinks ? wp - pages->sinks : 0;
-    const int n = (lim > 0 ? (lim - 1) / PAGE + 1 : 0) - pages->skip;
-    return n > 0 ? (n + 1) / 2 : 1;
-  }
-  return lim > 0 ? (lim - 1) / TILE + 1 : 1;
-}
-
-__device__ __forceinline__ int64_t plan_sum(int64_t v, int64_t* tmp, int64_t* total) {
-  // inclusive sum over 1024 threads
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += u;
-  }
-  if (lane == 31) tmp[warp] = v;
-  __syncthreads();
-  if (warp == 0) {
-    int64_t w = tmp[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t u = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += u;
-    }
-    tmp[lane] = w;
-  }
-  __syncthreads();
-  if (warp > 0) v += tmp[warp - 1];
-  *total = tmp[31];
-  __syncthreads();
-  return v;
-}
-
-// Sequences that share a prefix.  The rows of a group's sequences lie behind one another, so that the
-// prefix is one more sequence, whose rows are the group's and which all of them see whole, and the
-// others keep the keys behind it; entry g is group g's prefix, entry G + b sequence b.  Either gives
-// parts (f32 o, l and M_g of every row), which the join adds up; a sequence that shares nothing
-// is as in a call without groups.
-//
-// The prefix is whole pages that every row of the group sees; a group takes part where its row tiles
-// are fewer together than apart by more than the parts cost: SHARE key tiles a row tile (its start, and
-// 256 rows of f32 written twice and read twice), and where its sequences have PART_ROWS rows on average
-// at most (above, they fill their row tiles, and little is saved).
-constexpr int PART_ROWS = 1024, SHARE = SWITCH + 10;
-
-__device__ __forceinline__ int64_t warp_sum(int64_t v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-__device__ __forceinline__ int64_t warp_min(int64_t v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const int64_t u = __shfl_xor_sync(0xffffffffu, v, o);
-    v = u < v ? u : v;
-  }
-  return v;
-}
-
-__device__ void make_entries(const ChunkArgs& a, Plan* plan, int64_t* tmp) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int bad = 0;
-  for (int g = threadIdx.x; g < a.G; g += 1024) {
-    const int f = __ldg(&a.group_start[g]), l = __ldg(&a.group_start[g + 1]);
-    bad |= f < 0 || l < f || l > a.B;
-    a.entries[g].u = make_int4(0, 0, 0, 0);
-    a.entries[g].v = make_int4(0, 0, -1, 0);
-  }
-  for (int b = threadIdx.x; b < a.B; b += 1024) {
-    const SeqInfo<kPlain> s = seq_info<kPlain>(a, b, true);
-    a.entries[a.G + b].u = make_int4((int)s.q0, s.nq, s.T, b);
-    a.entries[a.G + b].v = make_int4(0, a.causal, -1, 0);
-  }
-  if (threadIdx.x == 0) plan->part_rows = 0;
-  bad = __syncthreads_or(bad);
-  if (bad && threadIdx.x == 0) atomicOr(a.err, ERR_BLOCK_TABLE);
-  if (bad || a.G == 0) return;  // (ranges that may overlap: nothing is shared)
-  // what each group would share, a warp per group
-  for (int g = warp; g < a.G; g += 32) {
-    const int f = __ldg(&a.group_start[g]), l = __ldg(&a.group_start[g + 1]);
-    int64_t P = __ldg(&a.shared_len[g]), apart = 0, tokens = 0, members = 0, q0 = INT32_MAX, row = INT32_MAX;
-    if (P < 0 && lane == 0) atomicOr(a.err, ERR_SEQ_LEN);
-    for (int b = f + lane; b < l; b += 32) {
-      const int4 u = a.entries[a.G + b].u;
-      // (a range that breaks the order has no query; nothing is shared then)
-      if (__ldg(&a.q_start[b + 1]) - __ldg(&a.q_start[b]) != u.y) P = 0;
-      if (u.y == 0) continue;
-      const int64_t see = a.causal ? (int64_t)u.z - u.y + 1 : u.z;
-      P = see < P ? see : P;
-      apart += ((int64_t)u.y * a.H + ROWS - 1) / ROWS;
-      tokens += u.y;
-      ++members;
-      if (row == INT32_MAX) row = b;  // (a sequence without queries need not hold the prefix)
-      q0 = u.x < q0 ? u.x : q0;
-    }
-    P = warp_min(P);
-    q0 = warp_min(q0);
-    row = warp_min(row);
-    apart = warp_sum(apart);
-    tokens = warp_sum(tokens);
-    members = warp_sum(members);
-    P = P > 0 ? P / PAGE : 0;
-    const int64_t rows = tokens * a.H, together = (rows + ROWS - 1) / ROWS, tiles = (P + 1) / 2;
-    const bool take = members > 1 && P > 0 && rows <= PART_ROWS * members && together * (tiles + SHARE) < apart * tiles;
-    if (take && lane == 0) {
-      a.entries[g].u = make_int4((int)q0, (int)tokens, (int)P * PAGE, (int)row);
-      a.entries[g].v = make_int4(0, 0, 0, 0);
-    }
-  }
-  __syncthreads();
-  // the rows of their parts, as far as there is room
-  int64_t at = 0;
-  for (int g0 = 0; g0 < a.G; g0 += 1024) {
-    const int g = g0 + threadIdx.x;
-    const int64_t rows = g < a.G ? (int64_t)a.entries[g].u.y * a.H : 0;
-    int64_t sum;
-    const int64_t from = at + plan_sum(rows, tmp, &sum) - rows;
-    if (rows > 0) {
-      // (the groups that have room are the first ones: those behind one without begin further on)
-      if (from + rows <= a.part_rows) {
-        a.entries[g].v.z = (int)from;
-        atomicMax(reinterpret_cast<unsigned long long*>(&plan->part_rows), (unsigned long long)(from + rows));
-      } else {
-        a.entries[g].u.y = 0;
-      }
-    }
-    at += sum;
-  }
-  __syncthreads();
-  for (int g = warp; g < a.G; g += 32) {
-    const int4 u = a.entries[g].u;
-    if (u.y == 0) continue;
-    const int f = __ldg(&a.group_start[g]), l = __ldg(&a.group_start[g + 1]), from = a.entries[g].v.z;
-    for (int b = f + lane; b < l; b += 32) {
-      int4 m = a.entries[a.G + b].u;
-      if (m.y == 0) continue;
-      const int token = m.x - u.x;
-      m.z -= u.z;
-      a.entries[a.G + b].u = m;
-      a.entries[a.G + b].v = make_int4(u.z / PAGE, a.causal, (int)a.part_rows + from + token * a.H, 0);
-      for (int i = 0; i < m.y; ++i) a.part_seq[from / a.H + token + i] = make_int2(g, b);
-    }
-  }
-  __syncthreads();
-}
+using Way = Walk<MODE, Geo>;
+static_assert(sizeof(Way<kShared>) * N_LANE_WARPS <= OFF_SC - OFF_WALK && sizeof(Way<kWindow>) <= sizeof(Way<kShared>),
+              "segments");
 
 constexpr int PLAN_NEAR = 4096;
 
-// One CTA: row tiles before each sequence (base, in shared memory if they fit), the units of every row tile,
-// their total, and the row tile that each cluster's range starts in.
+// (base: in shared memory if it fits, but for a shared call, whose join reads it)
 template <int MODE>
-__global__ void __launch_bounds__(1024) plan_kernel(const ChunkArgs a, Plan* plan, int64_t* base, int clusters) {
+__global__ void __launch_bounds__(1024) plan_kernel(const ChunkArgs a, Plan<Geo>* plan, int64_t* base, int clusters) {
   grid_dependents_launch();
   __shared__ int64_t tmp[32];
-  __shared__ int64_t near[MODE == kShared ? 1 : PLAN_NEAR];  // (the join reads it of a shared call)
+  __shared__ int64_t near[MODE == kShared ? 1 : PLAN_NEAR];
   if constexpr (MODE != kShared) {
     if (a.B < PLAN_NEAR) base = near;
   }
   if (threadIdx.x == 0) *a.err = 0;
   __syncthreads();
-  const int n_seq = MODE == kShared ? a.G + a.B : a.B;
-  if constexpr (MODE == kShared) make_entries(a, plan, tmp);
-  int64_t pairs = 0;
-  for (int b0 = 0; b0 < n_seq; b0 += 1024) {
-    const int b = b0 + threadIdx.x;
-    const int64_t n = b < n_seq ? row_tiles(a, seq_info<MODE>(a, b, true)) : 0;
-    int64_t sum;
-    const int64_t inc = plan_sum(n, tmp, &sum);
-    if (b < n_seq) base[b] = pairs + inc - n;
-    pairs += sum;
-  }
-  if (threadIdx.x == 0) base[n_seq] = pairs;
-  __syncthreads();
-  int b = 0, rt = 0;
-  auto tiles = [&](int64_t p) -> int64_t {
-    if (p >= pairs) return 0;
-    int lo = 0, hi = n_seq;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (base[mid] <= p) lo = mid; else hi = mid;
-    }
-    b = lo;
-    rt = (int)(p - base[lo]);
-    Pages<MODE> pages;
-    return key_tiles(a, seq_info<MODE>(a, b, false), rt, &pages);
-  };
-  // The ranges are equal on an axis where a row tile is SWITCH + nt long, and the border falls on a
-  // key tile of it; x counts units (key tiles).
-  int64_t mine = 0, units;
-  for (int64_t p = threadIdx.x; p < pairs; p += 1024) mine += tiles(p);
-  (void)plan_sum(mine, tmp, &units);
-  const int64_t total = units + pairs * SWITCH;
-  int64_t nc = units / MIN_TILES > pairs ? units / MIN_TILES : pairs;
-  nc = nc > clusters ? clusters : (nc < 1 ? (units > 0 ? 1 : 0) : nc);
-  if (threadIdx.x == 0) {
-    plan->n_clusters = nc;
-    plan->units = units;
-    if (MODE == kShared) a.unit[pairs] = units;
-  }
-  int64_t at = 0;
-  for (int64_t p0 = 0; p0 < pairs; p0 += 1024) {
-    const int64_t p = p0 + threadIdx.x, n = pairs <= 1024 ? mine : tiles(p);
-    int64_t sum;
-    const int64_t before = at + plan_sum(n, tmp, &sum) - n;  // units before the row tile
-    const int64_t S = before + p * SWITCH, len = n + SWITCH;
-    if (MODE == kShared && p < pairs) a.unit[p] = before;
-    int64_t k = n > 0 ? S * nc / total : nc;
-    while (k < nc && k * total / nc < S) ++k;
-    for (; k < nc; ++k) {
-      const int64_t x = k * total / nc;
-      if (x >= S + len) break;
-      PlanEntry e;
-      e.b = b;
-      e.rt = rt;
-      e.nt = (int32_t)n;
-      e.off = (int32_t)(x - S > SWITCH ? x - S - SWITCH : 0);
-      e.x = before + e.off;
-      plan->e[k] = e;
-    }
-    at += sum;
-  }
-}
-
-// A cluster's way through its range: one segment (a run of key tiles of one row tile)
-// after the other.
-template <int MODE>
-struct Walk : Pages<MODE> {
-  SeqInfo<MODE> s;
-  int b, rt, nt, t;   // row tile, its key tiles, first key tile of the segment
-  int n;              // key tiles of the segment
-  int seg;            // segments before this one
-  int64_t left;       // units from this segment on
-  __device__ __forceinline__ void start(const ChunkArgs& a, const Plan& plan, int k) {
-    const PlanEntry e = plan.e[k];
-    b = e.b;
-    rt = e.rt;
-    nt = e.nt;
-    t = e.off;
-    left = (k + 1 < plan.n_clusters ? plan.e[k + 1].x : plan.units) - e.x;
-    seg = 0;
-    s = seq_info<MODE>(a, b, false);
-    if constexpr (MODE == kWindow) (void)key_tiles(a, s, rt, this);
-    n = (int)(left < nt - t ? left : nt - t);
-  }
-  __device__ __forceinline__ bool more() const { return left > 0; }
-  __device__ __forceinline__ void next(const ChunkArgs& a) {
-    left -= n;
-    ++seg;
-    if (left <= 0) return;
-    t = 0;
-    if (++rt >= row_tiles(a, s)) {
-      rt = 0;
-      do {
-        s = seq_info<MODE>(a, ++b, false);
-      } while (s.nq == 0);
-    }
-    nt = key_tiles(a, s, rt, this);
-    n = (int)(left < nt ? left : nt);
-  }
-  __device__ __forceinline__ bool whole() const { return t == 0 && n == nt; }
-  // whether the row tile's results are final (and not parts that the join adds up)
-  __device__ __forceinline__ bool final() const {
-    if constexpr (MODE == kShared) {
-      if (s.part >= 0) return false;
-    }
-    return whole();
-  }
-};
-
-static_assert(sizeof(Walk<kShared>) * N_LANE_WARPS <= OFF_SC - OFF_WALK && sizeof(Walk<kWindow>) <= sizeof(Walk<kShared>),
-              "segments");
-
-// The block-table entries of 32 of a row tile's pages, one per lane, from page `from` on.
-struct PageWindow {
-  int64_t from;
-  int32_t e;
-  // cache slot of the page's first row, or -1 (past the sequence, or an entry out of range)
-  template <int MODE>
-  __device__ __forceinline__ int64_t slot(const ChunkArgs& a, const Walk<MODE>& w, int64_t page, int lane, bool tell) {
-    if (page < from || page >= from + 32) {
-      from = page;
-      e = -1;
-      const int64_t at = MODE == kWindow ? w.at((int)page + lane) : page + lane;
-      if (at * PAGE < w.s.T) {
-        if constexpr (MODE == kShared)
-          e = __ldg(&a.block_table[(int64_t)w.s.row * a.max_blocks + w.s.page0 + at]);
-        else
-          e = __ldg(&a.block_table[(int64_t)w.b * a.max_blocks + at]);
-        if (e < 0 || (int64_t)e >= a.n_blocks) {
-          if (tell) atomicOr(a.err, ERR_BLOCK_TABLE);
-          e = -1;
-        }
-      }
-    }
-    const int32_t v = __shfl_sync(0xffffffffu, e, (int)(page - from));
-    return v < 0 ? -1 : (int64_t)v * PAGE;
-  }
-};
-
-// ------------------------------------------------------------------ arithmetic
-__device__ __forceinline__ uint64_t pk2(float lo, float hi) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
-  return d;
-}
-__device__ __forceinline__ float2 up2(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-__device__ __forceinline__ float lg2_approx(float x) {
-  float y;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
-
-// Two e4m3 terms of an f16 pair on its scale: hi = e4m3(x), lo = e4m3(x - hi) (the residual is exact in f16).
-__device__ __forceinline__ void split_h2(uint32_t x, uint16_t& hi, uint16_t& lo) {
-  const __half2 v = *reinterpret_cast<const __half2*>(&x);
-  hi = f16x2_to_e4m3x2(v);
-  const uint32_t d = e4m3x2_to_f16x2(hi);
-  lo = f16x2_to_e4m3x2(__hsub2(v, *reinterpret_cast<const __half2*>(&d)));
-}
-__device__ __forceinline__ uint32_t scaled_h2(uint32_t x, __half2 s) {
-  const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&x), s);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-// NaN codes (0x7F, 0xFF) of four bytes set to 0
-__device__ __forceinline__ uint32_t no_nan(uint32_t v) {
-  return v & ~__vcmpeq4(v & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-}
-
-__device__ __forceinline__ void sts64(uint32_t addr, uint2 v) {
-  asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(addr), "r"(v.x), "r"(v.y) : "memory");
+  if constexpr (MODE == kShared) make_entries(a, &plan->part_rows, tmp);
+  make_plan<MODE>(a, plan, base, MODE == kShared ? a.G + a.B : a.B, clusters, tmp,
+                  MODE == kShared ? a.unit : nullptr, nullptr);
 }
 
 // byte offset of 16-byte unit u (0..15) of row r in a payload: unit 4 s + i holds tokens
@@ -642,14 +211,14 @@ __device__ __forceinline__ uint32_t prow(int r, int u) {
 }
 
 struct Workspace {
-  Plan* plan;
+  Plan<Geo>* plan;
   float* m;   // [2 MAX_CLUSTERS][256]: slot 2k the first segment of cluster k, 2k + 1 its last
   float* l;
   float* o;   // [..][256][512]
   int64_t parts;  // (shared prefixes) behind the slots: the parts of row tiles that one cluster held whole
   // where the parts of row `row` of a row tile go, as a row of these arrays
   template <int MODE>
-  __device__ __forceinline__ int64_t part_row(const Walk<MODE>& w, int k, int row) const {
+  __device__ __forceinline__ int64_t part_row(const Way<MODE>& w, int k, int row) const {
     if constexpr (MODE == kShared) {
       if (w.whole()) return parts + w.s.part + (int64_t)w.rt * ROWS + row;
     }
@@ -719,8 +288,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
   const uint32_t tmem = *tmem_slot;
   grid_dependency_wait();  // the plan
   grid_dependents_launch();  // (the join kernel may come as soon as there is room)
-  const bool work = k < ws.plan->n_clusters;
-  Walk<MODE> w;
+  const bool work = k < ws.plan->n;
+  Way<MODE> w;
   if (work) w.start(a, *ws.plan, k);
   else w.left = 0;
   int gt = 0;  // key tiles of the range before this segment
@@ -792,7 +361,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
       bool ok = true;
       for (; ok && w.more(); w.next(a)) {
         // (and meanwhile the next row tile's queries come into L2)
-        Walk<MODE> wn = w;
+        Way<MODE> wn = w;
         wn.next(a);
         if (wn.more()) {
           const int64_t r0 = (int64_t)wn.rt * ROWS + rank * CROWS, rows = (int64_t)wn.s.nq * a.H;
@@ -917,7 +486,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
       float* mgs = reinterpret_cast<float*>(sm + OFF_MG);
       int* lim = reinterpret_cast<int*>(sm + OFF_LIM);
       float* cs = reinterpret_cast<float*>(sm + OFF_C);
-      Walk<MODE>* walk = reinterpret_cast<Walk<MODE>*>(sm + OFF_WALK) + (warp - W_LANE);  // (it has no registers to spare)
+      Way<MODE>* walk = reinterpret_cast<Way<MODE>*>(sm + OFF_WALK) + (warp - W_LANE);  // (it has no registers to spare)
       const int rh = row0 + 16 * hl;          // the thread's rows of a tile: rh, rh + 8
       const int mh = rh + 8 * (i4 & 1);       // the row this lane speaks for there
       uint32_t px = 0;
@@ -929,7 +498,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
       // The queries of a row tile: two e4m3 terms on the scale that puts a row's largest value
       // in [128, 256); c folds the scale back in, with sm_scale log2 e. Two of the thread's rows
       // at a time, their channels all in flight at once.
-      auto load_query = [&](const Walk<MODE>& x) -> bool {
+      auto load_query = [&](const Way<MODE>& x) -> bool {
         const int64_t r0 = (int64_t)x.rt * ROWS + rank * CROWS, rows = (int64_t)x.s.nq * a.H;
         const uint32_t qlo = smem_u32(sm + OFF_QL) + part * OP_ATOM, qrp = smem_u32(sm + OFF_QR);
         if (part == 0) {  // the keys that row q * 32 + lane sees (rows past the last one are copies of it)
@@ -1022,7 +591,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
       if (more) *walk = w;  // (every lane, the same)
       __syncwarp();
       while (ok && more) {
-        const Walk<MODE>& x = *walk;
+        const Way<MODE>& x = *walk;
         ok = load_query(x) && quarter_sync();  // (the sync: cs and lim are read by every part)
         if (!ok) break;
         const int n_tiles = x.n;
@@ -1215,7 +784,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
           st_async_b32(to + 4, __float_as_uint(mm), bar);
         }
         gt += n_tiles;
-        Walk<MODE> wn = x;
+        Way<MODE> wn = x;
         wn.next(a);
         more = wn.more();
         __syncwarp();
@@ -1337,9 +906,9 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
       const uint32_t rs = map_to(smem_u32(&bars[B_RS]), 2);
       bool ok = true;
       for (; ok && w.more(); w.next(a)) {
-        const int lim0 = limit_of(a, w.s, first_token<MODE>(a, w.rt));  // the tile's first row sees least
+        const int lim0 = limit_of(a, w.s, first_token<Geo>(a, w.rt));  // the tile's first row sees least
         // (a window: that of the tile's last row begins last)
-        const int from = MODE == kWindow ? window_from(a, limit_of(a, w.s, last_token(a, w.s, w.rt))) : 0;
+        const int from = MODE == kWindow ? window_from(a, limit_of(a, w.s, last_token<Geo>(a, w.s, w.rt))) : 0;
         float ref = -INFINITY, hi = -INFINITY;  // the row's reference in O, and the highest one so far
         for (int i = 0; i < w.n; ++i) {
           const int g = gt + i, pb = g & 1, vs = g % NVT;
@@ -1556,7 +1125,7 @@ constexpr int FEW_ROW_TILES = 8;
 // tile's or those that range borders cut it into, by one warp.
 __device__ __forceinline__ void join_parts(const ChunkArgs& a, const Workspace& ws, const int64_t* base, int64_t row,
                                            int lane) {
-  const int64_t nc = ws.plan->n_clusters;
+  const int64_t nc = ws.plan->n;
   const int2 of = a.part_seq[row / a.H];
   // where the ranges begin, two a lane (behind the last: never)
   int64_t xs[2];
@@ -1661,7 +1230,7 @@ __global__ void __launch_bounds__(256) join_kernel(const ChunkArgs a, const Work
       return;
     }
   }
-  const int64_t nc = ws.plan->n_clusters;
+  const int64_t nc = ws.plan->n;
   if (k >= nc) return;
   __shared__ int64_t xs[MAX_CLUSTERS + 1];    // the units where the ranges begin
   if (threadIdx.x <= nc) xs[threadIdx.x] = threadIdx.x < nc ? ws.plan->e[threadIdx.x].x : ws.plan->units;
@@ -1741,7 +1310,7 @@ __global__ void __launch_bounds__(256) join_kernel(const ChunkArgs a, const Work
 }
 
 constexpr int64_t OFF_PLAN = 256, OFF_BASE = 2048;
-static_assert(OFF_PLAN + sizeof(Plan) <= OFF_BASE, "plan area");
+static_assert(OFF_PLAN + sizeof(Plan<Geo>) <= OFF_BASE, "plan area");
 
 // What the workspace of a call holds, behind the plan (from sizes alone).
 struct Layout {
@@ -1783,6 +1352,10 @@ Layout layout_of(int B, int H, int64_t total_q, int max_blocks, int G, int64_t w
   return w;
 }
 
+// Whether a call's sequences have so few rows on average that the kernel for them is faster.
+constexpr int FEW_ROWS = 32;
+bool few_rows(int B, int H, int64_t total_q) { return total_q * H <= (int64_t)FEW_ROWS * B; }
+
 template <int MODE>
 cudaError_t launch(ChunkArgs a, void* workspace, cudaStream_t s) {
   static std::atomic<int> memo[MAX_DEVICES];
@@ -1811,7 +1384,7 @@ cudaError_t launch(ChunkArgs a, void* workspace, cudaStream_t s) {
   a.part_seq = reinterpret_cast<int2*>(p + w.part_seq);
   a.part_rows = w.part_rows;
   Workspace ws;
-  ws.plan = reinterpret_cast<Plan*>(p + OFF_PLAN);
+  ws.plan = reinterpret_cast<Plan<Geo>*>(p + OFF_PLAN);
   int64_t* base = reinterpret_cast<int64_t*>(p + OFF_BASE);
   ws.m = reinterpret_cast<float*>(p + w.m);
   ws.l = ws.m + w.rows;
@@ -1843,6 +1416,7 @@ int64_t chunk_workspace(int B, int H, int64_t total_q, int max_blocks) {
   return layout_of<kPlain>(B, H, total_q, max_blocks, 0, 0, 0).bytes;
 }
 int64_t window_workspace(int B, int H, int64_t total_q, int max_blocks, int window, int n_sink) {
+  if (few_rows(B, H, total_q)) return rows_window_workspace(B, H, total_q, max_blocks, window, n_sink);
   return layout_of<kWindow>(B, H, total_q, max_blocks, 0, window, n_sink).bytes;
 }
 int64_t shared_workspace(int B, int H, int64_t total_q, int max_blocks, int G) {
@@ -1850,7 +1424,9 @@ int64_t shared_workspace(int B, int H, int64_t total_q, int max_blocks, int G) {
 }
 
 cudaError_t launch_chunk(const ChunkArgs& a, void* workspace, cudaStream_t s) { return launch<kPlain>(a, workspace, s); }
-cudaError_t launch_window(const ChunkArgs& a, void* workspace, cudaStream_t s) { return launch<kWindow>(a, workspace, s); }
+cudaError_t launch_window(const ChunkArgs& a, void* workspace, cudaStream_t s) {
+  return few_rows(a.B, a.H, a.total_q) ? launch_rows_window(a, workspace, s) : launch<kWindow>(a, workspace, s);
+}
 cudaError_t launch_shared(const ChunkArgs& a, void* workspace, cudaStream_t s) { return launch<kShared>(a, workspace, s); }
 
 }  // namespace kv8

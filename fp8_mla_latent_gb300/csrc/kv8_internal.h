@@ -216,6 +216,9 @@ struct ChunkArgs {
 int64_t chunk_workspace(int B, int H, int64_t total_q, int max_blocks);
 int64_t window_workspace(int B, int H, int64_t total_q, int max_blocks, int window, int n_sink);
 int64_t shared_workspace(int B, int H, int64_t total_q, int max_blocks, int G);
+// (sequences of few rows: rows.cu)
+int64_t rows_window_workspace(int B, int H, int64_t total_q, int max_blocks, int window, int n_sink);
+cudaError_t launch_rows_window(const ChunkArgs& a, void* workspace, cudaStream_t s);
 cudaError_t launch_chunk(const ChunkArgs& a, void* workspace, cudaStream_t s);
 cudaError_t launch_window(const ChunkArgs& a, void* workspace, cudaStream_t s);
 cudaError_t launch_shared(const ChunkArgs& a, void* workspace, cudaStream_t s);

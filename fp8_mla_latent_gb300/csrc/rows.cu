@@ -1,0 +1,850 @@
+// rows.cu -- absorbed MLA attention over the paged fp8 latent cache for sequences of few rows (single
+// tokens of a few heads): the same mathematics and precision as chunk.cu,
+//   z_t = sm * ( sLc_t <q_lat, dec(Lc_t)> + sRc_t <q_rope, dec(Rc_t)> ),   out = sum_t softmax(z)_t sLc_t dec(Lc_t)
+// with the keys as the MMAs' M and a row tile of 16 (token, head) pairs as their N, on one CTA per SM.
+//
+// A range of (row tile, key tile) units is one CTA's.  Per key tile of 128 tokens, whose bytes are loaded
+// once by TMA and read by both contractions as they are (kind::f8f6f4):
+//   S[t][r]  = K_t . Q_r       M = 128, N = 32: the query's hi terms, then its lo terms; Lc and Rc apart
+//   g'[r][t] = 2^(c u - M_r + 7) sLc_t   as two e4m3 terms; M_r follows the row's largest weight 2^(c u) sLc
+//   O[d][r] += sum_t V[t][d] g'[r][t]    four blocks of 128 channels, N = 32
+//
+// The keys alternate between two streams, each with eight softmax warps, its own references, sums and O
+// (TMEM holds both: 2 x 128 columns, and four buffers of S), which are joined at the row tile's end.
+// A tile's chain -- scores, maximum over its tokens, weights, context -- is longer than the time in
+// which its bytes come, so that two of them have to run at once.
+//
+// Warps: 0 loads; 1 issues the scores' MMAs; 2 the context's; 3-18 softmax: stream, half of the rows, and
+// TMEM lane quarter.  Every wait is bounded (2 s); on a timeout the CTA flags the workspace's error word,
+// drains its MMAs and copies and leaves.
+#include <cuda.h>
+
+#include "chunk_work.cuh"
+
+namespace kv8 {
+namespace {
+
+constexpr int N = 16;                        // rows of a row tile
+constexpr int NB = 2 * N;                    // columns: hi terms, lo terms
+constexpr int NH = 8;                        // rows of a softmax warp
+constexpr int KBLK = TILE * 128;             // 16 KB: [128 tokens x 128 bytes]
+constexpr int RBLK = TILE * 64;              // 8 KB: [128 tokens x 64 bytes]
+constexpr int RL = 11, RR = 2;               // rings of Lc blocks and Rc blocks
+constexpr int NTF = 4;                       // tiles loaded: barriers, row scales
+constexpr int NS = 4;                        // S buffers
+static_assert(RL <= 12, "a block of tile i has the slot of tile i - 3 at the oldest: NTF tiles are told apart");
+constexpr int W_TMA = 0, W_MMA = 1, W_CTX = 2, W_SOFT = 3;
+constexpr int N_SOFT = 16, N_SET = 8;        // softmax warps, of a stream
+constexpr int NTHREADS = (W_SOFT + N_SOFT) * 32;
+constexpr float TAU = 1.0f, P_LOG = 7.0f, DOWN = 10.0f, LG_MIN = -40.0f, DOWN_CAP = 50.0f;  // (as in chunk.cu)
+constexpr uint64_t WAIT_NS = 2000000000ull;
+
+struct Geo {
+  static constexpr int ROWS = N, RANGES = NUM_SMS, SWITCH = 2, MIN_TILES = 1;
+};
+template <int MODE>
+using Way = Walk<MODE, Geo>;
+
+constexpr int B_TFULL = 0;                   // [NTF] a tile's blocks and scales loaded
+constexpr int B_LEMPTY = B_TFULL + NTF;      // [RL] read by the context's MMAs
+constexpr int B_REMPTY = B_LEMPTY + RL;      // [RR] read by the scores'
+constexpr int B_SFULL = B_REMPTY + RR;       // [NS] S of a tile in TMEM
+constexpr int B_SEMPTY = B_SFULL + NS;       // [NS] read (8 warps)
+constexpr int B_PFULL = B_SEMPTY + NS;       // [2 streams] weights written, O rescaled (8)
+constexpr int B_ODONE = B_PFULL + 2;         // [2] a tile's context MMAs done
+constexpr int B_G = B_ODONE + 2;             // [2][2] the four warps of a stream and half meet
+constexpr int B_QREADY = B_G + 4;            // a row tile's query in place (16)
+constexpr int B_EP = B_QREADY + 1;           // the softmax warps meet (16)
+constexpr int B_DRAIN = B_EP + 1;            // [2] the issuers' last MMAs
+constexpr int NBAR = B_DRAIN + 2;
+
+constexpr int OFF_FLAGS = 512;               // tmem base, abort flag
+constexpr int OFF_FACTS = 528;               // [NTF] pages present
+constexpr int OFF_CS = 640;                  // [2 segments][16] the rows' c
+constexpr int OFF_LIM = OFF_CS + 128;        // [2][16] the keys that they see
+constexpr int OFF_REF = OFF_LIM + 128;       // [2 streams][16] references at a row tile's end
+constexpr int OFF_LS = 1024;                 // [2][4 warps][16] sums
+constexpr int OFF_RMAX = OFF_LS + 512;       // [2][2 buffers][4][16] a tile's largest weights
+constexpr int OFF_WALK = OFF_RMAX + 1024;    // [16 warps] segments
+constexpr int OFF_SCR = 4096;                // [NTF][128][2] row scales
+constexpr int OFF_Q = OFF_SCR + NTF * TILE * 8;      // [4 blocks][NB x 128 B], [NB x 64 B]
+constexpr int OFF_P = OFF_Q + 4 * NB * 128 + NB * 64;  // [2 streams][NB x 128 tokens]
+constexpr int OFF_L = OFF_P + 2 * NB * 128;
+constexpr int OFF_R = OFF_L + RL * KBLK;
+constexpr int SMEM = OFF_R + RR * RBLK;
+constexpr int S_COLS = 2 * NB, T_O = NS * S_COLS, O_COLS = 4 * NB;
+static_assert(NBAR * 8 <= OFF_FLAGS && OFF_REF + 128 <= OFF_LS && OFF_WALK + N_SOFT * 64 <= OFF_SCR, "layout");
+static_assert(sizeof(Way<kShared>) <= 64 && sizeof(Way<kWindow>) <= 64, "segments");
+static_assert(OFF_Q % 1024 == 0 && OFF_P % 1024 == 0 && OFF_L % 1024 == 0 && OFF_R % 1024 == 0, "swizzle atoms");
+static_assert(SMEM <= 232448 && T_O + 2 * O_COLS <= 512, "shared memory and TMEM");
+
+// The reduction over the 32 lanes of each of 8 values: lane l is left with that of value l / 4.
+template <bool MAX>
+__device__ __forceinline__ float reduce8(const float (&v)[8], int lane) {
+  float t[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const bool up = lane & 16;
+    const float send = up ? v[j] : v[j + 4], keep = up ? v[j + 4] : v[j];
+    const float recv = __shfl_xor_sync(0xffffffffu, send, 16);
+    t[j] = MAX ? fmaxf(keep, recv) : keep + recv;
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const bool up = lane & 8;
+    const float send = up ? t[j] : t[j + 2], keep = up ? t[j + 2] : t[j];
+    const float recv = __shfl_xor_sync(0xffffffffu, send, 8);
+    t[j] = MAX ? fmaxf(keep, recv) : keep + recv;
+  }
+  {
+    const bool up = lane & 4;
+    const float send = up ? t[0] : t[1], keep = up ? t[1] : t[0];
+    const float recv = __shfl_xor_sync(0xffffffffu, send, 4);
+    t[0] = MAX ? fmaxf(keep, recv) : keep + recv;
+  }
+#pragma unroll
+  for (int o = 2; o > 0; o >>= 1) {
+    const float recv = __shfl_xor_sync(0xffffffffu, t[0], o);
+    t[0] = MAX ? fmaxf(t[0], recv) : t[0] + recv;
+  }
+  return t[0];
+}
+
+// 16-byte unit u (0..3) of row r in a 64-byte-swizzled block
+__device__ __forceinline__ uint32_t sw64(int r, int u) {
+  return (uint32_t)((r >> 3) * 512 + (r & 7) * 64 + ((u ^ ((r >> 1) & 3)) << 4));
+}
+__device__ __forceinline__ void sts8(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+struct Parts {
+  Plan<Geo>* plan;
+  float* m;       // [2 RANGES][16]: slot 2k the first segment of range k, 2k + 1 its last; behind them (shared
+  float* l;       // prefixes, from `whole` on) the row tiles that one range held whole
+  float* o;       // [..][512]
+  int64_t whole;
+  template <int MODE>
+  __device__ __forceinline__ int64_t row(const Way<MODE>& w, int k, int r) const {
+    if constexpr (MODE == kShared) {
+      if (w.whole()) return whole + w.s.part + (int64_t)w.rt * N + r;
+    }
+    return (int64_t)(2 * k + (w.seg == 0 ? 0 : 1)) * N + r;
+  }
+};
+
+template <int MODE>
+__global__ void __launch_bounds__(NTHREADS, 1)
+    rows_kernel(const ChunkArgs a, const Parts ps, const __grid_constant__ CUtensorMap kmap,
+                const __grid_constant__ CUtensorMap rmap, const __grid_constant__ CUtensorMap smap) {
+  extern __shared__ __align__(1024) uint8_t sm[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int k = (int)blockIdx.x;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + OFF_FLAGS);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + OFF_FLAGS + 4);
+  volatile uint32_t* facts = reinterpret_cast<volatile uint32_t*>(sm + OFF_FACTS);
+  const uint32_t qb = smem_u32(sm + OFF_Q), lring = smem_u32(sm + OFF_L), rring = smem_u32(sm + OFF_R);
+  auto fail = [&]() {
+    *abort_flag = 1;
+    atomicOr(a.err, ERR_TIMEOUT);
+  };
+  auto wait = [&](int bar, uint32_t parity) -> bool {
+    return mbar_wait_warp(&bars[bar], parity & 1, abort_flag, WAIT_NS);
+  };
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NBAR; ++i) mbar_init(&bars[i], 1);
+    for (int i = 0; i < NS; ++i) mbar_init(&bars[B_SEMPTY + i], N_SET);
+    for (int i = 0; i < 2; ++i) mbar_init(&bars[B_PFULL + i], N_SET);
+    for (int i = 0; i < 4; ++i) mbar_init(&bars[B_G + i], 4);
+    mbar_init(&bars[B_QREADY], N_SOFT);
+    mbar_init(&bars[B_EP], N_SOFT);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == W_MMA) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  grid_dependency_wait();    // the plan
+  grid_dependents_launch();
+  Way<MODE> w;
+  if (k < ps.plan->n) w.start(a, *ps.plan, k);
+  else w.left = 0;
+  int gt = 0;  // key tiles of the range before this segment
+
+  if (warp == W_TMA) {
+    bool ok = true;
+    int asked = 0;  // tiles whose barrier is armed
+    for (; ok && w.more(); w.next(a)) {
+      PageWindow pw;
+      pw.from = -64;
+      for (int i = 0; ok && i < w.n; ++i) {
+        const int g = gt + i, tf = g % NTF, rs = g % RR;
+        const int64_t page = 2 * (int64_t)(w.t + i);
+        const int64_t s0 = pw.slot(a, w, page, lane, true), s1 = pw.slot(a, w, page + 1, lane, true);
+        const uint32_t pages = (s0 >= 0 ? 1u : 0u) + (s1 >= 0 ? 1u : 0u);
+        uint64_t* tb = &bars[B_TFULL + tf];
+        if (!wait(B_REMPTY + rs, (uint32_t)(g / RR) ^ 1u)) {
+          ok = false;
+          break;
+        }
+#pragma unroll 1
+        for (int blk = 0; blk < 4; ++blk) {
+          const int jb = 4 * g + blk, ls = jb % RL;
+          if (!wait(B_LEMPTY + ls, (uint32_t)(jb / RL) ^ 1u)) {
+            ok = false;
+            break;
+          }
+          if (blk == 0) {
+            // (tile g - 4's scales are read: its context's MMAs, which come behind its weights, have freed
+            // this block's slot or one before it)
+            facts[tf] = (s0 >= 0 ? 1u : 0u) | (s1 >= 0 ? 2u : 0u);
+            mbar_arrive_expect_tx_warp(tb, pages * (uint32_t)(2 * PAGE * 4 + 4 * PAGE * 128 + PAGE * 64));
+            asked = g + 1;
+            const uint32_t sd = smem_u32(sm + OFF_SCR) + tf * TILE * 8, rd = rring + rs * RBLK;
+            if (s0 >= 0) {
+              tma_load_1d_warp(sd, &smap, (int)(2 * s0), tb);
+              tma_load_2d_warp(rd, &rmap, DL, (int)s0, tb);
+            }
+            if (s1 >= 0) {
+              tma_load_1d_warp(sd + 2 * PAGE * 4, &smap, (int)(2 * s1), tb);
+              tma_load_2d_warp(rd + PAGE * 64, &rmap, DL, (int)s1, tb);
+            }
+          }
+          const uint32_t ld = lring + ls * KBLK;
+          if (s0 >= 0) tma_load_2d_warp(ld, &kmap, 128 * blk, (int)s0, tb);
+          if (s1 >= 0) tma_load_2d_warp(ld + PAGE * 128, &kmap, 128 * blk, (int)s1, tb);
+        }
+      }
+      gt += w.n;
+    }
+    if (!ok) {
+      // (a tile requested in part never completes its barrier: that wait ends at its bound)
+      if (lane == 0) fail();
+      const int zero = 0;
+      for (int i = asked > NTF ? asked - NTF : 0; i < asked; ++i)
+        (void)mbar_wait(&bars[B_TFULL + i % NTF], (i / NTF) & 1, &zero, WAIT_NS);
+    }
+    __syncwarp();
+  } else if (warp == W_MMA) {
+    const uint32_t id = idesc_f16(128, NB, false, false);  // e4m3 x e4m3 (format 0)
+    bool ok = true;
+    for (; ok && w.more(); w.next(a)) {
+      if (!wait(B_QREADY, (uint32_t)w.seg)) {
+        ok = false;
+        break;
+      }
+      for (int i = 0; i < w.n; ++i) {
+        const int g = gt + i, sb = g % NS;
+        if (!wait(B_SEMPTY + sb, (uint32_t)(g / NS) ^ 1u) || !wait(B_TFULL + g % NTF, (uint32_t)(g / NTF))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t dl = tmem + sb * S_COLS, dr = dl + NB;
+#pragma unroll 1
+        for (int blk = 0; blk < 4; ++blk) {
+          const uint64_t ad = smem_desc(lring + ((4 * g + blk) % RL) * KBLK, 16, 1024, SW128);
+          const uint64_t bd = smem_desc(qb + blk * NB * 128, 16, 1024, SW128);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) mma_f8_warp(dl, ad + 2 * kk, bd + 2 * kk, id, (blk | kk) != 0);
+        }
+        const uint64_t ad = smem_desc(rring + (g % RR) * RBLK, 16, 512, SW64);
+        const uint64_t bd = smem_desc(qb + 4 * NB * 128, 16, 512, SW64);
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) mma_f8_warp(dr, ad + 2 * kk, bd + 2 * kk, id, kk != 0);
+        mma_commit_warp(&bars[B_REMPTY + g % RR]);
+        mma_commit_warp(&bars[B_SFULL + sb]);
+      }
+      gt += w.n;
+    }
+    if (!ok && lane == 0) fail();
+    const int zero = 0;
+    mma_commit_warp(&bars[B_DRAIN]);
+    (void)mbar_wait(&bars[B_DRAIN], 0, &zero, WAIT_NS);
+    __syncwarp();
+  } else if (warp == W_CTX) {
+    const uint32_t id = idesc_f16(128, NB, true, false);  // A = V, MN-major
+    const uint32_t pb = smem_u32(sm + OFF_P);
+    bool ok = true;
+    for (; ok && w.more(); w.next(a)) {
+      for (int i = 0; i < w.n; ++i) {
+        const int g = gt + i, st = g & 1;
+        if (!wait(B_PFULL + st, (uint32_t)(g >> 1)) || !wait(B_TFULL + g % NTF, (uint32_t)(g / NTF))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll 1
+        for (int m = 0; m < 4; ++m) {
+          const int ls = (4 * g + m) % RL;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_f8_warp(tmem + T_O + st * O_COLS + m * NB, smem_desc(lring + ls * KBLK + kk * 4096, KBLK, 1024, SW128),
+                        smem_desc(pb + st * NB * 128 + kk * 32, 16, 1024, SW128), id, (i > 1 || kk > 0) ? 1u : 0u);
+          mma_commit_warp(&bars[B_LEMPTY + ls]);
+        }
+        mma_commit_warp(&bars[B_ODONE + st]);
+      }
+      gt += w.n;
+    }
+    if (!ok && lane == 0) fail();
+    const int zero = 0;
+    mma_commit_warp(&bars[B_DRAIN + 1]);
+    (void)mbar_wait(&bars[B_DRAIN + 1], 0, &zero, WAIT_NS);
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------- query, softmax, results
+    const int sw = warp - W_SOFT;
+    const int set = sw >> 3, grp = (sw >> 2) & 1, wq = sw & 3;
+    const int hb = grp * NH;                     // rows hb .. hb + 7
+    const int row = (warp & 3) * 32 + lane;      // token of the tile (TMEM lane); channel of a block of O
+    const int half = row >> 6;                   // its page
+    const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
+    float* cs = reinterpret_cast<float*>(sm + OFF_CS);
+    int* lim = reinterpret_cast<int*>(sm + OFF_LIM);
+    float* refs = reinterpret_cast<float*>(sm + OFF_REF);
+    float* lsum = reinterpret_cast<float*>(sm + OFF_LS);
+    float* rmax = reinterpret_cast<float*>(sm + OFF_RMAX) + set * 128;
+    Way<MODE>* walk = reinterpret_cast<Way<MODE>*>(sm + OFF_WALK + sw * 64);
+    uint32_t gph = 0, eph = 0;
+    auto group_sync = [&]() -> bool {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[B_G + set * 2 + grp]);
+      return wait(B_G + set * 2 + grp, gph++);
+    };
+    auto all_sync = [&]() -> bool {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[B_EP]);
+      return wait(B_EP, eph++);
+    };
+    // Row `sw` of a row tile's query, by this warp: two e4m3 terms on the scale that puts its largest value
+    // in [128, 256), and c, which folds the scale back in, with sm_scale log2 e.  (Rows past the last one
+    // are copies of it.)
+    auto source = [&](const Way<MODE>& x, const uint16_t*& ql, const uint16_t*& qr) -> int {
+      const int64_t r = (int64_t)x.rt * N + sw, rows = (int64_t)x.s.nq * a.H;
+      const uint32_t at = (uint32_t)(r < rows ? r : rows - 1);
+      const int tok = (int)(at / (uint32_t)a.H), head = (int)(at % (uint32_t)a.H);
+      ql = a.q_lat + (x.s.q0 + tok) * a.ql_t + (int64_t)head * a.ql_h;
+      qr = a.q_rope + (x.s.q0 + tok) * a.qr_t + (int64_t)head * a.qr_h;
+      return tok;
+    };
+    auto load_query = [&](const Way<MODE>& x) {
+      const uint16_t *ql, *qr;
+      const int tok = source(x, ql, qr);
+      uint4 v[3];
+      v[0] = __ldg(reinterpret_cast<const uint4*>(ql) + lane);
+      v[1] = __ldg(reinterpret_cast<const uint4*>(ql) + 32 + lane);
+      v[2] = lane < 8 ? __ldg(reinterpret_cast<const uint4*>(qr) + lane) : make_uint4(0u, 0u, 0u, 0u);
+      // the largest magnitude, as bf16 bits (ordered; 0x7F80 and up is inf or NaN)
+      uint32_t t2 = 0;
+#pragma unroll
+      for (int j = 0; j < 3; ++j)
+        t2 = __vmaxu2(t2, __vmaxu2(__vmaxu2(v[j].x & 0x7FFF7FFFu, v[j].y & 0x7FFF7FFFu),
+                                   __vmaxu2(v[j].z & 0x7FFF7FFFu, v[j].w & 0x7FFF7FFFu)));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) t2 = __vmaxu2(t2, __shfl_xor_sync(0xffffffffu, t2, o));
+      const uint32_t mx = (t2 & 0xFFFFu) > (t2 >> 16) ? (t2 & 0xFFFFu) : (t2 >> 16);
+      const uint32_t nan = mx >= 0x7F80u ? 0x7F7F7F7Fu : 0u;
+      int e = (int)(mx >> 7) - 127;
+      e = e < -80 ? -80 : e;
+      if (mx == 0 || nan != 0u) e = 7;
+      const float sc = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
+      if (lane == 0) {
+        const int at = ((x.seg & 1) * N) + sw;
+        cs[at] = fmaxf(a.sm_scale * LOG2E * __uint_as_float((uint32_t)(127 - 7 + e) << 23), 1e-37f);
+        lim[at] = limit_of(a, x.s, tok);
+      }
+      auto terms = [&](uint32_t w0, uint32_t w1, uint32_t& hi, uint32_t& lo) {
+        const __half2 a0 = __floats2half2_rn(bf16_lo(w0) * sc, bf16_hi(w0) * sc);
+        const __half2 a1 = __floats2half2_rn(bf16_lo(w1) * sc, bf16_hi(w1) * sc);
+        uint16_t h0, l0, h1, l1;
+        split_h2(*reinterpret_cast<const uint32_t*>(&a0), h0, l0);
+        split_h2(*reinterpret_cast<const uint32_t*>(&a1), h1, l1);
+        hi = ((uint32_t)h0 | ((uint32_t)h1 << 16)) | nan;
+        lo = (uint32_t)l0 | ((uint32_t)l1 << 16);
+      };
+#pragma unroll
+      for (int j = 0; j < 3; ++j) {
+        uint2 hi, lo;
+        terms(v[j].x, v[j].y, hi.x, lo.x);
+        terms(v[j].z, v[j].w, hi.y, lo.y);
+        if (j < 2) {  // channels 256 j + 8 lane .. + 7: block 2 j + lane / 16, half of its unit lane % 16 / 2
+          const uint32_t blk = qb + (2 * j + (lane >> 4)) * NB * 128;
+          sts64(blk + sw128(sw, (lane & 15) >> 1) + (lane & 1) * 8, hi);
+          sts64(blk + sw128(N + sw, (lane & 15) >> 1) + (lane & 1) * 8, lo);
+        } else if (lane < 8) {
+          const uint32_t blk = qb + 4 * NB * 128;
+          sts64(blk + sw64(sw, lane >> 1) + (lane & 1) * 8, hi);
+          sts64(blk + sw64(N + sw, lane >> 1) + (lane & 1) * 8, lo);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[B_QREADY]);
+    };
+    // byte of weight [r][token `row`] in a K-major [NB x 128] block
+    auto p_off = [&](int r) -> uint32_t {
+      return (uint32_t)((r >> 3) * 1024 + (r & 7) * 128 + (((row >> 4) ^ (r & 7)) << 4) + (row & 15));
+    };
+    const uint32_t pb = smem_u32(sm + OFF_P) + set * NB * 128;
+    const uint32_t to = tmem + lane_addr + T_O + hb;  // O of stream 0, its rows' hi terms
+
+    bool ok = true, more = w.more();
+    if (more) {
+      *walk = w;  // (every lane, the same)
+      __syncwarp();
+      load_query(*walk);
+    }
+    while (ok && more) {
+      const Way<MODE>& x = *walk;
+      const int n_tiles = x.n, sp = (x.seg & 1) * N;
+      if (!wait(B_QREADY, (uint32_t)x.seg)) {
+        ok = false;
+        break;
+      }
+      float c[NH], mg[NH], mhi[NH], lp[NH];
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+        c[h] = cs[sp + hb + h];
+        mg[h] = mhi[h] = -INFINITY;
+        lp[h] = 0.f;
+      }
+      const int lim0 = lim[sp];  // the first row sees least
+      const int from = MODE == kWindow ? window_from(a, lim[sp + N - 1]) : 0;  // the last one's window begins last
+      {
+        // the next row tile's queries, into L2
+        Way<MODE> wn = x;
+        wn.next(a);
+        if (wn.more() && lane == 0) {
+          const uint16_t *ql, *qr;
+          (void)source(wn, ql, qr);
+          prefetch_l2(ql, DL * 2);
+          prefetch_l2(qr, DR * 2);
+        }
+        __syncwarp();
+      }
+#pragma unroll 1
+      for (int i = (set ^ gt) & 1; i < n_tiles; i += 2) {
+        const int g = gt + i, sb = g % NS, tf = g % NTF, kk = g >> 1;
+        if (!wait(B_TFULL + tf, (uint32_t)(g / NTF)) || !wait(B_SFULL + sb, (uint32_t)(g / NS))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t have = facts[tf];
+        bool full = have == 3u;
+        int t = 0;
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          const int t0 = x.at(2 * (x.t + i) + p) * PAGE;
+          full = full && lim0 - t0 >= PAGE && !(MODE == kWindow && t0 < from && a.n_sink - t0 < PAGE);
+          if (half == p) t = t0 + (row & (PAGE - 1));
+        }
+        const float2 s2 = *reinterpret_cast<const float2*>(sm + OFF_SCR + (tf * TILE + row) * 8);
+        // (sLc made finite: out of sight it may be anything, in sight the NaN or infinity shows in sRc)
+        const float sl = fminf(fmaxf(s2.x, 0.f), 3.0e38f), sr = fmaf(0.f, s2.x, s2.y);
+        const float lg = fmaxf(lg2_approx(sl), LG_MIN);
+        float u[NH];  // sLc S_L + sRc S_R
+        {
+          uint32_t r0[NH], r1[NH], r2[NH], r3[NH];
+          const uint32_t sa = tmem + lane_addr + sb * S_COLS + hb;
+          tmem_ld8(sa, r0);
+          tmem_ld8(sa + N, r1);
+          tmem_ld8(sa + 2 * N, r2);
+          tmem_ld8(sa + 3 * N, r3);
+          tmem_wait_ld();
+#pragma unroll
+          for (int h = 0; h < NH; ++h)
+            u[h] = fmaf(sr, __uint_as_float(r2[h]) + __uint_as_float(r3[h]),
+                        sl * (__uint_as_float(r0[h]) + __uint_as_float(r1[h])));
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[B_SEMPTY + sb]);
+        if (!full) {
+          const bool here = (have >> half) & 1u;
+#pragma unroll
+          for (int h = 0; h < NH; ++h) {
+            const int l = lim[sp + hb + h];
+            const bool sees = here && t < l && (MODE != kWindow || t >= window_from(a, l) || t < a.n_sink);
+            if (!sees) u[h] = -INFINITY;
+          }
+        }
+        // the rows' largest weights in the tile: over the warp's tokens, then the four warps'
+        {
+          float y[NH];
+#pragma unroll
+          for (int h = 0; h < NH; ++h) y[h] = fmaf(c[h], u[h], lg);
+          const float ym = reduce8<true>(y, lane);
+          if ((lane & 3) == 0) rmax[(kk & 1) * 64 + wq * N + hb + (lane >> 2)] = ym;
+        }
+        if (!group_sync()) {
+          ok = false;
+          break;
+        }
+        float f[NH];
+        bool moved = false;
+        {
+          const float* rm = rmax + (kk & 1) * 64 + hb;
+#pragma unroll
+          for (int h = 0; h < NH; ++h) {
+            const float ym = fmaxf(fmaxf(rm[h], rm[N + h]), fmaxf(rm[2 * N + h], rm[3 * N + h]));
+            float mn = mg[h];
+            if (ym > mg[h] + TAU) {
+              mn = ym;
+            } else if (ym < mg[h] - DOWN && ym >= mhi[h] - DOWN_CAP) {
+              mn = ym;
+            }
+            f[h] = mn == mg[h] ? 1.f : (mg[h] > -INFINITY ? ex2_approx(mg[h] - mn) : 0.f);
+            moved |= f[h] != 1.f;
+            mg[h] = mn;
+            mhi[h] = fmaxf(mhi[h], mn);
+          }
+        }
+        uint32_t phi[2], plo[2];
+#pragma unroll
+        for (int h = 0; h < NH; h += 4) {
+          float z[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            // (nothing in sight so far: u is -inf, and p 0)
+            const float p = ex2_approx(fmaf(c[h + j], u[h + j], P_LOG - fmaxf(mg[h + j], -3.0e38f)));
+            lp[h + j] = fmaf(lp[h + j], f[h + j], p);
+            z[j] = p * sl;
+          }
+          const __half2 x01 = __floats2half2_rn(z[0], z[1]), x23 = __floats2half2_rn(z[2], z[3]);
+          uint16_t h01, l01, h23, l23;
+          split_h2(*reinterpret_cast<const uint32_t*>(&x01), h01, l01);
+          split_h2(*reinterpret_cast<const uint32_t*>(&x23), h23, l23);
+          phi[h / 4] = (uint32_t)h01 | ((uint32_t)h23 << 16);
+          plo[h / 4] = (uint32_t)l01 | ((uint32_t)l23 << 16);
+        }
+        // the stream's tile before: its weights are read, and O is at rest
+        if (kk > 0 && !wait(B_ODONE + set, (uint32_t)(kk - 1))) {
+          ok = false;
+          break;
+        }
+        if (moved && i > 1) {
+          tc_fence_after();
+          __syncwarp();
+#pragma unroll 1
+          for (int term = 0; term < 2; ++term) {
+            uint32_t r[4][8];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) tmem_ld8(to + set * O_COLS + m * NB + term * N, r[m]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) r[m][j] = __float_as_uint(__uint_as_float(r[m][j]) * f[j]);
+              tmem_st8(to + set * O_COLS + m * NB + term * N, r[m]);
+            }
+          }
+          tmem_wait_st();
+        }
+        if (!full) {
+          // some row does not see all of this tile: no NaN code may stay in it
+#pragma unroll 1
+          for (int m = 0; m < 4; ++m) {
+            const uint32_t vb = lring + ((4 * g + m) % RL) * KBLK + (sw & 7) * 2048 + lane * 16;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint4 v = lds128(vb + j * 512);
+              sts128(vb + j * 512, make_uint4(no_nan(v.x), no_nan(v.y), no_nan(v.z), no_nan(v.w)));
+            }
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+          sts8(pb + p_off(hb + h), phi[h / 4] >> (8 * (h & 3)));
+          sts8(pb + p_off(N + hb + h), plo[h / 4] >> (8 * (h & 3)));
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[B_PFULL + set]);
+      }
+      if (!ok) break;
+      // ---- the row tile's (or its part's) end
+      const int last = gt + n_tiles - 1;
+      Way<MODE> wn = x;
+      wn.next(a);
+      more = wn.more();
+      if (more) {
+        // (its last scores are there: nothing reads the query any more)
+        if (!wait(B_SFULL + last % NS, (uint32_t)(last / NS))) {
+          ok = false;
+          break;
+        }
+        load_query(wn);
+      }
+      bool used[2];
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {
+        const int l = last - ((last ^ st) & 1);  // the stream's last tile
+        used[st] = l >= gt;
+        if (used[st] && !wait(B_ODONE + st, (uint32_t)(l >> 1))) ok = false;
+      }
+      if (!ok) break;
+      {
+        const float ls = reduce8<false>(lp, lane);
+        if ((lane & 3) == 0) lsum[(set * 4 + wq) * N + hb + (lane >> 2)] = ls;
+        float m = mg[0];
+#pragma unroll
+        for (int h = 1; h < NH; ++h) m = lane == h ? mg[h] : m;
+        if (wq == 0 && lane < NH) refs[set * N + hb + lane] = m;
+      }
+      if (!all_sync()) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      // both streams on the larger reference
+      auto joined = [&](int r, float& f0, float& f1, float& M) -> float {
+        const float m0 = refs[r], m1 = refs[N + r];
+        M = fmaxf(m0, m1);
+        f0 = m0 == M ? 1.f : ex2_approx(m0 - M);
+        f1 = m1 == M ? 1.f : ex2_approx(m1 - M);
+        const float* p = lsum + r;
+        return ((p[0] + p[N]) + (p[2 * N] + p[3 * N])) * f0 + ((p[4 * N] + p[5 * N]) + (p[6 * N] + p[7 * N])) * f1;
+      };
+      const bool final = x.final();
+      const int64_t rows = (int64_t)x.s.nq * a.H, r0 = (int64_t)x.rt * N;
+      float f0[NH], f1[NH];
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+        float M;
+        const float L = joined(hb + h, f0[h], f1[h], M);
+        const float inv = final ? (L == 0.f ? 0.f : 1.f / L) : (L == 0.f ? 0.f : 1.f);  // (a NaN stays one)
+        f0[h] *= inv;
+        f1[h] *= inv;
+      }
+      if (sw < N / NH * 4 && (sw & 3) == 0 && lane < NH && r0 + hb + lane < rows) {
+        float g0, g1, M;
+        const float L = joined(hb + lane, g0, g1, M);
+        M -= P_LOG;
+        const int64_t r = r0 + hb + lane;
+        if (final) {
+          if (a.lse != nullptr) a.lse[x.s.q0 * a.H + r] = L == 0.f ? -INFINITY : (M + log2f(L)) * LN2;
+        } else {
+          const int64_t at = ps.row(x, k, hb + lane);
+          ps.m[at] = M;
+          ps.l[at] = L;
+        }
+      }
+#pragma unroll 1
+      for (int mm = 0; mm < 2; ++mm) {
+        const int m = 2 * set + mm;  // (the streams' warps take half of the channels each)
+        float v[NH];
+#pragma unroll
+        for (int h = 0; h < NH; ++h) v[h] = 0.f;
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+          if (!used[st]) continue;
+          uint32_t rh[8], rl[8];
+          tmem_ld8(to + st * O_COLS + m * NB, rh);
+          tmem_ld8(to + st * O_COLS + m * NB + N, rl);
+          tmem_wait_ld();
+#pragma unroll
+          for (int h = 0; h < NH; ++h) {
+            const float f = st == 0 ? f0[h] : f1[h];
+            // (a factor of 0: nothing seen, or nothing that counts)
+            if (f != 0.f) v[h] = fmaf(__uint_as_float(rh[h]) + __uint_as_float(rl[h]), f, v[h]);
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+          if (r0 + hb + h >= rows) break;
+          if (final)
+            reinterpret_cast<__nv_bfloat16*>(a.out)[(x.s.q0 * a.H + r0 + hb + h) * DL + m * 128 + row] = __float2bfloat16_rn(v[h]);
+          else
+            ps.o[ps.row(x, k, hb + h) * DL + m * 128 + row] = v[h];
+        }
+      }
+      tc_fence_before();
+      if (!all_sync()) {  // O, the references and the sums may be written again
+        ok = false;
+        break;
+      }
+      gt += n_tiles;
+      *walk = wn;
+      __syncwarp();
+    }
+    if (!ok && lane == 0) fail();
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == W_MMA) tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------------ plan
+template <int MODE>
+__global__ void __launch_bounds__(1024) rows_plan_kernel(const ChunkArgs a, Plan<Geo>* plan, int64_t* base, int64_t* unit,
+                                                         int2* owner, int most) {
+  grid_dependents_launch();
+  __shared__ int64_t tmp[32];
+  if (threadIdx.x == 0) *a.err = 0;
+  __syncthreads();
+  make_plan<MODE>(a, plan, base, a.B, most, tmp, unit, owner);
+}
+
+// ------------------------------------------------------------------ join
+// The parts of a row tile's rows, a warp per row (and SPLIT-th of its channels), a block per row tile.
+template <int MODE, int SPLIT>
+__global__ void __launch_bounds__(N * 32) rows_join_kernel(const ChunkArgs a, const Parts ps, const int64_t* unit,
+                                                           const int2* owner) {
+  const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
+  const int64_t p = blockIdx.x / SPLIT;
+  const int ch = (int)(blockIdx.x % SPLIT) * (DL / SPLIT);
+  grid_dependency_wait();  // (every block: what it reads, and that this launch is not over before the kernel is)
+  const int64_t nc = ps.plan->n;
+  if (p >= ps.plan->tiles) return;
+  const int64_t S = unit[p], E = unit[p + 1];
+  __shared__ int64_t xs[Geo::RANGES + 1];
+  for (int i = threadIdx.x; i <= nc; i += N * 32) xs[i] = i < nc ? ps.plan->e[i].x : ps.plan->units;
+  __syncthreads();
+  // the ranges that it lies in: from the last that begins at S or before
+  const int k0 = __syncthreads_count(threadIdx.x < nc && xs[threadIdx.x < nc ? threadIdx.x : 0] <= S) - 1;
+  const int k1 = __syncthreads_count(threadIdx.x < nc && xs[threadIdx.x < nc ? threadIdx.x : 0] < E) - 1;
+  if (k0 == k1) return;  // whole
+  const int2 of = owner[p];
+  const SeqInfo<MODE> s = seq_info<MODE>(a, of.x, false);
+  const int64_t r = (int64_t)of.y * N + row;
+  if (r >= (int64_t)s.nq * a.H) return;
+  auto slot = [&](int j) -> int64_t { return (int64_t)(2 * j + (j == k0 && xs[k0] < S ? 1 : 0)) * N + row; };
+  auto there = [&](int j) { return j <= k1 && xs[j] != xs[j + 1]; };  // (a range without units has no part)
+  float M = -INFINITY, L = 0.f;
+  for (int j = k0 + lane; j <= k1; j += 32)
+    if (there(j)) M = fmaxf(M, ps.m[slot(j)]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  constexpr int Q = 4 / SPLIT;  // 16-byte units a lane
+  float4 acc[Q];
+#pragma unroll
+  for (int c = 0; c < Q; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int j0 = k0; j0 <= k1; j0 += 32) {
+    const int j = j0 + lane;
+    float wt = 0.f;
+    if (there(j)) {
+      const float m = ps.m[slot(j)];
+      wt = m > -INFINITY ? ex2_approx(m - M) : 1.f;  // (a NaN l stays one)
+      L += wt * ps.l[slot(j)];
+    }
+    const uint32_t has = __ballot_sync(0xffffffffu, there(j));
+    const int n = min(k1 - j0 + 1, 32);
+#pragma unroll(SPLIT == 1 ? 4 : 8)
+    for (int i = 0; i < n; ++i) {
+      const float w = __shfl_sync(0xffffffffu, wt, i);
+      const float4* o = reinterpret_cast<const float4*>(ps.o + slot(j0 + i) * DL + ch) + lane;
+#pragma unroll
+      for (int c = 0; c < Q; ++c) {
+        const float4 v = ((has >> i) & 1u) ? o[32 * c] : make_float4(0.f, 0.f, 0.f, 0.f);
+        acc[c].x += w * v.x;
+        acc[c].y += w * v.y;
+        acc[c].z += w * v.z;
+        acc[c].w += w * v.w;
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  const int64_t at = s.q0 * a.H + r;
+  uint2* out = reinterpret_cast<uint2*>(a.out + at * DL + ch) + lane;
+#pragma unroll
+  for (int c = 0; c < Q; ++c) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(acc[c].x * inv, acc[c].y * inv);
+    const __nv_bfloat162 y = __floats2bfloat162_rn(acc[c].z * inv, acc[c].w * inv);
+    out[32 * c] = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+  }
+  if (ch == 0 && a.lse != nullptr && lane == 0) a.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * LN2;
+}
+
+// ------------------------------------------------------------------ host
+constexpr int64_t OFF_PLAN = 256, OFF_BASE = 4096;
+static_assert(OFF_PLAN + sizeof(Plan<Geo>) <= OFF_BASE, "plan area");
+constexpr int FEW_ROW_TILES = 64;
+
+struct Layout {
+  int most;       // ranges
+  int64_t tiles;  // row tiles at most
+  int64_t unit, owner, m, rows, bytes;
+};
+Layout layout_of(int B, int H, int64_t total_q, int64_t keys) {
+  auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
+  Layout w;
+  w.tiles = total_q * H / N + B;
+  const int64_t units = w.tiles * keys;
+  w.most = (int)(units < 1 ? 1 : (units < NUM_SMS ? units : NUM_SMS));
+  int64_t at = OFF_BASE + up((int64_t)(B + 1) * 8);
+  w.unit = at;
+  at += up((w.tiles + 1) * 8);
+  w.owner = at;
+  at += up(w.tiles * 8);
+  w.m = at;
+  w.rows = w.most > 1 ? 2 * (int64_t)w.most * N : 0;
+  w.bytes = at + w.rows * (8 + DL * 4);
+  return w;
+}
+int64_t window_keys(int max_blocks, int64_t window, int64_t n_sink) {
+  const int64_t all = ((int64_t)max_blocks * PAGE + TILE - 1) / TILE, seen = (window + n_sink + N + 4 * PAGE) / TILE + 1;
+  return seen < all ? seen : all;
+}
+
+template <int MODE>
+cudaError_t launch(ChunkArgs a, const Layout& w, void* workspace, cudaStream_t s) {
+  static std::atomic<int> memo[MAX_DEVICES];
+  int done = 0;
+  cudaError_t e = per_device(memo, [](int* v) {
+    *v = 1;
+    return cudaFuncSetAttribute(rows_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+  }, &done);
+  if (e != cudaSuccess) return e;
+  char* p = static_cast<char*>(workspace);
+  a.err = reinterpret_cast<unsigned*>(p);
+  Parts ps;
+  ps.plan = reinterpret_cast<Plan<Geo>*>(p + OFF_PLAN);
+  ps.m = reinterpret_cast<float*>(p + w.m);
+  ps.l = ps.m + w.rows;
+  ps.o = ps.l + w.rows;
+  ps.whole = 0;
+  int64_t* unit = reinterpret_cast<int64_t*>(p + w.unit);
+  int2* owner = reinterpret_cast<int2*>(p + w.owner);
+  DecodeArgs d{};  // what the cache's tensor maps are made from
+  d.codes = a.codes;
+  d.scales = a.scales;
+  d.block_table = a.block_table;
+  d.n_blocks = a.n_blocks;
+  CUtensorMap kmap, rmap, smap;
+  if ((e = make_cache_map(d, &kmap)) != cudaSuccess || (e = make_rc_map(d, &rmap)) != cudaSuccess ||
+      (e = make_scale_map(d, &smap)) != cudaSuccess)
+    return e;
+  rows_plan_kernel<MODE><<<1, 1024, 0, s>>>(a, ps.plan, reinterpret_cast<int64_t*>(p + OFF_BASE), unit, owner, w.most);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  e = launch_after_prep(rows_kernel<MODE>, w.most, NTHREADS, SMEM, s, a, ps, kmap, rmap, smap);
+  if (e != cudaSuccess || w.most == 1) return e;
+  if (w.tiles < FEW_ROW_TILES)
+    return launch_after_prep(rows_join_kernel<MODE, 4>, (unsigned)(4 * w.tiles), N * 32, 0, s, a, ps,
+                             (const int64_t*)unit, (const int2*)owner);
+  return launch_after_prep(rows_join_kernel<MODE, 1>, (unsigned)w.tiles, N * 32, 0, s, a, ps, (const int64_t*)unit,
+                           (const int2*)owner);
+}
+
+}  // namespace
+
+int64_t rows_window_workspace(int B, int H, int64_t total_q, int max_blocks, int window, int n_sink) {
+  return layout_of(B, H, total_q, window_keys(max_blocks, window, n_sink)).bytes;
+}
+cudaError_t launch_rows_window(const ChunkArgs& a, void* workspace, cudaStream_t s) {
+  return launch<kWindow>(a, layout_of(a.B, a.H, a.total_q, window_keys(a.max_blocks, a.window, a.n_sink)), workspace, s);
+}
+
+}  // namespace kv8

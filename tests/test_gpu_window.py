@@ -58,6 +58,80 @@ def test_many_single_tokens():
     check(WindowCase(16, [1] * 200, lens, 150, 4, seed=5))
 
 
+FEW_LENS = [1, 2, 63, 64, 65, 127, 128, 129, 192, 257, 300, 700, 1500, 2, 640, 3]
+
+
+@pytest.mark.parametrize("sinks", [0, 1, 64, 70])
+@pytest.mark.parametrize("window", [1, 2, 63, 64, 65, 200, 5000])
+def test_single_tokens_around_pages_and_tiles(window, sinks):
+    check(WindowCase(16, [1] * 16, FEW_LENS, window, sinks, seed=window + sinks, pad=3))
+
+
+@pytest.mark.parametrize("H", [1, 3, 4, 8, 15, 16, 17, 20, 32])
+def test_few_rows_a_sequence(H):
+    """One to three tokens, some sequences with none, one with many: on average at most 32 rows."""
+    nq = [1, 1, 0, 1, 0, 1, 1, 0, 1, 1, 0, 1, 1, 0, 3, 1]
+    check(WindowCase(H, nq, FEW_LENS, 130, 5, seed=H, pad=2))
+    check(WindowCase(H, [0] * 14 + [9, 0], FEW_LENS, 400, 70, seed=H + 1))
+
+
+@pytest.mark.parametrize("H,T,window,sinks", [(16, 40000, 30000, 4), (1, 40000, 40000, 0), (4, 256, 100, 2), (32, 9000, 8000, 640),
+                                              (16, 1, 1, 0), (20, 5000, 1, 0), (8, 20000, 64, 9000)])
+def test_one_token(H, T, window, sinks):
+    check(WindowCase(H, [1], [T], window, sinks, seed=T + H))
+
+
+@pytest.mark.parametrize("B,T", [(300, 500), (152, 1000), (40, 3000)])
+def test_single_tokens_of_many_sequences_in_ranges_that_cross_them(B, T):
+    lens = [1 + (T * 7 * i) % T for i in range(B)]
+    check(WindowCase(16, [1] * B, lens, T // 2, 4, seed=B))
+
+
+def test_few_rows_that_see_nothing_and_queries_with_nan():
+    c = WindowCase(4, [3, 1, 4, 1], [2, 1, 0, 300], 40, 2, seed=17)
+    out, l = check(c)
+    c.q_lat[8, 2, 100] = math.nan
+    c.q_rope[3, 1, 3] = math.inf
+    got, gl, _ = run(c)
+    hit = torch.zeros(9, 4, dtype=torch.bool, device="cuda")
+    hit[8, 2] = hit[3, 1] = True
+    assert torch.isnan(got[hit]).all() and torch.isnan(gl[hit]).all()
+    assert torch.equal(got[~hit], out[~hit]) and torch.equal(gl[~hit], l[~hit])
+
+
+def test_keys_out_of_sight_never_reach_a_single_token():
+    """NaN behind a token's window, in pages that its window shares and in the last page behind its end."""
+    c = WindowCase(16, [1, 1, 1], [700, 333, 90], 100, 5, seed=18)
+    clean, clean_l, _ = run(c)
+    for b, at in ((0, 599), (0, 5), (0, 63), (1, 232), (1, 10)):
+        slot = int(c.slots[b][at])
+        c.codes[slot] = 0x7F
+        c.codes[slot, ::2] = 0xFF
+        c.scales[slot] = math.nan
+    out, l, err = run(c)
+    assert err == 0 and torch.equal(out, clean) and torch.equal(l, clean_l)
+    c.codes[int(c.slots[2][80])] = 0x7F
+    out, l, err = run(c)
+    assert torch.isnan(out[2]).all() and torch.isnan(l[2]).all() and torch.equal(out[:2], clean[:2])
+
+
+def test_row_scales_of_every_size_and_dominant_keys_for_single_tokens():
+    def rows(b, t, g):
+        x = torch.randn((t, 576), generator=g) * 2.0 ** torch.randint(-4, 5, (t, 1), generator=g)
+        x[::17] = 0
+        x[5::31] *= 1e-38
+        if b == 1:
+            x = 0.3 * torch.randn((t, 576), generator=g) + 0.5
+            x[2] *= 8
+            x[t - 40] *= 6
+        return x
+    c = WindowCase(16, [1, 1, 1], [700, 1500, 260], 600, 4, seed=19, rows=rows)
+    c.q_lat[1] = (c.q_lat[1].float() * 0.4 + 0.3).bfloat16()
+    c.q_lat[2] *= 1e-30
+    c.q_rope[2] *= 1e-30
+    check(c)
+
+
 def test_mixed_batch_with_sequences_that_have_no_query_or_no_token():
     check(WindowCase(16, [0, 3, 0, 1, 40, 0], [70, 500, 0, 1, 290, 64], 50, 3, seed=6, pad=9))
 
