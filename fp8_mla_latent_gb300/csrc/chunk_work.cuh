@@ -260,12 +260,15 @@ __device__ __forceinline__ void make_entries(const ChunkArgs& a, int64_t* part_r
   __syncthreads();
 }
 
+// owner[p] of row tile p: its sequence, its place there, the slot of its first part -- slot 2 k is the first
+// segment of range k, 2 k + 1 its last -- and the last range that it lies in.
+//
 // One CTA of 1024 threads: row tiles before each of n_seq sequences (base), the units of every row tile, their
 // total, and the row tile that each range starts in; with `unit`, the units before each row tile, and
-// with `owner`, its sequence and place there.
+// with `owner`, whose it is (below).
 template <int MODE, class G>
 __device__ __forceinline__ void make_plan(const ChunkArgs& a, Plan<G>* plan, int64_t* base, int n_seq, int most,
-                                          int64_t* tmp, int64_t* unit, int2* owner) {
+                                          int64_t* tmp, int64_t* unit, int4* owner) {
   int64_t pairs = 0;
   for (int b0 = 0; b0 < n_seq; b0 += 1024) {
     const int b = b0 + threadIdx.x;
@@ -311,9 +314,10 @@ __device__ __forceinline__ void make_plan(const ChunkArgs& a, Plan<G>* plan, int
     const int64_t before = at + plan_sum(n, tmp, &sum) - n;  // units before the row tile
     const int64_t S = before + p * G::SWITCH, len = n + G::SWITCH;
     if (unit != nullptr && p < pairs) unit[p] = before;
-    if (owner != nullptr && p < pairs) owner[p] = make_int2(b, rt);
     int64_t k = n > 0 ? S * nc / total : nc;
     while (k < nc && k * total / nc < S) ++k;
+    int64_t first = k - 1;  // the range that holds its first unit: one from before, or the last that begins there
+    bool before_it = true;
     for (; k < nc; ++k) {
       const int64_t x = k * total / nc;
       if (x >= S + len) break;
@@ -324,7 +328,9 @@ __device__ __forceinline__ void make_plan(const ChunkArgs& a, Plan<G>* plan, int
       e.off = (int32_t)(x - S > G::SWITCH ? x - S - G::SWITCH : 0);
       e.x = before + e.off;
       plan->e[k] = e;
+      if (e.off == 0) first = k, before_it = false;
     }
+    if (owner != nullptr && p < pairs) owner[p] = make_int4(b, rt, (int)(2 * first + before_it), (int)(k - 1));
     at += sum;
   }
 }

@@ -45,8 +45,9 @@ struct Geo {
 template <int MODE>
 using Way = Walk<MODE, Geo>;
 
-constexpr int B_TFULL = 0;                   // [NTF] a tile's blocks and scales loaded
-constexpr int B_LEMPTY = B_TFULL + NTF;      // [RL] read by the context's MMAs
+constexpr int B_TFULL = 0;                   // [NTF] a tile's Rc block and scales loaded
+constexpr int B_LFULL = B_TFULL + NTF;       // [RL] an Lc block loaded
+constexpr int B_LEMPTY = B_LFULL + RL;       // [RL] read by the context's MMAs
 constexpr int B_REMPTY = B_LEMPTY + RL;      // [RR] read by the scores'
 constexpr int B_SFULL = B_REMPTY + RR;       // [NS] S of a tile in TMEM
 constexpr int B_SEMPTY = B_SFULL + NS;       // [NS] read (8 warps)
@@ -152,6 +153,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   auto wait = [&](int bar, uint32_t parity) -> bool {
     return mbar_wait_warp(&bars[bar], parity & 1, abort_flag, WAIT_NS);
   };
+  auto wait_block = [&](int jb) -> bool { return wait(B_LFULL + jb % RL, (uint32_t)(jb / RL)); };
   if (threadIdx.x == 0) {
     for (int i = 0; i < NBAR; ++i) mbar_init(&bars[i], 1);
     for (int i = 0; i < NS; ++i) mbar_init(&bars[B_SEMPTY + i], N_SET);
@@ -179,7 +181,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 
   if (warp == W_TMA) {
     bool ok = true;
-    int asked = 0;  // tiles whose barrier is armed
+    int asked = 0, blocks = 0;  // tiles and Lc blocks whose barriers are armed
     for (; ok && w.more(); w.next(a)) {
       PageWindow pw;
       pw.from = -64;
@@ -204,7 +206,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             // (tile g - 4's scales are read: its context's MMAs, which come behind its weights, have freed
             // this block's slot or one before it)
             facts[tf] = (s0 >= 0 ? 1u : 0u) | (s1 >= 0 ? 2u : 0u);
-            mbar_arrive_expect_tx_warp(tb, pages * (uint32_t)(2 * PAGE * 4 + 4 * PAGE * 128 + PAGE * 64));
+            mbar_arrive_expect_tx_warp(tb, pages * (uint32_t)(2 * PAGE * 4 + PAGE * 64));
             asked = g + 1;
             const uint32_t sd = smem_u32(sm + OFF_SCR) + tf * TILE * 8, rd = rring + rs * RBLK;
             if (s0 >= 0) {
@@ -217,16 +219,20 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             }
           }
           const uint32_t ld = lring + ls * KBLK;
-          if (s0 >= 0) tma_load_2d_warp(ld, &kmap, 128 * blk, (int)s0, tb);
-          if (s1 >= 0) tma_load_2d_warp(ld + PAGE * 128, &kmap, 128 * blk, (int)s1, tb);
+          mbar_arrive_expect_tx_warp(&bars[B_LFULL + ls], pages * (uint32_t)(PAGE * 128));
+          blocks = jb + 1;
+          if (s0 >= 0) tma_load_2d_warp(ld, &kmap, 128 * blk, (int)s0, &bars[B_LFULL + ls]);
+          if (s1 >= 0) tma_load_2d_warp(ld + PAGE * 128, &kmap, 128 * blk, (int)s1, &bars[B_LFULL + ls]);
         }
       }
       gt += w.n;
     }
     if (!ok) {
-      // (a tile requested in part never completes its barrier: that wait ends at its bound)
+      // let what was requested land before the CTA can leave
       if (lane == 0) fail();
       const int zero = 0;
+      for (int i = blocks > RL ? blocks - RL : 0; i < blocks; ++i)
+        (void)mbar_wait(&bars[B_LFULL + i % RL], (i / RL) & 1, &zero, WAIT_NS);
       for (int i = asked > NTF ? asked - NTF : 0; i < asked; ++i)
         (void)mbar_wait(&bars[B_TFULL + i % NTF], (i / NTF) & 1, &zero, WAIT_NS);
     }
@@ -241,19 +247,28 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
       for (int i = 0; i < w.n; ++i) {
         const int g = gt + i, sb = g % NS;
-        if (!wait(B_SEMPTY + sb, (uint32_t)(g / NS) ^ 1u) || !wait(B_TFULL + g % NTF, (uint32_t)(g / NTF))) {
+        if (!wait(B_SEMPTY + sb, (uint32_t)(g / NS) ^ 1u)) {
           ok = false;
           break;
         }
-        tc_fence_after();
         const uint32_t dl = tmem + sb * S_COLS, dr = dl + NB;
 #pragma unroll 1
         for (int blk = 0; blk < 4; ++blk) {
+          if (!wait_block(4 * g + blk)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
           const uint64_t ad = smem_desc(lring + ((4 * g + blk) % RL) * KBLK, 16, 1024, SW128);
           const uint64_t bd = smem_desc(qb + blk * NB * 128, 16, 1024, SW128);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) mma_f8_warp(dl, ad + 2 * kk, bd + 2 * kk, id, (blk | kk) != 0);
         }
+        if (!ok || !wait(B_TFULL + g % NTF, (uint32_t)(g / NTF))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
         const uint64_t ad = smem_desc(rring + (g % RR) * RBLK, 16, 512, SW64);
         const uint64_t bd = smem_desc(qb + 4 * NB * 128, 16, 512, SW64);
 #pragma unroll
@@ -275,20 +290,25 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     for (; ok && w.more(); w.next(a)) {
       for (int i = 0; i < w.n; ++i) {
         const int g = gt + i, st = g & 1;
-        if (!wait(B_PFULL + st, (uint32_t)(g >> 1)) || !wait(B_TFULL + g % NTF, (uint32_t)(g / NTF))) {
+        if (!wait(B_PFULL + st, (uint32_t)(g >> 1))) {
           ok = false;
           break;
         }
-        tc_fence_after();
 #pragma unroll 1
         for (int m = 0; m < 4; ++m) {
           const int ls = (4 * g + m) % RL;
+          if (!wait_block(4 * g + m)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             mma_f8_warp(tmem + T_O + st * O_COLS + m * NB, smem_desc(lring + ls * KBLK + kk * 4096, KBLK, 1024, SW128),
                         smem_desc(pb + st * NB * 128 + kk * 32, 16, 1024, SW128), id, (i > 1 || kk > 0) ? 1u : 0u);
           mma_commit_warp(&bars[B_LEMPTY + ls]);
         }
+        if (!ok) break;
         mma_commit_warp(&bars[B_ODONE + st]);
       }
       gt += w.n;
@@ -408,12 +428,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         ok = false;
         break;
       }
-      float c[NH], mg[NH], mhi[NH], lp[NH];
+      // per thread its token's share of the rows' sums; per lane row hb + lane % 8's reference, and the highest one so far
+      uint64_t c2[NH / 2], lp[NH / 2];
+      float mg = -INFINITY, mhi = -INFINITY;
 #pragma unroll
-      for (int h = 0; h < NH; ++h) {
-        c[h] = cs[sp + hb + h];
-        mg[h] = mhi[h] = -INFINITY;
-        lp[h] = 0.f;
+      for (int h = 0; h < NH / 2; ++h) {
+        c2[h] = pk2(cs[sp + hb + 2 * h], cs[sp + hb + 2 * h + 1]);
+        lp[h] = pk2(0.f, 0.f);
       }
       const int lim0 = lim[sp];  // the first row sees least
       const int from = MODE == kWindow ? window_from(a, lim[sp + N - 1]) : 0;  // the last one's window begins last
@@ -450,7 +471,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         // (sLc made finite: out of sight it may be anything, in sight the NaN or infinity shows in sRc)
         const float sl = fminf(fmaxf(s2.x, 0.f), 3.0e38f), sr = fmaf(0.f, s2.x, s2.y);
         const float lg = fmaxf(lg2_approx(sl), LG_MIN);
-        float u[NH];  // sLc S_L + sRc S_R
+        uint64_t u[NH / 2];  // sLc S_L + sRc S_R, of pairs of rows
+        const uint64_t sl2 = pk2(sl, sl), sr2 = pk2(sr, sr), lg2 = pk2(lg, lg);
         {
           uint32_t r0[NH], r1[NH], r2[NH], r3[NH];
           const uint32_t sa = tmem + lane_addr + sb * S_COLS + hb;
@@ -459,28 +481,37 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           tmem_ld8(sa + 2 * N, r2);
           tmem_ld8(sa + 3 * N, r3);
           tmem_wait_ld();
+          auto two = [](const uint32_t (&r)[NH], int h) {
+            return pk2(__uint_as_float(r[2 * h]), __uint_as_float(r[2 * h + 1]));
+          };
 #pragma unroll
-          for (int h = 0; h < NH; ++h)
-            u[h] = fmaf(sr, __uint_as_float(r2[h]) + __uint_as_float(r3[h]),
-                        sl * (__uint_as_float(r0[h]) + __uint_as_float(r1[h])));
+          for (int h = 0; h < NH / 2; ++h)
+            u[h] = fma2(sr2, add2(two(r2, h), two(r3, h)), mul2(sl2, add2(two(r0, h), two(r1, h))));
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[B_SEMPTY + sb]);
         if (!full) {
           const bool here = (have >> half) & 1u;
-#pragma unroll
-          for (int h = 0; h < NH; ++h) {
+          auto sees = [&](int h) {
             const int l = lim[sp + hb + h];
-            const bool sees = here && t < l && (MODE != kWindow || t >= window_from(a, l) || t < a.n_sink);
-            if (!sees) u[h] = -INFINITY;
+            return here && t < l && (MODE != kWindow || t >= window_from(a, l) || t < a.n_sink);
+          };
+#pragma unroll
+          for (int h = 0; h < NH / 2; ++h) {
+            const float2 v = up2(u[h]);
+            u[h] = pk2(sees(2 * h) ? v.x : -INFINITY, sees(2 * h + 1) ? v.y : -INFINITY);
           }
         }
         // the rows' largest weights in the tile: over the warp's tokens, then the four warps'
         {
           float y[NH];
 #pragma unroll
-          for (int h = 0; h < NH; ++h) y[h] = fmaf(c[h], u[h], lg);
+          for (int h = 0; h < NH / 2; ++h) {
+            const float2 v = up2(fma2(c2[h], u[h], lg2));
+            y[2 * h] = v.x;
+            y[2 * h + 1] = v.y;
+          }
           const float ym = reduce8<true>(y, lane);
           if ((lane & 3) == 0) rmax[(kk & 1) * 64 + wq * N + hb + (lane >> 2)] = ym;
         }
@@ -488,35 +519,42 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           ok = false;
           break;
         }
-        float f[NH];
-        bool moved = false;
+        float f;  // the factor of what row hb + lane % 8 added up before
+        bool moved;
         {
-          const float* rm = rmax + (kk & 1) * 64 + hb;
-#pragma unroll
-          for (int h = 0; h < NH; ++h) {
-            const float ym = fmaxf(fmaxf(rm[h], rm[N + h]), fmaxf(rm[2 * N + h], rm[3 * N + h]));
-            float mn = mg[h];
-            if (ym > mg[h] + TAU) {
-              mn = ym;
-            } else if (ym < mg[h] - DOWN && ym >= mhi[h] - DOWN_CAP) {
-              mn = ym;
-            }
-            f[h] = mn == mg[h] ? 1.f : (mg[h] > -INFINITY ? ex2_approx(mg[h] - mn) : 0.f);
-            moved |= f[h] != 1.f;
-            mg[h] = mn;
-            mhi[h] = fmaxf(mhi[h], mn);
+          const float* rm = rmax + (kk & 1) * 64 + hb + (lane & 7);
+          const float ym = fmaxf(fmaxf(rm[0], rm[N]), fmaxf(rm[2 * N], rm[3 * N]));
+          float mn = mg;
+          if (ym > mg + TAU) {
+            mn = ym;
+          } else if (ym < mg - DOWN && ym >= mhi - DOWN_CAP) {
+            mn = ym;
           }
+          f = mn == mg ? 1.f : (mg > -INFINITY ? ex2_approx(mg - mn) : 0.f);
+          mg = mn;
+          mhi = fmaxf(mhi, mn);
+          moved = __any_sync(0xffffffffu, f != 1.f);
         }
+        if (moved) {
+#pragma unroll
+          for (int h = 0; h < NH / 2; ++h)
+            lp[h] = mul2(lp[h], pk2(__shfl_sync(0xffffffffu, f, 2 * h), __shfl_sync(0xffffffffu, f, 2 * h + 1)));
+        }
+        const float mneg = P_LOG - fmaxf(mg, -3.0e38f);  // (nothing in sight so far: u is -inf, and p 0)
         uint32_t phi[2], plo[2];
 #pragma unroll
         for (int h = 0; h < NH; h += 4) {
           float z[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            // (nothing in sight so far: u is -inf, and p 0)
-            const float p = ex2_approx(fmaf(c[h + j], u[h + j], P_LOG - fmaxf(mg[h + j], -3.0e38f)));
-            lp[h + j] = fmaf(lp[h + j], f[h + j], p);
-            z[j] = p * sl;
+          for (int j = 0; j < 4; j += 2) {
+            const int q = (h + j) / 2;
+            const float2 e = up2(fma2(c2[q], u[q], pk2(__shfl_sync(0xffffffffu, mneg, h + j),
+                                                       __shfl_sync(0xffffffffu, mneg, h + j + 1))));
+            const uint64_t p = pk2(ex2_approx(e.x), ex2_approx(e.y));
+            lp[q] = add2(lp[q], p);
+            const float2 v = up2(mul2(p, sl2));
+            z[j] = v.x;
+            z[j + 1] = v.y;
           }
           const __half2 x01 = __floats2half2_rn(z[0], z[1]), x23 = __floats2half2_rn(z[2], z[3]);
           uint16_t h01, l01, h23, l23;
@@ -533,6 +571,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (moved && i > 1) {
           tc_fence_after();
           __syncwarp();
+          float fh[NH];
+#pragma unroll
+          for (int h = 0; h < NH; ++h) fh[h] = __shfl_sync(0xffffffffu, f, h);
 #pragma unroll 1
           for (int term = 0; term < 2; ++term) {
             uint32_t r[4][8];
@@ -542,7 +583,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
 #pragma unroll
-              for (int j = 0; j < 8; ++j) r[m][j] = __float_as_uint(__uint_as_float(r[m][j]) * f[j]);
+              for (int j = 0; j < 8; ++j) r[m][j] = __float_as_uint(__uint_as_float(r[m][j]) * fh[j]);
               tmem_st8(to + set * O_COLS + m * NB + term * N, r[m]);
             }
           }
@@ -552,6 +593,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           // some row does not see all of this tile: no NaN code may stay in it
 #pragma unroll 1
           for (int m = 0; m < 4; ++m) {
+            if (!wait_block(4 * g + m)) ok = false;
             const uint32_t vb = lring + ((4 * g + m) % RL) * KBLK + (sw & 7) * 2048 + lane * 16;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -593,49 +635,44 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
       if (!ok) break;
       {
-        const float ls = reduce8<false>(lp, lane);
-        if ((lane & 3) == 0) lsum[(set * 4 + wq) * N + hb + (lane >> 2)] = ls;
-        float m = mg[0];
+        float l[NH];
 #pragma unroll
-        for (int h = 1; h < NH; ++h) m = lane == h ? mg[h] : m;
-        if (wq == 0 && lane < NH) refs[set * N + hb + lane] = m;
+        for (int h = 0; h < NH / 2; ++h) {
+          const float2 v = up2(lp[h]);
+          l[2 * h] = v.x;
+          l[2 * h + 1] = v.y;
+        }
+        const float ls = reduce8<false>(l, lane);
+        if ((lane & 3) == 0) lsum[(set * 4 + wq) * N + hb + (lane >> 2)] = ls;
+        if (wq == 0 && lane < NH) refs[set * N + hb + lane] = mg;
       }
       if (!all_sync()) {
         ok = false;
         break;
       }
       tc_fence_after();
-      // both streams on the larger reference
-      auto joined = [&](int r, float& f0, float& f1, float& M) -> float {
-        const float m0 = refs[r], m1 = refs[N + r];
-        M = fmaxf(m0, m1);
-        f0 = m0 == M ? 1.f : ex2_approx(m0 - M);
-        f1 = m1 == M ? 1.f : ex2_approx(m1 - M);
-        const float* p = lsum + r;
-        return ((p[0] + p[N]) + (p[2 * N] + p[3 * N])) * f0 + ((p[4 * N] + p[5 * N]) + (p[6 * N] + p[7 * N])) * f1;
-      };
       const bool final = x.final();
-      const int64_t rows = (int64_t)x.s.nq * a.H, r0 = (int64_t)x.rt * N;
-      float f0[NH], f1[NH];
-#pragma unroll
-      for (int h = 0; h < NH; ++h) {
-        float M;
-        const float L = joined(hb + h, f0[h], f1[h], M);
-        const float inv = final ? (L == 0.f ? 0.f : 1.f / L) : (L == 0.f ? 0.f : 1.f);  // (a NaN stays one)
-        f0[h] *= inv;
-        f1[h] *= inv;
-      }
-      if (sw < N / NH * 4 && (sw & 3) == 0 && lane < NH && r0 + hb + lane < rows) {
-        float g0, g1, M;
-        const float L = joined(hb + lane, g0, g1, M);
-        M -= P_LOG;
-        const int64_t r = r0 + hb + lane;
-        if (final) {
-          if (a.lse != nullptr) a.lse[x.s.q0 * a.H + r] = L == 0.f ? -INFINITY : (M + log2f(L)) * LN2;
-        } else {
-          const int64_t at = ps.row(x, k, hb + lane);
-          ps.m[at] = M;
-          ps.l[at] = L;
+      const int rows = (int)((int64_t)x.s.nq * a.H - (int64_t)x.rt * N);  // (from the row tile's first one on)
+      const int64_t at0 = final ? x.s.q0 * a.H + (int64_t)x.rt * N : ps.row(x, k, 0);
+      // both streams on the larger reference, a row a lane
+      float f0, f1;
+      {
+        const int r = hb + (lane & 7);
+        const float m0 = refs[r], m1 = refs[N + r], M = fmaxf(m0, m1) - P_LOG;
+        f0 = m0 >= m1 ? 1.f : ex2_approx(m0 - m1);
+        f1 = m1 >= m0 ? 1.f : ex2_approx(m1 - m0);
+        const float* p = lsum + r;
+        const float L = ((p[0] + p[N]) + (p[2 * N] + p[3 * N])) * f0 + ((p[4 * N] + p[5 * N]) + (p[6 * N] + p[7 * N])) * f1;
+        const float inv = L == 0.f ? 0.f : (final ? 1.f / L : 1.f);  // (a NaN stays one)
+        f0 *= inv;
+        f1 *= inv;
+        if (set == 0 && wq == 0 && lane < NH && r < rows) {
+          if (!final) {
+            ps.m[at0 + r] = M;
+            ps.l[at0 + r] = L;
+          } else if (a.lse != nullptr) {
+            a.lse[at0 + r] = L == 0.f ? -INFINITY : (M + log2f(L)) * LN2;
+          }
         }
       }
 #pragma unroll 1
@@ -653,18 +690,17 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           tmem_wait_ld();
 #pragma unroll
           for (int h = 0; h < NH; ++h) {
-            const float f = st == 0 ? f0[h] : f1[h];
+            const float f = __shfl_sync(0xffffffffu, st == 0 ? f0 : f1, h);
             // (a factor of 0: nothing seen, or nothing that counts)
             if (f != 0.f) v[h] = fmaf(__uint_as_float(rh[h]) + __uint_as_float(rl[h]), f, v[h]);
           }
         }
+        const int64_t at = (at0 + hb) * DL + m * 128 + row;
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
-          if (r0 + hb + h >= rows) break;
-          if (final)
-            reinterpret_cast<__nv_bfloat16*>(a.out)[(x.s.q0 * a.H + r0 + hb + h) * DL + m * 128 + row] = __float2bfloat16_rn(v[h]);
-          else
-            ps.o[ps.row(x, k, hb + h) * DL + m * 128 + row] = v[h];
+          if (hb + h >= rows) continue;
+          if (final) reinterpret_cast<__nv_bfloat16*>(a.out)[at + h * DL] = __float2bfloat16_rn(v[h]);
+          else ps.o[at + h * DL] = v[h];
         }
       }
       tc_fence_before();
@@ -686,67 +722,61 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 }
 
 // ------------------------------------------------------------------ plan
+constexpr int PLAN_NEAR = 4096;
+
+// (base: in shared memory if it fits)
 template <int MODE>
-__global__ void __launch_bounds__(1024) rows_plan_kernel(const ChunkArgs a, Plan<Geo>* plan, int64_t* base, int64_t* unit,
-                                                         int2* owner, int most) {
+__global__ void __launch_bounds__(1024) rows_plan_kernel(const ChunkArgs a, Plan<Geo>* plan, int64_t* base, int4* owner,
+                                                         int most) {
   grid_dependents_launch();
   __shared__ int64_t tmp[32];
+  __shared__ int64_t near[PLAN_NEAR];
   if (threadIdx.x == 0) *a.err = 0;
   __syncthreads();
-  make_plan<MODE>(a, plan, base, a.B, most, tmp, unit, owner);
+  make_plan<MODE>(a, plan, a.B < PLAN_NEAR ? near : base, a.B, most, tmp, nullptr, owner);
 }
 
 // ------------------------------------------------------------------ join
 // The parts of a row tile's rows, a warp per row (and SPLIT-th of its channels), a block per row tile.
 template <int MODE, int SPLIT>
-__global__ void __launch_bounds__(N * 32) rows_join_kernel(const ChunkArgs a, const Parts ps, const int64_t* unit,
-                                                           const int2* owner) {
+__global__ void __launch_bounds__(N * 32) rows_join_kernel(const ChunkArgs a, const Parts ps, const int4* owner) {
   const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
   const int64_t p = blockIdx.x / SPLIT;
   const int ch = (int)(blockIdx.x % SPLIT) * (DL / SPLIT);
   grid_dependency_wait();  // (every block: what it reads, and that this launch is not over before the kernel is)
-  const int64_t nc = ps.plan->n;
-  if (p >= ps.plan->tiles) return;
-  const int64_t S = unit[p], E = unit[p + 1];
-  __shared__ int64_t xs[Geo::RANGES + 1];
-  for (int i = threadIdx.x; i <= nc; i += N * 32) xs[i] = i < nc ? ps.plan->e[i].x : ps.plan->units;
-  __syncthreads();
-  // the ranges that it lies in: from the last that begins at S or before
-  const int k0 = __syncthreads_count(threadIdx.x < nc && xs[threadIdx.x < nc ? threadIdx.x : 0] <= S) - 1;
-  const int k1 = __syncthreads_count(threadIdx.x < nc && xs[threadIdx.x < nc ? threadIdx.x : 0] < E) - 1;
-  if (k0 == k1) return;  // whole
-  const int2 of = owner[p];
+  const int64_t tiles = ps.plan->tiles;
+  const int4 of = owner[p];  // (there is room for as many as there are blocks)
+  if (p >= tiles) return;
+  const int k0 = of.z >> 1, n = of.w - k0 + 1;
+  if (n == 1) return;  // whole
+  auto slot = [&](int j) -> int64_t { return (int64_t)(j == 0 ? of.z : 2 * (k0 + j)) * N + row; };
   const SeqInfo<MODE> s = seq_info<MODE>(a, of.x, false);
   const int64_t r = (int64_t)of.y * N + row;
   if (r >= (int64_t)s.nq * a.H) return;
-  auto slot = [&](int j) -> int64_t { return (int64_t)(2 * j + (j == k0 && xs[k0] < S ? 1 : 0)) * N + row; };
-  auto there = [&](int j) { return j <= k1 && xs[j] != xs[j + 1]; };  // (a range without units has no part)
   float M = -INFINITY, L = 0.f;
-  for (int j = k0 + lane; j <= k1; j += 32)
-    if (there(j)) M = fmaxf(M, ps.m[slot(j)]);
+  for (int j = lane; j < n; j += 32) M = fmaxf(M, ps.m[slot(j)]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   constexpr int Q = 4 / SPLIT;  // 16-byte units a lane
   float4 acc[Q];
 #pragma unroll
   for (int c = 0; c < Q; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int j0 = k0; j0 <= k1; j0 += 32) {
+  for (int j0 = 0; j0 < n; j0 += 32) {
     const int j = j0 + lane;
     float wt = 0.f;
-    if (there(j)) {
+    if (j < n) {
       const float m = ps.m[slot(j)];
       wt = m > -INFINITY ? ex2_approx(m - M) : 1.f;  // (a NaN l stays one)
       L += wt * ps.l[slot(j)];
     }
-    const uint32_t has = __ballot_sync(0xffffffffu, there(j));
-    const int n = min(k1 - j0 + 1, 32);
+    const int some = min(n - j0, 32);
 #pragma unroll(SPLIT == 1 ? 4 : 8)
-    for (int i = 0; i < n; ++i) {
+    for (int i = 0; i < some; ++i) {
       const float w = __shfl_sync(0xffffffffu, wt, i);
       const float4* o = reinterpret_cast<const float4*>(ps.o + slot(j0 + i) * DL + ch) + lane;
 #pragma unroll
       for (int c = 0; c < Q; ++c) {
-        const float4 v = ((has >> i) & 1u) ? o[32 * c] : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4 v = o[32 * c];
         acc[c].x += w * v.x;
         acc[c].y += w * v.y;
         acc[c].z += w * v.z;
@@ -771,12 +801,12 @@ __global__ void __launch_bounds__(N * 32) rows_join_kernel(const ChunkArgs a, co
 // ------------------------------------------------------------------ host
 constexpr int64_t OFF_PLAN = 256, OFF_BASE = 4096;
 static_assert(OFF_PLAN + sizeof(Plan<Geo>) <= OFF_BASE, "plan area");
-constexpr int FEW_ROW_TILES = 64;
+constexpr int FEW_ROW_TILES = 512;
 
 struct Layout {
   int most;       // ranges
   int64_t tiles;  // row tiles at most
-  int64_t unit, owner, m, rows, bytes;
+  int64_t owner, m, rows, bytes;
 };
 Layout layout_of(int B, int H, int64_t total_q, int64_t keys) {
   auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
@@ -785,10 +815,8 @@ Layout layout_of(int B, int H, int64_t total_q, int64_t keys) {
   const int64_t units = w.tiles * keys;
   w.most = (int)(units < 1 ? 1 : (units < NUM_SMS ? units : NUM_SMS));
   int64_t at = OFF_BASE + up((int64_t)(B + 1) * 8);
-  w.unit = at;
-  at += up((w.tiles + 1) * 8);
   w.owner = at;
-  at += up(w.tiles * 8);
+  at += up(w.tiles * (int64_t)sizeof(int4));
   w.m = at;
   w.rows = w.most > 1 ? 2 * (int64_t)w.most * N : 0;
   w.bytes = at + w.rows * (8 + DL * 4);
@@ -816,8 +844,7 @@ cudaError_t launch(ChunkArgs a, const Layout& w, void* workspace, cudaStream_t s
   ps.l = ps.m + w.rows;
   ps.o = ps.l + w.rows;
   ps.whole = 0;
-  int64_t* unit = reinterpret_cast<int64_t*>(p + w.unit);
-  int2* owner = reinterpret_cast<int2*>(p + w.owner);
+  int4* owner = reinterpret_cast<int4*>(p + w.owner);
   DecodeArgs d{};  // what the cache's tensor maps are made from
   d.codes = a.codes;
   d.scales = a.scales;
@@ -827,15 +854,13 @@ cudaError_t launch(ChunkArgs a, const Layout& w, void* workspace, cudaStream_t s
   if ((e = make_cache_map(d, &kmap)) != cudaSuccess || (e = make_rc_map(d, &rmap)) != cudaSuccess ||
       (e = make_scale_map(d, &smap)) != cudaSuccess)
     return e;
-  rows_plan_kernel<MODE><<<1, 1024, 0, s>>>(a, ps.plan, reinterpret_cast<int64_t*>(p + OFF_BASE), unit, owner, w.most);
+  rows_plan_kernel<MODE><<<1, 1024, 0, s>>>(a, ps.plan, reinterpret_cast<int64_t*>(p + OFF_BASE), owner, w.most);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   e = launch_after_prep(rows_kernel<MODE>, w.most, NTHREADS, SMEM, s, a, ps, kmap, rmap, smap);
   if (e != cudaSuccess || w.most == 1) return e;
   if (w.tiles < FEW_ROW_TILES)
-    return launch_after_prep(rows_join_kernel<MODE, 4>, (unsigned)(4 * w.tiles), N * 32, 0, s, a, ps,
-                             (const int64_t*)unit, (const int2*)owner);
-  return launch_after_prep(rows_join_kernel<MODE, 1>, (unsigned)w.tiles, N * 32, 0, s, a, ps, (const int64_t*)unit,
-                           (const int2*)owner);
+    return launch_after_prep(rows_join_kernel<MODE, 4>, (unsigned)(4 * w.tiles), N * 32, 0, s, a, ps, (const int4*)owner);
+  return launch_after_prep(rows_join_kernel<MODE, 1>, (unsigned)w.tiles, N * 32, 0, s, a, ps, (const int4*)owner);
 }
 
 }  // namespace
