@@ -1353,7 +1353,7 @@ Layout layout_of(int B, int H, int64_t total_q, int max_blocks, int G, int64_t w
 }
 
 // Whether a call's sequences have so few rows on average that the kernel for them is faster.
-constexpr int FEW_ROWS = 32;
+constexpr int FEW_ROWS = 128;
 bool few_rows(int B, int H, int64_t total_q) { return total_q * H <= (int64_t)FEW_ROWS * B; }
 
 template <int MODE>

@@ -1,7 +1,7 @@
 // rows.cu -- absorbed MLA attention over the paged fp8 latent cache for sequences of few rows (single
 // tokens of a few heads): the same mathematics and precision as chunk.cu,
 //   z_t = sm * ( sLc_t <q_lat, dec(Lc_t)> + sRc_t <q_rope, dec(Rc_t)> ),   out = sum_t softmax(z)_t sLc_t dec(Lc_t)
-// with the keys as the MMAs' M and a row tile of 16 (token, head) pairs as their N, on one CTA per SM.
+// with the keys as the MMAs' M and a row tile of N = 16 or 32 (token, head) pairs as theirs, on one CTA per SM.
 //
 // A range of (row tile, key tile) units is one CTA's.  Per key tile of 128 tokens, whose bytes are loaded
 // once by TMA and read by both contractions as they are (kind::f8f6f4):
@@ -24,60 +24,67 @@
 namespace kv8 {
 namespace {
 
-constexpr int N = 16;                        // rows of a row tile
-constexpr int NB = 2 * N;                    // columns: hi terms, lo terms
 constexpr int NH = 8;                        // rows of a softmax warp
 constexpr int KBLK = TILE * 128;             // 16 KB: [128 tokens x 128 bytes]
 constexpr int RBLK = TILE * 64;              // 8 KB: [128 tokens x 64 bytes]
-constexpr int RL = 11, RR = 2;               // rings of Lc blocks and Rc blocks
 constexpr int NTF = 4;                       // tiles loaded: barriers, row scales
-constexpr int NS = 4;                        // S buffers
-static_assert(RL <= 12, "a block of tile i has the slot of tile i - 3 at the oldest: NTF tiles are told apart");
 constexpr int W_TMA = 0, W_MMA = 1, W_CTX = 2, W_SOFT = 3;
-constexpr int N_SOFT = 16, N_SET = 8;        // softmax warps, of a stream
+constexpr int N_SOFT = 16;                   // softmax warps: four, one per TMEM lane quarter, for 8 rows of a stream
 constexpr int NTHREADS = (W_SOFT + N_SOFT) * 32;
 constexpr float TAU = 1.0f, P_LOG = 7.0f, DOWN = 10.0f, LG_MIN = -40.0f, DOWN_CAP = 50.0f;  // (as in chunk.cu)
 constexpr uint64_t WAIT_NS = 2000000000ull;
 
+template <int N>
 struct Geo {
   static constexpr int ROWS = N, RANGES = NUM_SMS, SWITCH = 2, MIN_TILES = 1;
 };
-template <int MODE>
-using Way = Walk<MODE, Geo>;
+template <int MODE, int N>
+using Way = Walk<MODE, Geo<N>>;
 
-constexpr int B_TFULL = 0;                   // [NTF] a tile's Rc block and scales loaded
-constexpr int B_LFULL = B_TFULL + NTF;       // [RL] an Lc block loaded
-constexpr int B_LEMPTY = B_LFULL + RL;       // [RL] read by the context's MMAs
-constexpr int B_REMPTY = B_LEMPTY + RL;      // [RR] read by the scores'
-constexpr int B_SFULL = B_REMPTY + RR;       // [NS] S of a tile in TMEM
-constexpr int B_SEMPTY = B_SFULL + NS;       // [NS] read (8 warps)
-constexpr int B_PFULL = B_SEMPTY + NS;       // [2 streams] weights written, O rescaled (8)
-constexpr int B_ODONE = B_PFULL + 2;         // [2] a tile's context MMAs done
-constexpr int B_G = B_ODONE + 2;             // [2][2] the four warps of a stream and half meet
-constexpr int B_QREADY = B_G + 4;            // a row tile's query in place (16)
-constexpr int B_EP = B_QREADY + 1;           // the softmax warps meet (16)
-constexpr int B_DRAIN = B_EP + 1;            // [2] the issuers' last MMAs
-constexpr int NBAR = B_DRAIN + 2;
-
-constexpr int OFF_FLAGS = 512;               // tmem base, abort flag
-constexpr int OFF_FACTS = 528;               // [NTF] pages present
-constexpr int OFF_CS = 640;                  // [2 segments][16] the rows' c
-constexpr int OFF_LIM = OFF_CS + 128;        // [2][16] the keys that they see
-constexpr int OFF_REF = OFF_LIM + 128;       // [2 streams][16] references at a row tile's end
-constexpr int OFF_LS = 1024;                 // [2][4 warps][16] sums
-constexpr int OFF_RMAX = OFF_LS + 512;       // [2][2 buffers][4][16] a tile's largest weights
-constexpr int OFF_WALK = OFF_RMAX + 1024;    // [16 warps] segments
-constexpr int OFF_SCR = 4096;                // [NTF][128][2] row scales
-constexpr int OFF_Q = OFF_SCR + NTF * TILE * 8;      // [4 blocks][NB x 128 B], [NB x 64 B]
-constexpr int OFF_P = OFF_Q + 4 * NB * 128 + NB * 64;  // [2 streams][NB x 128 tokens]
-constexpr int OFF_L = OFF_P + 2 * NB * 128;
-constexpr int OFF_R = OFF_L + RL * KBLK;
-constexpr int SMEM = OFF_R + RR * RBLK;
-constexpr int S_COLS = 2 * NB, T_O = NS * S_COLS, O_COLS = 4 * NB;
-static_assert(NBAR * 8 <= OFF_FLAGS && OFF_REF + 128 <= OFF_LS && OFF_WALK + N_SOFT * 64 <= OFF_SCR, "layout");
-static_assert(sizeof(Way<kShared>) <= 64 && sizeof(Way<kWindow>) <= 64, "segments");
-static_assert(OFF_Q % 1024 == 0 && OFF_P % 1024 == 0 && OFF_L % 1024 == 0 && OFF_R % 1024 == 0, "swizzle atoms");
-static_assert(SMEM <= 232448 && T_O + 2 * O_COLS <= 512, "shared memory and TMEM");
+// Per row tile size N: rings, barriers, shared memory and TMEM columns.
+template <int N>
+struct Cfg {
+  static constexpr int NB = 2 * N;                     // columns: hi terms, lo terms
+  static constexpr int STREAMS = N_SOFT / 4 / (N / NH);
+  static constexpr int SET = N_SOFT / STREAMS;         // a stream's softmax warps
+  static constexpr int RL = N == 16 ? 11 : 9, RR = 2;  // rings of Lc blocks and Rc blocks
+  static constexpr int NS = 2 * STREAMS;               // S buffers
+  static_assert(RL <= 12, "a block of tile i has the slot of tile i - 3 at the oldest: NTF tiles are told apart");
+  static constexpr int B_TFULL = 0;                    // [NTF] a tile's Rc block and scales loaded
+  static constexpr int B_LFULL = B_TFULL + NTF;        // [RL] an Lc block loaded
+  static constexpr int B_LEMPTY = B_LFULL + RL;        // [RL] read by the context's MMAs
+  static constexpr int B_REMPTY = B_LEMPTY + RL;       // [RR] read by the scores'
+  static constexpr int B_SFULL = B_REMPTY + RR;        // [NS] S of a tile in TMEM
+  static constexpr int B_SEMPTY = B_SFULL + NS;        // [NS] read (a stream's warps)
+  static constexpr int B_PFULL = B_SEMPTY + NS;        // [2] of even and odd tiles: weights written, O rescaled (a stream's warps)
+  static constexpr int B_ODONE = B_PFULL + 2;          // [2] context MMAs done
+  static constexpr int B_G = B_ODONE + 2;              // [4] the four warps of a stream's 8 rows meet
+  static constexpr int B_QREADY = B_G + 4;             // a row tile's query in place (all softmax warps)
+  static constexpr int B_EP = B_QREADY + 1;            // the softmax warps meet
+  static constexpr int B_DRAIN = B_EP + 1;             // [2] the issuers' last MMAs
+  static constexpr int NBAR = B_DRAIN + 2;
+  static constexpr int OFF_FLAGS = 512;                // tmem base, abort flag
+  static constexpr int OFF_FACTS = 528;                // [NTF] pages present
+  static constexpr int OFF_CS = 640;                   // [2 segments][N] the rows' c
+  static constexpr int OFF_LIM = OFF_CS + 8 * N;       // [2][N] the keys that they see
+  static constexpr int OFF_REF = OFF_LIM + 8 * N;      // [STREAMS][N] references at a row tile's end
+  static constexpr int OFF_LS = OFF_REF + 128;         // [STREAMS][4 warps][N] sums
+  static constexpr int OFF_RMAX = OFF_LS + 512;        // [STREAMS][2 buffers][4][N] a tile's largest weights
+  static constexpr int OFF_WALK = OFF_RMAX + 1024;     // [16 warps] segments
+  static constexpr int OFF_SCR = 4096;                 // [NTF][128][2] row scales
+  static constexpr int OFF_Q = OFF_SCR + NTF * TILE * 8;        // [4 blocks][NB x 128 B], [NB x 64 B]
+  static constexpr int OFF_P = OFF_Q + 4 * NB * 128 + NB * 64;  // [2: even and odd tiles][NB x 128 tokens]
+  static constexpr int OFF_L = OFF_P + 2 * NB * 128;
+  static constexpr int OFF_R = OFF_L + RL * KBLK;
+  static constexpr int SMEM = OFF_R + RR * RBLK;
+  static constexpr int S_COLS = 2 * NB, T_O = NS * S_COLS, O_COLS = 4 * NB;
+  static_assert(N == 16 || N == 32, "two streams, or one");
+  static_assert(STREAMS * N * 4 <= 128 && STREAMS * 4 * N * 4 <= 512 && OFF_WALK % 16 == 0, "scratch");
+  static_assert(NBAR * 8 <= OFF_FLAGS && OFF_WALK + N_SOFT * 64 <= OFF_SCR, "layout");
+  static_assert(OFF_Q % 1024 == 0 && OFF_P % 1024 == 0 && OFF_L % 1024 == 0 && OFF_R % 1024 == 0, "swizzle atoms");
+  static_assert(SMEM <= 232448 && T_O + STREAMS * O_COLS <= 512, "shared memory and TMEM");
+};
+static_assert(sizeof(Way<kShared, 16>) <= 64 && sizeof(Way<kWindow, 16>) <= 64, "segments");
 
 // The reduction over the 32 lanes of each of 8 values: lane l is left with that of value l / 4.
 template <bool MAX>
@@ -119,14 +126,15 @@ __device__ __forceinline__ void sts8(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
+template <int N>
 struct Parts {
-  Plan<Geo>* plan;
-  float* m;       // [2 RANGES][16]: slot 2k the first segment of range k, 2k + 1 its last; behind them (shared
+  Plan<Geo<N>>* plan;
+  float* m;       // [2 RANGES][N]: slot 2k the first segment of range k, 2k + 1 its last; behind them (shared
   float* l;       // prefixes, from `whole` on) the row tiles that one range held whole
   float* o;       // [..][512]
   int64_t whole;
   template <int MODE>
-  __device__ __forceinline__ int64_t row(const Way<MODE>& w, int k, int r) const {
+  __device__ __forceinline__ int64_t row(const Way<MODE, N>& w, int k, int r) const {
     if constexpr (MODE == kShared) {
       if (w.whole()) return whole + w.s.part + (int64_t)w.rt * N + r;
     }
@@ -134,18 +142,21 @@ struct Parts {
   }
 };
 
-template <int MODE>
+template <int MODE, int N>
 __global__ void __launch_bounds__(NTHREADS, 1)
-    rows_kernel(const ChunkArgs a, const Parts ps, const __grid_constant__ CUtensorMap kmap,
+    rows_kernel(const ChunkArgs a, const Parts<N> ps, const __grid_constant__ CUtensorMap kmap,
                 const __grid_constant__ CUtensorMap rmap, const __grid_constant__ CUtensorMap smap) {
+  using C = Cfg<N>;
+  constexpr int NB = C::NB, STREAMS = C::STREAMS, RL = C::RL, RR = C::RR, NS = C::NS, S_COLS = C::S_COLS, T_O = C::T_O,
+                O_COLS = C::O_COLS;
   extern __shared__ __align__(1024) uint8_t sm[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int k = (int)blockIdx.x;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + OFF_FLAGS);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + OFF_FLAGS + 4);
-  volatile uint32_t* facts = reinterpret_cast<volatile uint32_t*>(sm + OFF_FACTS);
-  const uint32_t qb = smem_u32(sm + OFF_Q), lring = smem_u32(sm + OFF_L), rring = smem_u32(sm + OFF_R);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::OFF_FLAGS);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + C::OFF_FLAGS + 4);
+  volatile uint32_t* facts = reinterpret_cast<volatile uint32_t*>(sm + C::OFF_FACTS);
+  const uint32_t qb = smem_u32(sm + C::OFF_Q), lring = smem_u32(sm + C::OFF_L), rring = smem_u32(sm + C::OFF_R);
   auto fail = [&]() {
     *abort_flag = 1;
     atomicOr(a.err, ERR_TIMEOUT);
@@ -153,14 +164,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   auto wait = [&](int bar, uint32_t parity) -> bool {
     return mbar_wait_warp(&bars[bar], parity & 1, abort_flag, WAIT_NS);
   };
-  auto wait_block = [&](int jb) -> bool { return wait(B_LFULL + jb % RL, (uint32_t)(jb / RL)); };
+  auto wait_block = [&](int jb) -> bool { return wait(C::B_LFULL + jb % RL, (uint32_t)(jb / RL)); };
   if (threadIdx.x == 0) {
-    for (int i = 0; i < NBAR; ++i) mbar_init(&bars[i], 1);
-    for (int i = 0; i < NS; ++i) mbar_init(&bars[B_SEMPTY + i], N_SET);
-    for (int i = 0; i < 2; ++i) mbar_init(&bars[B_PFULL + i], N_SET);
-    for (int i = 0; i < 4; ++i) mbar_init(&bars[B_G + i], 4);
-    mbar_init(&bars[B_QREADY], N_SOFT);
-    mbar_init(&bars[B_EP], N_SOFT);
+    for (int i = 0; i < C::NBAR; ++i) mbar_init(&bars[i], 1);
+    for (int i = 0; i < NS; ++i) mbar_init(&bars[C::B_SEMPTY + i], C::SET);
+    for (int i = 0; i < 2; ++i) mbar_init(&bars[C::B_PFULL + i], C::SET);
+    for (int i = 0; i < 4; ++i) mbar_init(&bars[C::B_G + i], 4);
+    mbar_init(&bars[C::B_QREADY], N_SOFT);
+    mbar_init(&bars[C::B_EP], N_SOFT);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -174,7 +185,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   const uint32_t tmem = *tmem_slot;
   grid_dependency_wait();    // the plan
   grid_dependents_launch();
-  Way<MODE> w;
+  Way<MODE, N> w;
   if (k < ps.plan->n) w.start(a, *ps.plan, k);
   else w.left = 0;
   int gt = 0;  // key tiles of the range before this segment
@@ -190,15 +201,15 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const int64_t page = 2 * (int64_t)(w.t + i);
         const int64_t s0 = pw.slot(a, w, page, lane, true), s1 = pw.slot(a, w, page + 1, lane, true);
         const uint32_t pages = (s0 >= 0 ? 1u : 0u) + (s1 >= 0 ? 1u : 0u);
-        uint64_t* tb = &bars[B_TFULL + tf];
-        if (!wait(B_REMPTY + rs, (uint32_t)(g / RR) ^ 1u)) {
+        uint64_t* tb = &bars[C::B_TFULL + tf];
+        if (!wait(C::B_REMPTY + rs, (uint32_t)(g / RR) ^ 1u)) {
           ok = false;
           break;
         }
 #pragma unroll 1
         for (int blk = 0; blk < 4; ++blk) {
           const int jb = 4 * g + blk, ls = jb % RL;
-          if (!wait(B_LEMPTY + ls, (uint32_t)(jb / RL) ^ 1u)) {
+          if (!wait(C::B_LEMPTY + ls, (uint32_t)(jb / RL) ^ 1u)) {
             ok = false;
             break;
           }
@@ -208,7 +219,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             facts[tf] = (s0 >= 0 ? 1u : 0u) | (s1 >= 0 ? 2u : 0u);
             mbar_arrive_expect_tx_warp(tb, pages * (uint32_t)(2 * PAGE * 4 + PAGE * 64));
             asked = g + 1;
-            const uint32_t sd = smem_u32(sm + OFF_SCR) + tf * TILE * 8, rd = rring + rs * RBLK;
+            const uint32_t sd = smem_u32(sm + C::OFF_SCR) + tf * TILE * 8, rd = rring + rs * RBLK;
             if (s0 >= 0) {
               tma_load_1d_warp(sd, &smap, (int)(2 * s0), tb);
               tma_load_2d_warp(rd, &rmap, DL, (int)s0, tb);
@@ -219,10 +230,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             }
           }
           const uint32_t ld = lring + ls * KBLK;
-          mbar_arrive_expect_tx_warp(&bars[B_LFULL + ls], pages * (uint32_t)(PAGE * 128));
+          mbar_arrive_expect_tx_warp(&bars[C::B_LFULL + ls], pages * (uint32_t)(PAGE * 128));
           blocks = jb + 1;
-          if (s0 >= 0) tma_load_2d_warp(ld, &kmap, 128 * blk, (int)s0, &bars[B_LFULL + ls]);
-          if (s1 >= 0) tma_load_2d_warp(ld + PAGE * 128, &kmap, 128 * blk, (int)s1, &bars[B_LFULL + ls]);
+          if (s0 >= 0) tma_load_2d_warp(ld, &kmap, 128 * blk, (int)s0, &bars[C::B_LFULL + ls]);
+          if (s1 >= 0) tma_load_2d_warp(ld + PAGE * 128, &kmap, 128 * blk, (int)s1, &bars[C::B_LFULL + ls]);
         }
       }
       gt += w.n;
@@ -232,22 +243,22 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (lane == 0) fail();
       const int zero = 0;
       for (int i = blocks > RL ? blocks - RL : 0; i < blocks; ++i)
-        (void)mbar_wait(&bars[B_LFULL + i % RL], (i / RL) & 1, &zero, WAIT_NS);
+        (void)mbar_wait(&bars[C::B_LFULL + i % RL], (i / RL) & 1, &zero, WAIT_NS);
       for (int i = asked > NTF ? asked - NTF : 0; i < asked; ++i)
-        (void)mbar_wait(&bars[B_TFULL + i % NTF], (i / NTF) & 1, &zero, WAIT_NS);
+        (void)mbar_wait(&bars[C::B_TFULL + i % NTF], (i / NTF) & 1, &zero, WAIT_NS);
     }
     __syncwarp();
   } else if (warp == W_MMA) {
     const uint32_t id = idesc_f16(128, NB, false, false);  // e4m3 x e4m3 (format 0)
     bool ok = true;
     for (; ok && w.more(); w.next(a)) {
-      if (!wait(B_QREADY, (uint32_t)w.seg)) {
+      if (!wait(C::B_QREADY, (uint32_t)w.seg)) {
         ok = false;
         break;
       }
       for (int i = 0; i < w.n; ++i) {
         const int g = gt + i, sb = g % NS;
-        if (!wait(B_SEMPTY + sb, (uint32_t)(g / NS) ^ 1u)) {
+        if (!wait(C::B_SEMPTY + sb, (uint32_t)(g / NS) ^ 1u)) {
           ok = false;
           break;
         }
@@ -264,7 +275,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) mma_f8_warp(dl, ad + 2 * kk, bd + 2 * kk, id, (blk | kk) != 0);
         }
-        if (!ok || !wait(B_TFULL + g % NTF, (uint32_t)(g / NTF))) {
+        if (!ok || !wait(C::B_TFULL + g % NTF, (uint32_t)(g / NTF))) {
           ok = false;
           break;
         }
@@ -273,24 +284,24 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const uint64_t bd = smem_desc(qb + 4 * NB * 128, 16, 512, SW64);
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) mma_f8_warp(dr, ad + 2 * kk, bd + 2 * kk, id, kk != 0);
-        mma_commit_warp(&bars[B_REMPTY + g % RR]);
-        mma_commit_warp(&bars[B_SFULL + sb]);
+        mma_commit_warp(&bars[C::B_REMPTY + g % RR]);
+        mma_commit_warp(&bars[C::B_SFULL + sb]);
       }
       gt += w.n;
     }
     if (!ok && lane == 0) fail();
     const int zero = 0;
-    mma_commit_warp(&bars[B_DRAIN]);
-    (void)mbar_wait(&bars[B_DRAIN], 0, &zero, WAIT_NS);
+    mma_commit_warp(&bars[C::B_DRAIN]);
+    (void)mbar_wait(&bars[C::B_DRAIN], 0, &zero, WAIT_NS);
     __syncwarp();
   } else if (warp == W_CTX) {
     const uint32_t id = idesc_f16(128, NB, true, false);  // A = V, MN-major
-    const uint32_t pb = smem_u32(sm + OFF_P);
+    const uint32_t pb = smem_u32(sm + C::OFF_P);
     bool ok = true;
     for (; ok && w.more(); w.next(a)) {
       for (int i = 0; i < w.n; ++i) {
-        const int g = gt + i, st = g & 1;
-        if (!wait(B_PFULL + st, (uint32_t)(g >> 1))) {
+        const int g = gt + i, st = g % STREAMS, pbuf = g & 1;
+        if (!wait(C::B_PFULL + pbuf, (uint32_t)(g >> 1))) {
           ok = false;
           break;
         }
@@ -305,58 +316,58 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             mma_f8_warp(tmem + T_O + st * O_COLS + m * NB, smem_desc(lring + ls * KBLK + kk * 4096, KBLK, 1024, SW128),
-                        smem_desc(pb + st * NB * 128 + kk * 32, 16, 1024, SW128), id, (i > 1 || kk > 0) ? 1u : 0u);
-          mma_commit_warp(&bars[B_LEMPTY + ls]);
+                        smem_desc(pb + pbuf * NB * 128 + kk * 32, 16, 1024, SW128), id, (i >= STREAMS || kk > 0) ? 1u : 0u);
+          mma_commit_warp(&bars[C::B_LEMPTY + ls]);
         }
         if (!ok) break;
-        mma_commit_warp(&bars[B_ODONE + st]);
+        mma_commit_warp(&bars[C::B_ODONE + pbuf]);
       }
       gt += w.n;
     }
     if (!ok && lane == 0) fail();
     const int zero = 0;
-    mma_commit_warp(&bars[B_DRAIN + 1]);
-    (void)mbar_wait(&bars[B_DRAIN + 1], 0, &zero, WAIT_NS);
+    mma_commit_warp(&bars[C::B_DRAIN + 1]);
+    (void)mbar_wait(&bars[C::B_DRAIN + 1], 0, &zero, WAIT_NS);
     __syncwarp();
   } else {
     // ---------------------------------------------------------- query, softmax, results
     const int sw = warp - W_SOFT;
-    const int set = sw >> 3, grp = (sw >> 2) & 1, wq = sw & 3;
+    const int set = (sw >> 2) / (N / NH), grp = (sw >> 2) % (N / NH), wq = sw & 3;
     const int hb = grp * NH;                     // rows hb .. hb + 7
     const int row = (warp & 3) * 32 + lane;      // token of the tile (TMEM lane); channel of a block of O
     const int half = row >> 6;                   // its page
     const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
-    float* cs = reinterpret_cast<float*>(sm + OFF_CS);
-    int* lim = reinterpret_cast<int*>(sm + OFF_LIM);
-    float* refs = reinterpret_cast<float*>(sm + OFF_REF);
-    float* lsum = reinterpret_cast<float*>(sm + OFF_LS);
-    float* rmax = reinterpret_cast<float*>(sm + OFF_RMAX) + set * 128;
-    Way<MODE>* walk = reinterpret_cast<Way<MODE>*>(sm + OFF_WALK + sw * 64);
+    float* cs = reinterpret_cast<float*>(sm + C::OFF_CS);
+    int* lim = reinterpret_cast<int*>(sm + C::OFF_LIM);
+    float* refs = reinterpret_cast<float*>(sm + C::OFF_REF);
+    float* lsum = reinterpret_cast<float*>(sm + C::OFF_LS);
+    float* rmax = reinterpret_cast<float*>(sm + C::OFF_RMAX) + set * 8 * N;
+    Way<MODE, N>* walk = reinterpret_cast<Way<MODE, N>*>(sm + C::OFF_WALK + sw * 64);
     uint32_t gph = 0, eph = 0;
     auto group_sync = [&]() -> bool {
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[B_G + set * 2 + grp]);
-      return wait(B_G + set * 2 + grp, gph++);
+      if (lane == 0) mbar_arrive(&bars[C::B_G + (sw >> 2)]);
+      return wait(C::B_G + (sw >> 2), gph++);
     };
     auto all_sync = [&]() -> bool {
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[B_EP]);
-      return wait(B_EP, eph++);
+      if (lane == 0) mbar_arrive(&bars[C::B_EP]);
+      return wait(C::B_EP, eph++);
     };
-    // Row `sw` of a row tile's query, by this warp: two e4m3 terms on the scale that puts its largest value
+    // Rows sw, sw + 16 of a row tile's query, by this warp: two e4m3 terms on the scale that puts its largest value
     // in [128, 256), and c, which folds the scale back in, with sm_scale log2 e.  (Rows past the last one
     // are copies of it.)
-    auto source = [&](const Way<MODE>& x, const uint16_t*& ql, const uint16_t*& qr) -> int {
-      const int64_t r = (int64_t)x.rt * N + sw, rows = (int64_t)x.s.nq * a.H;
+    auto source = [&](const Way<MODE, N>& x, int hr, const uint16_t*& ql, const uint16_t*& qr) -> int {
+      const int64_t r = (int64_t)x.rt * N + hr, rows = (int64_t)x.s.nq * a.H;
       const uint32_t at = (uint32_t)(r < rows ? r : rows - 1);
       const int tok = (int)(at / (uint32_t)a.H), head = (int)(at % (uint32_t)a.H);
       ql = a.q_lat + (x.s.q0 + tok) * a.ql_t + (int64_t)head * a.ql_h;
       qr = a.q_rope + (x.s.q0 + tok) * a.qr_t + (int64_t)head * a.qr_h;
       return tok;
     };
-    auto load_query = [&](const Way<MODE>& x) {
+    auto load_row = [&](const Way<MODE, N>& x, int hr) {
       const uint16_t *ql, *qr;
-      const int tok = source(x, ql, qr);
+      const int tok = source(x, hr, ql, qr);
       uint4 v[3];
       v[0] = __ldg(reinterpret_cast<const uint4*>(ql) + lane);
       v[1] = __ldg(reinterpret_cast<const uint4*>(ql) + 32 + lane);
@@ -376,7 +387,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (mx == 0 || nan != 0u) e = 7;
       const float sc = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
       if (lane == 0) {
-        const int at = ((x.seg & 1) * N) + sw;
+        const int at = ((x.seg & 1) * N) + hr;
         cs[at] = fmaxf(a.sm_scale * LOG2E * __uint_as_float((uint32_t)(127 - 7 + e) << 23), 1e-37f);
         lim[at] = limit_of(a, x.s, tok);
       }
@@ -396,24 +407,27 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         terms(v[j].z, v[j].w, hi.y, lo.y);
         if (j < 2) {  // channels 256 j + 8 lane .. + 7: block 2 j + lane / 16, half of its unit lane % 16 / 2
           const uint32_t blk = qb + (2 * j + (lane >> 4)) * NB * 128;
-          sts64(blk + sw128(sw, (lane & 15) >> 1) + (lane & 1) * 8, hi);
-          sts64(blk + sw128(N + sw, (lane & 15) >> 1) + (lane & 1) * 8, lo);
+          sts64(blk + sw128(hr, (lane & 15) >> 1) + (lane & 1) * 8, hi);
+          sts64(blk + sw128(N + hr, (lane & 15) >> 1) + (lane & 1) * 8, lo);
         } else if (lane < 8) {
           const uint32_t blk = qb + 4 * NB * 128;
-          sts64(blk + sw64(sw, lane >> 1) + (lane & 1) * 8, hi);
-          sts64(blk + sw64(N + sw, lane >> 1) + (lane & 1) * 8, lo);
+          sts64(blk + sw64(hr, lane >> 1) + (lane & 1) * 8, hi);
+          sts64(blk + sw64(N + hr, lane >> 1) + (lane & 1) * 8, lo);
         }
       }
+    };
+    auto load_query = [&](const Way<MODE, N>& x) {
+#pragma unroll 1
+      for (int hr = sw; hr < N; hr += N_SOFT) load_row(x, hr);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[B_QREADY]);
+      if (lane == 0) mbar_arrive(&bars[C::B_QREADY]);
     };
     // byte of weight [r][token `row`] in a K-major [NB x 128] block
     auto p_off = [&](int r) -> uint32_t {
       return (uint32_t)((r >> 3) * 1024 + (r & 7) * 128 + (((row >> 4) ^ (r & 7)) << 4) + (row & 15));
     };
-    const uint32_t pb = smem_u32(sm + OFF_P) + set * NB * 128;
-    const uint32_t to = tmem + lane_addr + T_O + hb;  // O of stream 0, its rows' hi terms
+        const uint32_t to = tmem + lane_addr + T_O + hb;  // O of stream 0, its rows' hi terms
 
     bool ok = true, more = w.more();
     if (more) {
@@ -422,9 +436,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       load_query(*walk);
     }
     while (ok && more) {
-      const Way<MODE>& x = *walk;
+      const Way<MODE, N>& x = *walk;
       const int n_tiles = x.n, sp = (x.seg & 1) * N;
-      if (!wait(B_QREADY, (uint32_t)x.seg)) {
+      if (!wait(C::B_QREADY, (uint32_t)x.seg)) {
         ok = false;
         break;
       }
@@ -440,20 +454,20 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       const int from = MODE == kWindow ? window_from(a, lim[sp + N - 1]) : 0;  // the last one's window begins last
       {
         // the next row tile's queries, into L2
-        Way<MODE> wn = x;
+        Way<MODE, N> wn = x;
         wn.next(a);
-        if (wn.more() && lane == 0) {
+        if (wn.more() && lane < N / N_SOFT) {
           const uint16_t *ql, *qr;
-          (void)source(wn, ql, qr);
+          (void)source(wn, sw + N_SOFT * lane, ql, qr);
           prefetch_l2(ql, DL * 2);
           prefetch_l2(qr, DR * 2);
         }
         __syncwarp();
       }
 #pragma unroll 1
-      for (int i = (set ^ gt) & 1; i < n_tiles; i += 2) {
-        const int g = gt + i, sb = g % NS, tf = g % NTF, kk = g >> 1;
-        if (!wait(B_TFULL + tf, (uint32_t)(g / NTF)) || !wait(B_SFULL + sb, (uint32_t)(g / NS))) {
+      for (int i = (set + gt) % STREAMS; i < n_tiles; i += STREAMS) {
+        const int g = gt + i, sb = g % NS, tf = g % NTF, kk = g / STREAMS;
+        if (!wait(C::B_TFULL + tf, (uint32_t)(g / NTF)) || !wait(C::B_SFULL + sb, (uint32_t)(g / NS))) {
           ok = false;
           break;
         }
@@ -467,7 +481,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           full = full && lim0 - t0 >= PAGE && !(MODE == kWindow && t0 < from && a.n_sink - t0 < PAGE);
           if (half == p) t = t0 + (row & (PAGE - 1));
         }
-        const float2 s2 = *reinterpret_cast<const float2*>(sm + OFF_SCR + (tf * TILE + row) * 8);
+        const float2 s2 = *reinterpret_cast<const float2*>(sm + C::OFF_SCR + (tf * TILE + row) * 8);
         // (sLc made finite: out of sight it may be anything, in sight the NaN or infinity shows in sRc)
         const float sl = fminf(fmaxf(s2.x, 0.f), 3.0e38f), sr = fmaf(0.f, s2.x, s2.y);
         const float lg = fmaxf(lg2_approx(sl), LG_MIN);
@@ -490,7 +504,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[B_SEMPTY + sb]);
+        if (lane == 0) mbar_arrive(&bars[C::B_SEMPTY + sb]);
         if (!full) {
           const bool here = (have >> half) & 1u;
           auto sees = [&](int h) {
@@ -513,7 +527,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             y[2 * h + 1] = v.y;
           }
           const float ym = reduce8<true>(y, lane);
-          if ((lane & 3) == 0) rmax[(kk & 1) * 64 + wq * N + hb + (lane >> 2)] = ym;
+          if ((lane & 3) == 0) rmax[(kk & 1) * 4 * N + wq * N + hb + (lane >> 2)] = ym;
         }
         if (!group_sync()) {
           ok = false;
@@ -522,7 +536,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         float f;  // the factor of what row hb + lane % 8 added up before
         bool moved;
         {
-          const float* rm = rmax + (kk & 1) * 64 + hb + (lane & 7);
+          const float* rm = rmax + (kk & 1) * 4 * N + hb + (lane & 7);
           const float ym = fmaxf(fmaxf(rm[0], rm[N]), fmaxf(rm[2 * N], rm[3 * N]));
           float mn = mg;
           if (ym > mg + TAU) {
@@ -563,12 +577,16 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           phi[h / 4] = (uint32_t)h01 | ((uint32_t)h23 << 16);
           plo[h / 4] = (uint32_t)l01 | ((uint32_t)l23 << 16);
         }
-        // the stream's tile before: its weights are read, and O is at rest
-        if (kk > 0 && !wait(B_ODONE + set, (uint32_t)(kk - 1))) {
+        // the weights of tile g - 2 are read, and with two streams O is at rest
+        if (g > 1 && !wait(C::B_ODONE + (g & 1), (uint32_t)((g >> 1) - 1))) {
           ok = false;
           break;
         }
-        if (moved && i > 1) {
+        if (moved && i >= STREAMS) {
+          if (STREAMS == 1 && !wait(C::B_ODONE + ((g - 1) & 1), (uint32_t)((g - 1) >> 1))) {
+            ok = false;
+            break;
+          }
           tc_fence_after();
           __syncwarp();
           float fh[NH];
@@ -594,14 +612,15 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll 1
           for (int m = 0; m < 4; ++m) {
             if (!wait_block(4 * g + m)) ok = false;
-            const uint32_t vb = lring + ((4 * g + m) % RL) * KBLK + (sw & 7) * 2048 + lane * 16;
+            const uint32_t vb = lring + ((4 * g + m) % RL) * KBLK + (sw % C::SET) * (KBLK / C::SET) + lane * 16;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < KBLK / C::SET / 512; ++j) {
               const uint4 v = lds128(vb + j * 512);
               sts128(vb + j * 512, make_uint4(no_nan(v.x), no_nan(v.y), no_nan(v.z), no_nan(v.w)));
             }
           }
         }
+        const uint32_t pb = smem_u32(sm + C::OFF_P) + (g & 1) * NB * 128;
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
           sts8(pb + p_off(hb + h), phi[h / 4] >> (8 * (h & 3)));
@@ -610,28 +629,28 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[B_PFULL + set]);
+        if (lane == 0) mbar_arrive(&bars[C::B_PFULL + (g & 1)]);
       }
       if (!ok) break;
       // ---- the row tile's (or its part's) end
       const int last = gt + n_tiles - 1;
-      Way<MODE> wn = x;
+      Way<MODE, N> wn = x;
       wn.next(a);
       more = wn.more();
       if (more) {
         // (its last scores are there: nothing reads the query any more)
-        if (!wait(B_SFULL + last % NS, (uint32_t)(last / NS))) {
+        if (!wait(C::B_SFULL + last % NS, (uint32_t)(last / NS))) {
           ok = false;
           break;
         }
         load_query(wn);
       }
-      bool used[2];
+      bool used[2];  // (a stream each, where there are two)
 #pragma unroll
-      for (int st = 0; st < 2; ++st) {
-        const int l = last - ((last ^ st) & 1);  // the stream's last tile
-        used[st] = l >= gt;
-        if (used[st] && !wait(B_ODONE + st, (uint32_t)(l >> 1))) ok = false;
+      for (int b = 0; b < 2; ++b) {
+        const int l = last - ((last + b) & 1);  // the last even or odd tile
+        used[b] = l >= gt;
+        if (used[b] && !wait(C::B_ODONE + b, (uint32_t)(l >> 1))) ok = false;
       }
       if (!ok) break;
       {
@@ -654,15 +673,21 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       const bool final = x.final();
       const int rows = (int)((int64_t)x.s.nq * a.H - (int64_t)x.rt * N);  // (from the row tile's first one on)
       const int64_t at0 = final ? x.s.q0 * a.H + (int64_t)x.rt * N : ps.row(x, k, 0);
-      // both streams on the larger reference, a row a lane
+      // the streams on the larger reference, a row a lane
       float f0, f1;
       {
         const int r = hb + (lane & 7);
-        const float m0 = refs[r], m1 = refs[N + r], M = fmaxf(m0, m1) - P_LOG;
-        f0 = m0 >= m1 ? 1.f : ex2_approx(m0 - m1);
-        f1 = m1 >= m0 ? 1.f : ex2_approx(m1 - m0);
         const float* p = lsum + r;
-        const float L = ((p[0] + p[N]) + (p[2 * N] + p[3 * N])) * f0 + ((p[4 * N] + p[5 * N]) + (p[6 * N] + p[7 * N])) * f1;
+        float M = refs[r], L = (p[0] + p[N]) + (p[2 * N] + p[3 * N]);
+        f0 = f1 = 1.f;
+        if constexpr (STREAMS == 2) {
+          const float m1 = refs[N + r];
+          f0 = M >= m1 ? 1.f : ex2_approx(M - m1);
+          f1 = m1 >= M ? 1.f : ex2_approx(m1 - M);
+          M = fmaxf(M, m1);
+          L = L * f0 + ((p[4 * N] + p[5 * N]) + (p[6 * N] + p[7 * N])) * f1;
+        }
+        M -= P_LOG;
         const float inv = L == 0.f ? 0.f : (final ? 1.f / L : 1.f);  // (a NaN stays one)
         f0 *= inv;
         f1 *= inv;
@@ -676,14 +701,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
       }
 #pragma unroll 1
-      for (int mm = 0; mm < 2; ++mm) {
-        const int m = 2 * set + mm;  // (the streams' warps take half of the channels each)
+      for (int mm = 0; mm < 4 / STREAMS; ++mm) {
+        const int m = 4 / STREAMS * set + mm;  // (two streams' warps take half of the channels each)
         float v[NH];
 #pragma unroll
         for (int h = 0; h < NH; ++h) v[h] = 0.f;
 #pragma unroll
-        for (int st = 0; st < 2; ++st) {
-          if (!used[st]) continue;
+        for (int st = 0; st < STREAMS; ++st) {
+          if (STREAMS == 2 && !used[st]) continue;
           uint32_t rh[8], rl[8];
           tmem_ld8(to + st * O_COLS + m * NB, rh);
           tmem_ld8(to + st * O_COLS + m * NB + N, rl);
@@ -725,8 +750,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 constexpr int PLAN_NEAR = 4096;
 
 // (base: in shared memory if it fits)
-template <int MODE>
-__global__ void __launch_bounds__(1024) rows_plan_kernel(const ChunkArgs a, Plan<Geo>* plan, int64_t* base, int4* owner,
+template <int MODE, int N>
+__global__ void __launch_bounds__(1024) rows_plan_kernel(const ChunkArgs a, Plan<Geo<N>>* plan, int64_t* base, int4* owner,
                                                          int most) {
   grid_dependents_launch();
   __shared__ int64_t tmp[32];
@@ -738,8 +763,8 @@ __global__ void __launch_bounds__(1024) rows_plan_kernel(const ChunkArgs a, Plan
 
 // ------------------------------------------------------------------ join
 // The parts of a row tile's rows, a warp per row (and SPLIT-th of its channels), a block per row tile.
-template <int MODE, int SPLIT>
-__global__ void __launch_bounds__(N * 32) rows_join_kernel(const ChunkArgs a, const Parts ps, const int4* owner) {
+template <int MODE, int N, int SPLIT>
+__global__ void __launch_bounds__(N * 32) rows_join_kernel(const ChunkArgs a, const Parts<N> ps, const int4* owner) {
   const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
   const int64_t p = blockIdx.x / SPLIT;
   const int ch = (int)(blockIdx.x % SPLIT) * (DL / SPLIT);
@@ -800,7 +825,7 @@ __global__ void __launch_bounds__(N * 32) rows_join_kernel(const ChunkArgs a, co
 
 // ------------------------------------------------------------------ host
 constexpr int64_t OFF_PLAN = 256, OFF_BASE = 4096;
-static_assert(OFF_PLAN + sizeof(Plan<Geo>) <= OFF_BASE, "plan area");
+static_assert(OFF_PLAN + sizeof(Plan<Geo<16>>) <= OFF_BASE, "plan area");
 constexpr int FEW_ROW_TILES = 512;
 
 struct Layout {
@@ -808,6 +833,7 @@ struct Layout {
   int64_t tiles;  // row tiles at most
   int64_t owner, m, rows, bytes;
 };
+template <int N>
 Layout layout_of(int B, int H, int64_t total_q, int64_t keys) {
   auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
   Layout w;
@@ -823,23 +849,26 @@ Layout layout_of(int B, int H, int64_t total_q, int64_t keys) {
   return w;
 }
 int64_t window_keys(int max_blocks, int64_t window, int64_t n_sink) {
-  const int64_t all = ((int64_t)max_blocks * PAGE + TILE - 1) / TILE, seen = (window + n_sink + N + 4 * PAGE) / TILE + 1;
+  const int64_t all = ((int64_t)max_blocks * PAGE + TILE - 1) / TILE, seen = (window + n_sink + 32 + 4 * PAGE) / TILE + 1;
   return seen < all ? seen : all;
 }
 
-template <int MODE>
+// Row tiles of 32: where sequences have more than 16 rows on average.
+bool wide(int B, int H, int64_t total_q) { return total_q * H > 16 * (int64_t)B; }
+
+template <int MODE, int N>
 cudaError_t launch(ChunkArgs a, const Layout& w, void* workspace, cudaStream_t s) {
   static std::atomic<int> memo[MAX_DEVICES];
   int done = 0;
   cudaError_t e = per_device(memo, [](int* v) {
     *v = 1;
-    return cudaFuncSetAttribute(rows_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    return cudaFuncSetAttribute(rows_kernel<MODE, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<N>::SMEM);
   }, &done);
   if (e != cudaSuccess) return e;
   char* p = static_cast<char*>(workspace);
   a.err = reinterpret_cast<unsigned*>(p);
-  Parts ps;
-  ps.plan = reinterpret_cast<Plan<Geo>*>(p + OFF_PLAN);
+  Parts<N> ps;
+  ps.plan = reinterpret_cast<Plan<Geo<N>>*>(p + OFF_PLAN);
   ps.m = reinterpret_cast<float*>(p + w.m);
   ps.l = ps.m + w.rows;
   ps.o = ps.l + w.rows;
@@ -854,22 +883,25 @@ cudaError_t launch(ChunkArgs a, const Layout& w, void* workspace, cudaStream_t s
   if ((e = make_cache_map(d, &kmap)) != cudaSuccess || (e = make_rc_map(d, &rmap)) != cudaSuccess ||
       (e = make_scale_map(d, &smap)) != cudaSuccess)
     return e;
-  rows_plan_kernel<MODE><<<1, 1024, 0, s>>>(a, ps.plan, reinterpret_cast<int64_t*>(p + OFF_BASE), owner, w.most);
+  rows_plan_kernel<MODE, N><<<1, 1024, 0, s>>>(a, ps.plan, reinterpret_cast<int64_t*>(p + OFF_BASE), owner, w.most);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  e = launch_after_prep(rows_kernel<MODE>, w.most, NTHREADS, SMEM, s, a, ps, kmap, rmap, smap);
+  e = launch_after_prep(rows_kernel<MODE, N>, w.most, NTHREADS, Cfg<N>::SMEM, s, a, ps, kmap, rmap, smap);
   if (e != cudaSuccess || w.most == 1) return e;
   if (w.tiles < FEW_ROW_TILES)
-    return launch_after_prep(rows_join_kernel<MODE, 4>, (unsigned)(4 * w.tiles), N * 32, 0, s, a, ps, (const int4*)owner);
-  return launch_after_prep(rows_join_kernel<MODE, 1>, (unsigned)w.tiles, N * 32, 0, s, a, ps, (const int4*)owner);
+    return launch_after_prep(rows_join_kernel<MODE, N, 4>, (unsigned)(4 * w.tiles), N * 32, 0, s, a, ps, (const int4*)owner);
+  return launch_after_prep(rows_join_kernel<MODE, N, 1>, (unsigned)w.tiles, N * 32, 0, s, a, ps, (const int4*)owner);
 }
 
 }  // namespace
 
 int64_t rows_window_workspace(int B, int H, int64_t total_q, int max_blocks, int window, int n_sink) {
-  return layout_of(B, H, total_q, window_keys(max_blocks, window, n_sink)).bytes;
+  const int64_t keys = window_keys(max_blocks, window, n_sink);
+  return wide(B, H, total_q) ? layout_of<32>(B, H, total_q, keys).bytes : layout_of<16>(B, H, total_q, keys).bytes;
 }
 cudaError_t launch_rows_window(const ChunkArgs& a, void* workspace, cudaStream_t s) {
-  return launch<kWindow>(a, layout_of(a.B, a.H, a.total_q, window_keys(a.max_blocks, a.window, a.n_sink)), workspace, s);
+  const int64_t keys = window_keys(a.max_blocks, a.window, a.n_sink);
+  return wide(a.B, a.H, a.total_q) ? launch<kWindow, 32>(a, layout_of<32>(a.B, a.H, a.total_q, keys), workspace, s)
+                                   : launch<kWindow, 16>(a, layout_of<16>(a.B, a.H, a.total_q, keys), workspace, s);
 }
 
 }  // namespace kv8
