@@ -78,23 +78,12 @@
 namespace kv8 {
 namespace {
 
-constexpr int ROWS = 256;                    // rows of a row tile: 128 per CTA of a pair
+constexpr int ROWS = WideGeo::ROWS;           // rows of a row tile: 128 per CTA of a pair
 constexpr int CROWS = 128;
 constexpr int W_TMA = 0, W_MMA = 1, W_SCALE = 2, W_LANE = 3;
 constexpr int N_LANE_WARPS = 16;             // four per TMEM lane quarter, and per scheduler
 constexpr int NTHREADS = (W_LANE + N_LANE_WARPS) * 32;
-constexpr int MAX_CLUSTERS = NUM_SMS / 4;
-// A cluster per row tile, or more while that gives each MIN_TILES key tiles on average.  (The ranges
-// differ by up to SWITCH, below, which is counted in front of every row tile, the first of a range
-// among them: 4 tiles fall into ranges of 0 and 4, 16 into 0, 0, 2, 3, 2, 3, 3, 3.)  Device times for
-// 1, 2 and 4, us: one token of 128 heads over 512 keys 30.8, 28.7, 26.7, over 2048 35.4, 32.8, 36.8,
-// over 8192 47.2, 47.0, 41.0; two row tiles of 8 key tiles 32.8, 34.9, 38.7.
-constexpr int MIN_TILES = 2;
-// What beginning a row tile costs, in key tiles: 19 thousand cycles (the query is loaded and split
-// while the context pair writes its results, and the pipeline fills) against 3.1 thousand a tile.  A
-// prompt of 4096 tokens at 128 heads: 2.40 ms when ranges count 4 for it, 2.17 for 5, 2.04 for 6, 2.06
-// for 7, 2.09 for 8; five sequences without a mask 103, 102, 98, 99, 100 us.
-constexpr int SWITCH = 6;
+constexpr int MAX_CLUSTERS = WideGeo::RANGES, MIN_TILES = WideGeo::MIN_TILES;
 constexpr int BLK = PAGE * 128;              // 8 KB: [64 tokens x 128 bytes]
 constexpr int RBLK = PAGE * DR;              // 4 KB: [64 tokens x 64 bytes]
 constexpr int KTILE = 4 * BLK + RBLK;        // a score CTA's page of a tile: 36 KB
@@ -177,10 +166,7 @@ static_assert(OFF_K % 1024 == 0 && KTILE % 1024 == 0 && OFF_V % 1024 == 0 && P_S
 static_assert(P_BYTES <= P_STRIDE && N_LANE_WARPS * 2048 <= 4 * OP_ATOM, "payload and staging");
 static_assert(SMEM <= 232448, "shared memory above the per-CTA limit");
 
-struct Geo {
-  static constexpr int ROWS = kv8::ROWS, RANGES = MAX_CLUSTERS, SWITCH = kv8::SWITCH, MIN_TILES = kv8::MIN_TILES;
-};
-static_assert(ROWS == WIDE, "the row tiles that a shared prefix's cost is counted in");
+using Geo = WideGeo;
 template <int MODE>
 using Way = Walk<MODE, Geo>;
 static_assert(sizeof(Way<kShared>) * N_LANE_WARPS <= OFF_SC - OFF_WALK && sizeof(Way<kWindow>) <= sizeof(Way<kShared>),
@@ -199,7 +185,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const ChunkArgs a, Plan<Geo>
   }
   if (threadIdx.x == 0) *a.err = 0;
   __syncthreads();
-  if constexpr (MODE == kShared) make_entries(a, &plan->part_rows, tmp);
+  if constexpr (MODE == kShared) make_entries<Geo, 1>(a, &plan->part_rows, tmp, true);
   make_plan<MODE>(a, plan, base, MODE == kShared ? a.G + a.B : a.B, clusters, tmp,
                   MODE == kShared ? a.unit : nullptr, nullptr);
 }
@@ -1352,15 +1338,24 @@ Layout layout_of(int B, int H, int64_t total_q, int max_blocks, int G, int64_t w
   return w;
 }
 
-// Whether a call's sequences have so few rows on average that the kernel for them is faster.
-constexpr int FEW_ROWS = 128;
-bool few_rows(int B, int H, int64_t total_q) { return total_q * H <= (int64_t)FEW_ROWS * B; }
+// Whether a call's sequences have so few rows on average that the kernel for them (rows.cu) is faster: up
+// to 64, or 128 over few key tiles.  (It reads a key tile once for 32 rows, this one for 256, but a row
+// tile starts faster there.)
+constexpr int FEW_ROWS = 64, FEW_TILES = 20;
+bool few_rows(int B, int H, int64_t total_q, int64_t keys) {
+  const int64_t rows = total_q * H;
+  return rows <= (int64_t)FEW_ROWS * B || (rows <= 2 * (int64_t)FEW_ROWS * B && keys <= FEW_TILES * TILE);
+}
+int64_t window_keys(int max_blocks, int64_t window, int64_t n_sink) {
+  const int64_t all = (int64_t)max_blocks * PAGE;
+  return window + n_sink < all ? window + n_sink : all;
+}
 
+// Clusters of the kernel that the device holds at once.
 template <int MODE>
-cudaError_t launch(ChunkArgs a, void* workspace, cudaStream_t s) {
+cudaError_t capacity(int* fit) {
   static std::atomic<int> memo[MAX_DEVICES];
-  int fit = 0;  // clusters that the device holds at once
-  cudaError_t e = per_device(memo, [](int* v) {
+  return per_device(memo, [](int* v) {
     cudaError_t r = cudaFuncSetAttribute(chunk_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (r != cudaSuccess) return r;
     cudaLaunchConfig_t cfg = {};
@@ -1373,7 +1368,13 @@ cudaError_t launch(ChunkArgs a, void* workspace, cudaStream_t s) {
     if (n < 1) return cudaErrorLaunchOutOfResources;
     *v = n > MAX_CLUSTERS ? MAX_CLUSTERS : n;
     return cudaSuccess;
-  }, &fit);
+  }, fit);
+}
+
+template <int MODE>
+cudaError_t launch(ChunkArgs a, void* workspace, cudaStream_t s) {
+  int fit = 0;
+  cudaError_t e = capacity<MODE>(&fit);
   if (e != cudaSuccess) return e;
   const Layout w = layout_of<MODE>(a.B, a.H, a.total_q, a.max_blocks, a.G, a.window, a.n_sink);
   const int clusters = w.most < fit ? w.most : fit;
@@ -1416,17 +1417,34 @@ int64_t chunk_workspace(int B, int H, int64_t total_q, int max_blocks) {
   return layout_of<kPlain>(B, H, total_q, max_blocks, 0, 0, 0).bytes;
 }
 int64_t window_workspace(int B, int H, int64_t total_q, int max_blocks, int window, int n_sink) {
-  if (few_rows(B, H, total_q)) return rows_window_workspace(B, H, total_q, max_blocks, window, n_sink);
+  if (few_rows(B, H, total_q, window_keys(max_blocks, window, n_sink)))
+    return rows_window_workspace(B, H, total_q, max_blocks, window, n_sink);
   return layout_of<kWindow>(B, H, total_q, max_blocks, 0, window, n_sink).bytes;
 }
 int64_t shared_workspace(int B, int H, int64_t total_q, int max_blocks, int G) {
+  if (few_rows(B, H, total_q, INT64_MAX)) return rows_shared_workspace(B, H, total_q, max_blocks, G);
   return layout_of<kShared>(B, H, total_q, max_blocks, G, 0, 0).bytes;
 }
 
 cudaError_t launch_chunk(const ChunkArgs& a, void* workspace, cudaStream_t s) { return launch<kPlain>(a, workspace, s); }
 cudaError_t launch_window(const ChunkArgs& a, void* workspace, cudaStream_t s) {
-  return few_rows(a.B, a.H, a.total_q) ? launch_rows_window(a, workspace, s) : launch<kWindow>(a, workspace, s);
+  return few_rows(a.B, a.H, a.total_q, window_keys(a.max_blocks, a.window, a.n_sink))
+             ? launch_rows_window(a, workspace, s) : launch<kWindow>(a, workspace, s);
 }
-cudaError_t launch_shared(const ChunkArgs& a, void* workspace, cudaStream_t s) { return launch<kShared>(a, workspace, s); }
+cudaError_t launch_shared(const ChunkArgs& a, void* workspace, cudaStream_t s) {
+  return few_rows(a.B, a.H, a.total_q, INT64_MAX) ? launch_rows_shared(a, workspace, s) : launch<kShared>(a, workspace, s);
+}
+
+cudaError_t prefix_capacity(int* clusters) { return capacity<kShared>(clusters); }
+cudaError_t launch_prefixes(const ChunkArgs& a, const PrefixParts& p, int clusters, const CUtensorMap& kmap,
+                            const CUtensorMap& rmap, const CUtensorMap& smap, cudaStream_t s) {
+  Workspace ws;
+  ws.plan = static_cast<Plan<Geo>*>(p.plan);
+  ws.m = p.m;
+  ws.l = p.l;
+  ws.o = p.o;
+  ws.parts = p.whole;
+  return launch_after_prep(chunk_kernel<kShared>, 4 * clusters, NTHREADS, SMEM, s, a, ws, kmap, rmap, smap);
+}
 
 }  // namespace kv8

@@ -25,6 +25,22 @@ constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 
 // ------------------------------------------------------------------ work
+// The geometry of chunk.cu: a cluster of four CTAs is a range's.
+struct WideGeo {
+  static constexpr int ROWS = 256, RANGES = NUM_SMS / 4;
+  // A cluster per row tile, or more while that gives each MIN_TILES key tiles on average.  (The ranges
+  // differ by up to SWITCH, below, which is counted in front of every row tile, the first of a range
+  // among them: 4 tiles fall into ranges of 0 and 4, 16 into 0, 0, 2, 3, 2, 3, 3, 3.)  Device times for
+  // 1, 2 and 4, us: one token of 128 heads over 512 keys 30.8, 28.7, 26.7, over 2048 35.4, 32.8, 36.8,
+  // over 8192 47.2, 47.0, 41.0; two row tiles of 8 key tiles 32.8, 34.9, 38.7.
+  static constexpr int MIN_TILES = 2;
+  // What beginning a row tile costs, in key tiles: 19 thousand cycles (the query is loaded and split
+  // while the context pair writes its results, and the pipeline fills) against 3.1 thousand a tile.  A
+  // prompt of 4096 tokens at 128 heads: 2.40 ms when ranges count 4 for it, 2.17 for 5, 2.04 for 6, 2.06
+  // for 7, 2.09 for 8; five sequences without a mask 103, 102, 98, 99, 100 us.
+  static constexpr int SWITCH = 6;
+};
+
 // Plan of range k: its first row tile (sequence b, row tile rt, nt key tiles of
 // which off come before the range), the unit where the range starts and its units.
 struct PlanEntry {
@@ -156,8 +172,10 @@ __device__ __forceinline__ int64_t plan_sum(int64_t v, int64_t* tmp, int64_t* to
 // The prefix is whole pages that every row of the group sees; a group takes part where its row tiles
 // are fewer together than apart by more than the parts cost: SHARE key tiles a row tile (6 for its start, and
 // 256 rows of f32 written twice and read twice), and where its sequences have PART_ROWS rows on average
-// at most (above, they fill their row tiles, and little is saved).
-constexpr int PART_ROWS = 1024, SHARE = 16, WIDE = 256;  // (rows of the prefixes' row tiles)
+// at most (above, they fill their row tiles, and little is saved).  G is the geometry of what the
+// sequences would be computed with otherwise, COST of whose (row tile, key tile) pairs take an SM as long as
+// one of a prefix.
+constexpr int PART_ROWS = 1024, SHARE = 16;
 
 __device__ __forceinline__ int64_t warp_sum(int64_t v) {
 #pragma unroll
@@ -173,29 +191,37 @@ __device__ __forceinline__ int64_t warp_min(int64_t v) {
   return v;
 }
 
-__device__ __forceinline__ void make_entries(const ChunkArgs& a, int64_t* part_rows, int64_t* tmp) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Whether the groups' ranges break their order (by a whole CTA of 1024 threads); that and lengths below 0 are told.
+__device__ __forceinline__ bool groups_bad(const ChunkArgs& a, bool tell) {
   int bad = 0;
   for (int g = threadIdx.x; g < a.G; g += 1024) {
     const int f = __ldg(&a.group_start[g]), l = __ldg(&a.group_start[g + 1]);
     bad |= f < 0 || l < f || l > a.B;
+    if (tell && __ldg(&a.shared_len[g]) < 0) atomicOr(a.err, ERR_SEQ_LEN);
+  }
+  bad = __syncthreads_or(bad);
+  if (tell && bad && threadIdx.x == 0) atomicOr(a.err, ERR_BLOCK_TABLE);
+  return bad;
+}
+
+template <class G, int COST>
+__device__ __forceinline__ void make_entries(const ChunkArgs& a, int64_t* part_rows, int64_t* tmp, bool tell) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int g = threadIdx.x; g < a.G; g += 1024) {
     a.entries[g].u = make_int4(0, 0, 0, 0);
     a.entries[g].v = make_int4(0, 0, -1, 0);
   }
   for (int b = threadIdx.x; b < a.B; b += 1024) {
-    const SeqInfo<kPlain> s = seq_info<kPlain>(a, b, true);
+    const SeqInfo<kPlain> s = seq_info<kPlain>(a, b, tell);
     a.entries[a.G + b].u = make_int4((int)s.q0, s.nq, s.T, b);
     a.entries[a.G + b].v = make_int4(0, a.causal, -1, 0);
   }
   if (threadIdx.x == 0) *part_rows = 0;
-  bad = __syncthreads_or(bad);
-  if (bad && threadIdx.x == 0) atomicOr(a.err, ERR_BLOCK_TABLE);
-  if (bad || a.G == 0) return;  // (ranges that may overlap: nothing is shared)
+  if (groups_bad(a, tell) || a.G == 0) return;  // (ranges that may overlap: nothing is shared)
   // what each group would share, a warp per group
   for (int g = warp; g < a.G; g += 32) {
     const int f = __ldg(&a.group_start[g]), l = __ldg(&a.group_start[g + 1]);
     int64_t P = __ldg(&a.shared_len[g]), apart = 0, tokens = 0, members = 0, q0 = INT32_MAX, row = INT32_MAX;
-    if (P < 0 && lane == 0) atomicOr(a.err, ERR_SEQ_LEN);
     for (int b = f + lane; b < l; b += 32) {
       const int4 u = a.entries[a.G + b].u;
       // (a range that breaks the order has no query; nothing is shared then)
@@ -203,7 +229,7 @@ __device__ __forceinline__ void make_entries(const ChunkArgs& a, int64_t* part_r
       if (u.y == 0) continue;
       const int64_t see = a.causal ? (int64_t)u.z - u.y + 1 : u.z;
       P = see < P ? see : P;
-      apart += ((int64_t)u.y * a.H + WIDE - 1) / WIDE;
+      apart += ((int64_t)u.y * a.H + G::ROWS - 1) / G::ROWS;
       tokens += u.y;
       ++members;
       if (row == INT32_MAX) row = b;  // (a sequence without queries need not hold the prefix)
@@ -216,8 +242,8 @@ __device__ __forceinline__ void make_entries(const ChunkArgs& a, int64_t* part_r
     tokens = warp_sum(tokens);
     members = warp_sum(members);
     P = P > 0 ? P / PAGE : 0;
-    const int64_t rows = tokens * a.H, together = (rows + WIDE - 1) / WIDE, tiles = (P + 1) / 2;
-    const bool take = members > 1 && P > 0 && rows <= PART_ROWS * members && together * (tiles + SHARE) < apart * tiles;
+    const int64_t rows = tokens * a.H, together = (rows + WideGeo::ROWS - 1) / WideGeo::ROWS, tiles = (P + 1) / 2;
+    const bool take = members > 1 && P > 0 && rows <= PART_ROWS * members && together * (tiles + SHARE) * COST < apart * tiles;
     if (take && lane == 0) {
       a.entries[g].u = make_int4((int)q0, (int)tokens, (int)P * PAGE, (int)row);
       a.entries[g].v = make_int4(0, 0, 0, 0);
@@ -253,8 +279,9 @@ __device__ __forceinline__ void make_entries(const ChunkArgs& a, int64_t* part_r
       const int token = m.x - u.x;
       m.z -= u.z;
       a.entries[a.G + b].u = m;
-      a.entries[a.G + b].v = make_int4(u.z / PAGE, a.causal, (int)a.part_rows + from + token * a.H, 0);
-      for (int i = 0; i < m.y; ++i) a.part_seq[from / a.H + token + i] = make_int2(g, b);
+      a.entries[a.G + b].v = make_int4(u.z / PAGE, a.causal, (int)a.part_rows + from + token * a.H, g);
+      if (a.part_seq != nullptr)
+        for (int i = 0; i < m.y; ++i) a.part_seq[from / a.H + token + i] = make_int2(g, b);
     }
   }
   __syncthreads();

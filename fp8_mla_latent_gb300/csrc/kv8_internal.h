@@ -209,7 +209,7 @@ struct ChunkArgs {
   int G;
   ChunkEntry* entries;         // [G + B] the prefixes, the sequences
   int64_t* unit;               // [row tiles + 1] units before each
-  int2* part_seq;              // group and sequence of the tokens that have parts
+  int2* part_seq;              // group and sequence of the tokens that have parts, or nullptr
   int64_t part_rows;           // room for their rows
 };
 // Bytes of workspace (deterministic in their arguments), and the calls on them.
@@ -219,6 +219,17 @@ int64_t shared_workspace(int B, int H, int64_t total_q, int max_blocks, int G);
 // (sequences of few rows: rows.cu)
 int64_t rows_window_workspace(int B, int H, int64_t total_q, int max_blocks, int window, int n_sink);
 cudaError_t launch_rows_window(const ChunkArgs& a, void* workspace, cudaStream_t s);
+int64_t rows_shared_workspace(int B, int H, int64_t total_q, int max_blocks, int G);
+cudaError_t launch_rows_shared(const ChunkArgs& a, void* workspace, cudaStream_t s);
+// (shared prefixes alone, by chunk.cu: the kernel on a given plan over entries of prefixes; `whole` as there)
+struct PrefixParts {
+  void* plan;
+  float *m, *l, *o;
+  int64_t whole;
+};
+cudaError_t prefix_capacity(int* clusters);
+cudaError_t launch_prefixes(const ChunkArgs& a, const PrefixParts& p, int clusters, const CUtensorMap& kmap,
+                            const CUtensorMap& rmap, const CUtensorMap& smap, cudaStream_t s);
 cudaError_t launch_chunk(const ChunkArgs& a, void* workspace, cudaStream_t s);
 cudaError_t launch_window(const ChunkArgs& a, void* workspace, cudaStream_t s);
 cudaError_t launch_shared(const ChunkArgs& a, void* workspace, cudaStream_t s);

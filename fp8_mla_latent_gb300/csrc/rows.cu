@@ -36,7 +36,7 @@ constexpr uint64_t WAIT_NS = 2000000000ull;
 
 template <int N>
 struct Geo {
-  static constexpr int ROWS = N, RANGES = NUM_SMS, SWITCH = 2, MIN_TILES = 1;
+  static constexpr int ROWS = N, RANGES = NUM_SMS, SWITCH = 3, MIN_TILES = 1;
 };
 template <int MODE, int N>
 using Way = Walk<MODE, Geo<N>>;
@@ -729,7 +729,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
       }
       tc_fence_before();
-      if (!all_sync()) {  // O, the references and the sums may be written again
+      if (more && !all_sync()) {  // O, the references and the sums may be written again
         ok = false;
         break;
       }
@@ -758,13 +758,41 @@ __global__ void __launch_bounds__(1024) rows_plan_kernel(const ChunkArgs a, Plan
   __shared__ int64_t near[PLAN_NEAR];
   if (threadIdx.x == 0) *a.err = 0;
   __syncthreads();
+  if (MODE == kPlain && a.G > 0) (void)groups_bad(a, true);  // (groups too small to share anything)
   make_plan<MODE>(a, plan, a.B < PLAN_NEAR ? near : base, a.B, most, tmp, nullptr, owner);
 }
 
+// The plans of a call with shared prefixes, each with entries of its own: block 0 that of the prefixes (whose
+// base the join reads), block 1 that of the sequences.  (COST: 12.4 thousand cycles of an SM for a
+// prefix's unit, against 3.2 or 4.3 here.)
+template <int N>
+__global__ void __launch_bounds__(1024) rows_shared_plan_kernel(ChunkArgs a, Plan<Geo<N>>* plan, int64_t* base,
+                                                                int4* owner, int most, Plan<WideGeo>* prefix_plan,
+                                                                int64_t* prefix_base, int4* prefix_owner,
+                                                                int prefix_most) {
+  grid_dependents_launch();
+  __shared__ int64_t tmp[32];
+  __shared__ int64_t near[PLAN_NEAR];
+  const bool own = blockIdx.x == 1;
+  if (own && threadIdx.x == 0) *a.err = 0;
+  __syncthreads();
+  if (own) a.entries += a.G + a.B;
+  make_entries<Geo<N>, N == 16 ? 4 : 3>(a, own ? &plan->part_rows : &prefix_plan->part_rows, tmp, own);
+  if (own) {
+    a.entries += a.G;
+    make_plan<kShared>(a, plan, a.B < PLAN_NEAR ? near : base, a.B, most, tmp, nullptr, owner);
+  } else {
+    make_plan<kShared>(a, prefix_plan, prefix_base, a.G, prefix_most, tmp, nullptr, prefix_owner);
+  }
+}
+
 // ------------------------------------------------------------------ join
-// The parts of a row tile's rows, a warp per row (and SPLIT-th of its channels), a block per row tile.
+// The parts of a row tile's rows, a warp per row (and SPLIT-th of its channels), a block per row tile.  With
+// a shared prefix they are those of the row's own keys, then those of the prefix.
 template <int MODE, int N, int SPLIT>
-__global__ void __launch_bounds__(N * 32) rows_join_kernel(const ChunkArgs a, const Parts<N> ps, const int4* owner) {
+__global__ void __launch_bounds__(N * 32) rows_join_kernel(const ChunkArgs a, const Parts<N> ps, const int4* owner,
+                                                           const int64_t* prefix_base, const int4* prefix_owner,
+                                                           int64_t prefix_slots) {
   const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
   const int64_t p = blockIdx.x / SPLIT;
   const int ch = (int)(blockIdx.x % SPLIT) * (DL / SPLIT);
@@ -772,12 +800,40 @@ __global__ void __launch_bounds__(N * 32) rows_join_kernel(const ChunkArgs a, co
   const int64_t tiles = ps.plan->tiles;
   const int4 of = owner[p];  // (there is room for as many as there are blocks)
   if (p >= tiles) return;
-  const int k0 = of.z >> 1, n = of.w - k0 + 1;
-  if (n == 1) return;  // whole
-  auto slot = [&](int j) -> int64_t { return (int64_t)(j == 0 ? of.z : 2 * (k0 + j)) * N + row; };
+  const int k0 = of.z >> 1, n_own = of.w - k0 + 1;
   const SeqInfo<MODE> s = seq_info<MODE>(a, of.x, false);
+  bool shares = false;
+  if constexpr (MODE == kShared) shares = s.part >= 0;
+  if (n_own == 1 && !shares) return;  // whole
   const int64_t r = (int64_t)of.y * N + row;
   if (r >= (int64_t)s.nq * a.H) return;
+  int n = n_own, prefix_k0 = 0;
+  int64_t own_whole = 0, prefix_whole = 0, prefix_row = 0;
+  int4 pf = make_int4(0, 0, 0, 0);
+  if constexpr (MODE == kShared) {
+    if (shares) {
+      const int g = a.entries[of.x].v.w;
+      const ChunkEntry e = a.entries[g - a.G];
+      const int64_t in_group = (s.q0 - e.u.x) * a.H + r;
+      pf = prefix_owner[prefix_base[g] + in_group / WideGeo::ROWS];
+      prefix_k0 = pf.z >> 1;
+      n += pf.w - prefix_k0 + 1;
+      own_whole = ps.whole + s.part + r;
+      prefix_whole = ps.whole + e.v.z + in_group;
+      prefix_row = in_group % WideGeo::ROWS - prefix_slots;  // (the prefixes' slots lie in front of these)
+    }
+  }
+  auto slot = [&](int j) -> int64_t {
+    if (MODE == kShared && shares) {
+      if (j >= n_own) {
+        j -= n_own;
+        if (n - n_own == 1) return prefix_whole;
+        return (int64_t)(j == 0 ? pf.z : 2 * (prefix_k0 + j)) * WideGeo::ROWS + prefix_row;
+      }
+      if (n_own == 1) return own_whole;
+    }
+    return (int64_t)(j == 0 ? of.z : 2 * (k0 + j)) * N + row;
+  };
   float M = -INFINITY, L = 0.f;
   for (int j = lane; j < n; j += 32) M = fmaxf(M, ps.m[slot(j)]);
 #pragma unroll
@@ -824,37 +880,61 @@ __global__ void __launch_bounds__(N * 32) rows_join_kernel(const ChunkArgs a, co
 }
 
 // ------------------------------------------------------------------ host
-constexpr int64_t OFF_PLAN = 256, OFF_BASE = 4096;
-static_assert(OFF_PLAN + sizeof(Plan<Geo<16>>) <= OFF_BASE, "plan area");
+constexpr int64_t OFF_PLAN = 256, OFF_PREFIX_PLAN = 4096, OFF_BASE = 5376;
+static_assert(OFF_PLAN + sizeof(Plan<Geo<16>>) <= OFF_PREFIX_PLAN && OFF_PREFIX_PLAN + sizeof(Plan<WideGeo>) <= OFF_BASE,
+              "plan area");
 constexpr int FEW_ROW_TILES = 512;
 
 struct Layout {
-  int most;       // ranges
-  int64_t tiles;  // row tiles at most
-  int64_t owner, m, rows, bytes;
+  int most, prefix_most;         // ranges, and the prefixes' clusters
+  int64_t tiles;                 // row tiles at most
+  int64_t part_rows;             // room for rows that have parts
+  int64_t owner, entries, prefix_base, prefix_owner, m, prefix_slots, slots, bytes;
+  int64_t rows() const { return prefix_slots + slots + 2 * part_rows; }
 };
+// (G < 0: no shared prefixes)
 template <int N>
-Layout layout_of(int B, int H, int64_t total_q, int64_t keys) {
+Layout layout_of(int B, int H, int64_t total_q, int64_t keys, int G) {
   auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
-  Layout w;
+  Layout w{};
   w.tiles = total_q * H / N + B;
   const int64_t units = w.tiles * keys;
   w.most = (int)(units < 1 ? 1 : (units < NUM_SMS ? units : NUM_SMS));
   int64_t at = OFF_BASE + up((int64_t)(B + 1) * 8);
   w.owner = at;
   at += up(w.tiles * (int64_t)sizeof(int4));
+  if (G >= 0) {
+    const int64_t rows = total_q * H, few = (int64_t)PART_ROWS * B, cap = 1 << 20, wide = rows / WideGeo::ROWS + G;
+    w.part_rows = rows < few ? rows : few;
+    if (w.part_rows > cap) w.part_rows = cap;
+    const int64_t u = wide * keys / WideGeo::MIN_TILES;
+    w.prefix_most = (int)(u < 1 ? 1 : (u < WideGeo::RANGES ? u : WideGeo::RANGES));
+    w.entries = at;
+    at += up(2 * (int64_t)(G + B) * (int64_t)sizeof(ChunkEntry));
+    w.prefix_base = at;
+    at += up((int64_t)(G + 1) * 8);
+    w.prefix_owner = at;
+    at += up(wide * (int64_t)sizeof(int4));
+    w.prefix_slots = 2 * (int64_t)w.prefix_most * WideGeo::ROWS;
+  }
   w.m = at;
-  w.rows = w.most > 1 ? 2 * (int64_t)w.most * N : 0;
-  w.bytes = at + w.rows * (8 + DL * 4);
+  w.slots = w.most > 1 || G >= 0 ? 2 * (int64_t)w.most * N : 0;  // (one range cuts no row tile)
+  w.bytes = at + w.rows() * (8 + DL * 4);
   return w;
 }
+int64_t all_keys(int max_blocks) { return ((int64_t)max_blocks * PAGE + TILE - 1) / TILE; }
 int64_t window_keys(int max_blocks, int64_t window, int64_t n_sink) {
-  const int64_t all = ((int64_t)max_blocks * PAGE + TILE - 1) / TILE, seen = (window + n_sink + 32 + 4 * PAGE) / TILE + 1;
+  const int64_t all = all_keys(max_blocks), seen = (window + n_sink + 32 + 4 * PAGE) / TILE + 1;
   return seen < all ? seen : all;
 }
 
 // Row tiles of 32: where sequences have more than 16 rows on average.
 bool wide(int B, int H, int64_t total_q) { return total_q * H > 16 * (int64_t)B; }
+
+// Whether a call may have a prefix whose sharing pays: four clusters' worth of the sequences' row tiles.
+bool may_share(int B, int H, int64_t total_q, int G) {
+  return G > 0 && B > 1 && total_q * H / (wide(B, H, total_q) ? 32 : 16) + B > 4;
+}
 
 template <int MODE, int N>
 cudaError_t launch(ChunkArgs a, const Layout& w, void* workspace, cudaStream_t s) {
@@ -867,13 +947,19 @@ cudaError_t launch(ChunkArgs a, const Layout& w, void* workspace, cudaStream_t s
   if (e != cudaSuccess) return e;
   char* p = static_cast<char*>(workspace);
   a.err = reinterpret_cast<unsigned*>(p);
+  float* m = reinterpret_cast<float*>(p + w.m);
+  float* l = m + w.rows();
+  float* o = l + w.rows();
   Parts<N> ps;
   ps.plan = reinterpret_cast<Plan<Geo<N>>*>(p + OFF_PLAN);
-  ps.m = reinterpret_cast<float*>(p + w.m);
-  ps.l = ps.m + w.rows;
-  ps.o = ps.l + w.rows;
-  ps.whole = 0;
+  ps.m = m + w.prefix_slots;
+  ps.l = l + w.prefix_slots;
+  ps.o = o + w.prefix_slots * DL;
+  ps.whole = w.slots;
+  int64_t* base = reinterpret_cast<int64_t*>(p + OFF_BASE);
+  int64_t* prefix_base = reinterpret_cast<int64_t*>(p + w.prefix_base);
   int4* owner = reinterpret_cast<int4*>(p + w.owner);
+  int4* prefix_owner = reinterpret_cast<int4*>(p + w.prefix_owner);
   DecodeArgs d{};  // what the cache's tensor maps are made from
   d.codes = a.codes;
   d.scales = a.scales;
@@ -883,25 +969,57 @@ cudaError_t launch(ChunkArgs a, const Layout& w, void* workspace, cudaStream_t s
   if ((e = make_cache_map(d, &kmap)) != cudaSuccess || (e = make_rc_map(d, &rmap)) != cudaSuccess ||
       (e = make_scale_map(d, &smap)) != cudaSuccess)
     return e;
-  rows_plan_kernel<MODE, N><<<1, 1024, 0, s>>>(a, ps.plan, reinterpret_cast<int64_t*>(p + OFF_BASE), owner, w.most);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if constexpr (MODE == kShared) {
+    int fit = 0;
+    if ((e = prefix_capacity(&fit)) != cudaSuccess) return e;
+    const int clusters = w.prefix_most < fit ? w.prefix_most : fit;
+    a.entries = reinterpret_cast<ChunkEntry*>(p + w.entries);
+    a.part_rows = w.part_rows;
+    Plan<WideGeo>* prefix_plan = reinterpret_cast<Plan<WideGeo>*>(p + OFF_PREFIX_PLAN);
+    rows_shared_plan_kernel<N><<<2, 1024, 0, s>>>(a, ps.plan, base, owner, w.most, prefix_plan, prefix_base, prefix_owner,
+                                                  clusters);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = launch_prefixes(a, PrefixParts{prefix_plan, m, l, o, w.prefix_slots + w.slots}, clusters, kmap, rmap, smap, s);
+    if (e != cudaSuccess) return e;
+    a.entries += a.G + a.B + a.G;  // the sequences, of the second plan's copy
+  } else {
+    rows_plan_kernel<MODE, N><<<1, 1024, 0, s>>>(a, ps.plan, base, owner, w.most);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
   e = launch_after_prep(rows_kernel<MODE, N>, w.most, NTHREADS, Cfg<N>::SMEM, s, a, ps, kmap, rmap, smap);
-  if (e != cudaSuccess || w.most == 1) return e;
+  if (e != cudaSuccess || (MODE != kShared && w.most == 1)) return e;
+  const int64_t* pb = prefix_base;
+  const int4 *ow = owner, *po = prefix_owner;
   if (w.tiles < FEW_ROW_TILES)
-    return launch_after_prep(rows_join_kernel<MODE, N, 4>, (unsigned)(4 * w.tiles), N * 32, 0, s, a, ps, (const int4*)owner);
-  return launch_after_prep(rows_join_kernel<MODE, N, 1>, (unsigned)w.tiles, N * 32, 0, s, a, ps, (const int4*)owner);
+    return launch_after_prep(rows_join_kernel<MODE, N, 4>, (unsigned)(4 * w.tiles), N * 32, 0, s, a, ps, ow, pb, po, w.prefix_slots);
+  return launch_after_prep(rows_join_kernel<MODE, N, 1>, (unsigned)w.tiles, N * 32, 0, s, a, ps, ow, pb, po, w.prefix_slots);
 }
 
 }  // namespace
 
 int64_t rows_window_workspace(int B, int H, int64_t total_q, int max_blocks, int window, int n_sink) {
   const int64_t keys = window_keys(max_blocks, window, n_sink);
-  return wide(B, H, total_q) ? layout_of<32>(B, H, total_q, keys).bytes : layout_of<16>(B, H, total_q, keys).bytes;
+  return wide(B, H, total_q) ? layout_of<32>(B, H, total_q, keys, -1).bytes : layout_of<16>(B, H, total_q, keys, -1).bytes;
 }
 cudaError_t launch_rows_window(const ChunkArgs& a, void* workspace, cudaStream_t s) {
   const int64_t keys = window_keys(a.max_blocks, a.window, a.n_sink);
-  return wide(a.B, a.H, a.total_q) ? launch<kWindow, 32>(a, layout_of<32>(a.B, a.H, a.total_q, keys), workspace, s)
-                                   : launch<kWindow, 16>(a, layout_of<16>(a.B, a.H, a.total_q, keys), workspace, s);
+  return wide(a.B, a.H, a.total_q) ? launch<kWindow, 32>(a, layout_of<32>(a.B, a.H, a.total_q, keys, -1), workspace, s)
+                                   : launch<kWindow, 16>(a, layout_of<16>(a.B, a.H, a.total_q, keys, -1), workspace, s);
+}
+
+int64_t rows_shared_workspace(int B, int H, int64_t total_q, int max_blocks, int G) {
+  const int64_t keys = all_keys(max_blocks);
+  const int g = may_share(B, H, total_q, G) ? G : -1;
+  return wide(B, H, total_q) ? layout_of<32>(B, H, total_q, keys, g).bytes : layout_of<16>(B, H, total_q, keys, g).bytes;
+}
+cudaError_t launch_rows_shared(const ChunkArgs& a, void* workspace, cudaStream_t s) {
+  const int64_t keys = all_keys(a.max_blocks);
+  const bool w32 = wide(a.B, a.H, a.total_q);
+  if (!may_share(a.B, a.H, a.total_q, a.G))
+    return w32 ? launch<kPlain, 32>(a, layout_of<32>(a.B, a.H, a.total_q, keys, -1), workspace, s)
+               : launch<kPlain, 16>(a, layout_of<16>(a.B, a.H, a.total_q, keys, -1), workspace, s);
+  return w32 ? launch<kShared, 32>(a, layout_of<32>(a.B, a.H, a.total_q, keys, a.G), workspace, s)
+             : launch<kShared, 16>(a, layout_of<16>(a.B, a.H, a.total_q, keys, a.G), workspace, s);
 }
 
 }  // namespace kv8

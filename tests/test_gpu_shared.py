@@ -35,6 +35,22 @@ def check(c, causal=True, lse=True):
     return out, l
 
 
+def run_with(c, shared_len, group_start=None):
+    old = c.shared_len, c.group_start
+    c.shared_len, c.group_start = shared_len, old[1] if group_start is None else group_start
+    try:
+        return run(c)
+    finally:
+        c.shared_len, c.group_start = old
+
+
+def check_with(c, shared_len):
+    out, l, err = run_with(c, shared_len)
+    assert err == 0
+    c.check(out, l)
+    return out, l
+
+
 def chunk(c, causal=True):
     l = torch.full(c.q_lat.shape[:2], 7.0, device="cuda")
     out = torch.full((*c.q_lat.shape[:2], DL), 7.0, dtype=torch.bfloat16, device="cuda")
@@ -93,6 +109,21 @@ def test_many_sequences_in_many_groups():
     check(SharedCase(4, [1] * 300, lens, [5] * 60, [490] * 60, seed=7), lse=False)
 
 
+@pytest.mark.parametrize("H", [1, 4, 16, 17, 20, 32, 64])
+def test_single_tokens_behind_a_long_prefix(H):
+    """Prefix and rest are different kernels' parts, cut by the borders of either's ranges."""
+    lens = [5000 + (613 * i) % 1500 for i in range(40)]
+    check(SharedCase(H, [1] * 40, lens, [25, 15], [4999, 3000], seed=H, pad=2))
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_few_rows_in_groups_of_every_kind(causal):
+    """Groups that share and that do not, sequences without queries, some with several tokens, some in none."""
+    nq = [1, 0, 2, 1, 1, 1, 0, 0, 3, 1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 0, 4, 1, 1]
+    lens = [800, 900, 801, 1000, 850, 900, 640, 0, 700, 70, 64, 1, 128] + [2000 + 65 * i for i in range(11)]
+    check(SharedCase(16, nq, lens, [5, 4, 4, 8], [790, 640, 60, 1990], seed=30, pad=7), causal)
+
+
 def test_a_prefix_is_computed_once():
     """The other members' entries for it are not looked up where sharing pays."""
     c = SharedCase(16, [1] * 16, [2000] * 16, [16], [1984], seed=8)
@@ -105,23 +136,27 @@ def test_a_prefix_is_computed_once():
 @pytest.mark.parametrize("groups", [[0, 3, 2, 8], [-1, 4, 8, 8], [0, 4, 8, 9], [5, 4, 3, 2]])
 def test_groups_that_cannot_be_are_told_and_share_nothing(groups):
     c = SharedCase(16, [1] * 8, [900] * 8, [8], [850], seed=9)
-    want = chunk(c)
+    c.group_start = torch.zeros(4, dtype=torch.int32, device="cuda")
+    c.shared_len = torch.zeros(3, dtype=torch.int32, device="cuda")
+    want = check(c)
     c.group_start = torch.tensor(groups, dtype=torch.int32, device="cuda")
     c.shared_len = torch.tensor([850] * 3, dtype=torch.int32, device="cuda")
     out, l, err = run(c)
     assert err == -5 and torch.equal(out, want[0]) and torch.equal(l, want[1])
 
 
-def test_a_negative_length_is_told_and_shares_nothing():
-    c = SharedCase(16, [1] * 8, [900] * 8, [8], [850], seed=10)
-    want = chunk(c)
-    c.shared_len.fill_(-5)
-    out, l, err = run(c)
+@pytest.mark.parametrize("B", [2, 8])
+def test_a_negative_length_is_told_and_shares_nothing(B):
+    c = SharedCase(4, [1] * B, [900] * B, [B], [850], seed=10)
+    shared = c.shared_len.clone()
+    want = check_with(c, shared * 0)
+    out, l, err = run_with(c, shared * 0 - 5)
     assert err == -5 and torch.equal(out, want[0]) and torch.equal(l, want[1])
+    assert run_with(c, shared, c.group_start + 1)[2] == -5
 
 
 def test_without_groups_the_bits_of_chunk_attention():
-    c = SharedCase(16, [1, 40, 3], [900, 300, 70], [], [], seed=11, pad=4)
+    c = SharedCase(128, [1, 40, 3], [900, 300, 70], [], [], seed=11, pad=4)
     out, l, err = run(c)
     want = chunk(c)
     assert err == 0 and torch.equal(out, want[0]) and torch.equal(l, want[1])
@@ -130,11 +165,13 @@ def test_without_groups_the_bits_of_chunk_attention():
 def test_a_bad_query_range_is_told():
     """Its sequence has no query, the group shares nothing, and the others are right."""
     c = SharedCase(16, [1] * 6, [900] * 6, [6], [850], seed=12)
-    want = chunk(c)
     c.start[3] = 10 ** 6
     out, l, err = run(c)
     assert err == -5
-    assert torch.equal(out[:2], want[0][:2]) and torch.equal(out[4:], want[0][4:])
+    c.start[3] = 3
+    for b in (0, 1, 4, 5):
+        ref, ref_l, tol, tol_l = c.reference(b)
+        assert ((out[b: b + 1].double() - ref).abs() <= tol).all() and ((l[b: b + 1] - ref_l).abs() <= tol_l).all()
 
 
 def test_nan_in_the_prefix_and_in_one_sequence():
