@@ -123,7 +123,14 @@ def _is_device(t) -> bool:
     return t.is_cuda
 
 
+_Tensor, _BF16, _F32, _I32, _U8 = torch.Tensor, torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
+
 def _need(t, name, dtype, ndim=None, device=True):
+    # (what is right is found to be so at once: a call's checks are most of its time on the host)
+    if (isinstance(t, _Tensor) and t.dtype is dtype and t.is_contiguous() and (ndim is None or t.dim() == ndim)
+            and (not device or _is_device(t))):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -138,9 +145,10 @@ def _need(t, name, dtype, ndim=None, device=True):
 
 def _need_cache(kv_codes, kv_scales):
     """The cache: codes uint8 [slots, 576] and their row scales f32 [slots, 2]."""
-    _need(kv_codes, "kv_codes", torch.uint8, 2)
-    _need(kv_scales, "kv_scales", torch.float32, 2)
-    if kv_codes.shape[1] != KV8_D or tuple(kv_scales.shape) != (kv_codes.shape[0], 2):
+    _need(kv_codes, "kv_codes", _U8, 2)
+    _need(kv_scales, "kv_scales", _F32, 2)
+    slots, width = kv_codes.shape
+    if width != KV8_D or kv_scales.shape != (slots, 2):
         raise ValueError("kv_codes must be [slots,576] and kv_scales [slots,2]")
 
 
@@ -214,9 +222,9 @@ def kv8_produce_rows(src, norm_weight, eps, positions, rope_cos, rope_sin, kv_co
 _ROW_TYPES = {torch.bfloat16: KV8_BF16, torch.float16: KV8_F16, torch.float32: KV8_F32}
 
 
-def _row_stride(t):
+def _row_stride(t, shape):
     """Elements between the rows of a 2-D tensor (its width for a single row, whose stride says nothing)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return t.stride(0) if shape[0] > 1 else shape[1]
 
 
 def kv8_norm_quantize_rows(x, norm_weight, eps, residual=None, residual_out=None, normed=None, codes=None,
@@ -225,41 +233,45 @@ def kv8_norm_quantize_rows(x, norm_weight, eps, residual=None, residual_out=None
     (f32 [n, 1], or [n, ceil(width / group)] with a scale for every `group` channels) of y.  x [n, width]
     is bf16, f16 or f32; residual_out takes t and normed takes y in that type.  Rows may be strided.
     Returns (codes, scales)."""
-    if not (isinstance(x, torch.Tensor) and x.dtype in _ROW_TYPES and _is_device(x) and x.dim() == 2
-            and x.shape[1] >= 1 and (x.stride(1) == 1 or x.shape[1] == 1)):
+    dtype = x.dtype if isinstance(x, _Tensor) else None
+    if not (dtype in _ROW_TYPES and _is_device(x) and x.dim() == 2 and x.shape[1] >= 1
+            and (x.stride(1) == 1 or x.shape[1] == 1)):
         raise ValueError("x must be a CUDA bfloat16, float16 or float32 [n, width] tensor with unit column stride")
-    n, width = x.shape
-    for t, name, dtype in ((residual, "residual", x.dtype), (residual_out, "residual_out", x.dtype),
-                           (normed, "normed", x.dtype), (codes, "codes", torch.uint8)):
+    shape = n, width = x.shape
+    args = [x.data_ptr(), _row_stride(x, shape)]
+    for t, name, want in ((residual, "residual", dtype), (residual_out, "residual_out", dtype),
+                          (normed, "normed", dtype), (codes, "codes", _U8)):
         if t is None:
+            args += (None, 0)
             continue
-        if not (isinstance(t, torch.Tensor) and t.dtype == dtype and _is_device(t) and t.shape == (n, width)
+        if not (isinstance(t, _Tensor) and t.dtype is want and _is_device(t) and t.shape == shape
                 and (t.stride(1) == 1 or width == 1)):
-            raise ValueError(f"{name} must be a CUDA {dtype} [{n}, {width}] tensor with unit column stride")
+            raise ValueError(f"{name} must be a CUDA {want} [{n}, {width}] tensor with unit column stride")
+        args += (t.data_ptr(), _row_stride(t, shape))
     if residual_out is not None and residual is None:
         raise ValueError("residual_out needs residual")
-    _need(norm_weight, "norm_weight", torch.float32, 1)
-    if norm_weight.shape[0] != width:
+    _need(norm_weight, "norm_weight", _F32, 1)
+    if norm_weight.numel() != width:
         raise ValueError("norm_weight must have one entry per column of x")
-    group = int(group)
     if group not in (0, 32, 64, 128, 256):
         raise ValueError("group must be 0, 32, 64, 128 or 256")
     groups = -(-width // group) if group else 1
-    if codes is None or scales is None:
+    if codes is None:
         with _allocating(stream):
-            codes = torch.empty((n, width), dtype=torch.uint8, device=x.device) if codes is None else codes
-            scales = torch.empty((n, groups), dtype=torch.float32, device=x.device) if scales is None else scales
-    _need(scales, "scales", torch.float32, 2)
+            codes = torch.empty((n, width), dtype=torch.uint8, device=x.device)
+        args[8:] = codes.data_ptr(), width
+    if scales is None:
+        with _allocating(stream):
+            scales = torch.empty((n, groups), dtype=torch.float32, device=x.device)
+    _need(scales, "scales", _F32, 2)
     if scales.shape != (n, groups):
         raise ValueError(f"scales must be [{n}, {groups}]")
     with _on_device_of(x, residual, residual_out, norm_weight, normed, codes, scales):
         st = lib().kv8_norm_quantize_rows(
-            _ptr(x), _row_stride(x), _ptr(residual), 0 if residual is None else _row_stride(residual),
-            _ptr(residual_out), 0 if residual_out is None else _row_stride(residual_out), _ptr(norm_weight),
-            float(eps), n, width, _ROW_TYPES[x.dtype], group, _ptr(normed),
-            0 if normed is None else _row_stride(normed), _ptr(codes), _row_stride(codes), _ptr(scales),
-            _stream(stream))
-    _check("kv8_norm_quantize_rows", st)
+            *args[:6], norm_weight.data_ptr(), float(eps), n, width, _ROW_TYPES[dtype], int(group), *args[6:],
+            scales.data_ptr(), _stream(stream))
+    if st != 0:
+        raise Kv8Error("kv8_norm_quantize_rows", st)
     return codes, scales
 
 
@@ -484,11 +496,13 @@ def mla_absorb_decode_fp8_batch_noalloc(q_lat, q_rope, kv_codes, kv_scales, bloc
     return out
 
 
-def _strides(t):
-    """Element strides of the first two dimensions (0 for one of size 1, whose stride says nothing)."""
-    a, b = t.stride()[:2]
-    rows, heads = t.shape[:2]
-    return a if rows > 1 else 0, b if heads > 1 else 0
+def _strides(t, shape=None):
+    """Element strides of the first two dimensions (0 for one of size 1, whose stride says nothing); with
+    the shape given, all of a 3-D tensor's."""
+    if shape is None:
+        return _strides(t, t.shape)[:2]
+    a, b, c = t.stride()
+    return a if shape[0] > 1 else 0, b if shape[1] > 1 else 0, c
 
 
 _AS_IS = contextlib.nullcontext()
@@ -510,8 +524,24 @@ def _on_device_of(first, *others):
 
 
 # ----------------------------------------------------------------- chunks of new tokens
+_sizes = {}
+
+
+def _size(name, *args) -> int:
+    """A workspace size of the library's, which follows from the sizes alone: asked for once."""
+    L = lib()
+    if L is not _lib:
+        return getattr(L, name)(*args)
+    n = _sizes.get((name, args))
+    if n is None:
+        if len(_sizes) >= 4096:
+            _sizes.clear()
+        n = _sizes[name, args] = getattr(L, name)(*args)
+    return n
+
+
 def mla_absorb_chunk_fp8_batch_workspace_size(B: int, H: int, total_q: int, max_blocks: int) -> int:
-    n = lib().mla_absorb_chunk_fp8_batch_workspace_size(int(B), int(H), int(total_q), int(max_blocks))
+    n = _size("mla_absorb_chunk_fp8_batch_workspace_size", int(B), int(H), int(total_q), int(max_blocks))
     if n < 0:
         raise ValueError("invalid B, H, total_q or max_blocks")
     return int(n)
@@ -519,15 +549,16 @@ def mla_absorb_chunk_fp8_batch_workspace_size(B: int, H: int, total_q: int, max_
 
 def mla_absorb_window_fp8_batch_workspace_size(B: int, H: int, total_q: int, max_blocks: int, window: int,
                                                n_sink: int) -> int:
-    n = lib().mla_absorb_window_fp8_batch_workspace_size(int(B), int(H), int(total_q), int(max_blocks),
-                                                         int(window), int(n_sink))
+    n = _size("mla_absorb_window_fp8_batch_workspace_size", int(B), int(H), int(total_q), int(max_blocks),
+              int(window), int(n_sink))
     if n < 0:
         raise ValueError("invalid B, H, total_q, max_blocks, window or n_sink")
     return int(n)
 
 
 def mla_absorb_shared_fp8_batch_workspace_size(B: int, H: int, total_q: int, max_blocks: int, G: int) -> int:
-    n = lib().mla_absorb_shared_fp8_batch_workspace_size(int(B), int(H), int(total_q), int(max_blocks), int(G))
+    n = _size("mla_absorb_shared_fp8_batch_workspace_size", int(B), int(H), int(total_q), int(max_blocks),
+              int(G))
     if n < 0:
         raise ValueError("invalid B, H, total_q, max_blocks or G")
     return int(n)
@@ -538,46 +569,55 @@ def _chunk_call(fn, size, own, q_lat, q_rope, kv_codes, kv_scales, block_table, 
     """The checks and the call of an attention of new tokens over the paged cache: `size` are the arguments
     of its workspace size, and `own` those of its call, that it does not share with the others (`also`:
     the tensors among them)."""
+    strides = []
     for t, name, width in ((q_lat, "q_lat", KV8_DL), (q_rope, "q_rope", KV8_DR)):
-        if not (isinstance(t, torch.Tensor) and t.dtype == torch.bfloat16 and _is_device(t)
-                and t.dim() == 3 and t.shape[2] == width and t.stride(2) == 1):
-            raise ValueError(f"{name} must be a CUDA bfloat16 [total_q, H, {width}] tensor with unit "
-                             "stride in its last dimension")
+        shape = t.shape if isinstance(t, _Tensor) and t.dtype is _BF16 and _is_device(t) else ()
+        if len(shape) == 3 and shape[2] == width:
+            token, head, one = _strides(t, shape)
+            if one == 1:
+                strides.append((token, head, shape))
+                continue
+        raise ValueError(f"{name} must be a CUDA bfloat16 [total_q, H, {width}] tensor with unit "
+                         "stride in its last dimension")
     _need_cache(kv_codes, kv_scales)
-    _need(block_table, "block_table", torch.int32, 2)
-    _need(seq_lens, "seq_lens", torch.int32, 1)
-    _need(q_start, "q_start", torch.int32, 1)
-    rows, H, _ = q_lat.shape
+    _need(block_table, "block_table", _I32, 2)
+    _need(seq_lens, "seq_lens", _I32, 1)
+    _need(q_start, "q_start", _I32, 1)
+    (lat_token, lat_head, (rows, H, _)), (rope_token, rope_head, rope) = strides
     B, max_blocks = block_table.shape
-    if q_rope.shape[0] != rows or q_rope.shape[1] != H:
+    if rope[0] != rows or rope[1] != H:
         raise ValueError("q_lat must be [total_q,H,512] and q_rope [total_q,H,64]")
-    if seq_lens.shape[0] != B or q_start.shape[0] != B + 1:
+    if seq_lens.numel() != B or q_start.numel() != B + 1:
         raise ValueError("seq_lens needs one entry per row of block_table, and q_start one more")
     if out is None:
         with _allocating(stream):
             out = torch.empty((rows, H, KV8_DL), dtype=torch.bfloat16, device=q_lat.device)
     else:
-        _need(out, "out", torch.bfloat16, 3)
+        _need(out, "out", _BF16, 3)
         if out.shape != (rows, H, KV8_DL):
             raise ValueError("out must be [total_q,H,512]")
     if lse is not None:
-        _need(lse, "lse", torch.float32, 2)
+        _need(lse, "lse", _F32, 2)
         if lse.shape != (rows, H):
             raise ValueError("lse must be [total_q,H]")
     need = globals()[fn + "_workspace_size"](B, H, rows, max_blocks, *size)
     if workspace is None:
         with _allocating(stream):
             workspace = alloc_workspace(need, q_lat.device)
-    _need_workspace(workspace)
+    else:
+        _need_workspace(workspace)
+        need = workspace.numel() * workspace.element_size()
+    block_size = int(block_size)
     with _on_device_of(q_lat, q_rope, kv_codes, kv_scales, block_table, seq_lens, q_start, out, lse,
                        workspace, *also):
         st = getattr(lib(), fn)(
-            _ptr(q_lat), *_strides(q_lat), _ptr(q_rope), *_strides(q_rope), _ptr(kv_codes),
-            _ptr(kv_scales), _ptr(block_table), _ptr(seq_lens), _ptr(q_start), rows, B, H, max_blocks,
-            int(block_size), int(kv_codes.shape[0] // block_size), *own,
-            float(sm_scale), _ptr(out), _ptr(lse), _ptr(workspace),
-            workspace.numel() * workspace.element_size(), _stream(stream))
-    _check(fn, st)
+            q_lat.data_ptr(), lat_token, lat_head, q_rope.data_ptr(), rope_token, rope_head,
+            kv_codes.data_ptr(), kv_scales.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+            q_start.data_ptr(), rows, B, H, max_blocks, block_size, kv_codes.shape[0] // block_size, *own,
+            float(sm_scale), out.data_ptr(), None if lse is None else lse.data_ptr(),
+            workspace.data_ptr(), need, _stream(stream))
+    if st != 0:
+        raise Kv8Error(fn, st)
     return out
 
 
