@@ -222,11 +222,6 @@ def kv8_produce_rows(src, norm_weight, eps, positions, rope_cos, rope_sin, kv_co
 _ROW_TYPES = {torch.bfloat16: KV8_BF16, torch.float16: KV8_F16, torch.float32: KV8_F32}
 
 
-def _row_stride(t, shape):
-    """Elements between the rows of a 2-D tensor (its width for a single row, whose stride says nothing)."""
-    return t.stride(0) if shape[0] > 1 else shape[1]
-
-
 def kv8_norm_quantize_rows(x, norm_weight, eps, residual=None, residual_out=None, normed=None, codes=None,
                            scales=None, group=0, stream=None):
     """t = x + residual; y = RMS norm of t times norm_weight; codes (e4m3 as uint8 [n, width]) and scales
@@ -238,7 +233,8 @@ def kv8_norm_quantize_rows(x, norm_weight, eps, residual=None, residual_out=None
             and (x.stride(1) == 1 or x.shape[1] == 1)):
         raise ValueError("x must be a CUDA bfloat16, float16 or float32 [n, width] tensor with unit column stride")
     shape = n, width = x.shape
-    args = [x.data_ptr(), _row_stride(x, shape)]
+    d = x.get_device()
+    args = [x.data_ptr(), x.stride(0) if n > 1 else width]
     for t, name, want in ((residual, "residual", dtype), (residual_out, "residual_out", dtype),
                           (normed, "normed", dtype), (codes, "codes", _U8)):
         if t is None:
@@ -247,7 +243,9 @@ def kv8_norm_quantize_rows(x, norm_weight, eps, residual=None, residual_out=None
         if not (isinstance(t, _Tensor) and t.dtype is want and _is_device(t) and t.shape == shape
                 and (t.stride(1) == 1 or width == 1)):
             raise ValueError(f"{name} must be a CUDA {want} [{n}, {width}] tensor with unit column stride")
-        args += (t.data_ptr(), _row_stride(t, shape))
+        if t.get_device() != d:
+            raise ValueError("all tensors must be on the same device")
+        args += (t.data_ptr(), t.stride(0) if n > 1 else width)
     if residual_out is not None and residual is None:
         raise ValueError("residual_out needs residual")
     _need(norm_weight, "norm_weight", _F32, 1)
@@ -266,7 +264,9 @@ def kv8_norm_quantize_rows(x, norm_weight, eps, residual=None, residual_out=None
     _need(scales, "scales", _F32, 2)
     if scales.shape != (n, groups):
         raise ValueError(f"scales must be [{n}, {groups}]")
-    with _on_device_of(x, residual, residual_out, norm_weight, normed, codes, scales):
+    if norm_weight.get_device() != d or scales.get_device() != d:
+        raise ValueError("all tensors must be on the same device")
+    with _device(d):
         st = lib().kv8_norm_quantize_rows(
             *args[:6], norm_weight.data_ptr(), float(eps), n, width, _ROW_TYPES[dtype], int(group), *args[6:],
             scales.data_ptr(), _stream(stream))
@@ -496,13 +496,11 @@ def mla_absorb_decode_fp8_batch_noalloc(q_lat, q_rope, kv_codes, kv_scales, bloc
     return out
 
 
-def _strides(t, shape=None):
-    """Element strides of the first two dimensions (0 for one of size 1, whose stride says nothing); with
-    the shape given, all of a 3-D tensor's."""
-    if shape is None:
-        return _strides(t, t.shape)[:2]
-    a, b, c = t.stride()
-    return a if shape[0] > 1 else 0, b if shape[1] > 1 else 0, c
+def _strides(t):
+    """Element strides of the first two dimensions (0 for one of size 1, whose stride says nothing)."""
+    rows, heads, _ = t.shape
+    a, b, _ = t.stride()
+    return a if rows > 1 else 0, b if heads > 1 else 0
 
 
 _AS_IS = contextlib.nullcontext()
@@ -514,13 +512,22 @@ def _allocating(stream):
     return torch.cuda.stream(stream) if isinstance(stream, torch.cuda.Stream) else _AS_IS
 
 
-def _on_device_of(first, *others):
+def _device(d):
     """The device of a call's tensors, made current for it (its launch, its default stream)."""
+    return torch.cuda.device(d) if d >= 0 and d != torch.cuda.current_device() else _AS_IS
+
+
+def _same_device(first, *others):
     d = first.get_device()
     for t in others:
         if t is not None and t.get_device() != d:
             raise ValueError("all tensors must be on the same device")
-    return torch.cuda.device(d) if d >= 0 and d != torch.cuda.current_device() else _AS_IS
+    return d
+
+
+def _on_device_of(first, *others):
+    """The device that a call's tensors share, as _device()."""
+    return _device(_same_device(first, *others))
 
 
 # ----------------------------------------------------------------- chunks of new tokens
@@ -564,58 +571,90 @@ def mla_absorb_shared_fp8_batch_workspace_size(B: int, H: int, total_q: int, max
     return int(n)
 
 
+def _chunk_checks(q_lat, q_rope, kv_codes, kv_scales, block_table, seq_lens, q_start, out, lse, workspace, also):
+    """The checks of an attention of new tokens over the paged cache, one by one: what is wrong is told."""
+    for t, name, width in ((q_lat, "q_lat", KV8_DL), (q_rope, "q_rope", KV8_DR)):
+        if not (isinstance(t, torch.Tensor) and t.dtype == torch.bfloat16 and _is_device(t)
+                and t.dim() == 3 and t.shape[2] == width and t.stride(2) == 1):
+            raise ValueError(f"{name} must be a CUDA bfloat16 [total_q, H, {width}] tensor with unit "
+                             "stride in its last dimension")
+    _need_cache(kv_codes, kv_scales)
+    _need(block_table, "block_table", torch.int32, 2)
+    _need(seq_lens, "seq_lens", torch.int32, 1)
+    _need(q_start, "q_start", torch.int32, 1)
+    rows, H, _ = q_lat.shape
+    B = block_table.shape[0]
+    if q_rope.shape[0] != rows or q_rope.shape[1] != H:
+        raise ValueError("q_lat must be [total_q,H,512] and q_rope [total_q,H,64]")
+    if seq_lens.shape[0] != B or q_start.shape[0] != B + 1:
+        raise ValueError("seq_lens needs one entry per row of block_table, and q_start one more")
+    if out is not None:
+        _need(out, "out", torch.bfloat16, 3)
+        if out.shape != (rows, H, KV8_DL):
+            raise ValueError("out must be [total_q,H,512]")
+    if lse is not None:
+        _need(lse, "lse", torch.float32, 2)
+        if lse.shape != (rows, H):
+            raise ValueError("lse must be [total_q,H]")
+    if workspace is not None:
+        _need_workspace(workspace)
+    _same_device(q_lat, q_rope, kv_codes, kv_scales, block_table, seq_lens, q_start, out, lse, workspace, *also)
+
+
 def _chunk_call(fn, size, own, q_lat, q_rope, kv_codes, kv_scales, block_table, seq_lens, q_start, sm_scale,
                 out, lse, workspace, block_size, stream, also=()):
     """The checks and the call of an attention of new tokens over the paged cache: `size` are the arguments
     of its workspace size, and `own` those of its call, that it does not share with the others (`also`:
     the tensors among them)."""
-    strides = []
-    for t, name, width in ((q_lat, "q_lat", KV8_DL), (q_rope, "q_rope", KV8_DR)):
-        shape = t.shape if isinstance(t, _Tensor) and t.dtype is _BF16 and _is_device(t) else ()
-        if len(shape) == 3 and shape[2] == width:
-            token, head, one = _strides(t, shape)
-            if one == 1:
-                strides.append((token, head, shape))
-                continue
-        raise ValueError(f"{name} must be a CUDA bfloat16 [total_q, H, {width}] tensor with unit "
-                         "stride in its last dimension")
-    _need_cache(kv_codes, kv_scales)
-    _need(block_table, "block_table", _I32, 2)
-    _need(seq_lens, "seq_lens", _I32, 1)
-    _need(q_start, "q_start", _I32, 1)
-    (lat_token, lat_head, (rows, H, _)), (rope_token, rope_head, rope) = strides
+    d, right = -1, False
+    try:  # the checks at once: they are most of a call's time on the host
+        d = q_lat.get_device()
+        rows, H, _ = q_lat.shape
+        B = seq_lens.numel()
+        right = (
+            d >= 0 and q_lat.shape == (rows, H, 512) and q_lat.dtype is _BF16 and q_lat.stride(2) == 1
+            and q_rope.shape == (rows, H, 64) and q_rope.dtype is _BF16 and q_rope.stride(2) == 1
+            and q_rope.get_device() == d
+            and kv_codes.dtype is _U8 and kv_codes.is_contiguous() and kv_codes.get_device() == d
+            and kv_codes.shape == (kv_codes.shape[0], 576) and kv_scales.shape == (kv_codes.shape[0], 2)
+            and kv_scales.dtype is _F32 and kv_scales.is_contiguous() and kv_scales.get_device() == d
+            and block_table.dtype is _I32 and block_table.is_contiguous() and block_table.get_device() == d
+            and block_table.dim() == 2 and block_table.shape[0] == B
+            and seq_lens.dtype is _I32 and seq_lens.dim() == 1 and seq_lens.is_contiguous()
+            and seq_lens.get_device() == d
+            and q_start.dtype is _I32 and q_start.shape == (B + 1,) and q_start.is_contiguous()
+            and q_start.get_device() == d
+            and (out is None or (out.dtype is _BF16 and out.shape == (rows, H, 512) and out.is_contiguous()
+                                 and out.get_device() == d))
+            and (lse is None or (lse.dtype is _F32 and lse.shape == (rows, H) and lse.is_contiguous()
+                                 and lse.get_device() == d))
+            and (workspace is None or (workspace.is_contiguous() and workspace.get_device() == d)))
+        for t in also:
+            right = right and t.get_device() == d
+    except (AttributeError, TypeError, ValueError):
+        right = False
+    if not right:
+        _chunk_checks(q_lat, q_rope, kv_codes, kv_scales, block_table, seq_lens, q_start, out, lse, workspace,
+                      also)
+        rows, H, _ = q_lat.shape
     B, max_blocks = block_table.shape
-    if rope[0] != rows or rope[1] != H:
-        raise ValueError("q_lat must be [total_q,H,512] and q_rope [total_q,H,64]")
-    if seq_lens.numel() != B or q_start.numel() != B + 1:
-        raise ValueError("seq_lens needs one entry per row of block_table, and q_start one more")
-    if out is None:
+    need = _size(fn + "_workspace_size", B, H, rows, max_blocks, *size)
+    if need < 0:
+        globals()[fn + "_workspace_size"](B, H, rows, max_blocks, *size)  # (raises, in its words)
+    if out is None or workspace is None:
         with _allocating(stream):
-            out = torch.empty((rows, H, KV8_DL), dtype=torch.bfloat16, device=q_lat.device)
-    else:
-        _need(out, "out", _BF16, 3)
-        if out.shape != (rows, H, KV8_DL):
-            raise ValueError("out must be [total_q,H,512]")
-    if lse is not None:
-        _need(lse, "lse", _F32, 2)
-        if lse.shape != (rows, H):
-            raise ValueError("lse must be [total_q,H]")
-    need = globals()[fn + "_workspace_size"](B, H, rows, max_blocks, *size)
-    if workspace is None:
-        with _allocating(stream):
-            workspace = alloc_workspace(need, q_lat.device)
-    else:
-        _need_workspace(workspace)
-        need = workspace.numel() * workspace.element_size()
+            if out is None:
+                out = torch.empty((rows, H, KV8_DL), dtype=torch.bfloat16, device=q_lat.device)
+            if workspace is None:
+                workspace = alloc_workspace(need, q_lat.device)
     block_size = int(block_size)
-    with _on_device_of(q_lat, q_rope, kv_codes, kv_scales, block_table, seq_lens, q_start, out, lse,
-                       workspace, *also):
+    with _device(d):
         st = getattr(lib(), fn)(
-            q_lat.data_ptr(), lat_token, lat_head, q_rope.data_ptr(), rope_token, rope_head,
+            q_lat.data_ptr(), *_strides(q_lat), q_rope.data_ptr(), *_strides(q_rope),
             kv_codes.data_ptr(), kv_scales.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
             q_start.data_ptr(), rows, B, H, max_blocks, block_size, kv_codes.shape[0] // block_size, *own,
             float(sm_scale), out.data_ptr(), None if lse is None else lse.data_ptr(),
-            workspace.data_ptr(), need, _stream(stream))
+            workspace.data_ptr(), workspace.nbytes, _stream(stream))
     if st != 0:
         raise Kv8Error(fn, st)
     return out
