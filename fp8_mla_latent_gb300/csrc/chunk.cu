@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const ChunkArgs a, Plan<Geo>
   if (threadIdx.x == 0) *a.err = 0;
   __syncthreads();
   if constexpr (MODE == kShared) make_entries<Geo, 1>(a, &plan->part_rows, tmp, true);
-  make_plan<MODE>(a, plan, base, MODE == kShared ? a.G + a.B : a.B, clusters, tmp,
+  make_plan<MODE>(a, plan, base, 0, MODE == kShared ? a.G + a.B : a.B, clusters, tmp,
                   MODE == kShared ? a.unit : nullptr, nullptr);
 }
 
@@ -273,6 +273,17 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   grid_dependency_wait();  // the plan
+  if constexpr (MODE == kShared) {
+    // The kernel for few rows runs beside this one: it begins behind the word below, which it reads once and
+    // finds set, since this word is everywhere before any of this block's threads lets that kernel come.
+    if (blockIdx.x == 0) {
+      if (threadIdx.x == 0) {
+        store_release(&ws.plan->ready, 1u);
+        __threadfence();
+      }
+      __syncthreads();
+    }
+  }
   grid_dependents_launch();  // (the join kernel may come as soon as there is room)
   const bool work = k < ws.plan->n;
   Way<MODE> w;

@@ -41,6 +41,15 @@ struct WideGeo {
   static constexpr int SWITCH = 6;
 };
 
+__device__ __forceinline__ void store_release(unsigned* p, unsigned v) {
+  asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+__device__ __forceinline__ unsigned load_acquire(const unsigned* p) {
+  unsigned v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
 // Plan of range k: its first row tile (sequence b, row tile rt, nt key tiles of
 // which off come before the range), the unit where the range starts and its units.
 struct PlanEntry {
@@ -49,7 +58,9 @@ struct PlanEntry {
 };
 template <class G>
 struct Plan {
-  int64_t n, units, tiles, part_rows;  // ranges, their units, row tiles, rows that have parts (shared prefixes)
+  int64_t n, units, tiles;   // ranges, their units, row tiles
+  int64_t part_rows;         // (shared prefixes) rows that have parts
+  unsigned ready;            // (and in the prefixes' plan) whether the plans are made
   PlanEntry e[G::RANGES];
 };
 
@@ -290,16 +301,16 @@ __device__ __forceinline__ void make_entries(const ChunkArgs& a, int64_t* part_r
 // owner[p] of row tile p: its sequence, its place there, the slot of its first part -- slot 2 k is the first
 // segment of range k, 2 k + 1 its last -- and the last range that it lies in.
 //
-// One CTA of 1024 threads: row tiles before each of n_seq sequences (base), the units of every row tile, their
-// total, and the row tile that each range starts in; with `unit`, the units before each row tile, and
+// One CTA of 1024 threads: row tiles before each of n_seq sequences (base), which are the call's from `first` on
+// (or the entries), the units of every row tile, their total, and the row tile that each range starts in; with `unit`, the units before each row tile, and
 // with `owner`, whose it is (below).
 template <int MODE, class G>
-__device__ __forceinline__ void make_plan(const ChunkArgs& a, Plan<G>* plan, int64_t* base, int n_seq, int most,
+__device__ __forceinline__ void make_plan(const ChunkArgs& a, Plan<G>* plan, int64_t* base, int first, int n_seq, int most,
                                           int64_t* tmp, int64_t* unit, int4* owner) {
   int64_t pairs = 0;
   for (int b0 = 0; b0 < n_seq; b0 += 1024) {
     const int b = b0 + threadIdx.x;
-    const int64_t n = b < n_seq ? row_tiles<G>(a, seq_info<MODE>(a, b, true)) : 0;
+    const int64_t n = b < n_seq ? row_tiles<G>(a, seq_info<MODE>(a, first + b, true)) : 0;
     int64_t sum;
     const int64_t inc = plan_sum(n, tmp, &sum);
     if (b < n_seq) base[b] = pairs + inc - n;
@@ -315,7 +326,7 @@ __device__ __forceinline__ void make_plan(const ChunkArgs& a, Plan<G>* plan, int
       const int mid = (lo + hi) >> 1;
       if (base[mid] <= p) lo = mid; else hi = mid;
     }
-    b = lo;
+    b = first + lo;
     rt = (int)(p - base[lo]);
     Pages<MODE> pages;
     return key_tiles<G>(a, seq_info<MODE>(a, b, false), rt, &pages);
@@ -343,7 +354,7 @@ __device__ __forceinline__ void make_plan(const ChunkArgs& a, Plan<G>* plan, int
     if (unit != nullptr && p < pairs) unit[p] = before;
     int64_t k = n > 0 ? S * nc / total : nc;
     while (k < nc && k * total / nc < S) ++k;
-    int64_t first = k - 1;  // the range that holds its first unit: one from before, or the last that begins there
+    int64_t held = k - 1;  // the range that holds its first unit: one from before, or the last that begins there
     bool before_it = true;
     for (; k < nc; ++k) {
       const int64_t x = k * total / nc;
@@ -355,9 +366,9 @@ __device__ __forceinline__ void make_plan(const ChunkArgs& a, Plan<G>* plan, int
       e.off = (int32_t)(x - S > G::SWITCH ? x - S - G::SWITCH : 0);
       e.x = before + e.off;
       plan->e[k] = e;
-      if (e.off == 0) first = k, before_it = false;
+      if (e.off == 0) held = k, before_it = false;
     }
-    if (owner != nullptr && p < pairs) owner[p] = make_int4(b, rt, (int)(2 * first + before_it), (int)(k - 1));
+    if (owner != nullptr && p < pairs) owner[p] = make_int4(b, rt, (int)(2 * held + before_it), (int)(k - 1));
     at += sum;
   }
 }

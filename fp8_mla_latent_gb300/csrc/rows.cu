@@ -142,9 +142,12 @@ struct Parts {
   }
 };
 
+// kShared: the kernel of the prefixes is launched before this one, which runs beside it on the SMs that the
+// plans leave it.  What this one needs of earlier launches are the plans, behind the word `ready`; it waits for
+// that kernel when its own work is done, so that the join, which waits for this one, has both's parts.
 template <int MODE, int N>
 __global__ void __launch_bounds__(NTHREADS, 1)
-    rows_kernel(const ChunkArgs a, const Parts<N> ps, const __grid_constant__ CUtensorMap kmap,
+    rows_kernel(const ChunkArgs a, const Parts<N> ps, unsigned* ready, const __grid_constant__ CUtensorMap kmap,
                 const __grid_constant__ CUtensorMap rmap, const __grid_constant__ CUtensorMap smap) {
   using C = Cfg<N>;
   constexpr int NB = C::NB, STREAMS = C::STREAMS, RL = C::RL, RR = C::RR, NS = C::NS, S_COLS = C::S_COLS, T_O = C::T_O,
@@ -183,10 +186,17 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  grid_dependency_wait();    // the plan
+  bool ready_plan = true;
+  if constexpr (MODE == kShared) {
+    // (no wait: the kernel of the prefixes sets it before it lets this one come)
+    ready_plan = __syncthreads_and(load_acquire(ready) != 0u);
+    if (!ready_plan && threadIdx.x == 0) fail();
+  } else {
+    grid_dependency_wait();  // the plan
+  }
   grid_dependents_launch();
   Way<MODE, N> w;
-  if (k < ps.plan->n) w.start(a, *ps.plan, k);
+  if (ready_plan && k < ps.plan->n) w.start(a, *ps.plan, k);
   else w.left = 0;
   int gt = 0;  // key tiles of the range before this segment
 
@@ -744,9 +754,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == W_MMA) tmem_dealloc(tmem, 512);
+  if constexpr (MODE == kShared) grid_dependency_wait();
 }
 
-// ------------------------------------------------------------------ plan
 constexpr int PLAN_NEAR = 4096;
 
 // (base: in shared memory if it fits)
@@ -759,30 +769,50 @@ __global__ void __launch_bounds__(1024) rows_plan_kernel(const ChunkArgs a, Plan
   if (threadIdx.x == 0) *a.err = 0;
   __syncthreads();
   if (MODE == kPlain && a.G > 0) (void)groups_bad(a, true);  // (groups too small to share anything)
-  make_plan<MODE>(a, plan, a.B < PLAN_NEAR ? near : base, a.B, most, tmp, nullptr, owner);
+  make_plan<MODE>(a, plan, a.B < PLAN_NEAR ? near : base, 0, a.B, most, tmp, nullptr, owner);
 }
 
-// The plans of a call with shared prefixes, each with entries of its own: block 0 that of the prefixes (whose
-// base the join reads), block 1 that of the sequences.  (COST: 12.4 thousand cycles of an SM for a
-// prefix's unit, against 3.2 or 4.3 here.)
+// The plans of a call with shared prefixes, each with a copy of the entries of its own, one behind the other:
+// block 0 that of the prefixes (whose base the join reads), block 1 that of the sequences.  The device's
+// clusters are divided by what the two cost (COST: 12.4 thousand cycles of an SM for a prefix's unit,
+// against 3.2 or 4.3 for one of few rows).
 template <int N>
-__global__ void __launch_bounds__(1024) rows_shared_plan_kernel(ChunkArgs a, Plan<Geo<N>>* plan, int64_t* base,
+__global__ void __launch_bounds__(1024) rows_shared_plan_kernel(const ChunkArgs a, Plan<Geo<N>>* plan, int64_t* base,
                                                                 int4* owner, int most, Plan<WideGeo>* prefix_plan,
                                                                 int64_t* prefix_base, int4* prefix_owner,
-                                                                int prefix_most) {
+                                                                int prefix_most, int clusters) {
   grid_dependents_launch();
+  constexpr int COST = N == 16 ? 4 : 3;
   __shared__ int64_t tmp[32];
   __shared__ int64_t near[PLAN_NEAR];
   const bool own = blockIdx.x == 1;
   if (own && threadIdx.x == 0) *a.err = 0;
   __syncthreads();
-  if (own) a.entries += a.G + a.B;
-  make_entries<Geo<N>, N == 16 ? 4 : 3>(a, own ? &plan->part_rows : &prefix_plan->part_rows, tmp, own);
+  ChunkArgs c = a;
+  if (own) c.entries += a.G + a.B;
+  make_entries<Geo<N>, COST>(c, own ? &plan->part_rows : &prefix_plan->part_rows, tmp, own);
+  // (row tiles times the last one's key tiles: as much as the division needs)
+  auto cost = [&](int first, int n, int rows, int start) -> int64_t {
+    int64_t mine = 0, sum;
+    for (int i = threadIdx.x; i < n; i += 1024) {
+      const int4 u = c.entries[first + i].u;
+      mine += ((int64_t)u.y * a.H + rows - 1) / rows * ((u.z + TILE - 1) / TILE + start);
+    }
+    (void)plan_sum(mine, tmp, &sum);
+    return sum;
+  };
+  const int64_t wide = cost(0, a.G, WideGeo::ROWS, WideGeo::SWITCH) * COST, few = cost(a.G, a.B, N, Geo<N>::SWITCH);
+  int64_t split = wide + few > 0 ? (clusters * wide + (wide + few) / 2) / (wide + few) : 0;
+  if (wide > 0 && split < 1) split = 1;
+  if (split > prefix_most) split = prefix_most;
+  if (split > clusters - 1) split = clusters - 1;
   if (own) {
-    a.entries += a.G;
-    make_plan<kShared>(a, plan, a.B < PLAN_NEAR ? near : base, a.B, most, tmp, nullptr, owner);
+    const int64_t left = NUM_SMS - 4 * split;
+    make_plan<kShared>(a, plan, a.B < PLAN_NEAR ? near : base, 2 * a.G + a.B, a.B, most < left ? most : (int)left, tmp,
+                       nullptr, owner);
   } else {
-    make_plan<kShared>(a, prefix_plan, prefix_base, a.G, prefix_most, tmp, nullptr, prefix_owner);
+    if (threadIdx.x == 0) prefix_plan->ready = 0u;
+    make_plan<kShared>(a, prefix_plan, prefix_base, 0, a.G, (int)split, tmp, nullptr, prefix_owner);
   }
 }
 
@@ -813,7 +843,7 @@ __global__ void __launch_bounds__(N * 32) rows_join_kernel(const ChunkArgs a, co
   if constexpr (MODE == kShared) {
     if (shares) {
       const int g = a.entries[of.x].v.w;
-      const ChunkEntry e = a.entries[g - a.G];
+      const ChunkEntry e = a.entries[g];
       const int64_t in_group = (s.q0 - e.u.x) * a.H + r;
       pf = prefix_owner[prefix_base[g] + in_group / WideGeo::ROWS];
       prefix_k0 = pf.z >> 1;
@@ -965,6 +995,7 @@ cudaError_t launch(ChunkArgs a, const Layout& w, void* workspace, cudaStream_t s
   d.scales = a.scales;
   d.block_table = a.block_table;
   d.n_blocks = a.n_blocks;
+  unsigned* ready = nullptr;
   CUtensorMap kmap, rmap, smap;
   if ((e = make_cache_map(d, &kmap)) != cudaSuccess || (e = make_rc_map(d, &rmap)) != cudaSuccess ||
       (e = make_scale_map(d, &smap)) != cudaSuccess)
@@ -977,16 +1008,16 @@ cudaError_t launch(ChunkArgs a, const Layout& w, void* workspace, cudaStream_t s
     a.part_rows = w.part_rows;
     Plan<WideGeo>* prefix_plan = reinterpret_cast<Plan<WideGeo>*>(p + OFF_PREFIX_PLAN);
     rows_shared_plan_kernel<N><<<2, 1024, 0, s>>>(a, ps.plan, base, owner, w.most, prefix_plan, prefix_base, prefix_owner,
-                                                  clusters);
+                                                  clusters, fit);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     e = launch_prefixes(a, PrefixParts{prefix_plan, m, l, o, w.prefix_slots + w.slots}, clusters, kmap, rmap, smap, s);
     if (e != cudaSuccess) return e;
-    a.entries += a.G + a.B + a.G;  // the sequences, of the second plan's copy
+    ready = &prefix_plan->ready;
   } else {
     rows_plan_kernel<MODE, N><<<1, 1024, 0, s>>>(a, ps.plan, base, owner, w.most);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  e = launch_after_prep(rows_kernel<MODE, N>, w.most, NTHREADS, Cfg<N>::SMEM, s, a, ps, kmap, rmap, smap);
+  e = launch_after_prep(rows_kernel<MODE, N>, w.most, NTHREADS, Cfg<N>::SMEM, s, a, ps, ready, kmap, rmap, smap);
   if (e != cudaSuccess || (MODE != kShared && w.most == 1)) return e;
   const int64_t* pb = prefix_base;
   const int4 *ow = owner, *po = prefix_owner;
