@@ -24,6 +24,7 @@ STATUS = {0: "KV8_OK", -1: "KV8_EINVAL", -2: "KV8_EALIGN", -3: "KV8_EUNSUPPORTED
           -4: "KV8_ECUDA", -5: "KV8_EBOUNDS", -6: "KV8_EWORKSPACE", -7: "KV8_ETIMEOUT",
           -8: "KV8_ESCRATCH", -9: "KV8_EIO", -10: "KV8_EFORMAT"}
 KV8_BF16, KV8_F16, KV8_F32, KV8_NORM_MAX_WIDTH = 0, 1, 2, 32768
+KV8_SHARE_AUTO, KV8_SHARE_ALWAYS = 0, 1
 KV8_PAGES_EINDEX, KV8_PAGES_ENOROOM, KV8_PAGES_ETIMEOUT = 1, 2, 4  # bits of the pages' err_word
 
 _lock = threading.Lock()
@@ -78,7 +79,7 @@ def lib() -> ctypes.CDLL:
                                                       i32, i32, i32, i64, i32, i32, f32, P, P, P, i64, P]),
                 "mla_absorb_shared_fp8_batch_workspace_size": (i64, [i32, i32, i64, i32, i32]),
                 "mla_absorb_shared_fp8_batch": (i32, [P, i64, i64, P, i64, i64, P, P, P, P, P, i64, i32,
-                                                      i32, i32, i32, i64, P, P, i32, i32, f32, P, P, P,
+                                                      i32, i32, i32, i64, P, P, i32, i32, i32, f32, P, P, P,
                                                       i64, P]),
                 "kv8_pages_append": (i32, [P, P, P, i32, i32, i64, P, P, P, i64, P, P]),
                 "kv8_pages_fork": (i32, [P, P, P, i32, i32, i64, P, P, P, i32, P, P, P, P]),
@@ -688,17 +689,18 @@ def mla_absorb_window_fp8_batch(q_lat, q_rope, kv_codes, kv_scales, block_table,
 
 def mla_absorb_shared_fp8_batch(q_lat, q_rope, kv_codes, kv_scales, block_table, seq_lens, q_start,
                                 sm_scale, group_start, shared_len, causal=True, out=None, lse=None,
-                                workspace=None, block_size=KV8_BLOCK, stream=None):
+                                workspace=None, block_size=KV8_BLOCK, stream=None, share=KV8_SHARE_AUTO):
     """mla_absorb_chunk_fp8_batch where sequences group_start[g]..group_start[g+1]-1 share their first
     shared_len[g] tokens, the whole pages of them by the same table entries: computed once for the
-    group.  group_start int32 [G+1], shared_len int32 [G]."""
+    group, where that is faster (or, with share=KV8_SHARE_ALWAYS, wherever it can be).  group_start int32
+    [G+1], shared_len int32 [G]."""
     _need(group_start, "group_start", torch.int32, 1)
     _need(shared_len, "shared_len", torch.int32, 1)
     G = shared_len.shape[0]
     if group_start.shape[0] != G + 1:
         raise ValueError("group_start must have one entry more than shared_len")
     return _chunk_call("mla_absorb_shared_fp8_batch", (G,),
-                       (_ptr(group_start), _ptr(shared_len), G, int(bool(causal))), q_lat, q_rope, kv_codes,
+                       (_ptr(group_start), _ptr(shared_len), G, int(share), int(bool(causal))), q_lat, q_rope, kv_codes,
                        kv_scales, block_table, seq_lens, q_start, sm_scale, out, lse, workspace, block_size,
                        stream, (group_start, shared_len))
 

@@ -615,8 +615,9 @@ int mla_absorb_shared_fp8_batch(const uint16_t* q_lat, int64_t q_lat_token_strid
                                 const int32_t* q_start, int64_t total_q, int B, int H,
                                 int max_blocks, int block_size, int64_t n_blocks,
                                 const int32_t* group_start, const int32_t* shared_len, int G,
-                                int causal, float sm_scale, uint16_t* out, float* lse,
+                                int share, int causal, float sm_scale, uint16_t* out, float* lse,
                                 void* workspace, int64_t workspace_bytes, void* stream) {
+  if (share != KV8_SHARE_AUTO && share != KV8_SHARE_ALWAYS) return KV8_EINVAL;
   ChunkArgs a;
   const int64_t need = mla_absorb_shared_fp8_batch_workspace_size(B, H, total_q, max_blocks, G);
   const int st = chunk_args(a, need, q_lat, q_lat_token_stride, q_lat_head_stride, q_rope,
@@ -629,6 +630,7 @@ int mla_absorb_shared_fp8_batch(const uint16_t* q_lat, int64_t q_lat_token_strid
   a.group_start = group_start;
   a.shared_len = shared_len;
   a.G = G;
+  a.share = share;
   return told(launch_shared(a, workspace, static_cast<cudaStream_t>(stream)));
 }
 

@@ -185,8 +185,8 @@ __global__ void __launch_bounds__(1024) plan_kernel(const ChunkArgs a, Plan<Geo>
   }
   if (threadIdx.x == 0) *a.err = 0;
   __syncthreads();
-  if constexpr (MODE == kShared) make_entries<Geo, 1>(a, &plan->part_rows, tmp, true);
-  make_plan<MODE>(a, plan, base, 0, MODE == kShared ? a.G + a.B : a.B, clusters, tmp,
+  if constexpr (MODE == kShared) (void)make_entries<Geo>(a, &plan->part_rows, tmp, true);
+  make_plan<MODE>(a, plan, base, 0, 0, MODE == kShared ? a.G + a.B : a.B, clusters, tmp,
                   MODE == kShared ? a.unit : nullptr, nullptr);
 }
 

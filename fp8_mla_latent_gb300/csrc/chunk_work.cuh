@@ -180,13 +180,22 @@ __device__ __forceinline__ int64_t plan_sum(int64_t v, int64_t* tmp, int64_t* to
 // parts (f32 o, l and M_g of every row), which the join adds up; a sequence that shares nothing
 // is as in a call without groups.
 //
-// The prefix is whole pages that every row of the group sees; a group takes part where its row tiles
+// The prefix is whole pages that every row of the group sees; a group may take part where its row tiles
 // are fewer together than apart by more than the parts cost: SHARE key tiles a row tile (6 for its start, and
 // 256 rows of f32 written twice and read twice), and where its sequences have PART_ROWS rows on average
 // at most (above, they fill their row tiles, and little is saved).  G is the geometry of what the
-// sequences would be computed with otherwise, COST of whose (row tile, key tile) pairs take an SM as long as
-// one of a prefix.
+// sequences would be computed with otherwise.
 constexpr int PART_ROWS = 1024, SHARE = 16;
+// Whether the groups that may do, by what the call costs with and without them:
+// - in row tiles of 256, WORTH units have to be saved in all (two tokens of 128 heads over 16384 keys save 122
+//   and are 11 us slower; four save 244: 55 against 57; 32 over 4000 keys 400: 74 against 87);
+// - else in cycles: a unit is NARROW of an SM's, or WIDE of a cluster's; what a call takes besides is START,
+//   or START_WIDE and what the join and the plans take longer, JOIN_MORE.  (us, shared and apart: 64 tokens of 16
+//   heads over a prefix of 16384 keys 67 and 120, of 2000 keys 44 and 39; 8 over 16384 54 and 43; 32 x
+//   up to 4 tokens over 8000 keys 59 and 70.)
+constexpr int WORTH = 300, WIDE_CYCLES = 3100, START = 16000, START_WIDE = 42000, JOIN_MORE = 12000;
+template <class G>
+constexpr int NARROW = G::ROWS == 16 ? 3200 : 4300;
 
 __device__ __forceinline__ int64_t warp_sum(int64_t v) {
 #pragma unroll
@@ -215,8 +224,15 @@ __device__ __forceinline__ bool groups_bad(const ChunkArgs& a, bool tell) {
   return bad;
 }
 
-template <class G, int COST>
-__device__ __forceinline__ void make_entries(const ChunkArgs& a, int64_t* part_rows, int64_t* tmp, bool tell) {
+// (By a whole CTA of 1024 threads.)  The result: the clusters that the prefixes get beside a kernel for few rows,
+// `most` at most of the `clusters` there are.
+template <class G>
+__device__ __forceinline__ int make_entries(const ChunkArgs& a, int64_t* part_rows, int64_t* tmp, bool tell, int most = 0,
+                                            int clusters = 0) {
+  constexpr bool FEW = G::ROWS < WideGeo::ROWS;
+  __shared__ unsigned long long sums[2];  // units that the groups save, and those of their prefixes
+  if (threadIdx.x < 2) sums[threadIdx.x] = 0ull;
+
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int g = threadIdx.x; g < a.G; g += 1024) {
     a.entries[g].u = make_int4(0, 0, 0, 0);
@@ -228,7 +244,7 @@ __device__ __forceinline__ void make_entries(const ChunkArgs& a, int64_t* part_r
     a.entries[a.G + b].v = make_int4(0, a.causal, -1, 0);
   }
   if (threadIdx.x == 0) *part_rows = 0;
-  if (groups_bad(a, tell) || a.G == 0) return;  // (ranges that may overlap: nothing is shared)
+  if (groups_bad(a, tell) || a.G == 0) return 0;  // (ranges that may overlap: nothing is shared)
   // what each group would share, a warp per group
   for (int g = warp; g < a.G; g += 32) {
     const int f = __ldg(&a.group_start[g]), l = __ldg(&a.group_start[g + 1]);
@@ -254,13 +270,47 @@ __device__ __forceinline__ void make_entries(const ChunkArgs& a, int64_t* part_r
     members = warp_sum(members);
     P = P > 0 ? P / PAGE : 0;
     const int64_t rows = tokens * a.H, together = (rows + WideGeo::ROWS - 1) / WideGeo::ROWS, tiles = (P + 1) / 2;
-    const bool take = members > 1 && P > 0 && rows <= PART_ROWS * members && together * (tiles + SHARE) * COST < apart * tiles;
+    const bool take = members > 1 && P > 0 &&
+                      (a.share == KV8_SHARE_ALWAYS ||
+                       (rows <= PART_ROWS * members &&
+                        together * (tiles + SHARE) * 4 * WIDE_CYCLES < apart * tiles * (FEW ? NARROW<G> : 4 * WIDE_CYCLES)));
     if (take && lane == 0) {
+      atomicAdd(&sums[0], (unsigned long long)(apart * tiles));
+      atomicAdd(&sums[1], (unsigned long long)(together * (tiles + WideGeo::SWITCH)));
       a.entries[g].u = make_int4((int)q0, (int)tokens, (int)P * PAGE, (int)row);
       a.entries[g].v = make_int4(0, 0, 0, 0);
     }
   }
   __syncthreads();
+  int split = 0;
+  {
+    const int64_t saved = (int64_t)sums[0], wide = (int64_t)sums[1];
+    if (saved == 0) return 0;
+    bool worth = saved - wide > WORTH;
+    if constexpr (FEW) {
+      int64_t mine = 0, all;
+      for (int b = threadIdx.x; b < a.B; b += 1024) {
+        const int4 u = a.entries[a.G + b].u;
+        mine += ((int64_t)u.y * a.H + G::ROWS - 1) / G::ROWS * ((u.z + TILE - 1) / TILE + G::SWITCH);
+      }
+      (void)plan_sum(mine, tmp, &all);
+      const int64_t apart = all * NARROW<G> / NUM_SMS + START;
+      int64_t best = INT64_MAX;
+      for (int t = 1 + lane; t <= most && t < clusters; t += 32) {
+        const int64_t x = wide * WIDE_CYCLES / t + START_WIDE, y = (all - saved) * NARROW<G> / (NUM_SMS - 4 * t) + START;
+        const int64_t z = ((x > y ? x : y) + JOIN_MORE) * 64 + t;  // (t < 64)
+        best = z < best ? z : best;
+      }
+      best = warp_min(best);
+      worth = best / 64 < apart;
+      split = (int)(best % 64);
+    }
+    if (!worth && a.share != KV8_SHARE_ALWAYS) {
+      for (int g = threadIdx.x; g < a.G; g += 1024) a.entries[g].u.y = 0;
+      __syncthreads();
+      return 0;
+    }
+  }
   // the rows of their parts, as far as there is room
   int64_t at = 0;
   for (int g0 = 0; g0 < a.G; g0 += 1024) {
@@ -296,17 +346,19 @@ __device__ __forceinline__ void make_entries(const ChunkArgs& a, int64_t* part_r
     }
   }
   __syncthreads();
+  return split;
 }
 
 // owner[p] of row tile p: its sequence, its place there, the slot of its first part -- slot 2 k is the first
 // segment of range k, 2 k + 1 its last -- and the last range that it lies in.
 //
-// One CTA of 1024 threads: row tiles before each of n_seq sequences (base), which are the call's from `first` on
-// (or the entries), the units of every row tile, their total, and the row tile that each range starts in; with `unit`, the units before each row tile, and
-// with `owner`, whose it is (below).
+// One CTA of 1024 threads: row tiles before each of n_seq sequences (base), the units of every row tile, their
+// total, and the row tile that each range starts in; with `unit`, the units before each row tile, and
+// with `owner`, whose it is.  (The sequences are the call's, or entries, from `first` on, and `shift` further on
+// for who reads the plan.)
 template <int MODE, class G>
-__device__ __forceinline__ void make_plan(const ChunkArgs& a, Plan<G>* plan, int64_t* base, int first, int n_seq, int most,
-                                          int64_t* tmp, int64_t* unit, int4* owner) {
+__device__ __forceinline__ void make_plan(const ChunkArgs& a, Plan<G>* plan, int64_t* base, int first, int shift, int n_seq,
+                                          int most, int64_t* tmp, int64_t* unit, int4* owner) {
   int64_t pairs = 0;
   for (int b0 = 0; b0 < n_seq; b0 += 1024) {
     const int b = b0 + threadIdx.x;
@@ -360,7 +412,7 @@ __device__ __forceinline__ void make_plan(const ChunkArgs& a, Plan<G>* plan, int
       const int64_t x = k * total / nc;
       if (x >= S + len) break;
       PlanEntry e;
-      e.b = b;
+      e.b = b + shift;
       e.rt = rt;
       e.nt = (int32_t)n;
       e.off = (int32_t)(x - S > G::SWITCH ? x - S - G::SWITCH : 0);
@@ -368,7 +420,7 @@ __device__ __forceinline__ void make_plan(const ChunkArgs& a, Plan<G>* plan, int
       plan->e[k] = e;
       if (e.off == 0) held = k, before_it = false;
     }
-    if (owner != nullptr && p < pairs) owner[p] = make_int4(b, rt, (int)(2 * held + before_it), (int)(k - 1));
+    if (owner != nullptr && p < pairs) owner[p] = make_int4(b + shift, rt, (int)(2 * held + before_it), (int)(k - 1));
     at += sum;
   }
 }

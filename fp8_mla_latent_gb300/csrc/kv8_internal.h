@@ -206,7 +206,7 @@ struct ChunkArgs {
   // sequences that share prefixes: G groups of consecutive ones; the rest lies in the workspace
   const int32_t* group_start;  // [G + 1]
   const int32_t* shared_len;   // [G]
-  int G;
+  int G, share;                // (a kv8_share)
   ChunkEntry* entries;         // [G + B] the prefixes, the sequences
   int64_t* unit;               // [row tiles + 1] units before each
   int2* part_seq;              // group and sequence of the tokens that have parts, or nullptr

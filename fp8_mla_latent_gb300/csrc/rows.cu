@@ -155,6 +155,17 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   extern __shared__ __align__(1024) uint8_t sm[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int k = (int)blockIdx.x;
+  if constexpr (MODE == kShared) {
+    // (no wait: the kernel of the prefixes sets it before it lets this one come)
+    const bool there = load_acquire(ready) != 0u;
+    if (!there && threadIdx.x == 0) atomicOr(a.err, ERR_TIMEOUT);
+    if (!__syncthreads_and(there && k < ps.plan->n)) {  // nothing to do
+      grid_dependents_launch();
+      grid_dependency_wait();
+      return;
+    }
+    grid_dependents_launch();
+  }
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::OFF_FLAGS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + C::OFF_FLAGS + 4);
@@ -186,17 +197,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  bool ready_plan = true;
-  if constexpr (MODE == kShared) {
-    // (no wait: the kernel of the prefixes sets it before it lets this one come)
-    ready_plan = __syncthreads_and(load_acquire(ready) != 0u);
-    if (!ready_plan && threadIdx.x == 0) fail();
-  } else {
+  if constexpr (MODE != kShared) {
     grid_dependency_wait();  // the plan
+    grid_dependents_launch();
   }
-  grid_dependents_launch();
   Way<MODE, N> w;
-  if (ready_plan && k < ps.plan->n) w.start(a, *ps.plan, k);
+  if (k < ps.plan->n) w.start(a, *ps.plan, k);
   else w.left = 0;
   int gt = 0;  // key tiles of the range before this segment
 
@@ -769,50 +775,39 @@ __global__ void __launch_bounds__(1024) rows_plan_kernel(const ChunkArgs a, Plan
   if (threadIdx.x == 0) *a.err = 0;
   __syncthreads();
   if (MODE == kPlain && a.G > 0) (void)groups_bad(a, true);  // (groups too small to share anything)
-  make_plan<MODE>(a, plan, a.B < PLAN_NEAR ? near : base, 0, a.B, most, tmp, nullptr, owner);
+  make_plan<MODE>(a, plan, a.B < PLAN_NEAR ? near : base, 0, 0, a.B, most, tmp, nullptr, owner);
 }
 
 // The plans of a call with shared prefixes, each with a copy of the entries of its own, one behind the other:
-// block 0 that of the prefixes (whose base the join reads), block 1 that of the sequences.  The device's
-// clusters are divided by what the two cost (COST: 12.4 thousand cycles of an SM for a prefix's unit,
-// against 3.2 or 4.3 for one of few rows).
+// block 0 that of the prefixes (whose base the join reads), block 1 that of the sequences.  (The entries are
+// worked on in shared memory if they fit.)
+constexpr int ENTRIES_NEAR = 1024, SHARED_NEAR = 1024;
+
 template <int N>
 __global__ void __launch_bounds__(1024) rows_shared_plan_kernel(const ChunkArgs a, Plan<Geo<N>>* plan, int64_t* base,
                                                                 int4* owner, int most, Plan<WideGeo>* prefix_plan,
                                                                 int64_t* prefix_base, int4* prefix_owner,
                                                                 int prefix_most, int clusters) {
   grid_dependents_launch();
-  constexpr int COST = N == 16 ? 4 : 3;
   __shared__ int64_t tmp[32];
-  __shared__ int64_t near[PLAN_NEAR];
+  __shared__ int64_t near[SHARED_NEAR];
+  __shared__ ChunkEntry entries_near[ENTRIES_NEAR];
   const bool own = blockIdx.x == 1;
+  const int n = a.G + a.B;
   if (own && threadIdx.x == 0) *a.err = 0;
   __syncthreads();
+  ChunkEntry* entries = a.entries + (own ? n : 0);
   ChunkArgs c = a;
-  if (own) c.entries += a.G + a.B;
-  make_entries<Geo<N>, COST>(c, own ? &plan->part_rows : &prefix_plan->part_rows, tmp, own);
-  // (row tiles times the last one's key tiles: as much as the division needs)
-  auto cost = [&](int first, int n, int rows, int start) -> int64_t {
-    int64_t mine = 0, sum;
-    for (int i = threadIdx.x; i < n; i += 1024) {
-      const int4 u = c.entries[first + i].u;
-      mine += ((int64_t)u.y * a.H + rows - 1) / rows * ((u.z + TILE - 1) / TILE + start);
-    }
-    (void)plan_sum(mine, tmp, &sum);
-    return sum;
-  };
-  const int64_t wide = cost(0, a.G, WideGeo::ROWS, WideGeo::SWITCH) * COST, few = cost(a.G, a.B, N, Geo<N>::SWITCH);
-  int64_t split = wide + few > 0 ? (clusters * wide + (wide + few) / 2) / (wide + few) : 0;
-  if (wide > 0 && split < 1) split = 1;
-  if (split > prefix_most) split = prefix_most;
-  if (split > clusters - 1) split = clusters - 1;
+  c.entries = n <= ENTRIES_NEAR ? entries_near : entries;
+  const int split = make_entries<Geo<N>>(c, own ? &plan->part_rows : &prefix_plan->part_rows, tmp, own, prefix_most, clusters);
+  if (n <= ENTRIES_NEAR)
+    for (int i = threadIdx.x; i < n; i += 1024) entries[i] = entries_near[i];
   if (own) {
-    const int64_t left = NUM_SMS - 4 * split;
-    make_plan<kShared>(a, plan, a.B < PLAN_NEAR ? near : base, 2 * a.G + a.B, a.B, most < left ? most : (int)left, tmp,
-                       nullptr, owner);
+    const int left = NUM_SMS - 4 * split;
+    make_plan<kShared>(c, plan, a.B < SHARED_NEAR ? near : base, a.G, n, a.B, most < left ? most : left, tmp, nullptr, owner);
   } else {
     if (threadIdx.x == 0) prefix_plan->ready = 0u;
-    make_plan<kShared>(a, prefix_plan, prefix_base, 0, a.G, (int)split, tmp, nullptr, prefix_owner);
+    make_plan<kShared>(c, prefix_plan, prefix_base, 0, 0, a.G, split, tmp, nullptr, prefix_owner);
   }
 }
 
@@ -962,7 +957,8 @@ int64_t window_keys(int max_blocks, int64_t window, int64_t n_sink) {
 bool wide(int B, int H, int64_t total_q) { return total_q * H > 16 * (int64_t)B; }
 
 // Whether a call may have a prefix whose sharing pays: four clusters' worth of the sequences' row tiles.
-bool may_share(int B, int H, int64_t total_q, int G) {
+bool may_share(int B, int H, int64_t total_q, int G, int share) {
+  if (share == KV8_SHARE_ALWAYS) return G > 0 && B > 1;
   return G > 0 && B > 1 && total_q * H / (wide(B, H, total_q) ? 32 : 16) + B > 4;
 }
 
@@ -1040,13 +1036,13 @@ cudaError_t launch_rows_window(const ChunkArgs& a, void* workspace, cudaStream_t
 
 int64_t rows_shared_workspace(int B, int H, int64_t total_q, int max_blocks, int G) {
   const int64_t keys = all_keys(max_blocks);
-  const int g = may_share(B, H, total_q, G) ? G : -1;
+  const int g = may_share(B, H, total_q, G, KV8_SHARE_ALWAYS) ? G : -1;
   return wide(B, H, total_q) ? layout_of<32>(B, H, total_q, keys, g).bytes : layout_of<16>(B, H, total_q, keys, g).bytes;
 }
 cudaError_t launch_rows_shared(const ChunkArgs& a, void* workspace, cudaStream_t s) {
   const int64_t keys = all_keys(a.max_blocks);
   const bool w32 = wide(a.B, a.H, a.total_q);
-  if (!may_share(a.B, a.H, a.total_q, a.G))
+  if (!may_share(a.B, a.H, a.total_q, a.G, a.share))
     return w32 ? launch<kPlain, 32>(a, layout_of<32>(a.B, a.H, a.total_q, keys, -1), workspace, s)
                : launch<kPlain, 16>(a, layout_of<16>(a.B, a.H, a.total_q, keys, -1), workspace, s);
   return w32 ? launch<kShared, 32>(a, layout_of<32>(a.B, a.H, a.total_q, keys, a.G), workspace, s)

@@ -471,12 +471,15 @@ int mla_absorb_window_fp8_batch(const uint16_t* q_lat, int64_t q_lat_token_strid
  *                the whole pages of them.  0 shares nothing; less than 0 sets the error word
  *                (KV8_EBOUNDS) as well.
  *   G            >= 0 (with 0, group_start and shared_len may be NULL).
+ *   share        a kv8_share: KV8_SHARE_AUTO computes a prefix once where that is estimated to be
+ *                faster, KV8_SHARE_ALWAYS wherever it can (for up to 2^20 rows, and 1024 a sequence).
  *   workspace    >= mla_absorb_shared_fp8_batch_workspace_size(B, H, total_q, max_blocks, G) bytes.
- * What is computed once is whole pages that every row of the group sees, and only where that is
- * less work: the results are those of mla_absorb_chunk_fp8_batch within its precision in either
- * case.  Everything else is as there.
+ * What is computed once is whole pages that every row of the group sees.  Shared or not, the
+ * results are those of mla_absorb_chunk_fp8_batch within its precision, but not the same bits.
+ * Everything else is as there.
  * Errors: KV8_EINVAL, KV8_EALIGN, KV8_EUNSUPPORTED, KV8_EWORKSPACE, KV8_ECUDA.
  * ------------------------------------------------------------------------- */
+typedef enum { KV8_SHARE_AUTO = 0, KV8_SHARE_ALWAYS = 1 } kv8_share;
 int64_t mla_absorb_shared_fp8_batch_workspace_size(int B, int H, int64_t total_q, int max_blocks,
                                                    int G);
 int mla_absorb_shared_fp8_batch(const uint16_t* q_lat, int64_t q_lat_token_stride,
@@ -487,7 +490,7 @@ int mla_absorb_shared_fp8_batch(const uint16_t* q_lat, int64_t q_lat_token_strid
                                 const int32_t* q_start, int64_t total_q, int B, int H,
                                 int max_blocks, int block_size, int64_t n_blocks,
                                 const int32_t* group_start, const int32_t* shared_len, int G,
-                                int causal, float sm_scale, uint16_t* out, float* lse,
+                                int share, int causal, float sm_scale, uint16_t* out, float* lse,
                                 void* workspace, int64_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------

@@ -16,22 +16,27 @@ def workspace(c):
         len(c.nq), c.H, c.q_lat.shape[0], c.max_blocks, c.shared_len.numel()))
 
 
-def run(c, causal=True, lse=True, ws=None):
+ALWAYS, AUTO = pkg.KV8_SHARE_ALWAYS, pkg.KV8_SHARE_AUTO
+
+
+def run(c, causal=True, lse=True, ws=None, share=ALWAYS):
     rows = c.q_lat.shape[0]
     ws = workspace(c) if ws is None else ws
     out = torch.full((rows, c.H, DL), 7.0, dtype=torch.bfloat16, device="cuda")
     l = torch.full((rows, c.H), 7.0, device="cuda") if lse else None
     got = pkg.mla_absorb_shared_fp8_batch(*c.args(), SM_SCALE, c.group_start, c.shared_len, causal=causal, out=out,
-                                          lse=l, workspace=ws)
+                                          lse=l, workspace=ws, share=share)
     assert got is out
     return out, l, pkg.kv8_workspace_error(ws)
 
 
 def check(c, causal=True, lse=True):
-    out, l, err = run(c, causal, lse)
-    assert err == 0
-    c.check(out, l, causal)
-    assert (out[sum(c.nq):] == 7).all() and (l is None or (l[sum(c.nq):] == 7).all()), "rows behind the last"
+    """Where every prefix that can be is shared, and as the call decides by itself."""
+    for share in (AUTO, ALWAYS):
+        out, l, err = run(c, causal, lse, share=share)
+        assert err == 0
+        c.check(out, l, causal)
+        assert (out[sum(c.nq):] == 7).all() and (l is None or (l[sum(c.nq):] == 7).all()), "rows behind the last"
     return out, l
 
 
@@ -125,12 +130,22 @@ def test_few_rows_in_groups_of_every_kind(causal):
 
 
 def test_a_prefix_is_computed_once():
-    """The other members' entries for it are not looked up where sharing pays."""
-    c = SharedCase(16, [1] * 16, [2000] * 16, [16], [1984], seed=8)
-    want, want_l = check(c)
-    c.table[1:, :31] = 2 ** 30
-    out, l, err = run(c)
-    assert err == 0 and torch.equal(out, want) and torch.equal(l, want_l)
+    """The other members' entries for it are not looked up: wherever it can be, and where it is found to pay."""
+    for c, share in ((SharedCase(16, [1] * 16, [2000] * 16, [16], [1984], seed=8), ALWAYS),
+                     (SharedCase(128, [1] * 16, [2000] * 16, [16], [1984], seed=8), ALWAYS),
+                     (SharedCase(64, [1] * 24, [9000] * 24, [24], [8960], seed=8, rows=lambda b, t, g: torch.rand((t, 576)) - 0.5), AUTO)):
+        want, want_l, err = run(c, share=share)
+        assert err == 0
+        c.table[1:, : int(c.shared_len[0]) // PAGE] = 2 ** 30
+        out, l, err = run(c, share=share)
+        assert err == 0 and torch.equal(out, want) and torch.equal(l, want_l)
+
+
+def test_a_short_prefix_is_left_where_it_is():
+    """Too little to pay for a kernel more: the members' own entries are read."""
+    c = SharedCase(16, [1] * 6, [300] * 6, [6], [256], seed=31)
+    c.table[3, 1] = 2 ** 30
+    assert run(c, share=AUTO)[2] == -5 and run(c, share=ALWAYS)[2] == 0
 
 
 @pytest.mark.parametrize("groups", [[0, 3, 2, 8], [-1, 4, 8, 8], [0, 4, 8, 9], [5, 4, 3, 2]])
@@ -209,7 +224,8 @@ def test_captured_and_replayed_with_lengths_that_change():
     out, l = (torch.zeros_like(x) for x in check(c))
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
-        pkg.mla_absorb_shared_fp8_batch(*c.args(), SM_SCALE, c.group_start, c.shared_len, out=out, lse=l, workspace=ws)
+        pkg.mla_absorb_shared_fp8_batch(*c.args(), SM_SCALE, c.group_start, c.shared_len, out=out, lse=l, workspace=ws,
+                                        share=ALWAYS)
     for back in (5, 3, 0):
         c.lens.copy_(full - back)
         g.replay()
@@ -237,7 +253,7 @@ def test_fork_append_and_attend():
     q_lat = torch.randn((2 * n, H, 512), generator=g).bfloat16().cuda()
     q_rope = torch.randn((2 * n, H, 64), generator=g).bfloat16().cuda()
     args = (q_lat, q_rope, codes, scales, table, lens, start)
-    got = pkg.mla_absorb_shared_fp8_batch(*args, SM_SCALE, i32(1, n + 1), i32(T))
+    got = pkg.mla_absorb_shared_fp8_batch(*args, SM_SCALE, i32(1, n + 1), i32(T), share=ALWAYS)
     want = pkg.mla_absorb_chunk_fp8_batch(*args, SM_SCALE)
     # both are within 2^-9 + 3 2^-11 + 2^-8 (the weights, the rounding to bf16) of the exact value, up to
     # cancellation in the sum, which the largest magnitude stands for
