@@ -27,7 +27,6 @@ namespace {
 constexpr int NH = 8;                        // rows of a softmax warp
 constexpr int KBLK = TILE * 128;             // 16 KB: [128 tokens x 128 bytes]
 constexpr int RBLK = TILE * 64;              // 8 KB: [128 tokens x 64 bytes]
-constexpr int NTF = 4;                       // tiles loaded: barriers, row scales
 constexpr int W_TMA = 0, W_MMA = 1, W_CTX = 2, W_SOFT = 3;
 constexpr int N_SOFT = 16;                   // softmax warps: four, one per TMEM lane quarter, for 8 rows of a stream
 constexpr int NTHREADS = (W_SOFT + N_SOFT) * 32;
@@ -47,9 +46,10 @@ struct Cfg {
   static constexpr int NB = 2 * N;                     // columns: hi terms, lo terms
   static constexpr int STREAMS = N_SOFT / 4 / (N / NH);
   static constexpr int SET = N_SOFT / STREAMS;         // a stream's softmax warps
-  static constexpr int RL = N == 16 ? 11 : 9, RR = 2;  // rings of Lc blocks and Rc blocks
+  static constexpr int RL = N == 16 ? 11 : 10, RR = 2;  // rings of Lc blocks and Rc blocks
   static constexpr int NS = 2 * STREAMS;               // S buffers
-  static_assert(RL <= 12, "a block of tile i has the slot of tile i - 3 at the oldest: NTF tiles are told apart");
+  static constexpr int NTF = N == 16 ? 4 : 3;          // tiles loaded: barriers, row scales
+  static_assert(RL <= 4 * NTF, "tile i's first block has the slot of one of tile i - NTF's, or of a later tile's");
   static constexpr int B_TFULL = 0;                    // [NTF] a tile's Rc block and scales loaded
   static constexpr int B_LFULL = B_TFULL + NTF;        // [RL] an Lc block loaded
   static constexpr int B_LEMPTY = B_LFULL + RL;        // [RL] read by the context's MMAs
@@ -73,8 +73,8 @@ struct Cfg {
   static constexpr int OFF_WALK = OFF_RMAX + 1024;     // [16 warps] segments
   static constexpr int OFF_SCR = 4096;                 // [NTF][128][2] row scales
   static constexpr int OFF_Q = OFF_SCR + NTF * TILE * 8;        // [4 blocks][NB x 128 B], [NB x 64 B]
-  static constexpr int OFF_P = OFF_Q + 4 * NB * 128 + NB * 64;  // [2: even and odd tiles][NB x 128 tokens]
-  static constexpr int OFF_L = OFF_P + 2 * NB * 128;
+  static constexpr int OFF_P = OFF_Q + 4 * NB * 128 + NB * 64;  // [STREAMS][NB x 128 tokens]
+  static constexpr int OFF_L = OFF_P + STREAMS * NB * 128;
   static constexpr int OFF_R = OFF_L + RL * KBLK;
   static constexpr int SMEM = OFF_R + RR * RBLK;
   static constexpr int S_COLS = 2 * NB, T_O = NS * S_COLS, O_COLS = 4 * NB;
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     rows_kernel(const ChunkArgs a, const Parts<N> ps, unsigned* ready, const __grid_constant__ CUtensorMap kmap,
                 const __grid_constant__ CUtensorMap rmap, const __grid_constant__ CUtensorMap smap) {
   using C = Cfg<N>;
-  constexpr int NB = C::NB, STREAMS = C::STREAMS, RL = C::RL, RR = C::RR, NS = C::NS, S_COLS = C::S_COLS, T_O = C::T_O,
+  constexpr int NB = C::NB, STREAMS = C::STREAMS, RL = C::RL, RR = C::RR, NS = C::NS, NTF = C::NTF, S_COLS = C::S_COLS, T_O = C::T_O,
                 O_COLS = C::O_COLS;
   extern __shared__ __align__(1024) uint8_t sm[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             break;
           }
           if (blk == 0) {
-            // (tile g - 4's scales are read: its context's MMAs, which come behind its weights, have freed
+            // (tile g - NTF's scales are read: its context's MMAs, which come behind its weights, have freed
             // this block's slot or one before it)
             facts[tf] = (s0 >= 0 ? 1u : 0u) | (s1 >= 0 ? 2u : 0u);
             mbar_arrive_expect_tx_warp(tb, pages * (uint32_t)(2 * PAGE * 4 + PAGE * 64));
@@ -317,25 +317,23 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     for (; ok && w.more(); w.next(a)) {
       for (int i = 0; i < w.n; ++i) {
         const int g = gt + i, st = g % STREAMS, pbuf = g & 1;
-        if (!wait(C::B_PFULL + pbuf, (uint32_t)(g >> 1))) {
+        // (the blocks have long been there: their waits, for what they order, come before the one that counts)
+#pragma unroll 1
+        for (int m = 0; ok && m < 4; ++m) ok = wait_block(4 * g + m);
+        if (!ok || !wait(C::B_PFULL + pbuf, (uint32_t)(g >> 1))) {
           ok = false;
           break;
         }
-#pragma unroll 1
+        tc_fence_after();
+#pragma unroll
         for (int m = 0; m < 4; ++m) {
           const int ls = (4 * g + m) % RL;
-          if (!wait_block(4 * g + m)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             mma_f8_warp(tmem + T_O + st * O_COLS + m * NB, smem_desc(lring + ls * KBLK + kk * 4096, KBLK, 1024, SW128),
-                        smem_desc(pb + pbuf * NB * 128 + kk * 32, 16, 1024, SW128), id, (i >= STREAMS || kk > 0) ? 1u : 0u);
+                        smem_desc(pb + st * NB * 128 + kk * 32, 16, 1024, SW128), id, (i >= STREAMS || kk > 0) ? 1u : 0u);
           mma_commit_warp(&bars[C::B_LEMPTY + ls]);
         }
-        if (!ok) break;
         mma_commit_warp(&bars[C::B_ODONE + pbuf]);
       }
       gt += w.n;
@@ -593,16 +591,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           phi[h / 4] = (uint32_t)h01 | ((uint32_t)h23 << 16);
           plo[h / 4] = (uint32_t)l01 | ((uint32_t)l23 << 16);
         }
-        // the weights of tile g - 2 are read, and with two streams O is at rest
-        if (g > 1 && !wait(C::B_ODONE + (g & 1), (uint32_t)((g >> 1) - 1))) {
+        // the stream's tile before: its weights are read, and O is at rest
+        if (g >= STREAMS && !wait(C::B_ODONE + ((g - STREAMS) & 1), (uint32_t)((g - STREAMS) >> 1))) {
           ok = false;
           break;
         }
         if (moved && i >= STREAMS) {
-          if (STREAMS == 1 && !wait(C::B_ODONE + ((g - 1) & 1), (uint32_t)((g - 1) >> 1))) {
-            ok = false;
-            break;
-          }
           tc_fence_after();
           __syncwarp();
           float fh[NH];
@@ -636,7 +630,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             }
           }
         }
-        const uint32_t pb = smem_u32(sm + C::OFF_P) + (g & 1) * NB * 128;
+        const uint32_t pb = smem_u32(sm + C::OFF_P) + set * NB * 128;
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
           sts8(pb + p_off(hb + h), phi[h / 4] >> (8 * (h & 3)));
