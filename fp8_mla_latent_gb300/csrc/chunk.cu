@@ -134,7 +134,9 @@ constexpr int B_ODONE = B_RS + 4;            // [2 buffers][2] ranks 2, 3: a til
 constexpr int NRF = 4;
 constexpr int B_RF = B_ODONE + 4;            // [NRF] context: row factors of a finished row tile arrived
 constexpr int B_DRAIN = B_RF + NRF;          // every MMA done
-constexpr int NBAR = B_DRAIN + 1;
+constexpr int B_RFULL = B_DRAIN + 1;         // [2] solo score: Rc block loaded
+constexpr int B_REMPTY = B_RFULL + 2;        // [2] solo score: consumed
+constexpr int NBAR = B_REMPTY + 2;
 
 // shared memory (dynamic, 1024-byte aligned)
 constexpr int OFF_FLAGS = 512;               // tmem base, abort flag
@@ -158,6 +160,13 @@ constexpr int OFF_OP = OFF_P + 2 * P_STRIDE; // context: two operands (hi and lo
 constexpr int OFF_V = OFF_OP + 4 * OP_ATOM;
 constexpr int TOTAL_C = OFF_V + NVT * VTILE;
 constexpr int SMEM = TOTAL_S > TOTAL_C ? TOTAL_S : TOTAL_C;
+// Solo (one score and one context CTA): K as a ring of Lc blocks [128 tokens x 128 bytes] and two Rc blocks
+// behind it, V as the tile's two halves of 256 channels, each in a place of its own.
+constexpr int KBLK = 2 * BLK, NKB = 2 * NK;
+constexpr int OFF_KR = OFF_K + NKB * KBLK;
+constexpr int TOTAL_SOLO_S = OFF_KR + 2 * 2 * RBLK, TOTAL_SOLO_C = OFF_V + 4 * VBLK;
+constexpr int SMEM_SOLO = TOTAL_SOLO_S > TOTAL_SOLO_C ? TOTAL_SOLO_S : TOTAL_SOLO_C;
+static_assert(SMEM_SOLO <= 232448 && OFF_KR % 1024 == 0, "shared memory above the per-CTA limit");
 // TMEM columns of a score CTA
 constexpr int T_SL = 0, T_SR = 256, T_QH = 384;
 static_assert(NSC >= NK + 2 && NSC <= 8 && NVT <= 8 && OFF_FACTS + 32 <= OFF_XL, "rings");
@@ -166,9 +175,15 @@ static_assert(OFF_K % 1024 == 0 && KTILE % 1024 == 0 && OFF_V % 1024 == 0 && P_S
 static_assert(P_BYTES <= P_STRIDE && N_LANE_WARPS * 2048 <= 4 * OP_ATOM, "payload and staging");
 static_assert(SMEM <= 232448, "shared memory above the per-CTA limit");
 
+// The cluster of two CTAs is for sequences of 65 to 128 rows, whose row tiles are half of the others'.
+struct SoloGeo {
+  static constexpr int ROWS = CROWS, RANGES = NUM_SMS / 2, MIN_TILES = 2, SWITCH = 6;
+};
+template <bool SOLO>
+using GeoOf = typename std::conditional<SOLO, SoloGeo, WideGeo>::type;
 using Geo = WideGeo;
-template <int MODE>
-using Way = Walk<MODE, Geo>;
+template <int MODE, bool SOLO = false>
+using Way = Walk<MODE, GeoOf<SOLO>>;
 static_assert(sizeof(Way<kShared>) * N_LANE_WARPS <= OFF_SC - OFF_WALK && sizeof(Way<kWindow>) <= sizeof(Way<kShared>),
               "segments");
 
@@ -189,6 +204,15 @@ __global__ void __launch_bounds__(1024) plan_kernel(const ChunkArgs a, Plan<Geo>
   make_plan<MODE>(a, plan, base, 0, 0, MODE == kShared ? a.G + a.B : a.B, clusters, tmp,
                   MODE == kShared ? a.unit : nullptr, nullptr);
 }
+__global__ void __launch_bounds__(1024) solo_plan_kernel(const ChunkArgs a, Plan<SoloGeo>* plan, int64_t* base,
+                                                         int4* owner, int clusters) {
+  grid_dependents_launch();
+  __shared__ int64_t tmp[32];
+  __shared__ int64_t near[PLAN_NEAR];
+  if (threadIdx.x == 0) *a.err = 0;
+  __syncthreads();
+  make_plan<kWindow>(a, plan, a.B < PLAN_NEAR ? near : base, 0, 0, a.B, clusters, tmp, nullptr, owner);
+}
 
 // byte offset of 16-byte unit u (0..15) of row r in a payload: unit 4 s + i holds tokens
 // 32 s + 8 j + 2 i, + 1 for j = 0 .. 3
@@ -196,15 +220,17 @@ __device__ __forceinline__ uint32_t prow(int r, int u) {
   return (uint32_t)(r * 256 + ((u ^ (r & 7)) << 4));
 }
 
+template <bool SOLO = false>
 struct Workspace {
-  Plan<Geo>* plan;
+  static constexpr int ROWS = GeoOf<SOLO>::ROWS;
+  Plan<GeoOf<SOLO>>* plan;
   float* m;   // [2 MAX_CLUSTERS][256]: slot 2k the first segment of cluster k, 2k + 1 its last
   float* l;
   float* o;   // [..][256][512]
   int64_t parts;  // (shared prefixes) behind the slots: the parts of row tiles that one cluster held whole
   // where the parts of row `row` of a row tile go, as a row of these arrays
   template <int MODE>
-  __device__ __forceinline__ int64_t part_row(const Way<MODE>& w, int k, int row) const {
+  __device__ __forceinline__ int64_t part_row(const Way<MODE, SOLO>& w, int k, int row) const {
     if constexpr (MODE == kShared) {
       if (w.whole()) return parts + w.s.part + (int64_t)w.rt * ROWS + row;
     }
@@ -212,14 +238,28 @@ struct Workspace {
   }
 };
 
-template <int MODE>
-__global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
-    chunk_kernel(const ChunkArgs a, const Workspace ws, const __grid_constant__ CUtensorMap kmap,
+template <int MODE, bool SOLO = false>
+__global__ void __cluster_dims__(SOLO ? 2 : 4, 1, 1) __launch_bounds__(NTHREADS, 1)
+    chunk_kernel(const ChunkArgs a, const Workspace<SOLO> ws, const __grid_constant__ CUtensorMap kmap,
                  const __grid_constant__ CUtensorMap rmap, const __grid_constant__ CUtensorMap smap) {
   extern __shared__ __align__(1024) uint8_t sm[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // score CTAs (the context ones come behind them), rows of a row tile, and the MMAs of a pair or of this CTA
+  constexpr int SC = SOLO ? 1 : 2, ROWS = SC * CROWS;
   const uint32_t rank = cluster_rank();
-  const int k = (int)(blockIdx.x >> 2);
+  const int k = (int)(blockIdx.x / (2 * SC));
+  auto mma = [](uint32_t d, uint64_t ad, uint64_t bd, uint32_t id, uint32_t acc) {
+    if constexpr (SOLO) mma_f8_warp(d, ad, bd, id, acc);
+    else mma_f8_pair_warp(d, ad, bd, id, acc);
+  };
+  auto mma_ts = [](uint32_t d, uint32_t at, uint64_t bd, uint32_t id, uint32_t acc) {
+    if constexpr (SOLO) mma_f8_ts_warp(d, at, bd, id, acc);
+    else mma_f8_ts_pair_warp(d, at, bd, id, acc);
+  };
+  auto commit = [](uint64_t* bar, uint16_t mask) {  // (mask: the pair's CTAs)
+    if constexpr (SOLO) mma_commit_warp(bar);
+    else mma_commit_pair_warp(bar, mask);
+  };
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + OFF_FLAGS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + OFF_FLAGS + 4);
@@ -247,25 +287,30 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < NBAR; ++i) mbar_init(&bars[i], 1);
-    const int here = N_LANE_WARPS + (rank == 0 || rank == 2);  // (and the relay of the pair's other CTA)
-    for (int i = 0; i < 2; ++i) mbar_init(&bars[B_SEMPTY + i], 2 * N_LANE_WARPS);
+    const int here = N_LANE_WARPS + (!SOLO && (rank == 0 || rank == 2));  // (and the relay of the pair's other CTA)
+    for (int i = 0; i < 2; ++i) mbar_init(&bars[B_SEMPTY + i], SC * N_LANE_WARPS);
     mbar_init(&bars[B_QREADY], here);
     for (int i = 0; i < 4; ++i) mbar_init(&bars[B_PX + i], N_LANE_WARPS / 4);
     mbar_init(&bars[B_EP], N_LANE_WARPS);
-    for (int i = 0; i < 2; ++i) mbar_init(&bars[B_PFREE + i], rank < 2 ? 1 : N_LANE_WARPS);
-    for (int i = 0; i < 4; ++i) mbar_init(&bars[B_RS + i], 2 * N_LANE_WARPS);
+    for (int i = 0; i < 2; ++i) mbar_init(&bars[B_PFREE + i], rank < SC ? 1 : N_LANE_WARPS);
+    for (int i = 0; i < 4; ++i) mbar_init(&bars[B_RS + i], SC * N_LANE_WARPS);
     for (int i = 0; i < 2; ++i) mbar_init(&bars[B_OP + i], here);
     for (int i = 0; i < 2; ++i) mbar_init(&bars[B_SFULL + i], 2);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    if (rank >= 2) {  // what the context CTAs expect first
+    if (rank >= SC) {  // what the context CTAs expect first
       for (int i = 0; i < 2; ++i) mbar_arrive_expect_tx(&bars[B_PFULL + i], P_BYTES);
       for (int i = 0; i < NRF; ++i) mbar_arrive_expect_tx(&bars[B_RF + i], CROWS * 8);
     }
   }
   if (warp == W_MMA) {
-    tmem_alloc_pair(tmem_slot, 512);
-    tmem_relinquish_pair();
+    if constexpr (SOLO) {
+      tmem_alloc(tmem_slot, 512);
+      tmem_relinquish();
+    } else {
+      tmem_alloc_pair(tmem_slot, 512);
+      tmem_relinquish_pair();
+    }
   }
   __syncthreads();
   tc_fence_before();
@@ -286,12 +331,12 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
   }
   grid_dependents_launch();  // (the join kernel may come as soon as there is room)
   const bool work = k < ws.plan->n;
-  Way<MODE> w;
+  Way<MODE, SOLO> w;
   if (work) w.start(a, *ws.plan, k);
   else w.left = 0;
   int gt = 0;  // key tiles of the range before this segment
 
-  if (rank < 2) {
+  if (rank < SC) {
     // ================================================================ score CTAs
     const uint32_t kring = smem_u32(sm + OFF_K);
     const uint32_t scr = smem_u32(sm + OFF_SC);
@@ -300,7 +345,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
       // and both pages' row scales
       bool ok = true;
       const uint32_t kfull0 = map_to(smem_u32(&bars[B_KFULL]), 0);
-      int halves = 0, nsc = 0;
+      int halves = 0, nsc = 0, tiles = 0;
       for (; ok && w.more(); w.next(a)) {
         PageWindow pw;
         pw.from = -64;
@@ -309,8 +354,33 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
           const int64_t page = 2 * (int64_t)(w.t + i);
           const int64_t s0 = pw.slot(a, w, page, lane, rank == 0);
           const int64_t s1 = pw.slot(a, w, page + 1, lane, rank == 0);
-          const int64_t mine = rank == 0 ? s0 : s1;
           const uint32_t pages = (s0 >= 0 ? 1u : 0u) + (s1 >= 0 ? 1u : 0u);
+          if constexpr (SOLO) {
+            // an Lc block at a time, and the Rc block first
+            if (!wait(B_REMPTY + (g & 1), (uint32_t)(g >> 1) ^ 1u)) {
+              ok = false;
+              break;
+            }
+            const uint32_t rd = smem_u32(sm + OFF_KR) + (g & 1) * 2 * RBLK;
+            mbar_arrive_expect_tx_warp(&bars[B_RFULL + (g & 1)], pages * RBLK);
+            tiles = g + 1;
+            if (s0 >= 0) tma_load_2d_warp(rd, &rmap, DL, (int)s0, &bars[B_RFULL + (g & 1)]);
+            if (s1 >= 0) tma_load_2d_warp(rd + RBLK, &rmap, DL, (int)s1, &bars[B_RFULL + (g & 1)]);
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              const int jb = 4 * g + c, slot = jb % NKB;
+              if (!wait(B_KEMPTY + slot, (uint32_t)(jb / NKB) ^ 1u)) {
+                ok = false;
+                break;
+              }
+              mbar_arrive_expect_tx_warp(&bars[B_KFULL + slot], pages * BLK);
+              halves = jb + 1;
+              const uint32_t dst = kring + slot * KBLK;
+              if (s0 >= 0) tma_load_2d_warp(dst, &kmap, 128 * c, (int)s0, &bars[B_KFULL + slot]);
+              if (s1 >= 0) tma_load_2d_warp(dst + BLK, &kmap, 128 * c, (int)s1, &bars[B_KFULL + slot]);
+            }
+          } else {
+          const int64_t mine = rank == 0 ? s0 : s1;
           const uint32_t dst = kring + kb * KTILE;
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {
@@ -328,6 +398,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
               if (h) tma_load_2d_pair_warp(dst + 4 * BLK, &rmap, DL, (int)mine, kfull0 + bar * 8);
             }
           }
+          }
           if (!ok) break;
           // the row scales' slots held tile g - 5: the MMAs of tile g - 3, done by now, began
           // their last ones when the softmax warps had read S of tile g - 4, and so were
@@ -344,7 +415,12 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
         // let what was requested land before the cluster can leave
         if (lane == 0) fail();
         const int zero = 0;
-        if (rank == 0)
+        if constexpr (SOLO) {
+          for (int i = (halves > NKB ? halves - NKB : 0); i < halves; ++i)
+            (void)mbar_wait(&bars[B_KFULL + i % NKB], (i / NKB) & 1, &zero, WAIT_NS);
+          for (int i = (tiles > 2 ? tiles - 2 : 0); i < tiles; ++i)
+            (void)mbar_wait(&bars[B_RFULL + (i & 1)], (i >> 1) & 1, &zero, WAIT_NS);
+        } else if (rank == 0)
           for (int i = (halves > 2 * NK ? halves - 2 * NK : 0); i < halves; ++i)
             (void)mbar_wait(&bars[B_KFULL + 2 * ((i >> 1) % NK) + (i & 1)], ((i >> 1) / NK) & 1, &zero, WAIT_NS);
         for (int i = (nsc > NSC ? nsc - NSC : 0); i < nsc; ++i)
@@ -358,7 +434,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
       bool ok = true;
       for (; ok && w.more(); w.next(a)) {
         // (and meanwhile the next row tile's queries come into L2)
-        Way<MODE> wn = w;
+        Way<MODE, SOLO> wn = w;
         wn.next(a);
         if (wn.more()) {
           const int64_t r0 = (int64_t)wn.rt * ROWS + rank * CROWS, rows = (int64_t)wn.s.nq * a.H;
@@ -403,7 +479,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
       if (rank == 0) {
         const uint32_t id = idesc_f16(ROWS, TILE, false, false);  // e4m3 x e4m3 (format 0)
         const uint64_t kd = smem_desc(kring, 16, 1024, SW128);
-        const uint64_t rd = smem_desc(kring + 4 * BLK, 16, 512, SW64);
+        const uint64_t rd = smem_desc(SOLO ? smem_u32(sm + OFF_KR) : kring + 4 * BLK, 16, 512, SW64);
         const uint64_t ql = smem_desc(smem_u32(sm + OFF_QL), 16, 1024, SW128);
         const uint64_t qr = smem_desc(smem_u32(sm + OFF_QR), 16, 1024, SW128);
         bool ok = true;
@@ -416,6 +492,24 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
             const int g = gt + i, kb = g % NK;
             const uint64_t off = (uint64_t)(kb * KTILE >> 4);
             const uint32_t dl = tmem + T_SL + (g & 1) * TILE;
+            if constexpr (SOLO) {
+#pragma unroll 1
+              for (int c = 0; c < 4; ++c) {
+                const int jb = 4 * g + c, slot = jb % NKB;
+                if (!wait_cluster(B_KFULL + slot, (uint32_t)(jb / NKB))) {
+                  ok = false;
+                  break;
+                }
+                tc_fence_after();
+                const uint64_t bd = kd + (uint64_t)(slot * KBLK >> 4);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                  mma_ts(dl, tmem + T_QH + c * 32 + kk * 8, bd + 2 * kk, id, (c | kk) != 0);
+                  mma(dl, ql + (uint64_t)(c * OP_ATOM >> 4) + 2 * kk, bd + 2 * kk, id, 1u);
+                }
+                commit(&bars[B_KEMPTY + slot], 0);
+              }
+            } else {
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
               if (!wait_cluster(B_KFULL + 2 * kb + h, (uint32_t)(g / NK))) {
@@ -429,11 +523,12 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
                 const uint64_t bd = kd + off + (uint64_t)(c * BLK >> 4);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) {
-                  mma_f8_ts_pair_warp(dl, tmem + T_QH + c * 32 + kk * 8, bd + 2 * kk, id, (h | blk | kk) != 0);
-                  mma_f8_pair_warp(dl, ql + (uint64_t)(c * OP_ATOM >> 4) + 2 * kk, bd + 2 * kk, id, 1u);
+                  mma_ts(dl, tmem + T_QH + c * 32 + kk * 8, bd + 2 * kk, id, (h | blk | kk) != 0);
+                  mma(dl, ql + (uint64_t)(c * OP_ATOM >> 4) + 2 * kk, bd + 2 * kk, id, 1u);
                 }
               }
-              if (h == 0) mma_commit_pair_warp(&bars[B_KEMPTY + 2 * kb], 3);
+              if (h == 0) commit(&bars[B_KEMPTY + 2 * kb], 3);
+            }
             }
             if (!ok) break;
             // S_R (and the other S_L) of the previous tile read
@@ -441,19 +536,24 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
               ok = false;
               break;
             }
+            if (SOLO && !wait_cluster(B_RFULL + (g & 1), (uint32_t)(g >> 1))) {
+              ok = false;
+              break;
+            }
             tc_fence_after();
+            const uint64_t rb = SOLO ? rd + (uint64_t)((g & 1) * 2 * RBLK >> 4) : rd + off;
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) {
-              mma_f8_pair_warp(tmem + T_SR, qr + 2 * kk, rd + off + 2 * kk, id, kk != 0);
-              mma_f8_pair_warp(tmem + T_SR, qr + 4 + 2 * kk, rd + off + 2 * kk, id, 1u);
+              mma(tmem + T_SR, qr + 2 * kk, rb + 2 * kk, id, kk != 0);
+              mma(tmem + T_SR, qr + 4 + 2 * kk, rb + 2 * kk, id, 1u);
             }
-            mma_commit_pair_warp(&bars[B_KEMPTY + 2 * kb + 1], 3);
-            mma_commit_pair_warp(&bars[B_SFULL + (g & 1)], 3);
+            commit(SOLO ? &bars[B_REMPTY + (g & 1)] : &bars[B_KEMPTY + 2 * kb + 1], 3);
+            commit(&bars[B_SFULL + (g & 1)], 3);
           }
           gt += w.n;
         }
         if (!ok && lane == 0) fail();
-        mma_commit_pair_warp(&bars[B_DRAIN], 3);
+        commit(&bars[B_DRAIN], 3);
       } else {
         // rank 1 tells the MMA's issuer of its query
         const uint32_t qready = map_to(smem_u32(&bars[B_QREADY]), 0);
@@ -483,7 +583,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
       float* mgs = reinterpret_cast<float*>(sm + OFF_MG);
       int* lim = reinterpret_cast<int*>(sm + OFF_LIM);
       float* cs = reinterpret_cast<float*>(sm + OFF_C);
-      Way<MODE>* walk = reinterpret_cast<Way<MODE>*>(sm + OFF_WALK) + (warp - W_LANE);  // (it has no registers to spare)
+      Way<MODE, SOLO>* walk = reinterpret_cast<Way<MODE, SOLO>*>(sm + OFF_WALK) + (warp - W_LANE);  // (it has no registers to spare)
       const int rh = row0 + 16 * hl;          // the thread's rows of a tile: rh, rh + 8
       const int mh = rh + 8 * (i4 & 1);       // the row this lane speaks for there
       uint32_t px = 0;
@@ -495,7 +595,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
       // The queries of a row tile: two e4m3 terms on the scale that puts a row's largest value
       // in [128, 256); c folds the scale back in, with sm_scale log2 e. Two of the thread's rows
       // at a time, their channels all in flight at once.
-      auto load_query = [&](const Way<MODE>& x) -> bool {
+      auto load_query = [&](const Way<MODE, SOLO>& x) -> bool {
         const int64_t r0 = (int64_t)x.rt * ROWS + rank * CROWS, rows = (int64_t)x.s.nq * a.H;
         const uint32_t qlo = smem_u32(sm + OFF_QL) + part * OP_ATOM, qrp = smem_u32(sm + OFF_QR);
         if (part == 0) {  // the keys that row q * 32 + lane sees (rows past the last one are copies of it)
@@ -588,7 +688,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
       if (more) *walk = w;  // (every lane, the same)
       __syncwarp();
       while (ok && more) {
-        const Way<MODE>& x = *walk;
+        const Way<MODE, SOLO>& x = *walk;
         ok = load_query(x) && quarter_sync();  // (the sync: cs and lim are read by every part)
         if (!ok) break;
         const int n_tiles = x.n;
@@ -697,8 +797,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
 #pragma unroll
             for (int p = 0; p < 2; ++p) l[p] *= __shfl_sync(0xffffffffu, f, (lane & 28) + p);
           }
-          const uint32_t to = map_to(smem_u32(sm + OFF_P + buf * P_STRIDE), rank + 2);
-          const uint32_t bar = map_to(smem_u32(&bars[B_PFULL + buf]), rank + 2);
+          const uint32_t to = map_to(smem_u32(sm + OFF_P + buf * P_STRIDE), rank + SC);
+          const uint32_t bar = map_to(smem_u32(&bars[B_PFULL + buf]), rank + SC);
           if (i4 < 2) st_async_b32(to + P_F + (sub * CROWS + mh) * 4, __float_as_uint(mn), bar);
           if (warp == W_LANE && lane == 0) st_async_b32(to + P_PAGES, facts[sc], bar);
           // p = 2^(c u - M_g + 7) (nothing in sight so far: u is -inf, and p 0)
@@ -775,13 +875,13 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
             }
           }
           const int rf = x.seg % NRF;
-          const uint32_t to = map_to(smem_u32(sm + OFF_RF + (rf * CROWS + hh) * 8), rank + 2);
-          const uint32_t bar = map_to(smem_u32(&bars[B_RF + rf]), rank + 2);
+          const uint32_t to = map_to(smem_u32(sm + OFF_RF + (rf * CROWS + hh) * 8), rank + SC);
+          const uint32_t bar = map_to(smem_u32(&bars[B_RF + rf]), rank + SC);
           st_async_b32(to, __float_as_uint(f), bar);
           st_async_b32(to + 4, __float_as_uint(mm), bar);
         }
         gt += n_tiles;
-        Way<MODE> wn = x;
+        Way<MODE, SOLO> wn = x;
         wn.next(a);
         more = wn.more();
         __syncwarp();
@@ -801,7 +901,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
     // ================================================================ context CTAs
     const uint32_t pbuf = smem_u32(sm + OFF_P);
     const uint32_t vring = smem_u32(sm + OFF_V);
-    const int half_of = (int)rank - 2;  // channels 256 h + 128 half_of .. of each O half h
+    const int half_of = (int)rank - SC;  // channels 256 h + 128 half_of .. of each O half h (solo: all of them)
     if (warp == W_TMA) {
       bool ok = true;
       int nv = 0;
@@ -812,6 +912,25 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
           const int g = gt + i, vs = g % NVT;
           const int64_t page = 2 * (int64_t)(w.t + i);
           const int64_t s0 = pw.slot(a, w, page, lane, false), s1 = pw.slot(a, w, page + 1, lane, false);
+          if constexpr (SOLO) {
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+              if (!wait(B_VEMPTY + h, (uint32_t)g ^ 1u)) {
+                ok = false;
+                break;
+              }
+              mbar_arrive_expect_tx_warp(&bars[B_VT + h], 2u * BLK * ((s0 >= 0 ? 1u : 0u) + (s1 >= 0 ? 1u : 0u)));
+              nv = 2 * g + h + 1;
+#pragma unroll 1
+              for (int m = 0; m < 2; ++m) {
+                const uint32_t dst = vring + (2 * h + m) * VBLK;
+                if (s0 >= 0) tma_load_2d_warp(dst, &kmap, 256 * h + 128 * m, (int)s0, &bars[B_VT + h]);
+                if (s1 >= 0) tma_load_2d_warp(dst + BLK, &kmap, 256 * h + 128 * m, (int)s1, &bars[B_VT + h]);
+              }
+            }
+            if (!ok) break;
+            continue;
+          }
           if (!wait(B_VEMPTY + vs, (uint32_t)(g / NVT) ^ 1u)) {
             ok = false;
             break;
@@ -831,6 +950,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
       if (!ok) {
         if (lane == 0) fail();
         const int zero = 0;
+        static_assert(NVT == 2, "(solo: halves of tiles)");
         for (int i = (nv > NVT ? nv - NVT : 0); i < nv; ++i)
           (void)mbar_wait(&bars[B_VT + i % NVT], (i / NVT) & 1, &zero, WAIT_NS);
       }
@@ -838,49 +958,50 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
     } else if (warp == W_SCALE) {
       // (no scales here: this warp tells the score CTA which payloads are read, so that its writes of
       // the next ones come after those reads)
-      const uint32_t pfree = map_to(smem_u32(&bars[B_PFREE]), rank - 2);
+      const uint32_t pfree = map_to(smem_u32(&bars[B_PFREE]), rank - SC);
       bool ok = true;
       for (int64_t g = 0; ok && g < w.left; ++g)
         ok = relay(B_PFREE + (int)(g & 1), (uint32_t)(g >> 1), pfree + (int)(g & 1) * 8);
       if (!ok && lane == 0) fail();
       __syncwarp();
     } else if (warp == W_MMA) {
-      if (rank == 2) {
+      if (rank == SC) {
         const uint32_t id = idesc_f16(ROWS, 256, false, true);  // A K-major, B = V MN-major
         const uint64_t pd = smem_desc(smem_u32(sm + OFF_OP), 16, 1024, SW128);
-        const uint64_t vd = smem_desc(vring, 16, 1024, SW128);
+        const uint64_t vd = smem_desc(vring, SOLO ? VBLK : 16, 1024, SW128);
         bool ok = true;
         for (; ok && w.more(); w.next(a)) {
           for (int i = 0; ok && i < w.n; ++i) {
             const int g = gt + i;
             const uint64_t ad = pd + (uint64_t)((g & 1) * 2 * OP_ATOM >> 4);
-            if (!wait(B_VT + g % NVT, (uint32_t)(g / NVT)) || !wait_cluster(B_OP + (g & 1), (uint32_t)(g >> 1))) {
+            if ((!SOLO && !wait(B_VT + g % NVT, (uint32_t)(g / NVT))) || !wait_cluster(B_OP + (g & 1), (uint32_t)(g >> 1))) {
               ok = false;
               break;
             }
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
-              if (!wait_cluster(B_RS + 2 * (g & 1) + h, (uint32_t)(g >> 1))) {
+              if ((SOLO && !wait(B_VT + h, (uint32_t)g)) || !wait_cluster(B_RS + 2 * (g & 1) + h, (uint32_t)(g >> 1))) {
                 ok = false;
                 break;
               }
               tc_fence_after();
-              const uint64_t bd = vd + (uint64_t)(((g % NVT) * VTILE + h * VBLK) >> 4);
+              const uint64_t bd = vd + (uint64_t)((SOLO ? 2 * h * VBLK : (g % NVT) * VTILE + h * VBLK) >> 4);
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk) {
                 // A: 32 tokens of the hi / lo atom; B: 32 token rows (4 KB)
-                mma_f8_pair_warp(tmem + h * 256, ad + 2 * kk, bd + 256 * kk, id, (i > 0 || kk > 0) ? 1u : 0u);
-                mma_f8_pair_warp(tmem + h * 256, ad + (OP_ATOM >> 4) + 2 * kk, bd + 256 * kk, id, 1u);
+                mma(tmem + h * 256, ad + 2 * kk, bd + 256 * kk, id, (i > 0 || kk > 0) ? 1u : 0u);
+                mma(tmem + h * 256, ad + (OP_ATOM >> 4) + 2 * kk, bd + 256 * kk, id, 1u);
               }
-              mma_commit_pair_warp(&bars[B_ODONE + 2 * (g & 1) + h], 0xC);
+              commit(&bars[B_ODONE + 2 * (g & 1) + h], 0xC);
+              if constexpr (SOLO) commit(&bars[B_VEMPTY + h], 0);
             }
             if (!ok) break;
-            mma_commit_pair_warp(&bars[B_VEMPTY + g % NVT], 0xC);
+            if constexpr (!SOLO) commit(&bars[B_VEMPTY + g % NVT], 0xC);
           }
           gt += w.n;
         }
         if (!ok && lane == 0) fail();
-        mma_commit_pair_warp(&bars[B_DRAIN], 0xC);
+        commit(&bars[B_DRAIN], 0xC);
       } else {
         // rank 3 tells the MMA's issuer of its V tiles and operands
         const uint32_t op = map_to(smem_u32(&bars[B_OP]), 2);
@@ -900,12 +1021,12 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
       const int part = (warp - W_LANE) >> 2;  // 32 tokens of the tile; 64 columns of an O half
       const int hh = q * 32 + lane;
       const uint32_t lane_addr = (uint32_t)(q * 32) << 16;
-      const uint32_t rs = map_to(smem_u32(&bars[B_RS]), 2);
+      const uint32_t rs = map_to(smem_u32(&bars[B_RS]), SC);
       bool ok = true;
       for (; ok && w.more(); w.next(a)) {
-        const int lim0 = limit_of(a, w.s, first_token<Geo>(a, w.rt));  // the tile's first row sees least
+        const int lim0 = limit_of(a, w.s, first_token<GeoOf<SOLO>>(a, w.rt));  // the tile's first row sees least
         // (a window: that of the tile's last row begins last)
-        const int from = MODE == kWindow ? window_from(a, limit_of(a, w.s, last_token<Geo>(a, w.s, w.rt))) : 0;
+        const int from = MODE == kWindow ? window_from(a, limit_of(a, w.s, last_token<GeoOf<SOLO>>(a, w.s, w.rt))) : 0;
         float ref = -INFINITY, hi = -INFINITY;  // the row's reference in O, and the highest one so far
         for (int i = 0; i < w.n; ++i) {
           const int g = gt + i, pb = g & 1, vs = g % NVT;
@@ -977,13 +1098,15 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
           }
           if (part_seen || pages != 3u) {
             // some row does not see all of this tile: no NaN code may stay in it
-            if (!wait(B_VT + vs, (uint32_t)(g / NVT))) {
+            if (!wait(SOLO ? B_VT : B_VT + vs, SOLO ? (uint32_t)g : (uint32_t)(g / NVT)) ||
+                (SOLO && !wait(B_VT + 1, (uint32_t)g))) {
               ok = false;
               break;
             }
-            const uint32_t vb = vring + vs * VTILE + (warp - W_LANE) * 2048 + lane * 16;
+            constexpr int SHARE_OF_V = (SOLO ? 4 * VBLK : VTILE) / N_LANE_WARPS;
+            const uint32_t vb = vring + (SOLO ? 0 : vs * VTILE) + (warp - W_LANE) * SHARE_OF_V + lane * 16;
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < SHARE_OF_V / 512; ++u) {
               const uint4 v = lds128(vb + u * 512);
               sts128(vb + u * 512, make_uint4(no_nan(v.x), no_nan(v.y), no_nan(v.z), no_nan(v.w)));
             }
@@ -1106,7 +1229,10 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(NTHREADS, 1)
   tc_fence_before();
   cluster_sync();  // no CTA leaves while another may still write to it
   tc_fence_after();
-  if (warp == W_MMA) tmem_dealloc_pair(tmem, 512);
+  if (warp == W_MMA) {
+    if constexpr (SOLO) tmem_dealloc(tmem, 512);
+    else tmem_dealloc_pair(tmem, 512);
+  }
 }
 
 // Joins the parts of the row tiles that range borders cut: for every cluster k but the
@@ -1120,7 +1246,7 @@ constexpr int FEW_ROW_TILES = 8;
 
 // A row of a group with a shared prefix: the parts of the prefix and of the rest, each one whole row
 // tile's or those that range borders cut it into, by one warp.
-__device__ __forceinline__ void join_parts(const ChunkArgs& a, const Workspace& ws, const int64_t* base, int64_t row,
+__device__ __forceinline__ void join_parts(const ChunkArgs& a, const Workspace<>& ws, const int64_t* base, int64_t row,
                                            int lane) {
   const int64_t nc = ws.plan->n;
   const int2 of = a.part_seq[row / a.H];
@@ -1212,7 +1338,7 @@ __device__ __forceinline__ void join_parts(const ChunkArgs& a, const Workspace& 
 }
 
 template <int MODE, int SPLIT>
-__global__ void __launch_bounds__(256) join_kernel(const ChunkArgs a, const Workspace ws, const int64_t* base, int cut_blocks) {
+__global__ void __launch_bounds__(256) join_kernel(const ChunkArgs a, const Workspace<> ws, const int64_t* base, int cut_blocks) {
   static_assert(MAX_CLUSTERS <= 64, "two parts a lane");
   const int k = (int)blockIdx.x / (JOIN_BLOCKS * SPLIT) + 1, lane = threadIdx.x & 31;
   const int row = (int)blockIdx.x % (JOIN_BLOCKS * SPLIT) / SPLIT * 8 + (threadIdx.x >> 5);
@@ -1349,35 +1475,36 @@ Layout layout_of(int B, int H, int64_t total_q, int max_blocks, int G, int64_t w
   return w;
 }
 
-// Whether a call's sequences have so few rows on average that the kernel for them (rows.cu) is faster: up
-// to 64, or 128 over few key tiles.  (It reads a key tile once for 32 rows, this one for 256, but a row
-// tile starts faster there.)
+// Which kernel a call goes to, by the rows of its sequences on average: up to 64, the one for few rows
+// (rows.cu); up to 128, that one over few key tiles, else this one's clusters of two.
 constexpr int FEW_ROWS = 64, FEW_TILES = 20;
 bool few_rows(int B, int H, int64_t total_q, int64_t keys) {
   const int64_t rows = total_q * H;
   return rows <= (int64_t)FEW_ROWS * B || (rows <= 2 * (int64_t)FEW_ROWS * B && keys <= FEW_TILES * TILE);
 }
+bool solo_rows(int B, int H, int64_t total_q) { return total_q * H <= (int64_t)CROWS * B; }
 int64_t window_keys(int max_blocks, int64_t window, int64_t n_sink) {
   const int64_t all = (int64_t)max_blocks * PAGE;
   return window + n_sink < all ? window + n_sink : all;
 }
 
 // Clusters of the kernel that the device holds at once.
-template <int MODE>
+template <int MODE, bool SOLO = false>
 cudaError_t capacity(int* fit) {
   static std::atomic<int> memo[MAX_DEVICES];
   return per_device(memo, [](int* v) {
-    cudaError_t r = cudaFuncSetAttribute(chunk_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    constexpr int smem = SOLO ? SMEM_SOLO : SMEM;
+    cudaError_t r = cudaFuncSetAttribute(chunk_kernel<MODE, SOLO>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (r != cudaSuccess) return r;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(NUM_SMS, 1, 1);
     cfg.blockDim = dim3(NTHREADS, 1, 1);
-    cfg.dynamicSmemBytes = SMEM;
+    cfg.dynamicSmemBytes = smem;
     int n = 0;
-    r = cudaOccupancyMaxActiveClusters(&n, chunk_kernel<MODE>, &cfg);
+    r = cudaOccupancyMaxActiveClusters(&n, chunk_kernel<MODE, SOLO>, &cfg);
     if (r != cudaSuccess) return r;
     if (n < 1) return cudaErrorLaunchOutOfResources;
-    *v = n > MAX_CLUSTERS ? MAX_CLUSTERS : n;
+    *v = n > GeoOf<SOLO>::RANGES ? GeoOf<SOLO>::RANGES : n;
     return cudaSuccess;
   }, fit);
 }
@@ -1395,7 +1522,7 @@ cudaError_t launch(ChunkArgs a, void* workspace, cudaStream_t s) {
   a.unit = reinterpret_cast<int64_t*>(p + w.unit);
   a.part_seq = reinterpret_cast<int2*>(p + w.part_seq);
   a.part_rows = w.part_rows;
-  Workspace ws;
+  Workspace<> ws;
   ws.plan = reinterpret_cast<Plan<Geo>*>(p + OFF_PLAN);
   int64_t* base = reinterpret_cast<int64_t*>(p + OFF_BASE);
   ws.m = reinterpret_cast<float*>(p + w.m);
@@ -1422,6 +1549,58 @@ cudaError_t launch(ChunkArgs a, void* workspace, cudaStream_t s) {
   return launch_after_prep(join_kernel<MODE, 1>, blocks + part_blocks, 256, 0, s, a, ws, base, (int)blocks);
 }
 
+// The clusters of two, for a window.
+constexpr int64_t OFF_SOLO_BASE = 2560;
+static_assert(OFF_PLAN + sizeof(Plan<SoloGeo>) <= OFF_SOLO_BASE, "plan area");
+
+struct SoloLayout {
+  int most;
+  int64_t tiles, owner, m, rows, bytes;
+};
+SoloLayout solo_layout(int B, int H, int64_t total_q, int64_t keys) {
+  auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
+  SoloLayout w;
+  w.tiles = total_q * H / CROWS + B;
+  const int64_t units = w.tiles * ((keys + CROWS) / TILE + 4) / SoloGeo::MIN_TILES;
+  w.most = (int)(units < 1 ? 1 : (units < SoloGeo::RANGES ? units : SoloGeo::RANGES));
+  w.owner = OFF_SOLO_BASE + up((int64_t)(B + 1) * 8);
+  w.m = w.owner + up(w.tiles * (int64_t)sizeof(int4));
+  w.rows = w.most > 1 ? 2 * (int64_t)w.most * CROWS : 0;  // (one range cuts no row tile)
+  w.bytes = w.m + w.rows * (8 + DL * 4);
+  return w;
+}
+
+cudaError_t launch_solo(ChunkArgs a, const SoloLayout& w, void* workspace, cudaStream_t s) {
+  int fit = 0;
+  cudaError_t e = capacity<kWindow, true>(&fit);
+  if (e != cudaSuccess) return e;
+  const int clusters = w.most < fit ? w.most : fit;
+  char* p = static_cast<char*>(workspace);
+  a.err = reinterpret_cast<unsigned*>(p);
+  Workspace<true> ws;
+  ws.plan = reinterpret_cast<Plan<SoloGeo>*>(p + OFF_PLAN);
+  ws.m = reinterpret_cast<float*>(p + w.m);
+  ws.l = ws.m + w.rows;
+  ws.o = ws.l + w.rows;
+  ws.parts = 0;
+  int4* owner = reinterpret_cast<int4*>(p + w.owner);
+  DecodeArgs d{};  // what the cache's tensor maps are made from
+  d.codes = a.codes;
+  d.scales = a.scales;
+  d.block_table = a.block_table;
+  d.n_blocks = a.n_blocks;
+  CUtensorMap kmap, rmap, smap;
+  if ((e = make_cache_map(d, &kmap)) != cudaSuccess || (e = make_rc_map(d, &rmap)) != cudaSuccess ||
+      (e = make_scale_map(d, &smap)) != cudaSuccess)
+    return e;
+  solo_plan_kernel<<<1, 1024, 0, s>>>(a, ws.plan, reinterpret_cast<int64_t*>(p + OFF_SOLO_BASE), owner, clusters);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  e = launch_after_prep(chunk_kernel<kWindow, true>, 2 * clusters, NTHREADS, SMEM_SOLO, s, a, ws, kmap, rmap, smap);
+  if (e != cudaSuccess || clusters == 1) return e;
+  return launch_parts_join<kWindow, CROWS>(a, PartsJoin{&ws.plan->tiles, owner, ws.m, ws.l, ws.o, 0, nullptr, nullptr, 0},
+                                           w.tiles, s);
+}
+
 }  // namespace
 
 int64_t chunk_workspace(int B, int H, int64_t total_q, int max_blocks) {
@@ -1430,6 +1609,7 @@ int64_t chunk_workspace(int B, int H, int64_t total_q, int max_blocks) {
 int64_t window_workspace(int B, int H, int64_t total_q, int max_blocks, int window, int n_sink) {
   if (few_rows(B, H, total_q, window_keys(max_blocks, window, n_sink)))
     return rows_window_workspace(B, H, total_q, max_blocks, window, n_sink);
+  if (solo_rows(B, H, total_q)) return solo_layout(B, H, total_q, window_keys(max_blocks, window, n_sink)).bytes;
   return layout_of<kWindow>(B, H, total_q, max_blocks, 0, window, n_sink).bytes;
 }
 int64_t shared_workspace(int B, int H, int64_t total_q, int max_blocks, int G) {
@@ -1439,8 +1619,10 @@ int64_t shared_workspace(int B, int H, int64_t total_q, int max_blocks, int G) {
 
 cudaError_t launch_chunk(const ChunkArgs& a, void* workspace, cudaStream_t s) { return launch<kPlain>(a, workspace, s); }
 cudaError_t launch_window(const ChunkArgs& a, void* workspace, cudaStream_t s) {
-  return few_rows(a.B, a.H, a.total_q, window_keys(a.max_blocks, a.window, a.n_sink))
-             ? launch_rows_window(a, workspace, s) : launch<kWindow>(a, workspace, s);
+  const int64_t keys = window_keys(a.max_blocks, a.window, a.n_sink);
+  if (few_rows(a.B, a.H, a.total_q, keys)) return launch_rows_window(a, workspace, s);
+  if (solo_rows(a.B, a.H, a.total_q)) return launch_solo(a, solo_layout(a.B, a.H, a.total_q, keys), workspace, s);
+  return launch<kWindow>(a, workspace, s);
 }
 cudaError_t launch_shared(const ChunkArgs& a, void* workspace, cudaStream_t s) {
   return few_rows(a.B, a.H, a.total_q, INT64_MAX) ? launch_rows_shared(a, workspace, s) : launch<kShared>(a, workspace, s);
@@ -1449,7 +1631,7 @@ cudaError_t launch_shared(const ChunkArgs& a, void* workspace, cudaStream_t s) {
 cudaError_t prefix_capacity(int* clusters) { return capacity<kShared>(clusters); }
 cudaError_t launch_prefixes(const ChunkArgs& a, const PrefixParts& p, int clusters, const CUtensorMap& kmap,
                             const CUtensorMap& rmap, const CUtensorMap& smap, cudaStream_t s) {
-  Workspace ws;
+  Workspace<> ws;
   ws.plan = static_cast<Plan<Geo>*>(p.plan);
   ws.m = p.m;
   ws.l = p.l;

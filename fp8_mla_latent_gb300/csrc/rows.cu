@@ -805,104 +805,10 @@ __global__ void __launch_bounds__(1024) rows_shared_plan_kernel(const ChunkArgs 
   }
 }
 
-// ------------------------------------------------------------------ join
-// The parts of a row tile's rows, a warp per row (and SPLIT-th of its channels), a block per row tile.  With
-// a shared prefix they are those of the row's own keys, then those of the prefix.
-template <int MODE, int N, int SPLIT>
-__global__ void __launch_bounds__(N * 32) rows_join_kernel(const ChunkArgs a, const Parts<N> ps, const int4* owner,
-                                                           const int64_t* prefix_base, const int4* prefix_owner,
-                                                           int64_t prefix_slots) {
-  const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
-  const int64_t p = blockIdx.x / SPLIT;
-  const int ch = (int)(blockIdx.x % SPLIT) * (DL / SPLIT);
-  grid_dependency_wait();  // (every block: what it reads, and that this launch is not over before the kernel is)
-  const int64_t tiles = ps.plan->tiles;
-  const int4 of = owner[p];  // (there is room for as many as there are blocks)
-  if (p >= tiles) return;
-  const int k0 = of.z >> 1, n_own = of.w - k0 + 1;
-  const SeqInfo<MODE> s = seq_info<MODE>(a, of.x, false);
-  bool shares = false;
-  if constexpr (MODE == kShared) shares = s.part >= 0;
-  if (n_own == 1 && !shares) return;  // whole
-  const int64_t r = (int64_t)of.y * N + row;
-  if (r >= (int64_t)s.nq * a.H) return;
-  int n = n_own, prefix_k0 = 0;
-  int64_t own_whole = 0, prefix_whole = 0, prefix_row = 0;
-  int4 pf = make_int4(0, 0, 0, 0);
-  if constexpr (MODE == kShared) {
-    if (shares) {
-      const int g = a.entries[of.x].v.w;
-      const ChunkEntry e = a.entries[g];
-      const int64_t in_group = (s.q0 - e.u.x) * a.H + r;
-      pf = prefix_owner[prefix_base[g] + in_group / WideGeo::ROWS];
-      prefix_k0 = pf.z >> 1;
-      n += pf.w - prefix_k0 + 1;
-      own_whole = ps.whole + s.part + r;
-      prefix_whole = ps.whole + e.v.z + in_group;
-      prefix_row = in_group % WideGeo::ROWS - prefix_slots;  // (the prefixes' slots lie in front of these)
-    }
-  }
-  auto slot = [&](int j) -> int64_t {
-    if (MODE == kShared && shares) {
-      if (j >= n_own) {
-        j -= n_own;
-        if (n - n_own == 1) return prefix_whole;
-        return (int64_t)(j == 0 ? pf.z : 2 * (prefix_k0 + j)) * WideGeo::ROWS + prefix_row;
-      }
-      if (n_own == 1) return own_whole;
-    }
-    return (int64_t)(j == 0 ? of.z : 2 * (k0 + j)) * N + row;
-  };
-  float M = -INFINITY, L = 0.f;
-  for (int j = lane; j < n; j += 32) M = fmaxf(M, ps.m[slot(j)]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  constexpr int Q = 4 / SPLIT;  // 16-byte units a lane
-  float4 acc[Q];
-#pragma unroll
-  for (int c = 0; c < Q; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int j0 = 0; j0 < n; j0 += 32) {
-    const int j = j0 + lane;
-    float wt = 0.f;
-    if (j < n) {
-      const float m = ps.m[slot(j)];
-      wt = m > -INFINITY ? ex2_approx(m - M) : 1.f;  // (a NaN l stays one)
-      L += wt * ps.l[slot(j)];
-    }
-    const int some = min(n - j0, 32);
-#pragma unroll(SPLIT == 1 ? 4 : 8)
-    for (int i = 0; i < some; ++i) {
-      const float w = __shfl_sync(0xffffffffu, wt, i);
-      const float4* o = reinterpret_cast<const float4*>(ps.o + slot(j0 + i) * DL + ch) + lane;
-#pragma unroll
-      for (int c = 0; c < Q; ++c) {
-        const float4 v = o[32 * c];
-        acc[c].x += w * v.x;
-        acc[c].y += w * v.y;
-        acc[c].z += w * v.z;
-        acc[c].w += w * v.w;
-      }
-    }
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-  const float inv = L == 0.f ? 0.f : 1.f / L;
-  const int64_t at = s.q0 * a.H + r;
-  uint2* out = reinterpret_cast<uint2*>(a.out + at * DL + ch) + lane;
-#pragma unroll
-  for (int c = 0; c < Q; ++c) {
-    const __nv_bfloat162 x = __floats2bfloat162_rn(acc[c].x * inv, acc[c].y * inv);
-    const __nv_bfloat162 y = __floats2bfloat162_rn(acc[c].z * inv, acc[c].w * inv);
-    out[32 * c] = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
-  }
-  if (ch == 0 && a.lse != nullptr && lane == 0) a.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * LN2;
-}
-
 // ------------------------------------------------------------------ host
 constexpr int64_t OFF_PLAN = 256, OFF_PREFIX_PLAN = 4096, OFF_BASE = 5376;
 static_assert(OFF_PLAN + sizeof(Plan<Geo<16>>) <= OFF_PREFIX_PLAN && OFF_PREFIX_PLAN + sizeof(Plan<WideGeo>) <= OFF_BASE,
               "plan area");
-constexpr int FEW_ROW_TILES = 512;
 
 struct Layout {
   int most, prefix_most;         // ranges, and the prefixes' clusters
@@ -1009,11 +915,8 @@ cudaError_t launch(ChunkArgs a, const Layout& w, void* workspace, cudaStream_t s
   }
   e = launch_after_prep(rows_kernel<MODE, N>, w.most, NTHREADS, Cfg<N>::SMEM, s, a, ps, ready, kmap, rmap, smap);
   if (e != cudaSuccess || (MODE != kShared && w.most == 1)) return e;
-  const int64_t* pb = prefix_base;
-  const int4 *ow = owner, *po = prefix_owner;
-  if (w.tiles < FEW_ROW_TILES)
-    return launch_after_prep(rows_join_kernel<MODE, N, 4>, (unsigned)(4 * w.tiles), N * 32, 0, s, a, ps, ow, pb, po, w.prefix_slots);
-  return launch_after_prep(rows_join_kernel<MODE, N, 1>, (unsigned)w.tiles, N * 32, 0, s, a, ps, ow, pb, po, w.prefix_slots);
+  return launch_parts_join<MODE, N>(a, PartsJoin{&ps.plan->tiles, owner, ps.m, ps.l, ps.o, ps.whole, prefix_base, prefix_owner,
+                                                 w.prefix_slots}, w.tiles, s);
 }
 
 }  // namespace
