@@ -134,9 +134,11 @@ constexpr int B_ODONE = B_RS + 4;            // [2 buffers][2] ranks 2, 3: a til
 constexpr int NRF = 4;
 constexpr int B_RF = B_ODONE + 4;            // [NRF] context: row factors of a finished row tile arrived
 constexpr int B_DRAIN = B_RF + NRF;          // every MMA done
-constexpr int B_RFULL = B_DRAIN + 1;         // [2] solo score: Rc block loaded
-constexpr int B_REMPTY = B_RFULL + 2;        // [2] solo score: consumed
-constexpr int NBAR = B_REMPTY + 2;
+constexpr int B_RFULL = B_DRAIN + 1;         // solo score: Rc block loaded
+constexpr int B_REMPTY = B_RFULL + 1;        // solo score: consumed
+constexpr int B_SFREE = B_REMPTY + 1;        // [NKB] solo score: Lc block consumed
+constexpr int B_SFILL = B_KFULL;             // [NKB] solo score: loaded (in place of the halves' barriers)
+constexpr int NBAR = B_SFREE + 7;
 
 // shared memory (dynamic, 1024-byte aligned)
 constexpr int OFF_FLAGS = 512;               // tmem base, abort flag
@@ -160,11 +162,12 @@ constexpr int OFF_OP = OFF_P + 2 * P_STRIDE; // context: two operands (hi and lo
 constexpr int OFF_V = OFF_OP + 4 * OP_ATOM;
 constexpr int TOTAL_C = OFF_V + NVT * VTILE;
 constexpr int SMEM = TOTAL_S > TOTAL_C ? TOTAL_S : TOTAL_C;
-// Solo (one score and one context CTA): K as a ring of Lc blocks [128 tokens x 128 bytes] and two Rc blocks
-// behind it, V as the tile's two halves of 256 channels, each in a place of its own.
-constexpr int KBLK = 2 * BLK, NKB = 2 * NK;
+// Solo (one score and one context CTA): K as a ring of Lc blocks [128 tokens x 128 bytes] and an Rc block behind
+// it, V as the tile's two halves of 256 channels, each in a place of its own.
+constexpr int KBLK = 2 * BLK, NKB = 7;
+static_assert(NKB <= 7 && NKB <= 4 * NK, "their barriers");
 constexpr int OFF_KR = OFF_K + NKB * KBLK;
-constexpr int TOTAL_SOLO_S = OFF_KR + 2 * 2 * RBLK, TOTAL_SOLO_C = OFF_V + 4 * VBLK;
+constexpr int TOTAL_SOLO_S = OFF_KR + 2 * RBLK, TOTAL_SOLO_C = OFF_V + 4 * VBLK;
 constexpr int SMEM_SOLO = TOTAL_SOLO_S > TOTAL_SOLO_C ? TOTAL_SOLO_S : TOTAL_SOLO_C;
 static_assert(SMEM_SOLO <= 232448 && OFF_KR % 1024 == 0, "shared memory above the per-CTA limit");
 // TMEM columns of a score CTA
@@ -356,29 +359,29 @@ __global__ void __cluster_dims__(SOLO ? 2 : 4, 1, 1) __launch_bounds__(NTHREADS,
           const int64_t s1 = pw.slot(a, w, page + 1, lane, rank == 0);
           const uint32_t pages = (s0 >= 0 ? 1u : 0u) + (s1 >= 0 ? 1u : 0u);
           if constexpr (SOLO) {
-            // an Lc block at a time, and the Rc block first
-            if (!wait(B_REMPTY + (g & 1), (uint32_t)(g >> 1) ^ 1u)) {
-              ok = false;
-              break;
-            }
-            const uint32_t rd = smem_u32(sm + OFF_KR) + (g & 1) * 2 * RBLK;
-            mbar_arrive_expect_tx_warp(&bars[B_RFULL + (g & 1)], pages * RBLK);
-            tiles = g + 1;
-            if (s0 >= 0) tma_load_2d_warp(rd, &rmap, DL, (int)s0, &bars[B_RFULL + (g & 1)]);
-            if (s1 >= 0) tma_load_2d_warp(rd + RBLK, &rmap, DL, (int)s1, &bars[B_RFULL + (g & 1)]);
+            // an Lc block at a time, and the Rc block last
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
               const int jb = 4 * g + c, slot = jb % NKB;
-              if (!wait(B_KEMPTY + slot, (uint32_t)(jb / NKB) ^ 1u)) {
+              if (!wait(B_SFREE + slot, (uint32_t)(jb / NKB) ^ 1u)) {
                 ok = false;
                 break;
               }
-              mbar_arrive_expect_tx_warp(&bars[B_KFULL + slot], pages * BLK);
+              mbar_arrive_expect_tx_warp(&bars[B_SFILL + slot], pages * BLK);
               halves = jb + 1;
               const uint32_t dst = kring + slot * KBLK;
-              if (s0 >= 0) tma_load_2d_warp(dst, &kmap, 128 * c, (int)s0, &bars[B_KFULL + slot]);
-              if (s1 >= 0) tma_load_2d_warp(dst + BLK, &kmap, 128 * c, (int)s1, &bars[B_KFULL + slot]);
+              if (s0 >= 0) tma_load_2d_warp(dst, &kmap, 128 * c, (int)s0, &bars[B_SFILL + slot]);
+              if (s1 >= 0) tma_load_2d_warp(dst + BLK, &kmap, 128 * c, (int)s1, &bars[B_SFILL + slot]);
             }
+            if (!ok || !wait(B_REMPTY, (uint32_t)g ^ 1u)) {
+              ok = false;
+              break;
+            }
+            const uint32_t rd = smem_u32(sm + OFF_KR);
+            mbar_arrive_expect_tx_warp(&bars[B_RFULL], pages * RBLK);
+            tiles = g + 1;
+            if (s0 >= 0) tma_load_2d_warp(rd, &rmap, DL, (int)s0, &bars[B_RFULL]);
+            if (s1 >= 0) tma_load_2d_warp(rd + RBLK, &rmap, DL, (int)s1, &bars[B_RFULL]);
           } else {
           const int64_t mine = rank == 0 ? s0 : s1;
           const uint32_t dst = kring + kb * KTILE;
@@ -417,9 +420,8 @@ __global__ void __cluster_dims__(SOLO ? 2 : 4, 1, 1) __launch_bounds__(NTHREADS,
         const int zero = 0;
         if constexpr (SOLO) {
           for (int i = (halves > NKB ? halves - NKB : 0); i < halves; ++i)
-            (void)mbar_wait(&bars[B_KFULL + i % NKB], (i / NKB) & 1, &zero, WAIT_NS);
-          for (int i = (tiles > 2 ? tiles - 2 : 0); i < tiles; ++i)
-            (void)mbar_wait(&bars[B_RFULL + (i & 1)], (i >> 1) & 1, &zero, WAIT_NS);
+            (void)mbar_wait(&bars[B_SFILL + i % NKB], (i / NKB) & 1, &zero, WAIT_NS);
+          if (tiles > 0) (void)mbar_wait(&bars[B_RFULL], (tiles - 1) & 1, &zero, WAIT_NS);
         } else if (rank == 0)
           for (int i = (halves > 2 * NK ? halves - 2 * NK : 0); i < halves; ++i)
             (void)mbar_wait(&bars[B_KFULL + 2 * ((i >> 1) % NK) + (i & 1)], ((i >> 1) / NK) & 1, &zero, WAIT_NS);
@@ -496,7 +498,7 @@ __global__ void __cluster_dims__(SOLO ? 2 : 4, 1, 1) __launch_bounds__(NTHREADS,
 #pragma unroll 1
               for (int c = 0; c < 4; ++c) {
                 const int jb = 4 * g + c, slot = jb % NKB;
-                if (!wait_cluster(B_KFULL + slot, (uint32_t)(jb / NKB))) {
+                if (!wait(B_SFILL + slot, (uint32_t)(jb / NKB))) {
                   ok = false;
                   break;
                 }
@@ -507,7 +509,7 @@ __global__ void __cluster_dims__(SOLO ? 2 : 4, 1, 1) __launch_bounds__(NTHREADS,
                   mma_ts(dl, tmem + T_QH + c * 32 + kk * 8, bd + 2 * kk, id, (c | kk) != 0);
                   mma(dl, ql + (uint64_t)(c * OP_ATOM >> 4) + 2 * kk, bd + 2 * kk, id, 1u);
                 }
-                commit(&bars[B_KEMPTY + slot], 0);
+                commit(&bars[B_SFREE + slot], 0);
               }
             } else {
 #pragma unroll 1
@@ -536,18 +538,18 @@ __global__ void __cluster_dims__(SOLO ? 2 : 4, 1, 1) __launch_bounds__(NTHREADS,
               ok = false;
               break;
             }
-            if (SOLO && !wait_cluster(B_RFULL + (g & 1), (uint32_t)(g >> 1))) {
+            if (SOLO && !wait(B_RFULL, (uint32_t)g)) {
               ok = false;
               break;
             }
             tc_fence_after();
-            const uint64_t rb = SOLO ? rd + (uint64_t)((g & 1) * 2 * RBLK >> 4) : rd + off;
+            const uint64_t rb = SOLO ? rd : rd + off;
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) {
               mma(tmem + T_SR, qr + 2 * kk, rb + 2 * kk, id, kk != 0);
               mma(tmem + T_SR, qr + 4 + 2 * kk, rb + 2 * kk, id, 1u);
             }
-            commit(SOLO ? &bars[B_REMPTY + (g & 1)] : &bars[B_KEMPTY + 2 * kb + 1], 3);
+            commit(SOLO ? &bars[B_REMPTY] : &bars[B_KEMPTY + 2 * kb + 1], 3);
             commit(&bars[B_SFULL + (g & 1)], 3);
           }
           gt += w.n;
@@ -1475,12 +1477,16 @@ Layout layout_of(int B, int H, int64_t total_q, int max_blocks, int G, int64_t w
   return w;
 }
 
-// Which kernel a call goes to, by the rows of its sequences on average: up to 64, the one for few rows
-// (rows.cu); up to 128, that one over few key tiles, else this one's clusters of two.
-constexpr int FEW_ROWS = 64, FEW_TILES = 20;
+// Which kernel a call with a window goes to, by the rows of its sequences on average: up to 64, the one for
+// few rows (rows.cu), which reads a tile of keys for 32 rows at once; up to 128, the clusters of two here,
+// unless there are few (row tile, key tile) units, over which the other spreads better.  Device times of that
+// one, the clusters of two and of four, us, for single tokens of 128 heads: one over 1000 keys 22, 33, 32; 64 over 128
+// keys 35, 28, 40; 32 over 2048 keys 56, 49, 61; 64 over 8192 keys 277, 162, 239.  Of 64 heads, 32 over
+// 2048 keys: 36, 46, 57.
+constexpr int FEW_ROWS = 64, FEW_UNITS = 100;
 bool few_rows(int B, int H, int64_t total_q, int64_t keys) {
   const int64_t rows = total_q * H;
-  return rows <= (int64_t)FEW_ROWS * B || (rows <= 2 * (int64_t)FEW_ROWS * B && keys <= FEW_TILES * TILE);
+  return rows <= (int64_t)FEW_ROWS * B || (rows <= (int64_t)CROWS * B && (int64_t)B * (keys / TILE + 1) <= FEW_UNITS);
 }
 bool solo_rows(int B, int H, int64_t total_q) { return total_q * H <= (int64_t)CROWS * B; }
 int64_t window_keys(int max_blocks, int64_t window, int64_t n_sink) {
@@ -1613,7 +1619,7 @@ int64_t window_workspace(int B, int H, int64_t total_q, int max_blocks, int wind
   return layout_of<kWindow>(B, H, total_q, max_blocks, 0, window, n_sink).bytes;
 }
 int64_t shared_workspace(int B, int H, int64_t total_q, int max_blocks, int G) {
-  if (few_rows(B, H, total_q, INT64_MAX)) return rows_shared_workspace(B, H, total_q, max_blocks, G);
+  if (total_q * H <= (int64_t)FEW_ROWS * B) return rows_shared_workspace(B, H, total_q, max_blocks, G);
   return layout_of<kShared>(B, H, total_q, max_blocks, G, 0, 0).bytes;
 }
 
@@ -1625,7 +1631,7 @@ cudaError_t launch_window(const ChunkArgs& a, void* workspace, cudaStream_t s) {
   return launch<kWindow>(a, workspace, s);
 }
 cudaError_t launch_shared(const ChunkArgs& a, void* workspace, cudaStream_t s) {
-  return few_rows(a.B, a.H, a.total_q, INT64_MAX) ? launch_rows_shared(a, workspace, s) : launch<kShared>(a, workspace, s);
+  return a.total_q * a.H <= (int64_t)FEW_ROWS * a.B ? launch_rows_shared(a, workspace, s) : launch<kShared>(a, workspace, s);
 }
 
 cudaError_t prefix_capacity(int* clusters) { return capacity<kShared>(clusters); }

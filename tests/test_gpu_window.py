@@ -87,6 +87,39 @@ def test_single_tokens_of_many_sequences_in_ranges_that_cross_them(B, T):
     check(WindowCase(16, [1] * B, lens, T // 2, 4, seed=B))
 
 
+@pytest.mark.parametrize("H,nq", [(128, 1), (100, 1), (65, 1), (33, 3), (20, 6), (4, 30)])
+@pytest.mark.parametrize("window,sinks", [(70, 3), (1, 0), (300, 130)])
+def test_65_to_128_rows_a_sequence(H, nq, window, sinks):
+    """Row tiles of 128; more or fewer rows and none in some sequences."""
+    n = [nq] * 96
+    n[5:50:9] = [0] * len(n[5:50:9])
+    n[3], n[70] = 2 * nq, 2 * nq
+    lens = [max(n[i], 1 + (61 * i) % 450) for i in range(96)]
+    check(WindowCase(H, n, lens, window, sinks, seed=H + window, pad=2))
+
+
+def test_128_heads_in_ranges_that_cross_sequences():
+    check(WindowCase(128, [1] * 40, [1500 + 37 * i for i in range(40)], 1000, 64, seed=40))
+    check(WindowCase(128, [1, 1], [9000, 8500], 7000, 4, seed=41))
+
+
+def test_keys_out_of_sight_never_reach_a_row_of_65_to_128():
+    c = WindowCase(128, [1] * 70, [300 + i for i in range(70)], 100, 5, seed=42)
+    clean, clean_l, err = run(c)
+    for b in (0, 30, 69):
+        for at in (5, 63, c.lens_list[b] - 101):
+            slot = int(c.slots[b][at])
+            c.codes[slot] = 0x7F
+            c.codes[slot, ::2] = 0xFF
+            c.scales[slot] = math.nan
+    out, l, err = run(c)
+    assert err == 0 and torch.equal(out, clean) and torch.equal(l, clean_l)
+    c.codes[int(c.slots[7][250])] = 0x7F
+    out, l, err = run(c)
+    hit = torch.arange(70, device="cuda") == 7
+    assert torch.isnan(out[hit]).all() and torch.isnan(l[hit]).all() and torch.equal(out[~hit], clean[~hit])
+
+
 def test_few_rows_that_see_nothing_and_queries_with_nan():
     c = WindowCase(4, [3, 1, 4, 1], [2, 1, 0, 300], 40, 2, seed=17)
     out, l = check(c)
