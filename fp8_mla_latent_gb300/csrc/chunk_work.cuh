@@ -291,7 +291,7 @@ __device__ __forceinline__ int make_entries(const ChunkArgs& a, int64_t* part_ro
       int64_t mine = 0, all;
       for (int b = threadIdx.x; b < a.B; b += 1024) {
         const int4 u = a.entries[a.G + b].u;
-        mine += ((int64_t)u.y * a.H + G::ROWS - 1) / G::ROWS * ((u.z + TILE - 1) / TILE + G::SWITCH);
+        mine += ((int64_t)u.y * a.H + G::ROWS - 1) / G::ROWS * (((int64_t)u.z + TILE - 1) / TILE + G::SWITCH);
       }
       (void)plan_sum(mine, tmp, &all);
       const int64_t apart = all * NARROW<G> / NUM_SMS + START;

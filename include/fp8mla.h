@@ -156,7 +156,7 @@ int kv8_produce_rows(const float* src, int64_t n_rows, int64_t src_row_stride,
  *   signed zeros; NaN stored as 0x00).
  * t and y are rounded to the rows' type where they are written, but not on their way to the
  * codes.  A row whose sum of squares is NaN, or over the range of f32, has no finite y but
- * zeros: codes and scales are 0 then.  The sum has a fixed order for given sizes and alignment
+ * zeros: codes and scales are 0 then (and of a row of zeros with eps 0).  The sum has a fixed order for given sizes and alignment
  * (below), so the same call gives the same bits.
  *
  *   x             device [n_rows] rows of `width` values of dtype (a kv8_dtype), x_row_stride

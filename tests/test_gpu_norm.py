@@ -156,6 +156,51 @@ def test_subnormal_maximum():
     assert 0 < float(scales) < 1e-41
 
 
+@pytest.mark.parametrize("n", [3, 400])
+def test_eps_of_zero(n):
+    """A row of zeros has no norm: NaN in the normed row, codes and scale 0."""
+    x, r, weight = inputs(n, 1024, torch.bfloat16)
+    x[1] = r[1] = 0
+    y = torch.empty_like(x)
+    codes, scales = pkg.kv8_norm_quantize_rows(x, weight, 0.0, residual=r, normed=y)
+    assert torch.isnan(y[1]).all() and (codes[1] == 0).all() and scales[1] == 0
+    keep = torch.arange(n, device="cuda") != 1
+    check(x[keep], r[keep], weight, codes[keep], scales[keep], 0, None, y[keep], eps=0.0)
+
+
+@pytest.mark.parametrize("group", [0, 32, 64, 128, 256])
+@pytest.mark.parametrize("n,w,dtype", [(400, 7168, torch.bfloat16), (400, 8192, torch.float32), (200, 16384, torch.float16),
+                                       (300, 520, torch.float32), (300, 16376, torch.bfloat16), (160, 1000, torch.float16)])
+def test_many_rows_of_every_group_and_type(n, w, dtype, group):
+    for add in (True, False):
+        x, r, weight = inputs(n, w, dtype, seed=w + group, add=add)
+        t, y = torch.empty_like(x), torch.empty_like(x)
+        codes, scales = call(x, r, weight, group, residual_out=t if add else None, normed=y)
+        check(x, r, weight, codes, scales, group, t if add else None, y)
+
+
+@pytest.mark.parametrize("group", [0, 128])
+def test_zeros_nan_and_infinities_among_many_rows(group):
+    x, r, weight = inputs(400, 1024, torch.float32)
+    x[0], r[0] = 0.0, 0.0
+    x[1, 5] = math.nan
+    x[2, 7] = math.inf
+    x[3], r[3] = 1e30, 1e30
+    x[4, 100] = 3e18                   # its square is in range, and the others far below it
+    y = torch.empty_like(x)
+    codes, scales = call(x, r, weight, group, normed=y)
+    for k in (0, 1, 2, 3):
+        assert (codes[k] & 0x7F == 0).all() and (scales[k] == 0).all(), k
+    assert torch.isnan(y[1]).all() and torch.isnan(y[2, 7])
+    check(x[4:], r[4:], weight, codes[4:], scales[4:], group, None, y[4:])
+    weight[200], weight[300] = math.nan, math.inf
+    codes, scales = call(x, r, weight, group, normed=y)
+    assert (codes[4:, 200] == 0).all() and torch.isnan(y[4:, 200]).all()
+    # an infinite y: its scale is infinite, and what it scales is 0
+    assert torch.isinf(scales[5:, 300 // 128 if group else 0]).all()
+    assert (codes[5:, 300] & 0x7F == 0).all()
+
+
 def test_nothing_to_do():
     x, r, weight = inputs(0, 64, torch.bfloat16)
     codes, scales = call(x, r, weight)

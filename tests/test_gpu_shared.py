@@ -109,6 +109,12 @@ def test_rows_that_see_nothing():
     check(SharedCase(16, [5, 1, 1, 3], [2, 900, 900, 0], [4], [850], seed=6))
 
 
+@pytest.mark.parametrize("H", [1, 128])
+def test_more_sequences_than_the_plans_keep_near(H):
+    lens = [65 + (37 * i) % 60 for i in range(1400)]
+    check(SharedCase(H, [1] * 1400, lens, [7] * 200, [64] * 200, seed=32), lse=False)
+
+
 def test_many_sequences_in_many_groups():
     lens = [500 + (37 * i) % 300 for i in range(300)]
     check(SharedCase(4, [1] * 300, lens, [5] * 60, [490] * 60, seed=7), lse=False)

@@ -244,6 +244,45 @@ def test_a_bad_page_in_sight_is_told_and_left_out():
     c.check(out, l, keep=[keep])
 
 
+@pytest.mark.parametrize("H,nq", [(16, 1), (128, 1), (16, 40)])
+def test_lengths_that_cannot_be_are_told_and_clamped(H, nq):
+    """A length over the table's room and one below 0, beside good ones."""
+    B = 70
+    c = WindowCase(H, [nq] * B, [300] * B, 100, 4, seed=43)
+    check(c)
+    c.lens[3], c.lens[5] = 10 ** 6, -7
+    out, l, err = run(c)
+    assert err == -5
+    for b in set(range(B)) - {3, 5}:
+        ref, ref_l, tol, tol_l = c.reference(b)
+        rows = slice(b * nq, (b + 1) * nq)
+        assert ((out[rows].double() - ref).abs() <= tol).all() and ((l[rows] - ref_l).abs() <= tol_l).all(), b
+    assert (out[5 * nq: 6 * nq] == 0).all() and torch.isneginf(l[5 * nq: 6 * nq]).all()
+
+
+@pytest.mark.parametrize("H", [16, 200])
+def test_lengths_near_2_to_the_31(H):
+    """The longest table there is, of whose pages only the last four, the window's, are there."""
+    mb, k = (1 << 25) - 1, 4
+    c = WindowCase(H, [1], [k * PAGE], 200, 0, seed=45)
+    table = torch.full((1, mb), -1, dtype=torch.int32, device="cuda")
+    table[0, mb - k:] = c.table[0, :k]
+    got_l = torch.empty(1, H, device="cuda")
+    ws = pkg.alloc_workspace(pkg.mla_absorb_window_fp8_batch_workspace_size(1, H, 1, mb, 200, 0))
+    got = pkg.mla_absorb_window_fp8_batch(c.q_lat, c.q_rope, c.codes, c.scales, table,
+                                          torch.tensor([mb * PAGE], dtype=torch.int32, device="cuda"), c.start, SM_SCALE,
+                                          200, 0, lse=got_l, workspace=ws)
+    assert pkg.kv8_workspace_error(ws) == 0
+    ref, ref_l, tol, tol_l = c.reference(0)
+    assert ((got.double() - ref).abs() <= tol).all() and ((got_l - ref_l).abs() <= tol_l).all()
+
+
+@pytest.mark.parametrize("H", [1, 65])
+def test_more_sequences_than_the_plan_keeps_near(H):
+    lens = [1 + (37 * i) % 150 for i in range(4200)]
+    check(WindowCase(H, [1] * 4200, lens, 70, 2, seed=46), lse=False)
+
+
 def test_strided_queries():
     c = WindowCase(20, [7, 3], [190, 401], 64, 4, seed=14)
     want, want_l = check(c)
@@ -285,10 +324,11 @@ def test_captured_and_replayed_on_another_stream():
         assert torch.equal(out, want) and torch.equal(l, want_l) and torch.equal(other, want)
 
 
-def test_far_pages():
-    """Cache slots whose bytes lie behind 2^31 and 2^32."""
-    c = WindowCase(16, [2, 1], [400, 300], 150, 4, seed=16)
-    n_blocks = 2 ** 32 // (PAGE * 576) + 200
+@pytest.mark.parametrize("H,B", [(16, 2), (200, 2), (128, 70)])
+def test_far_pages(H, B):
+    """Cache slots whose bytes lie behind 2^31 and 2^32, in each of the kernels."""
+    c = WindowCase(H, [2 if H == 200 else 1] * B, [400 - b for b in range(B)], 150, 4, seed=16)
+    n_blocks = 2 ** 32 // (PAGE * 576) + 800
     want, want_l = check(c)
     codes = torch.full((n_blocks * PAGE, 576), 0x7F, dtype=torch.uint8, device="cuda")
     scales = torch.full((n_blocks * PAGE, 2), math.nan, device="cuda")
