@@ -202,6 +202,15 @@ int kv8_norm_quantize_rows(const void* x, int64_t x_row_stride, const void* resi
   if (!aligned(x, size) || !aligned(residual, size) || !aligned(residual_out, size) ||
       !aligned(normed, size) || !aligned(norm_weight, 4) || !aligned(scales, 4))
     return KV8_EALIGN;
+  // rows written over rows that are read lie as those do, and only one result over them
+  auto over = [&](const void* out, int64_t out_stride, const void* in, int64_t stride) {
+    return out != nullptr && out == in && n_rows > 1 && out_stride != stride;
+  };
+  if (over(residual_out, residual_out_row_stride, x, x_row_stride) ||
+      over(residual_out, residual_out_row_stride, residual, residual_row_stride) ||
+      over(normed, normed_row_stride, x, x_row_stride) || over(normed, normed_row_stride, residual, residual_row_stride) ||
+      (normed != nullptr && normed == residual_out))
+    return KV8_EINVAL;
   NormArgs a{};
   a.x = x;
   a.residual = residual;

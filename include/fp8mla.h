@@ -156,8 +156,8 @@ int kv8_produce_rows(const float* src, int64_t n_rows, int64_t src_row_stride,
  *   signed zeros; NaN stored as 0x00).
  * t and y are rounded to the rows' type where they are written, but not on their way to the
  * codes.  A row whose sum of squares is NaN, or over the range of f32, has no finite y but
- * zeros: codes and scales are 0 then (and of a row of zeros with eps 0).  The sum has a fixed order for given sizes and alignment
- * (below), so the same call gives the same bits.
+ * zeros: codes and scales are 0 then (and those of a row of zeros with eps 0).  The sum has a
+ * fixed order for given sizes and alignment (below), so the same call gives the same bits.
  *
  *   x             device [n_rows] rows of `width` values of dtype (a kv8_dtype), x_row_stride
  *                 (elements, >= 0) apart.
@@ -168,8 +168,8 @@ int kv8_produce_rows(const float* src, int64_t n_rows, int64_t src_row_stride,
  *   eps           finite, >= 0.
  *   n_rows, width n_rows >= 0 (0 launches nothing), 1 <= width <= KV8_NORM_MAX_WIDTH.
  *   group         0, 32, 64, 128 or 256.
- *   normed        y in dtype, rows normed_row_stride apart, or NULL.  It may be x itself, with
- *                 its stride, or residual where that is not residual_out.
+ *   normed        y in dtype, rows normed_row_stride apart, or NULL.  It may be x or residual
+ *                 itself, with that one's stride, but not residual_out.
  *   codes         device uint8, rows codes_row_stride apart.
  *   scales        device f32 [n_rows][1], or [n_rows][ceil(width / group)].
  * Rows are aligned to their elements; strides of what is written are >= width.  Rows of whole
@@ -592,7 +592,7 @@ int kv8_pages_copy(uint8_t* kv_codes, float* kv_scales, int n_layers, int64_t n_
                    unsigned* err_word, void* stream);
 
 /* kv8_workspace_error -- synchronises `stream`, then reports the device-side
- * error word of the last decode or chunk call that used `workspace` (a call with
+ * error word of the last decode, chunk, window or shared call that used `workspace` (a call with
  * nothing to do, B = 0 or total_q = 0, does not): KV8_OK, KV8_EBOUNDS (a bad
  * block-table entry, seq_len or query range) or KV8_ETIMEOUT (a kernel gave up a
  * wait after its bound and returned without a result).  A debugging aid; the calls

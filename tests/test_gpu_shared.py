@@ -240,6 +240,43 @@ def test_captured_and_replayed_with_lengths_that_change():
         assert torch.equal(out, want) and torch.equal(l, want_l)
 
 
+@pytest.mark.parametrize("H,P", [(16, 8000), (128, 4000)])
+def test_two_calls_at_once_and_groups_that_change_in_a_graph(H, P):
+    """Two streams with a workspace each, and a captured call (where sharing pays) whose groups are made anew."""
+    B = 64
+    c = SharedCase(H, [1] * B, [P + 9 + 3 * i for i in range(B)], [32, 32], [P, P], seed=33)
+    want, want_l = check(c)
+    ws, outs = [workspace(c) for _ in range(3)], [torch.zeros_like(want) for _ in range(3)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+
+    def call(i):
+        pkg.mla_absorb_shared_fp8_batch(*c.args(), SM_SCALE, c.group_start, c.shared_len, out=outs[i], workspace=ws[i])
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                outs[i].zero_()
+                call(i)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], outs[1])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(2)
+    groups = c.group_start.clone()
+    for edge, P1 in ((groups, P), (torch.zeros_like(groups), P), (groups // 2, 640), (groups, P)):
+        c.group_start.copy_(edge)
+        c.shared_len.fill_(P1)
+        outs[2].zero_()
+        g.replay()
+        assert pkg.kv8_workspace_error(ws[2]) == 0
+        for b in (0, 15, 16, 31, 32, 63):
+            ref, _, tol, _ = c.reference(b)
+            assert ((outs[2][b].double() - ref[0]).abs() <= tol[0]).all(), (b, P1)
+    assert torch.equal(outs[2], outs[0])
+    for o in outs:
+        c.check(o)
+
+
 def test_fork_append_and_attend():
     """Sequences made by the page calls: a prompt forked eight times, tokens appended, one step of attention."""
     T, n, H = 1000, 8, 16

@@ -324,6 +324,22 @@ def test_captured_and_replayed_on_another_stream():
         assert torch.equal(out, want) and torch.equal(l, want_l) and torch.equal(other, want)
 
 
+@pytest.mark.parametrize("H,nq", [(16, 1), (32, 1), (128, 1), (128, 5)])
+def test_two_calls_at_once(H, nq):
+    c = WindowCase(H, [nq] * 70, [600 + 5 * i for i in range(70)], 300, 4, seed=47)
+    want, _ = check(c)
+    ws = [pkg.alloc_workspace(pkg.mla_absorb_window_fp8_batch_workspace_size(70, H, 70 * nq, c.max_blocks, 300, 4)) for _ in range(2)]
+    outs, streams = [torch.zeros_like(want) for _ in range(2)], [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for w, o, s in zip(ws, outs, streams):
+            with torch.cuda.stream(s):
+                o.zero_()
+                pkg.mla_absorb_window_fp8_batch(*c.args(), SM_SCALE, 300, 4, out=o, workspace=w)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want) and torch.equal(outs[1], want)
+
+
 @pytest.mark.parametrize("H,B", [(16, 2), (200, 2), (128, 70)])
 def test_far_pages(H, B):
     """Cache slots whose bytes lie behind 2^31 and 2^32, in each of the kernels."""

@@ -107,6 +107,10 @@ def test_norm_refuses_bad_arguments():
     for k in ("p_w", "p_s"):
         assert f(**{k: G + 2}) == EALIGN, k
     assert f(n=0) == 0
+    # results over the rows that are read, or over one another
+    apart = dict(p_x=G, p_r=2 * G, p_ro=3 * G, p_y=4 * G, p_c=5 * G, p_s=6 * G, p_w=7 * G)
+    for kw in (dict(p_ro=G, xs=101), dict(p_ro=2 * G, ros=101), dict(p_y=G, ys=101), dict(p_y=2 * G, rs=104), dict(p_y=3 * G)):
+        assert f(**{**apart, **kw}) == EINVAL, kw
 
 
 # ------------------------------------------------------------------ the binding
