@@ -241,12 +241,14 @@ def kv8_norm_quantize_rows(x, norm_weight, eps, residual=None, residual_out=None
         if t is None:
             args += (None, 0)
             continue
-        if not (isinstance(t, _Tensor) and t.dtype is want and _is_device(t) and t.shape == shape
-                and (t.stride(1) == 1 or width == 1)):
+        if not (isinstance(t, _Tensor) and t.dtype is want and t.shape == shape and _is_device(t)):
+            raise ValueError(f"{name} must be a CUDA {want} [{n}, {width}] tensor with unit column stride")
+        step, one = t.stride()
+        if one != 1 and width != 1:
             raise ValueError(f"{name} must be a CUDA {want} [{n}, {width}] tensor with unit column stride")
         if t.get_device() != d:
             raise ValueError("all tensors must be on the same device")
-        args += (t.data_ptr(), t.stride(0) if n > 1 else width)
+        args += (t.data_ptr(), step if n > 1 else width)
     if residual_out is not None and residual is None:
         raise ValueError("residual_out needs residual")
     _need(norm_weight, "norm_weight", _F32, 1)
@@ -515,7 +517,7 @@ def _allocating(stream):
 
 def _device(d):
     """The device of a call's tensors, made current for it (its launch, its default stream)."""
-    return torch.cuda.device(d) if d >= 0 and d != torch.cuda.current_device() else _AS_IS
+    return torch.cuda.device(d) if d >= 0 and d != torch._C._cuda_getDevice() else _AS_IS
 
 
 def _same_device(first, *others):
@@ -610,24 +612,31 @@ def _chunk_call(fn, size, own, q_lat, q_rope, kv_codes, kv_scales, block_table, 
     d, right = -1, False
     try:  # the checks at once: they are most of a call's time on the host
         d = q_lat.get_device()
-        rows, H, _ = q_lat.shape
-        B = seq_lens.numel()
+        rows, H, _ = shape = q_lat.shape
+        lt, lh, l1 = q_lat.stride()
+        rt, rh, r1 = q_rope.stride()
+        slots, _ = kv_codes.shape
+        B, max_blocks = block_table.shape
+        if rows == 1:  # (as _strides)
+            lt = rt = 0
+        if H == 1:
+            lh = rh = 0
         right = (
-            d >= 0 and q_lat.shape == (rows, H, 512) and q_lat.dtype is _BF16 and q_lat.stride(2) == 1
-            and q_rope.shape == (rows, H, 64) and q_rope.dtype is _BF16 and q_rope.stride(2) == 1
+            d >= 0 and shape == (rows, H, 512) and q_lat.dtype is _BF16 and l1 == 1
+            and q_rope.shape == (rows, H, 64) and q_rope.dtype is _BF16 and r1 == 1
             and q_rope.get_device() == d
-            and kv_codes.dtype is _U8 and kv_codes.is_contiguous() and kv_codes.get_device() == d
-            and kv_codes.shape == (kv_codes.shape[0], 576) and kv_scales.shape == (kv_codes.shape[0], 2)
-            and kv_scales.dtype is _F32 and kv_scales.is_contiguous() and kv_scales.get_device() == d
+            and kv_codes.shape == (slots, 576) and kv_codes.dtype is _U8 and kv_codes.is_contiguous()
+            and kv_codes.get_device() == d
+            and kv_scales.shape == (slots, 2) and kv_scales.dtype is _F32 and kv_scales.is_contiguous()
+            and kv_scales.get_device() == d
             and block_table.dtype is _I32 and block_table.is_contiguous() and block_table.get_device() == d
-            and block_table.dim() == 2 and block_table.shape[0] == B
-            and seq_lens.dtype is _I32 and seq_lens.dim() == 1 and seq_lens.is_contiguous()
+            and seq_lens.shape == (B,) and seq_lens.dtype is _I32 and seq_lens.is_contiguous()
             and seq_lens.get_device() == d
-            and q_start.dtype is _I32 and q_start.shape == (B + 1,) and q_start.is_contiguous()
+            and q_start.shape == (B + 1,) and q_start.dtype is _I32 and q_start.is_contiguous()
             and q_start.get_device() == d
-            and (out is None or (out.dtype is _BF16 and out.shape == (rows, H, 512) and out.is_contiguous()
+            and (out is None or (out.shape == (rows, H, 512) and out.dtype is _BF16 and out.is_contiguous()
                                  and out.get_device() == d))
-            and (lse is None or (lse.dtype is _F32 and lse.shape == (rows, H) and lse.is_contiguous()
+            and (lse is None or (lse.shape == (rows, H) and lse.dtype is _F32 and lse.is_contiguous()
                                  and lse.get_device() == d))
             and (workspace is None or (workspace.is_contiguous() and workspace.get_device() == d)))
         for t in also:
@@ -638,24 +647,37 @@ def _chunk_call(fn, size, own, q_lat, q_rope, kv_codes, kv_scales, block_table, 
         _chunk_checks(q_lat, q_rope, kv_codes, kv_scales, block_table, seq_lens, q_start, out, lse, workspace,
                       also)
         rows, H, _ = q_lat.shape
-    B, max_blocks = block_table.shape
+        (lt, lh), (rt, rh) = _strides(q_lat), _strides(q_rope)
+        slots = kv_codes.shape[0]
+        B, max_blocks = block_table.shape
     need = _size(fn + "_workspace_size", B, H, rows, max_blocks, *size)
     if need < 0:
         globals()[fn + "_workspace_size"](B, H, rows, max_blocks, *size)  # (raises, in its words)
-    if out is None or workspace is None:
+    if out is None:
         with _allocating(stream):
-            if out is None:
-                out = torch.empty((rows, H, KV8_DL), dtype=torch.bfloat16, device=q_lat.device)
-            if workspace is None:
-                workspace = alloc_workspace(need, q_lat.device)
+            out = torch.empty((rows, H, KV8_DL), dtype=torch.bfloat16, device=q_lat.device)
+    if workspace is None and d < 0:
+        workspace = alloc_workspace(need, q_lat.device)
     block_size = int(block_size)
     with _device(d):
-        st = getattr(lib(), fn)(
-            q_lat.data_ptr(), *_strides(q_lat), q_rope.data_ptr(), *_strides(q_rope),
-            kv_codes.data_ptr(), kv_scales.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
-            q_start.data_ptr(), rows, B, H, max_blocks, block_size, kv_codes.shape[0] // block_size, *own,
-            float(sm_scale), out.data_ptr(), None if lse is None else lse.data_ptr(),
-            workspace.data_ptr(), workspace.nbytes, _stream(stream))
+        stream = _stream(stream) if stream is not None or d < 0 else torch._C._cuda_getCurrentRawStream(d)
+        # A workspace of the call's own is the stream's memory, from torch's allocator without a tensor around it
+        # (which takes 6 us of a call's 25), and given back where the call is queued: what the stream runs later may have it.
+        own_ws = None
+        if workspace is None:
+            nbytes = need if need > 256 else 256
+            at = own_ws = torch._C._cuda_cudaCachingAllocator_raw_alloc(nbytes, stream)
+        else:
+            at, nbytes = workspace.data_ptr(), workspace.nbytes
+        try:
+            st = getattr(lib(), fn)(
+                q_lat.data_ptr(), lt, lh, q_rope.data_ptr(), rt, rh, kv_codes.data_ptr(), kv_scales.data_ptr(),
+                block_table.data_ptr(), seq_lens.data_ptr(), q_start.data_ptr(), rows, B, H, max_blocks,
+                block_size, slots // block_size, *own, float(sm_scale), out.data_ptr(),
+                None if lse is None else lse.data_ptr(), at, nbytes, stream)
+        finally:
+            if own_ws is not None:
+                torch._C._cuda_cudaCachingAllocator_raw_delete(own_ws)
     if st != 0:
         raise Kv8Error(fn, st)
     return out
