@@ -112,12 +112,12 @@ __device__ __forceinline__ int limit_of(const ChunkArgs& a, const SeqInfo<MODE>&
 }
 template <class G>
 __device__ __forceinline__ int first_token(const ChunkArgs& a, int rt) {
-  return (int)((uint32_t)(rt * G::ROWS) / (uint32_t)a.H);
+  return (int)((uint32_t)rt * G::ROWS / (uint32_t)a.H);
 }
 template <class G, int MODE>
 __device__ __forceinline__ int last_token(const ChunkArgs& a, const SeqInfo<MODE>& s, int rt) {
-  const int64_t last = ((int64_t)rt * G::ROWS + G::ROWS - 1) / a.H;
-  return last < s.nq ? (int)last : s.nq - 1;
+  const int last = (int)(((uint32_t)rt * G::ROWS + G::ROWS - 1) / (uint32_t)a.H);  // (2^31 rows at most)
+  return last < s.nq ? last : s.nq - 1;
 }
 // A window's first key, of a row that sees keys up to lim.
 __device__ __forceinline__ int window_from(const ChunkArgs& a, int lim) { return lim > a.window ? lim - a.window : 0; }
@@ -148,31 +148,48 @@ __device__ __forceinline__ int key_tiles(const ChunkArgs& a, const SeqInfo<MODE>
   return lim > 0 ? (lim - 1) / TILE + 1 : 1;
 }
 
-__device__ __forceinline__ int64_t plan_sum(int64_t v, int64_t* tmp, int64_t* total) {
-  // inclusive sum over 1024 threads
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += u;
+// What a plan reads first, asked for before anything else it does.
+__device__ __forceinline__ void plan_prefetch(const ChunkArgs& a) {
+  for (int b = threadIdx.x; b < a.B && b < 2 * (int)blockDim.x; b += blockDim.x) {
+    asm volatile("prefetch.global.L1 [%0];" ::"l"(a.q_start + b) : "memory");
+    asm volatile("prefetch.global.L1 [%0];" ::"l"(a.seq_lens + b) : "memory");
   }
-  if (lane == 31) tmp[warp] = v;
-  __syncthreads();
-  if (warp == 0) {
-    int64_t w = tmp[lane];
+}
+
+// A plan is one CTA's of PLAN_THREADS threads, whose sums follow one another with a barrier each.
+constexpr int PLAN_THREADS = 512, PLAN_WARPS = PLAN_THREADS / 32;
+struct PlanScratch {
+  int64_t sums[2][PLAN_WARPS];   // of the warps, in turn
+  // row tiles, if they are as few: where they begin, their sequence and their place there
+  int64_t tile[PLAN_THREADS];
+  int2 of[PLAN_THREADS];
+};
+struct PlanSum {
+  PlanScratch& at;
+  int turn = 0;
+  // inclusive sum over the CTA's threads (of which those from `count` on have nothing to add), and the total
+  __device__ __forceinline__ int64_t operator()(int64_t v, int64_t count, int64_t* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t u = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += u;
+      const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
     }
-    tmp[lane] = w;
+    int64_t* sums = at.sums[turn];
+    turn ^= 1;  // (its next use lies behind the next sum's barrier)
+    if (lane == 31) sums[warp] = v;
+    __syncthreads();
+    int64_t before = 0, all = 0;
+    const int warps = count < PLAN_THREADS ? (int)(count + 31) >> 5 : PLAN_WARPS;
+    for (int w = 0; w < warps; ++w) {
+      const int64_t u = sums[w];
+      before += w < warp ? u : 0;
+      all += u;
+    }
+    *total = all;
+    return v + before;
   }
-  __syncthreads();
-  if (warp > 0) v += tmp[warp - 1];
-  *total = tmp[31];
-  __syncthreads();
-  return v;
-}
+};
 
 // Sequences that share a prefix.  The rows of a group's sequences lie behind one another, so that the
 // prefix is one more sequence, whose rows are the group's and which all of them see whole, and the
@@ -211,10 +228,10 @@ __device__ __forceinline__ int64_t warp_min(int64_t v) {
   return v;
 }
 
-// Whether the groups' ranges break their order (by a whole CTA of 1024 threads); that and lengths below 0 are told.
+// Whether the groups' ranges break their order (by a plan's CTA); that and lengths below 0 are told.
 __device__ __forceinline__ bool groups_bad(const ChunkArgs& a, bool tell) {
   int bad = 0;
-  for (int g = threadIdx.x; g < a.G; g += 1024) {
+  for (int g = threadIdx.x; g < a.G; g += PLAN_THREADS) {
     const int f = __ldg(&a.group_start[g]), l = __ldg(&a.group_start[g + 1]);
     bad |= f < 0 || l < f || l > a.B;
     if (tell && __ldg(&a.shared_len[g]) < 0) atomicOr(a.err, ERR_SEQ_LEN);
@@ -224,21 +241,21 @@ __device__ __forceinline__ bool groups_bad(const ChunkArgs& a, bool tell) {
   return bad;
 }
 
-// (By a whole CTA of 1024 threads.)  The result: the clusters that the prefixes get beside a kernel for few rows,
+// (By a plan's CTA.)  The result: the clusters that the prefixes get beside a kernel for few rows,
 // `most` at most of the `clusters` there are.
 template <class G>
-__device__ __forceinline__ int make_entries(const ChunkArgs& a, int64_t* part_rows, int64_t* tmp, bool tell, int most = 0,
+__device__ __forceinline__ int make_entries(const ChunkArgs& a, int64_t* part_rows, PlanSum& plan_sum, bool tell, int most = 0,
                                             int clusters = 0) {
   constexpr bool FEW = G::ROWS < WideGeo::ROWS;
   __shared__ unsigned long long sums[2];  // units that the groups save, and those of their prefixes
   if (threadIdx.x < 2) sums[threadIdx.x] = 0ull;
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int g = threadIdx.x; g < a.G; g += 1024) {
+  for (int g = threadIdx.x; g < a.G; g += PLAN_THREADS) {
     a.entries[g].u = make_int4(0, 0, 0, 0);
     a.entries[g].v = make_int4(0, 0, -1, 0);
   }
-  for (int b = threadIdx.x; b < a.B; b += 1024) {
+  for (int b = threadIdx.x; b < a.B; b += PLAN_THREADS) {
     const SeqInfo<kPlain> s = seq_info<kPlain>(a, b, tell);
     a.entries[a.G + b].u = make_int4((int)s.q0, s.nq, s.T, b);
     a.entries[a.G + b].v = make_int4(0, a.causal, -1, 0);
@@ -246,7 +263,7 @@ __device__ __forceinline__ int make_entries(const ChunkArgs& a, int64_t* part_ro
   if (threadIdx.x == 0) *part_rows = 0;
   if (groups_bad(a, tell) || a.G == 0) return 0;  // (ranges that may overlap: nothing is shared)
   // what each group would share, a warp per group
-  for (int g = warp; g < a.G; g += 32) {
+  for (int g = warp; g < a.G; g += PLAN_WARPS) {
     const int f = __ldg(&a.group_start[g]), l = __ldg(&a.group_start[g + 1]);
     int64_t P = __ldg(&a.shared_len[g]), apart = 0, tokens = 0, members = 0, q0 = INT32_MAX, row = INT32_MAX;
     for (int b = f + lane; b < l; b += 32) {
@@ -289,16 +306,18 @@ __device__ __forceinline__ int make_entries(const ChunkArgs& a, int64_t* part_ro
     bool worth = saved - wide > WORTH;
     if constexpr (FEW) {
       int64_t mine = 0, all;
-      for (int b = threadIdx.x; b < a.B; b += 1024) {
+      for (int b = threadIdx.x; b < a.B; b += PLAN_THREADS) {
         const int4 u = a.entries[a.G + b].u;
         mine += ((int64_t)u.y * a.H + G::ROWS - 1) / G::ROWS * (((int64_t)u.z + TILE - 1) / TILE + G::SWITCH);
       }
-      (void)plan_sum(mine, tmp, &all);
+      (void)plan_sum(mine, a.B, &all);
       const int64_t apart = all * NARROW<G> / NUM_SMS + START;
       int64_t best = INT64_MAX;
       for (int t = 1 + lane; t <= most && t < clusters; t += 32) {
-        const int64_t x = wide * WIDE_CYCLES / t + START_WIDE, y = (all - saved) * NARROW<G> / (NUM_SMS - 4 * t) + START;
-        const int64_t z = ((x > y ? x : y) + JOIN_MORE) * 64 + t;  // (t < 64)
+        // (estimates: f32 does, and its divisions are the cheaper ones)
+        const float x = (float)(wide * WIDE_CYCLES) / (float)t + START_WIDE;
+        const float y = (float)((all - saved) * NARROW<G>) / (float)(NUM_SMS - 4 * t) + START;
+        const int64_t z = (int64_t)(fmaxf(x, y) + JOIN_MORE) * 64 + t;  // (t < 64)
         best = z < best ? z : best;
       }
       best = warp_min(best);
@@ -306,18 +325,18 @@ __device__ __forceinline__ int make_entries(const ChunkArgs& a, int64_t* part_ro
       split = (int)(best % 64);
     }
     if (!worth && a.share != KV8_SHARE_ALWAYS) {
-      for (int g = threadIdx.x; g < a.G; g += 1024) a.entries[g].u.y = 0;
+      for (int g = threadIdx.x; g < a.G; g += PLAN_THREADS) a.entries[g].u.y = 0;
       __syncthreads();
       return 0;
     }
   }
   // the rows of their parts, as far as there is room
   int64_t at = 0;
-  for (int g0 = 0; g0 < a.G; g0 += 1024) {
+  for (int g0 = 0; g0 < a.G; g0 += PLAN_THREADS) {
     const int g = g0 + threadIdx.x;
     const int64_t rows = g < a.G ? (int64_t)a.entries[g].u.y * a.H : 0;
     int64_t sum;
-    const int64_t from = at + plan_sum(rows, tmp, &sum) - rows;
+    const int64_t from = at + plan_sum(rows, a.G - g0, &sum) - rows;
     if (rows > 0) {
       // (the groups that have room are the first ones: those behind one without begin further on)
       if (from + rows <= a.part_rows) {
@@ -330,7 +349,7 @@ __device__ __forceinline__ int make_entries(const ChunkArgs& a, int64_t* part_ro
     at += sum;
   }
   __syncthreads();
-  for (int g = warp; g < a.G; g += 32) {
+  for (int g = warp; g < a.G; g += PLAN_WARPS) {
     const int4 u = a.entries[g].u;
     if (u.y == 0) continue;
     const int f = __ldg(&a.group_start[g]), l = __ldg(&a.group_start[g + 1]), from = a.entries[g].v.z;
@@ -352,42 +371,53 @@ __device__ __forceinline__ int make_entries(const ChunkArgs& a, int64_t* part_ro
 // owner[p] of row tile p: its sequence, its place there, the slot of its first part -- slot 2 k is the first
 // segment of range k, 2 k + 1 its last -- and the last range that it lies in.
 //
-// One CTA of 1024 threads: row tiles before each of n_seq sequences (base), the units of every row tile, their
+// One CTA of PLAN_THREADS threads: row tiles before each of n_seq sequences (base, and
+// base_out for who reads the plan), the units of every row tile, their
 // total, and the row tile that each range starts in; with `unit`, the units before each row tile, and
 // with `owner`, whose it is.  (The sequences are the call's, or entries, from `first` on, and `shift` further on
 // for who reads the plan.)
 template <int MODE, class G>
-__device__ __forceinline__ void make_plan(const ChunkArgs& a, Plan<G>* plan, int64_t* base, int first, int shift, int n_seq,
-                                          int most, int64_t* tmp, int64_t* unit, int4* owner) {
+__device__ __forceinline__ void make_plan(const ChunkArgs& a, Plan<G>* plan, int64_t* base, int64_t* base_out, int first, int shift,
+                                          int n_seq, int most, PlanSum& plan_sum, int64_t* unit, int4* owner) {
+  static_assert(G::RANGES <= PLAN_THREADS, "a thread per range");
+  PlanScratch& sh = plan_sum.at;
   int64_t pairs = 0;
-  for (int b0 = 0; b0 < n_seq; b0 += 1024) {
+  for (int b0 = 0; b0 < n_seq; b0 += PLAN_THREADS) {
     const int b = b0 + threadIdx.x;
     const int64_t n = b < n_seq ? row_tiles<G>(a, seq_info<MODE>(a, first + b, true)) : 0;
     int64_t sum;
-    const int64_t inc = plan_sum(n, tmp, &sum);
-    if (b < n_seq) base[b] = pairs + inc - n;
+    const int64_t inc = plan_sum(n, n_seq - b0, &sum);
+    if (b < n_seq) {
+      base[b] = pairs + inc - n;
+      if (base_out != nullptr) base_out[b] = pairs + inc - n;
+    }
     pairs += sum;
   }
   if (threadIdx.x == 0) base[n_seq] = pairs;
   __syncthreads();
-  int b = 0, rt = 0;
-  auto tiles = [&](int64_t p) -> int64_t {
-    if (p >= pairs) return 0;
+  // row tile p's sequence (of these) and its place there
+  auto find = [&](int64_t p, int* rt) -> int {
     int lo = 0, hi = n_seq;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (base[mid] <= p) lo = mid; else hi = mid;
     }
-    b = first + lo;
-    rt = (int)(p - base[lo]);
+    *rt = (int)(p - base[lo]);
+    return first + lo;
+  };
+  int b = 0, rt = 0;
+  auto tiles = [&](int64_t p) -> int64_t {
+    if (p >= pairs) return 0;
+    b = find(p, &rt);
     Pages<MODE> pages;
     return key_tiles<G>(a, seq_info<MODE>(a, b, false), rt, &pages);
   };
   // The ranges are equal on an axis where a row tile is G::SWITCH + nt long, and the border falls on a
   // key tile of it; x counts units (key tiles).
+  const bool few = pairs <= PLAN_THREADS;
   int64_t mine = 0, units;
-  for (int64_t p = threadIdx.x; p < pairs; p += 1024) mine += tiles(p);
-  (void)plan_sum(mine, tmp, &units);
+  for (int64_t p = threadIdx.x; p < pairs; p += PLAN_THREADS) mine += tiles(p);
+  const int64_t upto = plan_sum(mine, pairs, &units);
   const int64_t total = units + pairs * G::SWITCH;
   int64_t nc = units / G::MIN_TILES > pairs ? units / G::MIN_TILES : pairs;
   nc = nc > most ? most : (nc < 1 ? (units > 0 ? 1 : 0) : nc);
@@ -397,31 +427,60 @@ __device__ __forceinline__ void make_plan(const ChunkArgs& a, Plan<G>* plan, int
     plan->tiles = pairs;
     if (unit != nullptr) unit[pairs] = units;
   }
-  int64_t at = 0;
-  for (int64_t p0 = 0; p0 < pairs; p0 += 1024) {
-    const int64_t p = p0 + threadIdx.x, n = pairs <= 1024 ? mine : tiles(p);
-    int64_t sum;
-    const int64_t before = at + plan_sum(n, tmp, &sum) - n;  // units before the row tile
-    const int64_t S = before + p * G::SWITCH, len = n + G::SWITCH;
-    if (unit != nullptr && p < pairs) unit[p] = before;
-    int64_t k = n > 0 ? S * nc / total : nc;
-    while (k < nc && k * total / nc < S) ++k;
-    int64_t held = k - 1;  // the range that holds its first unit: one from before, or the last that begins there
-    bool before_it = true;
-    for (; k < nc; ++k) {
-      const int64_t x = k * total / nc;
-      if (x >= S + len) break;
-      PlanEntry e;
-      e.b = b + shift;
-      e.rt = rt;
-      e.nt = (int32_t)n;
-      e.off = (int32_t)(x - S > G::SWITCH ? x - S - G::SWITCH : 0);
-      e.x = before + e.off;
-      plan->e[k] = e;
-      if (e.off == 0) held = k, before_it = false;
+  // Range k begins at k total / nc, so that as many as at nc / total, rounded up, begin before `at`.  (Its products
+  // have 32 bits as a rule, and a division of 64 takes five times as long.)
+  const bool narrow = total < INT32_MAX / NUM_SMS;
+  auto divide = [&](int64_t x, int64_t by) -> int64_t { return narrow ? (int64_t)((uint32_t)x / (uint32_t)by) : x / by; };
+  auto ranges_before = [&](int64_t at) -> int { return (int)divide(at * nc + total - 1, total); };
+  auto entry = [&](int k, int64_t x, int seq, int place, int64_t n, int64_t S, int64_t before) {
+    PlanEntry e;
+    e.b = seq + shift;
+    e.rt = place;
+    e.nt = (int32_t)n;
+    e.off = (int32_t)(x - S > G::SWITCH ? x - S - G::SWITCH : 0);
+    e.x = before + e.off;
+    plan->e[k] = e;
+  };
+  if (few) {
+    if (threadIdx.x < pairs) {
+      sh.tile[threadIdx.x] = upto - mine + threadIdx.x * G::SWITCH;
+      sh.of[threadIdx.x] = make_int2(b, rt);
     }
-    if (owner != nullptr && p < pairs) owner[p] = make_int4(b + shift, rt, (int)(2 * held + before_it), (int)(k - 1));
-    at += sum;
+    __syncthreads();
+    // a thread per range, which finds its row tile (the last threads, beside the first ones' row tiles)
+    const int k = PLAN_THREADS - 1 - (int)threadIdx.x;
+    if (k < nc) {
+      const int64_t x = divide(k * total, nc);
+      int lo = 0, hi = (int)pairs;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (sh.tile[mid] <= x) lo = mid; else hi = mid;
+      }
+      const int64_t S = sh.tile[lo], end = lo + 1 < pairs ? sh.tile[lo + 1] : total;
+      entry(k, x, sh.of[lo].x, sh.of[lo].y, end - S - G::SWITCH, S, S - (int64_t)lo * G::SWITCH);
+    }
+  }
+  int64_t at = 0;
+  for (int64_t p0 = 0; p0 < pairs; p0 += PLAN_THREADS) {  // a thread per row tile
+    const int64_t p = p0 + threadIdx.x;
+    int64_t n = mine, before = upto - mine;  // units before the row tile
+    if (!few) {
+      int64_t sum;
+      n = tiles(p);
+      before = at + plan_sum(n, pairs - p0, &sum) - n;
+      at += sum;
+    }
+    if (p >= pairs) continue;
+    if (unit != nullptr) unit[p] = before;
+    const int64_t S = before + p * G::SWITCH;
+    const int k0 = ranges_before(S), k1 = ranges_before(S + G::SWITCH + n);
+    if (owner != nullptr) {
+      // the range that holds its first unit: the last that begins there, or one from before
+      const int kh = ranges_before(S + G::SWITCH + 1);
+      owner[p] = make_int4(b + shift, rt, 2 * (kh - 1) + (kh > k0 ? 0 : 1), k1 - 1);
+    }
+    if (!few)
+      for (int k = k0; k < k1; ++k) entry(k, divide(k * total, nc), b, rt, n, S, before);
   }
 }
 
@@ -616,34 +675,51 @@ __global__ void __launch_bounds__(JOIN_ROWS * 32) parts_join_kernel(const ChunkA
     }
     return (int64_t)(j == 0 ? of.z : 2 * (k0 + j)) * N + row;
   };
-  float M = -INFINITY, L = 0.f;
-  for (int j = lane; j < n; j += 32) M = fmaxf(M, ps.m[slot(j)]);
+  // (the first parts' values are asked for together with the weights of all of them, and the others four at a time)
+  constexpr int Q = 4 / SPLIT, AT_ONCE = 4;  // 16-byte units a lane
+  float4 v[AT_ONCE][Q], acc[Q];
+  auto ask = [&](int j0) {
+#pragma unroll
+    for (int i = 0; i < AT_ONCE; ++i) {
+      if (j0 + i >= n) break;
+      const float4* o = reinterpret_cast<const float4*>(ps.o + slot(j0 + i) * DL + ch) + lane;
+#pragma unroll
+      for (int c = 0; c < Q; ++c) v[i][c] = o[32 * c];
+    }
+  };
+  float M = -INFINITY, L = 0.f, m0 = -INFINITY, l0 = 0.f;
+  if (lane < n) {
+    M = m0 = ps.m[slot(lane)];
+    l0 = ps.l[slot(lane)];
+  }
+  ask(0);
+  for (int j = lane + 32; j < n; j += 32) M = fmaxf(M, ps.m[slot(j)]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  constexpr int Q = 4 / SPLIT;  // 16-byte units a lane
-  float4 acc[Q];
 #pragma unroll
   for (int c = 0; c < Q; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int j0 = 0; j0 < n; j0 += 32) {
     const int j = j0 + lane;
     float wt = 0.f;
     if (j < n) {
-      const float m = ps.m[slot(j)];
+      const float m = j0 == 0 ? m0 : ps.m[slot(j)];
       wt = m > -INFINITY ? ex2_approx(m - M) : 1.f;  // (a NaN l stays one)
-      L += wt * ps.l[slot(j)];
+      L += wt * (j0 == 0 ? l0 : ps.l[slot(j)]);
     }
     const int some = min(n - j0, 32);
-#pragma unroll(SPLIT == 1 ? 4 : 8)
-    for (int i = 0; i < some; ++i) {
-      const float w = __shfl_sync(0xffffffffu, wt, i);
-      const float4* o = reinterpret_cast<const float4*>(ps.o + slot(j0 + i) * DL + ch) + lane;
+    for (int i0 = 0; i0 < some; i0 += AT_ONCE) {
+      if (j0 + i0 > 0) ask(j0 + i0);
 #pragma unroll
-      for (int c = 0; c < Q; ++c) {
-        const float4 v = o[32 * c];
-        acc[c].x += w * v.x;
-        acc[c].y += w * v.y;
-        acc[c].z += w * v.z;
-        acc[c].w += w * v.w;
+      for (int i = 0; i < AT_ONCE; ++i) {
+        if (i0 + i >= some) break;
+        const float w = __shfl_sync(0xffffffffu, wt, i0 + i);
+#pragma unroll
+        for (int c = 0; c < Q; ++c) {
+          acc[c].x += w * v[i][c].x;
+          acc[c].y += w * v[i][c].y;
+          acc[c].z += w * v[i][c].z;
+          acc[c].w += w * v[i][c].w;
+        }
       }
     }
   }

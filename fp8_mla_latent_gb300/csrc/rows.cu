@@ -761,47 +761,52 @@ constexpr int PLAN_NEAR = 4096;
 
 // (base: in shared memory if it fits)
 template <int MODE, int N>
-__global__ void __launch_bounds__(1024) rows_plan_kernel(const ChunkArgs a, Plan<Geo<N>>* plan, int64_t* base, int4* owner,
+__global__ void __launch_bounds__(PLAN_THREADS) rows_plan_kernel(const ChunkArgs a, Plan<Geo<N>>* plan, int64_t* base, int4* owner,
                                                          int most) {
   grid_dependents_launch();
-  __shared__ int64_t tmp[32];
+  __shared__ PlanScratch scratch;
+  PlanSum sums{scratch};
   __shared__ int64_t near[PLAN_NEAR];
+  plan_prefetch(a);
   if (threadIdx.x == 0) *a.err = 0;
   __syncthreads();
   if (MODE == kPlain && a.G > 0) (void)groups_bad(a, true);  // (groups too small to share anything)
-  make_plan<MODE>(a, plan, a.B < PLAN_NEAR ? near : base, 0, 0, a.B, most, tmp, nullptr, owner);
+  make_plan<MODE>(a, plan, a.B < PLAN_NEAR ? near : base, nullptr, 0, 0, a.B, most, sums, nullptr, owner);
 }
 
 // The plans of a call with shared prefixes, each with a copy of the entries of its own, one behind the other:
 // block 0 that of the prefixes (whose base the join reads), block 1 that of the sequences.  (The entries are
 // worked on in shared memory if they fit.)
-constexpr int ENTRIES_NEAR = 1024, SHARED_NEAR = 1024;
+constexpr int ENTRIES_NEAR = 1024, SHARED_NEAR = 512;
 
 template <int N>
-__global__ void __launch_bounds__(1024) rows_shared_plan_kernel(const ChunkArgs a, Plan<Geo<N>>* plan, int64_t* base,
+__global__ void __launch_bounds__(PLAN_THREADS) rows_shared_plan_kernel(const ChunkArgs a, Plan<Geo<N>>* plan, int64_t* base,
                                                                 int4* owner, int most, Plan<WideGeo>* prefix_plan,
                                                                 int64_t* prefix_base, int4* prefix_owner,
                                                                 int prefix_most, int clusters) {
   grid_dependents_launch();
-  __shared__ int64_t tmp[32];
+  __shared__ PlanScratch scratch;
+  PlanSum sums{scratch};
   __shared__ int64_t near[SHARED_NEAR];
   __shared__ ChunkEntry entries_near[ENTRIES_NEAR];
   const bool own = blockIdx.x == 1;
   const int n = a.G + a.B;
+  plan_prefetch(a);
   if (own && threadIdx.x == 0) *a.err = 0;
   __syncthreads();
   ChunkEntry* entries = a.entries + (own ? n : 0);
   ChunkArgs c = a;
   c.entries = n <= ENTRIES_NEAR ? entries_near : entries;
-  const int split = make_entries<Geo<N>>(c, own ? &plan->part_rows : &prefix_plan->part_rows, tmp, own, prefix_most, clusters);
+  const int split = make_entries<Geo<N>>(c, own ? &plan->part_rows : &prefix_plan->part_rows, sums, own, prefix_most, clusters);
   if (n <= ENTRIES_NEAR)
-    for (int i = threadIdx.x; i < n; i += 1024) entries[i] = entries_near[i];
+    for (int i = threadIdx.x; i < n; i += PLAN_THREADS) entries[i] = entries_near[i];
   if (own) {
     const int left = NUM_SMS - 4 * split;
-    make_plan<kShared>(c, plan, a.B < SHARED_NEAR ? near : base, a.G, n, a.B, most < left ? most : left, tmp, nullptr, owner);
+    make_plan<kShared>(c, plan, a.B < SHARED_NEAR ? near : base, nullptr, a.G, n, a.B, most < left ? most : left, sums, nullptr, owner);
   } else {
     if (threadIdx.x == 0) prefix_plan->ready = 0u;
-    make_plan<kShared>(c, prefix_plan, prefix_base, 0, 0, a.G, split, tmp, nullptr, prefix_owner);
+    make_plan<kShared>(c, prefix_plan, a.G < SHARED_NEAR ? near : prefix_base, a.G < SHARED_NEAR ? prefix_base : nullptr, 0, 0,
+                       a.G, split, sums, nullptr, prefix_owner);
   }
 }
 
@@ -903,14 +908,14 @@ cudaError_t launch(ChunkArgs a, const Layout& w, void* workspace, cudaStream_t s
     a.entries = reinterpret_cast<ChunkEntry*>(p + w.entries);
     a.part_rows = w.part_rows;
     Plan<WideGeo>* prefix_plan = reinterpret_cast<Plan<WideGeo>*>(p + OFF_PREFIX_PLAN);
-    rows_shared_plan_kernel<N><<<2, 1024, 0, s>>>(a, ps.plan, base, owner, w.most, prefix_plan, prefix_base, prefix_owner,
+    rows_shared_plan_kernel<N><<<2, PLAN_THREADS, 0, s>>>(a, ps.plan, base, owner, w.most, prefix_plan, prefix_base, prefix_owner,
                                                   clusters, fit);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     e = launch_prefixes(a, PrefixParts{prefix_plan, m, l, o, w.prefix_slots + w.slots}, clusters, kmap, rmap, smap, s);
     if (e != cudaSuccess) return e;
     ready = &prefix_plan->ready;
   } else {
-    rows_plan_kernel<MODE, N><<<1, 1024, 0, s>>>(a, ps.plan, base, owner, w.most);
+    rows_plan_kernel<MODE, N><<<1, PLAN_THREADS, 0, s>>>(a, ps.plan, base, owner, w.most);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   e = launch_after_prep(rows_kernel<MODE, N>, w.most, NTHREADS, Cfg<N>::SMEM, s, a, ps, ready, kmap, rmap, smap);
