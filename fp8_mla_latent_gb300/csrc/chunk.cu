@@ -1607,7 +1607,7 @@ cudaError_t launch_solo(ChunkArgs a, const SoloLayout& w, void* workspace, cudaS
   e = launch_after_prep(chunk_kernel<kWindow, true>, 2 * clusters, NTHREADS, SMEM_SOLO, s, a, ws, kmap, rmap, smap);
   if (e != cudaSuccess || clusters == 1) return e;
   return launch_parts_join<kWindow, CROWS>(a, PartsJoin{&ws.plan->tiles, owner, ws.m, ws.l, ws.o, 0, nullptr, nullptr, 0},
-                                           w.tiles, s);
+                                           w.tiles, clusters, s);
 }
 
 }  // namespace

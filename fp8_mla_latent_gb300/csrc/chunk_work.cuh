@@ -616,8 +616,10 @@ __device__ __forceinline__ void sts64(uint32_t addr, uint2 v) {
 }
 
 // ------------------------------------------------------------------ join
-// The parts of a row tile's rows (N of them), a warp per row (and SPLIT-th of its channels), a block for 16
-// rows.  With a shared prefix they are those of the row's own keys, then those of the prefix.
+// The parts of a row tile's rows (N of them).  With a shared prefix they are those of the row's own keys, then
+// those of the prefix.  A warp per row (or per row and SPLIT-th of its channels), a block for 16 rows; or where
+// rows have many parts, a block per row, whose WARPS warps take every WARPS-th part each and are added up in order
+// (one token of 16 heads over 40000 keys, 152 parts: 25 us, with a warp per row 66).
 struct PartsJoin {
   const int64_t* tiles;          // their number
   const int4* owner;
@@ -628,14 +630,16 @@ struct PartsJoin {
   int64_t prefix_slots;
 };
 
-constexpr int JOIN_ROWS = 16;
+constexpr int JOIN_WARPS = 16;
 
-template <int MODE, int N, int SPLIT>
-__global__ void __launch_bounds__(JOIN_ROWS * 32) parts_join_kernel(const ChunkArgs a, const PartsJoin ps) {
-  constexpr int BLOCKS = N / JOIN_ROWS * SPLIT;
-  const int lane = threadIdx.x & 31;
+template <int MODE, int N, int SPLIT, int WARPS>
+__global__ void __launch_bounds__(JOIN_WARPS * 32, SPLIT == 1 && WARPS == 1 ? 2 : 0)
+    parts_join_kernel(const ChunkArgs a, const PartsJoin ps) {
+  static_assert(WARPS == 1 || (WARPS == JOIN_WARPS && SPLIT == 1), "a warp per row, or a block");
+  constexpr int JOIN_ROWS = JOIN_WARPS / WARPS, BLOCKS = N / JOIN_ROWS * SPLIT;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t p = blockIdx.x / BLOCKS;
-  const int row = (int)(blockIdx.x % BLOCKS) / SPLIT * JOIN_ROWS + (threadIdx.x >> 5);
+  const int row = (int)(blockIdx.x % BLOCKS) / SPLIT * JOIN_ROWS + warp / WARPS;
   const int ch = (int)(blockIdx.x % SPLIT) * (DL / SPLIT);
   grid_dependency_wait();  // (every block: what it reads, and that this launch is not over before the kernel is)
   const int64_t tiles = *ps.tiles;
@@ -647,7 +651,7 @@ __global__ void __launch_bounds__(JOIN_ROWS * 32) parts_join_kernel(const ChunkA
   if constexpr (MODE == kShared) shares = s.part >= 0;
   if (n_own == 1 && !shares) return;  // whole
   const int64_t r = (int64_t)of.y * N + row;
-  if (r >= (int64_t)s.nq * a.H) return;
+  if (r >= (int64_t)s.nq * a.H) return;  // (with a block per row, all of it)
   int n = n_own, prefix_k0 = 0;
   int64_t own_whole = 0, prefix_whole = 0, prefix_row = 0;
   int4 pf = make_int4(0, 0, 0, 0);
@@ -675,14 +679,15 @@ __global__ void __launch_bounds__(JOIN_ROWS * 32) parts_join_kernel(const ChunkA
     }
     return (int64_t)(j == 0 ? of.z : 2 * (k0 + j)) * N + row;
   };
-  // (the first parts' values are asked for together with the weights of all of them, and the others four at a time)
-  constexpr int Q = 4 / SPLIT, AT_ONCE = 4;  // 16-byte units a lane
+  // (the first parts' values are asked for together with the weights of all of them, and the others AT_ONCE at a time)
+  constexpr int Q = 4 / SPLIT, AT_ONCE = SPLIT == 1 && WARPS == 1 ? 2 : 4;  // 16-byte units a lane
+  const int first = warp % WARPS;
   float4 v[AT_ONCE][Q], acc[Q];
   auto ask = [&](int j0) {
 #pragma unroll
     for (int i = 0; i < AT_ONCE; ++i) {
-      if (j0 + i >= n) break;
-      const float4* o = reinterpret_cast<const float4*>(ps.o + slot(j0 + i) * DL + ch) + lane;
+      if (j0 + i * WARPS >= n) break;
+      const float4* o = reinterpret_cast<const float4*>(ps.o + slot(j0 + i * WARPS) * DL + ch) + lane;
 #pragma unroll
       for (int c = 0; c < Q; ++c) v[i][c] = o[32 * c];
     }
@@ -692,27 +697,36 @@ __global__ void __launch_bounds__(JOIN_ROWS * 32) parts_join_kernel(const ChunkA
     M = m0 = ps.m[slot(lane)];
     l0 = ps.l[slot(lane)];
   }
-  ask(0);
+  ask(first);
   for (int j = lane + 32; j < n; j += 32) M = fmaxf(M, ps.m[slot(j)]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
 #pragma unroll
   for (int c = 0; c < Q; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int j0 = 0; j0 < n; j0 += 32) {
-    const int j = j0 + lane;
-    float wt = 0.f;
-    if (j < n) {
-      const float m = j0 == 0 ? m0 : ps.m[slot(j)];
-      wt = m > -INFINITY ? ex2_approx(m - M) : 1.f;  // (a NaN l stays one)
-      L += wt * (j0 == 0 ? l0 : ps.l[slot(j)]);
+  constexpr int BATCH = WARPS == 1 ? 32 : AT_ONCE * WARPS;  // parts whose weights are at hand, those of each
+  constexpr int EACH = BATCH / 32;                          // 32 of them a lane's
+  for (int j0 = 0; j0 < n; j0 += BATCH) {
+    float wt[EACH];
+#pragma unroll
+    for (int h = 0; h < EACH; ++h) {
+      const int j = j0 + 32 * h + lane;
+      wt[h] = 0.f;
+      if (j < n) {
+        const float m = j == lane ? m0 : ps.m[slot(j)];
+        wt[h] = m > -INFINITY ? ex2_approx(m - M) : 1.f;  // (a NaN l stays one)
+        L += wt[h] * (j == lane ? l0 : ps.l[slot(j)]);
+      }
     }
-    const int some = min(n - j0, 32);
-    for (int i0 = 0; i0 < some; i0 += AT_ONCE) {
-      if (j0 + i0 > 0) ask(j0 + i0);
+    for (int i0 = first; i0 < BATCH && j0 + i0 < n; i0 += AT_ONCE * WARPS) {
+      if (j0 + i0 > first) ask(j0 + i0);
 #pragma unroll
       for (int i = 0; i < AT_ONCE; ++i) {
-        if (i0 + i >= some) break;
-        const float w = __shfl_sync(0xffffffffu, wt, i0 + i);
+        const int at = i0 + i * WARPS;  // (the same for the warp)
+        if (j0 + at >= n) break;
+        float w = 0.f;
+#pragma unroll
+        for (int h = 0; h < EACH; ++h)
+          if (at >> 5 == h) w = __shfl_sync(0xffffffffu, wt[h], at & 31);
 #pragma unroll
         for (int c = 0; c < Q; ++c) {
           acc[c].x += w * v[i][c].x;
@@ -727,24 +741,39 @@ __global__ void __launch_bounds__(JOIN_ROWS * 32) parts_join_kernel(const ChunkA
   for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
   const float inv = L == 0.f ? 0.f : 1.f / L;
   const int64_t at = s.q0 * a.H + r;
-  uint2* out = reinterpret_cast<uint2*>(a.out + at * DL + ch) + lane;
+  if (first == 0 && ch == 0 && a.lse != nullptr && lane == 0) a.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * LN2;
+  if constexpr (WARPS == 1) {
+    uint2* out = reinterpret_cast<uint2*>(a.out + at * DL + ch) + lane;
 #pragma unroll
-  for (int c = 0; c < Q; ++c) {
-    const __nv_bfloat162 x = __floats2bfloat162_rn(acc[c].x * inv, acc[c].y * inv);
-    const __nv_bfloat162 y = __floats2bfloat162_rn(acc[c].z * inv, acc[c].w * inv);
-    out[32 * c] = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+    for (int c = 0; c < Q; ++c) {
+      const __nv_bfloat162 x = __floats2bfloat162_rn(acc[c].x * inv, acc[c].y * inv);
+      const __nv_bfloat162 y = __floats2bfloat162_rn(acc[c].z * inv, acc[c].w * inv);
+      out[32 * c] = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+    }
+  } else {
+    __shared__ float part[WARPS][DL];
+#pragma unroll
+    for (int c = 0; c < Q; ++c) reinterpret_cast<float4*>(part[warp])[32 * c + lane] = acc[c];
+    __syncthreads();
+    static_assert(WARPS * 32 == DL, "a thread per channel");
+    float x = 0.f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) x += part[w][threadIdx.x];
+    reinterpret_cast<__nv_bfloat16*>(a.out)[at * DL + threadIdx.x] = __float2bfloat16_rn(x * inv);
   }
-  if (ch == 0 && a.lse != nullptr && lane == 0) a.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * LN2;
 }
 
-// Its launch for at most `tiles` row tiles: where there are few, more blocks for each.
+// Its launch for at most `tiles` row tiles, of at most `ranges` ranges: a block per row where row tiles may have
+// MANY_PARTS parts each, and with few row tiles more blocks for each.
 template <int MODE, int N>
-cudaError_t launch_parts_join(const ChunkArgs& a, const PartsJoin& ps, int64_t tiles, cudaStream_t s) {
-  constexpr int64_t FEW_ROWS_TO_JOIN = 8192;
-  const int64_t blocks = tiles * (N / JOIN_ROWS);
+cudaError_t launch_parts_join(const ChunkArgs& a, const PartsJoin& ps, int64_t tiles, int64_t ranges, cudaStream_t s) {
+  constexpr int64_t FEW_ROWS_TO_JOIN = 8192, MANY_PARTS = 8;
+  const int64_t blocks = tiles * (N / JOIN_WARPS);
+  if (ranges >= MANY_PARTS * tiles)
+    return launch_after_prep(parts_join_kernel<MODE, N, 1, JOIN_WARPS>, (unsigned)(tiles * N), JOIN_WARPS * 32, 0, s, a, ps);
   if (tiles * N < FEW_ROWS_TO_JOIN)
-    return launch_after_prep(parts_join_kernel<MODE, N, 4>, (unsigned)(4 * blocks), JOIN_ROWS * 32, 0, s, a, ps);
-  return launch_after_prep(parts_join_kernel<MODE, N, 1>, (unsigned)blocks, JOIN_ROWS * 32, 0, s, a, ps);
+    return launch_after_prep(parts_join_kernel<MODE, N, 4, 1>, (unsigned)(4 * blocks), JOIN_WARPS * 32, 0, s, a, ps);
+  return launch_after_prep(parts_join_kernel<MODE, N, 1, 1>, (unsigned)blocks, JOIN_WARPS * 32, 0, s, a, ps);
 }
 
 }  // namespace

@@ -921,7 +921,7 @@ cudaError_t launch(ChunkArgs a, const Layout& w, void* workspace, cudaStream_t s
   e = launch_after_prep(rows_kernel<MODE, N>, w.most, NTHREADS, Cfg<N>::SMEM, s, a, ps, ready, kmap, rmap, smap);
   if (e != cudaSuccess || (MODE != kShared && w.most == 1)) return e;
   return launch_parts_join<MODE, N>(a, PartsJoin{&ps.plan->tiles, owner, ps.m, ps.l, ps.o, ps.whole, prefix_base, prefix_owner,
-                                                 w.prefix_slots}, w.tiles, s);
+                                                 w.prefix_slots}, w.tiles, w.most, s);
 }
 
 }  // namespace
