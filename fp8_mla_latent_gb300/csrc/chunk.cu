@@ -52,6 +52,19 @@
 // plan kernel from q_start and seq_lens on the device (36 clusters are resident at once: their
 // 144 SMs are what a call uses).
 //
+// With a window (kWindow) a token sees t <= p with t > p - window or t < n_sink.  A row tile's pages are then those
+// of the first tokens, and from the one on in which its first row's window begins: the gap between them is
+// left out of the order in which pages are walked (chunk_work.cuh, Pages), so that a key tile is any two pages, and
+// the plan counts what is walked.  Only row tiles on a window's or the prompt's edge take the masked path.
+//
+// With shared prefixes (kShared) the plan's sequences are entries: each group's prefix, whose rows are
+// those of all its sequences, and each sequence's rest.  Either leaves f32 parts, which a join adds up
+// with those that range borders cut (join_parts; one read of 16384 keys for 32 tokens of 128 heads in place of 32).
+//
+// For 65 to 128 rows a sequence (SOLO) a cluster is two CTAs, one for the scores and one for the context, with
+// M = 128 and cta_group::1: half of a pair's rows would be copies.  B is not shared then, so that an MMA reads as
+// many bytes for half the rows: shared memory bounds it, about 4800 cycles a tile.  K is a ring of seven Lc blocks.
+//
 // What bounds it.  A tile's MMAs take 2304 cycles on a score pair (36 of 64 cycles: 576 channels,
 // twice for the query's two terms, at twice the rate of bf16) and 2048 on a context pair.  A tile
 // takes about 3100 on normal values with outlying rows: the sixteen warps of either side are a chain
@@ -66,7 +79,11 @@
 // tokens over 65536 keys at 128 heads 6.2 ms, 1500 TFLOP/s, 0.79; a prompt of 4096 tokens 2.04 ms,
 // 1150, 0.61 (row tiles begin every 16 key tiles on average); 32 x 4 drafted tokens over up to
 // 16384 keys 0.235 ms, 1060, 0.56; one token of 4 heads over 256 keys 22.5 us, of which 4 are the plan,
-// 5 the query, 5 the pipeline and 5 the results.
+// 5 the query, 5 the pipeline and 5 the results.  With a window of 2048 a later chunk of 4096 tokens 2.25 ms,
+// 1105 TFLOP/s, 0.57 (a row tile begins every 17 key tiles); 24 x up to 61 tokens of 20 heads, window 1111, 74 us,
+// 0.23 (72 row tiles of 11 key tiles: 11 us to a cluster's first weights, 5 for each f32 part's results); clusters of two:
+// 32 tokens of 128 heads, window 2048, 47.5 us, 0.20 (7 tiles a cluster, the same starts and ends), 64 with
+// a window of 8192 156 us, 0.48.  32 tokens of 128 heads behind a shared prefix of 32768 keys 234 us, 0.65.
 //
 // Every wait is bounded (2 s): on a timeout
 // the CTA flags the workspace error word, drains its MMAs and copies and meets its cluster
@@ -1483,9 +1500,9 @@ Layout layout_of(int B, int H, int64_t total_q, int max_blocks, int G, int64_t w
 // Which kernel a call with a window goes to, by the rows of its sequences on average: up to 64, the one for
 // few rows (rows.cu), which reads a tile of keys for 32 rows at once; up to 128, the clusters of two here,
 // unless there are few (row tile, key tile) units, over which the other spreads better.  Device times of that
-// one, the clusters of two and of four, us, for single tokens of 128 heads: one over 1000 keys 22, 33, 32; 64 over 128
-// keys 35, 28, 40; 32 over 2048 keys 56, 49, 61; 64 over 8192 keys 277, 162, 239.  Of 64 heads, 32 over
-// 2048 keys: 36, 46, 57.
+// one, the clusters of two and of four, us, for single tokens of 128 heads: one over 1000 keys 18, 31, 30, over
+// 8192 20, 31, 38; 64 over 128 keys 33, 27, 40; 32 over 2048 keys 54, 47, 60; 64 over 8192 keys 262, 156,
+// 239.  Of 64 heads: 32 over 2048 keys 35, 44, 56; 64 over 8192 keys 142, 150, 232.
 constexpr int FEW_ROWS = 64, FEW_UNITS = 100;
 bool few_rows(int B, int H, int64_t total_q, int64_t keys) {
   const int64_t rows = total_q * H;

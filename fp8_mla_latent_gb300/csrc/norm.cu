@@ -4,9 +4,15 @@
 //   scale = max |y| / 448 of the row, or of every `group` channels;  code = e4m3(y * (448 / max |y|))
 // with the quantizer's rules of kv8_quantize_rows for zeros, NaN and a subnormal maximum.
 //
-// A thread keeps its channels in registers, eight (a unit) at a time, E units of them; unit u of the
-// row is thread u mod N's, so that a group's units lie in neighbouring lanes.  Rows of up to 32 E units
-// are one warp's, longer ones a CTA's.
+// A thread keeps its channels in registers, eight (a unit) at a time, up to four units of them; unit u of the
+// row is thread u mod N's, so that a group's units lie in neighbouring lanes.  Rows of up to 64 units
+// are one warp's, longer ones a CTA's; many long ones go to the kernel with a ring, below.
+//
+// The kernel right below is for what that one does not take.  It is a chain of loads, a sum, a maximum and
+// stores a row: few rows are latency (one of 7168 channels 3.0 us, 64 3.3), short rows the instructions (16384 x 512
+// bf16 with a residual 12.2 us, 0.71 of the copy rate; x 128 6.3 us, 0.34).  Odd widths and addresses are read
+// and written by the element, 32 neighbours a warp, which issues four to eight times the accesses (517 x 1501 f16
+// 5.6 us, 16384 x 7169 bf16 431 us, 0.28): shifting whole units through shared memory would mend that, and is not built.
 #include <cuda_bf16.h>
 
 #include "kv8_common.cuh"

@@ -1,20 +1,33 @@
 // rows.cu -- absorbed MLA attention over the paged fp8 latent cache for sequences of few rows (single
 // tokens of a few heads): the same mathematics and precision as chunk.cu,
 //   z_t = sm * ( sLc_t <q_lat, dec(Lc_t)> + sRc_t <q_rope, dec(Rc_t)> ),   out = sum_t softmax(z)_t sLc_t dec(Lc_t)
-// with the keys as the MMAs' M and a row tile of N = 16 or 32 (token, head) pairs as theirs, on one CTA per SM.
+// with the keys as the MMAs' M and a row tile of N = 16 or 32 (token, head) pairs as theirs, on one CTA per SM
+// (chunk.cu's 256 rows would be 240 copies for a token of 16 heads, at four SMs a range).
 //
 // A range of (row tile, key tile) units is one CTA's.  Per key tile of 128 tokens, whose bytes are loaded
 // once by TMA and read by both contractions as they are (kind::f8f6f4):
-//   S[t][r]  = K_t . Q_r       M = 128, N = 32: the query's hi terms, then its lo terms; Lc and Rc apart
+//   S[t][r]  = K_t . Q_r       M = 128, 2 N columns: the query's hi terms, then its lo terms; Lc and Rc apart
 //   g'[r][t] = 2^(c u - M_r + 7) sLc_t   as two e4m3 terms; M_r follows the row's largest weight 2^(c u) sLc
-//   O[d][r] += sum_t V[t][d] g'[r][t]    four blocks of 128 channels, N = 32
+//   O[d][r] += sum_t V[t][d] g'[r][t]    four blocks of 128 channels, 2 N columns
+// A token is a TMEM lane, so that a row's maximum and sum go over lanes and warps: eight rows are a warp's, reduced
+// together (a round halves the values a lane has left, 11 shuffles in place of 40).
 //
-// The keys alternate between two streams, each with eight softmax warps, its own references, sums and O
-// (TMEM holds both: 2 x 128 columns, and four buffers of S), which are joined at the row tile's end.
-// A tile's chain -- scores, maximum over its tokens, weights, context -- is longer than the time in
-// which its bytes come, so that two of them have to run at once.
+// N = 16: the keys alternate between two streams, each with eight softmax warps, its own references, sums and
+// O (TMEM holds both: 2 x 128 columns, and four buffers of S), which are joined at the row tile's end.  A
+// tile's chain -- scores, maximum over its tokens, weights, context -- is longer than the time in which its
+// bytes come, so that two of them have to run at once.  N = 32: one stream of sixteen
+// warps (shared memory and TMEM hold no second one's weights and O), two buffers of S.
 //
-// Warps: 0 loads; 1 issues the scores' MMAs; 2 the context's; 3-18 softmax: stream, half of the rows, and
+// What bounds it.  N = 16: HBM.  A tile takes about 3500 cycles, 75 KB on each of 152 SMs, 6.2 TB/s, 0.92 of the copy rate.
+// N = 32: the one chain and the ring of keys, about 4000 cycles.  Around the tiles: plan 2.8 us, first
+// query 4 (its load, and the pipeline's), a row tile's end 1.7, join 4.
+//
+// Measured, one GB300 (device time; fractions of the copy rate, 6775 GB/s, of the bytes in sight): 64 tokens of 16 heads with
+// a window of 4096, ragged, 42.9 us, 0.46; of 8192 70.6 us, 0.65; 512 tokens, window 2048, 148 us, 0.63;
+// 32 heads, window 8192, 81 us, 0.57; 32 tokens of 16 heads, window 2048, 24.2 us, 0.24; one token, window
+// 128, 15 us, which is latency.
+//
+// Warps: 0 loads; 1 issues the scores' MMAs; 2 the context's; 3-18 softmax: stream, eight of the rows, and
 // TMEM lane quarter.  Every wait is bounded (2 s); on a timeout the CTA flags the workspace's error word,
 // drains its MMAs and copies and leaves.
 #include <cuda.h>
@@ -441,7 +454,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     auto p_off = [&](int r) -> uint32_t {
       return (uint32_t)((r >> 3) * 1024 + (r & 7) * 128 + (((row >> 4) ^ (r & 7)) << 4) + (row & 15));
     };
-        const uint32_t to = tmem + lane_addr + T_O + hb;  // O of stream 0, its rows' hi terms
+    const uint32_t to = tmem + lane_addr + T_O + hb;  // O of stream 0, its rows' hi terms
 
     bool ok = true, more = w.more();
     if (more) {
@@ -858,7 +871,9 @@ int64_t window_keys(int max_blocks, int64_t window, int64_t n_sink) {
   return seen < all ? seen : all;
 }
 
-// Row tiles of 32: where sequences have more than 16 rows on average.
+// Row tiles of 32: where sequences have more than 16 rows on average.  (us, in row tiles of 16 and of 32: 32
+// tokens of 16 heads, window 2048, 24.3 and 26.0, of 20 heads 30.0 and 26.3; 64 with a window of 8192 71 and
+// 77, 119 and 79.  Of one token of 128 heads with a window of 1000 17.2 and 18.2, of 8192 21.2 and 20.2.)
 bool wide(int B, int H, int64_t total_q) { return total_q * H > 16 * (int64_t)B; }
 
 // Whether a call may have a prefix whose sharing pays: four clusters' worth of the sequences' row tiles.
