@@ -108,27 +108,27 @@ __global__ void __launch_bounds__(WARP ? ROW_WARPS * 32 : MAX_THREADS) norm_kern
   if (WARP && row >= a.n_rows) return;
   auto at = [&](int i) { return VEC ? (i * n + me) * UNIT : (i * n + me - lane) * UNIT + lane; };
   const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
+  // (both rows are asked for before any of the sum is written, which may lie over them)
   float t[UNITS][UNIT];
+  const T* r = a.residual == nullptr ? nullptr : static_cast<const T*>(a.residual) + row * a.residual_stride;
 #pragma unroll
   for (int i = 0; i < UNITS; ++i) {
     const int c = at(i);
 #pragma unroll
     for (int j = 0; j < UNIT; ++j) t[i][j] = 0.f;
-    if (c < a.width) load_unit<T, VEC>(x + c, a.width - c, t[i]);
+    if (c >= a.width) continue;
+    load_unit<T, VEC>(x + c, a.width - c, t[i]);
+    if (r == nullptr) continue;
+    float v[UNIT];
+    load_unit<T, VEC>(r + c, a.width - c, v);
+#pragma unroll
+    for (int j = 0; j < UNIT; ++j) t[i][j] = __fadd_rn(t[i][j], v[j]);
   }
-  if (a.residual != nullptr) {
-    const T* r = static_cast<const T*>(a.residual) + row * a.residual_stride;
-    T* out = a.residual_out == nullptr ? nullptr : static_cast<T*>(a.residual_out) + row * a.residual_out_stride;
+  if (a.residual_out != nullptr) {
+    T* out = static_cast<T*>(a.residual_out) + row * a.residual_out_stride;
 #pragma unroll
-    for (int i = 0; i < UNITS; ++i) {
-      const int c = at(i);
-      if (c >= a.width) continue;
-      float v[UNIT];
-      load_unit<T, VEC>(r + c, a.width - c, v);
-#pragma unroll
-      for (int j = 0; j < UNIT; ++j) t[i][j] = __fadd_rn(t[i][j], v[j]);
-      if (out != nullptr) store_unit<T, VEC>(out + c, a.width - c, t[i]);
-    }
+    for (int i = 0; i < UNITS; ++i)
+      if (at(i) < a.width) store_unit<T, VEC>(out + at(i), a.width - at(i), t[i]);
   }
   float ss = 0.f;
 #pragma unroll
