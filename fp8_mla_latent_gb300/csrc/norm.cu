@@ -10,9 +10,10 @@
 //
 // The kernel right below is for what that one does not take.  It is a chain of loads, a sum, a maximum and
 // stores a row: few rows are latency (one of 7168 channels 3.0 us, 64 3.3), short rows the instructions (16384 x 512
-// bf16 with a residual 12.2 us, 0.71 of the copy rate; x 128 6.3 us, 0.34).  Odd widths and addresses are read
-// and written by the element, 32 neighbours a warp, which issues four to eight times the accesses (517 x 1501 f16
-// 5.6 us, 16384 x 7169 bf16 431 us, 0.28): shifting whole units through shared memory would mend that, and is not built.
+// bf16 with a residual 12.0 us, 0.73 of the copy rate; x 128 6.3 us, 0.34).  Rows at odd addresses are read and
+// written by the element, 32 neighbours a warp, some 90 instructions for each 32 (16384 x 7169 bf16 with a residual and
+// a scale for every 128 channels 390 us, 0.31): such rows with groups, and odd ones that are few, short or over
+// 2048 units, are left to it.
 #include <cuda_bf16.h>
 
 #include "kv8_common.cuh"
@@ -257,6 +258,14 @@ __global__ void __launch_bounds__(WARP ? ROW_WARPS * 32 : MAX_THREADS) norm_kern
 // thirds do not depend on the units, so rows without a residual take four units a thread and three CTAs
 // (16384 x 7168 bf16 rows: 90 us with two, 74 with four; with a residual 124 and 127; f32 89 and 97).
 // Measured, one GB300, 16384 x 7168 bf16 with a residual: 124 us, 6.68 TB/s, 0.99 of the copy rate.
+//
+// Rows of odd widths (SHIFT) begin anywhere, but if all the row's arrays begin equally far behind a multiple of
+// eight elements, `shift` of them, the units are taken from there: whole ones as above, the first and the last
+// by the element where they are written.  (What is read with these lies in the 16 bytes of one of the row's own
+// elements; it is set to 0.)  A CTA's rows lie a multiple of eight apart, so that it has one shift, and its weights
+// stay in registers.  With a scale a group the shift has to be 0 (rows that only end oddly).  16384 x 7169 bf16
+// 92 us, 282 by the element (with a residual 163, 0.74 of the copy rate); 16384 x 1501 f16 with a residual and
+// normed rows 46, 69 by the element; 517 rows of those 4.9, 5.6.
 constexpr int STAGES = 2;
 
 __device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
@@ -328,7 +337,18 @@ __device__ __forceinline__ void store_pairs(T* p, const uint64_t (&v)[4]) {
   }
 }
 
-template <typename T, bool ADD, int E, int THREADS>
+// the same by the element, for those at c .. c + 7 that lie in [0, width)
+template <typename T>
+__device__ __forceinline__ void store_some(T* p, int c, int width, const uint64_t (&v)[4]) {
+#pragma unroll
+  for (int j = 0; j < UNIT; ++j) {
+    const float2 f = of_pair(v[j / 2]);
+    if (c + j >= 0 && c + j < width) p[j] = from_f32<T>(j & 1 ? f.y : f.x);
+  }
+}
+static_assert(NUM_SMS % UNIT == 0, "a CTA's rows lie a multiple of eight apart");
+
+template <typename T, bool ADD, bool SHIFT, int E, int THREADS>
 __global__ void __launch_bounds__(THREADS, E == 2 ? 2 : (THREADS <= 256 ? 3 : 1)) norm_stream_kernel(const NormArgs a) {
   constexpr int Q = UNIT * (int)sizeof(T) / 16;  // 16-byte pieces of a unit
   constexpr int ROWS_IN = ADD ? 2 : 1;
@@ -338,6 +358,9 @@ __global__ void __launch_bounds__(THREADS, E == 2 ? 2 : (THREADS <= 256 ? 3 : 1)
   for (int i = me; i < 4 * THREADS / 32; i += n) reinterpret_cast<float*>(tmp)[i] = 0.f;
   __syncthreads();
   const uint32_t mine = (uint32_t)__cvta_generic_to_shared(ring) + me * 16;
+  const int shift = SHIFT ? (int)((reinterpret_cast<uintptr_t>(a.x) / sizeof(T) + (uint64_t)blockIdx.x * a.x_stride) % UNIT) : 0;
+  auto at = [&](int i) { return (i * n + me) * UNIT - shift; };  // the first channel of a unit
+  auto edge = [&](int c) { return SHIFT && (c < 0 || c + UNIT > a.width); };
   const uint32_t stage_bytes = (uint32_t)(ROWS_IN * E * Q * n * 16);
   auto ask = [&](int64_t row, int stage) {
     if (row < a.n_rows) {
@@ -347,11 +370,14 @@ __global__ void __launch_bounds__(THREADS, E == 2 ? 2 : (THREADS <= 256 ? 3 : 1)
                             : static_cast<const T*>(a.residual) + row * a.residual_stride;
 #pragma unroll
         for (int i = 0; i < E; ++i) {
-          const int c = (i * n + me) * UNIT;
+          const int c = at(i);
           if (c >= a.width) continue;
 #pragma unroll
-          for (int q = 0; q < Q; ++q)
-            copy_async16(mine + stage * stage_bytes + (uint32_t)(((w * E + i) * Q + q) * n * 16), p + c + q * (16 / (int)sizeof(T)));
+          for (int q = 0; q < Q; ++q) {
+            constexpr int PIECE = 16 / (int)sizeof(T);
+            if (SHIFT && Q > 1 && (c + (q + 1) * PIECE <= 0 || c + q * PIECE >= a.width)) continue;
+            copy_async16(mine + stage * stage_bytes + (uint32_t)(((w * E + i) * Q + q) * n * 16), p + c + q * PIECE);
+          }
         }
       }
     }
@@ -364,12 +390,19 @@ __global__ void __launch_bounds__(THREADS, E == 2 ? 2 : (THREADS <= 256 ? 3 : 1)
   uint64_t wt[E][4];
 #pragma unroll
   for (int i = 0; i < E; ++i) {
-    const int c = (i * n + me) * UNIT;
+    const int c = at(i);
 #pragma unroll
     for (int j = 0; j < 4; ++j) wt[i][j] = 0;
     if (c < a.width) {
-      const float4 u = __ldg(reinterpret_cast<const float4*>(a.weight + c));
-      const float4 v = __ldg(reinterpret_cast<const float4*>(a.weight + c) + 1);
+      float4 u, v;
+      if constexpr (SHIFT) {
+        auto w = [&](int j) { return c + j >= 0 && c + j < a.width ? __ldg(a.weight + c + j) : 0.f; };
+        u = make_float4(w(0), w(1), w(2), w(3));
+        v = make_float4(w(4), w(5), w(6), w(7));
+      } else {
+        u = __ldg(reinterpret_cast<const float4*>(a.weight + c));
+        v = __ldg(reinterpret_cast<const float4*>(a.weight + c) + 1);
+      }
       wt[i][0] = pair_of(u.x, u.y);
       wt[i][1] = pair_of(u.z, u.w);
       wt[i][2] = pair_of(v.x, v.y);
@@ -386,7 +419,7 @@ __global__ void __launch_bounds__(THREADS, E == 2 ? 2 : (THREADS <= 256 ? 3 : 1)
     uint64_t ss2 = 0;
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-      const int c = (i * n + me) * UNIT;
+      const int c = at(i);
 #pragma unroll
       for (int j = 0; j < 4; ++j) t[i][j] = 0;
       if (c >= a.width) continue;
@@ -409,8 +442,19 @@ __global__ void __launch_bounds__(THREADS, E == 2 ? 2 : (THREADS <= 256 ? 3 : 1)
 #pragma unroll
         for (int j = 0; j < 4; ++j) t[i][j] = w == 0 ? v[j] : add_pair(t[i][j], v[j]);
       }
-      if (ADD && a.residual_out != nullptr)
-        store_pairs<T>(static_cast<T*>(a.residual_out) + row * a.residual_out_stride + c, t[i]);
+      if (edge(c)) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = of_pair(t[i][j]);
+          const int k = c + 2 * j;
+          t[i][j] = pair_of(k >= 0 && k < a.width ? f.x : 0.f, k >= -1 && k + 1 < a.width ? f.y : 0.f);
+        }
+      }
+      if (ADD && a.residual_out != nullptr) {
+        T* p = static_cast<T*>(a.residual_out) + row * a.residual_out_stride + c;
+        if (edge(c)) store_some<T>(p, c, a.width, t[i]);
+        else store_pairs<T>(p, t[i]);
+      }
 #pragma unroll
       for (int j = 0; j < 4; ++j) ss2 = fma_pair(t[i][j], t[i][j], ss2);
     }
@@ -433,7 +477,7 @@ __global__ void __launch_bounds__(THREADS, E == 2 ? 2 : (THREADS <= 256 ? 3 : 1)
     float top[E], all = 0.f;
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-      const int c = (i * n + me) * UNIT;
+      const int c = at(i);
       float m = 0.f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -442,8 +486,11 @@ __global__ void __launch_bounds__(THREADS, E == 2 ? 2 : (THREADS <= 256 ? 3 : 1)
         m = max_abs(f.x, f.y, m);
       }
       if (c >= a.width) m = 0.f;  // (nothing times an infinity)
-      if (a.normed != nullptr && c < a.width)
-        store_pairs<T>(static_cast<T*>(a.normed) + row * a.normed_stride + c, t[i]);
+      if (a.normed != nullptr && c < a.width) {
+        T* p = static_cast<T*>(a.normed) + row * a.normed_stride + c;
+        if (edge(c)) store_some<T>(p, c, a.width, t[i]);
+        else store_pairs<T>(p, t[i]);
+      }
       top[i] = m;
       all = fmaxf(all, m);
     }
@@ -476,7 +523,7 @@ __global__ void __launch_bounds__(THREADS, E == 2 ? 2 : (THREADS <= 256 ? 3 : 1)
     const float fr = __fdiv_rn(448.f, all);
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-      const int c = (i * n + me) * UNIT;
+      const int c = at(i);
       const float f = a.group == 0 ? fr : __shfl_sync(0xffffffffu, fr, (lane & ~(a.group / UNIT - 1)) + i);
       if (c >= a.width) continue;
       uint32_t q[2];
@@ -498,7 +545,14 @@ __global__ void __launch_bounds__(THREADS, E == 2 ? 2 : (THREADS <= 256 ? 3 : 1)
           q[h] = zero_byte(u.x) | (zero_byte(u.y) << 8) | (zero_byte(v.x) << 16) | (zero_byte(v.y) << 24);
         }
       }
-      *reinterpret_cast<uint2*>(a.codes + row * a.codes_stride + c) = make_uint2(q[0], q[1]);
+      uint8_t* p = a.codes + row * a.codes_stride + c;
+      if (edge(c)) {
+#pragma unroll
+        for (int j = 0; j < UNIT; ++j)
+          if (c + j >= 0 && c + j < a.width) p[j] = (uint8_t)(q[j / 4] >> (8 * (j & 3)));
+      } else {
+        *reinterpret_cast<uint2*>(p) = make_uint2(q[0], q[1]);
+      }
     }
     turn ^= 1;
     if (++stage == STAGES) stage = 0;
@@ -507,14 +561,14 @@ __global__ void __launch_bounds__(THREADS, E == 2 ? 2 : (THREADS <= 256 ? 3 : 1)
 
 constexpr size_t STREAM_SMEM = 220 * 1024;
 
-template <typename T, bool ADD, int E, int THREADS>
-cudaError_t launch_stream(const NormArgs& a, cudaStream_t s) {
-  const int threads = ((a.width / UNIT + E - 1) / E + 31) / 32 * 32;
+template <typename T, bool ADD, bool SHIFT, int E, int THREADS>
+cudaError_t launch_stream(const NormArgs& a, int units, cudaStream_t s) {
+  const int threads = ((units + E - 1) / E + 31) / 32 * 32;
   const size_t smem = (size_t)STAGES * (ADD ? 2 : 1) * E * UNIT * sizeof(T) * threads;
   static std::atomic<int> memo[THREADS / 32][MAX_DEVICES];
   int per_sm = 0;
   const cudaError_t e = per_device(memo[threads / 32 - 1], [&](int* v) {
-    auto kernel = norm_stream_kernel<T, ADD, E, THREADS>;
+    auto kernel = norm_stream_kernel<T, ADD, SHIFT, E, THREADS>;
     cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)STREAM_SMEM);
     if (r != cudaSuccess) return r;
     int k = 0;
@@ -524,8 +578,26 @@ cudaError_t launch_stream(const NormArgs& a, cudaStream_t s) {
   }, &per_sm);
   if (e != cudaSuccess) return e;
   const int64_t cap = (int64_t)NUM_SMS * per_sm;
-  norm_stream_kernel<T, ADD, E, THREADS><<<(unsigned)(a.n_rows < cap ? a.n_rows : cap), threads, smem, s>>>(a);
+  norm_stream_kernel<T, ADD, SHIFT, E, THREADS><<<(unsigned)(a.n_rows < cap ? a.n_rows : cap), threads, smem, s>>>(a);
   return cudaGetLastError();
+}
+
+// Whether rows go to the kernel with a ring: many, of more units than a warp's.
+template <typename T>
+bool streams(const NormArgs& a, int units) {
+  return units > 64 && a.n_rows > NUM_SMS && units <= (sizeof(T) == 2 ? 2048 : 1024);  // (two rows of twice 16384 values of 32 bits do not fit)
+}
+template <typename T, bool SHIFT>
+cudaError_t launch_streams(const NormArgs& a, int units, cudaStream_t s) {
+  const bool add = a.residual != nullptr;
+  if (units <= 1024) {
+    if (add) return launch_stream<T, true, SHIFT, 2, 512>(a, units, s);
+    if constexpr (sizeof(T) == 4) return launch_stream<T, false, SHIFT, 2, 512>(a, units, s);
+    else return launch_stream<T, false, SHIFT, 4, 256>(a, units, s);
+  }
+  if constexpr (sizeof(T) == 2)
+    return add ? launch_stream<T, true, SHIFT, 4, 512>(a, units, s) : launch_stream<T, false, SHIFT, 4, 512>(a, units, s);
+  return cudaErrorInvalidValue;  // (streams() lets none through)
 }
 
 template <typename T, bool VEC>
@@ -533,20 +605,6 @@ cudaError_t launch_as(const NormArgs& a, cudaStream_t s) {
   const int units = (a.width + UNIT - 1) / UNIT;
   const unsigned warps = (unsigned)((a.n_rows + ROW_WARPS - 1) / ROW_WARPS), rows = (unsigned)a.n_rows;
   auto threads = [&](int e) { return ((units + e - 1) / e + 31) / 32 * 32; };
-  if constexpr (VEC) {
-    if (units > 64 && a.n_rows > NUM_SMS) {
-      const bool add = a.residual != nullptr;
-      if (units <= 1024) {
-        if (add) return launch_stream<T, true, 2, 512>(a, s);
-        if constexpr (sizeof(T) == 4) return launch_stream<T, false, 2, 512>(a, s);
-        else return launch_stream<T, false, 4, 256>(a, s);
-      }
-      // (two rows of twice 16384 values of 32 bits do not fit)
-      if constexpr (sizeof(T) == 2) {
-        if (units <= 2048) return add ? launch_stream<T, true, 4, 512>(a, s) : launch_stream<T, false, 4, 512>(a, s);
-      }
-    }
-  }
   if (units <= 32) norm_kernel<T, 1, VEC, true><<<warps, ROW_WARPS * 32, 0, s>>>(a);
   else if (units <= 64) norm_kernel<T, 2, VEC, true><<<warps, ROW_WARPS * 32, 0, s>>>(a);
   else if (units <= 1024 && a.n_rows <= NUM_SMS) norm_kernel<T, 1, VEC, false><<<rows, threads(1), 0, s>>>(a);
@@ -566,7 +624,20 @@ cudaError_t launch_typed(const NormArgs& a, cudaStream_t s) {
                    even(a.residual_out, a.residual_out_stride) && even(a.normed, a.normed_stride) &&
                    reinterpret_cast<uintptr_t>(a.weight) % 16 == 0 && reinterpret_cast<uintptr_t>(a.codes) % UNIT == 0 &&
                    (a.codes_stride % UNIT == 0 || a.n_rows == 1);
-  return vec ? launch_as<T, true>(a, s) : launch_as<T, false>(a, s);
+  const int units = (a.width + UNIT - 1) / UNIT;
+  if (vec) return streams<T>(a, units) ? launch_streams<T, false>(a, units, s) : launch_as<T, true>(a, s);
+  // rows whose arrays begin equally far behind a multiple of a unit, each of them
+  const uint64_t x_at = reinterpret_cast<uintptr_t>(a.x) / sizeof(T);
+  auto alike = [&](const void* p, int size, int64_t stride) {
+    return p == nullptr || ((reinterpret_cast<uintptr_t>(p) / size - x_at) % UNIT == 0 && (stride - a.x_stride) % UNIT == 0);
+  };
+  constexpr int SIZE = (int)sizeof(T);
+  const int most = (a.width + 2 * UNIT - 2) / UNIT;  // units, with any shift
+  if (streams<T>(a, most) && alike(a.residual, SIZE, a.residual_stride) && alike(a.residual_out, SIZE, a.residual_out_stride) &&
+      alike(a.normed, SIZE, a.normed_stride) && alike(a.codes, 1, a.codes_stride) &&
+      (a.group == 0 || (x_at % UNIT == 0 && a.x_stride % UNIT == 0)))
+    return launch_streams<T, true>(a, most, s);
+  return launch_as<T, false>(a, s);
 }
 
 }  // namespace

@@ -96,6 +96,47 @@ def test_strided_rows_and_what_lies_between_them(w, dtype):
             assert (b[:, :off] == v).all() and (b[:, off + w:] == v).all()
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,w", [(153, 513), (400, 519), (1300, 1501), (700, 2047), (330, 7169), (200, 8191), (170, 8193),
+                                 (160, 16383)])
+def test_many_rows_of_odd_widths(n, w, dtype):
+    """Rows behind one another, each at a place of its own; in parts of wider arrays at equal and at different
+    places; and over the rows that are read.  Nothing but the rows is written."""
+    for add in (True, False):
+        x, r, weight = inputs(n, w, dtype, seed=w, add=add)
+        t, y = (torch.empty_like(x) if add else None), torch.empty_like(x)
+        want = call(x, r, weight, residual_out=t, normed=y)
+        check(x, r, weight, *want, 0, t, y)
+        for offs, gap, group in (((3, 3, 3, 3, 3), 11, 0), ((8, 8, 8, 8, 8), 32 + -w % 8, 128), ((1, 2, 3, 4, 5), 11, 64)):
+            big = [torch.full((n, w + gap), 5.0, dtype=dtype, device="cuda") for _ in range(4)]
+            codes = torch.full((n, w + gap), 99, dtype=torch.uint8, device="cuda")
+            part = [b[:, o: o + w] for b, o in zip(big + [codes], offs)]
+            part[0].copy_(x)
+            if add:
+                part[1].copy_(r)
+            got = call(part[0], part[1] if add else None, weight, group, residual_out=part[2] if add else None,
+                       normed=part[3], codes=part[4])
+            check(x, r, weight, *got, group, part[2] if add else None, part[3])
+            for b, o, v in zip(big + [codes], offs, (5.0, 5.0, 5.0, 5.0, 99)):
+                assert (b[:, :o] == v).all() and (b[:, o + w:] == v).all()
+        if add:
+            x2, r2 = x.clone(), r.clone()
+            got = call(x2, r2, weight, residual_out=r2, normed=x2)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+            assert torch.equal(r2, t) and torch.equal(x2, y)
+
+
+def test_nan_and_infinities_in_odd_rows_stay_in_them():
+    x, r, weight = inputs(1000, 1501, torch.float16)
+    clean = call(x, r, weight)
+    x[7, 0], x[8, 1500], x[300, 750], r[999, 1500] = math.nan, math.inf, math.nan, math.nan
+    got = call(x, r, weight)
+    hit = torch.zeros(1000, dtype=torch.bool, device="cuda")
+    hit[[7, 8, 300, 999]] = True
+    assert (got[0][hit] & 0x7F == 0).all() and (got[1][hit] == 0).all()
+    assert torch.equal(got[0][~hit], clean[0][~hit]) and torch.equal(got[1][~hit], clean[1][~hit])
+
+
 def test_one_row_for_all():
     """A residual (or input) that is one row, read again for every row."""
     x, r, weight = inputs(9, 264, torch.bfloat16)
