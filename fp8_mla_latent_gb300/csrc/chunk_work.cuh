@@ -378,10 +378,13 @@ __device__ __forceinline__ int make_entries(const ChunkArgs& a, int64_t* part_ro
 // base_out for who reads the plan), the units of every row tile, their
 // total, and the row tile that each range starts in; with `unit`, the units before each row tile, and
 // with `owner`, whose it is.  (The sequences are the call's, or entries, from `first` on, and `shift` further on
-// for who reads the plan.)
+// for who reads the plan.)  `alone`: a range for every row tile (of which there are `most` at most).
+// There is room for `room` row tiles, which query ranges that overlap (and are told, since one of them then ends before
+// it begins) may exceed: those behind are left out.
 template <int MODE, class G>
 __device__ __forceinline__ void make_plan(const ChunkArgs& a, Plan<G>* plan, int64_t* base, int64_t* base_out, int first, int shift,
-                                          int n_seq, int most, PlanSum& plan_sum, int64_t* unit, int4* owner) {
+                                          int n_seq, int64_t room, int most, PlanSum& plan_sum, int64_t* unit,
+                                          int4* owner, bool alone = false) {
   static_assert(G::RANGES <= PLAN_THREADS, "a thread per range");
   PlanScratch& sh = plan_sum.at;
   int64_t pairs = 0;
@@ -396,6 +399,7 @@ __device__ __forceinline__ void make_plan(const ChunkArgs& a, Plan<G>* plan, int
     }
     pairs += sum;
   }
+  if (pairs > room) pairs = room;
   if (threadIdx.x == 0) base[n_seq] = pairs;
   __syncthreads();
   // row tile p's sequence (of these) and its place there
@@ -424,6 +428,7 @@ __device__ __forceinline__ void make_plan(const ChunkArgs& a, Plan<G>* plan, int
   const int64_t total = units + pairs * G::SWITCH;
   int64_t nc = units / G::MIN_TILES > pairs ? units / G::MIN_TILES : pairs;
   nc = nc > most ? most : (nc < 1 ? (units > 0 ? 1 : 0) : nc);
+  if (alone) nc = pairs;
   if (threadIdx.x == 0) {
     plan->n = nc;
     plan->units = units;
@@ -453,7 +458,7 @@ __device__ __forceinline__ void make_plan(const ChunkArgs& a, Plan<G>* plan, int
     // a thread per range, which finds its row tile (the last threads, beside the first ones' row tiles)
     const int k = PLAN_THREADS - 1 - (int)threadIdx.x;
     if (k < nc) {
-      const int64_t x = divide(k * total, nc);
+      const int64_t x = alone ? sh.tile[k] : divide(k * total, nc);
       int lo = 0, hi = (int)pairs;
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;

@@ -775,7 +775,7 @@ constexpr int PLAN_NEAR = 4096;
 // (base: in shared memory if it fits)
 template <int MODE, int N>
 __global__ void __launch_bounds__(PLAN_THREADS) rows_plan_kernel(const ChunkArgs a, Plan<Geo<N>>* plan, int64_t* base, int4* owner,
-                                                         int most) {
+                                                         int64_t room, int most, bool alone) {
   grid_dependents_launch();
   __shared__ PlanScratch scratch;
   PlanSum sums{scratch};
@@ -784,7 +784,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) rows_plan_kernel(const ChunkArgs
   if (threadIdx.x == 0) *a.err = 0;
   __syncthreads();
   if (MODE == kPlain && a.G > 0) (void)groups_bad(a, true);  // (groups too small to share anything)
-  make_plan<MODE>(a, plan, a.B < PLAN_NEAR ? near : base, nullptr, 0, 0, a.B, most, sums, nullptr, owner);
+  make_plan<MODE>(a, plan, a.B < PLAN_NEAR ? near : base, nullptr, 0, 0, a.B, room, most, sums, nullptr, owner, alone);
 }
 
 // The plans of a call with shared prefixes, each with a copy of the entries of its own, one behind the other:
@@ -794,9 +794,10 @@ constexpr int ENTRIES_NEAR = 1024, SHARED_NEAR = 512;
 
 template <int N>
 __global__ void __launch_bounds__(PLAN_THREADS) rows_shared_plan_kernel(const ChunkArgs a, Plan<Geo<N>>* plan, int64_t* base,
-                                                                int4* owner, int most, Plan<WideGeo>* prefix_plan,
-                                                                int64_t* prefix_base, int4* prefix_owner,
-                                                                int prefix_most, int clusters) {
+                                                                int4* owner, int64_t room, int most,
+                                                                Plan<WideGeo>* prefix_plan, int64_t* prefix_base,
+                                                                int4* prefix_owner, int64_t prefix_room, int prefix_most,
+                                                                int clusters) {
   grid_dependents_launch();
   __shared__ PlanScratch scratch;
   PlanSum sums{scratch};
@@ -815,11 +816,12 @@ __global__ void __launch_bounds__(PLAN_THREADS) rows_shared_plan_kernel(const Ch
     for (int i = threadIdx.x; i < n; i += PLAN_THREADS) entries[i] = entries_near[i];
   if (own) {
     const int left = NUM_SMS - 4 * split;
-    make_plan<kShared>(c, plan, a.B < SHARED_NEAR ? near : base, nullptr, a.G, n, a.B, most < left ? most : left, sums, nullptr, owner);
+    make_plan<kShared>(c, plan, a.B < SHARED_NEAR ? near : base, nullptr, a.G, n, a.B, room, most < left ? most : left, sums, nullptr,
+                       owner);
   } else {
     if (threadIdx.x == 0) prefix_plan->ready = 0u;
     make_plan<kShared>(c, prefix_plan, a.G < SHARED_NEAR ? near : prefix_base, a.G < SHARED_NEAR ? prefix_base : nullptr, 0, 0,
-                       a.G, split, sums, nullptr, prefix_owner);
+                       a.G, prefix_room, split, sums, nullptr, prefix_owner);
   }
 }
 
@@ -830,24 +832,35 @@ static_assert(OFF_PLAN + sizeof(Plan<Geo<16>>) <= OFF_PREFIX_PLAN && OFF_PREFIX_
 
 struct Layout {
   int most, prefix_most;         // ranges, and the prefixes' clusters
-  int64_t tiles;                 // row tiles at most
+  int64_t tiles, prefix_tiles;   // row tiles at most
+  bool alone;                    // a range for each of them
   int64_t part_rows;             // room for rows that have parts
   int64_t owner, entries, prefix_base, prefix_owner, m, prefix_slots, slots, bytes;
   int64_t rows() const { return prefix_slots + slots + 2 * part_rows; }
 };
+// Short row tiles, if an SM holds one at most, are a range's each: they have no parts, and nothing is launched to
+// join them.  Up to 4 key tiles, or 6 where a row tile has less than three SMs.  (us, with ranges of their own and of
+// equal length: tokens of 16 heads, window 128: one 14.4 and 15.2, 64 15.0 and 16.4; 256: one 16.5 and 15.9 (of which
+// the launch saves the host 1.6), 64 17.0 and 20.1, 140 18.0 and 25.3; 450: one 19.7 and 15.9; 512: 64 20.5 and 21.9.)
+constexpr int64_t ALONE_KEYS = 4, ALONE_KEYS_MANY = 6;
+
 // (G < 0: no shared prefixes)
 template <int N>
 Layout layout_of(int B, int H, int64_t total_q, int64_t keys, int G) {
   auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
   Layout w{};
+  const int64_t by_token = total_q * ((H + N - 1) / N);
   w.tiles = total_q * H / N + B;
+  if (by_token < w.tiles) w.tiles = by_token;
   const int64_t units = w.tiles * keys;
-  w.most = (int)(units < 1 ? 1 : (units < NUM_SMS ? units : NUM_SMS));
+  w.alone = G < 0 && keys <= (3 * w.tiles > NUM_SMS ? ALONE_KEYS_MANY : ALONE_KEYS) && w.tiles <= NUM_SMS;
+  w.most = (int)(w.alone ? w.tiles : (units < 1 ? 1 : (units < NUM_SMS ? units : NUM_SMS)));
   int64_t at = OFF_BASE + up((int64_t)(B + 1) * 8);
   w.owner = at;
   at += up(w.tiles * (int64_t)sizeof(int4));
   if (G >= 0) {
     const int64_t rows = total_q * H, few = (int64_t)PART_ROWS * B, cap = 1 << 20, wide = rows / WideGeo::ROWS + G;
+    w.prefix_tiles = wide;
     w.part_rows = rows < few ? rows : few;
     if (w.part_rows > cap) w.part_rows = cap;
     const int64_t u = wide * keys / WideGeo::MIN_TILES;
@@ -861,14 +874,15 @@ Layout layout_of(int B, int H, int64_t total_q, int64_t keys, int G) {
     w.prefix_slots = 2 * (int64_t)w.prefix_most * WideGeo::ROWS;
   }
   w.m = at;
-  w.slots = w.most > 1 || G >= 0 ? 2 * (int64_t)w.most * N : 0;  // (one range cuts no row tile)
+  w.slots = (w.most > 1 && !w.alone) || G >= 0 ? 2 * (int64_t)w.most * N : 0;  // (one range cuts no row tile)
   w.bytes = at + w.rows() * (8 + DL * 4);
   return w;
 }
 int64_t all_keys(int max_blocks) { return ((int64_t)max_blocks * PAGE + TILE - 1) / TILE; }
-int64_t window_keys(int max_blocks, int64_t window, int64_t n_sink) {
-  const int64_t all = all_keys(max_blocks), seen = (window + n_sink + 32 + 4 * PAGE) / TILE + 1;
-  return seen < all ? seen : all;
+// (a row tile's tokens lie within N of one another, and its window's keys begin and end inside a page)
+int64_t window_keys(int max_blocks, int64_t window, int64_t n_sink, int N) {
+  const int64_t all = all_keys(max_blocks), pages = (n_sink + PAGE - 1) / PAGE + (window + N - 2 + PAGE - 1) / PAGE + 1;
+  return (pages + 1) / 2 < all ? (pages + 1) / 2 : all;
 }
 
 // Row tiles of 32: where sequences have more than 16 rows on average.  (us, in row tiles of 16 and of 32: 32
@@ -923,18 +937,18 @@ cudaError_t launch(ChunkArgs a, const Layout& w, void* workspace, cudaStream_t s
     a.entries = reinterpret_cast<ChunkEntry*>(p + w.entries);
     a.part_rows = w.part_rows;
     Plan<WideGeo>* prefix_plan = reinterpret_cast<Plan<WideGeo>*>(p + OFF_PREFIX_PLAN);
-    rows_shared_plan_kernel<N><<<2, PLAN_THREADS, 0, s>>>(a, ps.plan, base, owner, w.most, prefix_plan, prefix_base, prefix_owner,
-                                                  clusters, fit);
+    rows_shared_plan_kernel<N><<<2, PLAN_THREADS, 0, s>>>(a, ps.plan, base, owner, w.tiles, w.most, prefix_plan, prefix_base,
+                                                           prefix_owner, w.prefix_tiles, clusters, fit);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     e = launch_prefixes(a, PrefixParts{prefix_plan, m, l, o, w.prefix_slots + w.slots}, clusters, kmap, rmap, smap, s);
     if (e != cudaSuccess) return e;
     ready = &prefix_plan->ready;
   } else {
-    rows_plan_kernel<MODE, N><<<1, PLAN_THREADS, 0, s>>>(a, ps.plan, base, owner, w.most);
+    rows_plan_kernel<MODE, N><<<1, PLAN_THREADS, 0, s>>>(a, ps.plan, base, w.alone ? nullptr : owner, w.tiles, w.most, w.alone);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   e = launch_after_prep(rows_kernel<MODE, N>, w.most, NTHREADS, Cfg<N>::SMEM, s, a, ps, ready, kmap, rmap, smap);
-  if (e != cudaSuccess || (MODE != kShared && w.most == 1)) return e;
+  if (e != cudaSuccess || w.alone || (MODE != kShared && w.most == 1)) return e;
   return launch_parts_join<MODE, N>(a, PartsJoin{&ps.plan->tiles, owner, ps.m, ps.l, ps.o, ps.whole, prefix_base, prefix_owner,
                                                  w.prefix_slots}, w.tiles, w.most, s);
 }
@@ -942,13 +956,15 @@ cudaError_t launch(ChunkArgs a, const Layout& w, void* workspace, cudaStream_t s
 }  // namespace
 
 int64_t rows_window_workspace(int B, int H, int64_t total_q, int max_blocks, int window, int n_sink) {
-  const int64_t keys = window_keys(max_blocks, window, n_sink);
-  return wide(B, H, total_q) ? layout_of<32>(B, H, total_q, keys, -1).bytes : layout_of<16>(B, H, total_q, keys, -1).bytes;
+  return wide(B, H, total_q) ? layout_of<32>(B, H, total_q, window_keys(max_blocks, window, n_sink, 32), -1).bytes
+                             : layout_of<16>(B, H, total_q, window_keys(max_blocks, window, n_sink, 16), -1).bytes;
 }
 cudaError_t launch_rows_window(const ChunkArgs& a, void* workspace, cudaStream_t s) {
-  const int64_t keys = window_keys(a.max_blocks, a.window, a.n_sink);
-  return wide(a.B, a.H, a.total_q) ? launch<kWindow, 32>(a, layout_of<32>(a.B, a.H, a.total_q, keys, -1), workspace, s)
-                                   : launch<kWindow, 16>(a, layout_of<16>(a.B, a.H, a.total_q, keys, -1), workspace, s);
+  if (wide(a.B, a.H, a.total_q))
+    return launch<kWindow, 32>(a, layout_of<32>(a.B, a.H, a.total_q, window_keys(a.max_blocks, a.window, a.n_sink, 32), -1),
+                               workspace, s);
+  return launch<kWindow, 16>(a, layout_of<16>(a.B, a.H, a.total_q, window_keys(a.max_blocks, a.window, a.n_sink, 16), -1),
+                             workspace, s);
 }
 
 int64_t rows_shared_workspace(int B, int H, int64_t total_q, int max_blocks, int G) {

@@ -195,6 +195,25 @@ def test_a_bad_query_range_is_told():
         assert ((out[b: b + 1].double() - ref).abs() <= tol).all() and ((l[b: b + 1] - ref_l).abs() <= tol_l).all()
 
 
+@pytest.mark.parametrize("H,n", [(16, 1), (20, 3), (128, 2), (128, 60)])
+def test_query_ranges_that_overlap_are_told_and_stay_in_the_workspace(H, n):
+    """Every second sequence has the same n tokens, far more in all than the arrays hold."""
+    B = 90
+    c = SharedCase(H, [n] + [0] * (B - 1), [400] * B, [40, 50], [320, 320], seed=34)
+    want, _ = check(c)
+    c.start.copy_(torch.tensor([0, n] * (B // 2) + [0]))
+    size = pkg.mla_absorb_shared_fp8_batch_workspace_size(B, H, n, c.max_blocks, 2)
+    for share in (AUTO, ALWAYS):
+        room = torch.full((size + (1 << 20),), 0xA5, dtype=torch.uint8, device="cuda")
+        out = torch.full((n, H, DL), 7.0, dtype=torch.bfloat16, device="cuda")
+        pkg.mla_absorb_shared_fp8_batch(*c.args(), SM_SCALE, c.group_start, c.shared_len, out=out, workspace=room[:size],
+                                        share=share)
+        assert pkg.kv8_workspace_error(room) == -5
+        assert (room[size:] == 0xA5).all()
+    c.start.copy_(torch.tensor([0] + [n] * B))
+    assert torch.equal(run(c)[0], want)
+
+
 def test_nan_in_the_prefix_and_in_one_sequence():
     c = SharedCase(16, [1, 2, 1, 1, 1, 1, 1, 1], [1000] * 8, [8], [960], seed=13)
     clean, clean_l = check(c)

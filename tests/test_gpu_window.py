@@ -260,6 +260,23 @@ def test_lengths_that_cannot_be_are_told_and_clamped(H, nq):
     assert (out[5 * nq: 6 * nq] == 0).all() and torch.isneginf(l[5 * nq: 6 * nq]).all()
 
 
+@pytest.mark.parametrize("H,n", [(1, 3), (16, 1), (20, 5), (128, 1), (128, 70), (200, 40)])
+def test_query_ranges_that_overlap_are_told_and_stay_in_the_workspace(H, n):
+    """Every second sequence has the same n tokens, far more in all than the arrays hold."""
+    B = 90
+    c = WindowCase(H, [n] + [0] * (B - 1), [400] * B, 200, 4, seed=48)
+    want, _ = check(c)
+    c.start.copy_(torch.tensor([0, n] * (B // 2) + [0]))
+    size = pkg.mla_absorb_window_fp8_batch_workspace_size(B, H, n, c.max_blocks, 200, 4)
+    room = torch.full((size + (1 << 20),), 0xA5, dtype=torch.uint8, device="cuda")
+    out = torch.full((n, H, DL), 7.0, dtype=torch.bfloat16, device="cuda")
+    pkg.mla_absorb_window_fp8_batch(*c.args(), SM_SCALE, 200, 4, out=out, workspace=room[:size])
+    assert pkg.kv8_workspace_error(room) == -5
+    assert (room[size:] == 0xA5).all()
+    c.start.copy_(torch.tensor([0] + [n] * B))
+    assert torch.equal(run(c)[0], want)
+
+
 @pytest.mark.parametrize("H", [16, 200])
 def test_lengths_near_2_to_the_31(H):
     """The longest table there is, of whose pages only the last four, the window's, are there."""
