@@ -223,12 +223,9 @@ def kv8_produce_rows(src, norm_weight, eps, positions, rope_cos, rope_sin, kv_co
 _ROW_TYPES = {torch.bfloat16: KV8_BF16, torch.float16: KV8_F16, torch.float32: KV8_F32}
 
 
-def kv8_norm_quantize_rows(x, norm_weight, eps, residual=None, residual_out=None, normed=None, codes=None,
-                           scales=None, group=0, stream=None):
-    """t = x + residual; y = RMS norm of t times norm_weight; codes (e4m3 as uint8 [n, width]) and scales
-    (f32 [n, 1], or [n, ceil(width / group)] with a scale for every `group` channels) of y.  x [n, width]
-    is bf16, f16 or f32; residual_out takes t and normed takes y in that type.  Rows may be strided.
-    Returns (codes, scales)."""
+def _norm_checks(x, norm_weight, residual, residual_out, normed, codes, scales, group, stream):
+    """The checks of kv8_norm_quantize_rows one by one: what is wrong is told, and what is missing is made.  Its
+    pointers and strides, codes and scales."""
     dtype = x.dtype if isinstance(x, _Tensor) else None
     if not (dtype in _ROW_TYPES and _is_device(x) and x.dim() == 2 and x.shape[1] >= 1
             and (x.stride(1) == 1 or x.shape[1] == 1)):
@@ -269,10 +266,44 @@ def kv8_norm_quantize_rows(x, norm_weight, eps, residual=None, residual_out=None
         raise ValueError(f"scales must be [{n}, {groups}]")
     if norm_weight.get_device() != d or scales.get_device() != d:
         raise ValueError("all tensors must be on the same device")
+    return args, codes, scales
+
+
+def kv8_norm_quantize_rows(x, norm_weight, eps, residual=None, residual_out=None, normed=None, codes=None,
+                           scales=None, group=0, stream=None):
+    """t = x + residual; y = RMS norm of t times norm_weight; codes (e4m3 as uint8 [n, width]) and scales
+    (f32 [n, 1], or [n, ceil(width / group)] with a scale for every `group` channels) of y.  x [n, width]
+    is bf16, f16 or f32; residual_out takes t and normed takes y in that type.  Rows may be strided.
+    Returns (codes, scales)."""
+    d, right = -1, False
+    try:  # the checks at once, as those of an attention call
+        dtype, d = x.dtype, x.get_device()
+        n, width = shape = x.shape
+        step, one = x.stride()
+        args = [x.data_ptr(), step, None, 0, None, 0, None, 0, codes.data_ptr(), 0]
+        args[9], ones = codes.stride()
+        right = (d >= 0 and dtype in _ROW_TYPES and one == 1 and ones == 1 and n > 0 and width > 1
+                 and codes.dtype is _U8 and codes.shape == shape and codes.get_device() == d
+                 and norm_weight.dtype is _F32 and norm_weight.shape == (width,) and norm_weight.is_contiguous()
+                 and norm_weight.get_device() == d
+                 and group in (0, 32, 64, 128, 256) and scales.shape == (n, -(-width // group) if group else 1)
+                 and scales.dtype is _F32 and scales.is_contiguous() and scales.get_device() == d
+                 and (residual is not None or residual_out is None))
+        for at, t in ((2, residual), (4, residual_out), (6, normed)):
+            if t is not None:
+                args[at] = t.data_ptr()
+                args[at + 1], one = t.stride()
+                right = right and one == 1 and t.dtype is dtype and t.shape == shape and t.get_device() == d
+    except (AttributeError, TypeError, ValueError):
+        right = False
+    if not right:
+        args, codes, scales = _norm_checks(x, norm_weight, residual, residual_out, normed, codes, scales, group, stream)
+        dtype, d = x.dtype, x.get_device()
+        n, width = x.shape
     with _device(d):
         st = lib().kv8_norm_quantize_rows(
             *args[:6], norm_weight.data_ptr(), float(eps), n, width, _ROW_TYPES[dtype], int(group), *args[6:],
-            scales.data_ptr(), _stream(stream))
+            scales.data_ptr(), _stream(stream) if stream is not None or d < 0 else torch._C._cuda_getCurrentRawStream(d))
     if st != 0:
         raise Kv8Error("kv8_norm_quantize_rows", st)
     return codes, scales
