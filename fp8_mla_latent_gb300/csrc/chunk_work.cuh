@@ -153,6 +153,10 @@ __device__ __forceinline__ int key_tiles(const ChunkArgs& a, const SeqInfo<MODE>
 
 // What a plan reads first, asked for before anything else it does.
 __device__ __forceinline__ void plan_prefetch(const ChunkArgs& a) {
+  for (int g = threadIdx.x; g < a.G && g < (int)blockDim.x; g += blockDim.x) {
+    asm volatile("prefetch.global.L1 [%0];" ::"l"(a.group_start + g) : "memory");
+    asm volatile("prefetch.global.L1 [%0];" ::"l"(a.shared_len + g) : "memory");
+  }
   for (int b = threadIdx.x; b < a.B && b < 2 * (int)blockDim.x; b += blockDim.x) {
     asm volatile("prefetch.global.L1 [%0];" ::"l"(a.q_start + b) : "memory");
     asm volatile("prefetch.global.L1 [%0];" ::"l"(a.seq_lens + b) : "memory");
@@ -258,10 +262,12 @@ __device__ __forceinline__ int make_entries(const ChunkArgs& a, int64_t* part_ro
     a.entries[g].u = make_int4(0, 0, 0, 0);
     a.entries[g].v = make_int4(0, 0, -1, 0);
   }
+  int64_t mine = 0, all = 0;  // (few) the axis's length with nothing shared
   for (int b = threadIdx.x; b < a.B; b += PLAN_THREADS) {
     const SeqInfo<kPlain> s = seq_info<kPlain>(a, b, tell);
     a.entries[a.G + b].u = make_int4((int)s.q0, s.nq, s.T, b);
     a.entries[a.G + b].v = make_int4(0, a.causal, -1, 0);
+    if constexpr (FEW) mine += ((int64_t)s.nq * a.H + G::ROWS - 1) / G::ROWS * (((int64_t)s.T + TILE - 1) / TILE + G::SWITCH);
   }
   if (threadIdx.x == 0) *part_rows = 0;
   if (groups_bad(a, tell) || a.G == 0) return 0;  // (ranges that may overlap: nothing is shared)
@@ -301,19 +307,14 @@ __device__ __forceinline__ int make_entries(const ChunkArgs& a, int64_t* part_ro
       a.entries[g].v = make_int4(0, 0, 0, 0);
     }
   }
-  __syncthreads();
+  if constexpr (FEW) (void)plan_sum(mine, a.B, &all);  // (a barrier)
+  else __syncthreads();
   int split = 0;
   {
     const int64_t saved = (int64_t)sums[0], wide = (int64_t)sums[1];
     if (saved == 0) return 0;
     bool worth = saved - wide > WORTH;
     if constexpr (FEW) {
-      int64_t mine = 0, all;
-      for (int b = threadIdx.x; b < a.B; b += PLAN_THREADS) {
-        const int4 u = a.entries[a.G + b].u;
-        mine += ((int64_t)u.y * a.H + G::ROWS - 1) / G::ROWS * (((int64_t)u.z + TILE - 1) / TILE + G::SWITCH);
-      }
-      (void)plan_sum(mine, a.B, &all);
       const int64_t apart = all * NARROW<G> / NUM_SMS + START;
       int64_t best = INT64_MAX;
       for (int t = 1 + lane; t <= most && t < clusters; t += 32) {
