@@ -355,6 +355,17 @@ __global__ void __cluster_dims__(SOLO ? 2 : 4, 1, 1) __launch_bounds__(NTHREADS,
   }
   grid_dependents_launch();  // (the join kernel may come as soon as there is room)
   const bool work = k < ws.plan->n;
+  if constexpr (MODE == kShared) {
+    // nothing to do, like the cluster's other CTAs: out of the way of the kernel for few rows, which waits for the SM
+    if (!work) {
+      __syncthreads();
+      tc_fence_before();
+      cluster_sync();
+      tc_fence_after();
+      if (warp == W_MMA) tmem_dealloc_pair(tmem, 512);
+      return;
+    }
+  }
   Way<MODE, SOLO> w;
   if (work) w.start(a, *ws.plan, k);
   else w.left = 0;

@@ -214,10 +214,11 @@ constexpr int PART_ROWS = 1024, SHARE = 16;
 // - in row tiles of 256, WORTH units have to be saved in all (two tokens of 128 heads over 16384 keys save 122
 //   and are 11 us slower; four save 244: 55 against 57; 32 over 4000 keys 400: 74 against 87);
 // - else in cycles: a unit is NARROW of an SM's, or WIDE of a cluster's; what a call takes besides is START,
-//   or START_WIDE and what the join and the plans take longer, JOIN_MORE.  (us, shared and apart: 64 tokens of 16
-//   heads over a prefix of 16384 keys 67 and 120, of 2000 keys 44 and 39; 8 over 16384 54 and 43; 32 x
-//   up to 4 tokens over 8000 keys 59 and 70.)
-constexpr int WORTH = 300, WIDE_CYCLES = 3100, START = 16000, START_WIDE = 42000, JOIN_MORE = 12000;
+//   or START_WIDE and what the join takes longer, JOIN_MORE.  (us, shared and not, by the same call: 64 tokens of 16
+//   heads over a prefix of 2000 keys 37 and 35, of 4000 41 and 45, of 8000 48 and 67; 8 over 16384 39 and 31;
+//   32 x up to 4 tokens over 3000 keys 41 and 39, over 8000 50 and 62; 32 tokens of 64 heads over 4000 51 and
+//   53.  A call without groups saves the plan's weighing and a launch: 30, 40, 62; 26; 33, 56; 46.)
+constexpr int WORTH = 300, WIDE_CYCLES = 3100, START = 16000, START_WIDE = 40000, JOIN_MORE = 4000;
 template <class G>
 constexpr int NARROW = G::ROWS == 16 ? 3200 : 4300;
 
