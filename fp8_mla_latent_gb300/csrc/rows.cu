@@ -844,14 +844,18 @@ struct Layout {
 // the launch saves the host 1.6), 64 17.0 and 20.1, 140 18.0 and 25.3; 450: one 19.7 and 15.9; 512: 64 20.5 and 21.9.)
 constexpr int64_t ALONE_KEYS = 4, ALONE_KEYS_MANY = 6;
 
+template <int N>
+int64_t row_tiles_at_most(int B, int H, int64_t total_q) {
+  const int64_t by_row = total_q * H / N + B, by_token = total_q * ((H + N - 1) / N);
+  return by_row < by_token ? by_row : by_token;
+}
+
 // (G < 0: no shared prefixes)
 template <int N>
 Layout layout_of(int B, int H, int64_t total_q, int64_t keys, int G) {
   auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
   Layout w{};
-  const int64_t by_token = total_q * ((H + N - 1) / N);
-  w.tiles = total_q * H / N + B;
-  if (by_token < w.tiles) w.tiles = by_token;
+  w.tiles = row_tiles_at_most<N>(B, H, total_q);
   const int64_t units = w.tiles * keys;
   w.alone = G < 0 && keys <= (3 * w.tiles > NUM_SMS ? ALONE_KEYS_MANY : ALONE_KEYS) && w.tiles <= NUM_SMS;
   w.most = (int)(w.alone ? w.tiles : (units < 1 ? 1 : (units < NUM_SMS ? units : NUM_SMS)));
@@ -890,10 +894,20 @@ int64_t window_keys(int max_blocks, int64_t window, int64_t n_sink, int N) {
 // 77, 119 and 79.  Of one token of 128 heads with a window of 1000 17.2 and 18.2, of 8192 21.2 and 20.2.)
 bool wide(int B, int H, int64_t total_q) { return total_q * H > 16 * (int64_t)B; }
 
-// Whether a call may have a prefix whose sharing pays: four clusters' worth of the sequences' row tiles.
-bool may_share(int B, int H, int64_t total_q, int G, int share) {
-  if (share == KV8_SHARE_ALWAYS) return G > 0 && B > 1;
-  return G > 0 && B > 1 && total_q * H / (wide(B, H, total_q) ? 32 : 16) + B > 4;
+// Whether a call may have a prefix whose sharing pays, in the plan's terms: what all that its sizes allow for costs apart,
+// and with all of it one prefix.  Less than GAIN cycles between them, and the call goes without the plan that weighs and
+// the prefixes' launch, which take 5 us.  (64 tokens of 16 heads behind 2000 keys 35 us with them, 30 without; behind
+// 4000, shared, 42, and 40; 8 behind 16384 32 and 26; 16 behind 16384, shared, 44, and 39.)
+constexpr int64_t GAIN = 12000;
+template <int N>
+bool pays_to_share(int B, int H, int64_t total_q, int max_blocks) {
+  const int64_t keys = all_keys(max_blocks), wide = (total_q * H + WideGeo::ROWS - 1) / WideGeo::ROWS;
+  const int64_t apart = row_tiles_at_most<N>(B, H, total_q) * (keys + Geo<N>::SWITCH) * NARROW<Geo<N>> / NUM_SMS + START;
+  return apart > wide * (keys + WideGeo::SWITCH) * WIDE_CYCLES / WideGeo::RANGES + START_WIDE + JOIN_MORE + GAIN;
+}
+bool may_share(int B, int H, int64_t total_q, int max_blocks, int G, int share) {
+  if (G < 1 || B < 2 || share == KV8_SHARE_ALWAYS) return G > 0 && B > 1;
+  return wide(B, H, total_q) ? pays_to_share<32>(B, H, total_q, max_blocks) : pays_to_share<16>(B, H, total_q, max_blocks);
 }
 
 template <int MODE, int N>
@@ -969,13 +983,13 @@ cudaError_t launch_rows_window(const ChunkArgs& a, void* workspace, cudaStream_t
 
 int64_t rows_shared_workspace(int B, int H, int64_t total_q, int max_blocks, int G) {
   const int64_t keys = all_keys(max_blocks);
-  const int g = may_share(B, H, total_q, G, KV8_SHARE_ALWAYS) ? G : -1;
+  const int g = may_share(B, H, total_q, max_blocks, G, KV8_SHARE_ALWAYS) ? G : -1;
   return wide(B, H, total_q) ? layout_of<32>(B, H, total_q, keys, g).bytes : layout_of<16>(B, H, total_q, keys, g).bytes;
 }
 cudaError_t launch_rows_shared(const ChunkArgs& a, void* workspace, cudaStream_t s) {
   const int64_t keys = all_keys(a.max_blocks);
   const bool w32 = wide(a.B, a.H, a.total_q);
-  if (!may_share(a.B, a.H, a.total_q, a.G, a.share))
+  if (!may_share(a.B, a.H, a.total_q, a.max_blocks, a.G, a.share))
     return w32 ? launch<kPlain, 32>(a, layout_of<32>(a.B, a.H, a.total_q, keys, -1), workspace, s)
                : launch<kPlain, 16>(a, layout_of<16>(a.B, a.H, a.total_q, keys, -1), workspace, s);
   return w32 ? launch<kShared, 32>(a, layout_of<32>(a.B, a.H, a.total_q, keys, a.G), workspace, s)
