@@ -78,11 +78,11 @@
 // Measured, one GB300 (fractions of the bf16 rate of a large matrix product, 1895 TFLOP/s): 2 x 256
 // tokens over 65536 keys at 128 heads 6.2 ms, 1500 TFLOP/s, 0.79; a prompt of 4096 tokens 2.04 ms,
 // 1150, 0.61 (row tiles begin every 16 key tiles on average); 32 x 4 drafted tokens over up to
-// 16384 keys 0.235 ms, 1060, 0.56; one token of 4 heads over 256 keys 22.5 us, of which 4 are the plan,
+// 16384 keys 0.235 ms, 1060, 0.56; one token of 4 heads over 256 keys 19.0 us, of which 3 are the plan,
 // 5 the query, 5 the pipeline and 5 the results.  With a window of 2048 a later chunk of 4096 tokens 2.25 ms,
 // 1105 TFLOP/s, 0.57 (a row tile begins every 17 key tiles); 24 x up to 61 tokens of 20 heads, window 1111, 74 us,
 // 0.23 (72 row tiles of 11 key tiles: 11 us to a cluster's first weights, 5 for each f32 part's results); clusters of two:
-// 32 tokens of 128 heads, window 2048, 47.5 us, 0.20 (7 tiles a cluster, the same starts and ends), 64 with
+// 32 tokens of 128 heads, window 2048, 46.6 us, 0.20 (7 tiles a cluster, the same starts and ends), 64 with
 // a window of 8192 156 us, 0.48.  32 tokens of 128 heads behind a shared prefix of 32768 keys 234 us, 0.65.
 //
 // Every wait is bounded (2 s): on a timeout
@@ -195,7 +195,9 @@ static_assert(OFF_K % 1024 == 0 && KTILE % 1024 == 0 && OFF_V % 1024 == 0 && P_S
 static_assert(P_BYTES <= P_STRIDE && N_LANE_WARPS * 2048 <= 4 * OP_ATOM, "payload and staging");
 static_assert(SMEM <= 232448, "shared memory above the per-CTA limit");
 
-// The cluster of two CTAs is for sequences of 65 to 128 rows, whose row tiles are half of the others'.
+// The cluster of two CTAs is for sequences of 65 to 128 rows, whose row tiles are half of the others'.  (Single tokens
+// of 128 heads, us, SWITCH 4, 6 and 8: 32 with a window of 2048 46.0, 46.8, 48.5; 64 with 512 44.0, 43.2, 41.9;
+// 64 ragged with 2048 67.4, 66.6, 65.1; 200 ragged with 1000 100.5, 102.6, 104.9.)
 struct SoloGeo {
   static constexpr int ROWS = CROWS, RANGES = NUM_SMS / 2, MIN_TILES = 2, SWITCH = 6;
 };

@@ -23,9 +23,9 @@
 // query 4 (its load, and the pipeline's), a row tile's end 1.7, join 4.
 //
 // Measured, one GB300 (device time; fractions of the copy rate, 6775 GB/s, of the bytes in sight): 64 tokens of 16 heads with
-// a window of 4096, ragged, 42.9 us, 0.46; of 8192 70.6 us, 0.65; 512 tokens, window 2048, 148 us, 0.63;
+// a window of 4096, ragged, 43.3 us, 0.45; of 8192 70.6 us, 0.65; 512 tokens, window 2048, 148 us, 0.63;
 // 32 heads, window 8192, 81 us, 0.57; 32 tokens of 16 heads, window 2048, 24.2 us, 0.24; one token, window
-// 128, 15 us, which is latency.
+// 128, 14.3 us, which is latency.
 //
 // Warps: 0 loads; 1 issues the scores' MMAs; 2 the context's; 3-18 softmax: stream, eight of the rows, and
 // TMEM lane quarter.  Every wait is bounded (2 s); on a timeout the CTA flags the workspace's error word,
@@ -46,6 +46,8 @@ constexpr int NTHREADS = (W_SOFT + N_SOFT) * 32;
 constexpr float TAU = 1.0f, P_LOG = 7.0f, DOWN = 10.0f, LG_MIN = -40.0f, DOWN_CAP = 50.0f;  // (as in chunk.cu)
 constexpr uint64_t WAIT_NS = 2000000000ull;
 
+// (us, SWITCH 2, 3 and 5: 64 tokens of 16 heads, ragged windows of 4096 46.3, 43.6, 42.1; 100 with 3000 41.9, 39.4,
+// 40.5; 300 with 1000 54.0, 54.4, 56.0; 64 of 32 heads with 8192 57.5, 54.2, 55.2; MIN_TILES 2 changes nothing.)
 template <int N>
 struct Geo {
   static constexpr int ROWS = N, RANGES = NUM_SMS, SWITCH = 3, MIN_TILES = 1;
