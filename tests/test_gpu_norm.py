@@ -145,6 +145,17 @@ def test_one_row_for_all():
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("w", [1024, 1501])
+def test_one_row_for_many_and_weights_at_an_odd_address(w):
+    x, r, weight = inputs(400, w, torch.bfloat16)
+    one = r[:1].expand(400, w)
+    check(x, one, weight, *call(x, one, weight), 0)
+    check(one, x, weight, *call(one, x, weight), 0)
+    odd = torch.empty(w + 1, device="cuda")[1:].copy_(weight)
+    t, y = torch.empty_like(x), torch.empty_like(x)
+    check(x, r, weight, *call(x, r, odd, 128, residual_out=t, normed=y), 128, t, y)
+
+
 @pytest.mark.parametrize("w", [64, 1000, 1001, 7168])
 def test_in_place(w):
     x, r, weight = inputs(20, w, torch.bfloat16)

@@ -296,6 +296,17 @@ def test_two_calls_at_once_and_groups_that_change_in_a_graph(H, P):
         c.check(o)
 
 
+@pytest.mark.parametrize("H", [16, 128])
+def test_queries_of_wider_arrays(H):
+    c = SharedCase(H, [1, 2, 1, 3, 1, 1, 1, 1], [700 + 9 * i for i in range(8)], [8], [640], seed=35)
+    want, want_l = check(c)
+    wide = torch.full((11, H + 1, 640), 7.0, dtype=torch.bfloat16, device="cuda")
+    wide[:, 1:, 32:608] = torch.cat([c.q_lat, c.q_rope], -1)
+    c.q_lat, c.q_rope = wide[:, 1:, 32:544], wide[:, 1:, 544:608]
+    out, l, err = run(c)
+    assert err == 0 and torch.equal(out, want) and torch.equal(l, want_l)
+
+
 def test_fork_append_and_attend():
     """Sequences made by the page calls: a prompt forked eight times, tokens appended, one step of attention."""
     T, n, H = 1000, 8, 16

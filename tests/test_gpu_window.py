@@ -310,6 +310,46 @@ def test_strided_queries():
     assert torch.equal(out, want) and torch.equal(l, want_l)
 
 
+@pytest.mark.parametrize("H,nq", [(16, [1] * 9), (20, [1, 0, 2, 1, 1]), (128, [1] * 70), (16, [40, 3])])
+def test_queries_of_wider_arrays_and_one_head_for_all(H, nq):
+    """In each of the kernels: rows of a wider array, heads outermost, and one head's query for every head."""
+    c = WindowCase(H, nq, [500 + 3 * i for i in range(len(nq))], 200, 4, seed=49)
+    want, want_l = check(c)
+    wide = torch.full((sum(nq) + 2, H + 1, 640), 7.0, dtype=torch.bfloat16, device="cuda")
+    wide[1:-1, 1:, 32:608] = torch.cat([c.q_lat, c.q_rope], -1)
+    c.q_lat, c.q_rope = wide[1:-1, 1:, 32:544], wide[1:-1, 1:, 544:608]
+    for _ in range(2):
+        out, l, err = run(c)
+        assert err == 0 and torch.equal(out, want) and torch.equal(l, want_l)
+        wide = wide.transpose(0, 1).contiguous().transpose(0, 1)
+        c.q_lat, c.q_rope = wide[1:-1, 1:, 32:544], wide[1:-1, 1:, 544:608]
+    c.q_lat, c.q_rope = c.q_lat[:, :1].expand(-1, H, -1), c.q_rope[:, :1].expand(-1, H, -1)
+    check(c)
+
+
+def test_workspaces_of_the_calls_own_on_a_given_stream_and_in_a_graph():
+    c = WindowCase(16, [1] * 40, [900 + 7 * i for i in range(40)], 600, 4, seed=50)
+    want, _ = check(c)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    outs = [pkg.mla_absorb_window_fp8_batch(*c.args(), SM_SCALE, 600, 4, stream=s) for _ in range(3)]
+    s.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+    outs = [torch.zeros_like(want) for _ in range(2)]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for o in outs:
+            pkg.mla_absorb_window_fp8_batch(*c.args(), SM_SCALE, 600, 4, out=o)
+    for _ in range(3):
+        junk = [torch.full((1 << 20,), 0xFF, dtype=torch.uint8, device="cuda") for _ in range(20)]
+        for o in outs:
+            o.zero_()
+        g.replay()
+        junk += [torch.full((1 << 22,), 0xFF, dtype=torch.uint8, device="cuda") for _ in range(20)]
+        assert torch.equal(outs[0], want) and torch.equal(outs[1], want)
+        assert torch.equal(pkg.mla_absorb_window_fp8_batch(*c.args(), SM_SCALE, 600, 4), want)
+
+
 def test_dominant_keys_behind_the_window_and_among_the_first_tokens():
     """The rows' largest keys leave the window in the middle of the chunk; the first tokens' are larger still."""
     def rows(b, t, g):
