@@ -213,8 +213,7 @@ constexpr int PLAN_NEAR = 4096;
 
 // (base: in shared memory if it fits, and for a shared call, whose join reads it, in the workspace as well)
 template <int MODE>
-__global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const ChunkArgs a, Plan<Geo>* plan, int64_t* base, int64_t room,
-                                                            int clusters) {
+__global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const ChunkArgs a, Plan<Geo>* plan, int64_t* base, int clusters) {
   grid_dependents_launch();
   __shared__ PlanScratch scratch;
   PlanSum sums{scratch};
@@ -223,13 +222,13 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const ChunkArgs a, P
   plan_prefetch(a);
   if (threadIdx.x == 0) *a.err = 0;
   __syncthreads();
-  if constexpr (MODE == kShared) (void)make_entries<Geo>(a, &plan->part_rows, sums, true);
+  bool turns = false;
+  if constexpr (MODE == kShared) (void)make_entries<Geo>(a, &plan->part_rows, sums, true, &turns);
   make_plan<MODE>(a, plan, n_seq < PLAN_NEAR ? near : base, MODE == kShared && n_seq < PLAN_NEAR ? base : nullptr, 0, 0,
-                  n_seq, MODE == kShared ? room : INT64_MAX, clusters, sums,
-                  MODE == kShared ? a.unit : nullptr, nullptr);
+                  n_seq, clusters, sums, MODE == kShared ? a.unit : nullptr, nullptr, false, turns);
 }
 __global__ void __launch_bounds__(PLAN_THREADS) solo_plan_kernel(const ChunkArgs a, Plan<SoloGeo>* plan, int64_t* base,
-                                                         int4* owner, int64_t room, int clusters) {
+                                                         int4* owner, int clusters) {
   grid_dependents_launch();
   __shared__ PlanScratch scratch;
   PlanSum sums{scratch};
@@ -237,7 +236,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) solo_plan_kernel(const ChunkArgs
   plan_prefetch(a);
   if (threadIdx.x == 0) *a.err = 0;
   __syncthreads();
-  make_plan<kWindow>(a, plan, a.B < PLAN_NEAR ? near : base, nullptr, 0, 0, a.B, room, clusters, sums, nullptr, owner);
+  make_plan<kWindow>(a, plan, a.B < PLAN_NEAR ? near : base, nullptr, 0, 0, a.B, clusters, sums, nullptr, owner);
 }
 
 // byte offset of 16-byte unit u (0..15) of row r in a payload: unit 4 s + i holds tokens
@@ -1578,7 +1577,7 @@ cudaError_t launch(ChunkArgs a, void* workspace, cudaStream_t s) {
   if ((e = make_cache_map(d, &kmap)) != cudaSuccess || (e = make_rc_map(d, &rmap)) != cudaSuccess ||
       (e = make_scale_map(d, &smap)) != cudaSuccess)
     return e;
-  plan_kernel<MODE><<<1, PLAN_THREADS, 0, s>>>(a, ws.plan, base, w.tiles, clusters);
+  plan_kernel<MODE><<<1, PLAN_THREADS, 0, s>>>(a, ws.plan, base, clusters);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   e = launch_after_prep(chunk_kernel<MODE>, 4 * clusters, NTHREADS, SMEM, s, a, ws, kmap, rmap, smap);
   const unsigned part_blocks = (unsigned)((w.part_rows + 7) / 8);
@@ -1633,7 +1632,7 @@ cudaError_t launch_solo(ChunkArgs a, const SoloLayout& w, void* workspace, cudaS
   if ((e = make_cache_map(d, &kmap)) != cudaSuccess || (e = make_rc_map(d, &rmap)) != cudaSuccess ||
       (e = make_scale_map(d, &smap)) != cudaSuccess)
     return e;
-  solo_plan_kernel<<<1, PLAN_THREADS, 0, s>>>(a, ws.plan, reinterpret_cast<int64_t*>(p + OFF_SOLO_BASE), owner, w.tiles, clusters);
+  solo_plan_kernel<<<1, PLAN_THREADS, 0, s>>>(a, ws.plan, reinterpret_cast<int64_t*>(p + OFF_SOLO_BASE), owner, clusters);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   e = launch_after_prep(chunk_kernel<kWindow, true>, 2 * clusters, NTHREADS, SMEM_SOLO, s, a, ws, kmap, rmap, smap);
   if (e != cudaSuccess || clusters == 1) return e;

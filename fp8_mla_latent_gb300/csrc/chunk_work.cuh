@@ -236,24 +236,32 @@ __device__ __forceinline__ int64_t warp_min(int64_t v) {
   return v;
 }
 
-// Whether the groups' ranges break their order (by a plan's CTA); that and lengths below 0 are told.
-__device__ __forceinline__ bool groups_bad(const ChunkArgs& a, bool tell) {
+// Whether sequence b's query range ends before it begins.  Ranges of which none does are apart: their row tiles are
+// as many as the workspace has room for, at most.
+__device__ __forceinline__ bool range_turns(const ChunkArgs& a, int b) {
+  return __ldg(&a.q_start[b + 1]) < __ldg(&a.q_start[b]);
+}
+
+// Whether the groups' ranges break their order (by a plan's CTA); that and lengths below 0 are told.  And whether the
+// queries' do: `turns`, a thread's own findings and then all of them.
+__device__ __forceinline__ bool groups_bad(const ChunkArgs& a, bool tell, bool* turns) {
   int bad = 0;
   for (int g = threadIdx.x; g < a.G; g += PLAN_THREADS) {
     const int f = __ldg(&a.group_start[g]), l = __ldg(&a.group_start[g + 1]);
     bad |= f < 0 || l < f || l > a.B;
     if (tell && __ldg(&a.shared_len[g]) < 0) atomicOr(a.err, ERR_SEQ_LEN);
   }
-  bad = __syncthreads_or(bad);
-  if (tell && bad && threadIdx.x == 0) atomicOr(a.err, ERR_BLOCK_TABLE);
-  return bad;
+  const bool any = __syncthreads_or(bad || *turns);
+  if (any) *turns = __syncthreads_or(*turns);
+  if (tell && any && threadIdx.x == 0) atomicOr(a.err, ERR_BLOCK_TABLE);
+  return any;
 }
 
 // (By a plan's CTA.)  The result: the clusters that the prefixes get beside a kernel for few rows,
-// `most` at most of the `clusters` there are.
+// `most` at most of the `clusters` there are.  `turns`: whether query ranges do, and may overlap; nothing is shared then.
 template <class G>
-__device__ __forceinline__ int make_entries(const ChunkArgs& a, int64_t* part_rows, PlanSum& plan_sum, bool tell, int most = 0,
-                                            int clusters = 0) {
+__device__ __forceinline__ int make_entries(const ChunkArgs& a, int64_t* part_rows, PlanSum& plan_sum, bool tell, bool* turns,
+                                            int most = 0, int clusters = 0) {
   constexpr bool FEW = G::ROWS < WideGeo::ROWS;
   __shared__ unsigned long long sums[2];  // units that the groups save, and those of their prefixes
   if (threadIdx.x < 2) sums[threadIdx.x] = 0ull;
@@ -264,14 +272,16 @@ __device__ __forceinline__ int make_entries(const ChunkArgs& a, int64_t* part_ro
     a.entries[g].v = make_int4(0, 0, -1, 0);
   }
   int64_t mine = 0, all = 0;  // (few) the axis's length with nothing shared
+  *turns = false;
   for (int b = threadIdx.x; b < a.B; b += PLAN_THREADS) {
     const SeqInfo<kPlain> s = seq_info<kPlain>(a, b, tell);
     a.entries[a.G + b].u = make_int4((int)s.q0, s.nq, s.T, b);
     a.entries[a.G + b].v = make_int4(0, a.causal, -1, 0);
+    *turns |= range_turns(a, b);
     if constexpr (FEW) mine += ((int64_t)s.nq * a.H + G::ROWS - 1) / G::ROWS * (((int64_t)s.T + TILE - 1) / TILE + G::SWITCH);
   }
   if (threadIdx.x == 0) *part_rows = 0;
-  if (groups_bad(a, tell) || a.G == 0) return 0;  // (ranges that may overlap: nothing is shared)
+  if (groups_bad(a, tell, turns) || a.G == 0) return 0;  // (ranges that may overlap: nothing is shared)
   // what each group would share, a warp per group
   for (int g = warp; g < a.G; g += PLAN_WARPS) {
     const int f = __ldg(&a.group_start[g]), l = __ldg(&a.group_start[g + 1]);
@@ -381,27 +391,36 @@ __device__ __forceinline__ int make_entries(const ChunkArgs& a, int64_t* part_ro
 // total, and the row tile that each range starts in; with `unit`, the units before each row tile, and
 // with `owner`, whose it is.  (The sequences are the call's, or entries, from `first` on, and `shift` further on
 // for who reads the plan.)  `alone`: a range for every row tile (of which there are `most` at most).
-// There is room for `room` row tiles, which query ranges that overlap (and are told, since one of them then ends before
-// it begins) may exceed: those behind are left out.
+// Query ranges that turn back (and are told) may overlap, and have any number of row tiles.  All of them are computed, but
+// none is cut then (`whole`, which a shared call's entries are asked with): a range begins where a row tile does, and
+// no row tile has parts, nor an entry in unit or owner, which have room for those of ranges that are apart.
 template <int MODE, class G>
 __device__ __forceinline__ void make_plan(const ChunkArgs& a, Plan<G>* plan, int64_t* base, int64_t* base_out, int first, int shift,
-                                          int n_seq, int64_t room, int most, PlanSum& plan_sum, int64_t* unit,
-                                          int4* owner, bool alone = false) {
+                                          int n_seq, int most, PlanSum& plan_sum, int64_t* unit, int4* owner,
+                                          bool alone = false, bool whole = false) {
   static_assert(G::RANGES <= PLAN_THREADS, "a thread per range");
   PlanScratch& sh = plan_sum.at;
+  constexpr int64_t TURN = 1ll << 44;  // (above the row tiles of PLAN_THREADS sequences)
   int64_t pairs = 0;
   for (int b0 = 0; b0 < n_seq; b0 += PLAN_THREADS) {
     const int b = b0 + threadIdx.x;
-    const int64_t n = b < n_seq ? row_tiles<G>(a, seq_info<MODE>(a, first + b, true)) : 0;
+    int64_t n = b < n_seq ? row_tiles<G>(a, seq_info<MODE>(a, first + b, true)) : 0;
+    if (MODE != kShared && b < n_seq && range_turns(a, first + b)) n |= TURN;
     int64_t sum;
-    const int64_t inc = plan_sum(n, n_seq - b0, &sum);
+    int64_t inc = plan_sum(n, n_seq - b0, &sum);
+    if constexpr (MODE != kShared) {
+      whole |= sum >= TURN;
+      n &= TURN - 1;
+      inc &= TURN - 1;
+      sum &= TURN - 1;
+    }
     if (b < n_seq) {
       base[b] = pairs + inc - n;
       if (base_out != nullptr) base_out[b] = pairs + inc - n;
     }
     pairs += sum;
   }
-  if (pairs > room) pairs = room;
+  if (owner == nullptr && unit == nullptr && !alone) whole = false;  // (nothing that they could exceed)
   if (threadIdx.x == 0) base[n_seq] = pairs;
   __syncthreads();
   // row tile p's sequence (of these) and its place there
@@ -430,12 +449,13 @@ __device__ __forceinline__ void make_plan(const ChunkArgs& a, Plan<G>* plan, int
   const int64_t total = units + pairs * G::SWITCH;
   int64_t nc = units / G::MIN_TILES > pairs ? units / G::MIN_TILES : pairs;
   nc = nc > most ? most : (nc < 1 ? (units > 0 ? 1 : 0) : nc);
+  if (whole) alone = false;
   if (alone) nc = pairs;
   if (threadIdx.x == 0) {
     plan->n = nc;
     plan->units = units;
-    plan->tiles = pairs;
-    if (unit != nullptr) unit[pairs] = units;
+    plan->tiles = whole ? 0 : pairs;
+    if (unit != nullptr && !whole) unit[pairs] = units;
   }
   // Range k begins at k total / nc, so that as many as at nc / total, rounded up, begin before `at`.  (Its products
   // have 32 bits as a rule, and a division of 64 takes five times as long.)
@@ -447,7 +467,7 @@ __device__ __forceinline__ void make_plan(const ChunkArgs& a, Plan<G>* plan, int
     e.b = seq + shift;
     e.rt = place;
     e.nt = (int32_t)n;
-    e.off = (int32_t)(x - S > G::SWITCH ? x - S - G::SWITCH : 0);
+    e.off = (int32_t)(x - S > G::SWITCH && !whole ? x - S - G::SWITCH : 0);
     e.x = before + e.off;
     plan->e[k] = e;
   };
@@ -481,10 +501,10 @@ __device__ __forceinline__ void make_plan(const ChunkArgs& a, Plan<G>* plan, int
       at += sum;
     }
     if (p >= pairs) continue;
-    if (unit != nullptr) unit[p] = before;
+    if (unit != nullptr && !whole) unit[p] = before;
     const int64_t S = before + p * G::SWITCH;
     const int k0 = ranges_before(S), k1 = ranges_before(S + G::SWITCH + n);
-    if (owner != nullptr) {
+    if (owner != nullptr && !whole) {
       // the range that holds its first unit: the last that begins there, or one from before
       const int kh = ranges_before(S + G::SWITCH + 1);
       owner[p] = make_int4(b + shift, rt, 2 * (kh - 1) + (kh > k0 ? 0 : 1), k1 - 1);

@@ -777,7 +777,7 @@ constexpr int PLAN_NEAR = 4096;
 // (base: in shared memory if it fits)
 template <int MODE, int N>
 __global__ void __launch_bounds__(PLAN_THREADS) rows_plan_kernel(const ChunkArgs a, Plan<Geo<N>>* plan, int64_t* base, int4* owner,
-                                                         int64_t room, int most, bool alone) {
+                                                         int most, bool alone) {
   grid_dependents_launch();
   __shared__ PlanScratch scratch;
   PlanSum sums{scratch};
@@ -785,8 +785,9 @@ __global__ void __launch_bounds__(PLAN_THREADS) rows_plan_kernel(const ChunkArgs
   plan_prefetch(a);
   if (threadIdx.x == 0) *a.err = 0;
   __syncthreads();
-  if (MODE == kPlain && a.G > 0) (void)groups_bad(a, true);  // (groups too small to share anything)
-  make_plan<MODE>(a, plan, a.B < PLAN_NEAR ? near : base, nullptr, 0, 0, a.B, room, most, sums, nullptr, owner, alone);
+  bool turns = false;
+  if (MODE == kPlain && a.G > 0) (void)groups_bad(a, true, &turns);  // (groups too small to share anything)
+  make_plan<MODE>(a, plan, a.B < PLAN_NEAR ? near : base, nullptr, 0, 0, a.B, most, sums, nullptr, owner, alone);
 }
 
 // The plans of a call with shared prefixes, each with a copy of the entries of its own, one behind the other:
@@ -796,9 +797,8 @@ constexpr int ENTRIES_NEAR = 1024, SHARED_NEAR = 512;
 
 template <int N>
 __global__ void __launch_bounds__(PLAN_THREADS) rows_shared_plan_kernel(const ChunkArgs a, Plan<Geo<N>>* plan, int64_t* base,
-                                                                int4* owner, int64_t room, int most,
-                                                                Plan<WideGeo>* prefix_plan, int64_t* prefix_base,
-                                                                int4* prefix_owner, int64_t prefix_room, int prefix_most,
+                                                                int4* owner, int most, Plan<WideGeo>* prefix_plan,
+                                                                int64_t* prefix_base, int4* prefix_owner, int prefix_most,
                                                                 int clusters) {
   grid_dependents_launch();
   __shared__ PlanScratch scratch;
@@ -813,17 +813,19 @@ __global__ void __launch_bounds__(PLAN_THREADS) rows_shared_plan_kernel(const Ch
   ChunkEntry* entries = a.entries + (own ? n : 0);
   ChunkArgs c = a;
   c.entries = n <= ENTRIES_NEAR ? entries_near : entries;
-  const int split = make_entries<Geo<N>>(c, own ? &plan->part_rows : &prefix_plan->part_rows, sums, own, prefix_most, clusters);
+  bool turns;
+  const int split =
+      make_entries<Geo<N>>(c, own ? &plan->part_rows : &prefix_plan->part_rows, sums, own, &turns, prefix_most, clusters);
   if (n <= ENTRIES_NEAR)
     for (int i = threadIdx.x; i < n; i += PLAN_THREADS) entries[i] = entries_near[i];
   if (own) {
     const int left = NUM_SMS - 4 * split;
-    make_plan<kShared>(c, plan, a.B < SHARED_NEAR ? near : base, nullptr, a.G, n, a.B, room, most < left ? most : left, sums, nullptr,
-                       owner);
+    make_plan<kShared>(c, plan, a.B < SHARED_NEAR ? near : base, nullptr, a.G, n, a.B, most < left ? most : left, sums, nullptr,
+                       owner, false, turns);
   } else {
     if (threadIdx.x == 0) prefix_plan->ready = 0u;
     make_plan<kShared>(c, prefix_plan, a.G < SHARED_NEAR ? near : prefix_base, a.G < SHARED_NEAR ? prefix_base : nullptr, 0, 0,
-                       a.G, prefix_room, split, sums, nullptr, prefix_owner);
+                       a.G, split, sums, nullptr, prefix_owner);
   }
 }
 
@@ -834,7 +836,7 @@ static_assert(OFF_PLAN + sizeof(Plan<Geo<16>>) <= OFF_PREFIX_PLAN && OFF_PREFIX_
 
 struct Layout {
   int most, prefix_most;         // ranges, and the prefixes' clusters
-  int64_t tiles, prefix_tiles;   // row tiles at most
+  int64_t tiles;                 // row tiles at most
   bool alone;                    // a range for each of them
   int64_t part_rows;             // room for rows that have parts
   int64_t owner, entries, prefix_base, prefix_owner, m, prefix_slots, slots, bytes;
@@ -866,7 +868,6 @@ Layout layout_of(int B, int H, int64_t total_q, int64_t keys, int G) {
   at += up(w.tiles * (int64_t)sizeof(int4));
   if (G >= 0) {
     const int64_t rows = total_q * H, few = (int64_t)PART_ROWS * B, cap = 1 << 20, wide = rows / WideGeo::ROWS + G;
-    w.prefix_tiles = wide;
     w.part_rows = rows < few ? rows : few;
     if (w.part_rows > cap) w.part_rows = cap;
     const int64_t u = wide * keys / WideGeo::MIN_TILES;
@@ -953,14 +954,14 @@ cudaError_t launch(ChunkArgs a, const Layout& w, void* workspace, cudaStream_t s
     a.entries = reinterpret_cast<ChunkEntry*>(p + w.entries);
     a.part_rows = w.part_rows;
     Plan<WideGeo>* prefix_plan = reinterpret_cast<Plan<WideGeo>*>(p + OFF_PREFIX_PLAN);
-    rows_shared_plan_kernel<N><<<2, PLAN_THREADS, 0, s>>>(a, ps.plan, base, owner, w.tiles, w.most, prefix_plan, prefix_base,
-                                                           prefix_owner, w.prefix_tiles, clusters, fit);
+    rows_shared_plan_kernel<N><<<2, PLAN_THREADS, 0, s>>>(a, ps.plan, base, owner, w.most, prefix_plan, prefix_base,
+                                                           prefix_owner, clusters, fit);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     e = launch_prefixes(a, PrefixParts{prefix_plan, m, l, o, w.prefix_slots + w.slots}, clusters, kmap, rmap, smap, s);
     if (e != cudaSuccess) return e;
     ready = &prefix_plan->ready;
   } else {
-    rows_plan_kernel<MODE, N><<<1, PLAN_THREADS, 0, s>>>(a, ps.plan, base, w.alone ? nullptr : owner, w.tiles, w.most, w.alone);
+    rows_plan_kernel<MODE, N><<<1, PLAN_THREADS, 0, s>>>(a, ps.plan, base, w.alone ? nullptr : owner, w.most, w.alone);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   e = launch_after_prep(rows_kernel<MODE, N>, w.most, NTHREADS, Cfg<N>::SMEM, s, a, ps, ready, kmap, rmap, smap);

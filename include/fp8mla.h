@@ -465,7 +465,7 @@ int mla_absorb_window_fp8_batch(const uint16_t* q_lat, int64_t q_lat_token_strid
  *   group_start  device int32 [G + 1], non-decreasing within [0, B]: group g is sequences
  *                group_start[g] .. group_start[g + 1] - 1.  Sequences outside every group share
  *                nothing.  Ranges that break that set the error word (KV8_EBOUNDS), and nothing
- *                is shared.
+ *                is shared, as where query ranges break their order (q_start).
  *   shared_len   device int32 [G]: the first shared_len[g] tokens of the group's sequences are
  *                the same, and the table rows of those that have queries name the same pages for
  *                the whole pages of them.  0 shares nothing; less than 0 sets the error word

@@ -331,3 +331,26 @@ def test_fork_append_and_attend():
     # both are within 2^-9 + 3 2^-11 + 2^-8 (the weights, the rounding to bf16) of the exact value, up to
     # cancellation in the sum, which the largest magnitude stands for
     assert float((got.double() - want.double()).abs().max()) <= 2 * (2 ** -9 + 3 * 2 ** -11 + 2 ** -8) * float(want.abs().max())
+
+
+@pytest.mark.parametrize("H,n,times,more", [(4, 60, 18, 40), (16, 60, 18, 40), (20, 30, 20, 70), (128, 60, 18, 2),
+                                            (128, 200, 30, 3)])
+def test_rows_that_no_other_range_touches_behind_ranges_that_overlap(H, n, times, more):
+    """The same n rows named again and again, then ranges of their own, a group among them: these are in order, and
+    computed as in any call, although there are more row tiles than of ranges that are apart."""
+    B = 2 * times - 1 + more  # (the n rows' sequences, with ranges that turn back between them, then the others)
+    nq = [n] + [0] * (2 * times - 2) + [1 + b % 2 for b in range(more)]
+    c = SharedCase(H, nq, [400 + b % 7 for b in range(B)], [2 * times - 1, more], [0, 320], seed=36)
+    check(c)
+    c.start[: 2 * times] = torch.tensor([0, n] * times)
+    for groups in ([0, 2 * times - 1, B], [0, 0, 0]):
+        for share in (AUTO, ALWAYS):
+            c.group_start.copy_(torch.tensor(groups))
+            size = pkg.mla_absorb_shared_fp8_batch_workspace_size(B, H, sum(nq), c.max_blocks, 2)
+            room = torch.full((size + (1 << 20),), 0xA5, dtype=torch.uint8, device="cuda")
+            out, l, err = run(c, ws=room[:size], share=share)
+            assert err == -5 and (room[size:] == 0xA5).all()
+            for b in range(2 * times - 1, B):
+                ref, ref_l, tol, tol_l = c.reference(b)
+                rows = slice(int(c.start[b]), int(c.start[b + 1]))
+                assert ((out[rows].double() - ref).abs() <= tol).all() and ((l[rows] - ref_l).abs() <= tol_l).all(), b

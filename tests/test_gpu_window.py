@@ -411,3 +411,25 @@ def test_far_pages(H, B):
     c.codes, c.scales = codes, scales
     out, l, err = run(c)
     assert err == 0 and torch.equal(out, want) and torch.equal(l, want_l)
+
+
+@pytest.mark.parametrize("H,n,times,more", [(1, 3, 60, 4), (16, 60, 18, 40), (20, 30, 20, 70), (128, 20, 40, 30), (128, 60, 18, 2),
+                                            (200, 40, 30, 3)])
+def test_rows_that_no_other_range_touches_behind_ranges_that_overlap(H, n, times, more):
+    """The same n rows named again and again, then ranges of their own: these are computed as in any call, although
+    there are more row tiles than of ranges that are apart."""
+    B = 2 * times - 1 + more  # (the n rows' sequences, with ranges that turn back between them, then the others)
+    nq = [n] + [0] * (2 * times - 2) + [1 + b % 2 for b in range(more)]
+    c = WindowCase(H, nq, [400 + b % 7 for b in range(B)], 200, 4, seed=51)
+    check(c)
+    c.start[: 2 * times] = torch.tensor([0, n] * times)
+    size = pkg.mla_absorb_window_fp8_batch_workspace_size(B, H, sum(nq), c.max_blocks, 200, 4)
+    room = torch.full((size + (1 << 20),), 0xA5, dtype=torch.uint8, device="cuda")
+    out = torch.full((sum(nq), H, DL), 7.0, dtype=torch.bfloat16, device="cuda")
+    l = torch.full((sum(nq), H), 7.0, device="cuda")
+    pkg.mla_absorb_window_fp8_batch(*c.args(), SM_SCALE, 200, 4, out=out, lse=l, workspace=room[:size])
+    assert pkg.kv8_workspace_error(room) == -5 and (room[size:] == 0xA5).all()
+    for b in range(2 * times - 1, B):
+        ref, ref_l, tol, tol_l = c.reference(b)
+        rows = slice(int(c.start[b]), int(c.start[b + 1]))
+        assert ((out[rows].double() - ref).abs() <= tol).all() and ((l[rows] - ref_l).abs() <= tol_l).all(), b
