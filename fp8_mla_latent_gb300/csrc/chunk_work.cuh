@@ -11,6 +11,7 @@
 #include <type_traits>
 
 #include "kv8_common.cuh"
+#include "share_split.h"
 #include "tc_ptx.cuh"
 
 namespace kv8 {
@@ -218,7 +219,7 @@ constexpr int PART_ROWS = 1024, SHARE = 16;
 //   heads over a prefix of 2000 keys 37 and 35, of 4000 41 and 45, of 8000 48 and 67; 8 over 16384 39 and 31;
 //   32 x up to 4 tokens over 3000 keys 41 and 39, over 8000 50 and 62; 32 tokens of 64 heads over 4000 51 and
 //   53.  A call without groups saves the plan's weighing and a launch: 30, 40, 62; 26; 33, 56; 46.)
-constexpr int WORTH = 300, WIDE_CYCLES = 3100, START = 16000, START_WIDE = 40000, JOIN_MORE = 4000;
+constexpr int WORTH = 300, WIDE_CYCLES = 3100;
 template <class G>
 constexpr int NARROW = G::ROWS == 16 ? 3200 : 4300;
 
@@ -324,22 +325,18 @@ __device__ __forceinline__ int make_entries(const ChunkArgs& a, int64_t* part_ro
   {
     const int64_t saved = (int64_t)sums[0], wide = (int64_t)sums[1];
     if (saved == 0) return 0;
-    bool worth = saved - wide > WORTH;
+    const bool always = a.share == KV8_SHARE_ALWAYS;
+    bool take = always || saved - wide > WORTH;
     if constexpr (FEW) {
-      const int64_t apart = all * NARROW<G> / NUM_SMS + START;
-      int64_t best = INT64_MAX;
+      int64_t least = INT64_MAX;
       for (int t = 1 + lane; t <= most && t < clusters; t += 32) {
-        // (estimates: f32 does, and its divisions are the cheaper ones)
-        const float x = (float)(wide * WIDE_CYCLES) / (float)t + START_WIDE;
-        const float y = (float)((all - saved) * NARROW<G>) / (float)(NUM_SMS - 4 * t) + START;
-        const int64_t z = (int64_t)(fmaxf(x, y) + JOIN_MORE) * 64 + t;  // (t < 64)
-        best = z < best ? z : best;
+        const int64_t z = split_cost((float)(wide * WIDE_CYCLES), (float)((all - saved) * NARROW<G>), t, NUM_SMS);
+        least = z < least ? z : least;
       }
-      best = warp_min(best);
-      worth = best / 64 < apart;
-      split = (int)(best % 64);
+      split = split_taken(warp_min(least), all * NARROW<G> / NUM_SMS + START, always);
+      take = split > 0;
     }
-    if (!worth && a.share != KV8_SHARE_ALWAYS) {
+    if (!take) {
       for (int g = threadIdx.x; g < a.G; g += PLAN_THREADS) a.entries[g].u.y = 0;
       __syncthreads();
       return 0;
