@@ -354,3 +354,54 @@ def test_rows_that_no_other_range_touches_behind_ranges_that_overlap(H, n, times
                 ref, ref_l, tol, tol_l = c.reference(b)
                 rows = slice(int(c.start[b]), int(c.start[b + 1]))
                 assert ((out[rows].double() - ref).abs() <= tol).all() and ((l[rows] - ref_l).abs() <= tol_l).all(), b
+
+
+@pytest.mark.parametrize("H", [16, 128])
+def test_far_pages(H):
+    """Cache slots whose bytes lie behind 2^31 and 2^32, of the prefix and of what lies behind it."""
+    c = SharedCase(H, [1, 2, 1, 1, 3, 1], [900 - 9 * b for b in range(6)], [6], [640], seed=37)
+    n_blocks = 2 ** 32 // (PAGE * 576) + 800
+    want = {share: run(c, share=share) for share in (AUTO, ALWAYS)}
+    check(c)
+    codes = torch.full((n_blocks * PAGE, 576), 0x7F, dtype=torch.uint8, device="cuda")
+    scales = torch.full((n_blocks * PAGE, 2), math.nan, device="cuda")
+    k = c.codes.shape[0]
+    codes[-k:], scales[-k:] = c.codes, c.scales
+    c.table = torch.where(c.table >= 0, c.table + (n_blocks - k // PAGE), c.table)
+    c.codes, c.scales = codes, scales
+    for share in (AUTO, ALWAYS):
+        out, l, err = run(c, share=share)
+        assert err == 0 and torch.equal(out, want[share][0]) and torch.equal(l, want[share][1])
+
+
+@pytest.mark.parametrize("H,B", [(16, 16), (128, 2)])
+@pytest.mark.parametrize("share", [AUTO, ALWAYS])
+def test_lengths_near_2_to_the_31(H, B, share):
+    """The longest table there is.  Of the prefix the first two pages and the last are there, of what lies behind it
+    four; the others are told and left out."""
+    mb = (1 << 25) - 1
+    c = SharedCase(H, [1] * B, [7 * PAGE] * B, [B], [3 * PAGE], seed=38)
+    table = torch.full((B, mb), -1, dtype=torch.int32, device="cuda")
+    table[:, :2] = c.table[:, :2]
+    table[:, mb - 5:] = c.table[:, 2:7]
+    out, l = torch.empty(B, H, DL, dtype=torch.bfloat16, device="cuda"), torch.empty(B, H, device="cuda")
+    ws = pkg.alloc_workspace(pkg.mla_absorb_shared_fp8_batch_workspace_size(B, H, B, mb, 1))
+    pkg.mla_absorb_shared_fp8_batch(c.q_lat, c.q_rope, c.codes, c.scales, table, torch.full_like(c.lens, mb * PAGE), c.start,
+                                    SM_SCALE, c.group_start, torch.full_like(c.shared_len, (mb - 4) * PAGE), out=out, lse=l,
+                                    workspace=ws, share=share)
+    assert pkg.kv8_workspace_error(ws) == -5
+    c.check(out, l)
+
+
+def test_a_group_with_room_for_its_parts_before_groups_without():
+    """The rows of the second group are more than there is room for: its members read the prefix themselves.  The
+    first one's is still computed once (the other members' entries for it are not looked up)."""
+    c = SharedCase(128, [1, 1, 60, 60, 1, 1], [900, 950, 1000, 980, 870, 1010], [2, 2, 2], [832, 850, 800], seed=39)
+    want, want_l, err = run(c)
+    assert err == 0
+    c.check(want, want_l)
+    c.table[1, : 832 // PAGE] = 2 ** 30
+    out, l, err = run(c)
+    assert err == 0 and torch.equal(out, want) and torch.equal(l, want_l)
+    c.table[3, 0] = 2 ** 30  # (not so the second one's)
+    assert run(c)[2] == -5
