@@ -1516,6 +1516,10 @@ Layout layout_of(int B, int H, int64_t total_q, int max_blocks, int G, int64_t w
 // one, the clusters of two and of four, us, for single tokens of 128 heads: one over 1000 keys 18, 31, 30, over
 // 8192 20, 31, 38; 64 over 128 keys 33, 27, 40; 32 over 2048 keys 54, 47, 60; 64 over 8192 keys 262, 156,
 // 239.  Of 64 heads: 32 over 2048 keys 35, 44, 56; 64 over 8192 keys 142, 150, 232.
+// The average is over all sequences, those without queries among them, and their number is all that the host knows: a
+// batch of which most have none may go to row tiles too small for the one that has.  (512 new tokens of 16 heads at
+// 8192 keys alone, beside 63 and beside 511 sequences without queries: window 2048 62, 66 and 132 us; 8192 128, 146
+// and 377; shared prefixes, in a group that shares nothing, 128, 129 and 382; of 128 heads, window 2048, 301, 301, 336.)
 constexpr int FEW_ROWS = 64, FEW_UNITS = 100;
 bool few_rows(int B, int H, int64_t total_q, int64_t keys) {
   const int64_t rows = total_q * H;

@@ -60,7 +60,7 @@ struct PlanEntry {
 template <class G>
 struct Plan {
   int64_t n, units, tiles;   // ranges, their units, row tiles
-  int64_t part_rows;         // (shared prefixes) rows that have parts
+  int64_t part_rows;         // (shared prefixes, all rows by chunk.cu) rows that have parts
   unsigned ready;            // (and in the prefixes' plan) whether the plans are made
   PlanEntry e[G::RANGES];
 };
@@ -83,16 +83,16 @@ __device__ __forceinline__ SeqInfo<MODE> seq_info(const ChunkArgs& a, int b, boo
     const int4 u = a.entries[b].u, v = a.entries[b].v;
     return {u.x, u.y, u.z, u.w, v.x, v.y, v.z};
   } else {
-  SeqInfo<MODE> s;
-  const int64_t q0 = __ldg(&a.q_start[b]), q1 = __ldg(&a.q_start[b + 1]);
-  const int64_t T = __ldg(&a.seq_lens[b]), room = (int64_t)a.max_blocks * PAGE;
-  const bool bad = q0 < 0 || q1 < q0 || q1 > a.total_q;
-  if (tell && bad) atomicOr(a.err, ERR_BLOCK_TABLE);
-  if (tell && (T < 0 || T > room)) atomicOr(a.err, ERR_SEQ_LEN);
-  s.q0 = q0;
-  s.nq = bad ? 0 : (int)(q1 - q0);
-  s.T = (int)(T < 0 ? 0 : (T > room ? room : T));
-  return s;
+    SeqInfo<MODE> s;
+    const int64_t q0 = __ldg(&a.q_start[b]), q1 = __ldg(&a.q_start[b + 1]);
+    const int64_t T = __ldg(&a.seq_lens[b]), room = (int64_t)a.max_blocks * PAGE;
+    const bool bad = q0 < 0 || q1 < q0 || q1 > a.total_q;
+    if (tell && bad) atomicOr(a.err, ERR_BLOCK_TABLE);
+    if (tell && (T < 0 || T > room)) atomicOr(a.err, ERR_SEQ_LEN);
+    s.q0 = q0;
+    s.nq = bad ? 0 : (int)(q1 - q0);
+    s.T = (int)(T < 0 ? 0 : (T > room ? room : T));
+    return s;
   }
 }
 template <class G, int MODE>
@@ -244,22 +244,22 @@ __device__ __forceinline__ bool range_turns(const ChunkArgs& a, int b) {
 }
 
 // Whether the groups' ranges break their order (by a plan's CTA); that and lengths below 0 are told.  And whether the
-// queries' do: `turns`, a thread's own findings and then all of them.
-__device__ __forceinline__ bool groups_bad(const ChunkArgs& a, bool tell, bool* turns) {
+// queries' do, if asked: `turns`, a thread's own findings and then all of them.
+__device__ __forceinline__ bool groups_bad(const ChunkArgs& a, bool tell, bool* turns = nullptr) {
   int bad = 0;
   for (int g = threadIdx.x; g < a.G; g += PLAN_THREADS) {
     const int f = __ldg(&a.group_start[g]), l = __ldg(&a.group_start[g + 1]);
     bad |= f < 0 || l < f || l > a.B;
     if (tell && __ldg(&a.shared_len[g]) < 0) atomicOr(a.err, ERR_SEQ_LEN);
   }
-  const bool any = __syncthreads_or(bad || *turns);
-  if (any) *turns = __syncthreads_or(*turns);
+  const bool any = __syncthreads_or(bad || (turns != nullptr && *turns));
+  if (turns != nullptr && any) *turns = __syncthreads_or(*turns);
   if (tell && any && threadIdx.x == 0) atomicOr(a.err, ERR_BLOCK_TABLE);
   return any;
 }
 
 // (By a plan's CTA.)  The result: the clusters that the prefixes get beside a kernel for few rows,
-// `most` at most of the `clusters` there are.  `turns`: whether query ranges do, and may overlap; nothing is shared then.
+// `most` at most of the `clusters` there are.  `part_rows`, for a join that asks for it: the rows that have parts.  `turns`: whether query ranges do, and may overlap; nothing is shared then.
 template <class G>
 __device__ __forceinline__ int make_entries(const ChunkArgs& a, int64_t* part_rows, PlanSum& plan_sum, bool tell, bool* turns,
                                             int most = 0, int clusters = 0) {
@@ -281,7 +281,7 @@ __device__ __forceinline__ int make_entries(const ChunkArgs& a, int64_t* part_ro
     *turns |= range_turns(a, b);
     if constexpr (FEW) mine += ((int64_t)s.nq * a.H + G::ROWS - 1) / G::ROWS * (((int64_t)s.T + TILE - 1) / TILE + G::SWITCH);
   }
-  if (threadIdx.x == 0) *part_rows = 0;
+  if (part_rows != nullptr && threadIdx.x == 0) *part_rows = 0;
   if (groups_bad(a, tell, turns) || a.G == 0) return 0;  // (ranges that may overlap: nothing is shared)
   // what each group would share, a warp per group
   for (int g = warp; g < a.G; g += PLAN_WARPS) {
@@ -353,7 +353,8 @@ __device__ __forceinline__ int make_entries(const ChunkArgs& a, int64_t* part_ro
       // (the groups that have room are the first ones: those behind one without begin further on)
       if (from + rows <= a.part_rows) {
         a.entries[g].v.z = (int)from;
-        atomicMax(reinterpret_cast<unsigned long long*>(part_rows), (unsigned long long)(from + rows));
+        if (part_rows != nullptr)
+          atomicMax(reinterpret_cast<unsigned long long*>(part_rows), (unsigned long long)(from + rows));
       } else {
         a.entries[g].u.y = 0;
       }

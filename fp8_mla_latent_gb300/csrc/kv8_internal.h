@@ -180,7 +180,8 @@ cudaError_t launch_pages_compact(const PageTable& t, int32_t* moves, int32_t* n_
 cudaError_t launch_pages_copy(uint8_t* codes, float* scales, int n_layers, int64_t n_slots, const int32_t* moves,
                               const int32_t* n_moves, int64_t max_moves, unsigned* err, cudaStream_t s);
 
-// A sequence of a call with shared prefixes (chunk.cu, SeqInfo): q0, nq, T, row; page0, causal, part, 0.
+// A sequence of a call with shared prefixes (chunk_work.cuh, SeqInfo): q0, nq, T, row; page0, causal, part, and
+// of a sequence that has parts its group (else 0).
 struct ChunkEntry {
   int4 u, v;
 };

@@ -255,8 +255,11 @@ __global__ void __launch_bounds__(WARP ? ROW_WARPS * 32 : MAX_THREADS) norm_kern
 // HBM bounds it: two CTAs of 16 warps hold one SM's share of the rows in flight (28 KB a CTA at 7168
 // channels of two 16-bit inputs; with four rows ahead instead of one it is slower, 131 us against 124).
 // With one input the instructions are next: 350 a warp and row of two units a thread, of which two
-// thirds do not depend on the units, so rows without a residual take four units a thread and three CTAs
-// (16384 x 7168 bf16 rows: 90 us with two, 74 with four; with a residual 124 and 127; f32 89 and 97).
+// thirds do not depend on the units, so 16-bit rows without a residual take four units a thread and three CTAs
+// (16384 x 7168 bf16 rows, a scale a row: 90 us with two, 74 with four, and 86 with a scale for every 128 channels; with
+// a residual 124 and 127; 4096 f32 rows with a residual 89 and 97).  f32 rows are far from the copy rate, 16384 x
+// 7168 without a residual 152 us, 0.57, with one 335, 0.67: a unit is two pieces of 16 bytes there, so that a warp's
+// request for one of them takes half of each 32-byte sector, and every sector comes from L2 twice (944 MB of 470).
 // Measured, one GB300, 16384 x 7168 bf16 with a residual: 124 us, 6.68 TB/s, 0.99 of the copy rate.
 //
 // Rows of odd widths (SHIFT) begin anywhere, but if all the row's arrays begin equally far behind a multiple of

@@ -785,8 +785,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) rows_plan_kernel(const ChunkArgs
   plan_prefetch(a);
   if (threadIdx.x == 0) *a.err = 0;
   __syncthreads();
-  bool turns = false;
-  if (MODE == kPlain && a.G > 0) (void)groups_bad(a, true, &turns);  // (groups too small to share anything)
+  if (MODE == kPlain && a.G > 0) (void)groups_bad(a, true);  // (groups too small to share anything)
   make_plan<MODE>(a, plan, a.B < PLAN_NEAR ? near : base, nullptr, 0, 0, a.B, most, sums, nullptr, owner, alone);
 }
 
@@ -814,8 +813,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) rows_shared_plan_kernel(const Ch
   ChunkArgs c = a;
   c.entries = n <= ENTRIES_NEAR ? entries_near : entries;
   bool turns;
-  const int split =
-      make_entries<Geo<N>>(c, own ? &plan->part_rows : &prefix_plan->part_rows, sums, own, &turns, prefix_most, clusters);
+  const int split = make_entries<Geo<N>>(c, nullptr, sums, own, &turns, prefix_most, clusters);
   if (n <= ENTRIES_NEAR)
     for (int i = threadIdx.x; i < n; i += PLAN_THREADS) entries[i] = entries_near[i];
   if (own) {
