@@ -157,7 +157,8 @@ int kv8_produce_rows(const float* src, int64_t n_rows, int64_t src_row_stride,
  * t and y are rounded to the rows' type where they are written, but not on their way to the
  * codes.  A row whose sum of squares is NaN, or over the range of f32, has no finite y but
  * zeros: codes and scales are 0 then (and those of a row of zeros with eps 0).  The sum has a
- * fixed order for given sizes and alignment (below), so the same call gives the same bits.
+ * fixed order for given sizes and alignment (below), so the same call gives the same bits; a
+ * row's last bits may differ where it is one of more or fewer rows, or lies otherwise.
  *
  *   x             device [n_rows] rows of `width` values of dtype (a kv8_dtype), x_row_stride
  *                 (elements, >= 0) apart.
@@ -437,7 +438,13 @@ int mla_absorb_chunk_fp8_batch(const uint16_t* q_lat, int64_t q_lat_token_stride
  * p = seq_lens[b] - n_b + i, sees keys
  *   t <= p   with   t > p - window   or   t < n_sink.
  * What no new token sees is neither read nor looked up: the table's entries of pages that hold
- * only such keys may be anything, and the pages given to others.
+ * only such keys may be anything, and the pages given to others.  (That is for tables a caller
+ * keeps: kv8_pages_free below empties whole sequences, and the page calls report an entry that a
+ * sequence holds and that names no page.)
+ *
+ * Which kernel a call goes to follows from its sizes, total_q * H / B rows a sequence among
+ * them.  Sequences without queries count there: a long chunk beside hundreds of them can take
+ * three times as long as without them.
  *
  *   window     >= 1 (itself among them).   n_sink  >= 0.
  *   workspace  >= mla_absorb_window_fp8_batch_workspace_size(B, H, total_q, max_blocks, window,
@@ -473,10 +480,13 @@ int mla_absorb_window_fp8_batch(const uint16_t* q_lat, int64_t q_lat_token_strid
  *   G            >= 0 (with 0, group_start and shared_len may be NULL).
  *   share        a kv8_share: KV8_SHARE_AUTO computes a prefix once where that is estimated to be
  *                faster, KV8_SHARE_ALWAYS wherever it can (for up to 2^20 rows, and 1024 a sequence).
+ *                Where the lengths decide, finding out takes 5 us that a call without groups saves.
  *   workspace    >= mla_absorb_shared_fp8_batch_workspace_size(B, H, total_q, max_blocks, G) bytes.
  * What is computed once is whole pages that every row of the group sees.  Shared or not, the
  * results are those of mla_absorb_chunk_fp8_batch within its precision, but not the same bits.
- * Everything else is as there.
+ * Sequences of up to 64 rows on average (those without queries count, as for a window) go in row
+ * tiles of 16 or 32 here, with or without groups, where that call has tiles of 256: single tokens
+ * of few heads are faster by this call with G = 0.  Everything else is as there.
  * Errors: KV8_EINVAL, KV8_EALIGN, KV8_EUNSUPPORTED, KV8_EWORKSPACE, KV8_ECUDA.
  * ------------------------------------------------------------------------- */
 typedef enum { KV8_SHARE_AUTO = 0, KV8_SHARE_ALWAYS = 1 } kv8_share;
